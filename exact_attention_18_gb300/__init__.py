@@ -17,6 +17,13 @@ call the ``_gqa`` entry points; ``window=(left, right)`` selects the
 sliding-window entry points.  ``forward_varlen`` and ``backward_varlen`` do
 the same for packed batches: [T, H, D] tensors and int32 ``cu_seqlens``.
 
+Around attention: ``rope`` and ``rope_backward`` rotate packed Q and K by their
+positions (``rope_inv_freq`` and ``rope_steps`` make the frequency table),
+``paged_append`` puts new tokens into a paged key/value cache and
+``forward_paged`` attends to it (raw: ``fa_rope``, ``fa_rope_bwd``,
+``fa_rope_inv_freq``, ``fa_rope_steps``, ``fa_paged_append``, ``fa_fwd_paged``,
+``fa_fwd_paged_workspace_size``, with a ``PagedCache`` structure).
+
 The first call loads the compiled library and raises if it has not been built
 (``python -m exact_attention_18_gb300.build``); there is no fallback
 implementation.
@@ -35,11 +42,24 @@ __all__ = ["fa_fwd", "fa_fwd_gqa", "fa_bwd", "fa_bwd_marked", "fa_bwd_gqa", "fa_
            "fa_fwd_window", "fa_bwd_window", "fa_bwd_window_marked", "fa_fwd_splitkv",
            "fa_fwd_splitkv_workspace_size", "fa_splitkv_num_splits", "fa_merge_lse", "forward_splitkv", "merge_lse", "fa_status_string", "fa_last_error_detail",
            "fa_check_device_errors", "fa_set_wait_limit_ns", "forward", "backward", "FAError", "FA_FP16", "FA_BF16", "STATUS",
-           "library_path", "load_library"]
+           "library_path", "load_library", "fa_rope", "fa_rope_bwd", "fa_rope_inv_freq", "fa_rope_steps",
+           "fa_paged_append", "fa_fwd_paged", "fa_fwd_paged_workspace_size", "PagedCache", "FA_ROPE_SCALING",
+           "rope", "rope_backward", "rope_inv_freq", "rope_steps", "paged_append", "forward_paged"]
 
 FA_FP16, FA_BF16 = 0, 1
 STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_ALIGNMENT",
           4: "FA_ERR_WORKSPACE", 5: "FA_ERR_CUDA", 6: "FA_ERR_TIMEOUT"}
+
+FA_ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+
+class PagedCache(ctypes.Structure):
+    """``fa_paged_cache`` of fa.h: device pointers, then sizes and element strides."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("kv_lens", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
 
 _lib = None
 
@@ -98,6 +118,22 @@ def _load():
     lib.fa_merge_lse.argtypes = [vp] * 4 + [i64] * 3 + [i32, vp]
     lib.fa_bwd_noalloc.restype = i32
     lib.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, f32, i32, vp]
+    f64 = ctypes.c_double
+    lib.fa_rope_inv_freq.restype = i32
+    lib.fa_rope_inv_freq.argtypes = [i64, f64, i32, f64, f64, f64, f64, ctypes.POINTER(f64), ctypes.POINTER(f32)]
+    lib.fa_rope_steps.restype = i32
+    lib.fa_rope_steps.argtypes = [vp, i64, vp]
+    for rope in (lib.fa_rope, lib.fa_rope_bwd):
+        rope.restype = i32
+        rope.argtypes = [vp, i64] * 4 + [vp, vp] + [i64] * 5 + [i32, f32, i32, vp]
+    lib.fa_paged_append.restype = i32
+    lib.fa_paged_append.argtypes = [vp, i64] * 4 + [ctypes.POINTER(PagedCache), vp, vp, vp] + [i64] * 7 \
+        + [i32, f32, i32, vp]
+    lib.fa_fwd_paged.restype = i32
+    lib.fa_fwd_paged.argtypes = [vp, vp, vp, ctypes.POINTER(PagedCache), vp] + [i64] * 7 + [i32, i64, i64, f32, i32,
+                                                                                           vp, sz, vp]
+    lib.fa_fwd_paged_workspace_size.restype = sz
+    lib.fa_fwd_paged_workspace_size.argtypes = [i64] * 6
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_status_string.argtypes = [i32]
     lib.fa_last_error_detail.restype = ctypes.c_char_p
@@ -236,6 +272,49 @@ def fa_bwd_workspace_size(B, H, S, D) -> int:
 
 def fa_bwd_gqa_workspace_size(B, H, H_kv, S, D) -> int:
     return _load().fa_bwd_gqa_workspace_size(B, H, H_kv, S, D)
+
+
+def fa_rope(q, q_stride, k, k_stride, q_out, q_out_stride, k_out, k_out_stride, positions, steps, total, H, H_kv, D,
+            rot_dim, interleaved, magnitude, dtype, stream) -> int:
+    return _load().fa_rope(q, q_stride, k, k_stride, q_out, q_out_stride, k_out, k_out_stride, positions, steps, total,
+                           H, H_kv, D, rot_dim, int(interleaved), float(magnitude), int(dtype), stream)
+
+
+def fa_rope_bwd(dq_out, dq_out_stride, dk_out, dk_out_stride, dq, dq_stride, dk, dk_stride, positions, steps, total, H,
+                H_kv, D, rot_dim, interleaved, magnitude, dtype, stream) -> int:
+    return _load().fa_rope_bwd(dq_out, dq_out_stride, dk_out, dk_out_stride, dq, dq_stride, dk, dk_stride, positions,
+                               steps, total, H, H_kv, D, rot_dim, int(interleaved), float(magnitude), int(dtype),
+                               stream)
+
+
+def fa_rope_inv_freq(rot_dim, base, scaling, factor, original_len, fast_turns, slow_turns, inv_freq, magnitude) -> int:
+    """``inv_freq``: a ctypes double array; ``magnitude``: a ctypes float passed by reference, or None."""
+    return _load().fa_rope_inv_freq(rot_dim, float(base), int(scaling), float(factor), float(original_len),
+                                    float(fast_turns), float(slow_turns), inv_freq, magnitude)
+
+
+def fa_rope_steps(inv_freq, n, steps) -> int:
+    return _load().fa_rope_steps(inv_freq, n, steps)
+
+
+def fa_paged_append(q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, cache, cu_seqlens, positions, steps,
+                    batch, max_seqlen, total, H, H_kv, D, rot_dim, interleaved, magnitude, dtype, stream) -> int:
+    """``cache``: a PagedCache."""
+    return _load().fa_paged_append(q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, cache, cu_seqlens,
+                                   positions, steps, batch, max_seqlen, total, H, H_kv, D, rot_dim, int(interleaved),
+                                   float(magnitude), int(dtype), stream)
+
+
+def fa_fwd_paged(q, o, lse, cache, cu_seqlens, batch, max_seqlen_q, max_seqlen_k, total, H, H_kv, D, causal,
+                 window_left, window_right, scale, dtype, workspace, workspace_bytes, stream) -> int:
+    """``cache``: a PagedCache."""
+    return _load().fa_fwd_paged(q, o, lse, cache, cu_seqlens, batch, max_seqlen_q, max_seqlen_k, total, H, H_kv, D,
+                                int(causal), int(window_left), int(window_right), float(scale), int(dtype), workspace,
+                                workspace_bytes, stream)
+
+
+def fa_fwd_paged_workspace_size(batch, max_seqlen_q, max_seqlen_k, H, H_kv, D) -> int:
+    return _load().fa_fwd_paged_workspace_size(batch, max_seqlen_q, max_seqlen_k, H, H_kv, D)
 
 
 def fa_status_string(status: int) -> str:
@@ -471,4 +550,195 @@ def merge_lse(o_part, lse_part, dtype, stream=None):
     code = FA_FP16 if dtype == torch.float16 else FA_BF16
     _check(fa_merge_lse(o_part.data_ptr(), lse_part.data_ptr(), o.data_ptr(), l.data_ptr(), P, rows, D, code,
                         _stream_ptr(stream)), "fa_merge_lse")
+    return o, l
+
+
+# ----------------------------------------------------------------------- rotary positions, paged cache
+def rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                  original_len: float = 0.0, fast_turns: float = 32.0, slow_turns: float = 1.0):
+    """(inverse frequencies, float64 CPU [rot_dim / 2]; magnitude) of ``fa_rope_inv_freq``."""
+    import torch
+    if scaling not in FA_ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(FA_ROPE_SCALING)}")
+    buf, mag = (ctypes.c_double * max(int(rot_dim) // 2, 1))(), ctypes.c_float()
+    _check(fa_rope_inv_freq(int(rot_dim), base, FA_ROPE_SCALING[scaling], factor, original_len, fast_turns, slow_turns,
+                            buf, ctypes.byref(mag)), "fa_rope_inv_freq")
+    return torch.tensor(list(buf), dtype=torch.float64), mag.value
+
+
+def rope_steps(inv_freq, device="cuda"):
+    """The phase steps ``rope`` and ``paged_append`` take (int64 bit patterns), from inverse frequencies
+    in radians per position; made once per model."""
+    import torch
+    f = inv_freq.detach().to("cpu", torch.float64).contiguous()
+    if f.dim() != 1:
+        raise ValueError("inv_freq must be 1-D")
+    steps = torch.empty(f.shape, dtype=torch.int64)
+    _check(fa_rope_steps(f.data_ptr(), f.numel(), steps.data_ptr()), "fa_rope_steps")
+    return steps.to(device)
+
+
+def _rows(x, name, like=None):
+    """A CUDA tensor [T, heads, D] with dense heads; its token stride in elements."""
+    if x.dim() != 3 or not x.is_cuda or (x.shape[2] > 1 and x.stride(2) != 1) \
+            or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+        raise ValueError(f"{name} must be a CUDA tensor [T, heads, D] with dense heads (any stride between tokens)")
+    if like is not None and (x.dtype != like.dtype or x.shape[0] != like.shape[0] or x.shape[2] != like.shape[2]):
+        raise ValueError(f"{name} must have as many tokens, the head dimension and the dtype of the other rows")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def _int_array(x, name, dtype, shape):
+    if x.dtype != dtype or not x.is_cuda or not x.is_contiguous() or tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+    return x.data_ptr()
+
+
+def _same_device(first, *others):
+    """All tensors on one device, the current one (kernels launch there)."""
+    import torch
+    d = first.device
+    for x in others:
+        if x is not None and x.device != d:
+            raise ValueError("all tensors must be on one device")
+    if d.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {d}, which is not the current CUDA device")
+
+
+def _on_stream(stream):
+    """Context in which allocations belong to the stream the call runs on."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _rotate(raw, what, q, k, positions, steps, interleaved, magnitude, q_out, k_out, stream):
+    import torch
+    qs, ks = _rows(q, "q"), _rows(k, "k", q)
+    T, H, D = q.shape
+    _same_device(q, k, positions, steps, q_out, k_out)
+    with _on_stream(stream):
+        if q_out is None:
+            q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        if k_out is None:
+            k_out = torch.empty((T, k.shape[1], D), dtype=q.dtype, device=q.device)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("outputs must have the inputs' shapes")
+    _check(raw(q.data_ptr(), qs, k.data_ptr(), ks, q_out.data_ptr(), _rows(q_out, "q output", q), k_out.data_ptr(),
+               _rows(k_out, "k output", q), _int_array(positions, "positions", torch.int32, (T,)),
+               _int_array(steps, "steps", torch.int64, (steps.numel(),)), T, H, k.shape[1], D, 2 * steps.numel(),
+               interleaved, magnitude, _dtype_code(q), _stream_ptr(stream)), what)
+    return q_out, k_out
+
+
+def rope(q, k, positions, steps, interleaved: bool = False, magnitude: float = 1.0, q_out=None, k_out=None,
+         stream=None):
+    """Rotate q [T, H, D] and k [T, H_kv, D] by int32 ``positions`` [T]; returns (q_out, k_out).
+
+    ``steps`` (from ``rope_steps``) has one entry per rotated pair: the first
+    2 * len(steps) columns turn, the rest pass.  q and k may be slices of one
+    projection (any token stride); ``q_out=q, k_out=k`` works in place.
+    """
+    return _rotate(fa_rope, "fa_rope", q, k, positions, steps, interleaved, magnitude, q_out, k_out, stream)
+
+
+def rope_backward(dq_out, dk_out, positions, steps, interleaved: bool = False, magnitude: float = 1.0, dq=None,
+                  dk=None, stream=None):
+    """Gradients (dq, dk) of ``rope``'s inputs from those of its outputs; arguments as ``rope``."""
+    return _rotate(fa_rope_bwd, "fa_rope_bwd", dq_out, dk_out, positions, steps, interleaved, magnitude, dq, dk,
+                   stream)
+
+
+def _paged_cache(k_cache, v_cache, block_table, kv_lens, batch):
+    """The C structure of a cache of [pages, page_size, H_kv, D] tensors (any order of strides, D dense)."""
+    import torch
+    if k_cache.dim() != 4 or not k_cache.is_cuda or not v_cache.is_cuda or v_cache.shape != k_cache.shape \
+            or v_cache.dtype != k_cache.dtype or v_cache.stride() != k_cache.stride() \
+            or (k_cache.shape[3] > 1 and k_cache.stride(3) != 1):
+        raise ValueError("k_cache and v_cache must be CUDA tensors [pages, page_size, H_kv, D] of one shape, dtype and "
+                         "strides, with D dense")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_cuda \
+            or block_table.shape[0] != batch or (block_table.shape[1] > 1 and block_table.stride(1) != 1) \
+            or (batch > 1 and block_table.stride(0) < block_table.shape[1]):
+        raise ValueError("block_table must be an int32 CUDA tensor [batch, pages per sequence] with dense rows")
+    pages, page_size, _, D = k_cache.shape
+    # The stride of a dimension of one entry is never used; it may be any number in torch.
+    sp, sr, sh = (k_cache.stride(i) if k_cache.shape[i] > 1 else D for i in range(3))
+    table_stride = block_table.stride(0) if batch > 1 else block_table.shape[1]
+    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                      _int_array(kv_lens, "kv_lens", torch.int32, (batch,)), table_stride, pages, page_size, sp, sr, sh)
+
+
+def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen: int, q=None, positions=None,
+                 steps=None, interleaved: bool = False, magnitude: float = 1.0, q_out=None, stream=None):
+    """Write new tokens' K (rotated) and V [T, H_kv, D] into the cache; returns rotated q (None without q).
+
+    The cache is ``k_cache``, ``v_cache`` [pages, page_size, H_kv, D] (any order
+    of strides), int32 ``block_table`` [batch, pages per sequence] and int32
+    ``kv_lens`` [batch], which already count the new tokens; ``cu_seqlens`` and
+    ``max_seqlen`` are the new tokens'.  A token's position is its key index
+    unless ``positions`` gives it; without ``steps`` nothing is rotated.
+    """
+    import torch
+    ks, vs = _rows(k, "k"), _rows(v, "v", k)
+    T, hk, D = k.shape
+    if v.shape != k.shape or k_cache.shape[2:] != k.shape[1:] or k_cache.dtype != k.dtype:
+        raise ValueError("v and the cache must have k's heads, head dimension and dtype")
+    batch = _cu(cu_seqlens, T)
+    cache = _paged_cache(k_cache, v_cache, block_table, kv_lens, batch)
+    _same_device(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, q, q_out, positions, steps)
+    H = 0
+    q_args = (None, 0, None, 0)
+    if q is not None:
+        qs, H = _rows(q, "q", k), q.shape[1]
+        if q_out is None:
+            with _on_stream(stream):
+                q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        q_args = (q.data_ptr(), qs, q_out.data_ptr(), _rows(q_out, "q_out", q))
+    n_steps = 0 if steps is None else steps.numel()
+    _check(fa_paged_append(*q_args, k.data_ptr(), ks, v.data_ptr(), vs, cache, cu_seqlens.data_ptr(),
+                           None if positions is None else _int_array(positions, "positions", torch.int32, (T,)),
+                           None if steps is None else _int_array(steps, "steps", torch.int64, (n_steps,)), batch,
+                           int(max_seqlen), T, H, hk, D, 2 * n_steps, interleaved, magnitude, _dtype_code(k),
+                           _stream_ptr(stream)), "fa_paged_append")
+    return q_out if q is not None else None
+
+
+def forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q: int, max_seqlen_k: int,
+                  causal: bool = True, window=None, scale: float | None = None, out=None, lse=None, workspace=None,
+                  stream=None):
+    """O [T, H, D] and L [H, T] of new tokens q [T, H, D] over a paged cache (arguments as ``paged_append``).
+
+    Query i of a sequence's n new tokens stands at key kv_lens - n + i.
+    ``max_seqlen_q`` and ``max_seqlen_k`` are host bounds on the new tokens and
+    on ``kv_lens``; a violation, or a bad page, is found on the device and
+    reported by ``fa_check_device_errors``.
+    """
+    import torch
+    q = _packed(q, "q")
+    T, H, D = q.shape
+    hk = k_cache.shape[2] if k_cache.dim() == 4 else 0
+    if k_cache.dim() != 4 or k_cache.shape[3] != D or k_cache.dtype != q.dtype or hk < 1 or H % hk != 0:
+        raise ValueError("the cache must be [pages, page_size, H_kv, D] with H_kv dividing H, in q's dtype")
+    batch = _cu(cu_seqlens, T)
+    cache = _paged_cache(k_cache, v_cache, block_table, kv_lens, batch)
+    _same_device(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, lse, workspace)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    left, right = (-1, -1) if window is None else window
+    with _on_stream(stream):
+        o = torch.empty_like(q) if out is None else out
+        l = torch.empty((H, T), dtype=torch.float32, device=q.device) if lse is None else lse
+        if workspace is None:
+            need = fa_fwd_paged_workspace_size(batch, int(max_seqlen_q), int(max_seqlen_k), H, hk, D)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    if o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous() or tuple(l.shape) != (H, T) \
+            or l.dtype != torch.float32 or not l.is_contiguous():
+        raise ValueError("out must be like q, lse contiguous fp32 [H, T]")
+    _check(fa_fwd_paged(q.data_ptr(), o.data_ptr(), l.data_ptr(), cache, cu_seqlens.data_ptr(), batch,
+                        int(max_seqlen_q), int(max_seqlen_k), T, H, hk, D, causal, left, right, scale, _dtype_code(q),
+                        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
+           "fa_fwd_paged")
     return o, l

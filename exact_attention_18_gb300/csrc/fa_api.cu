@@ -9,6 +9,7 @@
 
 #include "../../include/fa.h"
 #include "fa_internal.cuh"
+#include "fa_paged.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -426,6 +427,214 @@ Shape packed(const int32_t* cu, int64_t batch, int64_t max_seqlen, int64_t total
   return Shape{batch, H, H_kv, max_seqlen, D, cu, total, true};
 }
 
+// ---------------------------------------------------------------------------
+// Rotary positions and the paged cache.
+
+fa_status check_dtype_d(int64_t D, fa_dtype dtype) {
+  if (dtype != FA_FP16 && dtype != FA_BF16) return fail(FA_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  if (D != 16 && D != 32 && D != 64 && D != 128)
+    return fail(FA_ERR_UNSUPPORTED, "head dimension D=%lld is not one of 16, 32, 64, 128", (long long)D);
+  return FA_OK;
+}
+
+fa_status check_tokens(int64_t total, int64_t H, int64_t H_kv) {
+  if (total < 0 || H < 0 || H_kv < 0)
+    return fail(FA_ERR_INVALID_ARG, "negative size: total=%lld H=%lld H_kv=%lld", (long long)total, (long long)H,
+                (long long)H_kv);
+  // total, H, H_kv < 2^31 each, so their products with 128 fit 64 bits
+  if (total >= (int64_t(1) << 31) || H >= (int64_t(1) << 20) || H_kv >= (int64_t(1) << 20))
+    return fail(FA_ERR_UNSUPPORTED, "total must be below 2^31, H and H_kv below 2^20");
+  return FA_OK;
+}
+
+// Rows of `heads` dense heads, `stride` elements between tokens.
+fa_status check_rows(const void* p, int64_t stride, int64_t heads, int64_t D, const char* name) {
+  fa_status st = check_ptr(p, name);
+  if (st != FA_OK) return st;
+  if (stride % 8 != 0) return fail(FA_ERR_ALIGNMENT, "%s: stride %lld is not a multiple of 8 elements", name, (long long)stride);
+  if (stride < heads * D || stride > (int64_t(1) << 40))
+    return fail(FA_ERR_INVALID_ARG, "%s: stride %lld does not hold %lld heads of %lld", name, (long long)stride,
+                (long long)heads, (long long)D);
+  return FA_OK;
+}
+
+fa_status check_ints(const void* p, const char* name, unsigned bytes) {
+  if (!p) return fail(FA_ERR_INVALID_ARG, "%s is NULL", name);
+  if ((reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0)
+    return fail(FA_ERR_ALIGNMENT, "%s is not %u-byte aligned", name, bytes);
+  return FA_OK;
+}
+
+fa_status check_rotation(int64_t rot_dim, int64_t D, int64_t least, float magnitude, const void* steps) {
+  if (rot_dim < least || rot_dim > D || rot_dim % 2 != 0)
+    return fail(FA_ERR_INVALID_ARG, "rot_dim=%lld must be even, between %lld and D=%lld", (long long)rot_dim,
+                (long long)least, (long long)D);
+  if (!std::isfinite(magnitude)) return fail(FA_ERR_INVALID_ARG, "magnitude must be finite");
+  return rot_dim > 0 ? check_ints(steps, "steps", 8) : FA_OK;
+}
+
+fa_status check_cache(const fa_paged_cache* c, int64_t H_kv, int64_t D) {
+  if (!c) return fail(FA_ERR_INVALID_ARG, "cache is NULL");
+  fa_status st;
+  if ((st = check_ptr(c->k, "cache.k")) || (st = check_ptr(c->v, "cache.v")) ||
+      (st = check_ints(c->block_table, "cache.block_table", 4)) || (st = check_ints(c->kv_lens, "cache.kv_lens", 4)))
+    return st;
+  const int64_t ps = c->page_size;
+  if (ps < 16 || (ps & (ps - 1)) != 0 || ps > (int64_t(1) << 30))
+    return fail(FA_ERR_UNSUPPORTED, "page_size=%lld is not a power of two from 16 to 2^30", (long long)ps);
+  if (c->num_pages < 1 || c->num_pages >= (int64_t(1) << 31) - 1 || c->table_stride < 1 ||
+      c->table_stride >= (int64_t(1) << 31))
+    return fail(FA_ERR_INVALID_ARG, "num_pages=%lld and table_stride=%lld must be positive, below 2^31 - 1",
+                (long long)c->num_pages, (long long)c->table_stride);
+  const int64_t sp = c->page_stride, sr = c->row_stride, sh = c->head_stride;
+  if (sp <= 0 || sr <= 0 || sh <= 0) return fail(FA_ERR_INVALID_ARG, "cache strides must be positive");
+  if (sp % 8 != 0 || sr % 8 != 0 || sh % 8 != 0)
+    return fail(FA_ERR_ALIGNMENT, "cache strides must be multiples of 8 elements");
+  // 40 bits of bytes is what a tensor map's strides hold.
+  if (sp >= (int64_t(1) << 39) || sr >= (int64_t(1) << 39) || sh >= (int64_t(1) << 39))
+    return fail(FA_ERR_UNSUPPORTED, "cache strides must be below 2^39 elements");
+  if (sh < D || sr < D || sp < D) return fail(FA_ERR_INVALID_ARG, "cache strides must be at least D");
+  // Rows are apart when, sorted by stride, each dimension spans what is inside it.
+  struct Dim { int64_t stride, n; } d[3] = {{sh, H_kv}, {sr, ps}, {sp, c->num_pages}};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (d[j].n == 1 ? false : (d[j + 1].n == 1 || d[j].stride > d[j + 1].stride)) {
+        const Dim t = d[j];
+        d[j] = d[j + 1];
+        d[j + 1] = t;
+      }
+  int64_t span = D;
+  for (const Dim& x : d) {
+    if (x.n <= 1) continue;
+    if (x.stride < span) return fail(FA_ERR_INVALID_ARG, "cache strides make rows overlap");
+    if (x.n - 1 > ((int64_t(1) << 60) - span) / x.stride) return fail(FA_ERR_UNSUPPORTED, "cache too large");
+    span += (x.n - 1) * x.stride;
+  }
+  return FA_OK;
+}
+
+int log2_of(int64_t x) {
+  int s = 0;
+  while ((int64_t(1) << s) < x) ++s;
+  return s;
+}
+
+// Keys a row of the block table can hold (at most kMaxPagedLen).
+int64_t table_keys(const fa_paged_cache* c) {
+  return c->table_stride > fa::kMaxPagedLen / c->page_size ? fa::kMaxPagedLen : c->table_stride * c->page_size;
+}
+
+fa_status rope_impl(const void* q, int64_t q_stride, const void* k, int64_t k_stride, void* q_out,
+                    int64_t q_out_stride, void* k_out, int64_t k_out_stride, const int32_t* positions,
+                    const uint64_t* steps, int64_t total, int64_t H, int64_t H_kv, int64_t D, int64_t rot_dim,
+                    int interleaved, float magnitude, float sign, fa_dtype dtype, void* stream) {
+  g_detail[0] = 0;
+  fa_status st;
+  if ((st = check_dtype_d(D, dtype)) || (st = check_tokens(total, H, H_kv))) return st;
+  if (total == 0 || H + H_kv == 0) return FA_OK;
+  if (H > 0 && ((st = check_rows(q, q_stride, H, D, "q")) || (st = check_rows(q_out, q_out_stride, H, D, "q_out"))))
+    return st;
+  if (H_kv > 0 &&
+      ((st = check_rows(k, k_stride, H_kv, D, "k")) || (st = check_rows(k_out, k_out_stride, H_kv, D, "k_out"))))
+    return st;
+  if ((st = check_ints(positions, "positions", 4)) || (st = check_rotation(rot_dim, D, 2, magnitude, steps))) return st;
+  if ((H > 0 && q == q_out && q_stride != q_out_stride) || (H_kv > 0 && k == k_out && k_stride != k_out_stride))
+    return fail(FA_ERR_INVALID_ARG, "in place needs equal strides");
+  fa::RopeParams p = {};
+  p.q = q;
+  p.k = k;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_out_stride = k_out_stride;
+  p.positions = positions;
+  p.steps = reinterpret_cast<const unsigned long long*>(steps);
+  p.total = static_cast<int>(total);
+  p.H = static_cast<int>(H);
+  p.H_kv = static_cast<int>(H_kv);
+  p.D = static_cast<int>(D);
+  p.r = static_cast<int>(rot_dim / 2);
+  p.interleaved = interleaved ? 1 : 0;
+  p.copy_rest = (H > 0 && q != q_out) || (H_kv > 0 && k != k_out);
+  p.mag = magnitude;
+  p.mag_sin = sign * magnitude;
+  return from_cuda(fa::launch_rope(p, dtype == FA_BF16, false, 1, static_cast<cudaStream_t>(stream)), "rope launch");
+}
+
+// Rows of a unit (tokens x group) the paged kernel runs with, and its tiling.
+struct PagedPlan {
+  int N, tok_tile, tiles, grid;
+  size_t o_bytes, lse_bytes, bytes;
+};
+
+// The tiling of a call; false when it is empty or has too many units.
+bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t H_kv, int64_t D, PagedPlan* plan) {
+  if (batch <= 0 || max_q <= 0 || max_k < 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || H / H_kv > 128 ||
+      batch >= (int64_t(1) << 31) || max_q > fa::kMaxPagedLen || max_k > fa::kMaxPagedLen ||
+      H >= (int64_t(1) << 20))
+    return false;
+  const int64_t G = H / H_kv;
+  plan->N = fa::paged_rows(max_q * G > 128 ? 128 : max_q * G);
+  int64_t tok = plan->N / G;
+  if (tok > max_q) tok = max_q;
+  plan->tok_tile = static_cast<int>(tok);
+  plan->tiles = static_cast<int>((max_q + tok - 1) / tok);
+  if (batch > (int64_t(1) << 30) / plan->tiles) return false;
+  const int64_t units = batch * plan->tiles;       // at most 2^30
+  const int64_t blocks = (max_k + 127) / 128 + 1;  // of a unit, at most
+  if (units > (int64_t(1) << 37) / (blocks * H_kv)) return false;  // a CTA's run of blocks fits 31 bits
+  const int64_t most = units * H_kv * blocks;
+  plan->grid = static_cast<int>(most < fa::kPagedGrid ? most : fa::kPagedGrid);
+  plan->o_bytes = round256(static_cast<size_t>(2) * plan->grid * plan->N * D * sizeof(float));
+  plan->lse_bytes = round256(static_cast<size_t>(2) * plan->grid * plan->N * sizeof(float));
+  plan->bytes = plan->o_bytes + plan->lse_bytes + round256(static_cast<size_t>(plan->grid) * sizeof(int4));
+  return true;
+}
+
+// Tensor map of a packed [T, H, D] Q, box {row chunk, G heads, tok_tile tokens}.
+fa_status encode_paged_q(CUtensorMap* map, const void* q, bool bf16, int64_t total, int64_t H, int64_t D, int64_t G,
+                         int tok_tile) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const int rb = fa::row_bytes_for(static_cast<int>(D));
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(total)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D * 2), static_cast<cuuint64_t>(H * D * 2)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(rb / 2), static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tok_tile)};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUtensorMapSwizzle swz = rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : (rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+  CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                   const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "tensor map for q: cuTensorMapEncodeTiled error %d", (int)r);
+  return FA_OK;
+}
+
+// Tensor map of the cache's K or V: {D, H_kv, page_size, num_pages}, box
+// {row chunk, 1, min(page_size, 128), 1}.  Pages from num_pages on read zero.
+fa_status encode_paged_kv(CUtensorMap* map, const void* base, bool bf16, const fa_paged_cache* c, int64_t H_kv,
+                          int64_t D, const char* name) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const int rb = fa::row_bytes_for(static_cast<int>(D));
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H_kv),
+                        static_cast<cuuint64_t>(c->page_size), static_cast<cuuint64_t>(c->num_pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->head_stride * 2), static_cast<cuuint64_t>(c->row_stride * 2),
+                           static_cast<cuuint64_t>(c->page_stride * 2)};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(rb / 2), 1u,
+                       static_cast<cuuint32_t>(c->page_size < 128 ? c->page_size : 128), 1u};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  CUtensorMapSwizzle swz = rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : (rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+  CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "tensor map for %s: cuTensorMapEncodeTiled error %d", name, (int)r);
+  return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -610,6 +819,221 @@ fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void
                        static_cast<size_t>(fa::kNoAllocMaxRows) * sizeof(float), stream, nullptr);
 }
 
+fa_status fa_rope_inv_freq(int64_t rot_dim, double base, fa_rope_scaling scaling, double factor, double original_len,
+                           double fast_turns, double slow_turns, double* inv_freq, float* magnitude) {
+  g_detail[0] = 0;
+  if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > (1 << 20))
+    return fail(FA_ERR_INVALID_ARG, "rot_dim=%lld must be even and at least 2", (long long)rot_dim);
+  if (!inv_freq) return fail(FA_ERR_INVALID_ARG, "inv_freq is NULL");
+  if (!std::isfinite(base) || base <= 0) return fail(FA_ERR_INVALID_ARG, "base must be finite and positive");
+  if (scaling != FA_ROPE_NONE && scaling != FA_ROPE_LINEAR && scaling != FA_ROPE_BASE && scaling != FA_ROPE_PARTS)
+    return fail(FA_ERR_INVALID_ARG, "unknown scaling %d", (int)scaling);
+  if (scaling != FA_ROPE_NONE && (!std::isfinite(factor) || factor <= 0))
+    return fail(FA_ERR_INVALID_ARG, "factor must be finite and positive");
+  const bool parts = scaling == FA_ROPE_PARTS;
+  if (parts && !(original_len > 0 && slow_turns > 0 && fast_turns > slow_turns && std::isfinite(original_len) &&
+                 std::isfinite(fast_turns) && base > 1))
+    return fail(FA_ERR_INVALID_ARG, "scaling by parts needs original_len > 0, fast_turns > slow_turns > 0, base > 1");
+  const double rot = static_cast<double>(rot_dim);
+  // (rot_dim = 2 has one pair, of frequency 1 whatever the base)
+  if (scaling == FA_ROPE_BASE && rot_dim > 2) base *= std::pow(factor, rot / (rot - 2.0));
+  double lo = 0, hi = 0;
+  if (parts) {
+    // Pair index (a real number) that makes `turns` turns in original_len positions.
+    constexpr double kTwoPi = 6.283185307179586476925;
+    auto pair_of = [&](double turns) {
+      return rot * std::log(original_len / (turns * kTwoPi)) / (2.0 * std::log(base));
+    };
+    lo = std::fmax(std::floor(pair_of(fast_turns)), 0.0);
+    hi = std::fmin(std::ceil(pair_of(slow_turns)), rot - 1.0);
+    if (hi == lo) hi += 0.001;
+  }
+  for (int64_t i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * static_cast<double>(i) / rot);
+    if (scaling == FA_ROPE_LINEAR) f /= factor;
+    if (parts) {
+      const double ramp = std::fmin(std::fmax((static_cast<double>(i) - lo) / (hi - lo), 0.0), 1.0);
+      f = f / factor * ramp + f * (1.0 - ramp);
+    }
+    inv_freq[i] = f;
+  }
+  if (magnitude) *magnitude = parts && factor > 1 ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return FA_OK;
+}
+
+fa_status fa_rope_steps(const double* inv_freq, int64_t n, uint64_t* steps) {
+  g_detail[0] = 0;
+  if (n < 0) return fail(FA_ERR_INVALID_ARG, "n=%lld is negative", (long long)n);
+  if (n > 0 && (!inv_freq || !steps)) return fail(FA_ERR_INVALID_ARG, "inv_freq or steps is NULL");
+  for (int64_t i = 0; i < n; ++i)
+    if (!std::isfinite(inv_freq[i])) return fail(FA_ERR_INVALID_ARG, "inv_freq[%lld] is not finite", (long long)i);
+  for (int64_t i = 0; i < n; ++i) {
+    const double turns = inv_freq[i] / 6.283185307179586476925;
+    const double frac = turns - std::floor(turns);  // [0, 1]; 1 when a tiny negative rounds up
+    steps[i] = frac >= 1.0 ? 0 : static_cast<uint64_t>(std::ldexp(frac, 64));
+  }
+  return FA_OK;
+}
+
+fa_status fa_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, void* q_out,
+                  int64_t q_out_stride, void* k_out, int64_t k_out_stride, const int32_t* positions,
+                  const uint64_t* steps, int64_t total, int64_t H, int64_t H_kv, int64_t D, int64_t rot_dim,
+                  int interleaved, float magnitude, fa_dtype dtype, void* stream) {
+  return rope_impl(q, q_stride, k, k_stride, q_out, q_out_stride, k_out, k_out_stride, positions, steps, total, H,
+                   H_kv, D, rot_dim, interleaved, magnitude, 1.f, dtype, stream);
+}
+
+fa_status fa_rope_bwd(const void* dq_out, int64_t dq_out_stride, const void* dk_out, int64_t dk_out_stride, void* dq,
+                      int64_t dq_stride, void* dk, int64_t dk_stride, const int32_t* positions,
+                      const uint64_t* steps, int64_t total, int64_t H, int64_t H_kv, int64_t D, int64_t rot_dim,
+                      int interleaved, float magnitude, fa_dtype dtype, void* stream) {
+  return rope_impl(dq_out, dq_out_stride, dk_out, dk_out_stride, dq, dq_stride, dk, dk_stride, positions, steps, total,
+                   H, H_kv, D, rot_dim, interleaved, magnitude, -1.f, dtype, stream);
+}
+
+fa_status fa_paged_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, const fa_paged_cache* cache,
+                          const int32_t* cu_seqlens, const int32_t* positions, const uint64_t* steps, int64_t batch,
+                          int64_t max_seqlen, int64_t total, int64_t H, int64_t H_kv, int64_t D, int64_t rot_dim,
+                          int interleaved, float magnitude, fa_dtype dtype, void* stream) {
+  g_detail[0] = 0;
+  fa_status st;
+  if ((st = check_dtype_d(D, dtype)) || (st = check_tokens(total, H, H_kv))) return st;
+  if (batch < 0 || max_seqlen < 0)
+    return fail(FA_ERR_INVALID_ARG, "negative size: batch=%lld max_seqlen=%lld", (long long)batch, (long long)max_seqlen);
+  if (batch >= (int64_t(1) << 31) || max_seqlen >= (int64_t(1) << 31))
+    return fail(FA_ERR_UNSUPPORTED, "batch and max_seqlen must be below 2^31");
+  if (H > 0 && H_kv == 0) return fail(FA_ERR_INVALID_ARG, "H_kv=0 with H=%lld", (long long)H);
+  if (batch == 0 || max_seqlen == 0 || total == 0 || H_kv == 0) return FA_OK;
+  if (H > 0 && ((st = check_rows(q, q_stride, H, D, "q")) || (st = check_rows(q_out, q_out_stride, H, D, "q_out"))))
+    return st;
+  if (H > 0 && q == q_out && q_stride != q_out_stride) return fail(FA_ERR_INVALID_ARG, "in place needs equal strides");
+  if ((st = check_rows(k, k_stride, H_kv, D, "k")) || (st = check_rows(v, v_stride, H_kv, D, "v")) ||
+      (st = check_cache(cache, H_kv, D)) || (st = check_ints(cu_seqlens, "cu_seqlens", 4)) ||
+      (st = check_rotation(rot_dim, D, 0, magnitude, steps)))
+    return st;
+  if (positions && (st = check_ints(positions, "positions", 4))) return st;
+  fa::RopeParams p = {};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out = q_out;
+  p.k_out = cache->k;
+  p.v_out = cache->v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.positions = positions;
+  p.steps = reinterpret_cast<const unsigned long long*>(steps);
+  p.total = static_cast<int>(total);
+  p.H = static_cast<int>(H);
+  p.H_kv = static_cast<int>(H_kv);
+  p.D = static_cast<int>(D);
+  p.r = static_cast<int>(rot_dim / 2);
+  p.interleaved = interleaved ? 1 : 0;
+  p.copy_rest = 1;
+  p.mag = p.mag_sin = magnitude;
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = cache->kv_lens;
+  p.block_table = cache->block_table;
+  p.table_stride = cache->table_stride;
+  p.page_stride = cache->page_stride;
+  p.row_stride = cache->row_stride;
+  p.head_stride = cache->head_stride;
+  p.page_shift = log2_of(cache->page_size);
+  p.num_pages = static_cast<int>(cache->num_pages);
+  p.max_len = static_cast<int>(max_seqlen);
+  p.max_kv = static_cast<int>(table_keys(cache));
+  p.err = fa::device_error_word();
+  if (!p.err) return fail(FA_ERR_CUDA, "cannot resolve the device error word on the current device");
+  return from_cuda(
+      fa::launch_rope(p, dtype == FA_BF16, true, static_cast<int>(batch), static_cast<cudaStream_t>(stream)),
+      "append launch");
+}
+
+size_t fa_fwd_paged_workspace_size(int64_t batch, int64_t max_seqlen_q, int64_t max_seqlen_k, int64_t H,
+                                   int64_t H_kv, int64_t D) {
+  if (D != 16 && D != 32 && D != 64 && D != 128) return 0;
+  PagedPlan plan;
+  return paged_plan(batch, max_seqlen_q, max_seqlen_k, H, H_kv, D, &plan) ? plan.bytes : 0;
+}
+
+fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache* cache, const int32_t* cu_seqlens,
+                       int64_t batch, int64_t max_seqlen_q, int64_t max_seqlen_k, int64_t total, int64_t H,
+                       int64_t H_kv, int64_t D, int causal, int64_t window_left, int64_t window_right, float scale,
+                       fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  g_detail[0] = 0;
+  fa_status st;
+  if ((st = check_dtype_d(D, dtype)) || (st = check_tokens(total, H, H_kv)) || (st = check_heads(H, H_kv))) return st;
+  if (!std::isfinite(scale)) return fail(FA_ERR_INVALID_ARG, "scale must be finite");
+  if (batch < 0 || max_seqlen_q < 0 || max_seqlen_k < 0)
+    return fail(FA_ERR_INVALID_ARG, "negative size: batch=%lld max_seqlen_q=%lld max_seqlen_k=%lld", (long long)batch,
+                (long long)max_seqlen_q, (long long)max_seqlen_k);
+  if (batch == 0 || max_seqlen_q == 0 || total == 0 || H == 0) return FA_OK;
+  if (max_seqlen_q > fa::kMaxPagedLen || max_seqlen_k > fa::kMaxPagedLen)
+    return fail(FA_ERR_UNSUPPORTED, "max_seqlen_q and max_seqlen_k must be at most 2^29");
+  if (H / H_kv > 128) return fail(FA_ERR_UNSUPPORTED, "more than 128 query heads to a K/V head");
+  PagedPlan plan;
+  if (!paged_plan(batch, max_seqlen_q, max_seqlen_k, H, H_kv, D, &plan))
+    return fail(FA_ERR_UNSUPPORTED, "batch and lengths too large");
+  if ((st = check_ptr(q, "q")) || (st = check_ptr(o, "o")) || (st = check_ptr(lse, "lse")) ||
+      (st = check_cache(cache, H_kv, D)) || (st = check_ints(cu_seqlens, "cu_seqlens", 4)))
+    return st;
+  const int shift = log2_of(cache->page_size);
+  if (!workspace) return fail(FA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", plan.bytes);
+  if (workspace_bytes < plan.bytes)
+    return fail(FA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, plan.bytes);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(FA_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
+  const bool bf16 = dtype == FA_BF16;
+  const int64_t G = H / H_kv;
+  CUtensorMap tq, tk, tv;
+  if ((st = encode_paged_q(&tq, q, bf16, total, H, D, G, plan.tok_tile)) ||
+      (st = encode_paged_kv(&tk, cache->k, bf16, cache, H_kv, D, "cache.k")) ||
+      (st = encode_paged_kv(&tv, cache->v, bf16, cache, H_kv, D, "cache.v")))
+    return st;
+  fa::PagedParams p = {};
+  p.o = o;
+  p.lse = lse;
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = cache->kv_lens;
+  p.block_table = cache->block_table;
+  p.table_stride = cache->table_stride;
+  p.batch = static_cast<int>(batch);
+  p.H = static_cast<int>(H);
+  p.H_kv = static_cast<int>(H_kv);
+  p.G = static_cast<int>(G);
+  p.total = static_cast<int>(total);
+  p.max_q = static_cast<int>(max_seqlen_q);
+  p.max_k = static_cast<int>(max_seqlen_k < table_keys(cache) ? max_seqlen_k : table_keys(cache));
+  p.tok_tile = plan.tok_tile;
+  p.tiles = plan.tiles;
+  p.win_left = window_left < 0 || window_left >= max_seqlen_k ? fa::kNoWindow : static_cast<int>(window_left);
+  p.win_right =
+      causal ? 0 : (window_right < 0 || window_right >= max_seqlen_k + max_seqlen_q ? fa::kNoWindow : static_cast<int>(window_right));
+  p.page_shift = shift;
+  p.num_pages = static_cast<int>(cache->num_pages);
+  p.min_share = 1;
+  p.scale_log2 = scale * kLog2e;
+  char* ws = static_cast<char*>(workspace);
+  p.o_part = reinterpret_cast<float*>(ws);
+  p.lse_part = reinterpret_cast<float*>(ws + plan.o_bytes);
+  p.desc = reinterpret_cast<int4*>(ws + plan.o_bytes + plan.lse_bytes);
+  p.err = fa::device_error_word();
+  if (!p.err) return fail(FA_ERR_CUDA, "cannot resolve the device error word on the current device");
+  p.wait_ns = fa::wait_limit_ns();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (D) {
+    case 16: e = fa::launch_paged_d16(plan.N, bf16, tq, tk, tv, p, plan.grid, s); break;
+    case 32: e = fa::launch_paged_d32(plan.N, bf16, tq, tk, tv, p, plan.grid, s); break;
+    case 64: e = fa::launch_paged_d64(plan.N, bf16, tq, tk, tv, p, plan.grid, s); break;
+    case 128: e = fa::launch_paged_d128(plan.N, bf16, tq, tk, tv, p, plan.grid, s); break;
+  }
+  return from_cuda(e, "paged attention launch");
+}
+
 const char* fa_status_string(fa_status status) {
   switch (status) {
     case FA_OK: return "FA_OK";
@@ -642,6 +1066,10 @@ fa_status fa_check_device_errors(void* stream) {
     cudaMemcpyToSymbol(fa::g_fa_device_error, &zero, sizeof(int));
     if (code == fa::kErrBadSeqlens)
       return fail(FA_ERR_INVALID_ARG, "cu_seqlens contradicts max_seqlen or the token count (checked on the device)");
+    if (code == fa::kErrBadCache)
+      return fail(FA_ERR_INVALID_ARG, "a paged cache length contradicts the call (checked on the device)");
+    if (code == fa::kErrBadPage)
+      return fail(FA_ERR_INVALID_ARG, "a block table entry in use is not a page (checked on the device)");
     return fail(FA_ERR_TIMEOUT, "device pipeline wait timed out (code %d)", code);
   }
   return FA_OK;

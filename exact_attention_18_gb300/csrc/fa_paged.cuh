@@ -1,0 +1,90 @@
+// Parameters and launchers of the paged-cache operators: rotary positions,
+// the append of new tokens to the cache, and their attention over it.
+#pragma once
+
+#include "fa_internal.cuh"
+
+namespace fa {
+
+// Longest cache length (and largest window side): positions and their sums
+// with a window side stay inside 32 bits.
+constexpr int kMaxPagedLen = 1 << 29;
+
+// Row t of q starts at q + t * q_stride (elements), its head h at + h * D;
+// likewise k, v and the outputs.  Append: k_out and v_out are the caches'
+// bases, rows at page * page_stride + row * row_stride + head * head_stride.
+struct RopeParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_out;
+  void* v_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  const int* positions;  // [total]; append: may be nullptr (the cache position is the angle's)
+  const unsigned long long* steps;  // [r] phase steps in 2^-64 turns a position
+  int total;             // tokens
+  int H, H_kv, D;
+  int r;                 // rotated pairs
+  int interleaved;
+  int copy_rest;         // copy the columns past 2r (outputs are not the inputs)
+  int copies;            // items of a row that copy (set by the launcher)
+  int tok_per_cta;       // set by the launcher
+  int tiles;             // append: CTAs per sequence (set by the launcher)
+  float mag, mag_sin;    // factors of cos and sin (mag_sin = -mag turns back)
+  // append
+  const int* cu_seqlens;
+  const int* kv_lens;
+  const int* block_table;
+  int64_t table_stride;
+  int64_t page_stride, row_stride, head_stride;
+  int page_shift, num_pages;
+  int max_len;           // largest number of new tokens of a sequence
+  int max_kv;            // largest cache length the block table can hold
+  int* err;
+};
+
+cudaError_t launch_rope(RopeParams p, bool bf16, bool append, int batch, cudaStream_t stream);
+
+// Attention over the cache.  A "unit" is one (sequence, tile of tok_tile
+// tokens, K/V head): its rows are tok_tile tokens x G query heads (row n =
+// token n / G, head n % G), its work the 128-key blocks its rows can see.
+struct PagedParams {
+  void* o;               // [T, H, D]
+  float* lse;            // [H, T] natural log
+  const int* cu_seqlens;
+  const int* kv_lens;
+  const int* block_table;
+  int64_t table_stride;
+  int batch, H, H_kv, G;
+  int total;             // T
+  int max_q, max_k;
+  int tok_tile;          // tokens of a tile
+  int tiles;             // tiles of the longest sequence: ceil(max_q / tok_tile)
+  int win_left, win_right;  // key j visible to position i iff i - win_left <= j <= i + win_right (and j < kv_len)
+  int page_shift, num_pages;
+  int min_share;         // fewest blocks a CTA takes
+  float scale_log2;
+  float* o_part;         // [2 grid][N][D] fp32
+  float* lse_part;       // [2 grid][N] fp32, base 2
+  int4* desc;            // [grid] unit whose first blocks CTA c computed without finishing it:
+                         // {first token, tokens (0 = none), K/V head, last CTA}
+  int* err;
+  unsigned long long wait_ns;
+};
+
+// Rows of a unit the kernel is instantiated for; the smallest that holds
+// `rows`, else the largest.
+inline int paged_rows(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
+constexpr int kPagedGrid = 152;  // CTAs at most: one per SM
+
+cudaError_t launch_paged_d16(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PagedParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_paged_d32(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PagedParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_paged_d64(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PagedParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_paged_d128(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const PagedParams& p, int grid, cudaStream_t stream);
+
+}  // namespace fa

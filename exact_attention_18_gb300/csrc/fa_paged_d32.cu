@@ -1,0 +1,11 @@
+// The paged-cache attention kernels for head dimension 32.
+#include "fa_paged_kernel.cuh"
+
+namespace fa {
+
+cudaError_t launch_paged_d32(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PagedParams& p, int grid, cudaStream_t stream) {
+  return launch_paged_n<32>(N, bf16, tq, tk, tv, p, grid, stream);
+}
+
+}  // namespace fa

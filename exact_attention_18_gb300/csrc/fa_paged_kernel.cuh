@@ -1,0 +1,816 @@
+// Attention of new tokens over a paged key/value cache: a few rows per K/V
+// head (decoding, drafted tokens) up to whole chunks of a prompt.
+//
+//   O_i = sum_j softmax_j(scale q_i . k_j) v_j,   L_i = ln sum_j exp(scale q_i . k_j)
+//
+// over the keys j of the sequence's cache that row i sees.
+//
+// Keys are the matrix rows.  With few query rows a product that puts queries
+// on the tensor core's 128 rows would leave most of them empty, so both
+// products are taken transposed: S^T = K Q^T (128 keys x N rows) and
+// O^T += V^T P^T (D x N), N = 16 .. 128 query rows of one K/V head (tokens x
+// the group's heads).  K and V come from shared memory exactly as TMA wrote
+// them: K K-major, V MN-major.  A TMEM lane is a key, so a softmax thread
+// holds one key's scores for all N rows: running sums stay per thread until
+// the unit ends, and the running maximum is one value per row that all lanes
+// share.  It is taken exactly on a unit's first block and kept, stale, while
+// no score exceeds it by more than 2^8 (exact in real arithmetic, as in the
+// other forward kernels); a block that breaks the bound, or one that a mask
+// cuts, takes the block maximum across lanes.
+//
+// What bounds it: with few rows, reading the cache.  At D = 128 a 128-key
+// block is 64 KB, 2800 cycles of an SM's share of the memory's rate, against
+// ~650 cycles of tensor core and ~500 of softmax for N <= 32.  So the kernel
+// is organised around keeping copies in flight: one persistent CTA per SM,
+// its shared memory given to a ring of K and V tiles, and work dealt in
+// 128-key blocks: the blocks of all units, in order, are cut into equal runs,
+// one per CTA, whatever the sequences' lengths (each CTA finds its run from
+// the lengths on the device).  A unit cut between CTAs leaves fp32 partials
+// (O / l and the base-2 logsumexp), which a second kernel, launched as a
+// programmatic dependent, joins in CTA order: no atomics, the result depends
+// only on the lengths.
+//
+// Warp roles: 4 (N <= 64) or 8 softmax warps, one TMA producer, one MMA
+// issuer.  Order of the tensor core's work: S(0), then S(j+1), O(j) for each
+// block j, so scores of the next block are computed during the softmax.
+//
+// Pages.  A 128-key tile arrives as 128 / min(page, 128) boxes of whole or
+// part pages; boxes that hold no visible key are not read (an out-of-range
+// page coordinate, which the copy engine fills with zeros without reading).
+// Keys the unit cannot see inside a box (past the sequence's end, before the
+// window) may hold anything: their scores are never used, and their V rows
+// are set to zero in shared memory, since 0 * NaN in the second product would
+// not be 0.
+#pragma once
+
+#include "fa_paged.cuh"
+#include "fa_softmax.cuh"
+
+namespace fa {
+using namespace ptx;
+
+namespace {
+
+constexpr int kPBlk = 128;               // keys per block
+constexpr float kPagedTau = 8.0f;        // log2 of the largest P~ kept with a stale maximum
+
+template <int D, int N>
+struct PagedLayout {
+  using GK = TileGeom<D, kPBlk>;   // K and V tiles
+  using GQ = TileGeom<D, N>;       // Q tile, N rows
+  using GP = TileGeom<N, kPBlk>;   // P^T tile: 128 keys x N rows
+  static constexpr int kWgs = N > 64 ? 2 : 1;       // softmax warpgroups, each over kCols rows
+  static constexpr int kCols = N / kWgs;
+  static constexpr int kThreads = 128 * kWgs + 64;
+  static constexpr int kQBufs = N > 64 ? 1 : 2;
+  static constexpr int kQBytes = (GQ::kTileBytes + 1023) / 1024 * 1024;
+  static constexpr int kSmallBytes = 4096 + 512;    // barriers and per-row arrays
+  static constexpr int kBudget = 227 * 1024 - 1024;
+  static constexpr int kUnitsFit = (kBudget - 2 * GP::kTileBytes - kQBufs * kQBytes - kSmallBytes) / GK::kTileBytes;
+  static constexpr int kUnits = kUnitsFit > 16 ? 16 : kUnitsFit;  // ring stages, one K or V tile each
+  static_assert(kUnits >= 3, "ring");
+  static constexpr int kOffP = kUnits * GK::kTileBytes;
+  static constexpr int kOffQ = kOffP + 2 * GP::kTileBytes;
+  static constexpr int kOffSmall = kOffQ + kQBufs * kQBytes;
+  // full[U], empty[U], qfull[2], qempty[2], sfull[2], pfull[2], pv[2], vtmp, drain
+  static constexpr int kNumBars = 2 * kUnits + 10 + 2;
+  static_assert(kNumBars * 8 + 64 + 8 * N * 4 <= kSmallBytes, "small arrays");
+  // One CTA per SM: the request is padded above half of the SM's shared memory.
+  static constexpr int kSmemUsed = kOffSmall + kSmallBytes + 1024;
+  static constexpr int kSmemBytes = kSmemUsed > 116 * 1024 ? kSmemUsed : 116 * 1024;
+  static constexpr uint32_t kTmemCols = 3 * N <= 64 ? 64 : (3 * N <= 128 ? 128 : (3 * N <= 256 ? 256 : 512));
+  // V^T is D rows; the MMA's 128 rows past D repeat tile rows 8 further on
+  // (in bounds: the ring is followed by the P tiles) into TMEM lanes nobody reads.
+  static constexpr uint32_t kVLbo = D == 128 ? GK::kChunkBytes : 8 * GK::kRowBytes;
+};
+
+// Geometry of one unit; n_blk = 0 when it does not exist.
+struct Unit {
+  int tok0;    // first token (row of Q, O)
+  int n_tok;   // tokens
+  int pos0;    // cache position of its first token
+  int kv_len;
+  int lo, hi;  // keys any of its rows sees: [lo, hi)
+  int n_blk;   // 128-key blocks from lo / 128
+  int end_tile;  // tiles of the sequence (tiles from here on do not exist)
+};
+
+// Unit (b, tile) of the call.  A sequence whose lengths contradict the call is
+// recorded as an error and has no units.  A unit whose rows see no key keeps
+// one wholly masked block, which writes O = 0, L = -inf.
+__device__ __forceinline__ Unit paged_unit(const PagedParams& p, int b, int tile) {
+  Unit u;
+  const int a = __ldg(p.cu_seqlens + b), e = __ldg(p.cu_seqlens + b + 1), kv = __ldg(p.kv_lens + b);
+  u.n_blk = 0;
+  u.end_tile = 0;
+  u.tok0 = u.n_tok = u.pos0 = u.kv_len = u.lo = u.hi = 0;
+  if (a < 0 || e < a || e - a > p.max_q || e > p.total) {
+    record_error(p.err, kErrBadSeqlens);
+    return u;
+  }
+  if (kv < 0 || kv > p.max_k) {
+    record_error(p.err, kErrBadCache);
+    return u;
+  }
+  const int n = e - a;
+  u.end_tile = (n + p.tok_tile - 1) / p.tok_tile;
+  const int t0 = tile * p.tok_tile;
+  if (t0 >= n) return u;
+  u.tok0 = a + t0;
+  u.n_tok = min(p.tok_tile, n - t0);
+  u.pos0 = kv - n + t0;
+  u.kv_len = kv;
+  u.lo = max(0, u.pos0 - p.win_left);
+  u.hi = min(kv, u.pos0 + u.n_tok + p.win_right);
+  if (u.hi <= u.lo) {
+    u.lo = u.hi = 0;
+    u.n_blk = 1;
+  } else {
+    u.n_blk = (u.hi + kPBlk - 1) / kPBlk - u.lo / kPBlk;
+  }
+  return u;
+}
+
+// Walks the segments (runs of blocks of one unit) of a CTA's run of blocks.
+struct SegWalk {
+  int b, tile, kvh;
+  int blk;        // next block within the unit
+  int left;       // blocks left in the CTA's run
+  Unit u;
+  // Blocks of the current segment (0: the run is over).
+  __device__ __forceinline__ int seg_len() const { return min(left, u.n_blk - blk); }
+  __device__ __forceinline__ void start(const PagedParams& p, int x, int rem, int run) {
+    left = run;
+    b = tile = kvh = blk = 0;
+    u.n_blk = 0;
+    if (run <= 0) return;
+    b = x / p.tiles;
+    tile = x - b * p.tiles;
+    u = paged_unit(p, b, tile);
+    kvh = rem / u.n_blk;
+    blk = rem - kvh * u.n_blk;
+  }
+  // Past the current segment (its whole length was processed).
+  __device__ __forceinline__ void next(const PagedParams& p) {
+    left -= seg_len();
+    blk = 0;
+    if (left <= 0) {
+      left = 0;
+      return;
+    }
+    if (++kvh < p.H_kv) return;
+    kvh = 0;
+    do {
+      if (++tile >= u.end_tile) {
+        tile = 0;
+        ++b;
+      }
+      if (b >= p.batch) {  // cannot happen: the run ends inside the units
+        left = 0;
+        return;
+      }
+      u = paged_unit(p, b, tile);
+    } while (u.n_blk == 0);
+  }
+};
+
+// Sum or maximum over the warp's 32 lanes of each of NC values a lane holds
+// (NC = 16 or 32): lane l receives that of column l % NC.  Halving exchange:
+// each step keeps the half of the columns the lane's bit selects.
+template <int NC, bool MAX>
+__device__ __forceinline__ float warp_reduce_cols(const float* x) {
+  const int lane = threadIdx.x & 31;
+  auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+  float v[NC / 2];
+  constexpr int kTop = NC / 2;
+  {
+    const bool up = lane & kTop;
+#pragma unroll
+    for (int i = 0; i < kTop; ++i) {
+      const float keep = up ? x[i + kTop] : x[i], give = up ? x[i] : x[i + kTop];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, kTop));
+    }
+  }
+#pragma unroll
+  for (int h = kTop / 2; h >= 1; h /= 2) {
+    const bool up = lane & h;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float keep = up ? v[i + h] : v[i], give = up ? v[i] : v[i + h];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, h));
+    }
+  }
+  if (NC == 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+  return v[0];
+}
+
+// Byte offset of 16-byte chunk c of row k in a swizzled tile with rows of ROW_BYTES.
+template <int ROW_BYTES>
+__device__ __forceinline__ uint32_t swizzled(int k, int c) {
+  constexpr int kShift = ROW_BYTES == 128 ? 0 : (ROW_BYTES == 64 ? 1 : 2);
+  constexpr int kMask = ROW_BYTES / 16 - 1;
+  return static_cast<uint32_t>(k * ROW_BYTES + ((c ^ ((k >> kShift) & kMask)) << 4));
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+template <int NC>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
+  if constexpr (NC == 16) tmem_ld16(taddr, r);
+  else if constexpr (NC == 32) tmem_ld32(taddr, r);
+  else tmem_ld64(taddr, r);
+}
+
+}  // namespace
+
+// tm_q: {D, H, T} map, box {row chunk, G, tok_tile}; tm_k, tm_v: {D, H_kv,
+// page_size, pages} maps, box {row chunk, 1, min(page_size, 128), 1}.
+template <int D, int N, bool BF16>
+__global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
+    fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
+  using L = PagedLayout<D, N>;
+  using GK = typename L::GK;
+  using GQ = typename L::GQ;
+  using GP = typename L::GP;
+  using elem_t = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  constexpr int U = L::kUnits;
+  constexpr int NC = L::kCols;
+  constexpr int kSoftWarps = 4 * L::kWgs;
+  constexpr int kProducer = kSoftWarps, kMma = kSoftWarps + 1;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + L::kOffSmall);  // [U] tile landed
+  uint64_t* bar_empty = bar_full + U;      // [U] tile's MMAs done
+  uint64_t* bar_qfull = bar_empty + U;     // [2] segment's Q landed
+  uint64_t* bar_qempty = bar_qfull + 2;    // [2] segment's last score product done
+  uint64_t* bar_sfull = bar_qempty + 2;    // [2] S(i) computed (and O(i-2) done)
+  uint64_t* bar_pfull = bar_sfull + 2;     // [2] P(i) stored, O rescaled
+  uint64_t* bar_pv = bar_pfull + 2;        // [2] O(i) done
+  uint64_t* bar_vtmp = bar_pv + 2;         // a V tile that still needs rows cleared has landed
+  uint64_t* bar_drain = bar_vtmp + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_start = reinterpret_cast<int*>(tmem_slot + 2);  // {x, rem, run, share} of this CTA's run
+  float* s_m = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bar_full) + L::kNumBars * 8 + 48);
+  s_m = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(s_m) + 15) & ~static_cast<uintptr_t>(15));
+  float* s_negm = s_m + N;          // [N] -(maximum), 0 while no key was seen
+  float* s_alpha = s_negm + N;      // [N] factor of the last change of maximum; at a segment's end 1 / l
+  float* s_red = s_alpha + N;       // [N][4] per-warp partial of each row
+  short* s_tok = reinterpret_cast<short*>(s_red + 4 * N);  // [N] token of row n
+  short* s_head = s_tok + N;                               // [N] head of row n within the group
+
+  const int warp = warp_index();
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < U; ++s) {
+      mbar_init(&bar_full[s], 1);
+      mbar_init(&bar_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar_qfull[s], 1);
+      mbar_init(&bar_qempty[s], 1);
+      mbar_init(&bar_sfull[s], 1);
+      mbar_init(&bar_pfull[s], kSoftWarps);
+      mbar_init(&bar_pv[s], 1);
+    }
+    mbar_init(bar_vtmp, 1);
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    s_start[2] = 0;
+    p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    fence_mbar_init();
+  }
+  if (warp == kMma) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == kProducer && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  for (int n = threadIdx.x; n < N; n += L::kThreads) {
+    s_tok[n] = static_cast<short>(n / p.G);
+    s_head[n] = static_cast<short>(n % p.G);
+  }
+  // This CTA's run of blocks: units x = b * tiles + tile in order, H_kv heads
+  // each.  Every thread sums a stretch of units; a block-wide scan gives the
+  // stretch that holds the run's first block.
+  {
+    long long* s_warp = reinterpret_cast<long long*>(s_red);  // free until the first segment
+    const int X = p.batch * p.tiles;
+    const int per = (X + L::kThreads - 1) / L::kThreads;
+    const int x0 = min(X, static_cast<int>(threadIdx.x) * per), x1 = min(X, x0 + per);
+    long long mine = 0;
+    for (int x = x0; x < x1; ++x) mine += paged_unit(p, x / p.tiles, x % p.tiles).n_blk;
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < L::kThreads / 32; ++w) {
+      if (w < warp) before += s_warp[w];
+      total += s_warp[w];
+    }
+    total *= p.H_kv;
+    long long share = (total + gridDim.x - 1) / gridDim.x;
+    if (share < p.min_share) share = p.min_share;
+    const long long s = share * blockIdx.x;
+    long long at = (before + incl - mine) * p.H_kv;  // first block of this thread's stretch
+    if (s >= at && s < at + mine * p.H_kv) {
+      for (int x = x0; x < x1; ++x) {
+        const long long n = static_cast<long long>(paged_unit(p, x / p.tiles, x % p.tiles).n_blk) * p.H_kv;
+        if (s < at + n) {
+          s_start[0] = x;
+          s_start[1] = static_cast<int>(s - at);
+          s_start[2] = static_cast<int>(total - s < share ? total - s : share);
+          break;
+        }
+        at += n;
+      }
+    }
+    if (threadIdx.x == 0) s_start[3] = static_cast<int>(share);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();
+  const uint32_t tmem = *tmem_slot;
+  SegWalk w;
+  w.start(p, s_start[0], s_start[1], s_start[2]);
+
+  if (warp == kProducer) {
+    // -------------------------------------------------------------- producer
+    // The whole warp runs this; lane i copies page box i of each tile.
+    const int frag = min(kPBlk, 1 << p.page_shift);
+    const int n_frag = kPBlk / frag;
+    int c = 0;    // tiles started
+    int seg = 0;  // segments started
+    int n_cut = 0;  // V tiles that had rows cleared
+    bool ok = true;
+    auto box_page = [&](int blk) -> int {  // page (or out of range) of this lane's box of the unit's block
+      const int key = (w.u.lo / kPBlk + blk) * kPBlk + lane * frag;
+      if (lane >= n_frag || key >= w.u.hi || key + frag <= w.u.lo) return p.num_pages;
+      const int page = __ldg(p.block_table + static_cast<int64_t>(w.b) * p.table_stride + (key >> p.page_shift));
+      if (page >= 0 && page < p.num_pages) return page;
+      record_error(p.err, kErrBadPage);
+      return p.num_pages;
+    };
+    for (int n; ok && (n = w.seg_len()) > 0; w.next(p), ++seg) {
+      const int qb = L::kQBufs == 2 ? (seg & 1) : 0;
+      const int qu = L::kQBufs == 2 ? (seg >> 1) : seg;
+      if (qu > 0) ok = warp_wait(&bar_qempty[qb], (qu - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar_qfull[qb], GQ::kChunks * GQ::kRowBytes * p.G * p.tok_tile);
+#pragma unroll
+        for (int ch = 0; ch < GQ::kChunks; ++ch)
+          tma_load_3d(smem + L::kOffQ + qb * L::kQBytes + ch * GQ::kChunkBytes, &tm_q, &bar_qfull[qb],
+                      ch * (GQ::kRowBytes / 2), w.kvh * p.G, w.u.tok0);
+      }
+      int page = box_page(w.blk);
+      for (int j = 0; ok && j < n; ++j) {
+        const int page_next = j + 1 < n ? box_page(w.blk + j + 1) : 0;
+        const int key0 = (w.u.lo / kPBlk + w.blk + j) * kPBlk;
+        const int row = (key0 + lane * frag) & ((1 << p.page_shift) - 1);
+        const bool cut = key0 < w.u.lo || key0 + kPBlk > w.u.hi;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int st = c % U, use = c / U;
+          if (use > 0) {
+            ok = warp_wait(&bar_empty[st], (use - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
+            if (!ok) break;
+          }
+          uint8_t* tile = smem + st * GK::kTileBytes;
+          uint64_t* bar = kv == 1 && cut ? bar_vtmp : &bar_full[st];
+          if (lane == 0) mbar_arrive_expect_tx(bar, GK::kTileBytes);
+          __syncwarp();
+          if (lane < n_frag) {
+#pragma unroll
+            for (int ch = 0; ch < GK::kChunks; ++ch)
+              tma_load_4d(tile + ch * GK::kChunkBytes + lane * frag * GK::kRowBytes, kv == 0 ? &tm_k : &tm_v, bar,
+                          ch * (GK::kRowBytes / 2), w.kvh, row, page);
+          }
+          ++c;
+          if (kv == 1 && cut) {
+            // Clear the V rows no row of the unit sees.
+            drain_wait(bar_vtmp, n_cut & 1, p.err);
+            ++n_cut;
+            const int k0 = max(0, w.u.lo - key0), k1 = min(kPBlk, w.u.hi - key0);  // visible rows [k0, k1)
+            constexpr int kVecs = GK::kRowBytes / 16;
+            for (int i = lane; i < kPBlk * kVecs * GK::kChunks; i += 32) {
+              const int r = (i / kVecs) % kPBlk;
+              if (r < k0 || r >= k1)
+                *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_full[st]);
+          }
+        }
+        page = page_next;
+      }
+    }
+    // Teardown: every copy this warp started lands before the CTA exits.
+    for (int x = (c > U ? c - U : 0); x < c; ++x) drain_wait(&bar_full[x % U], (x / U) & 1, p.err);
+    for (int x = (seg > L::kQBufs ? seg - L::kQBufs : 0); x < seg; ++x)
+      drain_wait(&bar_qfull[x % L::kQBufs], (x / L::kQBufs) & 1, p.err);
+    __syncwarp();
+  } else if (warp == kMma) {
+    // -------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc_s = make_idesc_f16(BF16, 128, N, false, false);
+    constexpr uint32_t idesc_o = make_idesc_f16(BF16, 128, N, true, true);
+    const AccFlags acc = runtime_flags(p.batch);
+    const uint32_t s_ring = smem_u32(smem), s_p = smem_u32(smem + L::kOffP), s_q = smem_u32(smem + L::kOffQ);
+    const uint32_t t_o = tmem + 2 * N;
+    int seg = 0;
+    int seg_n = w.seg_len(), j = 0;  // the walk's block is block j of segment seg
+    const int run = w.left;
+    // S(i): the walk's current block.
+    auto scores = [&](int i) -> bool {
+      const int qb = L::kQBufs == 2 ? (seg & 1) : 0;
+      const int qu = L::kQBufs == 2 ? (seg >> 1) : seg;
+      if (j == 0 && !warp_wait(&bar_qfull[qb], qu & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma)) return false;
+      const int c = 2 * i, st = c % U;
+      if (!warp_wait(&bar_full[st], (c / U) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma)) return false;
+      tc_fence_after();
+      const uint64_t k_desc = make_sdesc(s_ring + st * GK::kTileBytes, 16, 8 * GK::kRowBytes, GK::kSwz);
+      const uint64_t q_desc = make_sdesc(s_q + qb * L::kQBytes, 16, 8 * GQ::kRowBytes, GQ::kSwz);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ss_warp(tmem + (i & 1) * N, desc_plus(k_desc, kmajor_step_bytes<D, kPBlk>(kk)),
+                    desc_plus(q_desc, kmajor_step_bytes<D, N>(kk)), idesc_s, kk > 0 ? acc.on : acc.off);
+      mma_commit_warp(&bar_sfull[i & 1]);
+      mma_commit_warp(&bar_empty[st]);
+      if (++j == seg_n) {  // the segment's last score product
+        mma_commit_warp(&bar_qempty[qb]);
+        w.next(p);
+        ++seg;
+        seg_n = w.seg_len();
+        j = 0;
+      }
+      return true;
+    };
+    bool ok = run > 0 && scores(0);
+    bool first = true;  // block i is its segment's first
+    for (int i = 0; ok && i < run; ++i) {
+      const bool first_next = j == 0;  // the walk stands at block i + 1
+      if (i + 1 < run && !(ok = scores(i + 1))) break;
+      ok = warp_wait(&bar_pfull[i & 1], (i >> 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
+      const int c = 2 * i + 1, st = c % U;
+      ok = ok && warp_wait(&bar_full[st], (c / U) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t v_desc = make_sdesc(s_ring + st * GK::kTileBytes, L::kVLbo, 8 * GK::kRowBytes, GK::kSwz);
+      const uint64_t p_desc =
+          make_sdesc(s_p + (i & 1) * GP::kTileBytes, GP::kChunkBytes, 8 * GP::kRowBytes, GP::kSwz);
+#pragma unroll
+      for (int kk = 0; kk < kPBlk / 16; ++kk)
+        mma_ss_warp(t_o, desc_plus(v_desc, mnmajor_step_bytes<D>(kk)), desc_plus(p_desc, mnmajor_step_bytes<N>(kk)),
+                    idesc_o, (!first || kk > 0) ? acc.on : acc.off);
+      mma_commit_warp(&bar_empty[st]);
+      mma_commit_warp(&bar_pv[i & 1]);
+      first = first_next;
+    }
+    mma_commit_warp(bar_drain);
+    drain_wait(bar_drain, 0, p.err);
+  } else {
+    // -------------------------------------------------------------- softmax
+    const int g = warp >> 2;             // warpgroup: rows g NC .. g NC + NC - 1
+    const int q4 = warp & 3;             // lane quarter
+    const int key_lane = q4 * 32 + lane;  // key within the block; row of O^T
+    const int wt = threadIdx.x & 127;    // thread within the warpgroup
+    const int bar_id = 1 + g;
+    const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + g * NC;
+    const uint32_t t_o = tmem + lane_base + 2 * N + g * NC;
+    float* m_s = s_m + g * NC;
+    float* negm_s = s_negm + g * NC;
+    float* alpha_s = s_alpha + g * NC;
+    float* red_s = s_red + g * NC * 4;
+    const short* tok_s = s_tok + g * NC;
+    const short* head_s = s_head + g * NC;
+    const float c = p.scale_log2;
+    const float2 c2 = make_float2(c, c);
+    // P^T tile row of this key: rows' columns g NC ..  (a column chunk of 64 per warpgroup)
+    uint8_t* p_tile = smem + L::kOffP + g * GP::kChunkBytes;
+    int i = 0;  // block within the CTA's run
+    bool alive = true;
+    float l[NC];
+    long long at = static_cast<long long>(blockIdx.x) * s_start[3];  // flattened index of the segment's first block
+    for (int n; alive && (n = w.seg_len()) > 0; w.next(p)) {
+      const Unit& u = w.u;
+      const int n_rows = u.n_tok * p.G;
+      const int blk_first = u.lo / kPBlk + w.blk;
+      // Blocks every row sees whole: keys in [full_lo, full_hi).
+      const int full_lo = max(0, u.pos0 + u.n_tok - 1 - p.win_left);
+      const int full_hi = min(u.kv_len, u.pos0 + 1 + p.win_right);
+#pragma unroll
+      for (int k = 0; k < NC; ++k) l[k] = 0.f;
+      if (wt < NC) m_s[wt] = -INFINITY;  // read and written by this thread only
+      bool exact_max = true;  // the first block, a cut block and the one after it take the block maximum
+      for (int jb = 0; jb < n; ++jb, ++i) {
+        bool ok = warp_wait(&bar_sfull[i & 1], (i >> 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
+        // O(i-2) is done (S(i) was issued after it).  Waiting for it keeps this
+        // warp one phase behind each of the two barriers, so that a wait for
+        // O(i-1) below cannot take the phase before it for it.
+        if (ok && i >= 2)
+          ok = warp_wait(&bar_pv[i & 1], ((i >> 1) - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
+        const int key0 = (blk_first + jb) * kPBlk;
+        const int key = key0 + key_lane;
+        const bool cut = key0 < full_lo || key0 + kPBlk > full_hi;
+        uint32_t sr[NC];
+        if (ok) {
+          tc_fence_after();
+          tmem_ld_cols<NC>(t_s + (i & 1) * N, sr);
+        }
+        float2 cc = c2;
+        if (cut && ok) {
+          // The scaled scores in place of the scores (cc = 1 from here on),
+          // -inf where the row does not see the key.
+          cc = make_float2(1.f, 1.f);
+#pragma unroll
+          for (int k = 0; k < NC; ++k) {
+            const int pos = u.pos0 + tok_s[k];
+            const bool hidden = key >= u.kv_len || key > pos + p.win_right || key < pos - p.win_left;
+            sr[k] = __float_as_uint(hidden ? -INFINITY : c * __uint_as_float(sr[k]));
+          }
+        }
+        bool need = exact_max || cut;
+        if (!need) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < NC; k += 2) {
+            const float2 nm = *reinterpret_cast<const float2*>(negm_s + k);
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, nm);
+            mx = max3(mx, y.x, y.y);
+          }
+          // One barrier per block makes the outcome the same for all lanes.
+          need = !named_sync_and(bar_id, 128, ok && mx <= kPagedTau);
+        }
+        if (need) {
+          if (!named_sync_and(bar_id, 128, ok)) {
+            alive = false;
+            break;
+          }
+          constexpr int kRed = NC < 32 ? NC : 32;
+#pragma unroll
+          for (int k0 = 0; k0 < NC; k0 += kRed) {
+            float y[kRed];
+#pragma unroll
+            for (int k = 0; k < kRed; ++k) y[k] = cc.x * __uint_as_float(sr[k0 + k]);
+            const float mk = warp_reduce_cols<kRed, true>(y);
+            if (lane < kRed) red_s[(k0 + lane) * 4 + q4] = mk;
+          }
+          named_sync(bar_id, 128);
+          bool moved = false;
+          if (wt < NC) {
+            const float4 r4 = *reinterpret_cast<const float4*>(red_s + wt * 4);
+            const float mb = fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w));
+            const float mo = m_s[wt];
+            const float mn = (mb > mo + kPagedTau || mo == -INFINITY) ? mb : mo;
+            float a = 1.f;
+            if (mn != mo) {
+              a = ex2(mo - mn);
+              moved = true;
+            }
+            m_s[wt] = mn;
+            negm_s[wt] = mn == -INFINITY ? 0.f : -mn;
+            alpha_s[wt] = a;
+          }
+          moved = !named_sync_and(bar_id, 128, !moved);
+          if (moved && jb > 0) {
+#pragma unroll
+            for (int k = 0; k < NC; ++k) l[k] *= alpha_s[k];
+            ok = warp_wait(&bar_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag, p.err, p.wait_ns,
+                           kErrTimeoutSoftmax);
+            if (!named_sync_and(bar_id, 128, ok)) {
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < NC; k += 16) {
+              uint32_t o16[16];
+              tmem_ld16(t_o + k, o16);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float a = alpha_s[k + e];  // 0: the row saw no key before
+                o16[e] = a == 0.f ? 0u : __float_as_uint(__uint_as_float(o16[e]) * a);
+              }
+              tmem_st16(t_o + k, o16);
+            }
+            tmem_st_wait();
+          }
+        }
+        exact_max = cut;
+        // P~ = 2^(c s - m), 16-bit, into the key's row of the P^T tile; the
+        // running sums take the unrounded values.
+        uint8_t* prow = p_tile + (i & 1) * GP::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < NC; k += 8) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float2 nm = *reinterpret_cast<const float2*>(negm_s + k + e);
+            const float2 y =
+                __ffma2_rn(make_float2(__uint_as_float(sr[k + e]), __uint_as_float(sr[k + e + 1])), cc, nm);
+            const float2 pe = make_float2(ex2(y.x), ex2(y.y));
+            l[k + e] += pe.x;
+            l[k + e + 1] += pe.y;
+            pk[e / 2] = pack2<BF16>(pe.x, pe.y);
+          }
+          *reinterpret_cast<uint4*>(prow + swizzled<GP::kRowBytes>(key_lane, k / 8)) =
+              make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&bar_pfull[i & 1]);
+      }
+      if (!alive) break;
+      // ------------------------------------------------------------ segment's end
+      const bool whole = n == u.n_blk;
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (w.blk == 0 ? 1 : 0);
+      bool ok =
+          warp_wait(&bar_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
+      constexpr int kRed = NC < 32 ? NC : 32;
+#pragma unroll
+      for (int k0 = 0; k0 < NC; k0 += kRed) {
+        const float lk = warp_reduce_cols<kRed, false>(l + k0);
+        if (lane < kRed) red_s[(k0 + lane) * 4 + q4] = lk;
+      }
+      if (!named_sync_and(bar_id, 128, ok)) {
+        alive = false;
+        break;
+      }
+      if (wt < NC) {
+        const float4 r4 = *reinterpret_cast<const float4*>(red_s + wt * 4);
+        const float lt = (r4.x + r4.y) + (r4.z + r4.w);
+        const bool seen = m_s[wt] != -INFINITY;
+        alpha_s[wt] = seen ? 1.f / lt : 0.f;
+        const float l2 = seen ? m_s[wt] + log2f(lt) : -INFINITY;
+        const int row = g * NC + wt;
+        if (row < n_rows) {
+          if (whole)
+            p.lse[static_cast<int64_t>(w.kvh * p.G + head_s[wt]) * p.total + u.tok0 + tok_s[wt]] =
+                l2 * 0.69314718055994530942f;
+          else
+            p.lse_part[static_cast<int64_t>(slot) * N + row] = l2;
+        }
+      }
+      if (!whole && w.blk == 0 && threadIdx.x == 0)
+        p.desc[blockIdx.x] = make_int4(u.tok0, u.n_tok, w.kvh, static_cast<int>((at + u.n_blk - 1) / s_start[3]));
+      named_sync(bar_id, 128);
+      tc_fence_after();
+#pragma unroll
+      for (int k0 = 0; k0 < NC; k0 += 16) {
+        if (g * NC + k0 >= n_rows) break;
+        uint32_t o16[16];
+        tmem_ld16(t_o + k0, o16);
+        if (key_lane < D) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int k = k0 + e;
+            if (g * NC + k >= n_rows) break;
+            const float inv = alpha_s[k];
+            const float v = inv == 0.f ? 0.f : __uint_as_float(o16[e]) * inv;
+            if (whole) {
+              elem_t* orow = static_cast<elem_t*>(p.o) +
+                             (static_cast<int64_t>(u.tok0 + tok_s[k]) * p.H + w.kvh * p.G + head_s[k]) * D;
+              if constexpr (BF16) orow[key_lane] = __float2bfloat16_rn(v);
+              else orow[key_lane] = __float2half_rn(v);
+            } else {
+              p.o_part[(static_cast<int64_t>(slot) * N + g * NC + k) * D + key_lane] = v;
+            }
+          }
+        }
+      }
+      named_sync(bar_id, 128);  // the per-row arrays are free for the next segment
+      tc_fence_before();
+      at += n;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+// Joins the partials of the units that were cut between CTAs:
+// L = log2 sum_s 2^(L_s), O = sum_s 2^(L_s - L) O_s, in CTA order.  CTA
+// (c, y) takes rows y, y + gridDim.y, ... of the unit whose first blocks CTA c
+// of the main kernel computed.  D / 4 threads span a row; the other threads
+// split the partials, summed in a fixed order at the end.
+template <int D, int N, bool BF16>
+__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p) {
+  using elem_t = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  constexpr int kLanes = D / 4, kGroups = 128 / kLanes;
+  __shared__ float4 s_o[kGroups][kLanes];
+  __shared__ float s_w[kGroups];
+  griddep_wait();
+  const int first = blockIdx.x;
+  const int4 d = p.desc[first];
+  const int n_rows = d.y * p.G;
+  if (n_rows == 0) return;
+  const int x = threadIdx.x % kLanes, y = threadIdx.x / kLanes;
+  const int parts = d.w - first + 1;
+  for (int row = blockIdx.y; row < n_rows; row += gridDim.y) {
+    // Partial s: slot 2 first + 1 for the first CTA, 2 c for the later ones.
+    auto slot = [&](int s) -> int64_t { return static_cast<int64_t>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * N + row; };
+    float mx = -INFINITY;
+    for (int s = 0; s < parts; ++s) mx = fmaxf(mx, p.lse_part[slot(s)]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float wsum = 0.f;
+    if (mx != -INFINITY) {
+      for (int s = y; s < parts; s += kGroups) {
+        const int64_t at = slot(s);
+        const float wt = exp2f(p.lse_part[at] - mx);
+        const float4 v = *reinterpret_cast<const float4*>(p.o_part + at * D + 4 * x);
+        wsum += wt;
+        o.x += wt * v.x; o.y += wt * v.y; o.z += wt * v.z; o.w += wt * v.w;
+      }
+    }
+    s_o[y][x] = o;
+    if (x == 0) s_w[y] = wsum;
+    __syncthreads();
+    if (y == 0) {
+      float total = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < kGroups; ++q) {
+        const float4 v = s_o[q][x];
+        total += s_w[q];
+        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+      }
+      const bool seen = mx != -INFINITY;
+      const float inv = seen ? 1.f / total : 0.f;
+      const int tok = d.x + row / p.G, head = d.z * p.G + row % p.G;
+      elem_t* orow = static_cast<elem_t*>(p.o) + (static_cast<int64_t>(tok) * p.H + head) * D;
+      *reinterpret_cast<uint2*>(orow + 4 * x) =
+          make_uint2(pack2<BF16>(a.x * inv, a.y * inv), pack2<BF16>(a.z * inv, a.w * inv));
+      if (x == 0)
+        p.lse[static_cast<int64_t>(head) * p.total + tok] =
+            seen ? (mx + log2f(total)) * 0.69314718055994530942f : -INFINITY;
+    }
+    __syncthreads();
+  }
+}
+
+namespace {
+
+template <int D, int N, bool BF16>
+cudaError_t launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+                           int grid, cudaStream_t stream) {
+  using L = PagedLayout<D, N>;
+  auto kern = fa_paged_kernel<D, N, BF16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, L::kThreads, L::kSmemBytes, stream>>>(tq, tk, tv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, N < 16 ? N : 16);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<D, N, BF16>, p);
+}
+
+template <int D>
+cudaError_t launch_paged_n(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const PagedParams& p, int grid, cudaStream_t s) {
+  switch (N) {
+    case 16: return bf16 ? launch_paged_t<D, 16, true>(tq, tk, tv, p, grid, s)
+                         : launch_paged_t<D, 16, false>(tq, tk, tv, p, grid, s);
+    case 32: return bf16 ? launch_paged_t<D, 32, true>(tq, tk, tv, p, grid, s)
+                         : launch_paged_t<D, 32, false>(tq, tk, tv, p, grid, s);
+    case 64: return bf16 ? launch_paged_t<D, 64, true>(tq, tk, tv, p, grid, s)
+                         : launch_paged_t<D, 64, false>(tq, tk, tv, p, grid, s);
+    case 128: return bf16 ? launch_paged_t<D, 128, true>(tq, tk, tv, p, grid, s)
+                          : launch_paged_t<D, 128, false>(tq, tk, tv, p, grid, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+}  // namespace fa

@@ -309,6 +309,149 @@ fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void
                          const float* lse, void* dq, void* dk, void* dv, int64_t B, int64_t H, int64_t S,
                          int64_t D, int causal, float scale, fa_dtype dtype, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions and a paged key/value cache.
+ *
+ * The pages stop at attention itself ("Inside FlashAttention" §6.1 names the
+ * packed and grouped interfaces); these calls are what a caller puts around
+ * it: positions rotated into Q and K (with their gradient, for training), and,
+ * for serving, new tokens appended to a cache of pages and attended to it.
+ * Conventions as above unless stated; tokens are packed, [T, heads, D], and
+ * cu_seqlens is fa_fwd_varlen's.
+ * ------------------------------------------------------------------------ */
+
+/* How inverse frequencies are scaled for contexts longer than `original_len`
+ * (fa_rope_inv_freq):
+ *   NONE    f_i = base^(-2 i / rot_dim)
+ *   LINEAR  f_i / factor
+ *   BASE    base * factor^(rot_dim / (rot_dim - 2)) in base's place
+ *   PARTS   f_i for pairs that turn more than `fast_turns` times in original_len
+ *           positions, f_i / factor for those that turn less than `slow_turns`
+ *           times, a linear ramp over the pair index between; the magnitude is
+ *           0.1 ln(factor) + 1 (1 for factor <= 1) */
+typedef enum { FA_ROPE_NONE = 0, FA_ROPE_LINEAR = 1, FA_ROPE_BASE = 2, FA_ROPE_PARTS = 3 } fa_rope_scaling;
+
+/*
+ * HOST helper: the rot_dim / 2 inverse frequencies (radians per position) and
+ * the factor on cos and sin.  rot_dim even, >= 2; base > 0; factor > 0 unless
+ * scaling is NONE; original_len > 0 and fast_turns > slow_turns > 0 for PARTS.
+ * inv_freq: HOST double [rot_dim / 2]; magnitude: HOST, may be NULL.
+ */
+fa_status fa_rope_inv_freq(int64_t rot_dim, double base, fa_rope_scaling scaling, double factor, double original_len,
+                           double fast_turns, double slow_turns, double* inv_freq, float* magnitude);
+
+/*
+ * HOST helper: each finite inverse frequency as a phase step, inv_freq / 2 pi
+ * turns in units of 2^-64 turns, modulo one turn.  A caller copies the n steps
+ * to the device once.  position * step mod 2^64 is then the angle's fraction of
+ * a turn without loss at any position.  inv_freq, steps: HOST arrays [n].
+ */
+fa_status fa_rope_steps(const double* inv_freq, int64_t n, uint64_t* steps);
+
+/*
+ * Rotates the first rot_dim columns of every row of q [T, H, D] and k
+ * [T, H_kv, D] by its token's position.  Pair i of a row is columns
+ * (i, rot_dim / 2 + i), or (2 i, 2 i + 1) when `interleaved`; with
+ * t = positions[token] * inv_freq[i] it becomes
+ *   (m (a cos t - b sin t), m (b cos t + a sin t)),  m = magnitude.
+ * Columns from rot_dim on pass unchanged.  Arithmetic in fp32, rounded once.
+ *   q_stride, ... : elements between tokens (heads and columns are dense), a
+ *                   multiple of 8 and at least heads * D, so q and k may be
+ *                   slices of one projection; H or H_kv may be 0 (its pointers
+ *                   are then not used).
+ *   q_out, k_out  : outputs; in place (q_out = q with the same stride) is
+ *                   allowed, any other overlap of rows is not.
+ *   positions     : DEVICE int32 [T], any sign;  steps: DEVICE uint64 [rot_dim / 2].
+ * rot_dim even, 2 .. D.  T = 0 or H = H_kv = 0 is an empty call.
+ */
+fa_status fa_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, void* q_out,
+                  int64_t q_out_stride, void* k_out, int64_t k_out_stride, const int32_t* positions,
+                  const uint64_t* steps, int64_t total, int64_t H, int64_t H_kv, int64_t D, int64_t rot_dim,
+                  int interleaved, float magnitude, fa_dtype dtype, void* stream);
+
+/* Gradient of fa_rope: dq, dk [T, heads, D] from the gradients of its outputs.
+ * The rotation is linear, so this is the rotation by -t, times m; the same
+ * arguments otherwise (dq_out, dk_out are read; dq, dk are written). */
+fa_status fa_rope_bwd(const void* dq_out, int64_t dq_out_stride, const void* dk_out, int64_t dk_out_stride, void* dq,
+                      int64_t dq_stride, void* dk, int64_t dk_stride, const int32_t* positions,
+                      const uint64_t* steps, int64_t total, int64_t H, int64_t H_kv, int64_t D, int64_t rot_dim,
+                      int interleaved, float magnitude, fa_dtype dtype, void* stream);
+
+/*
+ * A paged key/value cache.  Key j of sequence b, head g is the D elements at
+ *   k + block_table[b][j / page_size] * page_stride + (j % page_size) * row_stride + g * head_stride,
+ * its value likewise from v.  page_size is a power of two, 16 or more; strides
+ * are in elements, shared by k and v, multiples of 8, and leave rows apart
+ * (pages, rows and heads in any order of nesting).
+ *   block_table : DEVICE int32 [batch, table_stride]; entries past a
+ *                 sequence's last page, and of pages no query can see, are not
+ *                 used and may hold anything.
+ *   kv_lens     : DEVICE int32 [batch], keys of each sequence INCLUDING the
+ *                 call's new tokens, so token i of the n new ones is key
+ *                 kv_lens[b] - n + i.
+ * Lengths and entries are checked on the device: a length below 0, beyond the
+ * call's bound or the block table's row, or (append) below n leaves that sequence alone, an entry in use
+ * outside [0, num_pages) is read as zeros and never written; both make
+ * fa_check_device_errors() return FA_ERR_INVALID_ARG.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  const int32_t* block_table;
+  const int32_t* kv_lens;
+  int64_t table_stride;
+  int64_t num_pages, page_size;
+  int64_t page_stride, row_stride, head_stride;
+} fa_paged_cache;
+
+/*
+ * Appends the new tokens' K and V rows to the cache (the slots above must be
+ * there already), rotating K, and rotates Q on the way, in one launch:
+ *   q, k, v     : [T, H, D], [T, H_kv, D] with token strides as in fa_rope;
+ *   q_out       : rotated Q; H = 0 leaves Q alone (q, q_out not used);
+ *   positions   : DEVICE int32 [T], or NULL: a token's position is its key index;
+ *   steps       : DEVICE uint64 [rot_dim / 2]; rot_dim = 0 (steps not used)
+ *                 appends K as it is and copies Q;
+ *   max_seqlen  : host bound on the new tokens of a sequence.
+ * Two new tokens must not share a slot.  Other slots and rows of tokens that no
+ * sequence covers are left as they were.
+ */
+fa_status fa_paged_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, const fa_paged_cache* cache,
+                          const int32_t* cu_seqlens, const int32_t* positions, const uint64_t* steps, int64_t batch,
+                          int64_t max_seqlen, int64_t total, int64_t H, int64_t H_kv, int64_t D, int64_t rot_dim,
+                          int interleaved, float magnitude, fa_dtype dtype, void* stream);
+
+/*
+ * Attention of each sequence's new tokens over its cache: one token
+ * (decoding), a few, or a chunk of a prompt, mixed in one call.
+ *   q, o        : [T, H, D];  lse : [H, T] fp32 (as fa_fwd_varlen).
+ *   Query i of the n new tokens of sequence b stands at key position
+ *   p = kv_lens[b] - n + i and sees keys j < kv_lens[b] with
+ *   p - window_left <= j <= p + window_right (a negative side is unlimited;
+ *   `causal` makes the right side 0): the causal diagonal ends at the last key.
+ *   A row that sees no key gets O = 0, L = -inf.
+ *   H is a positive multiple of H_kv, at most 128 query heads to a K/V head.
+ *   max_seqlen_q, max_seqlen_k : host bounds on the new tokens and on kv_lens
+ *   (at most 2^29).
+ *   workspace   : fa_fwd_paged_workspace_size() bytes, 256-byte aligned, for the
+ *   partials of sequences that several CTAs share; its contents on entry do not
+ *   matter, and calls that may overlap on the GPU need one each.
+ * Cached keys no row sees (past the end, before the window) may hold anything,
+ * NaN included.  A NaN or infinity in V at a key some row sees reaches that
+ * row, and may reach other rows of the call that share the K/V head.
+ * The result depends on the lengths but not on timing: repeated calls give the
+ * same bits.
+ */
+fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache* cache, const int32_t* cu_seqlens,
+                       int64_t batch, int64_t max_seqlen_q, int64_t max_seqlen_k, int64_t total, int64_t H,
+                       int64_t H_kv, int64_t D, int causal, int64_t window_left, int64_t window_right, float scale,
+                       fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of fa_fwd_paged (0 for an empty or unsupported call). */
+size_t fa_fwd_paged_workspace_size(int64_t batch, int64_t max_seqlen_q, int64_t max_seqlen_k, int64_t H,
+                                   int64_t H_kv, int64_t D);
+
 /* Static, human-readable name of a status code. */
 const char* fa_status_string(fa_status status);
 
@@ -317,9 +460,10 @@ const char* fa_last_error_detail(void);
 
 /*
  * Synchronises `stream`, then reads and clears the device error word that the
- * kernels set when a pipeline wait times out or a packed batch's cu_seqlens
- * contradicts its call.  Returns FA_ERR_TIMEOUT or FA_ERR_INVALID_ARG (the
- * latter for cu_seqlens) if it was set, FA_ERR_CUDA if the synchronisation
+ * kernels set when a pipeline wait times out, or a packed batch's cu_seqlens
+ * or a paged cache's lengths or block table contradict the call.  Returns
+ * FA_ERR_TIMEOUT or FA_ERR_INVALID_ARG (the latter for cu_seqlens and the
+ * cache) if it was set, FA_ERR_CUDA if the synchronisation
  * failed, else FA_OK.  Meant for
  * tests and debugging; the compute entry points never synchronise.
  */
