@@ -33,6 +33,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libfa_gb300.so")
 
@@ -127,10 +128,10 @@ def _load():
         rope.restype = i32
         rope.argtypes = [vp, i64] * 4 + [vp, vp] + [i64] * 5 + [i32, f32, i32, vp]
     lib.fa_paged_append.restype = i32
-    lib.fa_paged_append.argtypes = [vp, i64] * 4 + [ctypes.POINTER(PagedCache), vp, vp, vp] + [i64] * 7 \
+    lib.fa_paged_append.argtypes = [vp, i64] * 4 + [vp] * 4 + [i64] * 7 \
         + [i32, f32, i32, vp]
     lib.fa_fwd_paged.restype = i32
-    lib.fa_fwd_paged.argtypes = [vp, vp, vp, ctypes.POINTER(PagedCache), vp] + [i64] * 7 + [i32, i64, i64, f32, i32,
+    lib.fa_fwd_paged.argtypes = [vp] * 5 + [i64] * 7 + [i32, i64, i64, f32, i32,
                                                                                            vp, sz, vp]
     lib.fa_fwd_paged_workspace_size.restype = sz
     lib.fa_fwd_paged_workspace_size.argtypes = [i64] * 6
@@ -299,7 +300,7 @@ def fa_rope_steps(inv_freq, n, steps) -> int:
 
 def fa_paged_append(q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, cache, cu_seqlens, positions, steps,
                     batch, max_seqlen, total, H, H_kv, D, rot_dim, interleaved, magnitude, dtype, stream) -> int:
-    """``cache``: a PagedCache."""
+    """``cache``: a PagedCache passed by reference, or its bytes."""
     return _load().fa_paged_append(q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, cache, cu_seqlens,
                                    positions, steps, batch, max_seqlen, total, H, H_kv, D, rot_dim, int(interleaved),
                                    float(magnitude), int(dtype), stream)
@@ -307,7 +308,7 @@ def fa_paged_append(q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, 
 
 def fa_fwd_paged(q, o, lse, cache, cu_seqlens, batch, max_seqlen_q, max_seqlen_k, total, H, H_kv, D, causal,
                  window_left, window_right, scale, dtype, workspace, workspace_bytes, stream) -> int:
-    """``cache``: a PagedCache."""
+    """``cache``: a PagedCache passed by reference, or its bytes."""
     return _load().fa_fwd_paged(q, o, lse, cache, cu_seqlens, batch, max_seqlen_q, max_seqlen_k, total, H, H_kv, D,
                                 int(causal), int(window_left), int(window_right), float(scale), int(dtype), workspace,
                                 workspace_bytes, stream)
@@ -578,56 +579,76 @@ def rope_steps(inv_freq, device="cuda"):
     return steps.to(device)
 
 
-def _rows(x, name, like=None):
-    """A CUDA tensor [T, heads, D] with dense heads; its token stride in elements."""
-    if x.dim() != 3 or not x.is_cuda or (x.shape[2] > 1 and x.stride(2) != 1) \
-            or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
-        raise ValueError(f"{name} must be a CUDA tensor [T, heads, D] with dense heads (any stride between tokens)")
-    if like is not None and (x.dtype != like.dtype or x.shape[0] != like.shape[0] or x.shape[2] != like.shape[2]):
-        raise ValueError(f"{name} must have as many tokens, the head dimension and the dtype of the other rows")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+# The calls below are made once per layer and step, on a few rows when decoding, so their checks read each
+# attribute of a tensor once and compare plain integers.
+def _raw_stream(device: int) -> int:
+    """The current stream's handle (the public call builds a Stream object each time)."""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device) if get is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _call_device(first, *others) -> int:
+    """The one device of all tensors, which must be the current one (kernels launch there)."""
+    import torch
+    d = first.get_device()
+    for x in others:
+        if x is not None and x.get_device() != d:
+            raise ValueError("all tensors must be on one CUDA device")
+    if d < 0 or d != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {first.device}, which is not the current CUDA device")
+    return d
+
+
+def _rows(x, name, shape, dtype):
+    """Token stride of x, which must be [T, heads, D] (``shape``) of ``dtype`` with dense heads."""
+    st = x.stride()
+    if x.dtype != dtype or x.shape != shape or len(st) != 3 or (st[2] != 1 and shape[2] > 1) \
+            or (st[1] != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} with dense heads (any stride "
+                         "between tokens)")
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _int_array(x, name, dtype, shape):
-    if x.dtype != dtype or not x.is_cuda or not x.is_contiguous() or tuple(x.shape) != tuple(shape):
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+    if x.dtype != dtype or x.shape != shape or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     return x.data_ptr()
 
 
-def _same_device(first, *others):
-    """All tensors on one device, the current one (kernels launch there)."""
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream the call runs on."""
     import torch
-    d = first.device
-    for x in others:
-        if x is not None and x.device != d:
-            raise ValueError("all tensors must be on one device")
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {d}, which is not the current CUDA device")
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _on_stream(stream):
-    """Context in which allocations belong to the stream the call runs on."""
-    import contextlib
+def _three(x, name):
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be a tensor [T, heads, D]")
+    return x.shape
+
+
+def _rotate(what, q, k, positions, steps, interleaved, magnitude, q_out, k_out, stream):
     import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _rotate(raw, what, q, k, positions, steps, interleaved, magnitude, q_out, k_out, stream):
-    import torch
-    qs, ks = _rows(q, "q"), _rows(k, "k", q)
-    T, H, D = q.shape
-    _same_device(q, k, positions, steps, q_out, k_out)
-    with _on_stream(stream):
-        if q_out is None:
-            q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-        if k_out is None:
-            k_out = torch.empty((T, k.shape[1], D), dtype=q.dtype, device=q.device)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError("outputs must have the inputs' shapes")
-    _check(raw(q.data_ptr(), qs, k.data_ptr(), ks, q_out.data_ptr(), _rows(q_out, "q output", q), k_out.data_ptr(),
-               _rows(k_out, "k output", q), _int_array(positions, "positions", torch.int32, (T,)),
-               _int_array(steps, "steps", torch.int64, (steps.numel(),)), T, H, k.shape[1], D, 2 * steps.numel(),
-               interleaved, magnitude, _dtype_code(q), _stream_ptr(stream)), what)
+    d = _call_device(q, k, positions, steps, q_out, k_out)
+    dtype, shape, k_shape = q.dtype, _three(q, "q"), _three(k, "k")
+    T, H, D = shape
+    hk = k_shape[1]
+    if k_shape[0] != T or k_shape[2] != D:
+        raise ValueError("k must have q's tokens and head dimension")
+    if q_out is None:
+        q_out = _empty(shape, dtype, d, stream)
+    if k_out is None:
+        k_out = _empty(k_shape, dtype, d, stream)
+    n = steps.numel()
+    _check(getattr(_load(), what)(q.data_ptr(), _rows(q, "q", shape, dtype), k.data_ptr(), _rows(k, "k", k_shape, dtype),
+               q_out.data_ptr(), _rows(q_out, "the q output", shape, dtype), k_out.data_ptr(),
+               _rows(k_out, "the k output", k_shape, dtype), _int_array(positions, "positions", torch.int32, (T,)),
+               _int_array(steps, "steps", torch.int64, (n,)), T, H, hk, D, 2 * n, interleaved, magnitude,
+               _dtype_code(q), _raw_stream(d) if stream is None else stream.cuda_stream), what)
     return q_out, k_out
 
 
@@ -639,34 +660,45 @@ def rope(q, k, positions, steps, interleaved: bool = False, magnitude: float = 1
     2 * len(steps) columns turn, the rest pass.  q and k may be slices of one
     projection (any token stride); ``q_out=q, k_out=k`` works in place.
     """
-    return _rotate(fa_rope, "fa_rope", q, k, positions, steps, interleaved, magnitude, q_out, k_out, stream)
+    return _rotate("fa_rope", q, k, positions, steps, interleaved, magnitude, q_out, k_out, stream)
 
 
 def rope_backward(dq_out, dk_out, positions, steps, interleaved: bool = False, magnitude: float = 1.0, dq=None,
                   dk=None, stream=None):
     """Gradients (dq, dk) of ``rope``'s inputs from those of its outputs; arguments as ``rope``."""
-    return _rotate(fa_rope_bwd, "fa_rope_bwd", dq_out, dk_out, positions, steps, interleaved, magnitude, dq, dk,
+    return _rotate("fa_rope_bwd", dq_out, dk_out, positions, steps, interleaved, magnitude, dq, dk,
                    stream)
 
 
-def _paged_cache(k_cache, v_cache, block_table, kv_lens, batch):
-    """The C structure of a cache of [pages, page_size, H_kv, D] tensors (any order of strides, D dense)."""
+_CACHE_FIELDS = struct.Struct("@10q")  # PagedCache's fields (four pointers, six 64-bit integers)
+
+
+def _paged_cache(k_cache, v_cache, block_table, kv_lens, batch, heads, D, dtype):
+    """The C structure's bytes for a cache of [pages, page_size, H_kv, D] tensors (any order of strides, D dense)."""
     import torch
-    if k_cache.dim() != 4 or not k_cache.is_cuda or not v_cache.is_cuda or v_cache.shape != k_cache.shape \
-            or v_cache.dtype != k_cache.dtype or v_cache.stride() != k_cache.stride() \
-            or (k_cache.shape[3] > 1 and k_cache.stride(3) != 1):
-        raise ValueError("k_cache and v_cache must be CUDA tensors [pages, page_size, H_kv, D] of one shape, dtype and "
-                         "strides, with D dense")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_cuda \
-            or block_table.shape[0] != batch or (block_table.shape[1] > 1 and block_table.stride(1) != 1) \
-            or (batch > 1 and block_table.stride(0) < block_table.shape[1]):
-        raise ValueError("block_table must be an int32 CUDA tensor [batch, pages per sequence] with dense rows")
-    pages, page_size, _, D = k_cache.shape
+    shape, st = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape[2] != heads or shape[3] != D or v_cache.shape != shape or v_cache.stride() != st \
+            or (st[3] != 1 and D > 1) or k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise ValueError(f"k_cache and v_cache must be {dtype} tensors [pages, page_size, {heads}, {D}] of the same "
+                         "strides, with the last dimension dense")
+    t_shape, t_st = block_table.shape, block_table.stride()
+    if block_table.dtype != torch.int32 or len(t_shape) != 2 or t_shape[0] != batch \
+            or (t_st[1] != 1 and t_shape[1] > 1) or (batch > 1 and t_st[0] < t_shape[1]):
+        raise ValueError("block_table must be an int32 tensor [batch, pages per sequence] with dense rows")
     # The stride of a dimension of one entry is never used; it may be any number in torch.
-    sp, sr, sh = (k_cache.stride(i) if k_cache.shape[i] > 1 else D for i in range(3))
-    table_stride = block_table.stride(0) if batch > 1 else block_table.shape[1]
-    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                      _int_array(kv_lens, "kv_lens", torch.int32, (batch,)), table_stride, pages, page_size, sp, sr, sh)
+    return _CACHE_FIELDS.pack(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                              _int_array(kv_lens, "kv_lens", torch.int32, (batch,)),
+                              t_st[0] if batch > 1 else t_shape[1], shape[0], shape[1],
+                              st[0] if shape[0] > 1 else D, st[1] if shape[1] > 1 else D, st[2] if heads > 1 else D)
+
+
+def _offsets(cu_seqlens):
+    """Sequences of cu_seqlens, an int32 [batch + 1] tensor."""
+    import torch
+    n = cu_seqlens.numel()
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or n < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor [batch + 1]")
+    return n - 1
 
 
 def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen: int, q=None, positions=None,
@@ -680,29 +712,29 @@ def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_s
     unless ``positions`` gives it; without ``steps`` nothing is rotated.
     """
     import torch
-    ks, vs = _rows(k, "k"), _rows(v, "v", k)
-    T, hk, D = k.shape
-    if v.shape != k.shape or k_cache.shape[2:] != k.shape[1:] or k_cache.dtype != k.dtype:
-        raise ValueError("v and the cache must have k's heads, head dimension and dtype")
-    batch = _cu(cu_seqlens, T)
-    cache = _paged_cache(k_cache, v_cache, block_table, kv_lens, batch)
-    _same_device(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, q, q_out, positions, steps)
+    d = _call_device(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, q, q_out, positions, steps)
+    dtype, shape = k.dtype, _three(k, "k")
+    T, hk, D = shape
+    batch = _offsets(cu_seqlens)
+    cache = _paged_cache(k_cache, v_cache, block_table, kv_lens, batch, hk, D, dtype)
     H = 0
     q_args = (None, 0, None, 0)
     if q is not None:
-        qs, H = _rows(q, "q", k), q.shape[1]
+        q_shape = _three(q, "q")
+        H = q_shape[1]
+        if q_shape[0] != T or q_shape[2] != D:
+            raise ValueError("q must have k's tokens and head dimension")
         if q_out is None:
-            with _on_stream(stream):
-                q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        q_args = (q.data_ptr(), qs, q_out.data_ptr(), _rows(q_out, "q_out", q))
-    n_steps = 0 if steps is None else steps.numel()
-    _check(fa_paged_append(*q_args, k.data_ptr(), ks, v.data_ptr(), vs, cache, cu_seqlens.data_ptr(),
+            q_out = _empty(q_shape, dtype, d, stream)
+        q_args = (q.data_ptr(), _rows(q, "q", q_shape, dtype), q_out.data_ptr(),
+                  _rows(q_out, "q_out", q_shape, dtype))
+    n = 0 if steps is None else steps.numel()
+    _check(_load().fa_paged_append(*q_args, k.data_ptr(), _rows(k, "k", shape, dtype), v.data_ptr(),
+                           _rows(v, "v", shape, dtype), cache, cu_seqlens.data_ptr(),
                            None if positions is None else _int_array(positions, "positions", torch.int32, (T,)),
-                           None if steps is None else _int_array(steps, "steps", torch.int64, (n_steps,)), batch,
-                           int(max_seqlen), T, H, hk, D, 2 * n_steps, interleaved, magnitude, _dtype_code(k),
-                           _stream_ptr(stream)), "fa_paged_append")
+                           None if steps is None else _int_array(steps, "steps", torch.int64, (n,)), batch,
+                           int(max_seqlen), T, H, hk, D, 2 * n, interleaved, magnitude, _dtype_code(k),
+                           _raw_stream(d) if stream is None else stream.cuda_stream), "fa_paged_append")
     return q_out if q is not None else None
 
 
@@ -717,28 +749,34 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seq
     reported by ``fa_check_device_errors``.
     """
     import torch
-    q = _packed(q, "q")
-    T, H, D = q.shape
+    d = _call_device(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, lse, workspace)
+    dtype, shape = q.dtype, _three(q, "q")
+    T, H, D = shape
     hk = k_cache.shape[2] if k_cache.dim() == 4 else 0
-    if k_cache.dim() != 4 or k_cache.shape[3] != D or k_cache.dtype != q.dtype or hk < 1 or H % hk != 0:
-        raise ValueError("the cache must be [pages, page_size, H_kv, D] with H_kv dividing H, in q's dtype")
-    batch = _cu(cu_seqlens, T)
-    cache = _paged_cache(k_cache, v_cache, block_table, kv_lens, batch)
-    _same_device(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, lse, workspace)
+    if not q.is_contiguous() or hk < 1 or H % hk != 0:
+        raise ValueError("q must be contiguous, and its heads a multiple of the cache's")
+    batch = _offsets(cu_seqlens)
+    cache = _paged_cache(k_cache, v_cache, block_table, kv_lens, batch, hk, D, dtype)
+    max_seqlen_q, max_seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     left, right = (-1, -1) if window is None else window
-    with _on_stream(stream):
-        o = torch.empty_like(q) if out is None else out
-        l = torch.empty((H, T), dtype=torch.float32, device=q.device) if lse is None else lse
-        if workspace is None:
-            need = fa_fwd_paged_workspace_size(batch, int(max_seqlen_q), int(max_seqlen_k), H, hk, D)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    if o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous() or tuple(l.shape) != (H, T) \
-            or l.dtype != torch.float32 or not l.is_contiguous():
-        raise ValueError("out must be like q, lse contiguous fp32 [H, T]")
-    _check(fa_fwd_paged(q.data_ptr(), o.data_ptr(), l.data_ptr(), cache, cu_seqlens.data_ptr(), batch,
-                        int(max_seqlen_q), int(max_seqlen_k), T, H, hk, D, causal, left, right, scale, _dtype_code(q),
-                        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
+    if out is None:
+        out = _empty(shape, dtype, d, stream)
+    elif out.shape != shape or out.dtype != dtype or not out.is_contiguous():
+        raise ValueError("out must be like q")
+    if lse is None:
+        lse = _empty((H, T), torch.float32, d, stream)
+    elif lse.shape != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [H, T]")
+    if workspace is None:
+        need = _load().fa_fwd_paged_workspace_size(batch, max_seqlen_q, max_seqlen_k, H, hk, D)
+        workspace = _empty((max(need, 256),), torch.uint8, d, stream)
+        have = need
+    else:
+        have = workspace.numel() * workspace.element_size()
+    _check(_load().fa_fwd_paged(q.data_ptr(), out.data_ptr(), lse.data_ptr(), cache, cu_seqlens.data_ptr(), batch,
+                        max_seqlen_q, max_seqlen_k, T, H, hk, D, causal, left, right, scale, _dtype_code(q),
+                        workspace.data_ptr(), have, _raw_stream(d) if stream is None else stream.cuda_stream),
            "fa_fwd_paged")
-    return o, l
+    return out, lse

@@ -557,7 +557,6 @@ fa_status rope_impl(const void* q, int64_t q_stride, const void* k, int64_t k_st
   p.D = static_cast<int>(D);
   p.r = static_cast<int>(rot_dim / 2);
   p.interleaved = interleaved ? 1 : 0;
-  p.copy_rest = (H > 0 && q != q_out) || (H_kv > 0 && k != k_out);
   p.mag = magnitude;
   p.mag_sin = sign * magnitude;
   return from_cuda(fa::launch_rope(p, dtype == FA_BF16, false, 1, static_cast<cudaStream_t>(stream)), "rope launch");
@@ -932,7 +931,6 @@ fa_status fa_paged_append(const void* q, int64_t q_stride, void* q_out, int64_t 
   p.D = static_cast<int>(D);
   p.r = static_cast<int>(rot_dim / 2);
   p.interleaved = interleaved ? 1 : 0;
-  p.copy_rest = 1;
   p.mag = p.mag_sin = magnitude;
   p.cu_seqlens = cu_seqlens;
   p.kv_lens = cache->kv_lens;

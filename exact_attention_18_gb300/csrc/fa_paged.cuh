@@ -27,8 +27,7 @@ struct RopeParams {
   int H, H_kv, D;
   int r;                 // rotated pairs
   int interleaved;
-  int copy_rest;         // copy the columns past 2r (outputs are not the inputs)
-  int copies;            // items of a row that copy (set by the launcher)
+  int log2_items;        // threads a row, log2 (set by the launcher)
   int tok_per_cta;       // set by the launcher
   int tiles;             // append: CTAs per sequence (set by the launcher)
   float mag, mag_sin;    // factors of cos and sin (mag_sin = -mag turns back)

@@ -18,12 +18,11 @@
 //
 // Every element is read once and written once and the arithmetic is a few
 // operations an element, so memory bounds the kernel.  A CTA takes a few
-// tokens, so the angles (r sine/cosine pairs a token) are computed once per
-// token, into shared memory, and used by all of its heads.  A thread keeps
-// its pair columns and walks over (token, head) rows, two rows in flight.
-// Measured (see the cache operators' table in the design notes for all
-// cases): 16384 tokens of 32 heads of 64 fp16 in 29 us, 4.6 TB/s of reads and
-// writes.
+// tokens; the angles (r sine/cosine pairs a token) are computed once per
+// token, into shared memory, and used by all of its heads.  A thread owns 16
+// columns (two 16-byte vectors) of kRows rows at a time and loads them all
+// before it works on the angles, so the angles' latency (positions, steps,
+// sincospif, a barrier) passes while the rows are on their way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -35,63 +34,48 @@ namespace fa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxTok = 16;   // tokens per CTA at most
-constexpr int kRopeMaxPairs = 64;  // D / 2 at most
-// Elements per CTA aimed at (tokens per CTA are chosen for it): four 16-pair
-// items a thread at D = 128.
-constexpr int kRopeElems = 16384;
+constexpr int kRopeRows = 4;        // rows a thread has in flight
+constexpr int kRopeMaxTok = 128;    // tokens per CTA at most
+constexpr int kRopeMaxAngles = 1024;  // tokens x pairs per CTA at most
+// Elements of a CTA's tokens aimed at: one round of kRopeRows rows a thread.
+constexpr int kRopeElems = kRopeThreads * 16 * kRopeRows;
 
-// N consecutive 16-bit elements.
-template <int N>
-struct Vec16;
-template <>
-struct Vec16<8> { using type = uint4; };
-template <>
-struct Vec16<4> { using type = uint2; };
-template <>
-struct Vec16<2> { using type = uint32_t; };
-template <>
-struct Vec16<1> { using type = uint16_t; };
-
-template <int N, bool BF16>
-struct Pack {
-  using V = typename Vec16<N>::type;
-  union {
-    V v;
-    uint16_t h[N];
-  };
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(h[i]) << 16);
-    else return __half2float(__ushort_as_half(h[i]));
-  }
-  __device__ __forceinline__ void set(int i, float x) {
-    if constexpr (BF16) h[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-    else h[i] = __half_as_ushort(__float2half_rn(x));
-  }
+enum RopeForm {
+  kInterleaved,   // pairs (2i, 2i+1): any r, a vector holds whole pairs
+  kHalf,          // pairs (i, r + i), r a multiple of 8: vectors at 8j and r + 8j
+  kHalfAny,       // any other r: partners come through shared memory
 };
 
-// One thread's share of one row: VEC pairs (two vectors of VEC elements), or
-// VEC elements past the rotated part to copy.
-template <int VEC, bool BF16>
-struct RopeItem {
-  Pack<VEC, BF16> a, b;
-  const uint16_t* src;
-  uint16_t* dst;  // nullptr: nothing to store
+// Eight 16-bit elements.
+union Vec8 {
+  uint4 v;
+  uint16_t h[8];
 };
+
+template <bool BF16>
+__device__ __forceinline__ float to_float(uint16_t h) {
+  if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(h) << 16);
+  else return __half2float(__ushort_as_half(h));
+}
+template <bool BF16>
+__device__ __forceinline__ uint16_t from_float(float x) {
+  if constexpr (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+  else return __half_as_ushort(__float2half_rn(x));
+}
 
 }  // namespace
 
-// VEC: pairs per item, the largest power of two up to 8 that divides r, so
-// that every vector is aligned.  APPEND: rows of a packed batch whose K goes
-// to its pages and whose V is copied there.
-template <int VEC, bool INTER, bool BF16, bool APPEND>
+// APPEND: rows of a packed batch; K rows go to their pages, and V rows (after
+// the K rows of a token) are copied to theirs.
+template <RopeForm FORM, bool BF16, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p) {
-  __shared__ float2 s_cs[kRopeMaxTok * kRopeMaxPairs];
-  __shared__ int64_t s_slot[kRopeMaxTok];  // element offset of the token's K (and V) row in the cache; -1: none
+  __shared__ float2 s_cs[kRopeMaxAngles];
+  __shared__ int64_t s_slot[APPEND ? kRopeMaxTok : 1];  // element offset of the token's rows in the caches; -1: none
+  __shared__ uint4 s_rows[FORM == kHalfAny ? kRopeThreads * 2 * kRopeRows : 1];
 
   int tile = blockIdx.x;
   int tok0, n_tok;  // the CTA's tokens
-  int pos0 = 0;  // append: cache position of token tok0
+  int pos0 = 0;     // append: cache position of token tok0
   int b = 0;
   if constexpr (APPEND) {
     b = tile / p.tiles;
@@ -114,140 +98,155 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
   }
   if (n_tok <= 0) return;
 
-  // Angles of the CTA's tokens, and (append) where their rows go.
-  for (int i = threadIdx.x; i < n_tok * p.r; i += kRopeThreads) {
-    const int t = i / p.r, j = i - t * p.r;
-    int pos;
-    if (APPEND && p.positions == nullptr) pos = pos0 + t;
-    else pos = __ldg(p.positions + tok0 + t);
-    const unsigned long long phase =
-        static_cast<unsigned long long>(static_cast<long long>(pos)) * __ldg(p.steps + j);
-    float s, c;
-    sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-    s_cs[i] = make_float2(c * p.mag, s * p.mag_sin);
+  const int r = p.r, D = p.D;
+  const int rot_heads = p.H + p.H_kv;                  // rows that turn
+  const int heads = rot_heads + (APPEND ? p.H_kv : 0);  // rows of a token: Q, K (and V)
+  const int n_rows = n_tok * heads;
+  const int lanes = kRopeThreads >> p.log2_items;  // rows the CTA takes at once
+  const int col = static_cast<int>(threadIdx.x) & ((1 << p.log2_items) - 1);
+  // This thread's two vectors of a row that turns; of a V row they are 16 col, 16 col + 8.
+  bool turns;  // kHalf: its columns turn
+  int oa, ob;
+  if (FORM == kHalf) {
+    turns = 8 * col < r;
+    oa = turns ? 8 * col : 2 * r + 16 * (col - r / 8);
+    ob = turns ? oa + r : oa + 8;
+  } else {
+    turns = 16 * col < 2 * r;
+    oa = 16 * col;
+    ob = oa + 8;
   }
-  if constexpr (APPEND) {
-    if (static_cast<int>(threadIdx.x) < n_tok) {
-      const int pos = pos0 + static_cast<int>(threadIdx.x);
-      const int page = __ldg(p.block_table + static_cast<int64_t>(b) * p.table_stride + (pos >> p.page_shift));
-      int64_t slot = -1;
-      if (page >= 0 && page < p.num_pages)
-        slot = static_cast<int64_t>(page) * p.page_stride +
-               static_cast<int64_t>(pos & ((1 << p.page_shift) - 1)) * p.row_stride;
-      else
-        ptx::record_error(p.err, kErrBadPage);
-      s_slot[threadIdx.x] = slot;
-    }
-  }
-  __syncthreads();
 
-  // Items of a row: R of VEC pairs, then C copies of VEC elements.
-  const int R = p.r / VEC;
-  const int heads = p.H + p.H_kv;
-  auto rows_of = [&](int row, const uint16_t** src, uint16_t** dst, int* t) {
-    *t = row / heads;
-    const int h = row - *t * heads;
-    const int64_t tk = tok0 + *t;
-    if (h < p.H) {
-      *src = static_cast<const uint16_t*>(p.q) + tk * p.q_stride + h * p.D;
-      *dst = static_cast<uint16_t*>(p.q_out) + tk * p.q_out_stride + h * p.D;
-    } else {
-      const int g = h - p.H;
-      *src = static_cast<const uint16_t*>(p.k) + tk * p.k_stride + g * p.D;
-      if constexpr (APPEND) {
-        const int64_t slot = s_slot[*t];
-        *dst = slot < 0 ? nullptr : static_cast<uint16_t*>(p.k_out) + slot + g * p.head_stride;
-      } else {
-        *dst = static_cast<uint16_t*>(p.k_out) + tk * p.k_out_stride + g * p.D;
+  for (int base = static_cast<int>(threadIdx.x) >> p.log2_items, round = 0; round == 0 || base - (static_cast<int>(threadIdx.x) >> p.log2_items) < n_rows;
+       base += kRopeRows * lanes, ++round) {
+    Vec8 x[kRopeRows], y[kRopeRows];
+#pragma unroll
+    for (int u = 0; u < kRopeRows; ++u) {
+      const int row = base + u * lanes;
+      if (row < n_rows) {
+        const int t = row / heads, h = row - t * heads;
+        const int64_t tk = tok0 + t;
+        const uint16_t* src;
+        if (h < p.H) src = static_cast<const uint16_t*>(p.q) + tk * p.q_stride + h * D;
+        else if (!APPEND || h < rot_heads) src = static_cast<const uint16_t*>(p.k) + tk * p.k_stride + (h - p.H) * D;
+        else src = static_cast<const uint16_t*>(p.v) + tk * p.v_stride + (h - rot_heads) * D;
+        const bool v_row = APPEND && h >= rot_heads;
+        x[u].v = *reinterpret_cast<const uint4*>(src + (v_row ? 16 * col : oa));
+        y[u].v = *reinterpret_cast<const uint4*>(src + (v_row ? 16 * col + 8 : ob));
       }
     }
-  };
-  using P = Pack<VEC, BF16>;
-  using V = typename P::V;
-  const int per = R + p.copies;  // items per row (at most 64)
-  const int lanes = kRopeThreads / per;
-  const int n_rows = n_tok * heads;
-  const int col = static_cast<int>(threadIdx.x) % per, row_first = static_cast<int>(threadIdx.x) / per;
-  if (row_first < lanes) {
-    const bool turn = col < R;
-    const int oa = turn ? (INTER ? 2 * VEC * col : VEC * col) : 2 * p.r + VEC * (col - R);
-    const int ob = INTER ? oa + VEC : oa + p.r;
-    for (int row = row_first; row < n_rows; row += 2 * lanes) {
-      P a[2], bb[2];
-      const uint16_t* src[2];
-      uint16_t* dst[2] = {nullptr, nullptr};
-      int t[2] = {0, 0};
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (row + u * lanes < n_rows) {
-          rows_of(row + u * lanes, &src[u], &dst[u], &t[u]);
-          a[u].v = *reinterpret_cast<const V*>(src[u] + oa);
-          if (turn) bb[u].v = *reinterpret_cast<const V*>(src[u] + ob);
+    if (round == 0) {
+      // Angles of the CTA's tokens, and (append) where their rows go.
+      for (int i = threadIdx.x; i < n_tok * r; i += kRopeThreads) {
+        const int t = i / r, j = i - t * r;
+        int pos;
+        if (APPEND && p.positions == nullptr) pos = pos0 + t;
+        else pos = __ldg(p.positions + tok0 + t);
+        const unsigned long long phase =
+            static_cast<unsigned long long>(static_cast<long long>(pos)) * __ldg(p.steps + j);
+        float s, c;
+        sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+        s_cs[i] = make_float2(c * p.mag, s * p.mag_sin);
+      }
+      if constexpr (APPEND) {
+        for (int i = threadIdx.x; i < n_tok; i += kRopeThreads) {
+          const int pos = pos0 + i;
+          const int page = __ldg(p.block_table + static_cast<int64_t>(b) * p.table_stride + (pos >> p.page_shift));
+          int64_t slot = -1;
+          if (page >= 0 && page < p.num_pages)
+            slot = static_cast<int64_t>(page) * p.page_stride +
+                   static_cast<int64_t>(pos & ((1 << p.page_shift) - 1)) * p.row_stride;
+          else
+            ptx::record_error(p.err, kErrBadPage);
+          s_slot[i] = slot;
         }
       }
+      __syncthreads();
+    }
+    uint16_t* stage = reinterpret_cast<uint16_t*>(s_rows);
+    if constexpr (FORM == kHalfAny) {
+      // A row's threads are neighbours in one warp: each row's D elements side by side.
+      __syncwarp();
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (dst[u] == nullptr) continue;
-        if (turn) {
-          const float2* cs = s_cs + t[u] * p.r + VEC * col;
-          P x, y;
+      for (int u = 0; u < kRopeRows; ++u) {
+        s_rows[2 * (u * kRopeThreads + static_cast<int>(threadIdx.x))] = x[u].v;
+        s_rows[2 * (u * kRopeThreads + static_cast<int>(threadIdx.x)) + 1] = y[u].v;
+      }
+      __syncwarp();
+    }
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            float va, vb;
-            if constexpr (INTER) {  // pair i: elements 2i, 2i + 1 of the 2 VEC
-              va = 2 * i < VEC ? a[u].get((2 * i) % VEC) : bb[u].get((2 * i) % VEC);
-              vb = 2 * i + 1 < VEC ? a[u].get((2 * i + 1) % VEC) : bb[u].get((2 * i + 1) % VEC);
-            } else {
-              va = a[u].get(i);
-              vb = bb[u].get(i);
-            }
-            const float2 w = cs[i];
-            const float ra = va * w.x - vb * w.y, rb = vb * w.x + va * w.y;
-            if constexpr (INTER) {
-              if (2 * i < VEC) x.set((2 * i) % VEC, ra); else y.set((2 * i) % VEC, ra);
-              if (2 * i + 1 < VEC) x.set((2 * i + 1) % VEC, rb); else y.set((2 * i + 1) % VEC, rb);
-            } else {
-              x.set(i, ra);
-              y.set(i, rb);
+    for (int u = 0; u < kRopeRows; ++u) {
+      const int row = base + u * lanes;
+      if (row >= n_rows) continue;
+      const int t = row / heads, h = row - t * heads;
+      const int64_t tk = tok0 + t;
+      uint16_t* dst;
+      const bool v_row = APPEND && h >= rot_heads;
+      if (h < p.H) {
+        dst = static_cast<uint16_t*>(p.q_out) + tk * p.q_out_stride + h * D;
+      } else if constexpr (APPEND) {
+        if (s_slot[t] < 0) continue;
+        dst = v_row ? static_cast<uint16_t*>(p.v_out) + s_slot[t] + (h - rot_heads) * p.head_stride
+                    : static_cast<uint16_t*>(p.k_out) + s_slot[t] + (h - p.H) * p.head_stride;
+      } else {
+        dst = static_cast<uint16_t*>(p.k_out) + tk * p.k_out_stride + (h - p.H) * D;
+      }
+      if (turns && !v_row) {
+        const float2* cs = s_cs + t * r;
+        if constexpr (FORM == kHalf) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 w = cs[oa + i];
+            const float a = to_float<BF16>(x[u].h[i]), bb = to_float<BF16>(y[u].h[i]);
+            x[u].h[i] = from_float<BF16>(a * w.x - bb * w.y);
+            y[u].h[i] = from_float<BF16>(bb * w.x + a * w.y);
+          }
+        } else if constexpr (FORM == kInterleaved) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = oa / 2 + i;  // the pair
+            if (j < r) {
+              Vec8& v = i < 4 ? x[u] : y[u];
+              const float2 w = cs[j];
+              const float a = to_float<BF16>(v.h[2 * (i & 3)]), bb = to_float<BF16>(v.h[2 * (i & 3) + 1]);
+              v.h[2 * (i & 3)] = from_float<BF16>(a * w.x - bb * w.y);
+              v.h[2 * (i & 3) + 1] = from_float<BF16>(bb * w.x + a * w.y);
             }
           }
-          *reinterpret_cast<V*>(dst[u] + oa) = x.v;
-          *reinterpret_cast<V*>(dst[u] + ob) = y.v;
         } else {
-          *reinterpret_cast<V*>(dst[u] + oa) = a[u].v;
+          // Column c pairs with c + r (c < r) or c - r, read from the staged row.
+          const uint16_t* line = stage + 16 * (u * kRopeThreads + static_cast<int>(threadIdx.x) - col);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int c = oa + i;
+            if (c < 2 * r) {
+              Vec8& v = i < 8 ? x[u] : y[u];
+              const bool low = c < r;
+              const float2 w = cs[low ? c : c - r];
+              const float own = to_float<BF16>(v.h[i & 7]), other = to_float<BF16>(line[low ? c + r : c - r]);
+              v.h[i & 7] = from_float<BF16>(low ? own * w.x - other * w.y : own * w.x + other * w.y);
+            }
+          }
         }
       }
-    }
-  }
-  if constexpr (APPEND) {  // V rows, 8 elements an item
-    const int pv = p.D / 8;
-    for (int i = threadIdx.x; i < n_tok * p.H_kv * pv; i += kRopeThreads) {
-      const int c = i % pv, rh = i / pv;
-      const int t = rh / p.H_kv, g = rh - t * p.H_kv;
-      if (s_slot[t] < 0) continue;
-      const uint16_t* src = static_cast<const uint16_t*>(p.v) + static_cast<int64_t>(tok0 + t) * p.v_stride +
-                            g * p.D + 8 * c;
-      uint16_t* dst = static_cast<uint16_t*>(p.v_out) + s_slot[t] + g * p.head_stride + 8 * c;
-      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+      *reinterpret_cast<uint4*>(dst + (v_row ? 16 * col : oa)) = x[u].v;
+      *reinterpret_cast<uint4*>(dst + (v_row ? 16 * col + 8 : ob)) = y[u].v;
     }
   }
 }
 
 namespace {
 
-template <int VEC, bool INTER, bool BF16>
-cudaError_t launch_rope_t(RopeParams p, bool append, dim3 grid, cudaStream_t stream) {
-  p.copies = p.copy_rest ? (p.D - 2 * p.r) / VEC : 0;
-  if (append) fa_rope_kernel<VEC, INTER, BF16, true><<<grid, kRopeThreads, 0, stream>>>(p);
-  else fa_rope_kernel<VEC, INTER, BF16, false><<<grid, kRopeThreads, 0, stream>>>(p);
+template <RopeForm FORM>
+cudaError_t launch_rope_f(const RopeParams& p, bool bf16, bool append, unsigned grid, cudaStream_t s) {
+  if (append) {
+    if (bf16) fa_rope_kernel<FORM, true, true><<<grid, kRopeThreads, 0, s>>>(p);
+    else fa_rope_kernel<FORM, false, true><<<grid, kRopeThreads, 0, s>>>(p);
+  } else {
+    if (bf16) fa_rope_kernel<FORM, true, false><<<grid, kRopeThreads, 0, s>>>(p);
+    else fa_rope_kernel<FORM, false, false><<<grid, kRopeThreads, 0, s>>>(p);
+  }
   return cudaGetLastError();
-}
-
-template <int VEC>
-cudaError_t launch_rope_v(const RopeParams& p, bool bf16, bool append, dim3 grid, cudaStream_t s) {
-  if (p.interleaved)
-    return bf16 ? launch_rope_t<VEC, true, true>(p, append, grid, s) : launch_rope_t<VEC, true, false>(p, append, grid, s);
-  return bf16 ? launch_rope_t<VEC, false, true>(p, append, grid, s) : launch_rope_t<VEC, false, false>(p, append, grid, s);
 }
 
 }  // namespace
@@ -255,17 +254,17 @@ cudaError_t launch_rope_v(const RopeParams& p, bool bf16, bool append, dim3 grid
 cudaError_t launch_rope(RopeParams p, bool bf16, bool append, int batch, cudaStream_t stream) {
   const int64_t per_tok = static_cast<int64_t>(p.H + (append ? 2 : 1) * p.H_kv) * p.D;
   int64_t tok = kRopeElems / per_tok;
+  if (p.r > 0 && tok > kRopeMaxAngles / p.r) tok = kRopeMaxAngles / p.r;
   p.tok_per_cta = static_cast<int>(tok < 1 ? 1 : (tok > kRopeMaxTok ? kRopeMaxTok : tok));
+  p.log2_items = p.D == 16 ? 0 : (p.D == 32 ? 1 : (p.D == 64 ? 2 : 3));  // D / 16 threads a row
   const int longest = append ? p.max_len : p.total;
   p.tiles = (longest + p.tok_per_cta - 1) / p.tok_per_cta;
   const int64_t ctas = static_cast<int64_t>(p.tiles) * (append ? batch : 1);
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(ctas));
-  const int r = p.r;
-  if (r % 8 == 0) return launch_rope_v<8>(p, bf16, append, grid, stream);
-  if (r % 4 == 0) return launch_rope_v<4>(p, bf16, append, grid, stream);
-  if (r % 2 == 0) return launch_rope_v<2>(p, bf16, append, grid, stream);
-  return launch_rope_v<1>(p, bf16, append, grid, stream);
+  const unsigned grid = static_cast<unsigned>(ctas);
+  if (p.interleaved) return launch_rope_f<kInterleaved>(p, bf16, append, grid, stream);
+  if (p.r % 8 == 0) return launch_rope_f<kHalf>(p, bf16, append, grid, stream);
+  return launch_rope_f<kHalfAny>(p, bf16, append, grid, stream);
 }
 
 }  // namespace fa

@@ -1,5 +1,6 @@
 """Pins for the rotary and paged-cache oracles, and the host helpers of the rotary entry points (no GPU)."""
 import cmath
+import ctypes
 import math
 
 import pytest
@@ -157,7 +158,7 @@ def _cache(**kw):
     a = dict(k=P, v=P, block_table=P, kv_lens=P, table_stride=8, num_pages=10, page_size=16, page_stride=16 * 128,
              row_stride=128, head_stride=64)
     a.update(kw)
-    return fa.PagedCache(**a)
+    return ctypes.byref(fa.PagedCache(**a))
 
 
 CACHE_BAD = [
