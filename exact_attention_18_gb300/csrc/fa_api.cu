@@ -562,11 +562,23 @@ fa_status rope_impl(const void* q, int64_t q_stride, const void* k, int64_t k_st
   return from_cuda(fa::launch_rope(p, dtype == FA_BF16, false, 1, static_cast<cudaStream_t>(stream)), "rope launch");
 }
 
-// Rows of a unit (tokens x group) the paged kernel runs with, and its tiling.
-struct PagedPlan {
-  int N, tok_tile, tiles, grid;
-  size_t o_bytes, lse_bytes, bytes;
+// One of the two paged-attention kernels in a call: its tiling, and its share
+// of the workspace.
+struct PagedPart {
+  bool used = false;
+  int N;               // fa_paged_kernel: rows it is instantiated for
+  int tok_tile, tiles, grid, part_rows;
+  int64_t rows_lo, rows_hi;
+  size_t o_at, lse_at, desc_at;  // byte offsets in the workspace
 };
+struct PagedPlan {
+  PagedPart few, tile;
+  size_t bytes;
+};
+
+// Query rows (new tokens x group) of a sequence up to which the keys-on-rows
+// kernel takes it: one of its units.
+constexpr int64_t kFewRows = 128;
 
 // The tiling of a call; false when it is empty or has too many units.
 bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t H_kv, int64_t D, PagedPlan* plan) {
@@ -575,20 +587,40 @@ bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t 
       H >= (int64_t(1) << 20))
     return false;
   const int64_t G = H / H_kv;
-  plan->N = fa::paged_rows(max_q * G > 128 ? 128 : max_q * G);
-  int64_t tok = plan->N / G;
-  if (tok > max_q) tok = max_q;
-  plan->tok_tile = static_cast<int>(tok);
-  plan->tiles = static_cast<int>((max_q + tok - 1) / tok);
-  if (batch > (int64_t(1) << 30) / plan->tiles) return false;
-  const int64_t units = batch * plan->tiles;       // at most 2^30
-  const int64_t blocks = (max_k + 127) / 128 + 1;  // of a unit, at most
-  if (units > (int64_t(1) << 37) / (blocks * H_kv)) return false;  // a CTA's run of blocks fits 31 bits
-  const int64_t most = units * H_kv * blocks;
-  plan->grid = static_cast<int>(most < fa::kPagedGrid ? most : fa::kPagedGrid);
-  plan->o_bytes = round256(static_cast<size_t>(2) * plan->grid * plan->N * D * sizeof(float));
-  plan->lse_bytes = round256(static_cast<size_t>(2) * plan->grid * plan->N * sizeof(float));
-  plan->bytes = plan->o_bytes + plan->lse_bytes + round256(static_cast<size_t>(plan->grid) * sizeof(int4));
+  plan->bytes = 0;
+  auto add = [&](PagedPart* part, int64_t tok, int64_t longest, int64_t block, int64_t slot_rows) -> bool {
+    part->used = true;
+    part->tok_tile = static_cast<int>(tok < longest ? tok : longest);
+    part->tiles = static_cast<int>((longest + part->tok_tile - 1) / part->tok_tile);
+    part->part_rows = static_cast<int>(slot_rows);
+    if (batch > (int64_t(1) << 30) / part->tiles) return false;
+    const int64_t units = batch * part->tiles;               // at most 2^30
+    const int64_t blocks = (max_k + block - 1) / block + 1;  // of a unit, at most
+    if (units > (int64_t(1) << 37) / (blocks * H_kv)) return false;  // a CTA's run of blocks fits 31 bits
+    const int64_t most = units * H_kv * blocks;
+    part->grid = static_cast<int>(most < fa::kPagedGrid ? most : fa::kPagedGrid);
+    part->o_at = plan->bytes;
+    part->lse_at = part->o_at + round256(static_cast<size_t>(2) * part->grid * part->part_rows * D * sizeof(float));
+    part->desc_at = part->lse_at + round256(static_cast<size_t>(2) * part->grid * part->part_rows * sizeof(float));
+    plan->bytes = part->desc_at + round256(static_cast<size_t>(part->grid) * sizeof(int4));
+    return true;
+  };
+  const bool chunks = max_q * G > kFewRows;
+  // Sequences of few rows: all of them, or those of a mixed batch.
+  if (!chunks || batch > 1) {
+    const int64_t longest = chunks ? kFewRows / G : max_q;
+    plan->few.N = fa::paged_rows(longest * G);
+    plan->few.rows_lo = 0;
+    plan->few.rows_hi = chunks ? longest * G : max_q * G;
+    if (!add(&plan->few, longest, longest, 128, plan->few.N)) return false;
+  }
+  if (chunks) {
+    const int Di = static_cast<int>(D);
+    plan->tile.rows_lo = plan->few.used ? plan->few.rows_hi + 1 : 0;
+    plan->tile.rows_hi = max_q * G;
+    const int64_t tok = fa::paged_tile_tiles(Di) * (128 / G);
+    if (!add(&plan->tile, tok, max_q, fa::paged_tile_block(Di), tok * G)) return false;
+  }
   return true;
 }
 
@@ -612,9 +644,9 @@ fa_status encode_paged_q(CUtensorMap* map, const void* q, bool bf16, int64_t tot
 }
 
 // Tensor map of the cache's K or V: {D, H_kv, page_size, num_pages}, box
-// {row chunk, 1, min(page_size, 128), 1}.  Pages from num_pages on read zero.
+// {row chunk, 1, min(page_size, block), 1}.  Pages from num_pages on read zero.
 fa_status encode_paged_kv(CUtensorMap* map, const void* base, bool bf16, const fa_paged_cache* c, int64_t H_kv,
-                          int64_t D, const char* name) {
+                          int64_t D, int64_t block, const char* name) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const int rb = fa::row_bytes_for(static_cast<int>(D));
@@ -623,7 +655,7 @@ fa_status encode_paged_kv(CUtensorMap* map, const void* base, bool bf16, const f
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->head_stride * 2), static_cast<cuuint64_t>(c->row_stride * 2),
                            static_cast<cuuint64_t>(c->page_stride * 2)};
   cuuint32_t box[4] = {static_cast<cuuint32_t>(rb / 2), 1u,
-                       static_cast<cuuint32_t>(c->page_size < 128 ? c->page_size : 128), 1u};
+                       static_cast<cuuint32_t>(c->page_size < block ? c->page_size : block), 1u};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   CUtensorMapSwizzle swz = rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                      : (rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
@@ -986,11 +1018,6 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
     return fail(FA_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
   const bool bf16 = dtype == FA_BF16;
   const int64_t G = H / H_kv;
-  CUtensorMap tq, tk, tv;
-  if ((st = encode_paged_q(&tq, q, bf16, total, H, D, G, plan.tok_tile)) ||
-      (st = encode_paged_kv(&tk, cache->k, bf16, cache, H_kv, D, "cache.k")) ||
-      (st = encode_paged_kv(&tv, cache->v, bf16, cache, H_kv, D, "cache.v")))
-    return st;
   fa::PagedParams p = {};
   p.o = o;
   p.lse = lse;
@@ -1005,8 +1032,6 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
   p.total = static_cast<int>(total);
   p.max_q = static_cast<int>(max_seqlen_q);
   p.max_k = static_cast<int>(max_seqlen_k < table_keys(cache) ? max_seqlen_k : table_keys(cache));
-  p.tok_tile = plan.tok_tile;
-  p.tiles = plan.tiles;
   p.win_left = window_left < 0 || window_left >= max_seqlen_k ? fa::kNoWindow : static_cast<int>(window_left);
   p.win_right =
       causal ? 0 : (window_right < 0 || window_right >= max_seqlen_k + max_seqlen_q ? fa::kNoWindow : static_cast<int>(window_right));
@@ -1014,22 +1039,58 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
   p.num_pages = static_cast<int>(cache->num_pages);
   p.min_share = 1;
   p.scale_log2 = scale * kLog2e;
-  char* ws = static_cast<char*>(workspace);
-  p.o_part = reinterpret_cast<float*>(ws);
-  p.lse_part = reinterpret_cast<float*>(ws + plan.o_bytes);
-  p.desc = reinterpret_cast<int4*>(ws + plan.o_bytes + plan.lse_bytes);
   p.err = fa::device_error_word();
   if (!p.err) return fail(FA_ERR_CUDA, "cannot resolve the device error word on the current device");
   p.wait_ns = fa::wait_limit_ns();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaErrorInvalidValue;
-  switch (D) {
-    case 16: e = fa::launch_paged_d16(plan.N, bf16, tq, tk, tv, p, plan.grid, s); break;
-    case 32: e = fa::launch_paged_d32(plan.N, bf16, tq, tk, tv, p, plan.grid, s); break;
-    case 64: e = fa::launch_paged_d64(plan.N, bf16, tq, tk, tv, p, plan.grid, s); break;
-    case 128: e = fa::launch_paged_d128(plan.N, bf16, tq, tk, tv, p, plan.grid, s); break;
-  }
-  return from_cuda(e, "paged attention launch");
+  char* ws = static_cast<char*>(workspace);
+  fa::PagedMergeParams mp = {};
+  mp.o = o;
+  mp.lse = lse;
+  mp.G = p.G;
+  mp.H = p.H;
+  mp.total = p.total;
+  int sets = 0, grid = 0;
+  auto run = [&](const PagedPart& part, bool tile) -> fa_status {
+    p.tok_tile = part.tok_tile;
+    p.tiles = part.tiles;
+    p.rows_lo = part.rows_lo;
+    p.rows_hi = part.rows_hi;
+    p.part_rows = part.part_rows;
+    p.o_part = reinterpret_cast<float*>(ws + part.o_at);
+    p.lse_part = reinterpret_cast<float*>(ws + part.lse_at);
+    p.desc = reinterpret_cast<int4*>(ws + part.desc_at);
+    mp.parts[sets++] = fa::PagedParts{p.o_part, p.lse_part, p.desc, part.part_rows, part.grid};
+    if (part.grid > grid) grid = part.grid;
+    const int Di = static_cast<int>(D);
+    const int64_t block = tile ? fa::paged_tile_block(Di) : 128;
+    CUtensorMap tq, tk, tv;
+    fa_status r;
+    if ((r = encode_paged_q(&tq, q, bf16, total, H, D, G, tile ? static_cast<int>(128 / G) : part.tok_tile)) ||
+        (r = encode_paged_kv(&tk, cache->k, bf16, cache, H_kv, D, block, "cache.k")) ||
+        (r = encode_paged_kv(&tv, cache->v, bf16, cache, H_kv, D, block, "cache.v")))
+      return r;
+    cudaError_t e = cudaErrorInvalidValue;
+    if (tile) {
+      switch (D) {
+        case 16: e = fa::launch_paged_tile_d16(bf16, tq, tk, tv, p, part.grid, s); break;
+        case 32: e = fa::launch_paged_tile_d32(bf16, tq, tk, tv, p, part.grid, s); break;
+        case 64: e = fa::launch_paged_tile_d64(bf16, tq, tk, tv, p, part.grid, s); break;
+        case 128: e = fa::launch_paged_tile_d128(bf16, tq, tk, tv, p, part.grid, s); break;
+      }
+    } else {
+      switch (D) {
+        case 16: e = fa::launch_paged_d16(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 32: e = fa::launch_paged_d32(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 64: e = fa::launch_paged_d64(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 128: e = fa::launch_paged_d128(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
+      }
+    }
+    return from_cuda(e, "paged attention launch");
+  };
+  if (plan.few.used && (st = run(plan.few, false))) return st;
+  if (plan.tile.used && (st = run(plan.tile, true))) return st;
+  return from_cuda(fa::launch_paged_merge(static_cast<int>(D), bf16, mp, grid, sets, s), "paged merge launch");
 }
 
 const char* fa_status_string(fa_status status) {

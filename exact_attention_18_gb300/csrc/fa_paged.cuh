@@ -46,8 +46,8 @@ struct RopeParams {
 cudaError_t launch_rope(RopeParams p, bool bf16, bool append, int batch, cudaStream_t stream);
 
 // Attention over the cache.  A "unit" is one (sequence, tile of tok_tile
-// tokens, K/V head): its rows are tok_tile tokens x G query heads (row n =
-// token n / G, head n % G), its work the 128-key blocks its rows can see.
+// tokens, K/V head): its rows are tok_tile tokens x G query heads, its work the
+// blocks of keys its rows can see.
 struct PagedParams {
   void* o;               // [T, H, D]
   float* lse;            // [H, T] natural log
@@ -62,21 +62,51 @@ struct PagedParams {
   int tiles;             // tiles of the longest sequence: ceil(max_q / tok_tile)
   int win_left, win_right;  // key j visible to position i iff i - win_left <= j <= i + win_right (and j < kv_len)
   int page_shift, num_pages;
+  int64_t rows_lo, rows_hi;  // sequences of rows_lo .. rows_hi query rows (new tokens x G) are this kernel's
   int min_share;         // fewest blocks a CTA takes
   float scale_log2;
-  float* o_part;         // [2 grid][N][D] fp32
-  float* lse_part;       // [2 grid][N] fp32, base 2
+  int part_rows;         // rows of a partial's slot
+  float* o_part;         // [2 grid][part_rows][D] fp32
+  float* lse_part;       // [2 grid][part_rows] fp32, base 2
   int4* desc;            // [grid] unit whose first blocks CTA c computed without finishing it:
                          // {first token, tokens (0 = none), K/V head, last CTA}
   int* err;
   unsigned long long wait_ns;
 };
 
+// One main kernel's partials; parts[z] is joined by grid slice z.
+struct PagedParts {
+  const float* o_part;
+  const float* lse_part;
+  const int4* desc;
+  int rows;  // of a slot
+  int grid;  // CTAs of the main kernel
+};
+struct PagedMergeParams {
+  PagedParts parts[2];
+  void* o;
+  float* lse;
+  int G, H, total;
+};
+
 // Rows of a unit the kernel is instantiated for; the smallest that holds
 // `rows`, else the largest.
 inline int paged_rows(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
 constexpr int kPagedGrid = 152;  // CTAs at most: one per SM
+// Rows of a unit of the tile kernel (tiles of 128 rows) and keys of its blocks.
+inline int paged_tile_tiles(int D) { return D == 128 ? 2 : 4; }
+inline int paged_tile_block(int D) { return D == 128 ? 128 : 64; }
 
+cudaError_t launch_paged_tile_d16(bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const PagedParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_paged_tile_d32(bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const PagedParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_paged_tile_d64(bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const PagedParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_paged_tile_d128(bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const PagedParams& p, int grid, cudaStream_t stream);
+// A programmatic dependent of the last main kernel; `sets` of parts.
+cudaError_t launch_paged_merge(int D, bool bf16, const PagedMergeParams& p, int grid, int sets, cudaStream_t stream);
 cudaError_t launch_paged_d16(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const PagedParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_paged_d32(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -43,7 +43,7 @@
 // not be 0.
 #pragma once
 
-#include "fa_paged.cuh"
+#include "fa_paged_units.cuh"
 #include "fa_softmax.cuh"
 
 namespace fa {
@@ -51,7 +51,8 @@ using namespace ptx;
 
 namespace {
 
-constexpr int kPBlk = 128;               // keys per block
+constexpr int kPShift = 7;               // 128 keys per block
+constexpr int kPBlk = 1 << kPShift;
 constexpr float kPagedTau = 8.0f;        // log2 of the largest P~ kept with a stale maximum
 
 template <int D, int N>
@@ -82,96 +83,6 @@ struct PagedLayout {
   // V^T is D rows; the MMA's 128 rows past D repeat tile rows 8 further on
   // (in bounds: the ring is followed by the P tiles) into TMEM lanes nobody reads.
   static constexpr uint32_t kVLbo = D == 128 ? GK::kChunkBytes : 8 * GK::kRowBytes;
-};
-
-// Geometry of one unit; n_blk = 0 when it does not exist.
-struct Unit {
-  int tok0;    // first token (row of Q, O)
-  int n_tok;   // tokens
-  int pos0;    // cache position of its first token
-  int kv_len;
-  int lo, hi;  // keys any of its rows sees: [lo, hi)
-  int n_blk;   // 128-key blocks from lo / 128
-  int end_tile;  // tiles of the sequence (tiles from here on do not exist)
-};
-
-// Unit (b, tile) of the call.  A sequence whose lengths contradict the call is
-// recorded as an error and has no units.  A unit whose rows see no key keeps
-// one wholly masked block, which writes O = 0, L = -inf.
-__device__ __forceinline__ Unit paged_unit(const PagedParams& p, int b, int tile) {
-  Unit u;
-  const int a = __ldg(p.cu_seqlens + b), e = __ldg(p.cu_seqlens + b + 1), kv = __ldg(p.kv_lens + b);
-  u.n_blk = 0;
-  u.end_tile = 0;
-  u.tok0 = u.n_tok = u.pos0 = u.kv_len = u.lo = u.hi = 0;
-  if (a < 0 || e < a || e - a > p.max_q || e > p.total) {
-    record_error(p.err, kErrBadSeqlens);
-    return u;
-  }
-  if (kv < 0 || kv > p.max_k) {
-    record_error(p.err, kErrBadCache);
-    return u;
-  }
-  const int n = e - a;
-  u.end_tile = (n + p.tok_tile - 1) / p.tok_tile;
-  const int t0 = tile * p.tok_tile;
-  if (t0 >= n) return u;
-  u.tok0 = a + t0;
-  u.n_tok = min(p.tok_tile, n - t0);
-  u.pos0 = kv - n + t0;
-  u.kv_len = kv;
-  u.lo = max(0, u.pos0 - p.win_left);
-  u.hi = min(kv, u.pos0 + u.n_tok + p.win_right);
-  if (u.hi <= u.lo) {
-    u.lo = u.hi = 0;
-    u.n_blk = 1;
-  } else {
-    u.n_blk = (u.hi + kPBlk - 1) / kPBlk - u.lo / kPBlk;
-  }
-  return u;
-}
-
-// Walks the segments (runs of blocks of one unit) of a CTA's run of blocks.
-struct SegWalk {
-  int b, tile, kvh;
-  int blk;        // next block within the unit
-  int left;       // blocks left in the CTA's run
-  Unit u;
-  // Blocks of the current segment (0: the run is over).
-  __device__ __forceinline__ int seg_len() const { return min(left, u.n_blk - blk); }
-  __device__ __forceinline__ void start(const PagedParams& p, int x, int rem, int run) {
-    left = run;
-    b = tile = kvh = blk = 0;
-    u.n_blk = 0;
-    if (run <= 0) return;
-    b = x / p.tiles;
-    tile = x - b * p.tiles;
-    u = paged_unit(p, b, tile);
-    kvh = rem / u.n_blk;
-    blk = rem - kvh * u.n_blk;
-  }
-  // Past the current segment (its whole length was processed).
-  __device__ __forceinline__ void next(const PagedParams& p) {
-    left -= seg_len();
-    blk = 0;
-    if (left <= 0) {
-      left = 0;
-      return;
-    }
-    if (++kvh < p.H_kv) return;
-    kvh = 0;
-    do {
-      if (++tile >= u.end_tile) {
-        tile = 0;
-        ++b;
-      }
-      if (b >= p.batch) {  // cannot happen: the run ends inside the units
-        left = 0;
-        return;
-      }
-      u = paged_unit(p, b, tile);
-    } while (u.n_blk == 0);
-  }
 };
 
 // Sum or maximum over the warp's 32 lanes of each of NC values a lane holds
@@ -210,15 +121,6 @@ __device__ __forceinline__ uint32_t swizzled(int k, int c) {
   constexpr int kShift = ROW_BYTES == 128 ? 0 : (ROW_BYTES == 64 ? 1 : 2);
   constexpr int kMask = ROW_BYTES / 16 - 1;
   return static_cast<uint32_t>(k * ROW_BYTES + ((c ^ ((k >> kShift) & kMask)) << 4));
-}
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
-                                            int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
 }
 
 template <int NC>
@@ -303,55 +205,13 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
     s_tok[n] = static_cast<short>(n / p.G);
     s_head[n] = static_cast<short>(n % p.G);
   }
-  // This CTA's run of blocks: units x = b * tiles + tile in order, H_kv heads
-  // each.  Every thread sums a stretch of units; a block-wide scan gives the
-  // stretch that holds the run's first block.
-  {
-    long long* s_warp = reinterpret_cast<long long*>(s_red);  // free until the first segment
-    const int X = p.batch * p.tiles;
-    const int per = (X + L::kThreads - 1) / L::kThreads;
-    const int x0 = min(X, static_cast<int>(threadIdx.x) * per), x1 = min(X, x0 + per);
-    long long mine = 0;
-    for (int x = x0; x < x1; ++x) mine += paged_unit(p, x / p.tiles, x % p.tiles).n_blk;
-    long long incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += o;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < L::kThreads / 32; ++w) {
-      if (w < warp) before += s_warp[w];
-      total += s_warp[w];
-    }
-    total *= p.H_kv;
-    long long share = (total + gridDim.x - 1) / gridDim.x;
-    if (share < p.min_share) share = p.min_share;
-    const long long s = share * blockIdx.x;
-    long long at = (before + incl - mine) * p.H_kv;  // first block of this thread's stretch
-    if (s >= at && s < at + mine * p.H_kv) {
-      for (int x = x0; x < x1; ++x) {
-        const long long n = static_cast<long long>(paged_unit(p, x / p.tiles, x % p.tiles).n_blk) * p.H_kv;
-        if (s < at + n) {
-          s_start[0] = x;
-          s_start[1] = static_cast<int>(s - at);
-          s_start[2] = static_cast<int>(total - s < share ? total - s : share);
-          break;
-        }
-        at += n;
-      }
-    }
-    if (threadIdx.x == 0) s_start[3] = static_cast<int>(share);
-  }
+  paged_find_run<kPShift, L::kThreads>(p, reinterpret_cast<long long*>(s_red), s_start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   griddep_launch_dependents();
   const uint32_t tmem = *tmem_slot;
-  SegWalk w;
+  SegWalk<kPShift> w;
   w.start(p, s_start[0], s_start[1], s_start[2]);
 
   if (warp == kProducer) {
@@ -713,65 +573,6 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
   }
 }
 
-// Joins the partials of the units that were cut between CTAs:
-// L = log2 sum_s 2^(L_s), O = sum_s 2^(L_s - L) O_s, in CTA order.  CTA
-// (c, y) takes rows y, y + gridDim.y, ... of the unit whose first blocks CTA c
-// of the main kernel computed.  D / 4 threads span a row; the other threads
-// split the partials, summed in a fixed order at the end.
-template <int D, int N, bool BF16>
-__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p) {
-  using elem_t = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  constexpr int kLanes = D / 4, kGroups = 128 / kLanes;
-  __shared__ float4 s_o[kGroups][kLanes];
-  __shared__ float s_w[kGroups];
-  griddep_wait();
-  const int first = blockIdx.x;
-  const int4 d = p.desc[first];
-  const int n_rows = d.y * p.G;
-  if (n_rows == 0) return;
-  const int x = threadIdx.x % kLanes, y = threadIdx.x / kLanes;
-  const int parts = d.w - first + 1;
-  for (int row = blockIdx.y; row < n_rows; row += gridDim.y) {
-    // Partial s: slot 2 first + 1 for the first CTA, 2 c for the later ones.
-    auto slot = [&](int s) -> int64_t { return static_cast<int64_t>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * N + row; };
-    float mx = -INFINITY;
-    for (int s = 0; s < parts; ++s) mx = fmaxf(mx, p.lse_part[slot(s)]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float wsum = 0.f;
-    if (mx != -INFINITY) {
-      for (int s = y; s < parts; s += kGroups) {
-        const int64_t at = slot(s);
-        const float wt = exp2f(p.lse_part[at] - mx);
-        const float4 v = *reinterpret_cast<const float4*>(p.o_part + at * D + 4 * x);
-        wsum += wt;
-        o.x += wt * v.x; o.y += wt * v.y; o.z += wt * v.z; o.w += wt * v.w;
-      }
-    }
-    s_o[y][x] = o;
-    if (x == 0) s_w[y] = wsum;
-    __syncthreads();
-    if (y == 0) {
-      float total = 0.f;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int q = 0; q < kGroups; ++q) {
-        const float4 v = s_o[q][x];
-        total += s_w[q];
-        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-      }
-      const bool seen = mx != -INFINITY;
-      const float inv = seen ? 1.f / total : 0.f;
-      const int tok = d.x + row / p.G, head = d.z * p.G + row % p.G;
-      elem_t* orow = static_cast<elem_t*>(p.o) + (static_cast<int64_t>(tok) * p.H + head) * D;
-      *reinterpret_cast<uint2*>(orow + 4 * x) =
-          make_uint2(pack2<BF16>(a.x * inv, a.y * inv), pack2<BF16>(a.z * inv, a.w * inv));
-      if (x == 0)
-        p.lse[static_cast<int64_t>(head) * p.total + tok] =
-            seen ? (mx + log2f(total)) * 0.69314718055994530942f : -INFINITY;
-    }
-    __syncthreads();
-  }
-}
-
 namespace {
 
 template <int D, int N, bool BF16>
@@ -782,17 +583,7 @@ cudaError_t launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const C
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
   if (e != cudaSuccess) return e;
   kern<<<grid, L::kThreads, L::kSmemBytes, stream>>>(tq, tk, tv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, N < 16 ? N : 16);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<D, N, BF16>, p);
+  return cudaGetLastError();
 }
 
 template <int D>

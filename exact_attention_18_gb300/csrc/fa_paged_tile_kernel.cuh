@@ -1,0 +1,481 @@
+// Attention of prompt chunks over a paged key/value cache: the query rows of
+// a unit are the tensor core's rows.
+//
+// fa_paged_kernel.cuh puts keys on the rows, which wastes nothing when a K/V
+// head has few query rows but sends P through shared memory.  Here a unit is
+// kTiles tiles of 128 query rows of one K/V head (tokens x the group's heads,
+// so a chunk of 64 tokens with 4 heads to a K/V head already fills two tiles);
+// S = Q K^T and O += P V keep P in TMEM, and a softmax thread owns a row, as in
+// the fixed-length forward kernels (same recurrence, same stale maximum).  The
+// tiles share every K and V block.  D = 128: two tiles, 128-key blocks;
+// D <= 64: four tiles, 64-key blocks (there the exponentials bound the kernel,
+// and sixteen softmax warps hide more of each other's latency than eight).
+//
+// Units, blocks, runs and partials are fa_paged_kernel.cuh's: one persistent
+// CTA per SM takes an equal run of blocks.  Within a unit each tile starts at
+// the first block its own rows see and stops after the last.
+//
+// Per tile the MMA warp issues O += P(j) V(j), then S(j+1), then one commit:
+// "S(j+1) ready" also means "P(j) consumed, O updated", so the softmax waits
+// once per block and may rescale O as soon as it sees S(j+1).
+#pragma once
+
+#include "fa_paged_units.cuh"
+#include "fa_softmax.cuh"
+
+namespace fa {
+using namespace ptx;
+
+namespace {
+
+template <int D>
+struct PagedTileLayout {
+  static constexpr int kTiles = D == 128 ? 2 : 4;
+  static constexpr int kShift = D == 128 ? 7 : 6;
+  static constexpr int kBlk = 1 << kShift;      // keys per block
+  using GQ = TileGeom<D, 128>;
+  using GK = TileGeom<D, kBlk>;
+  static constexpr int kSoftWarps = 4 * kTiles;
+  static constexpr int kThreads = 32 * kSoftWarps + 128;  // producer, two MMA warps, one idle
+  // Register split: every thread gets kLaunchRegs at launch, the last four
+  // warps drop to kRegsLow and the softmax warps rise to kRegsHigh.
+  static constexpr int kLaunchRegs = kTiles == 2 ? 168 : 96;
+  static constexpr uint32_t kRegsHigh = kTiles == 2 ? 216 : 104;
+  static constexpr uint32_t kRegsLow = kTiles == 2 ? 72 : 64;
+  static_assert(32 * kSoftWarps * kRegsHigh + 128 * kRegsLow <= kThreads * kLaunchRegs, "register split");
+  static constexpr int kSmallBytes = 2048;
+  static constexpr int kUnitsFit = (227 * 1024 - 1024 - kTiles * GQ::kTileBytes - kSmallBytes) / GK::kTileBytes;
+  static constexpr int kUnits = kUnitsFit > 20 ? 20 : kUnitsFit;  // ring stages, one K or V block each
+  static_assert(kUnits >= 4, "ring");
+  static constexpr int kOffQ = kUnits * GK::kTileBytes;
+  static constexpr int kOffSmall = kOffQ + kTiles * GQ::kTileBytes;
+  // full[U], empty[U], qfull, qempty, sfull[T], pfull[T], ofinal[T], vtmp, drain[2]
+  static constexpr int kNumBars = 2 * kUnits + 2 + 3 * kTiles + 3;
+  static_assert(kNumBars * 8 + 64 + 32 * 8 <= kSmallBytes, "barriers");
+  static constexpr int kSmemUsed = kOffSmall + kSmallBytes + 1024;
+  static constexpr int kSmemBytes = kSmemUsed > 116 * 1024 ? kSmemUsed : 116 * 1024;  // one CTA per SM
+  static constexpr uint32_t kTileCols = 512 / kTiles;  // TMEM columns of a tile: S (P over it), then O
+  static constexpr uint32_t kColO = kBlk;
+  static_assert(kColO + D <= kTileCols, "TMEM layout");
+};
+
+// Tile t of a unit: its tokens and the blocks [beg, end) of the current
+// segment that its rows see.
+struct TileSpan {
+  int ta, n_tok;  // first token within the unit, tokens
+  int pos0;       // cache position of its first token
+  int beg, end;
+};
+
+template <int SHIFT>
+__device__ __forceinline__ TileSpan tile_span(const PagedParams& p, const SegWalk<SHIFT>& w, int t, int tile_tok,
+                                              int n) {
+  TileSpan s;
+  s.ta = t * tile_tok;
+  s.n_tok = min(tile_tok, w.u.n_tok - s.ta);
+  s.pos0 = w.u.pos0 + s.ta;
+  s.beg = s.end = 0;
+  if (s.n_tok <= 0) return s;
+  const int lo = max(0, s.pos0 - p.win_left), hi = min(w.u.kv_len, s.pos0 + s.n_tok + p.win_right);
+  if (hi <= lo) return s;
+  const int base = (w.u.lo >> SHIFT) + w.blk;  // the segment's first block
+  s.beg = min(n, max(0, (lo >> SHIFT) - base));
+  s.end = min(n, max(0, ((hi + (1 << SHIFT) - 1) >> SHIFT) - base));
+  if (s.end <= s.beg) s.beg = s.end = 0;
+  return s;
+}
+
+}  // namespace
+
+// tm_q: {D, H, T} map, box {row chunk, G, tile tokens}; tm_k, tm_v: {D, H_kv,
+// page_size, pages} maps, box {row chunk, 1, min(page_size, block), 1}.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
+    fa_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
+  using L = PagedTileLayout<D>;
+  using GQ = typename L::GQ;
+  using GK = typename L::GK;
+  using elem_t = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  using Walk = SegWalk<L::kShift>;
+  constexpr int U = L::kUnits, T = L::kTiles, BN = L::kBlk;
+  constexpr int kProducer = L::kSoftWarps, kMma0 = L::kSoftWarps + 1;
+  constexpr int kTilesPerMma = T / 2;
+  constexpr float kSumLimit = 256.0f;  // largest block sum of P~ kept with a stale maximum
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + L::kOffSmall);  // [U] block landed
+  uint64_t* bar_empty = bar_full + U;    // [U] both MMA warps are done with it
+  uint64_t* bar_qfull = bar_empty + U;   // segment's Q landed
+  uint64_t* bar_qempty = bar_qfull + 1;  // both MMA warps' last score products of the segment are done
+  uint64_t* bar_sfull = bar_qempty + 1;  // [T] S_t computed (and the P_t V before it done)
+  uint64_t* bar_pfull = bar_sfull + T;   // [T] P_t stored, O_t rescaled
+  uint64_t* bar_ofinal = bar_pfull + T;  // [T] the segment's last P_t V done
+  uint64_t* bar_vtmp = bar_ofinal + T;   // a V block that still needs rows cleared has landed
+  uint64_t* bar_drain = bar_vtmp + 1;    // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_start = reinterpret_cast<int*>(tmem_slot + 2);  // {x, rem, run, share} of this CTA's run
+  long long* s_warp = reinterpret_cast<long long*>(smem + L::kOffSmall + L::kSmallBytes - 32 * 8);
+
+  const int warp = warp_index();
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < U; ++s) {
+      mbar_init(&bar_full[s], 1);
+      mbar_init(&bar_empty[s], 2);
+    }
+    mbar_init(bar_qfull, 1);
+    mbar_init(bar_qempty, 2);
+    for (int t = 0; t < T; ++t) {
+      mbar_init(&bar_sfull[t], 1);
+      mbar_init(&bar_pfull[t], 4);
+      mbar_init(&bar_ofinal[t], 1);
+    }
+    mbar_init(bar_vtmp, 1);
+    mbar_init(&bar_drain[0], 1);
+    mbar_init(&bar_drain[1], 1);
+    *abort_flag = 0;
+    s_start[2] = 0;
+    p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    fence_mbar_init();
+  }
+  if (warp == kMma0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == kProducer && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  __syncthreads();
+  paged_find_run<L::kShift, L::kThreads>(p, s_warp, s_start);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();
+  const uint32_t tmem = *tmem_slot;
+  const int tile_tok = 128 / p.G;  // tokens of a 128-row tile
+
+  if (warp >= kProducer) {
+    regs_decrease<L::kRegsLow>();
+    Walk w;
+    w.start(p, s_start[0], s_start[1], s_start[2]);
+    if (warp == kProducer) {
+      // ------------------------------------------------------------ producer
+      // The whole warp runs this; lane i copies page box i of each block.
+      const int frag = min(BN, 1 << p.page_shift);
+      const int n_frag = BN / frag;
+      int c = 0, seg = 0, n_cut = 0;  // blocks started, segments started, V blocks that had rows cleared
+      bool ok = true;
+      auto box_page = [&](int blk) -> int {  // page (or out of range) of this lane's box of the unit's block
+        const int key = ((w.u.lo >> L::kShift) + blk) * BN + lane * frag;
+        if (lane >= n_frag || key >= w.u.hi || key + frag <= w.u.lo) return p.num_pages;
+        const int page = __ldg(p.block_table + static_cast<int64_t>(w.b) * p.table_stride + (key >> p.page_shift));
+        if (page >= 0 && page < p.num_pages) return page;
+        record_error(p.err, kErrBadPage);
+        return p.num_pages;
+      };
+      for (int n; ok && (n = w.seg_len()) > 0; w.next(p), ++seg) {
+        if (seg > 0) ok = warp_wait(bar_qempty, (seg - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
+        if (!ok) break;
+        if (lane == 0) {
+          const int tiles = (w.u.n_tok + tile_tok - 1) / tile_tok;
+          mbar_arrive_expect_tx(bar_qfull, tiles * GQ::kChunks * GQ::kRowBytes * p.G * tile_tok);
+          for (int t = 0; t < tiles; ++t)
+#pragma unroll
+            for (int ch = 0; ch < GQ::kChunks; ++ch)
+              tma_load_3d(smem + L::kOffQ + t * GQ::kTileBytes + ch * GQ::kChunkBytes, &tm_q, bar_qfull,
+                          ch * (GQ::kRowBytes / 2), w.kvh * p.G, w.u.tok0 + t * tile_tok);
+        }
+        __syncwarp();
+        int page = box_page(w.blk);
+        for (int j = 0; ok && j < n; ++j) {
+          const int page_next = j + 1 < n ? box_page(w.blk + j + 1) : 0;
+          const int key0 = ((w.u.lo >> L::kShift) + w.blk + j) * BN;
+          const int row = (key0 + lane * frag) & ((1 << p.page_shift) - 1);
+          const bool cut = key0 < w.u.lo || key0 + BN > w.u.hi;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int st = c % U, use = c / U;
+            if (use > 0) {
+              ok = warp_wait(&bar_empty[st], (use - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
+              if (!ok) break;
+            }
+            uint8_t* tile = smem + st * GK::kTileBytes;
+            uint64_t* bar = kv == 1 && cut ? bar_vtmp : &bar_full[st];
+            if (lane == 0) mbar_arrive_expect_tx(bar, GK::kTileBytes);
+            __syncwarp();
+            if (lane < n_frag) {
+#pragma unroll
+              for (int ch = 0; ch < GK::kChunks; ++ch)
+                tma_load_4d(tile + ch * GK::kChunkBytes + lane * frag * GK::kRowBytes, kv == 0 ? &tm_k : &tm_v, bar,
+                            ch * (GK::kRowBytes / 2), w.kvh, row, page);
+            }
+            ++c;
+            if (kv == 1 && cut) {
+              // Clear the V rows no row of the unit sees (0 * NaN is not 0).
+              drain_wait(bar_vtmp, n_cut & 1, p.err);
+              ++n_cut;
+              const int k0 = max(0, w.u.lo - key0), k1 = min(BN, w.u.hi - key0);  // visible rows [k0, k1)
+              constexpr int kVecs = GK::kRowBytes / 16;
+              for (int i = lane; i < BN * kVecs * GK::kChunks; i += 32) {
+                const int r = (i / kVecs) % BN;
+                if (r < k0 || r >= k1) *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar_full[st]);
+            }
+          }
+          page = page_next;
+        }
+      }
+      // Teardown: every copy this warp started lands before the CTA exits.
+      for (int x = (c > U ? c - U : 0); x < c; ++x) drain_wait(&bar_full[x % U], (x / U) & 1, p.err);
+      if (seg > 0) drain_wait(bar_qfull, (seg - 1) & 1, p.err);
+      __syncwarp();
+    } else if (warp < kMma0 + 2) {
+      // ------------------------------------------------------------ MMA issuers
+      const int m = warp - kMma0;  // tiles m * kTilesPerMma ..
+      constexpr uint32_t idesc_qk = make_idesc_f16(BF16, 128, BN, false, false);
+      constexpr uint32_t idesc_pv = make_idesc_f16(BF16, 128, D, false, true);
+      const AccFlags acc = runtime_flags(p.batch);
+      const uint32_t s_ring = smem_u32(smem), s_q = smem_u32(smem + L::kOffQ);
+      int c = 0;                     // ring blocks before the segment
+      int done[kTilesPerMma];        // blocks of each tile whose P V was issued
+#pragma unroll
+      for (int h = 0; h < kTilesPerMma; ++h) done[h] = 0;
+      bool ok = true;
+      int seg = 0;
+      for (int n; ok && (n = w.seg_len()) > 0; w.next(p), ++seg) {
+        int beg[kTilesPerMma], end[kTilesPerMma];
+#pragma unroll
+        for (int h = 0; h < kTilesPerMma; ++h) {
+          const TileSpan s = tile_span<L::kShift>(p, w, m * kTilesPerMma + h, tile_tok, n);
+          beg[h] = s.beg;
+          end[h] = s.end;
+        }
+        ok = warp_wait(bar_qfull, seg & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
+        for (int j = -1; ok && j < n; ++j) {
+          const int kc = c + 2 * (j + 1), vc = c + 2 * j + 1;  // ring blocks of K(j+1), V(j)
+          const int ks = kc % U, vs = vc % U;
+          if (j >= 0)
+            ok = warp_wait(&bar_full[vs], (vc / U) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
+          if (ok && j + 1 < n)
+            ok = warp_wait(&bar_full[ks], (kc / U) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
+          if (!ok) break;
+#pragma unroll
+          for (int h = 0; h < kTilesPerMma; ++h) {
+            const int t = m * kTilesPerMma + h;
+            const uint32_t t_s = tmem + t * L::kTileCols;
+            if (j >= beg[h] && j < end[h]) {
+              if (!ok) break;
+              ok = warp_wait(&bar_pfull[t], done[h] & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
+              if (!ok) break;
+              ++done[h];
+              tc_fence_after();
+              const uint64_t v_desc =
+                  make_sdesc(s_ring + vs * GK::kTileBytes, GK::kChunkBytes, 8 * GK::kRowBytes, GK::kSwz);
+#pragma unroll
+              for (int kk = 0; kk < BN / 16; ++kk)
+                mma_ts_warp(t_s + L::kColO, t_s + kk * 8, desc_plus(v_desc, mnmajor_step_bytes<D>(kk)), idesc_pv,
+                            (j > beg[h] || kk > 0) ? acc.on : acc.off);
+              if (j == end[h] - 1) mma_commit_warp(&bar_ofinal[t]);
+            }
+            if (j + 1 >= beg[h] && j + 1 < end[h]) {
+              tc_fence_after();
+              const uint64_t q_desc = make_sdesc(s_q + t * GQ::kTileBytes, 16, 8 * GQ::kRowBytes, GQ::kSwz);
+              const uint64_t k_desc = make_sdesc(s_ring + ks * GK::kTileBytes, 16, 8 * GK::kRowBytes, GK::kSwz);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_ss_warp(t_s, desc_plus(q_desc, kmajor_step_bytes<D, 128>(kk)),
+                            desc_plus(k_desc, kmajor_step_bytes<D, BN>(kk)), idesc_qk, kk > 0 ? acc.on : acc.off);
+              mma_commit_warp(&bar_sfull[t]);
+            }
+          }
+          if (!ok) break;
+          if (j >= 0) mma_commit_warp(&bar_empty[vs]);
+          if (j + 1 < n) mma_commit_warp(&bar_empty[ks]);
+          if (j + 1 == n - 1) mma_commit_warp(bar_qempty);
+        }
+        c += 2 * n;
+      }
+      mma_commit_warp(&bar_drain[m]);
+      drain_wait(&bar_drain[m], 0, p.err);
+    }
+  } else {
+    regs_increase<L::kRegsHigh>();
+    // -------------------------------------------------------------- softmax
+    Walk w;
+    w.start(p, s_start[0], s_start[1], s_start[2]);
+    const int t = warp >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane;  // row of the tile == TMEM lane
+    const int rt = r / p.G, rh = r - rt * p.G;  // its token within the tile, head within the group
+    const uint32_t t_s = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + t * L::kTileCols;
+    const uint32_t t_o = t_s + L::kColO;
+    const float sl2 = p.scale_log2;
+    const float2 c2 = make_float2(sl2, sl2);
+    const bool neg_scale = sl2 < 0.f;
+    int cnt = 0, fin = 0;  // blocks of this tile so far; segments in which it had blocks
+    bool alive = true;
+    long long at = static_cast<long long>(blockIdx.x) * s_start[3];  // flattened index of the segment's first block
+    for (int n; alive && (n = w.seg_len()) > 0; w.next(p)) {
+      const TileSpan sp = tile_span<L::kShift>(p, w, t, tile_tok, n);
+      const bool row_ok = rt < sp.n_tok && rt < tile_tok;
+      const int pos = sp.pos0 + rt;
+      const int last = min(w.u.kv_len - 1, pos + p.win_right), first = pos - p.win_left;
+      // Keys every row of the tile sees: [all_lo, all_hi).
+      const int all_lo = sp.pos0 + sp.n_tok - 1 - p.win_left, all_hi = min(w.u.kv_len, sp.pos0 + 1 + p.win_right);
+      const int key_base = ((w.u.lo >> L::kShift) + w.blk) * BN;
+      float m = -INFINITY, l = 0.f;
+      for (int j = sp.beg; j < sp.end; ++j, ++cnt) {
+        if (!warp_wait(&bar_sfull[t], cnt & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sr[BN];
+        if constexpr (BN == 128) tmem_ld128(t_s, sr);
+        else tmem_ld64(t_s, sr);
+        const int key0 = key_base + j * BN;
+        const int lim = last - key0, lo = first - key0;  // columns lo <= c <= lim are visible to this row
+        const bool masked = key0 < all_lo || key0 + BN > all_hi;
+        if (j == sp.beg) m = block_max_scaled<BN, true>(sr, masked, lo, lim, sl2, neg_scale);
+        float alpha = 1.f;
+        bool upd = false;
+        auto exps = [&]() {
+          const float m_use = m == -INFINITY ? 0.f : m;  // rows with no visible key so far
+          const float2 negm = make_float2(-m_use, -m_use);
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                           make_float2(0.f, 0.f)};
+          if (masked) {
+#pragma unroll
+            for (int k0 = 0; k0 < BN; k0 += 16) {
+              uint32_t pk[8];
+              exp16<BF16, true, true>(sr, k0, c2, negm, lo, lim, acc, pk);
+              tmem_st8(t_s + k0 / 2, pk);
+            }
+          } else {
+#pragma unroll
+            for (int k0 = 0; k0 < BN; k0 += 16) {
+              uint32_t pk[8];
+              exp16<BF16, false>(sr, k0, c2, negm, lo, lim, acc, pk);
+              tmem_st8(t_s + k0 / 2, pk);
+            }
+          }
+          const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+          return a.x + a.y;
+        };
+        float blk = exps();
+        // A block whose sum breaks the bound (or a row's first visible key)
+        // moves the maximum, rescales O and is done again.  Lanes past the
+        // tile's rows hold anything and never ask for it.
+        bool need = row_ok && (!(blk <= kSumLimit) || (m == -INFINITY && max(lo, 0) <= min(lim, BN - 1)));
+        if (__any_sync(0xffffffffu, need)) {
+          const float m_blk = block_max_scaled<BN, true>(sr, masked, lo, lim, sl2, neg_scale);
+          if (need && m_blk > m) {
+            alpha = ex2(m - m_blk);
+            m = m_blk;
+            upd = true;
+          }
+          if (__any_sync(0xffffffffu, upd)) {
+            tmem_st_wait();  // the first pass's stores land before they are overwritten
+            blk = exps();
+            if (j > sp.beg) {
+#pragma unroll
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o16[16];
+                tmem_ld16(t_o + c, o16);
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                  const float2 v = __fmul2_rn(make_float2(__uint_as_float(o16[i]), __uint_as_float(o16[i + 1])),
+                                              make_float2(alpha, alpha));
+                  o16[i] = __float_as_uint(v.x);
+                  o16[i + 1] = __float_as_uint(v.y);
+                }
+                tmem_st16(t_o + c, o16);
+              }
+            }
+          }
+        }
+        l = l * alpha + blk;
+        tmem_st_wait();
+        warp_arrive(&bar_pfull[t]);
+      }
+      if (!alive) break;
+      // ------------------------------------------------------------ segment's end
+      const bool have = sp.end > sp.beg;
+      if (have) {
+        if (!warp_wait(&bar_ofinal[t], fin & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax)) {
+          alive = false;
+          break;
+        }
+        ++fin;
+        tc_fence_after();
+      }
+      const bool whole = n == w.u.n_blk;
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (w.blk == 0 ? 1 : 0);
+      const bool seen = have && l > 0.f;
+      const float inv_l = seen ? 1.f / l : 0.f;
+      const int tok = w.u.tok0 + sp.ta + rt, head = w.kvh * p.G + rh;
+      const int64_t prow = static_cast<int64_t>(slot) * p.part_rows + (sp.ta + rt) * p.G + rh;
+      elem_t* orow = static_cast<elem_t*>(p.o) + (static_cast<int64_t>(tok) * p.H + head) * D;
+      if (sp.n_tok > 0) {  // (warp-uniform)
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o16[16];
+          if (have) tmem_ld16(t_o + c, o16);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o16[i] = seen ? o16[i] : 0u;
+          if (row_ok) {
+            if (whole) store_row16<BF16>(orow + c, o16, inv_l);
+            else store_row16_f32(p.o_part + prow * D + c, o16, inv_l);
+          }
+        }
+        if (row_ok) {
+          const float l2 = seen ? m + log2f(l) : -INFINITY;
+          if (whole) p.lse[static_cast<int64_t>(head) * p.total + tok] = l2 * 0.69314718055994530942f;
+          else p.lse_part[prow] = l2;
+        }
+      }
+      if (!whole && w.blk == 0 && threadIdx.x == 0)
+        p.desc[blockIdx.x] =
+            make_int4(w.u.tok0, w.u.n_tok, w.kvh, static_cast<int>((at + w.u.n_blk - 1) / s_start[3]));
+      at += n;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+namespace {
+
+template <int D, bool BF16>
+cudaError_t launch_paged_tile_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const PagedParams& p, int grid, cudaStream_t stream) {
+  using L = PagedTileLayout<D>;
+  auto kern = fa_paged_tile_kernel<D, BF16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  // The register split assumes the launch gives exactly kLaunchRegs per
+  // thread; with fewer, the softmax warps' increase could never be met.
+  cudaFuncAttributes attr;
+  e = cudaFuncGetAttributes(&attr, kern);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs != L::kLaunchRegs) return cudaErrorInvalidConfiguration;
+  kern<<<grid, L::kThreads, L::kSmemBytes, stream>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+}  // namespace fa

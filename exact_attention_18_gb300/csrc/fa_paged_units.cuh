@@ -1,0 +1,166 @@
+// What the two paged-attention kernels share: the units of a call, the run of
+// blocks a CTA takes, and the walk over it.
+#pragma once
+
+#include "fa_kernel_common.cuh"
+#include "fa_paged.cuh"
+
+namespace fa {
+using namespace ptx;
+
+namespace {
+
+// Geometry of one unit; n_blk = 0 when it does not exist.
+struct Unit {
+  int tok0;    // first token (row of Q, O)
+  int n_tok;   // tokens
+  int pos0;    // cache position of its first token
+  int kv_len;
+  int lo, hi;  // keys any of its rows sees: [lo, hi)
+  int n_blk;   // blocks of 2^SHIFT keys, from block lo >> SHIFT
+  int end_tile;  // tiles of the sequence (tiles from here on do not exist)
+};
+
+// Unit (b, tile) of the call.  A sequence whose lengths contradict the call is
+// recorded as an error and has no units.  A unit whose rows see no key keeps
+// one wholly masked block, which writes O = 0, L = -inf.
+template <int SHIFT>
+__device__ __forceinline__ Unit paged_unit(const PagedParams& p, int b, int tile) {
+  Unit u;
+  const int a = __ldg(p.cu_seqlens + b), e = __ldg(p.cu_seqlens + b + 1), kv = __ldg(p.kv_lens + b);
+  u.n_blk = 0;
+  u.end_tile = 0;
+  u.tok0 = u.n_tok = u.pos0 = u.kv_len = u.lo = u.hi = 0;
+  if (a < 0 || e < a || e - a > p.max_q || e > p.total) {
+    record_error(p.err, kErrBadSeqlens);
+    return u;
+  }
+  if (kv < 0 || kv > p.max_k) {
+    record_error(p.err, kErrBadCache);
+    return u;
+  }
+  const int n = e - a;
+  const long long rows = static_cast<long long>(n) * p.G;
+  if (rows < p.rows_lo || rows > p.rows_hi) return u;  // another kernel of the call takes this sequence
+  u.end_tile = (n + p.tok_tile - 1) / p.tok_tile;
+  const int t0 = tile * p.tok_tile;
+  if (t0 >= n) return u;
+  u.tok0 = a + t0;
+  u.n_tok = min(p.tok_tile, n - t0);
+  u.pos0 = kv - n + t0;
+  u.kv_len = kv;
+  u.lo = max(0, u.pos0 - p.win_left);
+  u.hi = min(kv, u.pos0 + u.n_tok + p.win_right);
+  if (u.hi <= u.lo) {
+    u.lo = u.hi = 0;
+    u.n_blk = 1;
+  } else {
+    u.n_blk = ((u.hi + (1 << SHIFT) - 1) >> SHIFT) - (u.lo >> SHIFT);
+  }
+  return u;
+}
+
+// Walks the segments (runs of blocks of one unit) of a CTA's run of blocks.
+template <int SHIFT>
+struct SegWalk {
+  int b, tile, kvh;
+  int blk;        // next block within the unit
+  int left;       // blocks left in the CTA's run
+  Unit u;
+  // Blocks of the current segment (0: the run is over).
+  __device__ __forceinline__ int seg_len() const { return min(left, u.n_blk - blk); }
+  __device__ __forceinline__ void start(const PagedParams& p, int x, int rem, int run) {
+    left = run;
+    b = tile = kvh = blk = 0;
+    u.n_blk = 0;
+    if (run <= 0) return;
+    b = x / p.tiles;
+    tile = x - b * p.tiles;
+    u = paged_unit<SHIFT>(p, b, tile);
+    kvh = rem / u.n_blk;
+    blk = rem - kvh * u.n_blk;
+  }
+  // Past the current segment (its whole length was processed).
+  __device__ __forceinline__ void next(const PagedParams& p) {
+    left -= seg_len();
+    blk = 0;
+    if (left <= 0) {
+      left = 0;
+      return;
+    }
+    if (++kvh < p.H_kv) return;
+    kvh = 0;
+    do {
+      if (++tile >= u.end_tile) {
+        tile = 0;
+        ++b;
+      }
+      if (b >= p.batch) {  // cannot happen: the run ends inside the units
+        left = 0;
+        return;
+      }
+      u = paged_unit<SHIFT>(p, b, tile);
+    } while (u.n_blk == 0);
+  }
+};
+
+// This CTA's run of blocks, into s_start = {x, rem, run, share}: block rem of
+// unit group x = b * tiles + tile (its H_kv heads one after another), `run`
+// blocks, `share` blocks per CTA.  The blocks of all units, in order, are cut
+// into equal shares: every thread sums a stretch of units, and a block-wide
+// scan gives the stretch that holds the CTA's first block.  s_start[2] must be
+// 0 on entry; s_warp: one entry per warp.  Ends with the writes unsynchronised.
+template <int SHIFT, int THREADS>
+__device__ __forceinline__ void paged_find_run(const PagedParams& p, long long* s_warp, int* s_start) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int X = p.batch * p.tiles;
+  const int per = (X + THREADS - 1) / THREADS;
+  const int x0 = min(X, static_cast<int>(threadIdx.x) * per), x1 = min(X, x0 + per);
+  long long mine = 0;
+  for (int x = x0; x < x1; ++x) mine += paged_unit<SHIFT>(p, x / p.tiles, x % p.tiles).n_blk;
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  total *= p.H_kv;
+  long long share = (total + gridDim.x - 1) / gridDim.x;
+  if (share < p.min_share) share = p.min_share;
+  const long long s = share * blockIdx.x;
+  long long at = (before + incl - mine) * p.H_kv;  // first block of this thread's stretch
+  if (s >= at && s < at + mine * p.H_kv) {
+    for (int x = x0; x < x1; ++x) {
+      const long long n = static_cast<long long>(paged_unit<SHIFT>(p, x / p.tiles, x % p.tiles).n_blk) * p.H_kv;
+      if (s < at + n) {
+        s_start[0] = x;
+        s_start[1] = static_cast<int>(s - at);
+        s_start[2] = static_cast<int>(total - s < share ? total - s : share);
+        break;
+      }
+      at += n;
+    }
+  }
+  if (threadIdx.x == 0) s_start[3] = static_cast<int>(share);
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+}  // namespace
+
+}  // namespace fa
