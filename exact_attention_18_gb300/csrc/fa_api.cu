@@ -1080,16 +1080,18 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
       }
     } else {
       switch (D) {
-        case 16: e = fa::launch_paged_d16(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
-        case 32: e = fa::launch_paged_d32(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
-        case 64: e = fa::launch_paged_d64(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
-        case 128: e = fa::launch_paged_d128(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 16: e = fa::launch_paged_d16(part.N, bf16, tq, tk, tv, p, part.grid, plan.tile.used, s); break;
+        case 32: e = fa::launch_paged_d32(part.N, bf16, tq, tk, tv, p, part.grid, plan.tile.used, s); break;
+        case 64: e = fa::launch_paged_d64(part.N, bf16, tq, tk, tv, p, part.grid, plan.tile.used, s); break;
+        case 128: e = fa::launch_paged_d128(part.N, bf16, tq, tk, tv, p, part.grid, plan.tile.used, s); break;
       }
     }
     return from_cuda(e, "paged attention launch");
   };
-  if (plan.few.used && (st = run(plan.few, false))) return st;
+  // The long sequences first; the few-row kernel starts as a programmatic
+  // dependent, in the shadow of the tile kernel's last CTAs.
   if (plan.tile.used && (st = run(plan.tile, true))) return st;
+  if (plan.few.used && (st = run(plan.few, false))) return st;
   return from_cuda(fa::launch_paged_merge(static_cast<int>(D), bf16, mp, grid, sets, s), "paged merge launch");
 }
 

@@ -107,13 +107,14 @@ cudaError_t launch_paged_tile_d128(bool bf16, const CUtensorMap& tq, const CUten
                                   const PagedParams& p, int grid, cudaStream_t stream);
 // A programmatic dependent of the last main kernel; `sets` of parts.
 cudaError_t launch_paged_merge(int D, bool bf16, const PagedMergeParams& p, int grid, int sets, cudaStream_t stream);
+// dependent: a programmatic dependent of the tile kernel launched before it.
 cudaError_t launch_paged_d16(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedParams& p, int grid, cudaStream_t stream);
+                             const PagedParams& p, int grid, bool dependent, cudaStream_t stream);
 cudaError_t launch_paged_d32(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedParams& p, int grid, cudaStream_t stream);
+                             const PagedParams& p, int grid, bool dependent, cudaStream_t stream);
 cudaError_t launch_paged_d64(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedParams& p, int grid, cudaStream_t stream);
+                             const PagedParams& p, int grid, bool dependent, cudaStream_t stream);
 cudaError_t launch_paged_d128(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const PagedParams& p, int grid, cudaStream_t stream);
+                              const PagedParams& p, int grid, bool dependent, cudaStream_t stream);
 
 }  // namespace fa

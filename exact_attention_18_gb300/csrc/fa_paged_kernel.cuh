@@ -60,12 +60,15 @@ struct PagedLayout {
   using GK = TileGeom<D, kPBlk>;   // K and V tiles
   using GQ = TileGeom<D, N>;       // Q tile, N rows
   using GP = TileGeom<N, kPBlk>;   // P^T tile: 128 keys x N rows
-  static constexpr int kWgs = N > 64 ? 2 : 1;       // softmax warpgroups, each over kCols rows
-  static constexpr int kCols = N / kWgs;
+  // Softmax warpgroups, each over kCols rows.  32 rows a thread: with 64 a
+  // block of N = 64 took 2200 cycles of softmax (one warp per SM sub-partition
+  // hides nothing), above the 1400 that D = 64 has at the memory's rate.
+  static constexpr int kCols = N < 32 ? N : 32;
+  static constexpr int kWgs = N / kCols;
   static constexpr int kThreads = 128 * kWgs + 64;
   static constexpr int kQBufs = N > 64 ? 1 : 2;
   static constexpr int kQBytes = (GQ::kTileBytes + 1023) / 1024 * 1024;
-  static constexpr int kSmallBytes = 4096 + 512;    // barriers and per-row arrays
+  static constexpr int kSmallBytes = 5 * 1024;      // barriers and per-row arrays
   static constexpr int kBudget = 227 * 1024 - 1024;
   static constexpr int kUnitsFit = (kBudget - 2 * GP::kTileBytes - kQBufs * kQBytes - kSmallBytes) / GK::kTileBytes;
   static constexpr int kUnits = kUnitsFit > 16 ? 16 : kUnitsFit;  // ring stages, one K or V tile each
@@ -75,7 +78,7 @@ struct PagedLayout {
   static constexpr int kOffSmall = kOffQ + kQBufs * kQBytes;
   // full[U], empty[U], qfull[2], qempty[2], sfull[2], pfull[2], pv[2], vtmp, drain
   static constexpr int kNumBars = 2 * kUnits + 10 + 2;
-  static_assert(kNumBars * 8 + 64 + 8 * N * 4 <= kSmallBytes, "small arrays");
+  static_assert(kNumBars * 8 + 24 + sizeof(RunStart) + 8 * N * 4 + 2 * N <= kSmallBytes, "small arrays");
   // One CTA per SM: the request is padded above half of the SM's shared memory.
   static constexpr int kSmemUsed = kOffSmall + kSmallBytes + 1024;
   static constexpr int kSmemBytes = kSmemUsed > 116 * 1024 ? kSmemUsed : 116 * 1024;
@@ -161,17 +164,23 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
   uint64_t* bar_drain = bar_vtmp + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* s_start = reinterpret_cast<int*>(tmem_slot + 2);  // {x, rem, run, share} of this CTA's run
-  float* s_m = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bar_full) + L::kNumBars * 8 + 48);
+  RunStart* s_start = reinterpret_cast<RunStart*>(tmem_slot + 2);
+  float* s_m = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bar_full) + L::kNumBars * 8 + 8 + sizeof(RunStart));
   s_m = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(s_m) + 15) & ~static_cast<uintptr_t>(15));
   float* s_negm = s_m + N;          // [N] -(maximum), 0 while no key was seen
   float* s_alpha = s_negm + N;      // [N] factor of the last change of maximum; at a segment's end 1 / l
   float* s_red = s_alpha + N;       // [N][4] per-warp partial of each row
-  short* s_tok = reinterpret_cast<short*>(s_red + 4 * N);  // [N] token of row n
-  short* s_head = s_tok + N;                               // [N] head of row n within the group
+  int* s_off = reinterpret_cast<int*>(s_red + 4 * N);     // [N] output row of row n after its unit's first
+  short* s_tok = reinterpret_cast<short*>(s_off + N);     // [N] token of row n
 
   const int warp = warp_index();
   const int lane = threadIdx.x & 31;
+  SeqLens own{0, 0, 0};
+  {
+    int per;
+    const int x0 = paged_first_unit(p, L::kThreads, &per);
+    if (x0 < p.batch * p.tiles) own = seq_lens(p, p.tiles == 1 ? x0 : x0 / p.tiles);
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < U; ++s) {
@@ -188,7 +197,9 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
     mbar_init(bar_vtmp, 1);
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
-    s_start[2] = 0;
+    s_start->run = 0;
+    s_start->u.n_blk = 0;
+    s_start->blk = 0;
     p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     fence_mbar_init();
   }
@@ -203,16 +214,17 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
   }
   for (int n = threadIdx.x; n < N; n += L::kThreads) {
     s_tok[n] = static_cast<short>(n / p.G);
-    s_head[n] = static_cast<short>(n % p.G);
+    s_off[n] = (n / p.G) * p.H + n % p.G;
   }
-  paged_find_run<kPShift, L::kThreads>(p, reinterpret_cast<long long*>(s_red), s_start);
+  // (the per-row arrays are free until the first segment)
+  paged_find_run<kPShift, L::kThreads>(p, own, reinterpret_cast<long long*>(s_red), s_start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   griddep_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   SegWalk<kPShift> w;
-  w.start(p, s_start[0], s_start[1], s_start[2]);
+  w.start(*s_start);
 
   if (warp == kProducer) {
     // -------------------------------------------------------------- producer
@@ -364,15 +376,17 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
     float* alpha_s = s_alpha + g * NC;
     float* red_s = s_red + g * NC * 4;
     const short* tok_s = s_tok + g * NC;
-    const short* head_s = s_head + g * NC;
+    const int* off_s = s_off + g * NC;
     const float c = p.scale_log2;
     const float2 c2 = make_float2(c, c);
-    // P^T tile row of this key: rows' columns g NC ..  (a column chunk of 64 per warpgroup)
-    uint8_t* p_tile = smem + L::kOffP + g * GP::kChunkBytes;
+    // This warpgroup's columns of the P^T tile.
+    constexpr int kChunkCols = GP::kRowBytes / 2;
+    uint8_t* p_tile = smem + L::kOffP + (g * NC / kChunkCols) * GP::kChunkBytes;
+    const int p_chunk = (g * NC % kChunkCols) / 8;  // first 16-byte chunk of this warpgroup's rows
     int i = 0;  // block within the CTA's run
     bool alive = true;
     float l[NC];
-    long long at = static_cast<long long>(blockIdx.x) * s_start[3];  // flattened index of the segment's first block
+    long long at = static_cast<long long>(blockIdx.x) * s_start->share;  // flattened index of the segment's first block
     for (int n; alive && (n = w.seg_len()) > 0; w.next(p)) {
       const Unit& u = w.u;
       const int n_rows = u.n_tok * p.G;
@@ -495,7 +509,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
             l[k + e + 1] += pe.y;
             pk[e / 2] = pack2<BF16>(pe.x, pe.y);
           }
-          *reinterpret_cast<uint4*>(prow + swizzled<GP::kRowBytes>(key_lane, k / 8)) =
+          *reinterpret_cast<uint4*>(prow + swizzled<GP::kRowBytes>(key_lane, p_chunk + k / 8)) =
               make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
         fence_proxy_async_smem();
@@ -526,35 +540,45 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
         const int row = g * NC + wt;
         if (row < n_rows) {
           if (whole)
-            p.lse[static_cast<int64_t>(w.kvh * p.G + head_s[wt]) * p.total + u.tok0 + tok_s[wt]] =
+            p.lse[static_cast<int64_t>(w.kvh * p.G + row % p.G) * p.total + u.tok0 + tok_s[wt]] =
                 l2 * 0.69314718055994530942f;
           else
             p.lse_part[static_cast<int64_t>(slot) * N + row] = l2;
         }
       }
       if (!whole && w.blk == 0 && threadIdx.x == 0)
-        p.desc[blockIdx.x] = make_int4(u.tok0, u.n_tok, w.kvh, static_cast<int>((at + u.n_blk - 1) / s_start[3]));
+        p.desc[blockIdx.x] = make_int4(u.tok0, u.n_tok, w.kvh, static_cast<int>((at + u.n_blk - 1) / s_start->share));
       named_sync(bar_id, 128);
       tc_fence_after();
+      // Lane d of the warps holds column d of every row's O: a row is one
+      // coalesced store per warp.
+      const int rows_here = n_rows - g * NC;
+      float* part = p.o_part + (static_cast<int64_t>(slot) * N + g * NC) * D + key_lane;
+      elem_t* out = static_cast<elem_t*>(p.o) + (static_cast<int64_t>(u.tok0) * p.H + w.kvh * p.G) * D + key_lane;
 #pragma unroll
       for (int k0 = 0; k0 < NC; k0 += 16) {
-        if (g * NC + k0 >= n_rows) break;
-        uint32_t o16[16];
-        tmem_ld16(t_o + k0, o16);
-        if (key_lane < D) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int k = k0 + e;
-            if (g * NC + k >= n_rows) break;
-            const float inv = alpha_s[k];
-            const float v = inv == 0.f ? 0.f : __uint_as_float(o16[e]) * inv;
+        if (k0 < rows_here) {  // (warp-uniform)
+          uint32_t o16[16];
+          tmem_ld16(t_o + k0, o16);
+          if (key_lane < D) {
             if (whole) {
-              elem_t* orow = static_cast<elem_t*>(p.o) +
-                             (static_cast<int64_t>(u.tok0 + tok_s[k]) * p.H + w.kvh * p.G + head_s[k]) * D;
-              if constexpr (BF16) orow[key_lane] = __float2bfloat16_rn(v);
-              else orow[key_lane] = __float2half_rn(v);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float inv = alpha_s[k0 + e];
+                const float v = inv == 0.f ? 0.f : __uint_as_float(o16[e]) * inv;
+                if (k0 + e < rows_here) {
+                  elem_t* dst = out + static_cast<int64_t>(off_s[k0 + e]) * D;
+                  if constexpr (BF16) *dst = __float2bfloat16_rn(v);
+                  else *dst = __float2half_rn(v);
+                }
+              }
             } else {
-              p.o_part[(static_cast<int64_t>(slot) * N + g * NC + k) * D + key_lane] = v;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float inv = alpha_s[k0 + e];
+                const float v = inv == 0.f ? 0.f : __uint_as_float(o16[e]) * inv;
+                if (k0 + e < rows_here) part[(k0 + e) * D] = v;
+              }
             }
           }
         }
@@ -571,33 +595,49 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
+  // As a dependent of the tile kernel this grid shares nothing with it, but
+  // must not complete before it: the merge waits for this grid alone.
+  griddep_wait();
 }
 
 namespace {
 
 template <int D, int N, bool BF16>
 cudaError_t launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
-                           int grid, cudaStream_t stream) {
+                           int grid, bool dependent, cudaStream_t stream) {
   using L = PagedLayout<D, N>;
   auto kern = fa_paged_kernel<D, N, BF16>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<grid, L::kThreads, L::kSmemBytes, stream>>>(tq, tk, tv, p);
-  return cudaGetLastError();
+  if (!dependent) {
+    kern<<<grid, L::kThreads, L::kSmemBytes, stream>>>(tq, tk, tv, p);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p);
 }
 
 template <int D>
 cudaError_t launch_paged_n(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                           const PagedParams& p, int grid, cudaStream_t s) {
+                           const PagedParams& p, int grid, bool dependent, cudaStream_t s) {
   switch (N) {
-    case 16: return bf16 ? launch_paged_t<D, 16, true>(tq, tk, tv, p, grid, s)
-                         : launch_paged_t<D, 16, false>(tq, tk, tv, p, grid, s);
-    case 32: return bf16 ? launch_paged_t<D, 32, true>(tq, tk, tv, p, grid, s)
-                         : launch_paged_t<D, 32, false>(tq, tk, tv, p, grid, s);
-    case 64: return bf16 ? launch_paged_t<D, 64, true>(tq, tk, tv, p, grid, s)
-                         : launch_paged_t<D, 64, false>(tq, tk, tv, p, grid, s);
-    case 128: return bf16 ? launch_paged_t<D, 128, true>(tq, tk, tv, p, grid, s)
-                          : launch_paged_t<D, 128, false>(tq, tk, tv, p, grid, s);
+    case 16: return bf16 ? launch_paged_t<D, 16, true>(tq, tk, tv, p, grid, dependent, s)
+                         : launch_paged_t<D, 16, false>(tq, tk, tv, p, grid, dependent, s);
+    case 32: return bf16 ? launch_paged_t<D, 32, true>(tq, tk, tv, p, grid, dependent, s)
+                         : launch_paged_t<D, 32, false>(tq, tk, tv, p, grid, dependent, s);
+    case 64: return bf16 ? launch_paged_t<D, 64, true>(tq, tk, tv, p, grid, dependent, s)
+                         : launch_paged_t<D, 64, false>(tq, tk, tv, p, grid, dependent, s);
+    case 128: return bf16 ? launch_paged_t<D, 128, true>(tq, tk, tv, p, grid, dependent, s)
+                          : launch_paged_t<D, 128, false>(tq, tk, tv, p, grid, dependent, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -1,5 +1,5 @@
 // Joins the partials of the units that the paged-attention kernels cut between
-// CTAs.
+// CTAs (comment at the kernel).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -9,15 +9,20 @@
 namespace fa {
 using namespace ptx;
 
-// Joins the partials of the units that were cut between CTAs:
-// L = log2 sum_s 2^(L_s), O = sum_s 2^(L_s - L) O_s, in CTA order.  CTA
-// (c, y) takes rows y, y + gridDim.y, ... of the unit whose first blocks CTA c
-// of the main kernel computed.  D / 4 threads span a row; the other threads
-// split the partials, summed in a fixed order at the end.
+// L = log2 sum_s 2^(L_s), O = sum_s 2^(L_s - L) O_s, in CTA order: fixed by
+// the lengths alone.  Slice c of the grid joins the unit whose first blocks CTA
+// c of the main kernel computed; D / 4 threads span a row.  A CTA takes several
+// rows at once; only a unit in many parts (a long context, few rows) has them
+// one by one, the parts split over the CTA and summed in a fixed order.  The
+// partials come from L2; three dependent reads (descriptor, logsumexps,
+// partials) bound a CTA, so the grid is kept to a few CTAs per SM.
+constexpr int kMergeThreads = 256;
+constexpr int kMergeFew = 24;  // parts up to which a CTA takes several rows at once
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedMergeParams p) {
+__global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const PagedMergeParams p) {
   using elem_t = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  constexpr int kLanes = D / 4, kGroups = 128 / kLanes;
+  constexpr int kLanes = D / 4, kGroups = kMergeThreads / kLanes;
   __shared__ float4 s_o[kGroups][kLanes];
   __shared__ float s_w[kGroups];
   griddep_wait();
@@ -26,23 +31,57 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedMergePar
   if (first >= q.grid) return;
   const int4 d = q.desc[first];
   const int n_rows = d.y * p.G;
-  if (n_rows == 0) return;
   const int x = threadIdx.x % kLanes, y = threadIdx.x / kLanes;
   const int parts = d.w - first + 1;
+  // Row `row` of part s: slot 2 first + 1 for the first CTA, 2 c for the later ones.
+  auto at = [&](int s, int row) -> int64_t {
+    return static_cast<int64_t>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * q.rows + row;
+  };
+  auto store = [&](int row, float4 a, float total, float mx) {
+    const bool seen = mx != -INFINITY;
+    const float inv = seen ? 1.f / total : 0.f;
+    const int tok = d.x + row / p.G, head = d.z * p.G + row % p.G;
+    elem_t* orow = static_cast<elem_t*>(p.o) + (static_cast<int64_t>(tok) * p.H + head) * D;
+    *reinterpret_cast<uint2*>(orow + 4 * x) =
+        make_uint2(pack2<BF16>(a.x * inv, a.y * inv), pack2<BF16>(a.z * inv, a.w * inv));
+    if (x == 0)
+      p.lse[static_cast<int64_t>(head) * p.total + tok] =
+          seen ? (mx + log2f(total)) * 0.69314718055994530942f : -INFINITY;
+  };
+  auto add = [&](float4& o, float w, const float4 v) {
+    o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+  };
+  if (parts <= kMergeFew) {
+    for (int row = static_cast<int>(blockIdx.y) * kGroups + y; row < n_rows; row += gridDim.y * kGroups) {
+      float mx = -INFINITY;
+#pragma unroll 4
+      for (int s = 0; s < parts; ++s) mx = fmaxf(mx, q.lse_part[at(s, row)]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float total = 0.f;
+      if (mx != -INFINITY) {
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+          const float w = exp2f(q.lse_part[at(s, row)] - mx);
+          total += w;
+          add(o, w, *reinterpret_cast<const float4*>(q.o_part + at(s, row) * D + 4 * x));
+        }
+      }
+      store(row, o, total, mx);
+    }
+    return;
+  }
   for (int row = blockIdx.y; row < n_rows; row += gridDim.y) {
-    // Partial s: slot 2 first + 1 for the first CTA, 2 c for the later ones.
-    auto slot = [&](int s) -> int64_t { return static_cast<int64_t>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * q.rows + row; };
     float mx = -INFINITY;
-    for (int s = 0; s < parts; ++s) mx = fmaxf(mx, q.lse_part[slot(s)]);
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) mx = fmaxf(mx, q.lse_part[at(s, row)]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float wsum = 0.f;
     if (mx != -INFINITY) {
+#pragma unroll 4
       for (int s = y; s < parts; s += kGroups) {
-        const int64_t at = slot(s);
-        const float wt = exp2f(q.lse_part[at] - mx);
-        const float4 v = *reinterpret_cast<const float4*>(q.o_part + at * D + 4 * x);
-        wsum += wt;
-        o.x += wt * v.x; o.y += wt * v.y; o.z += wt * v.z; o.w += wt * v.w;
+        const float w = exp2f(q.lse_part[at(s, row)] - mx);
+        wsum += w;
+        add(o, w, *reinterpret_cast<const float4*>(q.o_part + at(s, row) * D + 4 * x));
       }
     }
     s_o[y][x] = o;
@@ -52,19 +91,10 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedMergePar
       float total = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int k = 0; k < kGroups; ++k) {
-        const float4 v = s_o[k][x];
         total += s_w[k];
-        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+        add(a, 1.f, s_o[k][x]);
       }
-      const bool seen = mx != -INFINITY;
-      const float inv = seen ? 1.f / total : 0.f;
-      const int tok = d.x + row / p.G, head = d.z * p.G + row % p.G;
-      elem_t* orow = static_cast<elem_t*>(p.o) + (static_cast<int64_t>(tok) * p.H + head) * D;
-      *reinterpret_cast<uint2*>(orow + 4 * x) =
-          make_uint2(pack2<BF16>(a.x * inv, a.y * inv), pack2<BF16>(a.z * inv, a.w * inv));
-      if (x == 0)
-        p.lse[static_cast<int64_t>(head) * p.total + tok] =
-            seen ? (mx + log2f(total)) * 0.69314718055994530942f : -INFINITY;
+      store(row, a, total, mx);
     }
     __syncthreads();
   }
@@ -75,8 +105,12 @@ namespace {
 template <int D, bool BF16>
 cudaError_t launch_paged_merge_t(const PagedMergeParams& p, int grid, int sets, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 16, sets);
-  cfg.blockDim = dim3(128);
+  // Slices for the widest unit's rows: two rounds of a CTA's rows each, 16 at most.
+  const int rows = sets > 1 && p.parts[1].rows > p.parts[0].rows ? p.parts[1].rows : p.parts[0].rows;
+  const int per = 2 * kMergeThreads / (D / 4);
+  const int slices = (rows + per - 1) / per;
+  cfg.gridDim = dim3(grid, slices < 8 ? 8 : (slices > 16 ? 16 : slices), sets);
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

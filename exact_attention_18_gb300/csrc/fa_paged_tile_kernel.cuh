@@ -51,7 +51,7 @@ struct PagedTileLayout {
   static constexpr int kOffSmall = kOffQ + kTiles * GQ::kTileBytes;
   // full[U], empty[U], qfull, qempty, sfull[T], pfull[T], ofinal[T], vtmp, drain[2]
   static constexpr int kNumBars = 2 * kUnits + 2 + 3 * kTiles + 3;
-  static_assert(kNumBars * 8 + 64 + 32 * 8 <= kSmallBytes, "barriers");
+  static_assert(kNumBars * 8 + 8 + sizeof(RunStart) + 32 * 8 <= kSmallBytes, "barriers");
   static constexpr int kSmemUsed = kOffSmall + kSmallBytes + 1024;
   static constexpr int kSmemBytes = kSmemUsed > 116 * 1024 ? kSmemUsed : 116 * 1024;  // one CTA per SM
   static constexpr uint32_t kTileCols = 512 / kTiles;  // TMEM columns of a tile: S (P over it), then O
@@ -116,11 +116,17 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   uint64_t* bar_drain = bar_vtmp + 1;    // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* s_start = reinterpret_cast<int*>(tmem_slot + 2);  // {x, rem, run, share} of this CTA's run
+  RunStart* s_start = reinterpret_cast<RunStart*>(tmem_slot + 2);
   long long* s_warp = reinterpret_cast<long long*>(smem + L::kOffSmall + L::kSmallBytes - 32 * 8);
 
   const int warp = warp_index();
   const int lane = threadIdx.x & 31;
+  SeqLens own{0, 0, 0};
+  {
+    int per;
+    const int x0 = paged_first_unit(p, L::kThreads, &per);
+    if (x0 < p.batch * p.tiles) own = seq_lens(p, p.tiles == 1 ? x0 : x0 / p.tiles);
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < U; ++s) {
@@ -138,7 +144,9 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     mbar_init(&bar_drain[0], 1);
     mbar_init(&bar_drain[1], 1);
     *abort_flag = 0;
-    s_start[2] = 0;
+    s_start->run = 0;
+    s_start->u.n_blk = 0;
+    s_start->blk = 0;
     p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     fence_mbar_init();
   }
@@ -151,8 +159,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  __syncthreads();
-  paged_find_run<L::kShift, L::kThreads>(p, s_warp, s_start);
+  paged_find_run<L::kShift, L::kThreads>(p, own, s_warp, s_start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   if (warp >= kProducer) {
     regs_decrease<L::kRegsLow>();
     Walk w;
-    w.start(p, s_start[0], s_start[1], s_start[2]);
+    w.start(*s_start);
     if (warp == kProducer) {
       // ------------------------------------------------------------ producer
       // The whole warp runs this; lane i copies page box i of each block.
@@ -311,7 +318,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     regs_increase<L::kRegsHigh>();
     // -------------------------------------------------------------- softmax
     Walk w;
-    w.start(p, s_start[0], s_start[1], s_start[2]);
+    w.start(*s_start);
     const int t = warp >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane;  // row of the tile == TMEM lane
     const int rt = r / p.G, rh = r - rt * p.G;  // its token within the tile, head within the group
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     const bool neg_scale = sl2 < 0.f;
     int cnt = 0, fin = 0;  // blocks of this tile so far; segments in which it had blocks
     bool alive = true;
-    long long at = static_cast<long long>(blockIdx.x) * s_start[3];  // flattened index of the segment's first block
+    long long at = static_cast<long long>(blockIdx.x) * s_start->share;  // flattened index of the segment's first block
     for (int n; alive && (n = w.seg_len()) > 0; w.next(p)) {
       const TileSpan sp = tile_span<L::kShift>(p, w, t, tile_tok, n);
       const bool row_ok = rt < sp.n_tok && rt < tile_tok;
@@ -444,7 +451,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       }
       if (!whole && w.blk == 0 && threadIdx.x == 0)
         p.desc[blockIdx.x] =
-            make_int4(w.u.tok0, w.u.n_tok, w.kvh, static_cast<int>((at + w.u.n_blk - 1) / s_start[3]));
+            make_int4(w.u.tok0, w.u.n_tok, w.kvh, static_cast<int>((at + w.u.n_blk - 1) / s_start->share));
       at += n;
     }
   }

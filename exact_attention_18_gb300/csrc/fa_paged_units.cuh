@@ -24,10 +24,16 @@ struct Unit {
 // Unit (b, tile) of the call.  A sequence whose lengths contradict the call is
 // recorded as an error and has no units.  A unit whose rows see no key keeps
 // one wholly masked block, which writes O = 0, L = -inf.
+struct SeqLens {
+  int a, e, kv;  // cu_seqlens[b], cu_seqlens[b + 1], kv_lens[b]
+};
+__device__ __forceinline__ SeqLens seq_lens(const PagedParams& p, int b) {
+  return SeqLens{__ldg(p.cu_seqlens + b), __ldg(p.cu_seqlens + b + 1), __ldg(p.kv_lens + b)};
+}
 template <int SHIFT>
-__device__ __forceinline__ Unit paged_unit(const PagedParams& p, int b, int tile) {
+__device__ __forceinline__ Unit paged_unit(const PagedParams& p, const SeqLens& s, int tile) {
   Unit u;
-  const int a = __ldg(p.cu_seqlens + b), e = __ldg(p.cu_seqlens + b + 1), kv = __ldg(p.kv_lens + b);
+  const int a = s.a, e = s.e, kv = s.kv;
   u.n_blk = 0;
   u.end_tile = 0;
   u.tok0 = u.n_tok = u.pos0 = u.kv_len = u.lo = u.hi = 0;
@@ -60,6 +66,14 @@ __device__ __forceinline__ Unit paged_unit(const PagedParams& p, int b, int tile
   return u;
 }
 
+// Where a CTA's run of blocks starts (in shared memory).
+struct RunStart {
+  int b, tile, kvh, blk;  // unit and block within it
+  int run;                // blocks of this CTA
+  int share;              // blocks of every CTA but the last
+  Unit u;
+};
+
 // Walks the segments (runs of blocks of one unit) of a CTA's run of blocks.
 template <int SHIFT>
 struct SegWalk {
@@ -69,16 +83,13 @@ struct SegWalk {
   Unit u;
   // Blocks of the current segment (0: the run is over).
   __device__ __forceinline__ int seg_len() const { return min(left, u.n_blk - blk); }
-  __device__ __forceinline__ void start(const PagedParams& p, int x, int rem, int run) {
-    left = run;
-    b = tile = kvh = blk = 0;
-    u.n_blk = 0;
-    if (run <= 0) return;
-    b = x / p.tiles;
-    tile = x - b * p.tiles;
-    u = paged_unit<SHIFT>(p, b, tile);
-    kvh = rem / u.n_blk;
-    blk = rem - kvh * u.n_blk;
+  __device__ __forceinline__ void start(const RunStart& s) {
+    b = s.b;
+    tile = s.tile;
+    kvh = s.kvh;
+    blk = s.blk;
+    left = s.run;
+    u = s.u;
   }
   // Past the current segment (its whole length was processed).
   __device__ __forceinline__ void next(const PagedParams& p) {
@@ -99,25 +110,43 @@ struct SegWalk {
         left = 0;
         return;
       }
-      u = paged_unit<SHIFT>(p, b, tile);
+      u = paged_unit<SHIFT>(p, seq_lens(p, b), tile);
     } while (u.n_blk == 0);
   }
 };
 
-// This CTA's run of blocks, into s_start = {x, rem, run, share}: block rem of
-// unit group x = b * tiles + tile (its H_kv heads one after another), `run`
-// blocks, `share` blocks per CTA.  The blocks of all units, in order, are cut
-// into equal shares: every thread sums a stretch of units, and a block-wide
-// scan gives the stretch that holds the CTA's first block.  s_start[2] must be
-// 0 on entry; s_warp: one entry per warp.  Ends with the writes unsynchronised.
-template <int SHIFT, int THREADS>
-__device__ __forceinline__ void paged_find_run(const PagedParams& p, long long* s_warp, int* s_start) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// This CTA's run of blocks.  The blocks of all units (x = b * tiles + tile in
+// order, H_kv heads each) are cut into equal shares: every thread sums a
+// stretch of units, and a block-wide scan gives the stretch that holds the
+// CTA's first block.  `own`: the lengths of this thread's first unit, loaded
+// by the caller before its other set-up so that they arrive meanwhile.
+// s_warp: one entry per warp.  Ends with the writes to *start unsynchronised;
+// start->run and start->u must be zero on entry.
+__device__ __forceinline__ int paged_first_unit(const PagedParams& p, int threads, int* per) {
   const int X = p.batch * p.tiles;
-  const int per = (X + THREADS - 1) / THREADS;
-  const int x0 = min(X, static_cast<int>(threadIdx.x) * per), x1 = min(X, x0 + per);
+  *per = X <= threads ? 1 : (X + threads - 1) / threads;
+  return min(X, static_cast<int>(threadIdx.x) * *per);
+}
+
+template <int SHIFT, int THREADS>
+__device__ __forceinline__ void paged_find_run(const PagedParams& p, const SeqLens& own, long long* s_warp,
+                                               RunStart* start) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int per;
+  const int x0 = paged_first_unit(p, THREADS, &per), x1 = min(p.batch * p.tiles, x0 + per);
+  int b = p.tiles == 1 ? x0 : x0 / p.tiles, tile = x0 - b * p.tiles;
+  Unit u0;
+  u0.n_blk = 0;
   long long mine = 0;
-  for (int x = x0; x < x1; ++x) mine += paged_unit<SHIFT>(p, x / p.tiles, x % p.tiles).n_blk;
+  for (int x = x0; x < x1; ++x) {
+    const Unit u = paged_unit<SHIFT>(p, x == x0 ? own : seq_lens(p, b), tile);
+    if (x == x0) u0 = u;
+    mine += u.n_blk;
+    if (++tile == p.tiles) {
+      tile = 0;
+      ++b;
+    }
+  }
   long long incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
@@ -129,27 +158,43 @@ __device__ __forceinline__ void paged_find_run(const PagedParams& p, long long* 
   long long before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
+    const long long v = s_warp[w];
+    if (w < warp) before += v;
+    total += v;
   }
   total *= p.H_kv;
-  long long share = (total + gridDim.x - 1) / gridDim.x;
+  // (a 64-bit division costs hundreds of cycles, and few calls need one)
+  long long share = total >> 31 == 0
+                        ? (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x
+                        : (total + gridDim.x - 1) / gridDim.x;
   if (share < p.min_share) share = p.min_share;
   const long long s = share * blockIdx.x;
   long long at = (before + incl - mine) * p.H_kv;  // first block of this thread's stretch
   if (s >= at && s < at + mine * p.H_kv) {
+    b = p.tiles == 1 ? x0 : x0 / p.tiles;
+    tile = x0 - b * p.tiles;
+    Unit u = u0;
     for (int x = x0; x < x1; ++x) {
-      const long long n = static_cast<long long>(paged_unit<SHIFT>(p, x / p.tiles, x % p.tiles).n_blk) * p.H_kv;
+      if (x > x0) u = paged_unit<SHIFT>(p, seq_lens(p, b), tile);
+      const long long n = static_cast<long long>(u.n_blk) * p.H_kv;
       if (s < at + n) {
-        s_start[0] = x;
-        s_start[1] = static_cast<int>(s - at);
-        s_start[2] = static_cast<int>(total - s < share ? total - s : share);
+        const int rem = static_cast<int>(s - at);
+        start->b = b;
+        start->tile = tile;
+        start->kvh = rem / u.n_blk;
+        start->blk = rem - start->kvh * u.n_blk;
+        start->run = static_cast<int>(total - s < share ? total - s : share);
+        start->u = u;
         break;
       }
       at += n;
+      if (++tile == p.tiles) {
+        tile = 0;
+        ++b;
+      }
     }
   }
-  if (threadIdx.x == 0) s_start[3] = static_cast<int>(share);
+  if (threadIdx.x == 0) start->share = static_cast<int>(share);
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
