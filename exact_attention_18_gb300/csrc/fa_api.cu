@@ -1057,10 +1057,11 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
     p.rows_lo = part.rows_lo;
     p.rows_hi = part.rows_hi;
     p.part_rows = part.part_rows;
+    p.after_tile = !tile && plan.tile.used;
     p.o_part = reinterpret_cast<float*>(ws + part.o_at);
     p.lse_part = reinterpret_cast<float*>(ws + part.lse_at);
     p.desc = reinterpret_cast<int4*>(ws + part.desc_at);
-    mp.parts[sets++] = fa::PagedParts{p.o_part, p.lse_part, p.desc, part.part_rows, part.grid};
+    mp.parts[sets++] = fa::PagedParts{p.o_part, p.lse_part, p.desc, part.part_rows, part.grid, tile ? 1 : 0};
     if (part.grid > grid) grid = part.grid;
     const int Di = static_cast<int>(D);
     const int64_t block = tile ? fa::paged_tile_block(Di) : 128;
@@ -1080,16 +1081,15 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
       }
     } else {
       switch (D) {
-        case 16: e = fa::launch_paged_d16(part.N, bf16, tq, tk, tv, p, part.grid, plan.tile.used, s); break;
-        case 32: e = fa::launch_paged_d32(part.N, bf16, tq, tk, tv, p, part.grid, plan.tile.used, s); break;
-        case 64: e = fa::launch_paged_d64(part.N, bf16, tq, tk, tv, p, part.grid, plan.tile.used, s); break;
-        case 128: e = fa::launch_paged_d128(part.N, bf16, tq, tk, tv, p, part.grid, plan.tile.used, s); break;
+        case 16: e = fa::launch_paged_d16(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 32: e = fa::launch_paged_d32(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 64: e = fa::launch_paged_d64(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 128: e = fa::launch_paged_d128(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
       }
     }
     return from_cuda(e, "paged attention launch");
   };
-  // The long sequences first; the few-row kernel starts as a programmatic
-  // dependent, in the shadow of the tile kernel's last CTAs.
+  // The long sequences first: the few-row kernel's CTAs start as theirs end.
   if (plan.tile.used && (st = run(plan.tile, true))) return st;
   if (plan.few.used && (st = run(plan.few, false))) return st;
   return from_cuda(fa::launch_paged_merge(static_cast<int>(D), bf16, mp, grid, sets, s), "paged merge launch");

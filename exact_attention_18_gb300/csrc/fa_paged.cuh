@@ -10,6 +10,27 @@ namespace fa {
 // with a window side stay inside 32 bits.
 constexpr int kMaxPagedLen = 1 << 29;
 
+// Launches as a programmatic dependent of whatever precedes it on the stream:
+// the grid may start while that kernel's last CTAs run.  Every kernel launched
+// this way waits for the grids before it (griddep_wait, in every thread) ahead
+// of its first access to the caller's memory, so it also never completes
+// before them.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                    const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Row t of q starts at q + t * q_stride (elements), its head h at + h * D;
 // likewise k, v and the outputs.  Append: k_out and v_out are the caches'
 // bases, rows at page * page_stride + row * row_stride + head * head_stride.
@@ -64,9 +85,10 @@ struct PagedParams {
   int page_shift, num_pages;
   int64_t rows_lo, rows_hi;  // sequences of rows_lo .. rows_hi query rows (new tokens x G) are this kernel's
   int min_share;         // fewest blocks a CTA takes
+  int after_tile;        // few-row kernel: launched behind the tile kernel of the same call
   float scale_log2;
   int part_rows;         // rows of a partial's slot
-  float* o_part;         // [2 grid][part_rows][D] fp32
+  float* o_part;         // [2 grid][part_rows x D] fp32, laid out as in PagedParts
   float* lse_part;       // [2 grid][part_rows] fp32, base 2
   int4* desc;            // [grid] unit whose first blocks CTA c computed without finishing it:
                          // {first token, tokens (0 = none), K/V head, last CTA}
@@ -81,6 +103,7 @@ struct PagedParts {
   const int4* desc;
   int rows;  // of a slot
   int grid;  // CTAs of the main kernel
+  int by_chunk;  // o_part is [slot][D / 4][rows][4] (the tile kernel's), else [slot][rows][D]
 };
 struct PagedMergeParams {
   PagedParts parts[2];
@@ -105,16 +128,15 @@ cudaError_t launch_paged_tile_d64(bool bf16, const CUtensorMap& tq, const CUtens
                                   const PagedParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_paged_tile_d128(bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                   const PagedParams& p, int grid, cudaStream_t stream);
-// A programmatic dependent of the last main kernel; `sets` of parts.
+// `sets` of parts.
 cudaError_t launch_paged_merge(int D, bool bf16, const PagedMergeParams& p, int grid, int sets, cudaStream_t stream);
-// dependent: a programmatic dependent of the tile kernel launched before it.
 cudaError_t launch_paged_d16(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedParams& p, int grid, bool dependent, cudaStream_t stream);
+                             const PagedParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_paged_d32(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedParams& p, int grid, bool dependent, cudaStream_t stream);
+                             const PagedParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_paged_d64(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedParams& p, int grid, bool dependent, cudaStream_t stream);
+                             const PagedParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_paged_d128(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const PagedParams& p, int grid, bool dependent, cudaStream_t stream);
+                              const PagedParams& p, int grid, cudaStream_t stream);
 
 }  // namespace fa

@@ -5,8 +5,8 @@
 namespace fa {
 
 cudaError_t launch_paged_d32(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedParams& p, int grid, bool dependent, cudaStream_t stream) {
-  return launch_paged_n<32>(N, bf16, tq, tk, tv, p, grid, dependent, stream);
+                             const PagedParams& p, int grid, cudaStream_t stream) {
+  return launch_paged_n<32>(N, bf16, tq, tk, tv, p, grid, stream);
 }
 
 cudaError_t launch_paged_tile_d32(bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -5,8 +5,8 @@
 namespace fa {
 
 cudaError_t launch_paged_d64(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedParams& p, int grid, bool dependent, cudaStream_t stream) {
-  return launch_paged_n<64>(N, bf16, tq, tk, tv, p, grid, dependent, stream);
+                             const PagedParams& p, int grid, cudaStream_t stream) {
+  return launch_paged_n<64>(N, bf16, tq, tk, tv, p, grid, stream);
 }
 
 cudaError_t launch_paged_tile_d64(bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -175,13 +175,6 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
 
   const int warp = warp_index();
   const int lane = threadIdx.x & 31;
-  SeqLens own{0, 0, 0};
-  {
-    int per;
-    const int x0 = paged_first_unit(p, L::kThreads, &per);
-    if (x0 < p.batch * p.tiles) own = seq_lens(p, p.tiles == 1 ? x0 : x0 / p.tiles);
-  }
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < U; ++s) {
       mbar_init(&bar_full[s], 1);
@@ -200,7 +193,6 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
     s_start->run = 0;
     s_start->u.n_blk = 0;
     s_start->blk = 0;
-    p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     fence_mbar_init();
   }
   if (warp == kMma) {
@@ -212,6 +204,19 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
+  // Up to here nothing of the caller's was touched.  After the tile kernel of
+  // the same call there is nothing to wait for: that kernel waited for all
+  // before it, and the two share no output; but this grid must not complete
+  // before that one (the wait at the end).
+  if (!p.after_tile) griddep_wait();
+  griddep_launch_dependents();
+  SeqLens own{0, 0, 0};
+  {
+    int per;
+    const int x0 = paged_first_unit(p, L::kThreads, &per);
+    if (x0 < p.batch * p.tiles) own = seq_lens(p, p.tiles == 1 ? x0 : x0 / p.tiles);
+  }
+  if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   for (int n = threadIdx.x; n < N; n += L::kThreads) {
     s_tok[n] = static_cast<short>(n / p.G);
     s_off[n] = (n / p.G) * p.H + n % p.G;
@@ -221,7 +226,6 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  griddep_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   SegWalk<kPShift> w;
   w.start(*s_start);
@@ -244,6 +248,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
       return p.num_pages;
     };
     for (int n; ok && (n = w.seg_len()) > 0; w.next(p), ++seg) {
+      int page = box_page(w.blk);
       const int qb = L::kQBufs == 2 ? (seg & 1) : 0;
       const int qu = L::kQBufs == 2 ? (seg >> 1) : seg;
       if (qu > 0) ok = warp_wait(&bar_qempty[qb], (qu - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
@@ -255,7 +260,6 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
           tma_load_3d(smem + L::kOffQ + qb * L::kQBytes + ch * GQ::kChunkBytes, &tm_q, &bar_qfull[qb],
                       ch * (GQ::kRowBytes / 2), w.kvh * p.G, w.u.tok0);
       }
-      int page = box_page(w.blk);
       for (int j = 0; ok && j < n; ++j) {
         const int page_next = j + 1 < n ? box_page(w.blk + j + 1) : 0;
         const int key0 = (w.u.lo / kPBlk + w.blk + j) * kPBlk;
@@ -595,49 +599,33 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
-  // As a dependent of the tile kernel this grid shares nothing with it, but
-  // must not complete before it: the merge waits for this grid alone.
-  griddep_wait();
+  if (p.after_tile) griddep_wait();
 }
 
 namespace {
 
 template <int D, int N, bool BF16>
 cudaError_t launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
-                           int grid, bool dependent, cudaStream_t stream) {
+                           int grid, cudaStream_t stream) {
   using L = PagedLayout<D, N>;
   auto kern = fa_paged_kernel<D, N, BF16>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
   if (e != cudaSuccess) return e;
-  if (!dependent) {
-    kern<<<grid, L::kThreads, L::kSmemBytes, stream>>>(tq, tk, tv, p);
-    return cudaGetLastError();
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(L::kThreads);
-  cfg.dynamicSmemBytes = L::kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p);
+  return launch_dependent(kern, dim3(grid), L::kThreads, L::kSmemBytes, stream, tq, tk, tv, p);
 }
 
 template <int D>
 cudaError_t launch_paged_n(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                           const PagedParams& p, int grid, bool dependent, cudaStream_t s) {
+                           const PagedParams& p, int grid, cudaStream_t s) {
   switch (N) {
-    case 16: return bf16 ? launch_paged_t<D, 16, true>(tq, tk, tv, p, grid, dependent, s)
-                         : launch_paged_t<D, 16, false>(tq, tk, tv, p, grid, dependent, s);
-    case 32: return bf16 ? launch_paged_t<D, 32, true>(tq, tk, tv, p, grid, dependent, s)
-                         : launch_paged_t<D, 32, false>(tq, tk, tv, p, grid, dependent, s);
-    case 64: return bf16 ? launch_paged_t<D, 64, true>(tq, tk, tv, p, grid, dependent, s)
-                         : launch_paged_t<D, 64, false>(tq, tk, tv, p, grid, dependent, s);
-    case 128: return bf16 ? launch_paged_t<D, 128, true>(tq, tk, tv, p, grid, dependent, s)
-                          : launch_paged_t<D, 128, false>(tq, tk, tv, p, grid, dependent, s);
+    case 16: return bf16 ? launch_paged_t<D, 16, true>(tq, tk, tv, p, grid, s)
+                         : launch_paged_t<D, 16, false>(tq, tk, tv, p, grid, s);
+    case 32: return bf16 ? launch_paged_t<D, 32, true>(tq, tk, tv, p, grid, s)
+                         : launch_paged_t<D, 32, false>(tq, tk, tv, p, grid, s);
+    case 64: return bf16 ? launch_paged_t<D, 64, true>(tq, tk, tv, p, grid, s)
+                         : launch_paged_t<D, 64, false>(tq, tk, tv, p, grid, s);
+    case 128: return bf16 ? launch_paged_t<D, 128, true>(tq, tk, tv, p, grid, s)
+                          : launch_paged_t<D, 128, false>(tq, tk, tv, p, grid, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -26,6 +26,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const Pag
   __shared__ float4 s_o[kGroups][kLanes];
   __shared__ float s_w[kGroups];
   griddep_wait();
+  griddep_launch_dependents();
   const int first = blockIdx.x;
   const PagedParts q = p.parts[blockIdx.z];
   if (first >= q.grid) return;
@@ -37,6 +38,44 @@ __global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const Pag
   auto at = [&](int s, int row) -> int64_t {
     return static_cast<int64_t>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * q.rows + row;
   };
+  if (q.by_chunk) {
+    // Lanes span rows, as the partials lie; a warp takes 32 rows x 8 columns at a time.
+    constexpr int kPairs = D / 8;
+    const int lane = threadIdx.x & 31;
+    const int tasks = (n_rows + 31) / 32 * kPairs;
+    for (int task = static_cast<int>(blockIdx.y) * (kMergeThreads / 32) + static_cast<int>(threadIdx.x >> 5);
+         task < tasks; task += gridDim.y * (kMergeThreads / 32)) {
+      const int row = task / kPairs * 32 + lane, pair = task % kPairs;
+      if (row >= n_rows) continue;
+      float mx = -INFINITY;
+#pragma unroll 4
+      for (int s = 0; s < parts; ++s) mx = fmaxf(mx, q.lse_part[at(s, row)]);
+      const bool seen = mx != -INFINITY;
+      float total = 0.f;
+      float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (seen) {
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+          const float w = exp2f(q.lse_part[at(s, row)] - mx);
+          const float4* src = reinterpret_cast<const float4*>(q.o_part + at(s, 0) * D) + 2 * pair * q.rows + row;
+          const float4 a = src[0], b = src[q.rows];
+          total += w;
+          o[0] += w * a.x; o[1] += w * a.y; o[2] += w * a.z; o[3] += w * a.w;
+          o[4] += w * b.x; o[5] += w * b.y; o[6] += w * b.z; o[7] += w * b.w;
+        }
+      }
+      const float inv = seen ? 1.f / total : 0.f;
+      const int tok = d.x + row / p.G, head = d.z * p.G + row % p.G;
+      elem_t* orow = static_cast<elem_t*>(p.o) + (static_cast<int64_t>(tok) * p.H + head) * D + 8 * pair;
+      *reinterpret_cast<uint4*>(orow) =
+          make_uint4(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv),
+                     pack2<BF16>(o[4] * inv, o[5] * inv), pack2<BF16>(o[6] * inv, o[7] * inv));
+      if (pair == 0)
+        p.lse[static_cast<int64_t>(head) * p.total + tok] =
+            seen ? (mx + log2f(total)) * 0.69314718055994530942f : -INFINITY;
+    }
+    return;
+  }
   auto store = [&](int row, float4 a, float total, float mx) {
     const bool seen = mx != -INFINITY;
     const float inv = seen ? 1.f / total : 0.f;
@@ -104,20 +143,12 @@ namespace {
 
 template <int D, bool BF16>
 cudaError_t launch_paged_merge_t(const PagedMergeParams& p, int grid, int sets, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
   // Slices for the widest unit's rows: two rounds of a CTA's rows each, 16 at most.
   const int rows = sets > 1 && p.parts[1].rows > p.parts[0].rows ? p.parts[1].rows : p.parts[0].rows;
   const int per = 2 * kMergeThreads / (D / 4);
   const int slices = (rows + per - 1) / per;
-  cfg.gridDim = dim3(grid, slices < 8 ? 8 : (slices > 16 ? 16 : slices), sets);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<D, BF16>, p);
+  return launch_dependent(fa_paged_merge_kernel<D, BF16>, dim3(grid, slices < 8 ? 8 : (slices > 16 ? 16 : slices), sets),
+                          kMergeThreads, 0, stream, p);
 }
 
 }  // namespace

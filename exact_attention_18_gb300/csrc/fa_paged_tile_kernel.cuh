@@ -44,13 +44,17 @@ struct PagedTileLayout {
   static constexpr uint32_t kRegsLow = kTiles == 2 ? 72 : 64;
   static_assert(32 * kSoftWarps * kRegsHigh + 128 * kRegsLow <= kThreads * kLaunchRegs, "register split");
   static constexpr int kSmallBytes = 2048;
-  static constexpr int kUnitsFit = (227 * 1024 - 1024 - kTiles * GQ::kTileBytes - kSmallBytes) / GK::kTileBytes;
+  // Two Q buffers where they fit beside the ring, so that the next unit's Q is
+  // there when the last blocks of this one are done.
+  static constexpr int kQBufs = D == 128 ? 1 : 2;
+  static constexpr int kQBytes = kTiles * GQ::kTileBytes;
+  static constexpr int kUnitsFit = (227 * 1024 - 1024 - kQBufs * kQBytes - kSmallBytes) / GK::kTileBytes;
   static constexpr int kUnits = kUnitsFit > 20 ? 20 : kUnitsFit;  // ring stages, one K or V block each
   static_assert(kUnits >= 4, "ring");
   static constexpr int kOffQ = kUnits * GK::kTileBytes;
-  static constexpr int kOffSmall = kOffQ + kTiles * GQ::kTileBytes;
-  // full[U], empty[U], qfull, qempty, sfull[T], pfull[T], ofinal[T], vtmp, drain[2]
-  static constexpr int kNumBars = 2 * kUnits + 2 + 3 * kTiles + 3;
+  static constexpr int kOffSmall = kOffQ + kQBufs * kQBytes;
+  // full[U], empty[U], qfull[2], qempty[2], sfull[T], pfull[T], ofinal[T], vtmp, drain[2]
+  static constexpr int kNumBars = 2 * kUnits + 4 + 3 * kTiles + 3;
   static_assert(kNumBars * 8 + 8 + sizeof(RunStart) + 32 * 8 <= kSmallBytes, "barriers");
   static constexpr int kSmemUsed = kOffSmall + kSmallBytes + 1024;
   static constexpr int kSmemBytes = kSmemUsed > 116 * 1024 ? kSmemUsed : 116 * 1024;  // one CTA per SM
@@ -107,9 +111,9 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + L::kOffSmall);  // [U] block landed
   uint64_t* bar_empty = bar_full + U;    // [U] both MMA warps are done with it
-  uint64_t* bar_qfull = bar_empty + U;   // segment's Q landed
-  uint64_t* bar_qempty = bar_qfull + 1;  // both MMA warps' last score products of the segment are done
-  uint64_t* bar_sfull = bar_qempty + 1;  // [T] S_t computed (and the P_t V before it done)
+  uint64_t* bar_qfull = bar_empty + U;   // [2] segment's Q landed
+  uint64_t* bar_qempty = bar_qfull + 2;  // [2] both MMA warps' last score products of the segment are done
+  uint64_t* bar_sfull = bar_qempty + 2;  // [T] S_t computed (and the P_t V before it done)
   uint64_t* bar_pfull = bar_sfull + T;   // [T] P_t stored, O_t rescaled
   uint64_t* bar_ofinal = bar_pfull + T;  // [T] the segment's last P_t V done
   uint64_t* bar_vtmp = bar_ofinal + T;   // a V block that still needs rows cleared has landed
@@ -121,20 +125,15 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
 
   const int warp = warp_index();
   const int lane = threadIdx.x & 31;
-  SeqLens own{0, 0, 0};
-  {
-    int per;
-    const int x0 = paged_first_unit(p, L::kThreads, &per);
-    if (x0 < p.batch * p.tiles) own = seq_lens(p, p.tiles == 1 ? x0 : x0 / p.tiles);
-  }
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < U; ++s) {
       mbar_init(&bar_full[s], 1);
       mbar_init(&bar_empty[s], 2);
     }
-    mbar_init(bar_qfull, 1);
-    mbar_init(bar_qempty, 2);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar_qfull[s], 1);
+      mbar_init(&bar_qempty[s], 2);
+    }
     for (int t = 0; t < T; ++t) {
       mbar_init(&bar_sfull[t], 1);
       mbar_init(&bar_pfull[t], 4);
@@ -147,7 +146,6 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     s_start->run = 0;
     s_start->u.n_blk = 0;
     s_start->blk = 0;
-    p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     fence_mbar_init();
   }
   if (warp == kMma0) {
@@ -159,11 +157,20 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
+  // Up to here nothing of the caller's was touched.
+  griddep_wait();
+  griddep_launch_dependents();
+  SeqLens own{0, 0, 0};
+  {
+    int per;
+    const int x0 = paged_first_unit(p, L::kThreads, &per);
+    if (x0 < p.batch * p.tiles) own = seq_lens(p, p.tiles == 1 ? x0 : x0 / p.tiles);
+  }
+  if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   paged_find_run<L::kShift, L::kThreads>(p, own, s_warp, s_start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  griddep_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   const int tile_tok = 128 / p.G;  // tokens of a 128-row tile
 
@@ -187,19 +194,21 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         return p.num_pages;
       };
       for (int n; ok && (n = w.seg_len()) > 0; w.next(p), ++seg) {
-        if (seg > 0) ok = warp_wait(bar_qempty, (seg - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
+        int page = box_page(w.blk);
+        const int qb = seg % L::kQBufs, qu = seg / L::kQBufs;
+        if (qu > 0) ok = warp_wait(&bar_qempty[qb], (qu - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
         if (!ok) break;
         if (lane == 0) {
           const int tiles = (w.u.n_tok + tile_tok - 1) / tile_tok;
-          mbar_arrive_expect_tx(bar_qfull, tiles * GQ::kChunks * GQ::kRowBytes * p.G * tile_tok);
+          mbar_arrive_expect_tx(&bar_qfull[qb], tiles * GQ::kChunks * GQ::kRowBytes * p.G * tile_tok);
           for (int t = 0; t < tiles; ++t)
 #pragma unroll
             for (int ch = 0; ch < GQ::kChunks; ++ch)
-              tma_load_3d(smem + L::kOffQ + t * GQ::kTileBytes + ch * GQ::kChunkBytes, &tm_q, bar_qfull,
+              tma_load_3d(smem + L::kOffQ + qb * L::kQBytes + t * GQ::kTileBytes + ch * GQ::kChunkBytes, &tm_q,
+                          &bar_qfull[qb],
                           ch * (GQ::kRowBytes / 2), w.kvh * p.G, w.u.tok0 + t * tile_tok);
         }
         __syncwarp();
-        int page = box_page(w.blk);
         for (int j = 0; ok && j < n; ++j) {
           const int page_next = j + 1 < n ? box_page(w.blk + j + 1) : 0;
           const int key0 = ((w.u.lo >> L::kShift) + w.blk + j) * BN;
@@ -243,7 +252,8 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       }
       // Teardown: every copy this warp started lands before the CTA exits.
       for (int x = (c > U ? c - U : 0); x < c; ++x) drain_wait(&bar_full[x % U], (x / U) & 1, p.err);
-      if (seg > 0) drain_wait(bar_qfull, (seg - 1) & 1, p.err);
+      for (int x = (seg > L::kQBufs ? seg - L::kQBufs : 0); x < seg; ++x)
+        drain_wait(&bar_qfull[x % L::kQBufs], (x / L::kQBufs) & 1, p.err);
       __syncwarp();
     } else if (warp < kMma0 + 2) {
       // ------------------------------------------------------------ MMA issuers
@@ -266,7 +276,8 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           beg[h] = s.beg;
           end[h] = s.end;
         }
-        ok = warp_wait(bar_qfull, seg & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
+        const int qb = seg % L::kQBufs;
+        ok = warp_wait(&bar_qfull[qb], (seg / L::kQBufs) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
         for (int j = -1; ok && j < n; ++j) {
           const int kc = c + 2 * (j + 1), vc = c + 2 * j + 1;  // ring blocks of K(j+1), V(j)
           const int ks = kc % U, vs = vc % U;
@@ -295,7 +306,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
             }
             if (j + 1 >= beg[h] && j + 1 < end[h]) {
               tc_fence_after();
-              const uint64_t q_desc = make_sdesc(s_q + t * GQ::kTileBytes, 16, 8 * GQ::kRowBytes, GQ::kSwz);
+              const uint64_t q_desc = make_sdesc(s_q + qb * L::kQBytes + t * GQ::kTileBytes, 16, 8 * GQ::kRowBytes, GQ::kSwz);
               const uint64_t k_desc = make_sdesc(s_ring + ks * GK::kTileBytes, 16, 8 * GK::kRowBytes, GK::kSwz);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk)
@@ -307,7 +318,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           if (!ok) break;
           if (j >= 0) mma_commit_warp(&bar_empty[vs]);
           if (j + 1 < n) mma_commit_warp(&bar_empty[ks]);
-          if (j + 1 == n - 1) mma_commit_warp(bar_qempty);
+          if (j + 1 == n - 1) mma_commit_warp(&bar_qempty[qb]);
         }
         c += 2 * n;
       }
@@ -325,8 +336,19 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     const uint32_t t_s = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + t * L::kTileCols;
     const uint32_t t_o = t_s + L::kColO;
     const float sl2 = p.scale_log2;
-    const float2 c2 = make_float2(sl2, sl2);
+    // Blocks that a mask cuts.  D <= 64: the scores a row does not see become
+    // -inf (+inf under a negative scale) in place, and one copy of the code
+    // serves all blocks; a copy of its own for the few cut ones cost up to 5000
+    // cycles of instruction fetch per unit (ragged chunks 129 -> 121 us).  At
+    // D = 128 the selects between load and maximum cost more than that (chunks
+    // of 2048: 668 us with a copy of its own, 723 in place).
+    constexpr bool kMaskInPlace = D <= 64;
+    // In place, a scale of 0 makes every visible score 0 (0 times a hidden key's infinity would not be -inf).
+    const bool zero_scale = kMaskInPlace && sl2 == 0.f;
+    const float ce = zero_scale ? 1.f : sl2;
+    const float2 c2 = make_float2(ce, ce);
     const bool neg_scale = sl2 < 0.f;
+    const uint32_t hidden = __float_as_uint(neg_scale ? INFINITY : -INFINITY);
     int cnt = 0, fin = 0;  // blocks of this tile so far; segments in which it had blocks
     bool alive = true;
     long long at = static_cast<long long>(blockIdx.x) * s_start->share;  // flattened index of the segment's first block
@@ -350,10 +372,23 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         else tmem_ld64(t_s, sr);
         const int key0 = key_base + j * BN;
         const int lim = last - key0, lo = first - key0;  // columns lo <= c <= lim are visible to this row
-        const bool masked = key0 < all_lo || key0 + BN > all_hi;
-        if (j == sp.beg) m = block_max_scaled<BN, true>(sr, masked, lo, lim, sl2, neg_scale);
+        const bool cut = key0 < all_lo || key0 + BN > all_hi;  // a mask cuts the block
+        if constexpr (kMaskInPlace) {
+          if (zero_scale) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c) sr[c] = 0;
+          }
+          if (cut) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c) sr[c] = c < lo || c > lim ? hidden : sr[c];
+          }
+        }
+        const bool masked = !kMaskInPlace && cut;
+        auto block_max = [&]() {
+          return block_max_scaled<BN, !kMaskInPlace>(sr, masked, lo, kMaskInPlace ? BN : lim, ce, neg_scale);
+        };
+        if (j == sp.beg) m = block_max();
         float alpha = 1.f;
-        bool upd = false;
         auto exps = [&]() {
           const float m_use = m == -INFINITY ? 0.f : m;  // rows with no visible key so far
           const float2 negm = make_float2(-m_use, -m_use);
@@ -363,14 +398,14 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
 #pragma unroll
             for (int k0 = 0; k0 < BN; k0 += 16) {
               uint32_t pk[8];
-              exp16<BF16, true, true>(sr, k0, c2, negm, lo, lim, acc, pk);
+              exp16<BF16, !kMaskInPlace, true>(sr, k0, c2, negm, lo, lim, acc, pk);
               tmem_st8(t_s + k0 / 2, pk);
             }
           } else {
 #pragma unroll
             for (int k0 = 0; k0 < BN; k0 += 16) {
               uint32_t pk[8];
-              exp16<BF16, false>(sr, k0, c2, negm, lo, lim, acc, pk);
+              exp16<BF16, false>(sr, k0, c2, negm, 0, BN, acc, pk);
               tmem_st8(t_s + k0 / 2, pk);
             }
           }
@@ -381,13 +416,13 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         // A block whose sum breaks the bound (or a row's first visible key)
         // moves the maximum, rescales O and is done again.  Lanes past the
         // tile's rows hold anything and never ask for it.
-        bool need = row_ok && (!(blk <= kSumLimit) || (m == -INFINITY && max(lo, 0) <= min(lim, BN - 1)));
+        const bool need = row_ok && (!(blk <= kSumLimit) || (m == -INFINITY && max(lo, 0) <= min(lim, BN - 1)));
         if (__any_sync(0xffffffffu, need)) {
-          const float m_blk = block_max_scaled<BN, true>(sr, masked, lo, lim, sl2, neg_scale);
-          if (need && m_blk > m) {
+          const float m_blk = block_max();
+          const bool upd = need && m_blk > m;
+          if (upd) {
             alpha = ex2(m - m_blk);
             m = m_blk;
-            upd = true;
           }
           if (__any_sync(0xffffffffu, upd)) {
             tmem_st_wait();  // the first pass's stores land before they are overwritten
@@ -429,7 +464,10 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       const bool seen = have && l > 0.f;
       const float inv_l = seen ? 1.f / l : 0.f;
       const int tok = w.u.tok0 + sp.ta + rt, head = w.kvh * p.G + rh;
-      const int64_t prow = static_cast<int64_t>(slot) * p.part_rows + (sp.ta + rt) * p.G + rh;
+      // Partials lie [slot][D / 4][part_rows][4]: neighbouring lanes (rows) write
+      // neighbouring 16 bytes.
+      const int prow = (sp.ta + rt) * p.G + rh;
+      float* part = p.o_part + static_cast<int64_t>(slot) * p.part_rows * D + prow * 4;
       elem_t* orow = static_cast<elem_t*>(p.o) + (static_cast<int64_t>(tok) * p.H + head) * D;
       if (sp.n_tok > 0) {  // (warp-uniform)
 #pragma unroll
@@ -440,13 +478,18 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           for (int i = 0; i < 16; ++i) o16[i] = seen ? o16[i] : 0u;
           if (row_ok) {
             if (whole) store_row16<BF16>(orow + c, o16, inv_l);
-            else store_row16_f32(p.o_part + prow * D + c, o16, inv_l);
+            else
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(part + static_cast<int64_t>((c + i) / 4) * p.part_rows * 4) =
+                    make_float4(__uint_as_float(o16[i]) * inv_l, __uint_as_float(o16[i + 1]) * inv_l,
+                                __uint_as_float(o16[i + 2]) * inv_l, __uint_as_float(o16[i + 3]) * inv_l);
           }
         }
         if (row_ok) {
           const float l2 = seen ? m + log2f(l) : -INFINITY;
           if (whole) p.lse[static_cast<int64_t>(head) * p.total + tok] = l2 * 0.69314718055994530942f;
-          else p.lse_part[prow] = l2;
+          else p.lse_part[static_cast<int64_t>(slot) * p.part_rows + prow] = l2;
         }
       }
       if (!whole && w.blk == 0 && threadIdx.x == 0)
@@ -479,8 +522,7 @@ cudaError_t launch_paged_tile_t(const CUtensorMap& tq, const CUtensorMap& tk, co
   e = cudaFuncGetAttributes(&attr, kern);
   if (e != cudaSuccess) return e;
   if (attr.numRegs != L::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  kern<<<grid, L::kThreads, L::kSmemBytes, stream>>>(tq, tk, tv, p);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3(grid), L::kThreads, L::kSmemBytes, stream, tq, tk, tv, p);
 }
 
 }  // namespace

@@ -73,6 +73,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
   __shared__ int64_t s_slot[APPEND ? kRopeMaxTok : 1];  // element offset of the token's rows in the caches; -1: none
   __shared__ uint4 s_rows[FORM == kHalfAny ? kRopeThreads * 2 * kRopeRows : 1];
 
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   int tile = blockIdx.x;
   int tok0, n_tok;  // the CTA's tokens
   int pos0 = 0;     // append: cache position of token tok0
@@ -239,14 +241,9 @@ namespace {
 
 template <RopeForm FORM>
 cudaError_t launch_rope_f(const RopeParams& p, bool bf16, bool append, unsigned grid, cudaStream_t s) {
-  if (append) {
-    if (bf16) fa_rope_kernel<FORM, true, true><<<grid, kRopeThreads, 0, s>>>(p);
-    else fa_rope_kernel<FORM, false, true><<<grid, kRopeThreads, 0, s>>>(p);
-  } else {
-    if (bf16) fa_rope_kernel<FORM, true, false><<<grid, kRopeThreads, 0, s>>>(p);
-    else fa_rope_kernel<FORM, false, false><<<grid, kRopeThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  auto kern = append ? (bf16 ? fa_rope_kernel<FORM, true, true> : fa_rope_kernel<FORM, false, true>)
+                     : (bf16 ? fa_rope_kernel<FORM, true, false> : fa_rope_kernel<FORM, false, false>);
+  return launch_dependent(kern, dim3(grid), kRopeThreads, 0, s, p);
 }
 
 }  // namespace
