@@ -30,6 +30,7 @@ implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -616,13 +617,32 @@ def _int_array(x, name, dtype, shape):
     return x.data_ptr()
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor that belongs to the stream the call runs on."""
+def _allocate(stream, device, *specs):
+    """New tensors of (shape, dtype), which belong to the stream the call runs on."""
     import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+
+
+# Scratch of forward_paged, one per stream: calls on a stream run one after another, so they can share it, and
+# an allocation per call is a tenth of what a decoding step's call costs on the host.  A call that is being
+# captured gets its own (the graph may run beside this stream's later calls).
+_scratch: dict = {}
+
+
+def _stream_scratch(nbytes: int, device: int, handle: int, stream):
+    """A device buffer of at least nbytes that only calls on this stream use."""
+    import torch
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        capturing = torch.cuda.is_current_stream_capturing()
+    if capturing:
+        return _allocate(stream, device, ((max(nbytes, 256),), torch.uint8))[0]
+    buf = _scratch.get((device, handle))
+    if buf is None or buf.numel() < nbytes:
+        buf = _scratch[device, handle] = _allocate(stream, device, ((max(nbytes, 1 << 20),), torch.uint8))[0]
+    return buf
 
 
 def _three(x, name):
@@ -639,10 +659,12 @@ def _rotate(what, q, k, positions, steps, interleaved, magnitude, q_out, k_out, 
     hk = k_shape[1]
     if k_shape[0] != T or k_shape[2] != D:
         raise ValueError("k must have q's tokens and head dimension")
-    if q_out is None:
-        q_out = _empty(shape, dtype, d, stream)
-    if k_out is None:
-        k_out = _empty(k_shape, dtype, d, stream)
+    if q_out is None and k_out is None:
+        q_out, k_out = _allocate(stream, d, (shape, dtype), (k_shape, dtype))
+    elif q_out is None:
+        q_out, = _allocate(stream, d, (shape, dtype))
+    elif k_out is None:
+        k_out, = _allocate(stream, d, (k_shape, dtype))
     n = steps.numel()
     _check(getattr(_load(), what)(q.data_ptr(), _rows(q, "q", shape, dtype), k.data_ptr(), _rows(k, "k", k_shape, dtype),
                q_out.data_ptr(), _rows(q_out, "the q output", shape, dtype), k_out.data_ptr(),
@@ -725,7 +747,7 @@ def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_s
         if q_shape[0] != T or q_shape[2] != D:
             raise ValueError("q must have k's tokens and head dimension")
         if q_out is None:
-            q_out = _empty(q_shape, dtype, d, stream)
+            q_out, = _allocate(stream, d, (q_shape, dtype))
         q_args = (q.data_ptr(), _rows(q, "q", q_shape, dtype), q_out.data_ptr(),
                   _rows(q_out, "q_out", q_shape, dtype))
     n = 0 if steps is None else steps.numel()
@@ -746,7 +768,8 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seq
     Query i of a sequence's n new tokens stands at key kv_lens - n + i.
     ``max_seqlen_q`` and ``max_seqlen_k`` are host bounds on the new tokens and
     on ``kv_lens``; a violation, or a bad page, is found on the device and
-    reported by ``fa_check_device_errors``.
+    reported by ``fa_check_device_errors``.  Without ``workspace`` the call uses
+    scratch kept for its stream (its own while a graph is captured).
     """
     import torch
     d = _call_device(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, lse, workspace)
@@ -761,22 +784,24 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seq
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     left, right = (-1, -1) if window is None else window
-    if out is None:
-        out = _empty(shape, dtype, d, stream)
-    elif out.shape != shape or out.dtype != dtype or not out.is_contiguous():
-        raise ValueError("out must be like q")
-    if lse is None:
-        lse = _empty((H, T), torch.float32, d, stream)
-    elif lse.shape != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous fp32 [H, T]")
+    handle = _raw_stream(d) if stream is None else stream.cuda_stream
+    if out is None and lse is None:
+        out, lse = _allocate(stream, d, (shape, dtype), ((H, T), torch.float32))
+    else:
+        if out is None:
+            out, = _allocate(stream, d, (shape, dtype))
+        if lse is None:
+            lse, = _allocate(stream, d, ((H, T), torch.float32))
+        if out.shape != shape or out.dtype != dtype or not out.is_contiguous():
+            raise ValueError("out must be like q")
+        if lse.shape != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous fp32 [H, T]")
     if workspace is None:
-        need = _load().fa_fwd_paged_workspace_size(batch, max_seqlen_q, max_seqlen_k, H, hk, D)
-        workspace = _empty((max(need, 256),), torch.uint8, d, stream)
-        have = need
+        have = _load().fa_fwd_paged_workspace_size(batch, max_seqlen_q, max_seqlen_k, H, hk, D)
+        workspace = _stream_scratch(have, d, handle, stream)
     else:
         have = workspace.numel() * workspace.element_size()
     _check(_load().fa_fwd_paged(q.data_ptr(), out.data_ptr(), lse.data_ptr(), cache, cu_seqlens.data_ptr(), batch,
                         max_seqlen_q, max_seqlen_k, T, H, hk, D, causal, left, right, scale, _dtype_code(q),
-                        workspace.data_ptr(), have, _raw_stream(d) if stream is None else stream.cuda_stream),
-           "fa_fwd_paged")
+                        workspace.data_ptr(), have, handle), "fa_fwd_paged")
     return out, lse

@@ -38,39 +38,47 @@ __global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const Pag
   auto at = [&](int s, int row) -> int64_t {
     return static_cast<int64_t>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * q.rows + row;
   };
+  auto add = [&](float4& o, float w, const float4 v) {
+    o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+  };
   if (q.by_chunk) {
-    // Lanes span rows, as the partials lie; a warp takes 32 rows x 8 columns at a time.
-    constexpr int kPairs = D / 8;
+    // Lanes span rows, as the partials lie; a warp takes 32 rows x 16 columns
+    // at a time (whole 32-byte sectors of the output).
+    constexpr int kStrips = D / 16;
     const int lane = threadIdx.x & 31;
-    const int tasks = (n_rows + 31) / 32 * kPairs;
+    const int tasks = (n_rows + 31) / 32 * kStrips;
     for (int task = static_cast<int>(blockIdx.y) * (kMergeThreads / 32) + static_cast<int>(threadIdx.x >> 5);
          task < tasks; task += gridDim.y * (kMergeThreads / 32)) {
-      const int row = task / kPairs * 32 + lane, pair = task % kPairs;
+      const int row = task / kStrips * 32 + lane, strip = task % kStrips;
       if (row >= n_rows) continue;
       float mx = -INFINITY;
 #pragma unroll 4
       for (int s = 0; s < parts; ++s) mx = fmaxf(mx, q.lse_part[at(s, row)]);
       const bool seen = mx != -INFINITY;
       float total = 0.f;
-      float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      float4 o[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (seen) {
-#pragma unroll 4
+#pragma unroll 2
         for (int s = 0; s < parts; ++s) {
           const float w = exp2f(q.lse_part[at(s, row)] - mx);
-          const float4* src = reinterpret_cast<const float4*>(q.o_part + at(s, 0) * D) + 2 * pair * q.rows + row;
-          const float4 a = src[0], b = src[q.rows];
+          const float4* src = reinterpret_cast<const float4*>(q.o_part + at(s, 0) * D) + 4 * strip * q.rows + row;
           total += w;
-          o[0] += w * a.x; o[1] += w * a.y; o[2] += w * a.z; o[3] += w * a.w;
-          o[4] += w * b.x; o[5] += w * b.y; o[6] += w * b.z; o[7] += w * b.w;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) add(o[c], w, src[c * q.rows]);
         }
       }
       const float inv = seen ? 1.f / total : 0.f;
       const int tok = d.x + row / p.G, head = d.z * p.G + row % p.G;
-      elem_t* orow = static_cast<elem_t*>(p.o) + (static_cast<int64_t>(tok) * p.H + head) * D + 8 * pair;
-      *reinterpret_cast<uint4*>(orow) =
-          make_uint4(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv),
-                     pack2<BF16>(o[4] * inv, o[5] * inv), pack2<BF16>(o[6] * inv, o[7] * inv));
-      if (pair == 0)
+      uint4* orow = reinterpret_cast<uint4*>(static_cast<elem_t*>(p.o) +
+                                             (static_cast<int64_t>(tok) * p.H + head) * D + 16 * strip);
+#pragma unroll
+      for (int c = 0; c < 4; c += 2)
+        orow[c / 2] = make_uint4(pack2<BF16>(o[c].x * inv, o[c].y * inv), pack2<BF16>(o[c].z * inv, o[c].w * inv),
+                                 pack2<BF16>(o[c + 1].x * inv, o[c + 1].y * inv),
+                                 pack2<BF16>(o[c + 1].z * inv, o[c + 1].w * inv));
+      if (strip == 0)
         p.lse[static_cast<int64_t>(head) * p.total + tok] =
             seen ? (mx + log2f(total)) * 0.69314718055994530942f : -INFINITY;
     }
@@ -86,9 +94,6 @@ __global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const Pag
     if (x == 0)
       p.lse[static_cast<int64_t>(head) * p.total + tok] =
           seen ? (mx + log2f(total)) * 0.69314718055994530942f : -INFINITY;
-  };
-  auto add = [&](float4& o, float w, const float4 v) {
-    o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
   };
   if (parts <= kMergeFew) {
     for (int row = static_cast<int>(blockIdx.y) * kGroups + y; row < n_rows; row += gridDim.y * kGroups) {
@@ -143,11 +148,15 @@ namespace {
 
 template <int D, bool BF16>
 cudaError_t launch_paged_merge_t(const PagedMergeParams& p, int grid, int sets, cudaStream_t stream) {
-  // Slices for the widest unit's rows: two rounds of a CTA's rows each, 16 at most.
-  const int rows = sets > 1 && p.parts[1].rows > p.parts[0].rows ? p.parts[1].rows : p.parts[0].rows;
-  const int per = 2 * kMergeThreads / (D / 4);
-  const int slices = (rows + per - 1) / per;
-  return launch_dependent(fa_paged_merge_kernel<D, BF16>, dim3(grid, slices < 8 ? 8 : (slices > 16 ? 16 : slices), sets),
+  // Slices: eight warps of one 32 x 16 strip each for the tile kernel's units,
+  // two rounds of a CTA's rows for the others.
+  int slices = 1;
+  for (int z = 0; z < sets; ++z) {
+    const int rows = p.parts[z].rows, per = 2 * kMergeThreads / (D / 4);
+    const int n = p.parts[z].by_chunk ? (rows + 31) / 32 * (D / 16) / (kMergeThreads / 32) : (rows + per - 1) / per;
+    if (n > slices) slices = n;
+  }
+  return launch_dependent(fa_paged_merge_kernel<D, BF16>, dim3(grid, slices < 8 ? 8 : slices, sets),
                           kMergeThreads, 0, stream, p);
 }
 
