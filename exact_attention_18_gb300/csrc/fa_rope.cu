@@ -33,12 +33,10 @@ namespace fa {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeRows = 4;        // rows a thread has in flight
+constexpr int kRopeMaxThreads = 256;
+constexpr int kRopeRows = 2;        // rows a thread has in flight
 constexpr int kRopeMaxTok = 128;    // tokens per CTA at most
 constexpr int kRopeMaxAngles = 1024;  // tokens x pairs per CTA at most
-// Elements of a CTA's tokens aimed at: one round of kRopeRows rows a thread.
-constexpr int kRopeElems = kRopeThreads * 16 * kRopeRows;
 
 enum RopeForm {
   kInterleaved,   // pairs (2i, 2i+1): any r, a vector holds whole pairs
@@ -49,6 +47,7 @@ enum RopeForm {
 // Eight 16-bit elements.
 union Vec8 {
   uint4 v;
+  uint32_t w[4];  // pairs of neighbours
   uint16_t h[8];
 };
 
@@ -56,6 +55,12 @@ template <bool BF16>
 __device__ __forceinline__ float to_float(uint16_t h) {
   if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(h) << 16);
   else return __half2float(__ushort_as_half(h));
+}
+// Two neighbours in a 32-bit word (the first in its low half).
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 template <bool BF16>
 __device__ __forceinline__ uint16_t from_float(float x) {
@@ -68,10 +73,10 @@ __device__ __forceinline__ uint16_t from_float(float x) {
 // APPEND: rows of a packed batch; K rows go to their pages, and V rows (after
 // the K rows of a token) are copied to theirs.
 template <RopeForm FORM, bool BF16, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p) {
-  __shared__ float2 s_cs[kRopeMaxAngles];
+__global__ void __launch_bounds__(kRopeMaxThreads) fa_rope_kernel(const RopeParams p) {
+  __shared__ __align__(16) float2 s_cs[kRopeMaxAngles];
   __shared__ int64_t s_slot[APPEND ? kRopeMaxTok : 1];  // element offset of the token's rows in the caches; -1: none
-  __shared__ uint4 s_rows[FORM == kHalfAny ? kRopeThreads * 2 * kRopeRows : 1];
+  __shared__ uint4 s_rows[FORM == kHalfAny ? kRopeMaxThreads * 2 * kRopeRows : 1];
 
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -101,10 +106,19 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
   if (n_tok <= 0) return;
 
   const int r = p.r, D = p.D;
+  // A token's angles in shared memory.  A thread that turns 8 pairs (8 col ..)
+  // reads them as four 16-byte words, the words of neighbouring threads side by
+  // side; side by side in pair order, eight threads would meet in two banks.
+  const int groups = (r + 7) / 8;
+  const int angles = FORM == kHalfAny ? r : 8 * groups;
+  auto angle_at = [&](int j) {
+    return FORM == kHalfAny ? j : 2 * (((j >> 1) & 3) * groups + (j >> 3)) + (j & 1);
+  };
   const int rot_heads = p.H + p.H_kv;                  // rows that turn
   const int heads = rot_heads + (APPEND ? p.H_kv : 0);  // rows of a token: Q, K (and V)
   const int n_rows = n_tok * heads;
-  const int lanes = kRopeThreads >> p.log2_items;  // rows the CTA takes at once
+  const int threads = blockDim.x;
+  const int lanes = threads >> p.log2_items;  // rows the CTA takes at once
   const int col = static_cast<int>(threadIdx.x) & ((1 << p.log2_items) - 1);
   // This thread's two vectors of a row that turns; of a V row they are 16 col, 16 col + 8.
   bool turns;  // kHalf: its columns turn
@@ -139,7 +153,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
     }
     if (round == 0) {
       // Angles of the CTA's tokens, and (append) where their rows go.
-      for (int i = threadIdx.x; i < n_tok * r; i += kRopeThreads) {
+      for (int i = threadIdx.x; i < n_tok * r; i += threads) {
         const int t = i / r, j = i - t * r;
         int pos;
         if (APPEND && p.positions == nullptr) pos = pos0 + t;
@@ -148,10 +162,10 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
             static_cast<unsigned long long>(static_cast<long long>(pos)) * __ldg(p.steps + j);
         float s, c;
         sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-        s_cs[i] = make_float2(c * p.mag, s * p.mag_sin);
+        s_cs[t * angles + angle_at(j)] = make_float2(c * p.mag, s * p.mag_sin);
       }
       if constexpr (APPEND) {
-        for (int i = threadIdx.x; i < n_tok; i += kRopeThreads) {
+        for (int i = threadIdx.x; i < n_tok; i += threads) {
           const int pos = pos0 + i;
           const int page = __ldg(p.block_table + static_cast<int64_t>(b) * p.table_stride + (pos >> p.page_shift));
           int64_t slot = -1;
@@ -171,8 +185,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
       __syncwarp();
 #pragma unroll
       for (int u = 0; u < kRopeRows; ++u) {
-        s_rows[2 * (u * kRopeThreads + static_cast<int>(threadIdx.x))] = x[u].v;
-        s_rows[2 * (u * kRopeThreads + static_cast<int>(threadIdx.x)) + 1] = y[u].v;
+        s_rows[2 * (u * threads + static_cast<int>(threadIdx.x))] = x[u].v;
+        s_rows[2 * (u * threads + static_cast<int>(threadIdx.x)) + 1] = y[u].v;
       }
       __syncwarp();
     }
@@ -194,30 +208,28 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
         dst = static_cast<uint16_t*>(p.k_out) + tk * p.k_out_stride + (h - p.H) * D;
       }
       if (turns && !v_row) {
-        const float2* cs = s_cs + t * r;
+        const float2* cs = s_cs + t * angles;
+        const float4* cs4 = reinterpret_cast<const float4*>(cs) + col;
         if constexpr (FORM == kHalf) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 w = cs[oa + i];
-            const float a = to_float<BF16>(x[u].h[i]), bb = to_float<BF16>(y[u].h[i]);
-            x[u].h[i] = from_float<BF16>(a * w.x - bb * w.y);
-            y[u].h[i] = from_float<BF16>(bb * w.x + a * w.y);
+          for (int i = 0; i < 4; ++i) {
+            const float4 w = cs4[i * groups];
+            const float2 a = unpack2<BF16>(x[u].w[i]), bb = unpack2<BF16>(y[u].w[i]);
+            x[u].w[i] = pack2<BF16>(a.x * w.x - bb.x * w.y, a.y * w.z - bb.y * w.w);
+            y[u].w[i] = pack2<BF16>(bb.x * w.x + a.x * w.y, bb.y * w.z + a.y * w.w);
           }
         } else if constexpr (FORM == kInterleaved) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int j = oa / 2 + i;  // the pair
-            if (j < r) {
-              Vec8& v = i < 4 ? x[u] : y[u];
-              const float2 w = cs[j];
-              const float a = to_float<BF16>(v.h[2 * (i & 3)]), bb = to_float<BF16>(v.h[2 * (i & 3) + 1]);
-              v.h[2 * (i & 3)] = from_float<BF16>(a * w.x - bb * w.y);
-              v.h[2 * (i & 3) + 1] = from_float<BF16>(bb * w.x + a * w.y);
-            }
+          for (int i = 0; i < 8; i += 2) {
+            const float4 w = cs4[i / 2 * groups];
+            uint32_t* v = i < 4 ? &x[u].w[i] : &y[u].w[i - 4];
+            const float2 a = unpack2<BF16>(v[0]), bb = unpack2<BF16>(v[1]);
+            if (8 * col + i < r) v[0] = pack2<BF16>(a.x * w.x - a.y * w.y, a.y * w.x + a.x * w.y);
+            if (8 * col + i + 1 < r) v[1] = pack2<BF16>(bb.x * w.z - bb.y * w.w, bb.y * w.z + bb.x * w.w);
           }
         } else {
           // Column c pairs with c + r (c < r) or c - r, read from the staged row.
-          const uint16_t* line = stage + 16 * (u * kRopeThreads + static_cast<int>(threadIdx.x) - col);
+          const uint16_t* line = stage + 16 * (u * threads + static_cast<int>(threadIdx.x) - col);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int c = oa + i;
@@ -240,28 +252,48 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
 namespace {
 
 template <RopeForm FORM>
-cudaError_t launch_rope_f(const RopeParams& p, bool bf16, bool append, unsigned grid, cudaStream_t s) {
+cudaError_t launch_rope_f(const RopeParams& p, bool bf16, bool append, unsigned grid, int threads, cudaStream_t s) {
   auto kern = append ? (bf16 ? fa_rope_kernel<FORM, true, true> : fa_rope_kernel<FORM, false, true>)
                      : (bf16 ? fa_rope_kernel<FORM, true, false> : fa_rope_kernel<FORM, false, false>);
-  return launch_dependent(kern, dim3(grid), kRopeThreads, 0, s, p);
+  return launch_dependent(kern, dim3(grid), threads, 0, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(RopeParams p, bool bf16, bool append, int batch, cudaStream_t stream) {
-  const int64_t per_tok = static_cast<int64_t>(p.H + (append ? 2 : 1) * p.H_kv) * p.D;
-  int64_t tok = kRopeElems / per_tok;
-  if (p.r > 0 && tok > kRopeMaxAngles / p.r) tok = kRopeMaxAngles / p.r;
-  p.tok_per_cta = static_cast<int>(tok < 1 ? 1 : (tok > kRopeMaxTok ? kRopeMaxTok : tok));
   p.log2_items = p.D == 16 ? 0 : (p.D == 32 ? 1 : (p.D == 64 ? 2 : 3));  // D / 16 threads a row
+  // Tokens and threads of a CTA: all rows in one round (kRopeRows of them a
+  // thread), with the fewest idle threads.  A second round's loads would wait
+  // for the first round's stores: 8192 tokens of 36 heads of 128, one token a
+  // CTA, took 29.4 us in two rounds of 128 threads (44 % of them idle).
+  const int64_t rows_tok = p.H + (append ? 2 : 1) * p.H_kv;
+  int64_t most = p.r > 0 ? kRopeMaxAngles / ((p.r + 7) / 8 * 8) : kRopeMaxTok;
+  most = most < 1 ? 1 : (most > kRopeMaxTok ? kRopeMaxTok : most);
+  const int64_t fits = (kRopeMaxThreads >> p.log2_items) * kRopeRows;  // rows of one round at most
+  int64_t tok = 1, threads = kRopeMaxThreads;
+  double best = -1.0;
+  for (int64_t t = 1; t <= most && (t == 1 || t * rows_tok <= fits); ++t) {
+    const int64_t rows = t * rows_tok;
+    int64_t th = (((rows + kRopeRows - 1) / kRopeRows << p.log2_items) + 31) / 32 * 32;
+    if (th > kRopeMaxThreads) th = kRopeMaxThreads;
+    if (th < 128 && t < most && (t + 1) * rows_tok <= fits) continue;  // (a CTA of a few warps is mostly set-up)
+    const int64_t round = (th >> p.log2_items) * kRopeRows;
+    const double full = static_cast<double>(rows) / static_cast<double>((rows + round - 1) / round * round);
+    if (full > best + 0.02) {
+      best = full;
+      tok = t;
+      threads = th;
+    }
+  }
+  p.tok_per_cta = static_cast<int>(tok);
   const int longest = append ? p.max_len : p.total;
   p.tiles = (longest + p.tok_per_cta - 1) / p.tok_per_cta;
   const int64_t ctas = static_cast<int64_t>(p.tiles) * (append ? batch : 1);
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(ctas);
-  if (p.interleaved) return launch_rope_f<kInterleaved>(p, bf16, append, grid, stream);
-  if (p.r % 8 == 0) return launch_rope_f<kHalf>(p, bf16, append, grid, stream);
-  return launch_rope_f<kHalfAny>(p, bf16, append, grid, stream);
+  if (p.interleaved) return launch_rope_f<kInterleaved>(p, bf16, append, grid, static_cast<int>(threads), stream);
+  if (p.r % 8 == 0) return launch_rope_f<kHalf>(p, bf16, append, grid, static_cast<int>(threads), stream);
+  return launch_rope_f<kHalfAny>(p, bf16, append, grid, static_cast<int>(threads), stream);
 }
 
 }  // namespace fa
