@@ -36,14 +36,21 @@ struct PagedTileLayout {
   using GQ = TileGeom<D, 128>;
   using GK = TileGeom<D, kBlk>;
   static constexpr int kSoftWarps = 4 * kTiles;
-  static constexpr int kThreads = 32 * kSoftWarps + 128;  // producer, two MMA warps, one idle
+  // Warps that issue MMAs, each for kTiles / kMmaWarps tiles.  Two tiles: one
+  // warp, which issues a tile's P V and next S as a whole before the other's.
+  // With a warp each the two tiles' products interleave whenever they meet, both
+  // come late, and the tiles stay in step for hundreds of blocks (a block of two
+  // tiles 2900 cycles, or up to 4000, instead of 2430).  Four tiles: two warps;
+  // one cannot keep the tensor core fed.
+  static constexpr int kMmaWarps = kTiles == 2 ? 1 : 2;
+  static constexpr int kThreads = 32 * kSoftWarps + 128;  // producer, MMA warps, the rest idle
   // Register split: every thread gets kLaunchRegs at launch, the last four
   // warps drop to kRegsLow and the softmax warps rise to kRegsHigh.
   static constexpr int kLaunchRegs = kTiles == 2 ? 168 : 96;
   static constexpr uint32_t kRegsHigh = kTiles == 2 ? 216 : 104;
   static constexpr uint32_t kRegsLow = kTiles == 2 ? 72 : 64;
   static_assert(32 * kSoftWarps * kRegsHigh + 128 * kRegsLow <= kThreads * kLaunchRegs, "register split");
-  static constexpr int kSmallBytes = 2048;
+  static constexpr int kSmallBytes = D == 128 ? 2048 : 3072;  // barriers, run, walks
   // Two Q buffers where they fit beside the ring, so that the next unit's Q is
   // there when the last blocks of this one are done.
   static constexpr int kQBufs = D == 128 ? 1 : 2;
@@ -55,7 +62,8 @@ struct PagedTileLayout {
   static constexpr int kOffSmall = kOffQ + kQBufs * kQBytes;
   // full[U], empty[U], qfull[2], qempty[2], sfull[T], pfull[T], ofinal[T], vtmp, drain[2]
   static constexpr int kNumBars = 2 * kUnits + 4 + 3 * kTiles + 3;
-  static_assert(kNumBars * 8 + 8 + sizeof(RunStart) + 32 * 8 <= kSmallBytes, "barriers");
+  static_assert(kNumBars * 8 + 16 + sizeof(RunStart) + kSoftWarps * sizeof(SegWalk<kShift>) + 32 * 8 <= kSmallBytes,
+                "barriers");
   static constexpr int kSmemUsed = kOffSmall + kSmallBytes + 1024;
   static constexpr int kSmemBytes = kSmemUsed > 116 * 1024 ? kSmemUsed : 116 * 1024;  // one CTA per SM
   static constexpr uint32_t kTileCols = 512 / kTiles;  // TMEM columns of a tile: S (P over it), then O
@@ -104,15 +112,15 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   using Walk = SegWalk<L::kShift>;
   constexpr int U = L::kUnits, T = L::kTiles, BN = L::kBlk;
   constexpr int kProducer = L::kSoftWarps, kMma0 = L::kSoftWarps + 1;
-  constexpr int kTilesPerMma = T / 2;
+  constexpr int kMmaWarps = L::kMmaWarps, kTilesPerMma = T / kMmaWarps;
   constexpr float kSumLimit = 256.0f;  // largest block sum of P~ kept with a stale maximum
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + L::kOffSmall);  // [U] block landed
-  uint64_t* bar_empty = bar_full + U;    // [U] both MMA warps are done with it
+  uint64_t* bar_empty = bar_full + U;    // [U] every MMA warp is done with it
   uint64_t* bar_qfull = bar_empty + U;   // [2] segment's Q landed
-  uint64_t* bar_qempty = bar_qfull + 2;  // [2] both MMA warps' last score products of the segment are done
+  uint64_t* bar_qempty = bar_qfull + 2;  // [2] the segment's last score products are done
   uint64_t* bar_sfull = bar_qempty + 2;  // [T] S_t computed (and the P_t V before it done)
   uint64_t* bar_pfull = bar_sfull + T;   // [T] P_t stored, O_t rescaled
   uint64_t* bar_ofinal = bar_pfull + T;  // [T] the segment's last P_t V done
@@ -121,6 +129,9 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   RunStart* s_start = reinterpret_cast<RunStart*>(tmem_slot + 2);
+  // Each softmax warp's walk, parked here while it works through a segment's
+  // blocks: in registers it made the block loop spill.
+  Walk* s_walk = reinterpret_cast<Walk*>(s_start + 1);
   long long* s_warp = reinterpret_cast<long long*>(smem + L::kOffSmall + L::kSmallBytes - 32 * 8);
 
   const int warp = warp_index();
@@ -128,11 +139,11 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < U; ++s) {
       mbar_init(&bar_full[s], 1);
-      mbar_init(&bar_empty[s], 2);
+      mbar_init(&bar_empty[s], kMmaWarps);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar_qfull[s], 1);
-      mbar_init(&bar_qempty[s], 2);
+      mbar_init(&bar_qempty[s], kMmaWarps);
     }
     for (int t = 0; t < T; ++t) {
       mbar_init(&bar_sfull[t], 1);
@@ -255,7 +266,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       for (int x = (seg > L::kQBufs ? seg - L::kQBufs : 0); x < seg; ++x)
         drain_wait(&bar_qfull[x % L::kQBufs], (x / L::kQBufs) & 1, p.err);
       __syncwarp();
-    } else if (warp < kMma0 + 2) {
+    } else if (warp < kMma0 + kMmaWarps) {
       // ------------------------------------------------------------ MMA issuers
       const int m = warp - kMma0;  // tiles m * kTilesPerMma ..
       constexpr uint32_t idesc_qk = make_idesc_f16(BF16, 128, BN, false, false);
@@ -355,13 +366,18 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     for (int n; alive && (n = w.seg_len()) > 0; w.next(p)) {
       const TileSpan sp = tile_span<L::kShift>(p, w, t, tile_tok, n);
       const bool row_ok = rt < sp.n_tok && rt < tile_tok;
-      const int pos = sp.pos0 + rt;
-      const int last = min(w.u.kv_len - 1, pos + p.win_right), first = pos - p.win_left;
-      // Keys every row of the tile sees: [all_lo, all_hi).
-      const int all_lo = sp.pos0 + sp.n_tok - 1 - p.win_left, all_hi = min(w.u.kv_len, sp.pos0 + 1 + p.win_right);
+      // Relative to the segment's first key: this row's visible keys [lo0, lim0],
+      // and the blocks [j_lo, j_hi) that every row of the tile sees whole.
       const int key_base = ((w.u.lo >> L::kShift) + w.blk) * BN;
+      const int pos = sp.pos0 + rt;
+      const int lim0 = min(w.u.kv_len - 1, pos + p.win_right) - key_base, lo0 = pos - p.win_left - key_base;
+      const int j_lo = (sp.pos0 + sp.n_tok - 1 - p.win_left - key_base + BN - 1) >> L::kShift;
+      const int j_hi = (min(w.u.kv_len, sp.pos0 + 1 + p.win_right) - key_base) >> L::kShift;
+      const int beg = sp.beg, end = sp.end;
+      if (lane == 0) s_walk[warp] = w;
+      __syncwarp();
       float m = -INFINITY, l = 0.f;
-      for (int j = sp.beg; j < sp.end; ++j, ++cnt) {
+      for (int j = beg; j < end; ++j, ++cnt) {
         if (!warp_wait(&bar_sfull[t], cnt & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax)) {
           alive = false;
           break;
@@ -370,9 +386,8 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         uint32_t sr[BN];
         if constexpr (BN == 128) tmem_ld128(t_s, sr);
         else tmem_ld64(t_s, sr);
-        const int key0 = key_base + j * BN;
-        const int lim = last - key0, lo = first - key0;  // columns lo <= c <= lim are visible to this row
-        const bool cut = key0 < all_lo || key0 + BN > all_hi;  // a mask cuts the block
+        const int lim = lim0 - j * BN, lo = lo0 - j * BN;  // columns lo <= c <= lim are visible to this row
+        const bool cut = j < j_lo || j >= j_hi;  // a mask cuts the block
         if constexpr (kMaskInPlace) {
           if (zero_scale) {
 #pragma unroll
@@ -387,7 +402,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         auto block_max = [&]() {
           return block_max_scaled<BN, !kMaskInPlace>(sr, masked, lo, kMaskInPlace ? BN : lim, ce, neg_scale);
         };
-        if (j == sp.beg) m = block_max();
+        if (j == beg) m = block_max();
         float alpha = 1.f;
         auto exps = [&]() {
           const float m_use = m == -INFINITY ? 0.f : m;  // rows with no visible key so far
@@ -416,7 +431,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         // A block whose sum breaks the bound (or a row's first visible key)
         // moves the maximum, rescales O and is done again.  Lanes past the
         // tile's rows hold anything and never ask for it.
-        const bool need = row_ok && (!(blk <= kSumLimit) || (m == -INFINITY && max(lo, 0) <= min(lim, BN - 1)));
+        const bool need = row_ok && (!(blk <= kSumLimit) || m == -INFINITY);
         if (__any_sync(0xffffffffu, need)) {
           const float m_blk = block_max();
           const bool upd = need && m_blk > m;
@@ -427,7 +442,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           if (__any_sync(0xffffffffu, upd)) {
             tmem_st_wait();  // the first pass's stores land before they are overwritten
             blk = exps();
-            if (j > sp.beg) {
+            if (j > beg) {
 #pragma unroll
               for (int c = 0; c < D; c += 16) {
                 uint32_t o16[16];
@@ -450,7 +465,8 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       }
       if (!alive) break;
       // ------------------------------------------------------------ segment's end
-      const bool have = sp.end > sp.beg;
+      w = s_walk[warp];
+      const bool have = end > beg;
       if (have) {
         if (!warp_wait(&bar_ofinal[t], fin & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax)) {
           alive = false;
@@ -463,13 +479,13 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       const int slot = 2 * static_cast<int>(blockIdx.x) + (w.blk == 0 ? 1 : 0);
       const bool seen = have && l > 0.f;
       const float inv_l = seen ? 1.f / l : 0.f;
-      const int tok = w.u.tok0 + sp.ta + rt, head = w.kvh * p.G + rh;
+      const int ta = t * tile_tok, tok = w.u.tok0 + ta + rt, head = w.kvh * p.G + rh;
       // Partials lie [slot][D / 4][part_rows][4]: neighbouring lanes (rows) write
       // neighbouring 16 bytes.
-      const int prow = (sp.ta + rt) * p.G + rh;
+      const int prow = (ta + rt) * p.G + rh;
       float* part = p.o_part + static_cast<int64_t>(slot) * p.part_rows * D + prow * 4;
       elem_t* orow = static_cast<elem_t*>(p.o) + (static_cast<int64_t>(tok) * p.H + head) * D;
-      if (sp.n_tok > 0) {  // (warp-uniform)
+      if (ta < w.u.n_tok) {  // (warp-uniform)
 #pragma unroll
         for (int c = 0; c < D; c += 16) {
           uint32_t o16[16];
