@@ -592,7 +592,7 @@ def _raw_stream(device: int) -> int:
 def _call_device(first, *others) -> int:
     """The one device of all tensors, which must be the current one (kernels launch there)."""
     import torch
-    d = first.get_device()
+    d = first.get_device()  # -1: not on a GPU
     for x in others:
         if x is not None and x.get_device() != d:
             raise ValueError("all tensors must be on one CUDA device")
@@ -656,21 +656,27 @@ def _rotate(what, q, k, positions, steps, interleaved, magnitude, q_out, k_out, 
     d = _call_device(q, k, positions, steps, q_out, k_out)
     dtype, shape, k_shape = q.dtype, _three(q, "q"), _three(k, "k")
     T, H, D = shape
-    hk = k_shape[1]
+    hk, n = k_shape[1], steps.numel()
     if k_shape[0] != T or k_shape[2] != D:
         raise ValueError("k must have q's tokens and head dimension")
+    qs, ks = _rows(q, "q", shape, dtype), _rows(k, "k", k_shape, dtype)
+    pos = _int_array(positions, "positions", torch.int32, (T,))
+    table = _int_array(steps, "steps", torch.int64, (n,))
+    qos, kos = H * D, hk * D  # token strides of outputs made here
+    if q_out is not None:
+        qos = _rows(q_out, "the q output", shape, dtype)
+    if k_out is not None:
+        kos = _rows(k_out, "the k output", k_shape, dtype)
     if q_out is None and k_out is None:
         q_out, k_out = _allocate(stream, d, (shape, dtype), (k_shape, dtype))
     elif q_out is None:
         q_out, = _allocate(stream, d, (shape, dtype))
     elif k_out is None:
         k_out, = _allocate(stream, d, (k_shape, dtype))
-    n = steps.numel()
-    _check(getattr(_load(), what)(q.data_ptr(), _rows(q, "q", shape, dtype), k.data_ptr(), _rows(k, "k", k_shape, dtype),
-               q_out.data_ptr(), _rows(q_out, "the q output", shape, dtype), k_out.data_ptr(),
-               _rows(k_out, "the k output", k_shape, dtype), _int_array(positions, "positions", torch.int32, (T,)),
-               _int_array(steps, "steps", torch.int64, (n,)), T, H, hk, D, 2 * n, interleaved, magnitude,
-               _dtype_code(q), _raw_stream(d) if stream is None else stream.cuda_stream), what)
+    st = getattr(_load(), what)(q.data_ptr(), qs, k.data_ptr(), ks, q_out.data_ptr(), qos, k_out.data_ptr(), kos, pos,
+                                table, T, H, hk, D, 2 * n, interleaved, magnitude, _dtype_code(q),
+                                _raw_stream(d) if stream is None else stream.cuda_stream)
+    _check(st, what)
     return q_out, k_out
 
 
@@ -746,10 +752,12 @@ def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_s
         H = q_shape[1]
         if q_shape[0] != T or q_shape[2] != D:
             raise ValueError("q must have k's tokens and head dimension")
+        qs, qos = _rows(q, "q", q_shape, dtype), H * D
         if q_out is None:
             q_out, = _allocate(stream, d, (q_shape, dtype))
-        q_args = (q.data_ptr(), _rows(q, "q", q_shape, dtype), q_out.data_ptr(),
-                  _rows(q_out, "q_out", q_shape, dtype))
+        else:
+            qos = _rows(q_out, "q_out", q_shape, dtype)
+        q_args = (q.data_ptr(), qs, q_out.data_ptr(), qos)
     n = 0 if steps is None else steps.numel()
     _check(_load().fa_paged_append(*q_args, k.data_ptr(), _rows(k, "k", shape, dtype), v.data_ptr(),
                            _rows(v, "v", shape, dtype), cache, cu_seqlens.data_ptr(),
