@@ -14,10 +14,13 @@ using namespace ptx;
 // c of the main kernel computed; D / 4 threads span a row.  A CTA takes several
 // rows at once; only a unit in many parts (a long context, few rows) has them
 // one by one, the parts split over the CTA and summed in a fixed order.  The
-// partials come from L2; three dependent reads (descriptor, logsumexps,
-// partials) bound a CTA, so the grid is kept to a few CTAs per SM.
-constexpr int kMergeThreads = 256;
+// partials come from L2, so what bounds the kernel is its launch and the chain
+// of reads: descriptor, then all of a row's parts at once.  Decoding over 4
+// contexts of 131072 keys takes 161 us with a loop over the parts and 150 with
+// their reads in flight together (the main kernel alone: 150).
+constexpr int kMergeThreads = 128;
 constexpr int kMergeFew = 24;  // parts up to which a CTA takes several rows at once
+constexpr int kMergeBatch = 8;  // parts whose reads are in flight together
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const PagedMergeParams p) {
@@ -28,7 +31,11 @@ __global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const Pag
   griddep_wait();
   griddep_launch_dependents();
   const int first = blockIdx.x;
-  const PagedParts q = p.parts[blockIdx.z];
+  // (an index into the parameters would put a copy of them on the stack)
+  const bool z = blockIdx.z != 0;
+  const PagedParts q{z ? p.parts[1].o_part : p.parts[0].o_part, z ? p.parts[1].lse_part : p.parts[0].lse_part,
+                     z ? p.parts[1].desc : p.parts[0].desc,     z ? p.parts[1].rows : p.parts[0].rows,
+                     z ? p.parts[1].grid : p.parts[0].grid,     z ? p.parts[1].by_chunk : p.parts[0].by_chunk};
   if (first >= q.grid) return;
   const int4 d = q.desc[first];
   const int n_rows = d.y * p.G;
@@ -51,24 +58,44 @@ __global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const Pag
          task < tasks; task += gridDim.y * (kMergeThreads / 32)) {
       const int row = task / kStrips * 32 + lane, strip = task % kStrips;
       if (row >= n_rows) continue;
-      float mx = -INFINITY;
-#pragma unroll 4
-      for (int s = 0; s < parts; ++s) mx = fmaxf(mx, q.lse_part[at(s, row)]);
-      const bool seen = mx != -INFINITY;
-      float total = 0.f;
+      float mx = -INFINITY, total = 0.f;
       float4 o[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (seen) {
-#pragma unroll 2
-        for (int s = 0; s < parts; ++s) {
-          const float w = exp2f(q.lse_part[at(s, row)] - mx);
-          const float4* src = reinterpret_cast<const float4*>(q.o_part + at(s, 0) * D) + 4 * strip * q.rows + row;
-          total += w;
+      constexpr int kBatch = 3;  // units of the tile kernel are in two or three parts as a rule
+      for (int s0 = 0; s0 < parts; s0 += kBatch) {
+        float l[kBatch];
+        float4 v[kBatch][4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) add(o[c], w, src[c * q.rows]);
+        for (int k = 0; k < kBatch; ++k) {
+          l[k] = -INFINITY;
+          if (s0 + k < parts) {
+            l[k] = q.lse_part[at(s0 + k, row)];
+            const float4* src = reinterpret_cast<const float4*>(q.o_part + at(s0 + k, 0) * D) + 4 * strip * q.rows + row;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[k][c] = src[c * q.rows];
+          }
+        }
+        float m_new = mx;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) m_new = fmaxf(m_new, l[k]);
+        if (m_new == -INFINITY) continue;
+        const float keep = exp2f(mx - m_new);
+        mx = m_new;
+        total *= keep;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = make_float4(o[c].x * keep, o[c].y * keep, o[c].z * keep, o[c].w * keep);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (l[k] != -INFINITY) {
+            const float w = exp2f(l[k] - mx);
+            total += w;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) add(o[c], w, v[k][c]);
+          }
         }
       }
+      const bool seen = mx != -INFINITY;
       const float inv = seen ? 1.f / total : 0.f;
       const int tok = d.x + row / p.G, head = d.z * p.G + row % p.G;
       uint4* orow = reinterpret_cast<uint4*>(static_cast<elem_t*>(p.o) +
@@ -97,17 +124,34 @@ __global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const Pag
   };
   if (parts <= kMergeFew) {
     for (int row = static_cast<int>(blockIdx.y) * kGroups + y; row < n_rows; row += gridDim.y * kGroups) {
-      float mx = -INFINITY;
-#pragma unroll 4
-      for (int s = 0; s < parts; ++s) mx = fmaxf(mx, q.lse_part[at(s, row)]);
+      float mx = -INFINITY, total = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float total = 0.f;
-      if (mx != -INFINITY) {
-#pragma unroll 4
-        for (int s = 0; s < parts; ++s) {
-          const float w = exp2f(q.lse_part[at(s, row)] - mx);
-          total += w;
-          add(o, w, *reinterpret_cast<const float4*>(q.o_part + at(s, row) * D + 4 * x));
+      for (int s0 = 0; s0 < parts; s0 += kMergeBatch) {
+        float l[kMergeBatch];
+        float4 v[kMergeBatch];
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) {
+          l[k] = -INFINITY;
+          if (s0 + k < parts) {
+            l[k] = q.lse_part[at(s0 + k, row)];
+            v[k] = *reinterpret_cast<const float4*>(q.o_part + at(s0 + k, row) * D + 4 * x);
+          }
+        }
+        float m_new = mx;
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) m_new = fmaxf(m_new, l[k]);
+        if (m_new == -INFINITY) continue;
+        const float keep = exp2f(mx - m_new);
+        mx = m_new;
+        total *= keep;
+        o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) {
+          if (l[k] != -INFINITY) {
+            const float w = exp2f(l[k] - mx);
+            total += w;
+            add(o, w, v[k]);
+          }
         }
       }
       store(row, o, total, mx);
@@ -148,15 +192,14 @@ namespace {
 
 template <int D, bool BF16>
 cudaError_t launch_paged_merge_t(const PagedMergeParams& p, int grid, int sets, cudaStream_t stream) {
-  // Slices: eight warps of one 32 x 16 strip each for the tile kernel's units,
-  // two rounds of a CTA's rows for the others.
+  // Slices: one round of a CTA's strips or rows.
   int slices = 1;
   for (int z = 0; z < sets; ++z) {
-    const int rows = p.parts[z].rows, per = 2 * kMergeThreads / (D / 4);
+    const int rows = p.parts[z].rows, per = kMergeThreads / (D / 4);
     const int n = p.parts[z].by_chunk ? (rows + 31) / 32 * (D / 16) / (kMergeThreads / 32) : (rows + per - 1) / per;
     if (n > slices) slices = n;
   }
-  return launch_dependent(fa_paged_merge_kernel<D, BF16>, dim3(grid, slices < 8 ? 8 : slices, sets),
+  return launch_dependent(fa_paged_merge_kernel<D, BF16>, dim3(grid, slices, sets),
                           kMergeThreads, 0, stream, p);
 }
 

@@ -193,6 +193,30 @@ def test_long_contexts_cut_between_ctas(fa):
     assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
+@pytest.mark.parametrize("q_len", [1, 3, 300])
+@pytest.mark.parametrize("D", [16, 64, 128])
+def test_one_long_sequence(fa, q_len, D):
+    """One sequence, one K/V head: the whole GPU shares each unit, in parts that a kernel of its own joins."""
+    case(fa, [9000], [q_len], 4, 1, D, 32, "fp16")
+
+
+@pytest.mark.parametrize("q_len", [1, 20, 200])
+def test_garbage_in_the_workspace_does_not_matter(fa, q_len):
+    """Every bit pattern a workspace may hold on entry; the same one used again and again."""
+    lens, q_lens = [3000, 777], [q_len, q_len]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, 64, 32, torch.bfloat16, 40)
+    q = rnd((cu[-1], 8, 64), 41, torch.bfloat16)
+    need = fa.fa_fwd_paged_workspace_size(2, q_len, 3000, 8, 2, 64)
+    first = None
+    for fill in (0, 255, 127, None, None):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda") if fill is not None else ws
+        o, lse = run(fa, q, kc, vc, table, lens, cu, workspace=ws)
+        if first is None:
+            check(o, lse, q, kc, vc, table, lens, cu)
+            first = (o, lse)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
 def test_many_sequences(fa):
     g = torch.Generator().manual_seed(11)
     lens = torch.randint(1, 200, (500,), generator=g).tolist()
