@@ -30,9 +30,9 @@
 // programmatic dependent, joins in CTA order: no atomics, the result depends
 // only on the lengths.
 //
-// Warp roles: 4 (N <= 64) or 8 softmax warps, one TMA producer, one MMA
-// issuer.  Order of the tensor core's work: S(0), then S(j+1), O(j) for each
-// block j, so scores of the next block are computed during the softmax.
+// Warp roles: 4 to 16 softmax warps, two TMA producers (K, V), one MMA issuer.
+// Order of the tensor core's work: S(0), then S(j+1), O(j) for each block j, so
+// scores of the next block are computed during the softmax.
 //
 // Pages.  A 128-key tile arrives as 128 / min(page, 128) boxes of whole or
 // part pages; boxes that hold no visible key are not read (an out-of-range
@@ -60,21 +60,31 @@ struct PagedLayout {
   using GK = TileGeom<D, kPBlk>;   // K and V tiles
   using GQ = TileGeom<D, N>;       // Q tile, N rows
   using GP = TileGeom<N, kPBlk>;   // P^T tile: 128 keys x N rows
-  // Softmax warpgroups, each over kCols rows.  32 rows a thread: with 64 a
-  // block of N = 64 took 2200 cycles of softmax (one warp per SM sub-partition
-  // hides nothing), above the 1400 that D = 64 has at the memory's rate.
-  static constexpr int kCols = N < 32 ? N : 32;
+  // Softmax warpgroups, each over kCols rows.  More of them hide more of each
+  // other's latency, down to 16 rows a thread; N = 128 has the registers for two
+  // only.  Measured, 16 sequences of 8192 keys at D = 64: N = 64 with 64 / 32 /
+  // 16 rows a thread 45 / 38.7 / 36.4 us, N = 128 with 32 / 64 68.4 / 57.1 us
+  // (32 spills).
+  static constexpr int kCols = N == 128 ? 64 : 16;
   static constexpr int kWgs = N / kCols;
-  static constexpr int kThreads = 128 * kWgs + 64;
+  static constexpr int kThreads = 128 * kWgs + 96;  // and the producers of K and V, the MMA issuer
   static constexpr int kQBufs = N > 64 ? 1 : 2;
   static constexpr int kQBytes = (GQ::kTileBytes + 1023) / 1024 * 1024;
   static constexpr int kSmallBytes = 5 * 1024;      // barriers and per-row arrays
   static constexpr int kBudget = 227 * 1024 - 1024;
-  static constexpr int kUnitsFit = (kBudget - 2 * GP::kTileBytes - kQBufs * kQBytes - kSmallBytes) / GK::kTileBytes;
-  static constexpr int kUnits = kUnitsFit > 16 ? 16 : kUnitsFit;  // ring stages, one K or V tile each
-  static_assert(kUnits >= 3, "ring");
+  // P tiles: two, so that a block's P is written while the tensor core reads the
+  // one before; one where two would leave the ring three stages.
+  static constexpr int kPBufs = N == 128 && D == 128 ? 1 : 2;
+  static constexpr int kUnitsFit =
+      (kBudget - kPBufs * GP::kTileBytes - kQBufs * kQBytes - kSmallBytes) / GK::kTileBytes;
+  // Ring stages, one K or V tile each.  An even number: K tiles have the even
+  // stages, V tiles the odd ones, and each producer sees every phase of its
+  // stages' barriers.  (On a stage that both used, a producer could take a
+  // phase for the one before the last: they have the same parity.)
+  static constexpr int kUnits = (kUnitsFit > 16 ? 16 : kUnitsFit) & ~1;
+  static_assert(kUnits >= 4, "ring");
   static constexpr int kOffP = kUnits * GK::kTileBytes;
-  static constexpr int kOffQ = kOffP + 2 * GP::kTileBytes;
+  static constexpr int kOffQ = kOffP + kPBufs * GP::kTileBytes;
   static constexpr int kOffSmall = kOffQ + kQBufs * kQBytes;
   // full[U], empty[U], qfull[2], qempty[2], sfull[2], pfull[2], pv[2], vtmp, drain
   static constexpr int kNumBars = 2 * kUnits + 10 + 2;
@@ -149,7 +159,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
   constexpr int U = L::kUnits;
   constexpr int NC = L::kCols;
   constexpr int kSoftWarps = 4 * L::kWgs;
-  constexpr int kProducer = kSoftWarps, kMma = kSoftWarps + 1;
+  constexpr int kProducer = kSoftWarps, kMma = kSoftWarps + 2;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -230,13 +240,17 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
   SegWalk<kPShift> w;
   w.start(*s_start);
 
-  if (warp == kProducer) {
-    // -------------------------------------------------------------- producer
-    // The whole warp runs this; lane i copies page box i of each tile.
+  if (warp == kProducer || warp == kProducer + 1) {
+    // -------------------------------------------------------------- producers
+    // One warp copies Q and the K tiles, one the V tiles (ring stages alternate).
+    // The whole warp runs this; lane i copies page box i of each tile.  With one
+    // warp for both, its 500-700 cycles per tile bounded the kernel at D <= 64.
+    const int kv = warp - kProducer;  // 0: K, 1: V
+    const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;
     const int frag = min(kPBlk, 1 << p.page_shift);
     const int n_frag = kPBlk / frag;
-    int c = 0;    // tiles started
-    int seg = 0;  // segments started
+    int c = kv;   // ring stage of the next tile, counted through (K even, V odd)
+    int seg = 0;  // segments started (Q tiles)
     int n_cut = 0;  // V tiles that had rows cleared
     bool ok = true;
     auto box_page = [&](int blk) -> int {  // page (or out of range) of this lane's box of the unit's block
@@ -249,63 +263,65 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
     };
     for (int n; ok && (n = w.seg_len()) > 0; w.next(p), ++seg) {
       int page = box_page(w.blk);
-      const int qb = L::kQBufs == 2 ? (seg & 1) : 0;
-      const int qu = L::kQBufs == 2 ? (seg >> 1) : seg;
-      if (qu > 0) ok = warp_wait(&bar_qempty[qb], (qu - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bar_qfull[qb], GQ::kChunks * GQ::kRowBytes * p.G * p.tok_tile);
+      if (kv == 0) {
+        const int qb = L::kQBufs == 2 ? (seg & 1) : 0;
+        const int qu = L::kQBufs == 2 ? (seg >> 1) : seg;
+        if (qu > 0) ok = warp_wait(&bar_qempty[qb], (qu - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar_qfull[qb], GQ::kChunks * GQ::kRowBytes * p.G * p.tok_tile);
 #pragma unroll
-        for (int ch = 0; ch < GQ::kChunks; ++ch)
-          tma_load_3d(smem + L::kOffQ + qb * L::kQBytes + ch * GQ::kChunkBytes, &tm_q, &bar_qfull[qb],
-                      ch * (GQ::kRowBytes / 2), w.kvh * p.G, w.u.tok0);
+          for (int ch = 0; ch < GQ::kChunks; ++ch)
+            tma_load_3d(smem + L::kOffQ + qb * L::kQBytes + ch * GQ::kChunkBytes, &tm_q, &bar_qfull[qb],
+                        ch * (GQ::kRowBytes / 2), w.kvh * p.G, w.u.tok0);
+        }
+        __syncwarp();
       }
       for (int j = 0; ok && j < n; ++j) {
         const int page_next = j + 1 < n ? box_page(w.blk + j + 1) : 0;
         const int key0 = (w.u.lo / kPBlk + w.blk + j) * kPBlk;
         const int row = (key0 + lane * frag) & ((1 << p.page_shift) - 1);
         const bool cut = key0 < w.u.lo || key0 + kPBlk > w.u.hi;
+        const int st = c % U, use = c / U;
+        if (use > 0) {
+          ok = warp_wait(&bar_empty[st], (use - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
+          if (!ok) break;
+        }
+        uint8_t* tile = smem + st * GK::kTileBytes;
+        uint64_t* bar = kv == 1 && cut ? bar_vtmp : &bar_full[st];
+        if (lane == 0) mbar_arrive_expect_tx(bar, GK::kTileBytes);
+        __syncwarp();
+        if (lane < n_frag) {
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int st = c % U, use = c / U;
-          if (use > 0) {
-            ok = warp_wait(&bar_empty[st], (use - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
-            if (!ok) break;
+          for (int ch = 0; ch < GK::kChunks; ++ch)
+            tma_load_4d(tile + ch * GK::kChunkBytes + lane * frag * GK::kRowBytes, map, bar, ch * (GK::kRowBytes / 2),
+                        w.kvh, row, page);
+        }
+        c += 2;
+        if (kv == 1 && cut) {
+          // Clear the V rows no row of the unit sees.
+          drain_wait(bar_vtmp, n_cut & 1, p.err);
+          ++n_cut;
+          const int k0 = max(0, w.u.lo - key0), k1 = min(kPBlk, w.u.hi - key0);  // visible rows [k0, k1)
+          constexpr int kVecs = GK::kRowBytes / 16;
+          for (int i = lane; i < kPBlk * kVecs * GK::kChunks; i += 32) {
+            const int r = (i / kVecs) % kPBlk;
+            if (r < k0 || r >= k1) *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
           }
-          uint8_t* tile = smem + st * GK::kTileBytes;
-          uint64_t* bar = kv == 1 && cut ? bar_vtmp : &bar_full[st];
-          if (lane == 0) mbar_arrive_expect_tx(bar, GK::kTileBytes);
+          fence_proxy_async_smem();
           __syncwarp();
-          if (lane < n_frag) {
-#pragma unroll
-            for (int ch = 0; ch < GK::kChunks; ++ch)
-              tma_load_4d(tile + ch * GK::kChunkBytes + lane * frag * GK::kRowBytes, kv == 0 ? &tm_k : &tm_v, bar,
-                          ch * (GK::kRowBytes / 2), w.kvh, row, page);
-          }
-          ++c;
-          if (kv == 1 && cut) {
-            // Clear the V rows no row of the unit sees.
-            drain_wait(bar_vtmp, n_cut & 1, p.err);
-            ++n_cut;
-            const int k0 = max(0, w.u.lo - key0), k1 = min(kPBlk, w.u.hi - key0);  // visible rows [k0, k1)
-            constexpr int kVecs = GK::kRowBytes / 16;
-            for (int i = lane; i < kPBlk * kVecs * GK::kChunks; i += 32) {
-              const int r = (i / kVecs) % kPBlk;
-              if (r < k0 || r >= k1)
-                *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_full[st]);
-          }
+          if (lane == 0) mbar_arrive(&bar_full[st]);
         }
         page = page_next;
       }
     }
-    // Teardown: every copy this warp started lands before the CTA exits.
-    for (int x = (c > U ? c - U : 0); x < c; ++x) drain_wait(&bar_full[x % U], (x / U) & 1, p.err);
-    for (int x = (seg > L::kQBufs ? seg - L::kQBufs : 0); x < seg; ++x)
-      drain_wait(&bar_qfull[x % L::kQBufs], (x / L::kQBufs) & 1, p.err);
+    // Teardown: every copy this warp started lands before the CTA exits (older
+    // ones of a stage were consumed before it was used again).
+    for (int x = c - 2; x >= 0 && x >= c - U; x -= 2)
+      drain_wait(&bar_full[x % U], (x / U) & 1, p.err);
+    if (kv == 0)
+      for (int x = (seg > L::kQBufs ? seg - L::kQBufs : 0); x < seg; ++x)
+        drain_wait(&bar_qfull[x % L::kQBufs], (x / L::kQBufs) & 1, p.err);
     __syncwarp();
   } else if (warp == kMma) {
     // -------------------------------------------------------------- MMA issuer
@@ -354,7 +370,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
       tc_fence_after();
       const uint64_t v_desc = make_sdesc(s_ring + st * GK::kTileBytes, L::kVLbo, 8 * GK::kRowBytes, GK::kSwz);
       const uint64_t p_desc =
-          make_sdesc(s_p + (i & 1) * GP::kTileBytes, GP::kChunkBytes, 8 * GP::kRowBytes, GP::kSwz);
+          make_sdesc(s_p + (i & 1) * (L::kPBufs - 1) * GP::kTileBytes, GP::kChunkBytes, 8 * GP::kRowBytes, GP::kSwz);
 #pragma unroll
       for (int kk = 0; kk < kPBlk / 16; ++kk)
         mma_ss_warp(t_o, desc_plus(v_desc, mnmajor_step_bytes<D>(kk)), desc_plus(p_desc, mnmajor_step_bytes<N>(kk)),
@@ -406,9 +422,12 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
         bool ok = warp_wait(&bar_sfull[i & 1], (i >> 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
         // O(i-2) is done (S(i) was issued after it).  Waiting for it keeps this
         // warp one phase behind each of the two barriers, so that a wait for
-        // O(i-1) below cannot take the phase before it for it.
-        if (ok && i >= 2)
-          ok = warp_wait(&bar_pv[i & 1], ((i >> 1) - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
+        // O(i-1) below cannot take the phase before it for it.  With one P tile,
+        // O(i-1) must be done before P(i) is written.
+        const int behind = L::kPBufs;
+        if (ok && i >= behind)
+          ok = warp_wait(&bar_pv[(i - behind) & 1], ((i - behind) >> 1) & 1, abort_flag, p.err, p.wait_ns,
+                         kErrTimeoutSoftmax);
         const int key0 = (blk_first + jb) * kPBlk;
         const int key = key0 + key_lane;
         const bool cut = key0 < full_lo || key0 + kPBlk > full_hi;
@@ -499,7 +518,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
         exact_max = cut;
         // P~ = 2^(c s - m), 16-bit, into the key's row of the P^T tile; the
         // running sums take the unrounded values.
-        uint8_t* prow = p_tile + (i & 1) * GP::kTileBytes;
+        uint8_t* prow = p_tile + (i & 1) * (L::kPBufs - 1) * GP::kTileBytes;
 #pragma unroll
         for (int k = 0; k < NC; k += 8) {
           uint32_t pk[4];
