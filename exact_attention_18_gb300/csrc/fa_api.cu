@@ -588,7 +588,8 @@ bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t 
     return false;
   const int64_t G = H / H_kv;
   plan->bytes = 0;
-  auto add = [&](PagedPart* part, int64_t tok, int64_t longest, int64_t block, int64_t slot_rows) -> bool {
+  auto add = [&](PagedPart* part, int64_t tok, int64_t longest, int64_t block, int64_t slot_rows,
+                 int64_t ctas) -> bool {
     part->used = true;
     part->tok_tile = static_cast<int>(tok < longest ? tok : longest);
     part->tiles = static_cast<int>((longest + part->tok_tile - 1) / part->tok_tile);
@@ -598,7 +599,7 @@ bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t 
     const int64_t blocks = (max_k + block - 1) / block + 1;  // of a unit, at most
     if (units > (int64_t(1) << 37) / (blocks * H_kv)) return false;  // a CTA's run of blocks fits 31 bits
     const int64_t most = units * H_kv * blocks;
-    part->grid = static_cast<int>(most < fa::kPagedGrid ? most : fa::kPagedGrid);
+    part->grid = static_cast<int>(most < ctas ? most : ctas);
     part->o_at = plan->bytes;
     part->lse_at = part->o_at + round256(static_cast<size_t>(2) * part->grid * part->part_rows * D * sizeof(float));
     part->desc_at = part->lse_at + round256(static_cast<size_t>(2) * part->grid * part->part_rows * sizeof(float));
@@ -612,14 +613,15 @@ bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t 
     plan->few.N = fa::paged_rows(longest * G);
     plan->few.rows_lo = 0;
     plan->few.rows_hi = chunks ? longest * G : max_q * G;
-    if (!add(&plan->few, longest, longest, 128, plan->few.N)) return false;
+    const int64_t ctas = fa::kPagedSms * fa::paged_ctas(static_cast<int>(D), plan->few.N);
+    if (!add(&plan->few, longest, longest, 128, plan->few.N, ctas)) return false;
   }
   if (chunks) {
     const int Di = static_cast<int>(D);
     plan->tile.rows_lo = plan->few.used ? plan->few.rows_hi + 1 : 0;
     plan->tile.rows_hi = max_q * G;
     const int64_t tok = fa::paged_tile_tiles(Di) * (128 / G);
-    if (!add(&plan->tile, tok, max_q, fa::paged_tile_block(Di), tok * G)) return false;
+    if (!add(&plan->tile, tok, max_q, fa::paged_tile_block(Di), tok * G, fa::kPagedSms)) return false;
   }
   return true;
 }

@@ -115,7 +115,9 @@ struct PagedMergeParams {
 // Rows of a unit the kernel is instantiated for; the smallest that holds
 // `rows`, else the largest.
 inline int paged_rows(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
-constexpr int kPagedGrid = 152;  // CTAs at most: one per SM
+constexpr int kPagedSms = 152;
+// CTAs per SM of the few-row kernel.
+constexpr int paged_ctas(int D, int N) { return D <= 64 && N == 16 ? 2 : 1; }
 // Rows of a unit of the tile kernel (tiles of 128 rows) and keys of its blocks.
 inline int paged_tile_tiles(int D) { return D == 128 ? 2 : 4; }
 inline int paged_tile_block(int D) { return D == 128 ? 128 : 64; }

@@ -21,8 +21,8 @@
 // What bounds it: with few rows, reading the cache.  At D = 128 a 128-key
 // block is 64 KB, 2800 cycles of an SM's share of the memory's rate, against
 // ~650 cycles of tensor core and ~500 of softmax for N <= 32.  So the kernel
-// is organised around keeping copies in flight: one persistent CTA per SM,
-// its shared memory given to a ring of K and V tiles, and work dealt in
+// is organised around keeping copies in flight: one or two persistent CTAs per
+// SM, their shared memory given to a ring of K and V tiles, and work dealt in
 // 128-key blocks: the blocks of all units, in order, are cut into equal runs,
 // one per CTA, whatever the sequences' lengths (each CTA finds its run from
 // the lengths on the device).  A unit cut between CTAs leaves fp32 partials
@@ -71,7 +71,11 @@ struct PagedLayout {
   static constexpr int kQBufs = N > 64 ? 1 : 2;
   static constexpr int kQBytes = (GQ::kTileBytes + 1023) / 1024 * 1024;
   static constexpr int kSmallBytes = 5 * 1024;      // barriers and per-row arrays
-  static constexpr int kBudget = 227 * 1024 - 1024;
+  // CTAs per SM (paged_ctas).  A block's chain of waits, loads and exponentials
+  // takes about 1100 cycles however narrow the heads; at D = 128 that hides
+  // behind the block's 2800 cycles of memory, below it a second CTA fills it.
+  static constexpr int kCtas = paged_ctas(D, N);
+  static constexpr int kBudget = (kCtas == 2 ? 113 : 227) * 1024 - 1024;
   // P tiles: two, so that a block's P is written while the tensor core reads the
   // one before; one where two would leave the ring three stages.
   static constexpr int kPBufs = N == 128 && D == 128 ? 1 : 2;
@@ -89,9 +93,12 @@ struct PagedLayout {
   // full[U], empty[U], qfull[2], qempty[2], sfull[2], pfull[2], pv[2], vtmp, drain
   static constexpr int kNumBars = 2 * kUnits + 10 + 2;
   static_assert(kNumBars * 8 + 24 + sizeof(RunStart) + 8 * N * 4 + 2 * N <= kSmallBytes, "small arrays");
-  // One CTA per SM: the request is padded above half of the SM's shared memory.
+  // The request is padded so that no more CTAs than meant share an SM, nor one
+  // of these with a kernel that takes the whole tensor memory (those ask for
+  // 116 KB at least).
   static constexpr int kSmemUsed = kOffSmall + kSmallBytes + 1024;
-  static constexpr int kSmemBytes = kSmemUsed > 116 * 1024 ? kSmemUsed : 116 * 1024;
+  static constexpr int kSmemLeast = (kCtas == 2 ? 112 : 116) * 1024;
+  static constexpr int kSmemBytes = kSmemUsed > kSmemLeast ? kSmemUsed : kSmemLeast;
   static constexpr uint32_t kTmemCols = 3 * N <= 64 ? 64 : (3 * N <= 128 ? 128 : (3 * N <= 256 ? 256 : 512));
   // V^T is D rows; the MMA's 128 rows past D repeat tile rows 8 further on
   // (in bounds: the ring is followed by the P tiles) into TMEM lanes nobody reads.
@@ -148,7 +155,7 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
 // tm_q: {D, H, T} map, box {row chunk, G, tok_tile}; tm_k, tm_v: {D, H_kv,
 // page_size, pages} maps, box {row chunk, 1, min(page_size, 128), 1}.
 template <int D, int N, bool BF16>
-__global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, 1)
+__global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>::kCtas)
     fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
   using L = PagedLayout<D, N>;
