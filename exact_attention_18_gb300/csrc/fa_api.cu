@@ -661,9 +661,16 @@ fa_status encode_paged_kv(CUtensorMap* map, const void* base, bool bf16, const f
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   CUtensorMapSwizzle swz = rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                      : (rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+  // L2 lines fetched along with a miss: no more than lies contiguous in the
+  // cache (a row of one head, unless a head's rows follow one another).
+  const int64_t run = c->row_stride == D ? 256 : D * 2;
+  const CUtensorMapL2promotion promote = run >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                         : run == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                         : run == 64  ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                                      : CU_TENSOR_MAP_L2_PROMOTION_NONE;
   CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "tensor map for %s: cuTensorMapEncodeTiled error %d", name, (int)r);
   return FA_OK;
 }
