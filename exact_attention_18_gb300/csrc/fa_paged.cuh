@@ -14,7 +14,9 @@ constexpr int kMaxPagedLen = 1 << 29;
 // the grid may start while that kernel's last CTAs run.  Every kernel launched
 // this way waits for the grids before it (griddep_wait, in every thread) ahead
 // of its first access to the caller's memory, so it also never completes
-// before them.
+// before them.  What the caller's earlier kernels may have written is read with
+// plain loads, never through the read-only path (__ldg): that path may serve a
+// line that was cached before the wait.
 template <typename... Params, typename... Args>
 inline cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                                     const Args&... args) {

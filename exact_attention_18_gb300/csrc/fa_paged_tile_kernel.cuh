@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       auto box_page = [&](int blk) -> int {  // page (or out of range) of this lane's box of the unit's block
         const int key = ((w.u.lo >> L::kShift) + blk) * BN + lane * frag;
         if (lane >= n_frag || key >= w.u.hi || key + frag <= w.u.lo) return p.num_pages;
-        const int page = __ldg(p.block_table + static_cast<int64_t>(w.b) * p.table_stride + (key >> p.page_shift));
+        const int page = p.block_table[static_cast<int64_t>(w.b) * p.table_stride + (key >> p.page_shift)];
         if (page >= 0 && page < p.num_pages) return page;
         record_error(p.err, kErrBadPage);
         return p.num_pages;

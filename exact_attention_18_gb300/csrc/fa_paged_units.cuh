@@ -28,7 +28,7 @@ struct SeqLens {
   int a, e, kv;  // cu_seqlens[b], cu_seqlens[b + 1], kv_lens[b]
 };
 __device__ __forceinline__ SeqLens seq_lens(const PagedParams& p, int b) {
-  return SeqLens{__ldg(p.cu_seqlens + b), __ldg(p.cu_seqlens + b + 1), __ldg(p.kv_lens + b)};
+  return SeqLens{p.cu_seqlens[b], p.cu_seqlens[b + 1], p.kv_lens[b]};
 }
 template <int SHIFT>
 __device__ __forceinline__ Unit paged_unit(const PagedParams& p, const SeqLens& s, int tile) {

@@ -88,9 +88,12 @@ __global__ void __launch_bounds__(kRopeMaxThreads) fa_rope_kernel(const RopePara
     b = tile / p.tiles;
     tile -= b * p.tiles;
     tok0 = tile * p.tok_per_cta;
-    int a, len;
-    if (!packed_sample(p.cu_seqlens, b, p.max_len, p.total, p.err, &a, &len)) return;
-    const int kv_len = __ldg(p.kv_lens + b);
+    const int a = p.cu_seqlens[b], e = p.cu_seqlens[b + 1], kv_len = p.kv_lens[b];
+    if (a < 0 || e < a || e - a > p.max_len || e > p.total) {
+      if (threadIdx.x == 0) ptx::record_error(p.err, kErrBadSeqlens);
+      return;
+    }
+    const int len = e - a;
     if (len == 0) return;
     if (kv_len < len || kv_len > p.max_kv) {
       if (threadIdx.x == 0) ptx::record_error(p.err, kErrBadCache);
@@ -157,9 +160,9 @@ __global__ void __launch_bounds__(kRopeMaxThreads) fa_rope_kernel(const RopePara
         const int t = i / r, j = i - t * r;
         int pos;
         if (APPEND && p.positions == nullptr) pos = pos0 + t;
-        else pos = __ldg(p.positions + tok0 + t);
+        else pos = p.positions[tok0 + t];
         const unsigned long long phase =
-            static_cast<unsigned long long>(static_cast<long long>(pos)) * __ldg(p.steps + j);
+            static_cast<unsigned long long>(static_cast<long long>(pos)) * p.steps[j];
         float s, c;
         sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
         s_cs[t * angles + angle_at(j)] = make_float2(c * p.mag, s * p.mag_sin);
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(kRopeMaxThreads) fa_rope_kernel(const RopePara
       if constexpr (APPEND) {
         for (int i = threadIdx.x; i < n_tok; i += threads) {
           const int pos = pos0 + i;
-          const int page = __ldg(p.block_table + static_cast<int64_t>(b) * p.table_stride + (pos >> p.page_shift));
+          const int page = p.block_table[static_cast<int64_t>(b) * p.table_stride + (pos >> p.page_shift)];
           int64_t slot = -1;
           if (page >= 0 && page < p.num_pages)
             slot = static_cast<int64_t>(page) * p.page_stride +

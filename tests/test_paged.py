@@ -336,6 +336,77 @@ def test_other_stream_and_captured_graph(fa):
         check(out, l2, qn, kc, vc, table, now, cu)
 
 
+def test_sequences_that_share_pages(fa):
+    """Two sequences with a common prefix in the same pages, and one twice in the batch."""
+    lens, q_lens = [100, 80, 100], [3, 1, 2]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, 64, 16, torch.float16, 50)
+    table[1, :4] = table[0, :4]
+    table[2] = table[0]
+    q = rnd((cu[-1], 4, 64), 51, torch.float16)
+    o, lse = run(fa, q, kc, vc, table, lens, cu)
+    check(o, lse, q, kc, vc, table, lens, cu)
+
+
+@pytest.mark.parametrize("q_len", [1, 150])
+def test_two_streams_at_once(fa, q_len):
+    """Calls on two streams, back to back and unsynchronised, each with its stream's scratch."""
+    lens, q_lens = [5000, 900], [q_len, q_len]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, 128, 64, torch.bfloat16, 52)
+    kcg, vcg = on_gpu(kc, vc)
+    args = (kcg, vcg, ints(table), ints(lens), ints(cu), q_len, 5000)
+    qs = [rnd((cu[-1], 8, 128), 53 + i, torch.bfloat16) for i in range(2)]
+    qg = [x.cuda() for x in qs]
+    want = [fa.forward_paged(x, *args) for x in qg]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(5):
+        got += [(i, fa.forward_paged(qg[i], *args, stream=streams[i])) for i in range(2)]
+    torch.cuda.synchronize()
+    assert fa.fa_check_device_errors(None) == 0
+    for i, (o, lse) in got:
+        assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+    check(want[0][0], want[0][1], qs[0], kc, vc, table, lens, cu)
+
+
+def test_captured_step_replayed(fa):
+    """Append and attention captured as one graph; lengths, positions and rows change between replays."""
+    H, hk, D, page = 8, 2, 128, 16
+    lens, cu = [300, 60, 1], [0, 1, 2, 3]
+    kc, vc, table, _ = paged_setup([n + 40 for n in lens], [1, 1, 1], hk, D, page, torch.bfloat16, 60)
+    kcg, vcg = on_gpu(kc, vc)
+    x = torch.empty(3, H + 2 * hk, D, dtype=torch.bfloat16, device="cuda")
+    tg, lg, cg, inv = ints(table), ints(lens), ints(cu), fa.rope_inv_freq(D)[0]
+    steps = fa.rope_steps(inv)
+
+    def step():
+        q = fa.paged_append(x[:, H:H + hk], x[:, H + hk:], kcg, vcg, tg, lg, cg, 1, q=x[:, :H], steps=steps)
+        return q, *fa.forward_paged(q, kcg, vcg, tg, lg, cg, 1, 340)
+
+    x.copy_(rnd(x.shape, 61, torch.bfloat16))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q, o, lse = step()
+    for i in range(1, 5):
+        now = [n + i for n in lens]
+        lg.copy_(ints(now))
+        x.copy_(rnd(x.shape, 61 + i, torch.bfloat16))
+        g.replay()
+        assert fa.fa_check_device_errors(None) == 0
+        check(o, lse, q.cpu(), kcg.cpu(), vcg.cpu(), table, now, cu)
+        pos = torch.tensor([n - 1 for n in now], dtype=torch.int32, device="cuda")
+        qr, kr = fa.rope(x[:, :H], x[:, H:H + hk], pos, steps)
+        assert torch.equal(q, qr)
+        at = torch.cat([paged.slots(table[b], [now[b] - 1], page) for b in range(3)])
+        assert torch.equal(kcg.view(-1, hk, D)[at.cuda()], kr)
+        assert torch.equal(vcg.view(-1, hk, D)[at.cuda()], x[:, H + hk:])
+
+
 def test_prefill_in_chunks_then_decode_matches_the_packed_forward(fa):
     """The operators together: rotate and append a chunk, attend, chunk after chunk and token by token; every
     step's rows agree with the packed causal forward on the whole rotated sequences."""
