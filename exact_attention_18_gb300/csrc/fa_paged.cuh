@@ -6,6 +6,10 @@
 
 namespace fa {
 
+// Codes of these kernels for the device error word, after DeviceErrorCode's.
+constexpr int kErrBadCache = 6;  // a length below the new tokens', or past what the call allows
+constexpr int kErrBadPage = 7;   // a block table entry in use is not a page
+
 // Longest cache length (and largest window side): positions and their sums
 // with a window side stay inside 32 bits.
 constexpr int kMaxPagedLen = 1 << 29;

@@ -24,8 +24,6 @@ enum DeviceErrorCode : int {
   kErrTimeoutSoftmax = 3,  // softmax warps waited too long for scores / partial O
   kErrTimeoutDrain = 4,    // teardown waited too long for in-flight copies / MMAs
   kErrBadSeqlens = 5,      // packed batch: cu_seqlens inconsistent with max_seqlen / total
-  kErrBadCache = 6,        // paged cache: a length below the new tokens', or past what the call allows
-  kErrBadPage = 7,         // paged cache: a block table entry in use is not a page
 };
 
 namespace ptx {
