@@ -1,7 +1,9 @@
 """Python binding of the exact-attention C-ABI library (fa.h) for GB300.
 
 Argument marshalling only: every step of the attention computation runs in
-the library's CUDA kernels.  PyTorch supplies device memory and streams.
+the library's CUDA kernels.  PyTorch supplies device memory and streams.  The
+wrappers of the rotary and cache calls, made once per layer and token when
+decoding, marshal in a compiled module (``csrc/fa_binding.cpp``).
 
 The raw entry points keep the C names and signatures (pointers as ints):
 ``fa_fwd``, ``fa_fwd_gqa``, ``fa_bwd``, ``fa_bwd_marked``, ``fa_bwd_gqa``,
@@ -30,13 +32,12 @@ implementation.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
-import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libfa_gb300.so")
+BINDING_PATH = os.path.join(os.path.dirname(LIB_PATH), "_fa_binding.so")
 
 __all__ = ["fa_fwd", "fa_fwd_gqa", "fa_bwd", "fa_bwd_marked", "fa_bwd_gqa", "fa_bwd_gqa_marked", "fa_bwd_noalloc",
            "fa_bwd_workspace_size", "fa_bwd_gqa_workspace_size", "fa_fwd_varlen", "fa_bwd_varlen",
@@ -64,6 +65,7 @@ class PagedCache(ctypes.Structure):
 
 
 _lib = None
+_binding = None
 
 
 def _load():
@@ -580,106 +582,31 @@ def rope_steps(inv_freq, device="cuda"):
     return steps.to(device)
 
 
-# The calls below are made once per layer and step, on a few rows when decoding, so their checks read each
-# attribute of a tensor once and compare plain integers.
-def _raw_stream(device: int) -> int:
-    """The current stream's handle (the public call builds a Stream object each time)."""
-    import torch
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(device) if get is not None else torch.cuda.current_stream(device).cuda_stream
+def _load_binding():
+    """The compiled tensor binding (``csrc/fa_binding.cpp``); raises if it has not been built."""
+    global _binding
+    import importlib.util
+    import torch  # noqa: F401  (the binding links against its libraries)
+    _load()
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"the tensor binding {BINDING_PATH} is not built; run "
+                           "`python -m exact_attention_18_gb300.build` first")
+    spec = importlib.util.spec_from_file_location("_fa_binding", BINDING_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    _binding = mod
+    return mod
 
 
-def _call_device(first, *others) -> int:
-    """The one device of all tensors, which must be the current one (kernels launch there)."""
-    import torch
-    d = first.get_device()  # -1: not on a GPU
-    for x in others:
-        if x is not None and x.get_device() != d:
-            raise ValueError("all tensors must be on one CUDA device")
-    if d < 0 or d != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {first.device}, which is not the current CUDA device")
-    return d
+def _result(r, what):
+    """A binding call's outputs; an int among them is a status to raise."""
+    if type(r) is int:
+        _check(r, what)
+    return r
 
 
-def _rows(x, name, shape, dtype):
-    """Token stride of x, which must be [T, heads, D] (``shape``) of ``dtype`` with dense heads."""
-    st = x.stride()
-    if x.dtype != dtype or x.shape != shape or len(st) != 3 or (st[2] != 1 and shape[2] > 1) \
-            or (st[1] != shape[2] and shape[1] > 1):
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} with dense heads (any stride "
-                         "between tokens)")
-    return st[0] if shape[0] > 1 else shape[1] * shape[2]
-
-
-def _int_array(x, name, dtype, shape):
-    if x.dtype != dtype or x.shape != shape or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-    return x.data_ptr()
-
-
-def _allocate(stream, device, *specs):
-    """New tensors of (shape, dtype), which belong to the stream the call runs on."""
-    import torch
-    if stream is None:
-        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
-    with torch.cuda.stream(stream):
-        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
-
-
-# Scratch of forward_paged, one per stream: calls on a stream run one after another, so they can share it, and
-# an allocation per call is a tenth of what a decoding step's call costs on the host.  A call that is being
-# captured gets its own (the graph may run beside this stream's later calls).
-_scratch: dict = {}
-
-
-def _stream_scratch(nbytes: int, device: int, handle: int, stream):
-    """A device buffer of at least nbytes that only calls on this stream use."""
-    import torch
-    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-        capturing = torch.cuda.is_current_stream_capturing()
-    if capturing:
-        return _allocate(stream, device, ((max(nbytes, 256),), torch.uint8))[0]
-    buf = _scratch.get((device, handle))
-    if buf is None or buf.numel() < nbytes:
-        buf = _scratch[device, handle] = _allocate(stream, device, ((max(nbytes, 1 << 20),), torch.uint8))[0]
-    return buf
-
-
-def _three(x, name):
-    if x.dim() != 3:
-        raise ValueError(f"{name} must be a tensor [T, heads, D]")
-    return x.shape
-
-
-def _rotate(what, q, k, positions, steps, interleaved, magnitude, q_out, k_out, stream):
-    import torch
-    d = _call_device(q, k, positions, steps, q_out, k_out)
-    dtype, shape, k_shape = q.dtype, _three(q, "q"), _three(k, "k")
-    T, H, D = shape
-    hk, n = k_shape[1], steps.numel()
-    if k_shape[0] != T or k_shape[2] != D:
-        raise ValueError("k must have q's tokens and head dimension")
-    qs, ks = _rows(q, "q", shape, dtype), _rows(k, "k", k_shape, dtype)
-    pos = _int_array(positions, "positions", torch.int32, (T,))
-    table = _int_array(steps, "steps", torch.int64, (n,))
-    qos, kos = H * D, hk * D  # token strides of outputs made here
-    if q_out is not None:
-        qos = _rows(q_out, "the q output", shape, dtype)
-    if k_out is not None:
-        kos = _rows(k_out, "the k output", k_shape, dtype)
-    if q_out is None and k_out is None:
-        q_out, k_out = _allocate(stream, d, (shape, dtype), (k_shape, dtype))
-    elif q_out is None:
-        q_out, = _allocate(stream, d, (shape, dtype))
-    elif k_out is None:
-        k_out, = _allocate(stream, d, (k_shape, dtype))
-    st = getattr(_load(), what)(q.data_ptr(), qs, k.data_ptr(), ks, q_out.data_ptr(), qos, k_out.data_ptr(), kos, pos,
-                                table, T, H, hk, D, 2 * n, interleaved, magnitude, _dtype_code(q),
-                                _raw_stream(d) if stream is None else stream.cuda_stream)
-    _check(st, what)
-    return q_out, k_out
-
-
+# These calls are made once per layer and step, on a few rows when decoding: their tensor checks, outputs and
+# argument marshalling are compiled (the other wrappers above do the same in Python).
 def rope(q, k, positions, steps, interleaved: bool = False, magnitude: float = 1.0, q_out=None, k_out=None,
          stream=None):
     """Rotate q [T, H, D] and k [T, H_kv, D] by int32 ``positions`` [T]; returns (q_out, k_out).
@@ -688,45 +615,23 @@ def rope(q, k, positions, steps, interleaved: bool = False, magnitude: float = 1
     2 * len(steps) columns turn, the rest pass.  q and k may be slices of one
     projection (any token stride); ``q_out=q, k_out=k`` works in place.
     """
-    return _rotate("fa_rope", q, k, positions, steps, interleaved, magnitude, q_out, k_out, stream)
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            return rope(q, k, positions, steps, interleaved, magnitude, q_out, k_out)
+    return _result((_binding or _load_binding()).rope(False, q, k, positions, steps, interleaved, magnitude, q_out,
+                                                      k_out), "fa_rope")
 
 
 def rope_backward(dq_out, dk_out, positions, steps, interleaved: bool = False, magnitude: float = 1.0, dq=None,
                   dk=None, stream=None):
     """Gradients (dq, dk) of ``rope``'s inputs from those of its outputs; arguments as ``rope``."""
-    return _rotate("fa_rope_bwd", dq_out, dk_out, positions, steps, interleaved, magnitude, dq, dk,
-                   stream)
-
-
-_CACHE_FIELDS = struct.Struct("@10q")  # PagedCache's fields (four pointers, six 64-bit integers)
-
-
-def _paged_cache(k_cache, v_cache, block_table, kv_lens, batch, heads, D, dtype):
-    """The C structure's bytes for a cache of [pages, page_size, H_kv, D] tensors (any order of strides, D dense)."""
-    import torch
-    shape, st = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 or shape[2] != heads or shape[3] != D or v_cache.shape != shape or v_cache.stride() != st \
-            or (st[3] != 1 and D > 1) or k_cache.dtype != dtype or v_cache.dtype != dtype:
-        raise ValueError(f"k_cache and v_cache must be {dtype} tensors [pages, page_size, {heads}, {D}] of the same "
-                         "strides, with the last dimension dense")
-    t_shape, t_st = block_table.shape, block_table.stride()
-    if block_table.dtype != torch.int32 or len(t_shape) != 2 or t_shape[0] != batch \
-            or (t_st[1] != 1 and t_shape[1] > 1) or (batch > 1 and t_st[0] < t_shape[1]):
-        raise ValueError("block_table must be an int32 tensor [batch, pages per sequence] with dense rows")
-    # The stride of a dimension of one entry is never used; it may be any number in torch.
-    return _CACHE_FIELDS.pack(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                              _int_array(kv_lens, "kv_lens", torch.int32, (batch,)),
-                              t_st[0] if batch > 1 else t_shape[1], shape[0], shape[1],
-                              st[0] if shape[0] > 1 else D, st[1] if shape[1] > 1 else D, st[2] if heads > 1 else D)
-
-
-def _offsets(cu_seqlens):
-    """Sequences of cu_seqlens, an int32 [batch + 1] tensor."""
-    import torch
-    n = cu_seqlens.numel()
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or n < 1 or not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor [batch + 1]")
-    return n - 1
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            return rope_backward(dq_out, dk_out, positions, steps, interleaved, magnitude, dq, dk)
+    return _result((_binding or _load_binding()).rope(True, dq_out, dk_out, positions, steps, interleaved, magnitude,
+                                                      dq, dk), "fa_rope_bwd")
 
 
 def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen: int, q=None, positions=None,
@@ -739,33 +644,14 @@ def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_s
     ``max_seqlen`` are the new tokens'.  A token's position is its key index
     unless ``positions`` gives it; without ``steps`` nothing is rotated.
     """
-    import torch
-    d = _call_device(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, q, q_out, positions, steps)
-    dtype, shape = k.dtype, _three(k, "k")
-    T, hk, D = shape
-    batch = _offsets(cu_seqlens)
-    cache = _paged_cache(k_cache, v_cache, block_table, kv_lens, batch, hk, D, dtype)
-    H = 0
-    q_args = (None, 0, None, 0)
-    if q is not None:
-        q_shape = _three(q, "q")
-        H = q_shape[1]
-        if q_shape[0] != T or q_shape[2] != D:
-            raise ValueError("q must have k's tokens and head dimension")
-        qs, qos = _rows(q, "q", q_shape, dtype), H * D
-        if q_out is None:
-            q_out, = _allocate(stream, d, (q_shape, dtype))
-        else:
-            qos = _rows(q_out, "q_out", q_shape, dtype)
-        q_args = (q.data_ptr(), qs, q_out.data_ptr(), qos)
-    n = 0 if steps is None else steps.numel()
-    _check(_load().fa_paged_append(*q_args, k.data_ptr(), _rows(k, "k", shape, dtype), v.data_ptr(),
-                           _rows(v, "v", shape, dtype), cache, cu_seqlens.data_ptr(),
-                           None if positions is None else _int_array(positions, "positions", torch.int32, (T,)),
-                           None if steps is None else _int_array(steps, "steps", torch.int64, (n,)), batch,
-                           int(max_seqlen), T, H, hk, D, 2 * n, interleaved, magnitude, _dtype_code(k),
-                           _raw_stream(d) if stream is None else stream.cuda_stream), "fa_paged_append")
-    return q_out if q is not None else None
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            return paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen, q, positions,
+                                steps, interleaved, magnitude, q_out)
+    return _result((_binding or _load_binding()).paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens,
+                                                              max_seqlen, q, positions, steps, interleaved, magnitude,
+                                                              q_out), "fa_paged_append")
 
 
 def forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q: int, max_seqlen_k: int,
@@ -779,37 +665,12 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seq
     reported by ``fa_check_device_errors``.  Without ``workspace`` the call uses
     scratch kept for its stream (its own while a graph is captured).
     """
-    import torch
-    d = _call_device(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, lse, workspace)
-    dtype, shape = q.dtype, _three(q, "q")
-    T, H, D = shape
-    hk = k_cache.shape[2] if k_cache.dim() == 4 else 0
-    if not q.is_contiguous() or hk < 1 or H % hk != 0:
-        raise ValueError("q must be contiguous, and its heads a multiple of the cache's")
-    batch = _offsets(cu_seqlens)
-    cache = _paged_cache(k_cache, v_cache, block_table, kv_lens, batch, hk, D, dtype)
-    max_seqlen_q, max_seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            return forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q, max_seqlen_k,
+                                 causal, window, scale, out, lse, workspace)
     left, right = (-1, -1) if window is None else window
-    handle = _raw_stream(d) if stream is None else stream.cuda_stream
-    if out is None and lse is None:
-        out, lse = _allocate(stream, d, (shape, dtype), ((H, T), torch.float32))
-    else:
-        if out is None:
-            out, = _allocate(stream, d, (shape, dtype))
-        if lse is None:
-            lse, = _allocate(stream, d, ((H, T), torch.float32))
-        if out.shape != shape or out.dtype != dtype or not out.is_contiguous():
-            raise ValueError("out must be like q")
-        if lse.shape != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
-            raise ValueError("lse must be contiguous fp32 [H, T]")
-    if workspace is None:
-        have = _load().fa_fwd_paged_workspace_size(batch, max_seqlen_q, max_seqlen_k, H, hk, D)
-        workspace = _stream_scratch(have, d, handle, stream)
-    else:
-        have = workspace.numel() * workspace.element_size()
-    _check(_load().fa_fwd_paged(q.data_ptr(), out.data_ptr(), lse.data_ptr(), cache, cu_seqlens.data_ptr(), batch,
-                        max_seqlen_q, max_seqlen_k, T, H, hk, D, causal, left, right, scale, _dtype_code(q),
-                        workspace.data_ptr(), have, handle), "fa_fwd_paged")
-    return out, lse
+    return _result((_binding or _load_binding()).forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens,
+                                                               max_seqlen_q, max_seqlen_k, causal, left, right, scale,
+                                                               out, lse, workspace), "fa_fwd_paged")

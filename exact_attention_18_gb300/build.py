@@ -3,14 +3,18 @@
 The shared object lands in ``exact_attention_18_gb300/_lib/libfa_gb300.so``
 (object files in ``_build/``); both are git-ignored.  Translation units are
 compiled in parallel with one ``-gencode`` target, then linked with nvcc.
+``_lib/_fa_binding.so``, the tensor binding of the serving calls, is host C++
+against PyTorch's and Python's headers, linked to the library.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfa_gb300.so")
+BINDING_SRC = os.path.join(CSRC, "fa_binding.cpp")
+BINDING_PATH = os.path.join(LIB_DIR, "_fa_binding.so")
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd4.cu", "fa_fwd4p.cu", "fa_bwd.cu", "fa_merge.cu", "fa_rope.cu",
            "fa_paged_d16.cu", "fa_paged_d32.cu", "fa_paged_d64.cu", "fa_paged_d128.cu",
@@ -36,7 +42,7 @@ def nvcc() -> str:
 
 
 def _deps():
-    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "fa.h")]
+    return [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != os.path.basename(BINDING_SRC)] + [os.path.join(INCLUDE, "fa.h")]
 
 
 def _stale(target: str, deps) -> bool:
@@ -57,15 +63,54 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_binding(verbose: bool) -> str:
+    """The tensor binding's object file.  Finds PyTorch's headers without importing it."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD_DIR, "fa_binding.o")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-I" + INCLUDE,
+           "-I" + os.path.join(torch_dir, "include"),
+           "-I" + os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I" + cuda_inc, "-c", BINDING_SRC, "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on fa_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str, verbose: bool) -> None:
+    torch_lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+    tmp = BINDING_PATH + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-shared", obj, "-o", tmp, "-L" + LIB_DIR, "-lfa_gb300",
+           "-Wl,-rpath,$ORIGIN", "-L" + torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the tensor binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Build (if stale) and return the path of the shared library."""
-    deps = _deps()
-    if not force and not _stale(LIB_PATH, deps):
-        return LIB_PATH
+    """Build (if stale) the library and its tensor binding; returns the library's path."""
+    lib_stale = force or _stale(LIB_PATH, _deps())
+    binding_stale = force or _stale(BINDING_PATH, [BINDING_SRC, os.path.join(INCLUDE, "fa.h")])
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding, verbose) if binding_stale else None
+        objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES)) if lib_stale else None
+        binding_obj = binding.result() if binding else None
+    if lib_stale:
+        _link_library(objs, verbose)
+    if binding_stale:
+        _link_binding(binding_obj, verbose)
+    return LIB_PATH
+
+
+def _link_library(objs, verbose: bool) -> None:
     tmp = LIB_PATH + ".tmp"
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
     if verbose:
@@ -74,7 +119,6 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":
