@@ -136,14 +136,17 @@ __global__ void __launch_bounds__(kRopeMaxThreads) fa_rope_kernel(const RopePara
     ob = oa + 8;
   }
 
-  for (int base = static_cast<int>(threadIdx.x) >> p.log2_items, round = 0; round == 0 || base - (static_cast<int>(threadIdx.x) >> p.log2_items) < n_rows;
-       base += kRopeRows * lanes, ++round) {
+  for (int first = 0; first < n_rows; first += kRopeRows * lanes) {  // (one round, but for very many heads)
+    const int base = first + (static_cast<int>(threadIdx.x) >> p.log2_items);
     Vec8 x[kRopeRows], y[kRopeRows];
+    int tok[kRopeRows], head[kRopeRows];  // of each row
 #pragma unroll
     for (int u = 0; u < kRopeRows; ++u) {
       const int row = base + u * lanes;
       if (row < n_rows) {
         const int t = row / heads, h = row - t * heads;
+        tok[u] = t;
+        head[u] = h;
         const int64_t tk = tok0 + t;
         const uint16_t* src;
         if (h < p.H) src = static_cast<const uint16_t*>(p.q) + tk * p.q_stride + h * D;
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(kRopeMaxThreads) fa_rope_kernel(const RopePara
         y[u].v = *reinterpret_cast<const uint4*>(src + (v_row ? 16 * col + 8 : ob));
       }
     }
-    if (round == 0) {
+    if (first == 0) {
       // Angles of the CTA's tokens, and (append) where their rows go.
       for (int i = threadIdx.x; i < n_tok * r; i += threads) {
         const int t = i / r, j = i - t * r;
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kRopeMaxThreads) fa_rope_kernel(const RopePara
     for (int u = 0; u < kRopeRows; ++u) {
       const int row = base + u * lanes;
       if (row >= n_rows) continue;
-      const int t = row / heads, h = row - t * heads;
+      const int t = tok[u], h = head[u];
       const int64_t tk = tok0 + t;
       uint16_t* dst;
       const bool v_row = APPEND && h >= rot_heads;
