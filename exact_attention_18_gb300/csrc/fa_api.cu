@@ -568,17 +568,13 @@ struct PagedPart {
   bool used = false;
   int N;               // fa_paged_kernel: rows it is instantiated for
   int tok_tile, tiles, grid, part_rows;
-  int64_t rows_lo, rows_hi;
+  int tok_lo, tok_hi, small;
   size_t o_at, lse_at, desc_at;  // byte offsets in the workspace
 };
 struct PagedPlan {
   PagedPart few, tile;
   size_t bytes;
 };
-
-// Query rows (new tokens x group) of a sequence up to which the keys-on-rows
-// kernel takes it: one of its units.
-constexpr int64_t kFewRows = 128;
 
 // The tiling of a call; false when it is empty or has too many units.
 bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t H_kv, int64_t D, PagedPlan* plan) {
@@ -600,26 +596,27 @@ bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t 
     if (units > (int64_t(1) << 37) / (blocks * H_kv)) return false;  // a CTA's run of blocks fits 31 bits
     const int64_t most = units * H_kv * blocks;
     part->grid = static_cast<int>(most < ctas ? most : ctas);
+    part->small = most < (int64_t(1) << 31) / 304;  // (share x CTA stays below 2^31 too)
     part->o_at = plan->bytes;
     part->lse_at = part->o_at + round256(static_cast<size_t>(2) * part->grid * part->part_rows * D * sizeof(float));
     part->desc_at = part->lse_at + round256(static_cast<size_t>(2) * part->grid * part->part_rows * sizeof(float));
     plan->bytes = part->desc_at + round256(static_cast<size_t>(part->grid) * sizeof(int4));
     return true;
   };
-  const bool chunks = max_q * G > kFewRows;
+  const bool chunks = max_q * G > fa::kFewRows;
   // Sequences of few rows: all of them, or those of a mixed batch.
-  if (!chunks || batch > 1) {
-    const int64_t longest = chunks ? kFewRows / G : max_q;
+  if (!chunks || (batch > 1 && G <= fa::kFewRows)) {
+    const int64_t longest = chunks ? fa::kFewRows / G : max_q;
     plan->few.N = fa::paged_rows(longest * G);
-    plan->few.rows_lo = 0;
-    plan->few.rows_hi = chunks ? longest * G : max_q * G;
+    plan->few.tok_lo = 0;
+    plan->few.tok_hi = static_cast<int>(longest);
     const int64_t ctas = fa::kPagedSms * fa::paged_ctas(static_cast<int>(D), plan->few.N);
     if (!add(&plan->few, longest, longest, 128, plan->few.N, ctas)) return false;
   }
   if (chunks) {
     const int Di = static_cast<int>(D);
-    plan->tile.rows_lo = plan->few.used ? plan->few.rows_hi + 1 : 0;
-    plan->tile.rows_hi = max_q * G;
+    plan->tile.tok_lo = plan->few.used ? plan->few.tok_hi + 1 : 0;
+    plan->tile.tok_hi = static_cast<int>(max_q);
     const int64_t tok = fa::paged_tile_tiles(Di) * (128 / G);
     if (!add(&plan->tile, tok, max_q, fa::paged_tile_block(Di), tok * G, fa::kPagedSms)) return false;
   }
@@ -1063,8 +1060,9 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
   auto run = [&](const PagedPart& part, bool tile) -> fa_status {
     p.tok_tile = part.tok_tile;
     p.tiles = part.tiles;
-    p.rows_lo = part.rows_lo;
-    p.rows_hi = part.rows_hi;
+    p.tok_lo = part.tok_lo;
+    p.tok_hi = part.tok_hi;
+    p.small = part.small;
     p.part_rows = part.part_rows;
     p.after_tile = !tile && plan.tile.used;
     p.o_part = reinterpret_cast<float*>(ws + part.o_at);

@@ -89,7 +89,8 @@ struct PagedParams {
   int tiles;             // tiles of the longest sequence: ceil(max_q / tok_tile)
   int win_left, win_right;  // key j visible to position i iff i - win_left <= j <= i + win_right (and j < kv_len)
   int page_shift, num_pages;
-  int64_t rows_lo, rows_hi;  // sequences of rows_lo .. rows_hi query rows (new tokens x G) are this kernel's
+  int tok_lo, tok_hi;    // sequences of tok_lo .. tok_hi new tokens are this kernel's
+  int small;             // all blocks of the call are below 2^31 / 304
   int min_share;         // fewest blocks a CTA takes
   int after_tile;        // few-row kernel: launched behind the tile kernel of the same call
   float scale_log2;
@@ -118,9 +119,14 @@ struct PagedMergeParams {
   int G, H, total;
 };
 
-// Rows of a unit the kernel is instantiated for; the smallest that holds
-// `rows`, else the largest.
-inline int paged_rows(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
+// Query rows (new tokens x G) of a sequence up to which the few-row kernel takes
+// it, and rows of a unit it is instantiated for: the smallest that holds `rows`.
+// Both kernels measured (us; 16 sequences of 8192 keys, G = 8): 80 rows, D = 64
+// few-row kernel (instantiated for 128) 58.7, tile kernel 55.9; D = 128 86.5 /
+// 67.9; 128 rows 56.7 / 56.8 and 68.5 / 70.9; 160 rows and more the tile kernel
+// by far (92.2 / 59.7, 111 / 73.5).  Below, a tile of 128 rows is mostly empty.
+constexpr int kFewRows = 64;
+inline int paged_rows(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
 constexpr int kPagedSms = 152;
 // CTAs per SM of the few-row kernel.
 constexpr int paged_ctas(int D, int N) { return D <= 64 && N == 16 ? 2 : 1; }

@@ -1,5 +1,5 @@
-// Attention of new tokens over a paged key/value cache: a few rows per K/V
-// head (decoding, drafted tokens) up to whole chunks of a prompt.
+// Attention of new tokens over a paged key/value cache: few query rows per K/V
+// head (decoding, drafted tokens).
 //
 //   O_i = sum_j softmax_j(scale q_i . k_j) v_j,   L_i = ln sum_j exp(scale q_i . k_j)
 //
@@ -8,7 +8,7 @@
 // Keys are the matrix rows.  With few query rows a product that puts queries
 // on the tensor core's 128 rows would leave most of them empty, so both
 // products are taken transposed: S^T = K Q^T (128 keys x N rows) and
-// O^T += V^T P^T (D x N), N = 16 .. 128 query rows of one K/V head (tokens x
+// O^T += V^T P^T (D x N), N = 16, 32 or 64 query rows of one K/V head (tokens x
 // the group's heads).  K and V come from shared memory exactly as TMA wrote
 // them: K K-major, V MN-major.  A TMEM lane is a key, so a softmax thread
 // holds one key's scores for all N rows: running sums stay per thread until
@@ -61,14 +61,12 @@ struct PagedLayout {
   using GQ = TileGeom<D, N>;       // Q tile, N rows
   using GP = TileGeom<N, kPBlk>;   // P^T tile: 128 keys x N rows
   // Softmax warpgroups, each over kCols rows.  More of them hide more of each
-  // other's latency, down to 16 rows a thread; N = 128 has the registers for two
-  // only.  Measured, 16 sequences of 8192 keys at D = 64: N = 64 with 64 / 32 /
-  // 16 rows a thread 45 / 38.7 / 36.4 us, N = 128 with 32 / 64 68.4 / 57.1 us
-  // (32 spills).
-  static constexpr int kCols = N == 128 ? 64 : 16;
+  // other's latency: 16 sequences of 8192 keys at D = 64, N = 64 with 32 / 16
+  // rows a thread 38.7 / 36.4 us; drafted tokens in a window, N = 64, kernel
+  // alone, with 64 / 32 29 / 16 us.
+  static constexpr int kCols = 16;
   static constexpr int kWgs = N / kCols;
   static constexpr int kThreads = 128 * kWgs + 96;  // and the producers of K and V, the MMA issuer
-  static constexpr int kQBufs = N > 64 ? 1 : 2;
   static constexpr int kQBytes = (GQ::kTileBytes + 1023) / 1024 * 1024;
   static constexpr int kSmallBytes = 5 * 1024;      // barriers and per-row arrays
   // CTAs per SM (paged_ctas).  A block's chain of waits, loads and exponentials
@@ -76,11 +74,8 @@ struct PagedLayout {
   // behind the block's 2800 cycles of memory, below it a second CTA fills it.
   static constexpr int kCtas = paged_ctas(D, N);
   static constexpr int kBudget = (kCtas == 2 ? 113 : 227) * 1024 - 1024;
-  // P tiles: two, so that a block's P is written while the tensor core reads the
-  // one before; one where two would leave the ring three stages.
-  static constexpr int kPBufs = N == 128 && D == 128 ? 1 : 2;
   static constexpr int kUnitsFit =
-      (kBudget - kPBufs * GP::kTileBytes - kQBufs * kQBytes - kSmallBytes) / GK::kTileBytes;
+      (kBudget - 2 * GP::kTileBytes - 2 * kQBytes - kSmallBytes) / GK::kTileBytes;
   // Ring stages, one K or V tile each.  An even number: K tiles have the even
   // stages, V tiles the odd ones, and each producer sees every phase of its
   // stages' barriers.  (On a stage that both used, a producer could take a
@@ -88,8 +83,8 @@ struct PagedLayout {
   static constexpr int kUnits = (kUnitsFit > 16 ? 16 : kUnitsFit) & ~1;
   static_assert(kUnits >= 4, "ring");
   static constexpr int kOffP = kUnits * GK::kTileBytes;
-  static constexpr int kOffQ = kOffP + kPBufs * GP::kTileBytes;
-  static constexpr int kOffSmall = kOffQ + kQBufs * kQBytes;
+  static constexpr int kOffQ = kOffP + 2 * GP::kTileBytes;
+  static constexpr int kOffSmall = kOffQ + 2 * kQBytes;
   // full[U], empty[U], qfull[2], qempty[2], sfull[2], pfull[2], pv[2], vtmp, drain
   static constexpr int kNumBars = 2 * kUnits + 10 + 2;
   static_assert(kNumBars * 8 + 24 + sizeof(RunStart) + 8 * N * 4 + 2 * N <= kSmallBytes, "small arrays");
@@ -99,31 +94,24 @@ struct PagedLayout {
   static constexpr int kSmemUsed = kOffSmall + kSmallBytes + 1024;
   static constexpr int kSmemLeast = (kCtas == 2 ? 112 : 116) * 1024;
   static constexpr int kSmemBytes = kSmemUsed > kSmemLeast ? kSmemUsed : kSmemLeast;
-  static constexpr uint32_t kTmemCols = 3 * N <= 64 ? 64 : (3 * N <= 128 ? 128 : (3 * N <= 256 ? 256 : 512));
+  static constexpr uint32_t kTmemCols = 4 * N;  // S twice, O, and up to a power of two
   // V^T is D rows; the MMA's 128 rows past D repeat tile rows 8 further on
   // (in bounds: the ring is followed by the P tiles) into TMEM lanes nobody reads.
   static constexpr uint32_t kVLbo = D == 128 ? GK::kChunkBytes : 8 * GK::kRowBytes;
 };
 
-// Sum or maximum over the warp's 32 lanes of each of NC values a lane holds
-// (NC = 16 or 32): lane l receives that of column l % NC.  Halving exchange:
-// each step keeps the half of the columns the lane's bit selects.
-template <int NC, bool MAX>
-__device__ __forceinline__ float warp_reduce_cols(const float* x) {
+// Sum or maximum over the warp's 32 lanes of each of 16 values a lane holds:
+// lane l receives that of column l % 16.  Halving exchange: each step keeps the
+// half of the columns the lane's bit selects.
+template <bool MAX>
+__device__ __forceinline__ float warp_reduce_cols16(const float* x) {
   const int lane = threadIdx.x & 31;
   auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
-  float v[NC / 2];
-  constexpr int kTop = NC / 2;
-  {
-    const bool up = lane & kTop;
+  float v[16];
 #pragma unroll
-    for (int i = 0; i < kTop; ++i) {
-      const float keep = up ? x[i + kTop] : x[i], give = up ? x[i] : x[i + kTop];
-      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, kTop));
-    }
-  }
+  for (int i = 0; i < 16; ++i) v[i] = x[i];
 #pragma unroll
-  for (int h = kTop / 2; h >= 1; h /= 2) {
+  for (int h = 8; h >= 1; h /= 2) {
     const bool up = lane & h;
 #pragma unroll
     for (int i = 0; i < h; ++i) {
@@ -131,8 +119,7 @@ __device__ __forceinline__ float warp_reduce_cols(const float* x) {
       v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, h));
     }
   }
-  if (NC == 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
-  return v[0];
+  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
 // Byte offset of 16-byte chunk c of row k in a swizzled tile with rows of ROW_BYTES.
@@ -141,13 +128,6 @@ __device__ __forceinline__ uint32_t swizzled(int k, int c) {
   constexpr int kShift = ROW_BYTES == 128 ? 0 : (ROW_BYTES == 64 ? 1 : 2);
   constexpr int kMask = ROW_BYTES / 16 - 1;
   return static_cast<uint32_t>(k * ROW_BYTES + ((c ^ ((k >> kShift) & kMask)) << 4));
-}
-
-template <int NC>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
-  if constexpr (NC == 16) tmem_ld16(taddr, r);
-  else if constexpr (NC == 32) tmem_ld32(taddr, r);
-  else tmem_ld64(taddr, r);
 }
 
 }  // namespace
@@ -192,25 +172,17 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
 
   const int warp = warp_index();
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < U; ++s) {
-      mbar_init(&bar_full[s], 1);
-      mbar_init(&bar_empty[s], 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar_qfull[s], 1);
-      mbar_init(&bar_qempty[s], 1);
-      mbar_init(&bar_sfull[s], 1);
-      mbar_init(&bar_pfull[s], kSoftWarps);
-      mbar_init(&bar_pv[s], 1);
-    }
-    mbar_init(bar_vtmp, 1);
-    mbar_init(bar_drain, 1);
-    *abort_flag = 0;
-    s_start->run = 0;
-    s_start->u.n_blk = 0;
-    s_start->blk = 0;
+  if (warp == 0) {
+    // Barriers lie in a row; only pfull counts more than one arrival.
+    for (int i = lane; i < L::kNumBars; i += 32)
+      mbar_init(bar_full + i, bar_full + i == bar_pfull || bar_full + i == bar_pfull + 1 ? kSoftWarps : 1);
     fence_mbar_init();
+    if (lane == 0) {
+      *abort_flag = 0;
+      s_start->run = 0;
+      s_start->u.n_blk = 0;
+      s_start->blk = 0;
+    }
   }
   if (warp == kMma) {
     tmem_alloc(tmem_slot, L::kTmemCols);
@@ -271,8 +243,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     for (int n; ok && (n = w.seg_len()) > 0; w.next(p), ++seg) {
       int page = box_page(w.blk);
       if (kv == 0) {
-        const int qb = L::kQBufs == 2 ? (seg & 1) : 0;
-        const int qu = L::kQBufs == 2 ? (seg >> 1) : seg;
+        const int qb = seg & 1, qu = seg >> 1;
         if (qu > 0) ok = warp_wait(&bar_qempty[qb], (qu - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
         if (!ok) break;
         if (lane == 0) {
@@ -327,8 +298,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     for (int x = c - 2; x >= 0 && x >= c - U; x -= 2)
       drain_wait(&bar_full[x % U], (x / U) & 1, p.err);
     if (kv == 0)
-      for (int x = (seg > L::kQBufs ? seg - L::kQBufs : 0); x < seg; ++x)
-        drain_wait(&bar_qfull[x % L::kQBufs], (x / L::kQBufs) & 1, p.err);
+      for (int x = (seg > 2 ? seg - 2 : 0); x < seg; ++x) drain_wait(&bar_qfull[x & 1], (x >> 1) & 1, p.err);
     __syncwarp();
   } else if (warp == kMma) {
     // -------------------------------------------------------------- MMA issuer
@@ -342,8 +312,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     const int run = w.left;
     // S(i): the walk's current block.
     auto scores = [&](int i) -> bool {
-      const int qb = L::kQBufs == 2 ? (seg & 1) : 0;
-      const int qu = L::kQBufs == 2 ? (seg >> 1) : seg;
+      const int qb = seg & 1, qu = seg >> 1;
       if (j == 0 && !warp_wait(&bar_qfull[qb], qu & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma)) return false;
       const int c = 2 * i, st = c % U;
       if (!warp_wait(&bar_full[st], (c / U) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma)) return false;
@@ -377,7 +346,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
       tc_fence_after();
       const uint64_t v_desc = make_sdesc(s_ring + st * GK::kTileBytes, L::kVLbo, 8 * GK::kRowBytes, GK::kSwz);
       const uint64_t p_desc =
-          make_sdesc(s_p + (i & 1) * (L::kPBufs - 1) * GP::kTileBytes, GP::kChunkBytes, 8 * GP::kRowBytes, GP::kSwz);
+          make_sdesc(s_p + (i & 1) * GP::kTileBytes, GP::kChunkBytes, 8 * GP::kRowBytes, GP::kSwz);
 #pragma unroll
       for (int kk = 0; kk < kPBlk / 16; ++kk)
         mma_ss_warp(t_o, desc_plus(v_desc, mnmajor_step_bytes<D>(kk)), desc_plus(p_desc, mnmajor_step_bytes<N>(kk)),
@@ -407,9 +376,8 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     const float c = p.scale_log2;
     const float2 c2 = make_float2(c, c);
     // This warpgroup's columns of the P^T tile.
-    constexpr int kChunkCols = GP::kRowBytes / 2;
-    uint8_t* p_tile = smem + L::kOffP + (g * NC / kChunkCols) * GP::kChunkBytes;
-    const int p_chunk = (g * NC % kChunkCols) / 8;  // first 16-byte chunk of this warpgroup's rows
+    uint8_t* p_tile = smem + L::kOffP;
+    const int p_chunk = g * NC / 8;  // first 16-byte chunk of this warpgroup's rows
     int i = 0;  // block within the CTA's run
     bool alive = true;
     float l[NC];
@@ -429,19 +397,16 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
         bool ok = warp_wait(&bar_sfull[i & 1], (i >> 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
         // O(i-2) is done (S(i) was issued after it).  Waiting for it keeps this
         // warp one phase behind each of the two barriers, so that a wait for
-        // O(i-1) below cannot take the phase before it for it.  With one P tile,
-        // O(i-1) must be done before P(i) is written.
-        const int behind = L::kPBufs;
-        if (ok && i >= behind)
-          ok = warp_wait(&bar_pv[(i - behind) & 1], ((i - behind) >> 1) & 1, abort_flag, p.err, p.wait_ns,
-                         kErrTimeoutSoftmax);
+        // O(i-1) below cannot take the phase before it for it.
+        if (ok && i >= 2)
+          ok = warp_wait(&bar_pv[i & 1], ((i >> 1) - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
         const int key0 = (blk_first + jb) * kPBlk;
         const int key = key0 + key_lane;
         const bool cut = key0 < full_lo || key0 + kPBlk > full_hi;
         uint32_t sr[NC];
         if (ok) {
           tc_fence_after();
-          tmem_ld_cols<NC>(t_s + (i & 1) * N, sr);
+          tmem_ld16(t_s + (i & 1) * N, sr);
         }
         float2 cc = c2;
         if (cut && ok) {
@@ -472,15 +437,11 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
             alive = false;
             break;
           }
-          constexpr int kRed = NC < 32 ? NC : 32;
+          float y[NC];
 #pragma unroll
-          for (int k0 = 0; k0 < NC; k0 += kRed) {
-            float y[kRed];
-#pragma unroll
-            for (int k = 0; k < kRed; ++k) y[k] = cc.x * __uint_as_float(sr[k0 + k]);
-            const float mk = warp_reduce_cols<kRed, true>(y);
-            if (lane < kRed) red_s[(k0 + lane) * 4 + q4] = mk;
-          }
+          for (int k = 0; k < NC; ++k) y[k] = cc.x * __uint_as_float(sr[k]);
+          const float mk = warp_reduce_cols16<true>(y);
+          if (lane < NC) red_s[lane * 4 + q4] = mk;
           named_sync(bar_id, 128);
           bool moved = false;
           if (wt < NC) {
@@ -508,24 +469,21 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
               break;
             }
             tc_fence_after();
+            uint32_t o16[NC];
+            tmem_ld16(t_o, o16);
 #pragma unroll
-            for (int k = 0; k < NC; k += 16) {
-              uint32_t o16[16];
-              tmem_ld16(t_o + k, o16);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float a = alpha_s[k + e];  // 0: the row saw no key before
-                o16[e] = a == 0.f ? 0u : __float_as_uint(__uint_as_float(o16[e]) * a);
-              }
-              tmem_st16(t_o + k, o16);
+            for (int e = 0; e < NC; ++e) {
+              const float a = alpha_s[e];  // 0: the row saw no key before
+              o16[e] = a == 0.f ? 0u : __float_as_uint(__uint_as_float(o16[e]) * a);
             }
+            tmem_st16(t_o, o16);
             tmem_st_wait();
           }
         }
         exact_max = cut;
         // P~ = 2^(c s - m), 16-bit, into the key's row of the P^T tile; the
         // running sums take the unrounded values.
-        uint8_t* prow = p_tile + (i & 1) * (L::kPBufs - 1) * GP::kTileBytes;
+        uint8_t* prow = p_tile + (i & 1) * GP::kTileBytes;
 #pragma unroll
         for (int k = 0; k < NC; k += 8) {
           uint32_t pk[4];
@@ -551,12 +509,8 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
       const int slot = 2 * static_cast<int>(blockIdx.x) + (w.blk == 0 ? 1 : 0);
       bool ok =
           warp_wait(&bar_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
-      constexpr int kRed = NC < 32 ? NC : 32;
-#pragma unroll
-      for (int k0 = 0; k0 < NC; k0 += kRed) {
-        const float lk = warp_reduce_cols<kRed, false>(l + k0);
-        if (lane < kRed) red_s[(k0 + lane) * 4 + q4] = lk;
-      }
+      const float lk = warp_reduce_cols16<false>(l);
+      if (lane < NC) red_s[lane * 4 + q4] = lk;
       if (!named_sync_and(bar_id, 128, ok)) {
         alive = false;
         break;
@@ -585,30 +539,27 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
       const int rows_here = n_rows - g * NC;
       float* part = p.o_part + (static_cast<int64_t>(slot) * N + g * NC) * D + key_lane;
       elem_t* out = static_cast<elem_t*>(p.o) + (static_cast<int64_t>(u.tok0) * p.H + w.kvh * p.G) * D + key_lane;
+      if (rows_here > 0) {  // (warp-uniform)
+        uint32_t o16[NC];
+        tmem_ld16(t_o, o16);
+        if (key_lane < D) {
+          if (whole) {
 #pragma unroll
-      for (int k0 = 0; k0 < NC; k0 += 16) {
-        if (k0 < rows_here) {  // (warp-uniform)
-          uint32_t o16[16];
-          tmem_ld16(t_o + k0, o16);
-          if (key_lane < D) {
-            if (whole) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float inv = alpha_s[k0 + e];
-                const float v = inv == 0.f ? 0.f : __uint_as_float(o16[e]) * inv;
-                if (k0 + e < rows_here) {
-                  elem_t* dst = out + static_cast<int64_t>(off_s[k0 + e]) * D;
-                  if constexpr (BF16) *dst = __float2bfloat16_rn(v);
-                  else *dst = __float2half_rn(v);
-                }
+            for (int e = 0; e < NC; ++e) {
+              const float inv = alpha_s[e];
+              const float v = inv == 0.f ? 0.f : __uint_as_float(o16[e]) * inv;
+              if (e < rows_here) {
+                elem_t* dst = out + static_cast<int64_t>(off_s[e]) * D;
+                if constexpr (BF16) *dst = __float2bfloat16_rn(v);
+                else *dst = __float2half_rn(v);
               }
-            } else {
+            }
+          } else {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float inv = alpha_s[k0 + e];
-                const float v = inv == 0.f ? 0.f : __uint_as_float(o16[e]) * inv;
-                if (k0 + e < rows_here) part[(k0 + e) * D] = v;
-              }
+            for (int e = 0; e < NC; ++e) {
+              const float inv = alpha_s[e];
+              const float v = inv == 0.f ? 0.f : __uint_as_float(o16[e]) * inv;
+              if (e < rows_here) part[e * D] = v;
             }
           }
         }
@@ -650,8 +601,6 @@ cudaError_t launch_paged_n(int N, bool bf16, const CUtensorMap& tq, const CUtens
                          : launch_paged_t<D, 32, false>(tq, tk, tv, p, grid, s);
     case 64: return bf16 ? launch_paged_t<D, 64, true>(tq, tk, tv, p, grid, s)
                          : launch_paged_t<D, 64, false>(tq, tk, tv, p, grid, s);
-    case 128: return bf16 ? launch_paged_t<D, 128, true>(tq, tk, tv, p, grid, s)
-                          : launch_paged_t<D, 128, false>(tq, tk, tv, p, grid, s);
     default: return cudaErrorInvalidValue;
   }
 }

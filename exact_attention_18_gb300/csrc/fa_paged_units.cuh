@@ -46,8 +46,7 @@ __device__ __forceinline__ Unit paged_unit(const PagedParams& p, const SeqLens& 
     return u;
   }
   const int n = e - a;
-  const long long rows = static_cast<long long>(n) * p.G;
-  if (rows < p.rows_lo || rows > p.rows_hi) return u;  // another kernel of the call takes this sequence
+  if (n < p.tok_lo || n > p.tok_hi) return u;  // another kernel of the call takes this sequence
   u.end_tile = (n + p.tok_tile - 1) / p.tok_tile;
   const int t0 = tile * p.tok_tile;
   if (t0 >= n) return u;
@@ -128,56 +127,56 @@ __device__ __forceinline__ int paged_first_unit(const PagedParams& p, int thread
   return min(X, static_cast<int>(threadIdx.x) * *per);
 }
 
-template <int SHIFT, int THREADS>
-__device__ __forceinline__ void paged_find_run(const PagedParams& p, const SeqLens& own, long long* s_warp,
-                                               RunStart* start) {
+// I: int where the host has bounded all blocks of the call below 2^31 (64-bit
+// scans and divisions cost a decoding call a microsecond), else long long.
+template <int SHIFT, int THREADS, typename I>
+__device__ __forceinline__ void paged_find_run_t(const PagedParams& p, const SeqLens& own, I* s_warp, RunStart* start) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int per;
   const int x0 = paged_first_unit(p, THREADS, &per), x1 = min(p.batch * p.tiles, x0 + per);
   int b = p.tiles == 1 ? x0 : x0 / p.tiles, tile = x0 - b * p.tiles;
   Unit u0;
   u0.n_blk = 0;
-  long long mine = 0;
-  for (int x = x0; x < x1; ++x) {
-    const Unit u = paged_unit<SHIFT>(p, x == x0 ? own : seq_lens(p, b), tile);
-    if (x == x0) u0 = u;
-    mine += u.n_blk;
-    if (++tile == p.tiles) {
-      tile = 0;
-      ++b;
+  I mine = 0;
+  if (x0 < x1) {
+    u0 = paged_unit<SHIFT>(p, own, tile);
+    mine = u0.n_blk;
+    for (int x = x0 + 1; x < x1; ++x) {
+      if (++tile == p.tiles) {
+        tile = 0;
+        ++b;
+      }
+      mine += paged_unit<SHIFT>(p, seq_lens(p, b), tile).n_blk;
     }
   }
-  long long incl = mine;
+  I incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    const I o = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += o;
   }
   if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
-  long long before = 0, total = 0;
+  I before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
-    const long long v = s_warp[w];
+    const I v = s_warp[w];
     if (w < warp) before += v;
     total += v;
   }
   total *= p.H_kv;
-  // (a 64-bit division costs hundreds of cycles, and few calls need one)
-  long long share = total >> 31 == 0
-                        ? (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x
-                        : (total + gridDim.x - 1) / gridDim.x;
+  I share = (total + static_cast<I>(gridDim.x) - 1) / static_cast<I>(gridDim.x);
   if (share < p.min_share) share = p.min_share;
-  const long long s = share * blockIdx.x;
-  long long at = (before + incl - mine) * p.H_kv;  // first block of this thread's stretch
-  if (s >= at && s < at + mine * p.H_kv) {
+  const I s = share * static_cast<I>(blockIdx.x);
+  I at = (before + incl - mine) * p.H_kv;  // first block of this thread's stretch
+  if (s >= at && s - at < mine * p.H_kv) {
     b = p.tiles == 1 ? x0 : x0 / p.tiles;
     tile = x0 - b * p.tiles;
     Unit u = u0;
     for (int x = x0; x < x1; ++x) {
       if (x > x0) u = paged_unit<SHIFT>(p, seq_lens(p, b), tile);
-      const long long n = static_cast<long long>(u.n_blk) * p.H_kv;
-      if (s < at + n) {
+      const I n = static_cast<I>(u.n_blk) * p.H_kv;
+      if (s - at < n) {
         const int rem = static_cast<int>(s - at);
         start->b = b;
         start->tile = tile;
@@ -195,6 +194,13 @@ __device__ __forceinline__ void paged_find_run(const PagedParams& p, const SeqLe
     }
   }
   if (threadIdx.x == 0) start->share = static_cast<int>(share);
+}
+
+template <int SHIFT, int THREADS>
+__device__ __forceinline__ void paged_find_run(const PagedParams& p, const SeqLens& own, long long* s_warp,
+                                               RunStart* start) {
+  if (p.small) paged_find_run_t<SHIFT, THREADS, int>(p, own, reinterpret_cast<int*>(s_warp), start);
+  else paged_find_run_t<SHIFT, THREADS, long long>(p, own, s_warp, start);
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,

@@ -200,6 +200,18 @@ def test_one_long_sequence(fa, q_len, D):
     case(fa, [9000], [q_len], 4, 1, D, 32, "fp16")
 
 
+@pytest.mark.parametrize("q_len", [1, 200])
+def test_loosest_bound(fa, q_len):
+    """The largest bound on the cache lengths there is (the kernels then count blocks in 64 bits)."""
+    lens, q_lens = [700, 300], [q_len, 1]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, 64, 32, torch.float16, 42)
+    q = rnd((cu[-1], 8, 64), 43, torch.float16)
+    o, lse = run(fa, q, kc, vc, table, lens, cu, max_k=1 << 29)
+    check(o, lse, q, kc, vc, table, lens, cu)
+    o2, l2 = run(fa, q, kc, vc, table, lens, cu)
+    assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
 @pytest.mark.parametrize("q_len", [1, 20, 200])
 def test_garbage_in_the_workspace_does_not_matter(fa, q_len):
     """Every bit pattern a workspace may hold on entry; the same one used again and again."""
