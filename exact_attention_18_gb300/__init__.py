@@ -59,8 +59,8 @@ FA_ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 class PagedCache(ctypes.Structure):
     """``fa_paged_cache`` of fa.h: device pointers, then sizes and element strides."""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
-                ("kv_lens", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("num_pages", ctypes.c_int64),
-                ("page_size", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("kv_lens", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_pages", ctypes.c_int64),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64)]
 
 

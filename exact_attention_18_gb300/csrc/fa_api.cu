@@ -486,6 +486,9 @@ fa_status check_cache(const fa_paged_cache* c, int64_t H_kv, int64_t D) {
       c->table_stride >= (int64_t(1) << 31))
     return fail(FA_ERR_INVALID_ARG, "num_pages=%lld and table_stride=%lld must be positive, below 2^31 - 1",
                 (long long)c->num_pages, (long long)c->table_stride);
+  if (c->table_pages < 0 || c->table_pages > c->table_stride)
+    return fail(FA_ERR_INVALID_ARG, "table_pages=%lld must be between 0 and table_stride=%lld",
+                (long long)c->table_pages, (long long)c->table_stride);
   const int64_t sp = c->page_stride, sr = c->row_stride, sh = c->head_stride;
   if (sp <= 0 || sr <= 0 || sh <= 0) return fail(FA_ERR_INVALID_ARG, "cache strides must be positive");
   if (sp % 8 != 0 || sr % 8 != 0 || sh % 8 != 0)
@@ -521,7 +524,8 @@ int log2_of(int64_t x) {
 
 // Keys a row of the block table can hold (at most kMaxPagedLen).
 int64_t table_keys(const fa_paged_cache* c) {
-  return c->table_stride > fa::kMaxPagedLen / c->page_size ? fa::kMaxPagedLen : c->table_stride * c->page_size;
+  const int64_t pages = c->table_pages ? c->table_pages : c->table_stride;
+  return pages > fa::kMaxPagedLen / c->page_size ? fa::kMaxPagedLen : pages * c->page_size;
 }
 
 fa_status rope_impl(const void* q, int64_t q_stride, const void* k, int64_t k_stride, void* q_out,

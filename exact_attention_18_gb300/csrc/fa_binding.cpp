@@ -117,7 +117,7 @@ fa_paged_cache paged_cache(const Tensor& k, const Tensor& v, const Tensor& table
               v.sizes() == k.sizes() && v.strides() == k.strides() && (k.stride(3) == 1 || D <= 1),
           "k_cache and v_cache must be [pages, page_size, H_kv, D] of the rows' heads, head dimension and dtype, with "
           "the same strides and the last dimension dense");
-  require(table.scalar_type() == at::kInt && table.dim() == 2 && table.size(0) == batch &&
+  require(table.scalar_type() == at::kInt && table.dim() == 2 && table.size(0) == batch && (batch == 0 || table.size(1) >= 1) &&
               (table.stride(1) == 1 || table.size(1) <= 1) && (batch <= 1 || table.stride(0) >= table.size(1)),
           "block_table must be an int32 tensor [batch, pages per sequence] with dense rows");
   fa_paged_cache c;
@@ -126,6 +126,7 @@ fa_paged_cache paged_cache(const Tensor& k, const Tensor& v, const Tensor& table
   c.block_table = static_cast<const int32_t*>(table.const_data_ptr());
   c.kv_lens = static_cast<const int32_t*>(ints(kv_lens, at::kInt, batch, "kv_lens"));
   c.table_stride = batch > 1 ? table.stride(0) : table.size(1);
+  c.table_pages = table.size(1);
   c.num_pages = k.size(0);
   c.page_size = k.size(1);
   // The stride of a dimension of one entry is never used; it may be any number in torch.

@@ -383,23 +383,24 @@ fa_status fa_rope_bwd(const void* dq_out, int64_t dq_out_stride, const void* dk_
  * its value likewise from v.  page_size is a power of two, 16 or more; strides
  * are in elements, shared by k and v, multiples of 8, and leave rows apart
  * (pages, rows and heads in any order of nesting).
- *   block_table : DEVICE int32 [batch, table_stride]; entries past a
- *                 sequence's last page, and of pages no query can see, are not
- *                 used and may hold anything.
+ *   block_table : DEVICE int32, rows of table_pages entries (0: table_stride
+ *                 of them), table_stride entries apart, so it may be a slice of a
+ *                 wider table; entries past a sequence's last page, and of
+ *                 pages no query can see, are not used and may hold anything.
  *   kv_lens     : DEVICE int32 [batch], keys of each sequence INCLUDING the
  *                 call's new tokens, so token i of the n new ones is key
  *                 kv_lens[b] - n + i.
  * Lengths and entries are checked on the device: a length below 0, beyond the
- * call's bound or the block table's row, or (append) below n leaves that sequence alone, an entry in use
- * outside [0, num_pages) is read as zeros and never written; both make
- * fa_check_device_errors() return FA_ERR_INVALID_ARG.
+ * call's bound or the block table's row, or (append) below n leaves that
+ * sequence alone, an entry in use outside [0, num_pages) is read as zeros and
+ * never written; both make fa_check_device_errors() return FA_ERR_INVALID_ARG.
  */
 typedef struct {
   void* k;
   void* v;
   const int32_t* block_table;
   const int32_t* kv_lens;
-  int64_t table_stride;
+  int64_t table_stride, table_pages;
   int64_t num_pages, page_size;
   int64_t page_stride, row_stride, head_stride;
 } fa_paged_cache;

@@ -164,6 +164,7 @@ def _cache(**kw):
 CACHE_BAD = [
     (dict(k=0), 1), (dict(v=P + 8), 3), (dict(block_table=0), 1), (dict(kv_lens=P + 2), 3),
     (dict(page_size=8), 2), (dict(page_size=48), 2), (dict(num_pages=0), 1), (dict(table_stride=0), 1),
+    (dict(table_pages=-1), 1), (dict(table_pages=9), 1),
     (dict(row_stride=0), 1), (dict(row_stride=132), 3), (dict(head_stride=32), 1),
     (dict(row_stride=64, head_stride=64), 1),          # rows of the two heads overlap
     (dict(page_stride=15 * 128), 1),                   # pages overlap

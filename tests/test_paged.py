@@ -15,7 +15,7 @@ import torch
 
 from oracle import paged
 from oracle.attention import as_f64
-from tests.test_rope import DT, ints, on_gpu, paged_setup, rnd
+from tests.test_rope import DT, ints, on_gpu, paged_setup, projection, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -284,6 +284,28 @@ def test_bad_pages_and_lengths_are_reported(fa):
         assert fa.STATUS[fa.fa_check_device_errors(None)] == "FA_ERR_INVALID_ARG"
     o, lse = run(fa, q, kc, vc, table, lens, cu)
     check(o, lse, q, kc, vc, table, lens, cu)
+
+
+def test_slice_of_a_wider_table(fa):
+    """A block table that is a slice: right, and a length past the slice's row is reported, not followed."""
+    lens, q_lens = [48, 33], [1, 1]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, 64, 16, torch.float16, 70)
+    (_, k, v), (qg, kg, vg) = projection(2, 4, 2, 64, torch.float16, 71)
+    kcg, vcg = on_gpu(kc, vc)
+    wide = torch.zeros(4, 16, dtype=torch.int32)
+    wide[:2, 2:5] = table[:, :3]
+    part = wide.cuda()[:2, 2:5]
+    o, lse = fa.forward_paged(qg.contiguous(), kcg, vcg, part, ints(lens), ints(cu), 1, 256)
+    assert fa.fa_check_device_errors(None) == 0
+    check(o, lse, qg.contiguous().cpu(), kc, vc, table, lens, cu)
+    for n in ([49, 33], [48, 49]):
+        fa.forward_paged(qg.contiguous(), kcg, vcg, part, ints(n), ints(cu), 1, 256)
+        assert fa.STATUS[fa.fa_check_device_errors(None)] == "FA_ERR_INVALID_ARG"
+    fa.paged_append(kg, vg, kcg, vcg, part, ints([49, 33]), ints(cu), 1)
+    assert fa.STATUS[fa.fa_check_device_errors(None)] == "FA_ERR_INVALID_ARG"
+    want = kc.clone()
+    want.view(-1, 2, 64)[paged.slots(table[1], torch.arange(32, 33), 16)] = k[1:]
+    assert torch.equal(kcg.cpu(), want)
 
 
 def test_a_bad_sequence_leaves_the_others_right(fa):
