@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <cmath>
 #include <map>
+#include <mutex>
 #include <stdexcept>
 #include <string>
 #include <utility>
@@ -152,6 +153,14 @@ Tensor scratch(int64_t bytes, const Tensor& like, cudaStream_t stream) {
   Tensor& t = (*kept)[{like.get_device(), stream}];
   if (!t.defined() || t.numel() < bytes) t = empty({std::max<int64_t>(bytes, 1 << 20)}, at::kByte, like);
   return t;
+}
+
+// Held while a call that uses kept scratch issues its launches: between two
+// threads that share a stream, one call's launches must not fall between the
+// other's.  Taken without the interpreter's lock.
+std::mutex& scratch_order() {
+  static auto* m = new std::mutex;
+  return *m;
 }
 
 // Calls f() and turns its exceptions into Python's.
@@ -304,6 +313,8 @@ PyObject* forward_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     const Tensor out = o ? *o : empty(q.sizes(), type, q), lse = l ? *l : empty({H, T}, at::kFloat, q);
     fa_status st;
     Py_BEGIN_ALLOW_THREADS
+    std::unique_lock<std::mutex> order(scratch_order(), std::defer_lock);
+    if (!ws) order.lock();
     st = fa_fwd_paged(q.const_data_ptr(), out.mutable_data_ptr(), static_cast<float*>(lse.mutable_data_ptr()), &cache,
                       static_cast<const int32_t*>(cu.const_data_ptr()), batch, max_q, max_k, T, H, hk, D, causal, left,
                       right, scale, code, work.mutable_data_ptr(), work.nbytes(), stream);

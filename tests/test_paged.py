@@ -9,6 +9,7 @@ Error bound of an output element, term by term (W = sum_j p_j |v_j|):
 L is off by e + 2^-22 |L| + 2^-21 (its logarithm).
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -401,6 +402,32 @@ def test_two_streams_at_once(fa, q_len):
     for i, (o, lse) in got:
         assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
     check(want[0][0], want[0][1], qs[0], kc, vc, table, lens, cu)
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_threads_that_share_a_stream(fa, q_len):
+    """Four threads' calls on one stream, which share its scratch."""
+    lens, q_lens = [5000, 900], [q_len, 1]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, 64, 64, torch.float16, 72)
+    kcg, vcg = on_gpu(kc, vc)
+    args = (kcg, vcg, ints(table), ints(lens), ints(cu), q_len, 5000)
+    qs = [rnd((cu[-1], 8, 64), 73 + i, torch.float16).cuda() for i in range(4)]
+    want = [fa.forward_paged(x, *args) for x in qs]
+    got = [[] for _ in qs]
+
+    def work(i):
+        for _ in range(100):
+            got[i].append(fa.forward_paged(qs[i], *args))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert fa.fa_check_device_errors(None) == 0
+    for w, g in zip(want, got):
+        assert len(g) == 100 and all(torch.equal(o, w[0]) and torch.equal(lse, w[1]) for o, lse in g)
 
 
 def test_captured_step_replayed(fa):
