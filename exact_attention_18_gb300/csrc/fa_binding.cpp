@@ -313,11 +313,11 @@ PyObject* forward_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     const Tensor out = o ? *o : empty(q.sizes(), type, q), lse = l ? *l : empty({H, T}, at::kFloat, q);
     fa_status st;
     Py_BEGIN_ALLOW_THREADS
-    std::unique_lock<std::mutex> order(scratch_order(), std::defer_lock);
-    if (!ws) order.lock();
+    if (!ws) scratch_order().lock();
     st = fa_fwd_paged(q.const_data_ptr(), out.mutable_data_ptr(), static_cast<float*>(lse.mutable_data_ptr()), &cache,
                       static_cast<const int32_t*>(cu.const_data_ptr()), batch, max_q, max_k, T, H, hk, D, causal, left,
                       right, scale, code, work.mutable_data_ptr(), work.nbytes(), stream);
+    if (!ws) scratch_order().unlock();
     Py_END_ALLOW_THREADS
     return st == FA_OK ? pair(out, lse) : PyLong_FromLong(st);
   });
