@@ -100,13 +100,13 @@ __global__ void __launch_bounds__(kRopeMaxThreads) fa_rope_kernel(const RopePara
       return;
     }
     n_tok = min(p.tok_per_cta, len - tok0);
+    if (n_tok <= 0) return;
     pos0 = kv_len - len + tok0;
     tok0 += a;
   } else {
     tok0 = tile * p.tok_per_cta;
     n_tok = min(p.tok_per_cta, p.total - tok0);
   }
-  if (n_tok <= 0) return;
 
   const int r = p.r, D = p.D;
   // A token's angles in shared memory.  A thread that turns 8 pairs (8 col ..)
@@ -292,8 +292,9 @@ cudaError_t launch_rope(RopeParams p, bool bf16, bool append, int batch, cudaStr
     }
   }
   p.tok_per_cta = static_cast<int>(tok);
-  const int longest = append ? p.max_len : p.total;
-  p.tiles = (longest + p.tok_per_cta - 1) / p.tok_per_cta;
+  // No sequence has more tokens than there are, whatever the caller's bound.
+  const int64_t longest = append && p.max_len < p.total ? p.max_len : p.total;
+  p.tiles = static_cast<int>((longest + tok - 1) / tok);
   const int64_t ctas = static_cast<int64_t>(p.tiles) * (append ? batch : 1);
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(ctas);

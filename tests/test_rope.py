@@ -223,6 +223,18 @@ def test_append_positions_and_no_rotation(fa):
     assert torch.equal(kc2.cpu(), paged.append(kc, kr.cpu(), table, lens, cu))
 
 
+def test_append_loosest_bound(fa):
+    """The largest bound on the new tokens there is: nothing but the tokens themselves sizes the launch."""
+    lens, q_lens = [20, 50], [3, 40]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, 64, 16, torch.bfloat16, 12)
+    (_, k, v), (_, kg, vg) = projection(43, 4, 2, 64, torch.bfloat16, 13)
+    kcg, vcg = on_gpu(kc, vc)
+    fa.paged_append(kg, vg, kcg, vcg, ints(table), ints(lens), ints(cu), (1 << 31) - 1)
+    assert fa.fa_check_device_errors(None) == 0
+    assert torch.equal(kcg.cpu(), paged.append(kc, k, table, lens, cu))
+    assert torch.equal(vcg.cpu(), paged.append(vc, v, table, lens, cu))
+
+
 def test_append_reports_bad_pages_and_lengths(fa):
     """A bad entry's tokens, or a sequence whose length is below its new tokens, are left out and reported."""
     lens, q_lens = [20, 18, 5], [20, 2, 5]
