@@ -92,6 +92,19 @@ def test_inverse_frequencies(rot, scaling):
         assert f[0] == 1.0 and abs(float(f[-1] / fa.rope_inv_freq(rot)[0][-1]) - 1 / 8) < 1e-14
 
 
+@pytest.mark.parametrize("base,original_len", [(10000.0, 0.01), (10000.0, 1e15), (1.5, 4096.0)])
+def test_ramp_beyond_every_pair(base, original_len):
+    """Turns counted pair by pair: all below slow_turns are divided by the factor, all above fast_turns are kept."""
+    rot, factor = 64, 8.0
+    plain = fa.rope_inv_freq(rot, base)[0]
+    turns = original_len * plain / (2 * math.pi)
+    assert bool((turns < 1).all()) or bool((turns > 32).all())
+    want = plain / factor if turns[0] < 1 else plain
+    kw = dict(scaling="parts", factor=factor, original_len=original_len)
+    assert torch.allclose(fa.rope_inv_freq(rot, base, **kw)[0], want, rtol=1e-14, atol=0)
+    assert torch.allclose(rope.inv_freq(rot, base, **kw)[0], want, rtol=1e-14, atol=0)
+
+
 def test_phase_steps_are_exact_fractions_of_a_turn():
     f = torch.tensor([2 * math.pi / 8, -2 * math.pi / 8, 0.0, 1.0, 2 * math.pi * 5.25], dtype=F64)
     steps = [int(x) % (1 << 64) for x in fa.rope_steps(f, device="cpu")]
