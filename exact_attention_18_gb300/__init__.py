@@ -131,11 +131,9 @@ def _load():
         rope.restype = i32
         rope.argtypes = [vp, i64] * 4 + [vp, vp] + [i64] * 5 + [i32, f32, i32, vp]
     lib.fa_paged_append.restype = i32
-    lib.fa_paged_append.argtypes = [vp, i64] * 4 + [vp] * 4 + [i64] * 7 \
-        + [i32, f32, i32, vp]
+    lib.fa_paged_append.argtypes = [vp, i64] * 4 + [vp] * 4 + [i64] * 7 + [i32, f32, i32, vp]
     lib.fa_fwd_paged.restype = i32
-    lib.fa_fwd_paged.argtypes = [vp] * 5 + [i64] * 7 + [i32, i64, i64, f32, i32,
-                                                                                           vp, sz, vp]
+    lib.fa_fwd_paged.argtypes = [vp] * 5 + [i64] * 7 + [i32, i64, i64, f32, i32, vp, sz, vp]
     lib.fa_fwd_paged_workspace_size.restype = sz
     lib.fa_fwd_paged_workspace_size.argtypes = [i64] * 6
     lib.fa_status_string.restype = ctypes.c_char_p

@@ -589,7 +589,7 @@ bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t 
   const int64_t G = H / H_kv;
   plan->bytes = 0;
   auto add = [&](PagedPart* part, int64_t tok, int64_t longest, int64_t block, int64_t slot_rows,
-                 int64_t ctas) -> bool {
+                 int64_t ctas, int64_t cost) -> bool {
     part->used = true;
     part->tok_tile = static_cast<int>(tok < longest ? tok : longest);
     part->tiles = static_cast<int>((longest + part->tok_tile - 1) / part->tok_tile);
@@ -600,7 +600,7 @@ bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t 
     if (units > (int64_t(1) << 37) / (blocks * H_kv)) return false;  // a CTA's run of blocks fits 31 bits
     const int64_t most = units * H_kv * blocks;
     part->grid = static_cast<int>(most < ctas ? most : ctas);
-    part->small = most < (int64_t(1) << 31) / 304;  // (share x CTA stays below 2^31 too)
+    part->small = most * cost < (int64_t(1) << 31) / 304;  // (share x CTA stays below 2^31 too)
     part->o_at = plan->bytes;
     part->lse_at = part->o_at + round256(static_cast<size_t>(2) * part->grid * part->part_rows * D * sizeof(float));
     part->desc_at = part->lse_at + round256(static_cast<size_t>(2) * part->grid * part->part_rows * sizeof(float));
@@ -615,14 +615,16 @@ bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t 
     plan->few.tok_lo = 0;
     plan->few.tok_hi = static_cast<int>(longest);
     const int64_t ctas = fa::kPagedSms * fa::paged_ctas(static_cast<int>(D), plan->few.N);
-    if (!add(&plan->few, longest, longest, 128, plan->few.N, ctas)) return false;
+    if (!add(&plan->few, longest, longest, 128, plan->few.N, ctas, 1)) return false;
   }
   if (chunks) {
     const int Di = static_cast<int>(D);
     plan->tile.tok_lo = plan->few.used ? plan->few.tok_hi + 1 : 0;
     plan->tile.tok_hi = static_cast<int>(max_q);
     const int64_t tok = fa::paged_tile_tiles(Di) * (128 / G);
-    if (!add(&plan->tile, tok, max_q, fa::paged_tile_block(Di), tok * G, fa::kPagedSms)) return false;
+    if (!add(&plan->tile, tok, max_q, fa::paged_tile_block(Di), tok * G, fa::kPagedSms,
+             fa::kMaxBlockCost))
+      return false;
   }
   return true;
 }
@@ -1050,7 +1052,6 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
       causal ? 0 : (window_right < 0 || window_right >= max_seqlen_k + max_seqlen_q ? fa::kNoWindow : static_cast<int>(window_right));
   p.page_shift = shift;
   p.num_pages = static_cast<int>(cache->num_pages);
-  p.min_share = 1;
   p.scale_log2 = scale * kLog2e;
   p.err = fa::device_error_word();
   if (!p.err) return fail(FA_ERR_CUDA, "cannot resolve the device error word on the current device");
@@ -1070,6 +1071,8 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
     p.tok_lo = part.tok_lo;
     p.tok_hi = part.tok_hi;
     p.small = part.small;
+    p.sub_tok = static_cast<int>(128 / G);
+    p.costs = fa::paged_costs(static_cast<int>(D));
     p.part_rows = part.part_rows;
     p.after_tile = !tile && plan.tile.used;
     p.o_part = reinterpret_cast<float*>(ws + part.o_at);

@@ -90,8 +90,9 @@ struct PagedParams {
   int win_left, win_right;  // key j visible to position i iff i - win_left <= j <= i + win_right (and j < kv_len)
   int page_shift, num_pages;
   int tok_lo, tok_hi;    // sequences of tok_lo .. tok_hi new tokens are this kernel's
-  int small;             // all blocks of the call are below 2^31 / 304
-  int min_share;         // fewest blocks a CTA takes
+  int small;             // the cost of all blocks of the call is below 2^31 / 304
+  int sub_tok;           // tile kernel: tokens of one of a unit's tiles
+  unsigned costs;        // tile kernel: byte i is the cost of a block of a unit that fills i + 1 tiles
   int after_tile;        // few-row kernel: launched behind the tile kernel of the same call
   float scale_log2;
   int part_rows;         // rows of a partial's slot
@@ -121,13 +122,19 @@ struct PagedMergeParams {
 
 // Query rows (new tokens x G) of a sequence up to which the few-row kernel takes
 // it, and rows of a unit it is instantiated for: the smallest that holds `rows`.
-// Both kernels measured (us; 16 sequences of 8192 keys, G = 8): 80 rows, D = 64
-// few-row kernel (instantiated for 128) 58.7, tile kernel 55.9; D = 128 86.5 /
-// 67.9; 128 rows 56.7 / 56.8 and 68.5 / 70.9; 160 rows and more the tile kernel
-// by far (92.2 / 59.7, 111 / 73.5).  Below, a tile of 128 rows is mostly empty.
+// Both kernels measured (us, few-row / tile; 16 sequences of 8192 keys, G = 8):
+// 40 rows D = 64 36.3 / 55.9, D = 128 47.6 / 66.8; 64 rows 34.5 / 55.4 and 48.8 /
+// 67.9; with an instantiation for 128 rows, 80 rows 58.7 / 55.9 and 86.5 / 67.9;
+// 128 rows 56.7 / 56.8 and 68.5 / 70.9; 160 rows 92.2 / 59.7 and 111 / 73.5.
 constexpr int kFewRows = 64;
 inline int paged_rows(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
 constexpr int kPagedSms = 152;
+// Costs of the tile kernel's blocks by the tiles of their unit.  256 units of
+// 8192 keys, 1 .. 4 tiles: D = 64 193, 218, 277, 300 us, D = 32 171, 193, 237, 268,
+// D = 16 161, 182, 215, 249; D = 128, 1 and 2 tiles: 198, 235.  (Fewer tiles leave
+// more of a block's chain of waits uncovered.)
+constexpr int kMaxBlockCost = 8;
+constexpr unsigned paged_costs(int D) { return D == 128 ? 0x0807u : 0x08070605u; }
 // CTAs per SM of the few-row kernel.
 constexpr int paged_ctas(int D, int N) { return D <= 64 && N == 16 ? 2 : 1; }
 // Rows of a unit of the tile kernel (tiles of 128 rows) and keys of its blocks.

@@ -19,9 +19,10 @@
 // cuts, takes the block maximum across lanes.
 //
 // What bounds it: with few rows, reading the cache.  At D = 128 a 128-key
-// block is 64 KB, 2800 cycles of an SM's share of the memory's rate, against
-// ~650 cycles of tensor core and ~500 of softmax for N <= 32.  So the kernel
-// is organised around keeping copies in flight: one or two persistent CTAs per
+// block is 64 KB, 2800 cycles of an SM's share of the memory's rate; decoding 32
+// sequences of up to 8192 keys keeps the tensor pipe active 4.5 % of the time
+// and takes 59 us with the join, 83 % of the copy rate (4 contexts of up to
+// 131072 keys: 150 - 157 us, 96 - 100 %).  So the kernel is organised around keeping copies in flight: one or two persistent CTAs per
 // SM, their shared memory given to a ring of K and V tiles, and work dealt in
 // 128-key blocks: the blocks of all units, in order, are cut into equal runs,
 // one per CTA, whatever the sequences' lengths (each CTA finds its run from
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     fence_mbar_init();
     if (lane == 0) {
       *abort_flag = 0;
-      s_start->run = 0;
+      s_start->left = 0;
       s_start->u.n_blk = 0;
       s_start->blk = 0;
     }
@@ -211,19 +212,19 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     s_off[n] = (n / p.G) * p.H + n % p.G;
   }
   // (the per-row arrays are free until the first segment)
-  paged_find_run<kPShift, L::kThreads>(p, own, reinterpret_cast<long long*>(s_red), s_start);
+  paged_find_run<kPShift, false, L::kThreads>(p, own, reinterpret_cast<long long*>(s_red), s_start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  SegWalk<kPShift> w;
-  w.start(*s_start);
+  SegWalk<kPShift, false> w;
+  w.start(p, *s_start);
 
   if (warp == kProducer || warp == kProducer + 1) {
     // -------------------------------------------------------------- producers
     // One warp copies Q and the K tiles, one the V tiles (ring stages alternate).
     // The whole warp runs this; lane i copies page box i of each tile.  With one
-    // warp for both, its 500-700 cycles per tile bounded the kernel at D <= 64.
+    // warp for both, its 450-750 cycles per tile bounded the kernel at D <= 64.
     const int kv = warp - kProducer;  // 0: K, 1: V
     const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;
     const int frag = min(kPBlk, 1 << p.page_shift);
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
       record_error(p.err, kErrBadPage);
       return p.num_pages;
     };
-    for (int n; ok && (n = w.seg_len()) > 0; w.next(p), ++seg) {
+    for (int n; ok && (n = w.seg_len()) > 0; w.next(p, n), ++seg) {
       int page = box_page(w.blk);
       if (kv == 0) {
         const int qb = seg & 1, qu = seg >> 1;
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
       mma_commit_warp(&bar_empty[st]);
       if (++j == seg_n) {  // the segment's last score product
         mma_commit_warp(&bar_qempty[qb]);
-        w.next(p);
+        w.next(p, seg_n);
         ++seg;
         seg_n = w.seg_len();
         j = 0;
@@ -381,8 +382,8 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     int i = 0;  // block within the CTA's run
     bool alive = true;
     float l[NC];
-    long long at = static_cast<long long>(blockIdx.x) * s_start->share;  // flattened index of the segment's first block
-    for (int n; alive && (n = w.seg_len()) > 0; w.next(p)) {
+    long long at = s_start->at;  // blocks before the segment's first
+    for (int n; alive && (n = w.seg_len()) > 0; w.next(p, n)) {
       const Unit& u = w.u;
       const int n_rows = u.n_tok * p.G;
       const int blk_first = u.lo / kPBlk + w.blk;

