@@ -129,12 +129,13 @@ struct PagedMergeParams {
 constexpr int kFewRows = 64;
 inline int paged_rows(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
 constexpr int kPagedSms = 152;
-// Costs of the tile kernel's blocks by the tiles of their unit.  256 units of
-// 8192 keys, 1 .. 4 tiles: D = 64 193, 218, 277, 300 us, D = 32 171, 193, 237, 268,
-// D = 16 161, 182, 215, 249; D = 128, 1 and 2 tiles: 198, 235.  (Fewer tiles leave
-// more of a block's chain of waits uncovered.)
+// Costs of the tile kernel's blocks by the row tiles of their unit.  256 units of
+// 8192 keys, 1 .. 4 tiles: D = 64 125, 171, 283, 301 us, D = 32 112, 149, 243, 275,
+// D = 16 106, 141, 225, 260; D = 128, 1 and 2 tiles: 203, 248.  A little is added
+// for short units' joins (ragged chunks of 16 heads, D = 64, with 3, 5, 7, 8 / 4, 5,
+// 8, 8: 87.3 / 85.7 us, chunks up to 1000 tokens 103.7 / 101.5).
 constexpr int kMaxBlockCost = 8;
-constexpr unsigned paged_costs(int D) { return D == 128 ? 0x0807u : 0x08070605u; }
+constexpr unsigned paged_costs(int D) { return D == 128 ? 0x0807u : 0x08080504u; }
 // CTAs per SM of the few-row kernel.
 constexpr int paged_ctas(int D, int N) { return D <= 64 && N == 16 ? 2 : 1; }
 // Rows of a unit of the tile kernel (tiles of 128 rows) and keys of its blocks.

@@ -12,16 +12,17 @@
 // and sixteen softmax warps hide more of each other's latency than eight).
 //
 // At D = 128 the tensor core bounds it: chunks of 2048 tokens over 16384 keys,
-// 32 heads on 4, take 588 us with the join, 1.53 PFLOP/s.  At D = 64 the softmax
-// does: ragged chunks of 16 heads take 94 us against 24 of memory or products.
+// 32 heads on 4, take 584 us with the join, 1.54 PFLOP/s.  At D = 64 the chain of
+// products and exponentials does: ragged chunks of 16 heads take 86 us, the
+// tensor pipes active a third of the time, DRAM a fifth.
 //
 // Units, blocks, runs and partials are fa_paged_kernel.cuh's: one persistent
-// CTA per SM takes an equal run of blocks.  Within a unit each tile starts at
-// the first block its own rows see and stops after the last.
+// CTA per SM takes a run of blocks, equal to the others' in cost.  Within a unit
+// each tile starts at the first block its own rows see and stops after the last.
 //
-// Per tile the MMA warp issues O += P(j) V(j), then S(j+1), then one commit:
-// "S(j+1) ready" also means "P(j) consumed, O updated", so the softmax waits
-// once per block and may rescale O as soon as it sees S(j+1).
+// Per tile the MMA warp issues O += P(j) V(j), then S of the tile's next block,
+// then one commit: "next S ready" also means "P(j) consumed, O updated", so the
+// softmax waits once per block and may rescale O as soon as it sees that S.
 #pragma once
 
 #include "fa_paged_units.cuh"
@@ -47,27 +48,29 @@ struct PagedTileLayout {
   // tiles 2900 cycles, or up to 4000, instead of 2430).  Four tiles: two warps;
   // one cannot keep the tensor core fed.
   static constexpr int kMmaWarps = kTiles == 2 ? 1 : 2;
-  static constexpr int kThreads = 32 * kSoftWarps + 128;  // producer, MMA warps, the rest idle
+  static constexpr int kThreads = 32 * kSoftWarps + 128;  // and the producers of K and V, the MMA warps
   // Register split: every thread gets kLaunchRegs at launch, the last four
   // warps drop to kRegsLow and the softmax warps rise to kRegsHigh.
   static constexpr int kLaunchRegs = kTiles == 2 ? 168 : 96;
   static constexpr uint32_t kRegsHigh = kTiles == 2 ? 216 : 104;
   static constexpr uint32_t kRegsLow = kTiles == 2 ? 72 : 64;
   static_assert(32 * kSoftWarps * kRegsHigh + 128 * kRegsLow <= kThreads * kLaunchRegs, "register split");
-  static constexpr int kSmallBytes = D == 128 ? 2048 : 3072;  // barriers, run, walks
+  static constexpr int kSmallBytes = D == 128 ? 2048 : 5120;  // barriers, run, walks, row statistics
+  static constexpr int kStatBytes = kTiles == 4 ? 3 * 128 * 8 : 32 * 8;
   // Two Q buffers where they fit beside the ring, so that the next unit's Q is
   // there when the last blocks of this one are done.
   static constexpr int kQBufs = D == 128 ? 1 : 2;
   static constexpr int kQBytes = kTiles * GQ::kTileBytes;
   static constexpr int kUnitsFit = (227 * 1024 - 1024 - kQBufs * kQBytes - kSmallBytes) / GK::kTileBytes;
-  static constexpr int kUnits = kUnitsFit > 20 ? 20 : kUnitsFit;  // ring stages, one K or V block each
-  static_assert(kUnits >= 4, "ring");
+  static constexpr int kUnits = kUnitsFit > 20 ? 20 : kUnitsFit;  // stages of both rings, one block each
+  static_assert(kUnits >= 4, "rings");
+  static constexpr int kUnitsK = (kUnits + 1) / 2, kUnitsV = kUnits / 2;
   static constexpr int kOffQ = kUnits * GK::kTileBytes;
   static constexpr int kOffSmall = kOffQ + kQBufs * kQBytes;
-  // full[U], empty[U], qfull[2], qempty[2], sfull[T], pfull[T], ofinal[T], vtmp, drain[2]
-  static constexpr int kNumBars = 2 * kUnits + 4 + 3 * kTiles + 3;
-  static_assert(kNumBars * 8 + 16 + sizeof(RunStart) + kSoftWarps * sizeof(SegWalk<kShift, true>) + 32 * 8 <= kSmallBytes,
-                "barriers");
+  // full[U], empty[U], qfull[2], qempty[2], sfull[T], pfull[T], ofinal[T], stat[T], freed[T], vtmp, drain[2]
+  static constexpr int kNumBars = 2 * kUnits + 4 + 5 * kTiles + 3;
+  static_assert(kNumBars * 8 + 16 + sizeof(RunStart) + kSoftWarps * (sizeof(SegWalk<kShift, true>) + 8) + kStatBytes <=
+                    kSmallBytes, "barriers");
   static constexpr int kSmemUsed = kOffSmall + kSmallBytes + 1024;
   static constexpr int kSmemBytes = kSmemUsed > 116 * 1024 ? kSmemUsed : 116 * 1024;  // one CTA per SM
   static constexpr uint32_t kTileCols = 512 / kTiles;  // TMEM columns of a tile: S (P over it), then O
@@ -75,28 +78,41 @@ struct PagedTileLayout {
   static_assert(kColO + D <= kTileCols, "TMEM layout");
 };
 
-// Tile t of a unit: its tokens and the blocks [beg, end) of the current
-// segment that its rows see.
+// Tile t of the CTA in the current unit.  With four tiles (D <= 64) a unit of
+// one or two row tiles would leave the others idle while a block's chain
+// (products, exponentials, products) runs uncovered, so they take its blocks in
+// turns, and their O are joined at the segment's end: 256 units of 8192 keys of
+// one row tile 192 -> 125 us, of two 216 -> 171 (D = 64).  With two (D = 128) the
+// chain is covered by the block's memory time: 203 us either way, so not there.
 struct TileSpan {
-  int ta, n_tok;  // first token within the unit, tokens
-  int pos0;       // cache position of its first token
-  int beg, end;
+  int tiles;       // row tiles of the unit
+  int turns;       // tiles of the CTA that share each of them (a power of two)
+  int row_tile, turn;  // this tile's; turn >= turns: it is idle
+  int ta, n_tok;   // first token within the unit, tokens
+  int pos0;        // cache position of its first token
+  int beg, end;    // its blocks: beg, beg + turns, .. end - 1
 };
 
-template <int SHIFT>
+template <int SHIFT, int TILES>
 __device__ __forceinline__ TileSpan tile_span(const PagedParams& p, const SegWalk<SHIFT, true>& w, int t, int tile_tok,
                                               int n) {
   TileSpan s;
-  s.ta = t * tile_tok;
+  s.tiles = (w.u.n_tok + tile_tok - 1) / tile_tok;
+  s.turns = TILES < 4 || s.tiles > 2 ? 1 : 4 / s.tiles;
+  s.turn = t / s.tiles;
+  s.row_tile = t - s.turn * s.tiles;
+  s.ta = s.row_tile * tile_tok;
   s.n_tok = min(tile_tok, w.u.n_tok - s.ta);
   s.pos0 = w.u.pos0 + s.ta;
   s.beg = s.end = 0;
-  if (s.n_tok <= 0) return s;
+  if (s.turn >= s.turns) return s;
   const int lo = max(0, s.pos0 - p.win_left), hi = min(w.u.kv_len, s.pos0 + s.n_tok + p.win_right);
   if (hi <= lo) return s;
   const int base = (w.u.lo >> SHIFT) + w.blk;  // the segment's first block
-  s.beg = min(n, max(0, (lo >> SHIFT) - base));
-  s.end = min(n, max(0, ((hi + (1 << SHIFT) - 1) >> SHIFT) - base));
+  const int beg = min(n, max(0, (lo >> SHIFT) - base));
+  const int end = min(n, max(0, ((hi + (1 << SHIFT) - 1) >> SHIFT) - base));
+  s.beg = beg + ((s.turn - beg) & (s.turns - 1));
+  s.end = end - ((end - 1 - s.turn) & (s.turns - 1));
   if (s.end <= s.beg) s.beg = s.end = 0;
   return s;
 }
@@ -115,7 +131,9 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   using elem_t = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   using Walk = SegWalk<L::kShift, true>;
   constexpr int U = L::kUnits, T = L::kTiles, BN = L::kBlk;
-  constexpr int kProducer = L::kSoftWarps, kMma0 = L::kSoftWarps + 1;
+  // The last four warps sit on one scheduler each; MMA issuers on the first
+  // two (the other way round four full tiles at D = 64 take 309 us, not 301).
+  constexpr int kMma0 = L::kSoftWarps, kProducer = L::kSoftWarps + 2, kProducerV = L::kSoftWarps + 3;
   constexpr int kMmaWarps = L::kMmaWarps, kTilesPerMma = T / kMmaWarps;
   constexpr float kSumLimit = 256.0f;  // largest block sum of P~ kept with a stale maximum
 
@@ -128,15 +146,23 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   uint64_t* bar_sfull = bar_qempty + 2;  // [T] S_t computed (and the P_t V before it done)
   uint64_t* bar_pfull = bar_sfull + T;   // [T] P_t stored, O_t rescaled
   uint64_t* bar_ofinal = bar_pfull + T;  // [T] the segment's last P_t V done
-  uint64_t* bar_vtmp = bar_ofinal + T;   // a V block that still needs rows cleared has landed
+  uint64_t* bar_stat = bar_ofinal + T;   // [T] this tile's share of a split unit can be joined
+  uint64_t* bar_freed = bar_stat + T;    // [T] row tile's other shares were joined
+  uint64_t* bar_vtmp = bar_freed + T;    // a V block that still needs rows cleared has landed
   uint64_t* bar_drain = bar_vtmp + 1;    // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   RunStart* s_start = reinterpret_cast<RunStart*>(tmem_slot + 2);
   // Each softmax warp's walk, parked here while it works through a segment's
   // blocks: in registers it made the block loop spill.
-  Walk* s_walk = reinterpret_cast<Walk*>(s_start + 1);
-  long long* s_warp = reinterpret_cast<long long*>(smem + L::kOffSmall + L::kSmallBytes - 32 * 8);
+  struct Parked {
+    Walk w;
+    unsigned phases;
+  };
+  Parked* s_walk = reinterpret_cast<Parked*>(s_start + 1);
+  // Maximum and sum of the rows of tiles 1 .. T-1 where they share a unit.
+  float2* s_stat = reinterpret_cast<float2*>(smem + L::kOffSmall + L::kSmallBytes - L::kStatBytes);
+  long long* s_warp = reinterpret_cast<long long*>(s_stat);  // (before the first unit)
 
   const int warp = warp_index();
   const int lane = threadIdx.x & 31;
@@ -153,6 +179,8 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       mbar_init(&bar_sfull[t], 1);
       mbar_init(&bar_pfull[t], 4);
       mbar_init(&bar_ofinal[t], 1);
+      mbar_init(&bar_stat[t], 4);
+      mbar_init(&bar_freed[t], 4);
     }
     mbar_init(bar_vtmp, 1);
     mbar_init(&bar_drain[0], 1);
@@ -189,16 +217,25 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int tile_tok = 128 / p.G;  // tokens of a 128-row tile
 
-  if (warp >= kProducer) {
+  if (warp >= L::kSoftWarps) {
     regs_decrease<L::kRegsLow>();
     Walk w;
     w.start(p, *s_start);
-    if (warp == kProducer) {
-      // ------------------------------------------------------------ producer
-      // The whole warp runs this; lane i copies page box i of each block.
+    if (warp == kProducer || warp == kProducerV) {
+      // ------------------------------------------------------------ producers
+      // One warp copies Q and the K blocks, one the V blocks, each through its
+      // own ring.  The whole warp runs this; lane i copies page box i of a block.
+      const int kv = warp == kProducer ? 0 : 1;
+      const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;
+      const int stages = kv == 0 ? L::kUnitsK : L::kUnitsV;
+      uint64_t* full = bar_full + (kv == 0 ? 0 : L::kUnitsK);
+      uint64_t* empty = bar_empty + (kv == 0 ? 0 : L::kUnitsK);
+      uint8_t* ring = smem + (kv == 0 ? 0 : L::kUnitsK * GK::kTileBytes);
       const int frag = min(BN, 1 << p.page_shift);
       const int n_frag = BN / frag;
       int c = 0, seg = 0, n_cut = 0;  // blocks started, segments started, V blocks that had rows cleared
+      int st = 0;         // ring stage of the next block
+      unsigned pass = 0;  // passes over the ring
       bool ok = true;
       auto box_page = [&](int blk) -> int {  // page (or out of range) of this lane's box of the unit's block
         const int key = ((w.u.lo >> L::kShift) + blk) * BN + lane * frag;
@@ -210,65 +247,67 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       };
       for (int n; ok && (n = w.seg_len()) > 0; w.next(p, n), ++seg) {
         int page = box_page(w.blk);
-        const int qb = seg % L::kQBufs, qu = seg / L::kQBufs;
-        if (qu > 0) ok = warp_wait(&bar_qempty[qb], (qu - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
-        if (!ok) break;
-        if (lane == 0) {
-          const int tiles = (w.u.n_tok + tile_tok - 1) / tile_tok;
-          mbar_arrive_expect_tx(&bar_qfull[qb], tiles * GQ::kChunks * GQ::kRowBytes * p.G * tile_tok);
-          for (int t = 0; t < tiles; ++t)
+        if (kv == 0) {
+          const int qb = seg % L::kQBufs, qu = seg / L::kQBufs;
+          if (qu > 0) ok = warp_wait(&bar_qempty[qb], (qu - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
+          if (!ok) break;
+          if (lane == 0) {
+            const int tiles = (w.u.n_tok + tile_tok - 1) / tile_tok;
+            mbar_arrive_expect_tx(&bar_qfull[qb], tiles * GQ::kChunks * GQ::kRowBytes * p.G * tile_tok);
+            for (int t = 0; t < tiles; ++t)
 #pragma unroll
-            for (int ch = 0; ch < GQ::kChunks; ++ch)
-              tma_load_3d(smem + L::kOffQ + qb * L::kQBytes + t * GQ::kTileBytes + ch * GQ::kChunkBytes, &tm_q,
-                          &bar_qfull[qb],
-                          ch * (GQ::kRowBytes / 2), w.kvh * p.G, w.u.tok0 + t * tile_tok);
+              for (int ch = 0; ch < GQ::kChunks; ++ch)
+                tma_load_3d(smem + L::kOffQ + qb * L::kQBytes + t * GQ::kTileBytes + ch * GQ::kChunkBytes, &tm_q,
+                            &bar_qfull[qb], ch * (GQ::kRowBytes / 2), w.kvh * p.G, w.u.tok0 + t * tile_tok);
+          }
+          __syncwarp();
         }
-        __syncwarp();
         for (int j = 0; ok && j < n; ++j) {
           const int page_next = j + 1 < n ? box_page(w.blk + j + 1) : 0;
           const int key0 = ((w.u.lo >> L::kShift) + w.blk + j) * BN;
           const int row = (key0 + lane * frag) & ((1 << p.page_shift) - 1);
-          const bool cut = key0 < w.u.lo || key0 + BN > w.u.hi;
+          const bool clear = kv == 1 && (key0 < w.u.lo || key0 + BN > w.u.hi);
+          if (pass > 0) {
+            ok = warp_wait(&empty[st], (pass - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
+            if (!ok) break;
+          }
+          uint8_t* tile = ring + st * GK::kTileBytes;
+          uint64_t* bar = clear ? bar_vtmp : &full[st];
+          if (lane == 0) mbar_arrive_expect_tx(bar, GK::kTileBytes);
+          __syncwarp();
+          if (lane < n_frag) {
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const int st = c % U, use = c / U;
-            if (use > 0) {
-              ok = warp_wait(&bar_empty[st], (use - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
-              if (!ok) break;
+            for (int ch = 0; ch < GK::kChunks; ++ch)
+              tma_load_4d(tile + ch * GK::kChunkBytes + lane * frag * GK::kRowBytes, map, bar,
+                          ch * (GK::kRowBytes / 2), w.kvh, row, page);
+          }
+          ++c;
+          if (clear) {
+            // Clear the V rows no row of the unit sees (0 * NaN is not 0).
+            drain_wait(bar_vtmp, n_cut & 1, p.err);
+            ++n_cut;
+            const int k0 = max(0, w.u.lo - key0), k1 = min(BN, w.u.hi - key0);  // visible rows [k0, k1)
+            constexpr int kVecs = GK::kRowBytes / 16;
+            for (int i = lane; i < BN * kVecs * GK::kChunks; i += 32) {
+              const int r = (i / kVecs) % BN;
+              if (r < k0 || r >= k1) *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
             }
-            uint8_t* tile = smem + st * GK::kTileBytes;
-            uint64_t* bar = kv == 1 && cut ? bar_vtmp : &bar_full[st];
-            if (lane == 0) mbar_arrive_expect_tx(bar, GK::kTileBytes);
+            fence_proxy_async_smem();
             __syncwarp();
-            if (lane < n_frag) {
-#pragma unroll
-              for (int ch = 0; ch < GK::kChunks; ++ch)
-                tma_load_4d(tile + ch * GK::kChunkBytes + lane * frag * GK::kRowBytes, kv == 0 ? &tm_k : &tm_v, bar,
-                            ch * (GK::kRowBytes / 2), w.kvh, row, page);
-            }
-            ++c;
-            if (kv == 1 && cut) {
-              // Clear the V rows no row of the unit sees (0 * NaN is not 0).
-              drain_wait(bar_vtmp, n_cut & 1, p.err);
-              ++n_cut;
-              const int k0 = max(0, w.u.lo - key0), k1 = min(BN, w.u.hi - key0);  // visible rows [k0, k1)
-              constexpr int kVecs = GK::kRowBytes / 16;
-              for (int i = lane; i < BN * kVecs * GK::kChunks; i += 32) {
-                const int r = (i / kVecs) % BN;
-                if (r < k0 || r >= k1) *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bar_full[st]);
-            }
+            if (lane == 0) mbar_arrive(&full[st]);
           }
           page = page_next;
+          if (++st == stages) {
+            st = 0;
+            ++pass;
+          }
         }
       }
       // Teardown: every copy this warp started lands before the CTA exits.
-      for (int x = (c > U ? c - U : 0); x < c; ++x) drain_wait(&bar_full[x % U], (x / U) & 1, p.err);
-      for (int x = (seg > L::kQBufs ? seg - L::kQBufs : 0); x < seg; ++x)
-        drain_wait(&bar_qfull[x % L::kQBufs], (x / L::kQBufs) & 1, p.err);
+      for (int x = max(0, c - stages); x < c; ++x) drain_wait(&full[x % stages], (x / stages) & 1, p.err);
+      if (kv == 0)
+        for (int x = (seg > L::kQBufs ? seg - L::kQBufs : 0); x < seg; ++x)
+          drain_wait(&bar_qfull[x % L::kQBufs], (x / L::kQBufs) & 1, p.err);
       __syncwarp();
     } else if (warp < kMma0 + kMmaWarps) {
       // ------------------------------------------------------------ MMA issuers
@@ -277,34 +316,39 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       constexpr uint32_t idesc_pv = make_idesc_f16(BF16, 128, D, false, true);
       const AccFlags acc = runtime_flags(p.batch);
       const uint32_t s_ring = smem_u32(smem), s_q = smem_u32(smem + L::kOffQ);
-      int c = 0;                     // ring blocks before the segment
+      int c = 0;                     // blocks before the segment
       int done[kTilesPerMma];        // blocks of each tile whose P V was issued
 #pragma unroll
       for (int h = 0; h < kTilesPerMma; ++h) done[h] = 0;
       bool ok = true;
       int seg = 0;
       for (int n; ok && (n = w.seg_len()) > 0; w.next(p, n), ++seg) {
-        int beg[kTilesPerMma], end[kTilesPerMma];
+        int beg[kTilesPerMma], end[kTilesPerMma], turn[kTilesPerMma], row_tile[kTilesPerMma], turns;
 #pragma unroll
         for (int h = 0; h < kTilesPerMma; ++h) {
-          const TileSpan s = tile_span<L::kShift>(p, w, m * kTilesPerMma + h, tile_tok, n);
+          const TileSpan s = tile_span<L::kShift, T>(p, w, m * kTilesPerMma + h, tile_tok, n);
           beg[h] = s.beg;
           end[h] = s.end;
+          turn[h] = s.turn;
+          row_tile[h] = s.row_tile;
+          turns = s.turns;
         }
         const int qb = seg % L::kQBufs;
         ok = warp_wait(&bar_qfull[qb], (seg / L::kQBufs) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
-        for (int j = -1; ok && j < n; ++j) {
-          const int kc = c + 2 * (j + 1), vc = c + 2 * j + 1;  // ring blocks of K(j+1), V(j)
-          const int ks = kc % U, vs = vc % U;
+        for (int j = -turns; ok && j < n; ++j) {
+          const int jk = j + turns;
+          const int kc = c + jk, vc = c + j;
+          const int ks = kc % L::kUnitsK, vs = vc % L::kUnitsV;  // ring stages of K(jk), V(j)
           if (j >= 0)
-            ok = warp_wait(&bar_full[vs], (vc / U) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
-          if (ok && j + 1 < n)
-            ok = warp_wait(&bar_full[ks], (kc / U) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
+            ok = warp_wait(&bar_full[L::kUnitsK + vs], (vc / L::kUnitsV) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
+          if (ok && jk < n)
+            ok = warp_wait(&bar_full[ks], (kc / L::kUnitsK) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
           if (!ok) break;
 #pragma unroll
           for (int h = 0; h < kTilesPerMma; ++h) {
             const int t = m * kTilesPerMma + h;
             const uint32_t t_s = tmem + t * L::kTileCols;
+            if (turn[h] != (jk & (turns - 1))) continue;
             if (j >= beg[h] && j < end[h]) {
               if (!ok) break;
               ok = warp_wait(&bar_pfull[t], done[h] & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
@@ -312,16 +356,17 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
               ++done[h];
               tc_fence_after();
               const uint64_t v_desc =
-                  make_sdesc(s_ring + vs * GK::kTileBytes, GK::kChunkBytes, 8 * GK::kRowBytes, GK::kSwz);
+                  make_sdesc(s_ring + (L::kUnitsK + vs) * GK::kTileBytes, GK::kChunkBytes, 8 * GK::kRowBytes, GK::kSwz);
 #pragma unroll
               for (int kk = 0; kk < BN / 16; ++kk)
                 mma_ts_warp(t_s + L::kColO, t_s + kk * 8, desc_plus(v_desc, mnmajor_step_bytes<D>(kk)), idesc_pv,
                             (j > beg[h] || kk > 0) ? acc.on : acc.off);
               if (j == end[h] - 1) mma_commit_warp(&bar_ofinal[t]);
             }
-            if (j + 1 >= beg[h] && j + 1 < end[h]) {
+            if (jk >= beg[h] && jk < end[h]) {
               tc_fence_after();
-              const uint64_t q_desc = make_sdesc(s_q + qb * L::kQBytes + t * GQ::kTileBytes, 16, 8 * GQ::kRowBytes, GQ::kSwz);
+              const uint64_t q_desc = make_sdesc(
+                  s_q + qb * L::kQBytes + row_tile[h] * GQ::kTileBytes, 16, 8 * GQ::kRowBytes, GQ::kSwz);
               const uint64_t k_desc = make_sdesc(s_ring + ks * GK::kTileBytes, 16, 8 * GK::kRowBytes, GK::kSwz);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk)
@@ -331,11 +376,11 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
             }
           }
           if (!ok) break;
-          if (j >= 0) mma_commit_warp(&bar_empty[vs]);
-          if (j + 1 < n) mma_commit_warp(&bar_empty[ks]);
-          if (j + 1 == n - 1) mma_commit_warp(&bar_qempty[qb]);
+          if (j >= 0) mma_commit_warp(&bar_empty[L::kUnitsK + vs]);
+          if (jk < n) mma_commit_warp(&bar_empty[ks]);
+          if (jk == n - 1) mma_commit_warp(&bar_qempty[qb]);
         }
-        c += 2 * n;
+        c += n;
       }
       mma_commit_warp(&bar_drain[m]);
       drain_wait(&bar_drain[m], 0, p.err);
@@ -358,6 +403,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     // D = 128 the selects between load and maximum cost more than that (chunks
     // of 2048: 668 us with a copy of its own, 723 in place).
     constexpr bool kMaskInPlace = D <= 64;
+    constexpr bool kShare = T == 4;  // tiles may share a unit's row tile
     // In place, a scale of 0 makes every visible score 0 (0 times a hidden key's infinity would not be -inf).
     const bool zero_scale = kMaskInPlace && sl2 == 0.f;
     const float ce = zero_scale ? 1.f : sl2;
@@ -366,9 +412,9 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     const uint32_t hidden = __float_as_uint(neg_scale ? INFINITY : -INFINITY);
     int cnt = 0, fin = 0;  // blocks of this tile so far; segments in which it had blocks
     bool alive = true;
-    long long at = s_start->at;  // cost of the blocks before the segment's first
+    if (lane == 0) s_walk[warp].phases = 0;
     for (int n; alive && (n = w.seg_len()) > 0; w.next(p, n)) {
-      const TileSpan sp = tile_span<L::kShift>(p, w, t, tile_tok, n);
+      const TileSpan sp = tile_span<L::kShift, T>(p, w, t, tile_tok, n);
       const bool row_ok = rt < sp.n_tok && rt < tile_tok;
       // Relative to the segment's first key: this row's visible keys [lo0, lim0],
       // and the blocks [j_lo, j_hi) that every row of the tile sees whole.
@@ -377,11 +423,13 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       const int lim0 = min(w.u.kv_len - 1, pos + p.win_right) - key_base, lo0 = pos - p.win_left - key_base;
       const int j_lo = (sp.pos0 + sp.n_tok - 1 - p.win_left - key_base + BN - 1) >> L::kShift;
       const int j_hi = (min(w.u.kv_len, sp.pos0 + 1 + p.win_right) - key_base) >> L::kShift;
-      const int beg = sp.beg, end = sp.end;
-      if (lane == 0) s_walk[warp] = w;
+      const int beg = sp.beg, end = sp.end, step = kShare ? sp.turns : 1;
+      if (lane == 0) s_walk[warp].w = w;
       __syncwarp();
+      // (the span is worked out again after the blocks: its other members would
+      // take registers from the block loop)
       float m = -INFINITY, l = 0.f;
-      for (int j = beg; j < end; ++j, ++cnt) {
+      for (int j = beg; j < end; j += step, ++cnt) {
         if (!warp_wait(&bar_sfull[t], cnt & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax)) {
           alive = false;
           break;
@@ -469,7 +517,8 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       }
       if (!alive) break;
       // ------------------------------------------------------------ segment's end
-      w = s_walk[warp];
+      w = s_walk[warp].w;
+      n = w.seg_len();
       const bool have = end > beg;
       if (have) {
         if (!warp_wait(&bar_ofinal[t], fin & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax)) {
@@ -479,23 +528,82 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         ++fin;
         tc_fence_after();
       }
+      const TileSpan es = tile_span<L::kShift, T>(p, w, t, tile_tok, n);
+      const int tiles = es.tiles, turn = es.turn, row_tile = es.row_tile, turns = kShare ? es.turns : 1;
+      const bool mine = have && l > 0.f;
+      // A unit's row tile whose blocks several tiles took in turns: the first
+      // of them joins the others' O and statistics to its own.
+      float w_own = 1.f, w_other[T - 1];
+#pragma unroll
+      for (int k = 1; k < T; ++k) w_other[k - 1] = 0.f;
+      if (turns > 1) {
+        const unsigned phases = s_walk[warp].phases;  // bit t: of bar_stat[t], bit T + t: of bar_freed[t]
+        if (turn > 0) {
+          s_stat[(t - 1) * 128 + r] = make_float2(m, mine ? l : 0.f);
+          warp_arrive(&bar_stat[t]);
+          alive = warp_wait(&bar_freed[row_tile], (phases >> (T + row_tile)) & 1, abort_flag, p.err, p.wait_ns,
+                            kErrTimeoutSoftmax);
+        } else {
+          float2 st[T - 1];
+          float top = mine ? m : -INFINITY;
+#pragma unroll
+          for (int k = 1; k < T; ++k) {
+            st[k - 1] = make_float2(-INFINITY, 0.f);
+            if (k < turns && alive) {
+              const int tk = k * tiles + row_tile;
+              alive = warp_wait(&bar_stat[tk], (phases >> tk) & 1, abort_flag, p.err, p.wait_ns,
+                                kErrTimeoutSoftmax);
+              st[k - 1] = s_stat[(tk - 1) * 128 + r];
+              if (st[k - 1].y > 0.f) top = fmaxf(top, st[k - 1].x);
+            }
+          }
+          w_own = mine ? ex2(m - top) : 0.f;
+          l = mine ? l * w_own : 0.f;
+#pragma unroll
+          for (int k = 1; k < T; ++k) {
+            if (st[k - 1].y > 0.f) w_other[k - 1] = ex2(st[k - 1].x - top);
+            l += w_other[k - 1] * st[k - 1].y;
+          }
+          m = top;
+        }
+        if (!alive) break;
+        tc_fence_after();
+        __syncwarp();
+        if (lane == 0) s_walk[warp].phases = phases ^ ((1u << T) - (1u << tiles)) ^ (((1u << tiles) - 1) << T);
+        __syncwarp();
+      }
       const bool whole = n == w.u.n_blk;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (w.blk == 0 ? 1 : 0);
-      const bool seen = have && l > 0.f;
+      const bool seen = turns > 1 ? l > 0.f : mine;
       const float inv_l = seen ? 1.f / l : 0.f;
-      const int ta = t * tile_tok, tok = w.u.tok0 + ta + rt, head = w.kvh * p.G + rh;
+      const int ta = row_tile * tile_tok, tok = w.u.tok0 + ta + rt, head = w.kvh * p.G + rh;
       // Partials lie [slot][D / 4][part_rows][4]: neighbouring lanes (rows) write
       // neighbouring 16 bytes.
       const int prow = (ta + rt) * p.G + rh;
       float* part = p.o_part + static_cast<int64_t>(slot) * p.part_rows * D + prow * 4;
       elem_t* orow = static_cast<elem_t*>(p.o) + (static_cast<int64_t>(tok) * p.H + head) * D;
-      if (ta < w.u.n_tok) {  // (warp-uniform)
+      if (turn == 0) {  // (warp-uniform)
 #pragma unroll
         for (int c = 0; c < D; c += 16) {
           uint32_t o16[16];
           if (have) tmem_ld16(t_o + c, o16);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o16[i] = seen ? o16[i] : 0u;
+          for (int i = 0; i < 16; ++i) o16[i] = mine ? o16[i] : 0u;
+          if (turns > 1) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o16[i] = __float_as_uint(w_own * __uint_as_float(o16[i]));
+#pragma unroll
+            for (int k = 1; k < T; ++k) {
+              const bool add = w_other[k - 1] > 0.f;
+              if (!__any_sync(0xffffffffu, add)) continue;  // (a tile without blocks holds an earlier unit's O)
+              uint32_t x16[16];
+              tmem_ld16(t_o + k * tiles * L::kTileCols + c, x16);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (add)
+                  o16[i] = __float_as_uint(__uint_as_float(o16[i]) + w_other[k - 1] * __uint_as_float(x16[i]));
+            }
+          }
           if (row_ok) {
             if (whole) store_row16<BF16>(orow + c, o16, inv_l);
             else
@@ -512,11 +620,11 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           else p.lse_part[static_cast<int64_t>(slot) * p.part_rows + prow] = l2;
         }
       }
-      if (!whole && w.blk == 0 && threadIdx.x == 0)
-        p.desc[blockIdx.x] =
-            make_int4(w.u.tok0, w.u.n_tok, w.kvh,
-                      static_cast<int>((at + static_cast<long long>(w.u.n_blk - 1) * w.cost) / s_start->share));
-      at += static_cast<long long>(n) * w.cost;
+      if (turns > 1 && turn == 0) warp_arrive(&bar_freed[row_tile]);
+      if (!whole && w.blk == 0 && threadIdx.x == 0) {
+        const long long last = s_start->at + s_start->left - w.left + static_cast<long long>(w.u.n_blk - 1) * w.cost;
+        p.desc[blockIdx.x] = make_int4(w.u.tok0, w.u.n_tok, w.kvh, static_cast<int>(last / s_start->share));
+      }
     }
   }
 

@@ -138,6 +138,21 @@ def test_not_causal(fa, window, q_len):
     case(fa, [400, q_len], [q_len, q_len], 4, 2, 64, 32, "fp16", causal=False, window=window)
 
 
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+@pytest.mark.parametrize("q_len", [9, 16, 17, 33, 48])
+@pytest.mark.parametrize("window", [None, (70, -1), (1000, -1)])
+def test_units_of_few_tiles(fa, q_len, D, window):
+    """One to three tiles of rows a unit (G = 8): blocks taken in turns, fewer blocks than tiles, cut and whole units."""
+    case(fa, [5000, 48, 1300, 64, 700, 129], [q_len] * 6, 8, 1, D, 32, "bf16", window=window)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_units_of_few_tiles_in_one_piece(fa, D):
+    """More units than CTAs, so that most are not cut, of one and two tiles each, in both orders."""
+    lens = [200 + 61 * i for i in range(12)]
+    case(fa, lens, [70 if i % 3 else 150 for i in range(12)], 16, 16, D, 64, "fp16")
+
+
 @pytest.mark.parametrize("q_len", [1, 40, 200])
 @pytest.mark.parametrize("D", [16, 128])
 def test_rows_that_see_nothing(fa, q_len, D):
