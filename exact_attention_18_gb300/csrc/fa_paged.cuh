@@ -123,9 +123,9 @@ struct PagedMergeParams {
 // Query rows (new tokens x G) of a sequence up to which the few-row kernel takes
 // it, and rows of a unit it is instantiated for: the smallest that holds `rows`.
 // Both kernels measured (us, few-row / tile; 16 sequences of 8192 keys, G = 8):
-// 40 rows D = 64 36.3 / 55.9, D = 128 47.6 / 66.8; 64 rows 34.5 / 55.4 and 48.8 /
-// 67.9; with an instantiation for 128 rows, 80 rows 58.7 / 55.9 and 86.5 / 67.9;
-// 128 rows 56.7 / 56.8 and 68.5 / 70.9; 160 rows 92.2 / 59.7 and 111 / 73.5.
+// 40 rows D = 64 36.4 / 46.6, D = 128 46.4 / 67.1; 64 rows 34.6 / 46.4 and 48.0 /
+// 68.3; with an instantiation for 128 rows, 80 rows 58.7 / 47.3 and 86.5 / 70.7;
+// 128 rows 56.7 / 48.8 and 68.5 / 73.4; 160 rows 92.2 / 57.9 and 111 / 78.0.
 constexpr int kFewRows = 64;
 inline int paged_rows(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
 constexpr int kPagedSms = 152;

@@ -21,8 +21,8 @@
 // What bounds it: with few rows, reading the cache.  At D = 128 a 128-key
 // block is 64 KB, 2800 cycles of an SM's share of the memory's rate; decoding 32
 // sequences of up to 8192 keys keeps the tensor pipe active 4.5 % of the time
-// and takes 59 us with the join, 83 % of the copy rate (4 contexts of up to
-// 131072 keys: 150 - 157 us, 96 - 100 %).  So the kernel is organised around keeping copies in flight: one or two persistent CTAs per
+// and takes 58 - 59 us with the join, 83 - 85 % of the copy rate (4 contexts of up
+// to 131072 keys: 150 - 157 us, 96 - 100 %).  So the kernel is organised around keeping copies in flight: one or two persistent CTAs per
 // SM, their shared memory given to a ring of K and V tiles, and work dealt in
 // 128-key blocks: the blocks of all units, in order, are cut into equal runs,
 // one per CTA, whatever the sequences' lengths (each CTA finds its run from

@@ -65,9 +65,8 @@ __device__ __forceinline__ Unit paged_unit(const PagedParams& p, const SeqLens& 
   return u;
 }
 
-// Cost of one of a unit's blocks, for dealing the call's blocks to CTAs.  COSTS:
-// by the tiles of tile_tok / max_tiles tokens that the unit fills (the tile
-// kernel, whose blocks wait for fewer tiles' exponentials then); else 1.
+// Cost of one of a unit's blocks, for dealing the call's blocks to CTAs.  COSTS
+// (the tile kernel): by the tiles of sub_tok tokens that the unit fills; else 1.
 template <bool COSTS>
 __device__ __forceinline__ int block_cost(const PagedParams& p, const Unit& u) {
   if constexpr (!COSTS) return 1;
