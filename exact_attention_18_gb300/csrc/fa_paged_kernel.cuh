@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
       if (wt < NC) {
         const float4 r4 = *reinterpret_cast<const float4*>(red_s + wt * 4);
         const float lt = (r4.x + r4.y) + (r4.z + r4.w);
-        const bool seen = m_s[wt] != -INFINITY;
+        const bool seen = lt != 0.f;  // (NaN scores make the sum NaN, and the row with it)
         alpha_s[wt] = seen ? 1.f / lt : 0.f;
         const float l2 = seen ? m_s[wt] + log2f(lt) : -INFINITY;
         const int row = g * NC + wt;

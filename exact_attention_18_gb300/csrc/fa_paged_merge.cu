@@ -18,6 +18,13 @@ using namespace ptx;
 // of reads: descriptor, then all of a row's parts at once.  Decoding over 4
 // contexts of 131072 keys takes 161 us with a loop over the parts and 150 with
 // their reads in flight together (the main kernel alone: 150).
+// A part whose L is NaN (NaN scores) makes the row NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 constexpr int kMergeThreads = 128;
 constexpr int kMergeFew = 24;  // parts up to which a CTA takes several rows at once
 constexpr int kMergeBatch = 8;  // parts whose reads are in flight together
@@ -78,7 +85,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const Pag
         }
         float m_new = mx;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) m_new = fmaxf(m_new, l[k]);
+        for (int k = 0; k < kBatch; ++k) m_new = max_nan(m_new, l[k]);
         if (m_new == -INFINITY) continue;
         const float keep = exp2f(mx - m_new);
         mx = m_new;
@@ -139,7 +146,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const Pag
         }
         float m_new = mx;
 #pragma unroll
-        for (int k = 0; k < kMergeBatch; ++k) m_new = fmaxf(m_new, l[k]);
+        for (int k = 0; k < kMergeBatch; ++k) m_new = max_nan(m_new, l[k]);
         if (m_new == -INFINITY) continue;
         const float keep = exp2f(mx - m_new);
         mx = m_new;
@@ -161,7 +168,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const Pag
   for (int row = blockIdx.y; row < n_rows; row += gridDim.y) {
     float mx = -INFINITY;
 #pragma unroll 4
-    for (int s = 0; s < parts; ++s) mx = fmaxf(mx, q.lse_part[at(s, row)]);
+    for (int s = 0; s < parts; ++s) mx = max_nan(mx, q.lse_part[at(s, row)]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float wsum = 0.f;
     if (mx != -INFINITY) {

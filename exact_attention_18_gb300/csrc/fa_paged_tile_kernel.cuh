@@ -530,7 +530,8 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       }
       const TileSpan es = tile_span<L::kShift, T>(p, w, t, tile_tok, n);
       const int tiles = es.tiles, turn = es.turn, row_tile = es.row_tile, turns = kShare ? es.turns : 1;
-      const bool mine = have && l > 0.f;
+      // (a sum of 0: no key was seen; NaN scores make it NaN, and the row with it)
+      const bool mine = have && l != 0.f;
       // A unit's row tile whose blocks several tiles took in turns: the first
       // of them joins the others' O and statistics to its own.
       float w_own = 1.f, w_other[T - 1];
@@ -554,14 +555,14 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
               alive = warp_wait(&bar_stat[tk], (phases >> tk) & 1, abort_flag, p.err, p.wait_ns,
                                 kErrTimeoutSoftmax);
               st[k - 1] = s_stat[(tk - 1) * 128 + r];
-              if (st[k - 1].y > 0.f) top = fmaxf(top, st[k - 1].x);
+              if (st[k - 1].y != 0.f) top = fmaxf(top, st[k - 1].x);
             }
           }
           w_own = mine ? ex2(m - top) : 0.f;
           l = mine ? l * w_own : 0.f;
 #pragma unroll
           for (int k = 1; k < T; ++k) {
-            if (st[k - 1].y > 0.f) w_other[k - 1] = ex2(st[k - 1].x - top);
+            if (st[k - 1].y != 0.f) w_other[k - 1] = ex2(st[k - 1].x - top);
             l += w_other[k - 1] * st[k - 1].y;
           }
           m = top;
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       }
       const bool whole = n == w.u.n_blk;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (w.blk == 0 ? 1 : 0);
-      const bool seen = turns > 1 ? l > 0.f : mine;
+      const bool seen = turns > 1 ? l != 0.f : mine;
       const float inv_l = seen ? 1.f / l : 0.f;
       const int ta = row_tile * tile_tok, tok = w.u.tok0 + ta + rt, head = w.kvh * p.G + rh;
       // Partials lie [slot][D / 4][part_rows][4]: neighbouring lanes (rows) write
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
             for (int i = 0; i < 16; ++i) o16[i] = __float_as_uint(w_own * __uint_as_float(o16[i]));
 #pragma unroll
             for (int k = 1; k < T; ++k) {
-              const bool add = w_other[k - 1] > 0.f;
+              const bool add = w_other[k - 1] != 0.f;
               if (!__any_sync(0xffffffffu, add)) continue;  // (a tile without blocks holds an earlier unit's O)
               uint32_t x16[16];
               tmem_ld16(t_o + k * tiles * L::kTileCols + c, x16);

@@ -439,7 +439,8 @@ fa_status fa_paged_append(const void* q, int64_t q_stride, void* q_out, int64_t 
  *   partials of sequences that several CTAs share; its contents on entry do not
  *   matter, and calls that may overlap on the GPU need one each.
  * Cached keys no row sees (past the end, before the window) may hold anything,
- * NaN included.  A NaN or infinity in V at a key some row sees reaches that
+ * NaN included.  A NaN in a query, or in a key that it sees, makes that row's
+ * O and L NaN.  A NaN or infinity in V at a key some row sees reaches that
  * row, and may reach other rows of the call that share the K/V head.
  * The result depends on the lengths but not on timing: repeated calls give the
  * same bits.

@@ -138,6 +138,30 @@ def test_not_causal(fa, window, q_len):
     case(fa, [400, q_len], [q_len, q_len], 4, 2, 64, 32, "fp16", causal=False, window=window)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_len,longest", [(1, 300), (1, 40000), (40, 300), (40, 20000), (70, 20000), (300, 400), (300, 20000)])
+@pytest.mark.parametrize("where", ["q", "k"])
+def test_nan_that_is_seen(fa, D, q_len, longest, where):
+    """NaN in a query, or in a key it sees, reaches the rows concerned, however the context is cut, and no others."""
+    lens, q_lens = [longest, q_len + 90], [q_len, q_len]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, D, 32, torch.bfloat16, 80)
+    q = rnd((cu[-1], 8, D), 81, torch.bfloat16)
+    q2, k2 = q.clone(), kc.clone()
+    bad = torch.zeros(cu[-1], 8, dtype=torch.bool)
+    if where == "q":
+        q2[q_len - 1, 1, 3] = float("nan")
+        bad[q_len - 1, 1] = True
+    else:  # key 3 of the first sequence, first K/V head: seen by all its rows at position 3 or later
+        k2.view(-1, 2, D)[paged.slots(table[0], torch.tensor([3]), 32), 0, 5] = float("nan")
+        bad[:q_len, :4] = True
+    o, lse = run(fa, q2, k2, vc, table, lens, cu)
+    bad = bad.cuda()
+    assert bool(o[bad].isnan().all()) and bool(lse.T[bad].isnan().all())
+    want_o, want_l = run(fa, q, kc, vc, table, lens, cu)
+    o[bad], lse.T[bad] = want_o[bad], want_l.T[bad]
+    check(o, lse, q, kc, vc, table, lens, cu)
+
+
 @pytest.mark.parametrize("D", [16, 32, 64, 128])
 @pytest.mark.parametrize("q_len", [9, 16, 17, 33, 48])
 @pytest.mark.parametrize("window", [None, (70, -1), (1000, -1)])
