@@ -138,6 +138,67 @@ def test_not_causal(fa, window, q_len):
     case(fa, [400, q_len], [q_len, q_len], 4, 2, 64, 32, "fp16", causal=False, window=window)
 
 
+FEW_TILES = [  # what is special, arguments of the case (G = 8: 12 tokens are one tile of rows, 30 are two)
+    ("no scale", dict(scale=0.0)), ("negative", dict(scale=-0.2)), ("steep", dict(scale=1.5)),
+    ("only itself", dict(window=(0, 0))), ("both sides", dict(causal=False, window=(100, 70))),
+    ("right side", dict(causal=False, window=(-1, 3))), ("all", dict(causal=False)), ("large", dict(std=8.0)),
+]
+
+
+@pytest.mark.parametrize("D", [16, 64])
+@pytest.mark.parametrize("q_len", [12, 30])
+@pytest.mark.parametrize("kw", [kw for _, kw in FEW_TILES], ids=[n for n, _ in FEW_TILES])
+def test_units_of_few_tiles_masks_and_scales(fa, q_len, D, kw):
+    case(fa, [2500, q_len, 700], [q_len] * 3, 8, 1, D, 16, "fp16", **kw)
+
+
+@pytest.mark.parametrize("D", [32, 64])
+@pytest.mark.parametrize("q_len", [12, 30])
+@pytest.mark.parametrize("down", [False, True])
+def test_units_of_few_tiles_moving_maximum(fa, q_len, D, down):
+    """Keys that grow, or shrink, along the cache: the tiles that share a unit end with maxima far apart."""
+    lens, q_lens = [3000, 400], [q_len, q_len]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, D, 32, torch.float16, 90)
+    at = paged.slots(table[0], torch.arange(3000), 32)
+    ramp = torch.linspace(0.05, 6, 3000)
+    kc.view(-1, 2, D)[at] *= (ramp.flip(0) if down else ramp)[:, None, None].half()
+    q = rnd((cu[-1], 16, D), 91, torch.float16)
+    o, lse = run(fa, q, kc, vc, table, lens, cu)
+    check(o, lse, q, kc, vc, table, lens, cu)
+
+
+@pytest.mark.parametrize("q_len", [12, 30])
+def test_units_of_few_tiles_long_context(fa, q_len):
+    """One sequence over all CTAs, rows that see nothing beside it, the same bits twice."""
+    lens, q_lens = [60000, 5, 0], [q_len] * 3
+    kc, vc, table, cu = paged_setup([60000, 5], [q_len] * 3, 1, 64, 64, torch.bfloat16, 92)
+    table = torch.cat((table, torch.full((1, table.shape[1]), -1, dtype=torch.int32)))
+    q = rnd((cu[-1], 8, 64), 93, torch.bfloat16)
+    o, lse = run(fa, q, kc, vc, table, lens, cu)
+    check(o, lse, q, kc, vc, table, lens, cu)
+    o2, l2 = run(fa, q, kc, vc, table, lens, cu)
+    assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("q_len", [12, 30])
+def test_units_of_few_tiles_wait_runs_out(fa, q_len):
+    """Tiles that wait for one another give up together, and the next call is right."""
+    lens, q_lens = [3000, 1000], [q_len, q_len]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, 64, 32, torch.bfloat16, 94)
+    q = rnd((cu[-1], 16, 64), 95, torch.bfloat16)
+    kcg, vcg = on_gpu(kc, vc)
+    assert fa.fa_check_device_errors(None) == 0
+    fa.fa_set_wait_limit_ns(1)
+    try:
+        fa.forward_paged(q.cuda(), kcg, vcg, ints(table), ints(lens), ints(cu), q_len, 3000)
+        st = fa.fa_check_device_errors(None)
+    finally:
+        fa.fa_set_wait_limit_ns(0)
+    assert fa.STATUS[st] == "FA_ERR_TIMEOUT"
+    o, lse = run(fa, q, kc, vc, table, lens, cu)
+    check(o, lse, q, kc, vc, table, lens, cu)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("q_len,longest", [(1, 300), (1, 40000), (40, 300), (40, 20000), (70, 20000), (300, 400), (300, 20000)])
 @pytest.mark.parametrize("where", ["q", "k"])
