@@ -12,10 +12,10 @@
 // and sixteen softmax warps hide more of each other's latency than eight).
 //
 // At D = 128 the tensor core bounds it: chunks of 2048 tokens over 16384 keys,
-// 32 heads on 4, take 588 us with the join, 1.53 PFLOP/s, at the power cap (557 before it
-// bites).  At D = 64 the chain of
-// products and exponentials does: ragged chunks of 16 heads take 85 us, the
-// tensor pipes active a third of the time, DRAM a fifth.
+// 32 heads on 4, take 588 us with the join, 1.53 PFLOP/s, at the power cap (557
+// before it bites).  At D = 64 the chain of products and exponentials does:
+// ragged chunks of 16 heads take 85 us, the tensor pipes active a third of the
+// time, DRAM a fifth.
 //
 // Units, blocks, runs and partials are fa_paged_kernel.cuh's: one persistent
 // CTA per SM takes a run of blocks, equal to the others' in cost.  Within a unit

@@ -338,6 +338,26 @@ def test_many_sequences(fa):
     case(fa, lens, q_lens, 2, 1, 32, 16, "fp16")
 
 
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("H,hk", [(1, 1), (8, 1), (128, 1)])
+def test_one_token_under_a_loose_bound(fa, D, H, hk):
+    """One sequence, one token, a bound of many: the kernel for chunks takes it."""
+    lens, q_lens = [5000], [1]
+    kc, vc, table, cu = paged_setup(lens, q_lens, hk, D, 16, torch.bfloat16, 96)
+    q = rnd((1, H, D), 97, torch.bfloat16)
+    o, lse = run(fa, q, kc, vc, table, lens, cu, max_q=2000, max_k=100000)
+    check(o, lse, q, kc, vc, table, lens, cu)
+
+
+@pytest.mark.parametrize("batch", [250, 650])
+@pytest.mark.parametrize("short", [0, 1, 5])
+def test_many_sequences_beside_long_ones(fa, batch, short):
+    """Many sequences of few (or no) new tokens behind two of many, more of them than a CTA has threads."""
+    q_lens = [130] + [short] * (batch - 2) + [90]
+    lens = [400] + [20 + i % 50 for i in range(batch - 2)] + [95]
+    case(fa, lens, q_lens, 4, 1, 64, 16, "fp16")
+
+
 def test_offsets_past_32_bits(fa):
     """Pages beyond 2^32 elements of the cache."""
     hk, D, page, pages = 2, 128, 256, 70000  # 4.6e9 elements a cache, one buffer for K and V
