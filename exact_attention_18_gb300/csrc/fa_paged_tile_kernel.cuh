@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   uint64_t* bar_pfull = bar_sfull + T;   // [T] P_t stored, O_t rescaled
   uint64_t* bar_ofinal = bar_pfull + T;  // [T] the segment's last P_t V done
   uint64_t* bar_stat = bar_ofinal + T;   // [T] this tile's share of a split unit can be joined
-  uint64_t* bar_freed = bar_stat + T;    // [T] row tile's other shares were joined
+  uint64_t* bar_freed = bar_stat + T;    // [T] this tile's share was joined
   uint64_t* bar_vtmp = bar_freed + T;    // a V block that still needs rows cleared has landed
   uint64_t* bar_drain = bar_vtmp + 1;    // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 2);
@@ -539,12 +539,19 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
 #pragma unroll
       for (int k = 1; k < T; ++k) w_other[k - 1] = 0.f;
       if (turns > 1) {
-        const unsigned phases = s_walk[warp].phases;  // bit t: of bar_stat[t], bit T + t: of bar_freed[t]
+        // Tile t >= tiles gives its share on bar_stat[t] and goes on when its row
+        // tile's joiner has released it on bar_freed[t].  A pair of its own each, so
+        // that no tile skips a phase it later waits past: with one bar_freed a row
+        // tile, a tile whose row tile changed from unit to unit took the phase
+        // before last for the last (the same parity) and ran ahead.  The joiner of
+        // bar_stat[3] is tile 0 or 1; its waits in this order (k = 1, 2, 3) keep the
+        // one from passing the other's phase: tile 1 gives bar_stat[1] only after
+        // it has seen bar_stat[3].
+        const unsigned phases = s_walk[warp].phases;  // bit t: of bar_stat[t] and bar_freed[t]
         if (turn > 0) {
           s_stat[(t - 1) * 128 + r] = make_float2(m, mine ? l : 0.f);
           warp_arrive(&bar_stat[t]);
-          alive = warp_wait(&bar_freed[row_tile], (phases >> (T + row_tile)) & 1, abort_flag, p.err, p.wait_ns,
-                            kErrTimeoutSoftmax);
+          alive = warp_wait(&bar_freed[t], (phases >> t) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
         } else {
           float2 st[T - 1];
           float top = mine ? m : -INFINITY;
@@ -571,7 +578,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         if (!alive) break;
         tc_fence_after();
         __syncwarp();
-        if (lane == 0) s_walk[warp].phases = phases ^ ((1u << T) - (1u << tiles)) ^ (((1u << tiles) - 1) << T);
+        if (lane == 0) s_walk[warp].phases = phases ^ ((1u << T) - (1u << tiles));
         __syncwarp();
       }
       const bool whole = n == w.u.n_blk;
@@ -622,7 +629,8 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           else p.lse_part[static_cast<int64_t>(slot) * p.part_rows + prow] = l2;
         }
       }
-      if (turns > 1 && turn == 0) warp_arrive(&bar_freed[row_tile]);
+      if (turns > 1 && turn == 0)
+        for (int k = 1; k < turns; ++k) warp_arrive(&bar_freed[k * tiles + row_tile]);
       if (!whole && w.blk == 0 && threadIdx.x == 0) {
         const long long last = s_start->at + s_start->left - w.left + static_cast<long long>(w.u.n_blk - 1) * w.cost;
         p.desc[blockIdx.x] = make_int4(w.u.tok0, w.u.n_tok, w.kvh, static_cast<int>(last / s_start->share));

@@ -1,0 +1,48 @@
+"""Paged attention of batches whose sequences differ in kind: prompts of different sizes beside one another and
+beside single tokens, loose bounds, and what must not reach a row from elsewhere.
+
+Error bounds are those of tests/test_paged.py (``check``).
+"""
+import pytest
+import torch
+
+from tests.test_paged import case, fa  # noqa: F401  (fa is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture
+def wait_limit(fa):  # noqa: F811
+    """A pipeline wait that is never satisfied ends after 0.2 s."""
+    fa.fa_set_wait_limit_ns(200_000_000)
+    yield
+    fa.fa_set_wait_limit_ns(0)
+
+
+# ------------------------------------------------- prompts that fill different numbers of row tiles
+@pytest.mark.parametrize("D", [16, 32, 64])
+def test_short_prompts_of_one_and_two_tiles(fa, wait_limit, D):  # noqa: F811
+    """Units of two row tiles and of one by turns, of a block or two of keys each: the tiles that share a unit's
+    blocks change partners from unit to unit."""
+    q_lens = [40, 20] * 32
+    for _ in range(3):
+        case(fa, q_lens, q_lens, 32, 8, D, 16, "bf16")
+
+
+@pytest.mark.parametrize("D", [16, 32, 64])
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_random_prompts(fa, wait_limit, D, seed):  # noqa: F811
+    """One to four row tiles a unit in any order, one to a dozen blocks."""
+    g = torch.Generator().manual_seed(seed)
+    q_lens = torch.randint(17, 200, (64,), generator=g).tolist()
+    lens = [n + int(x) for n, x in zip(q_lens, torch.randint(0, 2 + 300 * seed, (64,), generator=g))]
+    case(fa, lens, q_lens, 32, 8, D, 16, "fp16")
+
+
+@pytest.mark.parametrize("D", [16, 64])
+def test_one_two_and_three_tiles_in_a_run(fa, wait_limit, D):  # noqa: F811
+    """Every order of one, two, three and four row tiles, of units of one to eight blocks, few CTAs' worth."""
+    g = torch.Generator().manual_seed(7)
+    q_lens = [(17, 33, 65, 97)[int(x)] for x in torch.randint(0, 4, (300,), generator=g)]
+    lens = [n + int(x) for n, x in zip(q_lens, torch.randint(0, 400, (300,), generator=g))]
+    case(fa, lens, q_lens, 4, 1, D, 16, "bf16")
