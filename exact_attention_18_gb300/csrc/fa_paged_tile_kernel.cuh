@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       if (!alive) break;
       // ------------------------------------------------------------ segment's end
       w = s_walk[warp].w;
+      __syncwarp();  // (a tile without blocks meets no other before lane 0 parks the next segment's)
       n = w.seg_len();
       const bool have = end > beg;
       if (have) {

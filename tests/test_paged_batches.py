@@ -46,3 +46,11 @@ def test_one_two_and_three_tiles_in_a_run(fa, wait_limit, D):  # noqa: F811
     q_lens = [(17, 33, 65, 97)[int(x)] for x in torch.randint(0, 4, (300,), generator=g)]
     lens = [n + int(x) for n, x in zip(q_lens, torch.randint(0, 400, (300,), generator=g))]
     case(fa, lens, q_lens, 4, 1, D, 16, "bf16")
+
+
+@pytest.mark.parametrize("D,tokens", [(128, 9), (128, 32), (64, 80)])
+def test_tiles_without_blocks(fa, wait_limit, D, tokens):  # noqa: F811
+    """Many units in a row that leave one of the CTA's tiles nothing to do (one row tile of two, three of four)."""
+    g = torch.Generator().manual_seed(8)
+    lens = [tokens + int(x) for x in torch.randint(0, 300, (400,), generator=g)]
+    case(fa, lens, [tokens] * 400, 4, 1, D, 16, "fp16")
