@@ -93,7 +93,7 @@ struct PagedParams {
   int small;             // the cost of all blocks of the call is below 2^31 / 304
   int sub_tok;           // tile kernel: tokens of one of a unit's tiles
   unsigned costs;        // tile kernel: byte i is the cost of a block of a unit that fills i + 1 tiles
-  int after_tile;        // few-row kernel: launched behind the tile kernel of the same call
+  int after_tile;        // few-row kernel: launched behind the tile kernel of the same call, whose CTAs fill the SMs
   float scale_log2;
   int part_rows;         // rows of a partial's slot
   float* o_part;         // [2 grid][part_rows x D] fp32, laid out as in PagedParts

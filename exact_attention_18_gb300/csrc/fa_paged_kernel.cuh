@@ -171,19 +171,18 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
   int* s_off = reinterpret_cast<int*>(s_red + 4 * N);     // [N] output row of row n after its unit's first
   short* s_tok = reinterpret_cast<short*>(s_off + N);     // [N] token of row n
 
-  // After the tile kernel of the same call there is nothing to wait for: that
-  // kernel waited for all before it, and the two share no output; but this grid
-  // must not complete before that one (the wait at the end).  Where no sequence
-  // is short enough for this kernel, it leaves before any set-up.
+  // Behind the tile kernel of the same call: where no sequence is short enough
+  // for this kernel, it leaves before any set-up.  (Its CTAs start as that
+  // kernel's end, so there is no time to fill with set-up before the wait.)
   SeqLens own{0, 0, 0};
   const bool all_known = p.after_tile && p.batch <= L::kThreads;  // a thread each
   if (all_known) {
+    griddep_wait();
     if (static_cast<int>(threadIdx.x) < p.batch) own = seq_lens(p, threadIdx.x);
     const int n = own.e - own.a;
     if (!__syncthreads_or(n > 0 && n <= p.tok_hi)) {
       if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
       griddep_launch_dependents();
-      griddep_wait();
       return;
     }
   }
@@ -211,8 +210,8 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  // (Behind other kernels nothing of the caller's was touched up to here.)
-  if (!p.after_tile) griddep_wait();
+  // Up to here nothing of the caller's was touched (or this grid has waited already).
+  griddep_wait();
   griddep_launch_dependents();
   if (!all_known) {
     int per;
@@ -590,7 +589,6 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
-  if (p.after_tile) griddep_wait();
 }
 
 namespace {

@@ -6,7 +6,8 @@ Error bounds are those of tests/test_paged.py (``check``).
 import pytest
 import torch
 
-from tests.test_paged import case, fa  # noqa: F401  (fa is a fixture)
+from tests.test_paged import case, check, fa  # noqa: F401  (fa is a fixture)
+from tests.test_rope import ints, on_gpu, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +55,50 @@ def test_tiles_without_blocks(fa, wait_limit, D, tokens):  # noqa: F811
     g = torch.Generator().manual_seed(8)
     lens = [tokens + int(x) for x in torch.randint(0, 300, (400,), generator=g)]
     case(fa, lens, [tokens] * 400, 4, 1, D, 16, "fp16")
+
+
+# ------------------------------------------------- chunks beside single tokens
+@pytest.mark.parametrize("D", [64, 128])
+def test_mixed_step_replayed_with_new_tables(fa, D):  # noqa: F811
+    """A chunk beside single tokens, append and attention in one graph, the lengths and the block table written by a
+    kernel of the graph right before: each replay moves the sequences to other pages and lengths."""
+    H, hk, page, q_lens = 8, 2, 16, [150, 1, 1, 3, 1]
+    cu = [0, 150, 151, 152, 155, 156]
+    g = torch.Generator().manual_seed(50 + D)
+    per = 40  # pages a sequence
+    pages = 5 * per + 3
+    kc, vc = (rnd((pages, page, hk, D), 51 + i, torch.bfloat16) for i in range(2))
+    kcg, vcg = on_gpu(kc, vc)
+    x = rnd((156, H + 2 * hk, D), 53, torch.bfloat16).cuda()
+    lens_in, table_in = ints([0] * 5), ints(torch.zeros(5, per))
+    lens, table, cug = torch.empty_like(lens_in), torch.empty_like(table_in), ints(cu)
+    steps = fa.rope_steps(fa.rope_inv_freq(D)[0])
+
+    def step():
+        torch.add(lens_in, 0, out=lens)
+        torch.add(table_in, 0, out=table)
+        q = fa.paged_append(x[:, H:H + hk], x[:, H + hk:], kcg, vcg, table, lens, cug, 150, q=x[:, :H], steps=steps)
+        return q, *fa.forward_paged(q, kcg, vcg, table, lens, cug, 150, per * page)
+
+    def deal():
+        now = [n + int(v) for n, v in zip(q_lens, torch.randint(0, 480, (5,), generator=g))]
+        pick = torch.randperm(pages, generator=g)[:5 * per].view(5, per)
+        lens_in.copy_(ints(now))
+        table_in.copy_(ints(pick))
+        return now, pick
+
+    deal()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q, o, lse = step()
+    for _ in range(6):
+        now, pick = deal()
+        graph.replay()
+        graph.replay()  # (the second finds what the first left in the caches)
+        assert fa.fa_check_device_errors(None) == 0
+        check(o, lse, q.cpu(), kcg.cpu(), vcg.cpu(), pick, now, cu)
