@@ -6,8 +6,9 @@ Error bounds are those of tests/test_paged.py (``check``).
 import pytest
 import torch
 
-from tests.test_paged import case, check, fa  # noqa: F401  (fa is a fixture)
-from tests.test_rope import ints, on_gpu, rnd
+from oracle import paged
+from tests.test_paged import case, check, fa, run  # noqa: F401  (fa is a fixture)
+from tests.test_rope import ints, on_gpu, paged_setup, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -102,3 +103,35 @@ def test_mixed_step_replayed_with_new_tables(fa, D):  # noqa: F811
         graph.replay()  # (the second finds what the first left in the caches)
         assert fa.fa_check_device_errors(None) == 0
         check(o, lse, q.cpu(), kcg.cpu(), vcg.cpu(), pick, now, cu)
+
+
+# ------------------------------------------------- what other rows must not do
+def test_other_sequences_queries_do_not_reach_a_row(fa):  # noqa: F811
+    """The query rows of a unit that are not its own (here the next sequence's) have no say in its rows' running
+    maximum: whatever they are, the first sequence's bits stay.
+
+    Scores 1/64 and 131/16 with this scale differ by 8 powers of two so closely that a test of the rounded sum
+    lets the maximum stay and one of the rounded terms moves it, so any vote from elsewhere shows in L.
+    """
+    scale, low, high = float.fromhex("0x1.5b6d58p-1"), 1 / 64, 131 / 16
+    hk, D, page, n = 8, 16, 128, 128 * 100
+    lens, q_lens = [n, 20], [1, 8]
+    kc, vc, table, cu = paged_setup(lens, q_lens, hk, D, page, torch.bfloat16, 60)
+    kc.zero_()
+    at = paged.slots(table[0], torch.arange(n), page)
+    k = -torch.randint(1, 192, (n, hk), generator=torch.Generator().manual_seed(61)) / 64
+    rise = torch.randint(0, 2, (n // 128,), generator=torch.Generator().manual_seed(62)).bool()
+    k.view(-1, 128, hk)[:, 5] = torch.where(rise, high, low)[:, None]
+    rows = torch.zeros(n, hk, D)
+    rows[..., 0] = k
+    rows.view(-1, 128, hk, D)[rise, :, :, 5] = 2.0
+    kc.view(-1, hk, D)[at] = rows.bfloat16()
+    q = torch.zeros(9, hk, D, dtype=torch.bfloat16)
+    q[0, :, 0] = 1.0
+    outs = []
+    for other in (0.0, 100.0, -100.0):
+        q[1:, :, 5] = other
+        outs.append(run(fa, q, kc, vc, table, lens, cu, scale=scale))
+        check(*outs[-1], q, kc, vc, table, lens, cu, scale=scale)
+    for o, lse in outs[1:]:
+        assert torch.equal(o[0], outs[0][0][0]) and torch.equal(lse[:, 0], outs[0][1][:, 0])
