@@ -405,7 +405,8 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     // of 2048: 668 us with a copy of its own, 723 in place).
     constexpr bool kMaskInPlace = D <= 64;
     constexpr bool kShare = T == 4;  // tiles may share a unit's row tile
-    // In place, a scale of 0 makes every visible score 0 (0 times a hidden key's infinity would not be -inf).
+    // In place, a scale of 0 is applied ahead of the mask (0 times a hidden key's
+    // infinity would not be -inf); a NaN stays one.
     const bool zero_scale = kMaskInPlace && sl2 == 0.f;
     const float ce = zero_scale ? 1.f : sl2;
     const float2 c2 = make_float2(ce, ce);
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         if constexpr (kMaskInPlace) {
           if (zero_scale) {
 #pragma unroll
-            for (int c = 0; c < BN; ++c) sr[c] = 0;
+            for (int c = 0; c < BN; ++c) sr[c] = __float_as_uint(0.f * __uint_as_float(sr[c]));
           }
           if (cut) {
 #pragma unroll

@@ -135,3 +135,28 @@ def test_other_sequences_queries_do_not_reach_a_row(fa):  # noqa: F811
         check(*outs[-1], q, kc, vc, table, lens, cu, scale=scale)
     for o, lse in outs[1:]:
         assert torch.equal(o[0], outs[0][0][0]) and torch.equal(lse[:, 0], outs[0][1][:, 0])
+
+
+# ------------------------------------------------- special values that a row sees
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("q_len", [1, 20, 40, 300])
+@pytest.mark.parametrize("where", ["q", "k"])
+def test_nan_under_a_scale_of_zero(fa, D, q_len, where):  # noqa: F811
+    """0 times NaN: the rows concerned are NaN, whichever kernel takes them, the others the mean of their values."""
+    lens, q_lens = [700, q_len + 90], [q_len, q_len]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, D, 32, torch.bfloat16, 82)
+    q = rnd((cu[-1], 8, D), 83, torch.bfloat16)
+    q2, k2 = q.clone(), kc.clone()
+    bad = torch.zeros(cu[-1], 8, dtype=torch.bool)
+    if where == "q":
+        q2[q_len - 1, 1, 3] = float("nan")
+        bad[q_len - 1, 1] = True
+    else:
+        k2.view(-1, 2, D)[paged.slots(table[0], torch.tensor([3]), 32), 0, 5] = float("nan")
+        bad[:q_len, :4] = True
+    o, lse = run(fa, q2, k2, vc, table, lens, cu, scale=0.0)
+    bad = bad.cuda()
+    assert bool(o[bad].isnan().all()) and bool(lse.T[bad].isnan().all())
+    want_o, want_l = run(fa, q, kc, vc, table, lens, cu, scale=0.0)
+    o[bad], lse.T[bad] = want_o[bad], want_l.T[bad]
+    check(o, lse, q, kc, vc, table, lens, cu, scale=0.0)
