@@ -404,8 +404,10 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
       const int full_hi = min(u.kv_len, u.pos0 + 1 + p.win_right);
 #pragma unroll
       for (int k = 0; k < NC; ++k) l[k] = 0.f;
-      if (wt < NC) m_s[wt] = -INFINITY;  // read and written by this thread only
-      bool exact_max = true;  // the first block, a cut block and the one after it take the block maximum
+      if (wt < NC) m_s[wt] = -INFINITY;
+      // The first block, a cut block, the one after it, and any block as long as
+      // a row has seen no score above -inf take the block maximum.
+      bool exact_max = true;
       for (int jb = 0; jb < n; ++jb, ++i) {
         bool ok = warp_wait(&bar_sfull[i & 1], (i >> 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
         // O(i-2) is done (S(i) was issued after it).  Waiting for it keeps this
@@ -434,6 +436,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
           }
         }
         bool need = exact_max || cut;
+        exact_max = cut;
         if (!need) {
           float mx = -INFINITY;
 #pragma unroll
@@ -471,11 +474,18 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
               a = ex2(mo - mn);
               moved = true;
             }
-            m_s[wt] = mn;
+            m_s[wt] = is_row ? mn : 0.f;
             negm_s[wt] = !is_row ? -INFINITY : (mn == -INFINITY ? 0.f : -mn);
             alpha_s[wt] = a;
           }
           moved = !named_sync_and(bar_id, 128, !moved);
+          if (jb + 1 < n) {
+#pragma unroll
+            for (int k = 0; k < NC; k += 4) {
+              const float4 m4 = *reinterpret_cast<const float4*>(m_s + k);
+              exact_max |= fminf(fminf(m4.x, m4.y), fminf(m4.z, m4.w)) == -INFINITY;
+            }
+          }
           if (moved && jb > 0) {
 #pragma unroll
             for (int k = 0; k < NC; ++k) l[k] *= alpha_s[k];
@@ -497,7 +507,6 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
             tmem_st_wait();
           }
         }
-        exact_max = cut;
         // P~ = 2^(c s - m), 16-bit, into the key's row of the P^T tile; the
         // running sums take the unrounded values.
         uint8_t* prow = p_tile + (i & 1) * GP::kTileBytes;

@@ -160,3 +160,20 @@ def test_nan_under_a_scale_of_zero(fa, D, q_len, where):  # noqa: F811
     want_o, want_l = run(fa, q, kc, vc, table, lens, cu, scale=0.0)
     o[bad], lse.T[bad] = want_o[bad], want_l.T[bad]
     check(o, lse, q, kc, vc, table, lens, cu, scale=0.0)
+
+
+@pytest.mark.parametrize("H,D", [(2, 64), (16, 128), (256, 64)])
+def test_blocks_whose_scores_are_all_minus_infinity(fa, H, D):  # noqa: F811
+    """Keys that overflowed to -infinity, whole blocks of them before others: they weigh nothing, and the rest of
+    the sequence is what it is without them."""
+    hk, page, blocks = 2, 128, 400
+    n = 128 * blocks
+    kc, vc, table, cu = paged_setup([n], [1], hk, D, page, torch.float16, 84)
+    keep = torch.rand(blocks, generator=torch.Generator().manual_seed(85)) < 0.4
+    keep[-1] = True
+    q = rnd((1, H, D), 86, torch.float16)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    kc[table[0, :blocks][~keep].long(), :, :, 0] = float("-inf")
+    o, lse = run(fa, q, kc, vc, table, [n], cu)
+    kept = table[:, :blocks][:, keep]
+    check(o, lse, q, kc, vc, kept, [128 * int(keep.sum())], cu)
