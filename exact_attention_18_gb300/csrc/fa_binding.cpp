@@ -163,6 +163,16 @@ std::mutex& scratch_order() {
   return *m;
 }
 
+// The interpreter's lock, given up for the scope's life.  Inside it nothing of a
+// tensor is asked for: its pointers can throw (no storage behind it) or allocate
+// (a lazy copy), so they are read before.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // Calls f() and turns its exceptions into Python's.
 template <typename F>
 PyObject* guarded(F f) {
@@ -216,13 +226,15 @@ PyObject* rope(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     const bool back = a.flag(0), inter = a.flag(5);
     const float mag = static_cast<float>(a.real(6));
     void* stream = c10::cuda::getCurrentCUDAStream().stream();
+    const void *q_at = q.const_data_ptr(), *k_at = k.const_data_ptr();
+    void *qo_at = q_out.mutable_data_ptr(), *ko_at = k_out.mutable_data_ptr();
     fa_status st;
-    Py_BEGIN_ALLOW_THREADS
-    st = (back ? fa_rope_bwd : fa_rope)(q.const_data_ptr(), qs, k.const_data_ptr(), ks, q_out.mutable_data_ptr(), qos,
-                                        k_out.mutable_data_ptr(), kos, static_cast<const int32_t*>(p),
-                                        static_cast<const uint64_t*>(s), T, H, hk, D, 2 * pairs, inter, mag, code,
-                                        stream);
-    Py_END_ALLOW_THREADS
+    {
+      const Unlocked unlocked;
+      st = (back ? fa_rope_bwd : fa_rope)(q_at, qs, k_at, ks, qo_at, qos, ko_at, kos, static_cast<const int32_t*>(p),
+                                          static_cast<const uint64_t*>(s), T, H, hk, D, 2 * pairs, inter, mag, code,
+                                          stream);
+    }
     return st == FA_OK ? pair(q_out, k_out) : PyLong_FromLong(st);
   });
 }
@@ -264,14 +276,16 @@ PyObject* paged_append(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     const bool inter = a.flag(11);
     const float mag = static_cast<float>(a.real(12));
     void* stream = c10::cuda::getCurrentCUDAStream().stream();
+    const void *q_at = q ? q->const_data_ptr() : nullptr, *k_at = k.const_data_ptr(), *v_at = v.const_data_ptr(),
+               *cu_at = cu.const_data_ptr();
+    void* qo_at = q ? q_out.mutable_data_ptr() : nullptr;
     fa_status st;
-    Py_BEGIN_ALLOW_THREADS
-    st = fa_paged_append(q ? q->const_data_ptr() : nullptr, qs, q ? q_out.mutable_data_ptr() : nullptr, qos,
-                         k.const_data_ptr(), ks, v.const_data_ptr(), vs, &cache,
-                         static_cast<const int32_t*>(cu.const_data_ptr()), static_cast<const int32_t*>(p),
-                         static_cast<const uint64_t*>(s), batch, max_len, T, H, hk, D, 2 * pairs, inter, mag, code,
-                         stream);
-    Py_END_ALLOW_THREADS
+    {
+      const Unlocked unlocked;
+      st = fa_paged_append(q_at, qs, qo_at, qos, k_at, ks, v_at, vs, &cache, static_cast<const int32_t*>(cu_at),
+                           static_cast<const int32_t*>(p), static_cast<const uint64_t*>(s), batch, max_len, T, H, hk, D,
+                           2 * pairs, inter, mag, code, stream);
+    }
     if (st != FA_OK) return PyLong_FromLong(st);
     if (q) return THPVariable_Wrap(q_out);
     Py_RETURN_NONE;
@@ -311,14 +325,17 @@ PyObject* forward_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     const int64_t need = static_cast<int64_t>(fa_fwd_paged_workspace_size(batch, max_q, max_k, H, hk, D));
     const Tensor work = ws ? *ws : scratch(need, q, stream);
     const Tensor out = o ? *o : empty(q.sizes(), type, q), lse = l ? *l : empty({H, T}, at::kFloat, q);
+    const void *q_at = q.const_data_ptr(), *cu_at = cu.const_data_ptr();
+    void *o_at = out.mutable_data_ptr(), *l_at = lse.mutable_data_ptr(), *work_at = work.mutable_data_ptr();
+    const size_t work_bytes = work.nbytes();
     fa_status st;
-    Py_BEGIN_ALLOW_THREADS
-    if (!ws) scratch_order().lock();
-    st = fa_fwd_paged(q.const_data_ptr(), out.mutable_data_ptr(), static_cast<float*>(lse.mutable_data_ptr()), &cache,
-                      static_cast<const int32_t*>(cu.const_data_ptr()), batch, max_q, max_k, T, H, hk, D, causal, left,
-                      right, scale, code, work.mutable_data_ptr(), work.nbytes(), stream);
-    if (!ws) scratch_order().unlock();
-    Py_END_ALLOW_THREADS
+    {
+      const Unlocked unlocked;
+      std::unique_lock<std::mutex> turn(scratch_order(), std::defer_lock);  // (ends before the interpreter's is taken)
+      if (!ws) turn.lock();
+      st = fa_fwd_paged(q_at, o_at, static_cast<float*>(l_at), &cache, static_cast<const int32_t*>(cu_at), batch, max_q,
+                        max_k, T, H, hk, D, causal, left, right, scale, code, work_at, work_bytes, stream);
+    }
     return st == FA_OK ? pair(out, lse) : PyLong_FromLong(st);
   });
 }

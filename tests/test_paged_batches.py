@@ -177,3 +177,41 @@ def test_blocks_whose_scores_are_all_minus_infinity(fa, H, D):  # noqa: F811
     o, lse = run(fa, q, kc, vc, table, [n], cu)
     kept = table[:, :blocks][:, keep]
     check(o, lse, q, kc, vc, kept, [128 * int(keep.sum())], cu)
+
+
+# ------------------------------------------------- tensors without storage
+def test_tensors_without_storage_are_refused(fa):  # noqa: F811
+    """Tensors that stand for others while a program is traced have no memory behind them: a Python exception, and
+    the next call, which takes the same locks, works."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    lens, q_lens = [40, 33], [2, 1]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, 64, 16, torch.float16, 87)
+    kcg, vcg = on_gpu(kc, vc)
+    q = rnd((3, 4, 64), 88, torch.float16)
+    qg, kg, pos = q.cuda(), rnd((3, 2, 64), 89, torch.float16).cuda(), ints([0, 1, 2])
+    steps = fa.rope_steps(fa.rope_inv_freq(64)[0])
+    mode = FakeTensorMode()
+    fake, fake_k = mode.from_tensor(qg), mode.from_tensor(kg)
+    args = (ints(table), ints(lens), ints(cu), 2)
+
+    def traced():
+        with mode:
+            fa.rope(fake, fake_k, mode.from_tensor(pos), mode.from_tensor(steps))
+
+    for call in (lambda: fa.rope(fake, kg, pos, steps), lambda: fa.rope(qg, fake_k, pos, steps),
+                 lambda: fa.rope(qg, kg, pos, steps, q_out=fake), traced,
+                 lambda: fa.paged_append(fake_k, kg, kcg, vcg, *args), lambda: fa.paged_append(kg, fake_k, kcg, vcg, *args),
+                 lambda: fa.paged_append(kg, kg, kcg, vcg, *args, q=fake),
+                 lambda: fa.forward_paged(fake, kcg, vcg, *args, 40),
+                 lambda: fa.forward_paged(qg, kcg, vcg, *args, 40, out=fake)):
+        with pytest.raises(Exception):
+            call()
+    assert torch.equal(kcg.cpu(), kc) and torch.equal(vcg.cpu(), vc)
+    for _ in range(2):
+        o, lse = fa.forward_paged(qg, kcg, vcg, *args, 40)
+    assert fa.fa_check_device_errors(None) == 0
+    check(o, lse, q, kc, vc, table, lens, cu)
+    lazy = torch._lazy_clone(qg)  # shares its memory until one side is written
+    qo, _ = fa.rope(lazy, kg, pos, steps, q_out=lazy)
+    want, _ = fa.rope(qg, kg, pos, steps)
+    assert torch.equal(qo, want) and torch.equal(qg.cpu(), q)
