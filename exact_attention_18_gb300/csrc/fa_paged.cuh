@@ -57,6 +57,7 @@ struct RopeParams {
   int log2_items;        // threads a row, log2 (set by the launcher)
   int tok_per_cta;       // set by the launcher
   int tiles;             // append: CTAs per sequence (set by the launcher)
+  int batch;             // append: sequences (set by the launcher)
   float mag, mag_sin;    // factors of cos and sin (mag_sin = -mag turns back)
   // append
   const int* cu_seqlens;

@@ -215,3 +215,73 @@ def test_tensors_without_storage_are_refused(fa):  # noqa: F811
     qo, _ = fa.rope(lazy, kg, pos, steps, q_out=lazy)
     want, _ = fa.rope(qg, kg, pos, steps)
     assert torch.equal(qo, want) and torch.equal(qg.cpu(), q)
+
+
+# ------------------------------------------------- loose bounds on the new tokens
+def appended(fa, q_lens, lens, H, hk, D, max_seqlen, page=16, seed=70):  # noqa: F811
+    """An append of these batches against the rotation alone, row for row and slot for slot (the same bits)."""
+    T, n_pages = sum(q_lens), [-(-n // page) for n in lens]
+    first = torch.tensor([0] + n_pages).cumsum(0)
+    table = torch.zeros(len(lens), max(n_pages), dtype=torch.int32)
+    for b, n in enumerate(n_pages):
+        table[b, :n] = torch.arange(first[b], first[b] + n)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(T + 2, H + 2 * hk, D, generator=g, device="cuda").half()
+    kc, vc = (torch.full((int(first[-1]), page, hk, D), 9.0, dtype=torch.float16, device="cuda") for _ in range(2))
+    cu = torch.tensor([0] + q_lens).cumsum(0)
+    steps = fa.rope_steps(fa.rope_inv_freq(D)[0])
+    q_out = torch.full((T + 2, H, D), 7.0, dtype=torch.float16, device="cuda")
+    fa.paged_append(x[:, H:H + hk], x[:, H + hk:], kc, vc, ints(table), ints(lens), ints(cu), max_seqlen, q=x[:, :H],
+                    steps=steps, q_out=q_out)
+    assert fa.fa_check_device_errors(None) == 0
+    seq = torch.repeat_interleave(torch.arange(len(lens)), torch.tensor(q_lens))
+    pos = torch.arange(T) - cu[seq + 1] + torch.tensor(lens)[seq]
+    qr, kr = fa.rope(x[:T, :H], x[:T, H:H + hk], ints(pos), steps)
+    assert torch.equal(q_out[:T], qr) and bool((q_out[T:] == 7).all())
+    at = (first[seq] * page + pos).cuda()
+    for cache, rows in ((kc, kr), (vc, x[:T, H + hk:])):
+        flat = cache.view(-1, hk, D)
+        assert torch.equal(flat[at], rows)
+        left = torch.ones(flat.shape[0], dtype=torch.bool, device="cuda")
+        left[at] = False
+        assert bool((flat[left] == 9).all())
+
+
+@pytest.mark.parametrize("H,hk,D", [(4, 1, 64), (32, 4, 128), (2, 2, 16)])
+@pytest.mark.parametrize("q_lens", [[1] * 600, [500] + [1] * 63, [1] * 40 + [700] + [2] * 40, [0, 3, 0, 0, 900, 0, 5, 0],
+                                    [0] * 30 + [250] + [0] * 30])
+@pytest.mark.parametrize("bound", [None, (1 << 31) - 1])
+def test_append_under_loose_bounds(fa, H, hk, D, q_lens, bound):  # noqa: F811
+    """Many short sequences under a loose bound, one long beside many short ones, empty ones anywhere."""
+    g = torch.Generator().manual_seed(71)
+    lens = [n + int(v) for n, v in zip(q_lens, torch.randint(0, 60, (len(q_lens),), generator=g))]
+    appended(fa, q_lens, lens, H, hk, D, bound or max(q_lens))
+
+
+def test_append_of_a_very_large_batch_under_a_loose_bound(fa):  # noqa: F811
+    """Sequences times the CTAs that the longest may need pass 2^31 here."""
+    appended(fa, [1] * 47000, [1 + i % 16 for i in range(47000)], 62, 1, 128, 1 << 20)
+
+
+@pytest.mark.parametrize("bound", [40, (1 << 31) - 1])
+def test_append_reports_every_bad_sequence_under_a_loose_bound(fa, bound):  # noqa: F811
+    """A cache length below the new tokens, or past the table, is found and left out, the others appended."""
+    q_lens, lens = [40] + [1] * 60, [40] + [5] * 60
+    kc, vc, table, cu = paged_setup(lens, q_lens, 1, 64, 16, torch.float16, 72)
+    k, v = rnd((cu[-1], 1, 64), 73, torch.float16), rnd((cu[-1], 1, 64), 74, torch.float16)
+    for b, n in ((0, 39), (7, 0), (60, -3), (33, 16 * table.shape[1] + 1)):
+        now = list(lens)
+        now[b] = n
+        kcg, vcg = on_gpu(kc, vc)
+        fa.paged_append(k.cuda(), v.cuda(), kcg, vcg, ints(table), ints(now), ints(cu), bound)
+        assert fa.STATUS[fa.fa_check_device_errors(None)] == "FA_ERR_INVALID_ARG"
+        want = kc.clone()
+        for s in range(61):
+            if s != b:
+                want.view(-1, 1, 64)[paged.slots(table[s], torch.arange(lens[s] - q_lens[s], lens[s]), 16)] = \
+                    k[cu[s]:cu[s + 1]]
+        assert torch.equal(kcg.cpu(), want)
+    for bad in (cu[:-1] + [cu[-1] + 1], [0, 40] + [41] * 60, [-1] + cu[1:], cu[:30] + [cu[30] + 5000] + cu[31:]):
+        kcg, vcg = on_gpu(kc, vc)
+        fa.paged_append(k.cuda(), v.cuda(), kcg, vcg, ints(table), ints([50] * 61), ints(bad), 30 if bad[1] == 40 else bound)
+        assert fa.STATUS[fa.fa_check_device_errors(None)] == "FA_ERR_INVALID_ARG"
