@@ -580,8 +580,11 @@ struct PagedPlan {
   size_t bytes;
 };
 
-// The tiling of a call; false when it is empty or has too many units.
-bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t H_kv, int64_t D, PagedPlan* plan) {
+// The tiling of a call; false when it is empty or, with `launch`, has too many
+// units.  The workspace never grows as max_q or max_k get smaller, so a launch
+// may plan with tighter bounds than those its workspace was sized for.
+bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t H_kv, int64_t D, bool launch,
+                PagedPlan* plan) {
   if (batch <= 0 || max_q <= 0 || max_k < 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || H / H_kv > 128 ||
       batch >= (int64_t(1) << 31) || max_q > fa::kMaxPagedLen || max_k > fa::kMaxPagedLen ||
       H >= (int64_t(1) << 20))
@@ -594,17 +597,19 @@ bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t 
     part->tok_tile = static_cast<int>(tok < longest ? tok : longest);
     part->tiles = static_cast<int>((longest + part->tok_tile - 1) / part->tok_tile);
     part->part_rows = static_cast<int>(slot_rows);
-    if (batch > (int64_t(1) << 30) / part->tiles) return false;
-    const int64_t units = batch * part->tiles;               // at most 2^30
+    if (launch && batch > (int64_t(1) << 30) / part->tiles) return false;
+    const int64_t units = batch * part->tiles;               // at most 2^30 in a launch
     const int64_t blocks = (max_k + block - 1) / block + 1;  // of a unit, at most
-    if (units > (int64_t(1) << 37) / (blocks * H_kv)) return false;  // a CTA's run of blocks fits 31 bits
-    const int64_t most = units * H_kv * blocks;
+    const bool many = units > (int64_t(1) << 37) / (blocks * H_kv);
+    if (launch && many) return false;  // a CTA's run of blocks fits 31 bits
+    const int64_t most = many ? int64_t(1) << 37 : units * H_kv * blocks;
     part->grid = static_cast<int>(most < ctas ? most : ctas);
     part->small = most * cost < (int64_t(1) << 31) / 304;  // (share x CTA stays below 2^31 too)
     part->o_at = plan->bytes;
     part->lse_at = part->o_at + round256(static_cast<size_t>(2) * part->grid * part->part_rows * D * sizeof(float));
     part->desc_at = part->lse_at + round256(static_cast<size_t>(2) * part->grid * part->part_rows * sizeof(float));
-    plan->bytes = part->desc_at + round256(static_cast<size_t>(part->grid) * sizeof(int4));
+    // (not by the grid: a call of fewer rows a unit may have twice the CTAs)
+    plan->bytes = part->desc_at + round256(static_cast<size_t>(2 * fa::kPagedSms) * sizeof(int4));
     return true;
   };
   const bool chunks = max_q * G > fa::kFewRows;
@@ -1001,7 +1006,7 @@ size_t fa_fwd_paged_workspace_size(int64_t batch, int64_t max_seqlen_q, int64_t 
                                    int64_t H_kv, int64_t D) {
   if (D != 16 && D != 32 && D != 64 && D != 128) return 0;
   PagedPlan plan;
-  return paged_plan(batch, max_seqlen_q, max_seqlen_k, H, H_kv, D, &plan) ? plan.bytes : 0;
+  return paged_plan(batch, max_seqlen_q, max_seqlen_k, H, H_kv, D, false, &plan) ? plan.bytes : 0;
 }
 
 fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache* cache, const int32_t* cu_seqlens,
@@ -1019,12 +1024,16 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
   if (max_seqlen_q > fa::kMaxPagedLen || max_seqlen_k > fa::kMaxPagedLen)
     return fail(FA_ERR_UNSUPPORTED, "max_seqlen_q and max_seqlen_k must be at most 2^29");
   if (H / H_kv > 128) return fail(FA_ERR_UNSUPPORTED, "more than 128 query heads to a K/V head");
-  PagedPlan plan;
-  if (!paged_plan(batch, max_seqlen_q, max_seqlen_k, H, H_kv, D, &plan))
-    return fail(FA_ERR_UNSUPPORTED, "batch and lengths too large");
   if ((st = check_ptr(q, "q")) || (st = check_ptr(o, "o")) || (st = check_ptr(lse, "lse")) ||
       (st = check_cache(cache, H_kv, D)) || (st = check_ints(cu_seqlens, "cu_seqlens", 4)))
     return st;
+  // No sequence has more new tokens than there are, or more keys than its row of
+  // the table holds, however loose the bounds.
+  const int64_t most_q = max_seqlen_q < total ? max_seqlen_q : total;
+  const int64_t most_k = max_seqlen_k < table_keys(cache) ? max_seqlen_k : table_keys(cache);
+  PagedPlan plan;
+  if (!paged_plan(batch, most_q, most_k, H, H_kv, D, true, &plan))
+    return fail(FA_ERR_UNSUPPORTED, "batch and lengths too large");
   const int shift = log2_of(cache->page_size);
   if (!workspace) return fail(FA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", plan.bytes);
   if (workspace_bytes < plan.bytes)
@@ -1046,7 +1055,7 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
   p.G = static_cast<int>(G);
   p.total = static_cast<int>(total);
   p.max_q = static_cast<int>(max_seqlen_q);
-  p.max_k = static_cast<int>(max_seqlen_k < table_keys(cache) ? max_seqlen_k : table_keys(cache));
+  p.max_k = static_cast<int>(most_k);
   p.win_left = window_left < 0 || window_left >= max_seqlen_k ? fa::kNoWindow : static_cast<int>(window_left);
   p.win_right =
       causal ? 0 : (window_right < 0 || window_right >= max_seqlen_k + max_seqlen_q ? fa::kNoWindow : static_cast<int>(window_right));

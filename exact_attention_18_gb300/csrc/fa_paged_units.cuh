@@ -153,6 +153,19 @@ __device__ __forceinline__ int paged_first_unit(const PagedParams& p, int thread
   return min(X, static_cast<int>(threadIdx.x) * *per);
 }
 
+// The unit index after x = b * tiles + tile, whose unit is u.  The tiles that a
+// sequence does not have are stepped over: under a loose bound they are most.
+__device__ __forceinline__ int next_tile(const PagedParams& p, const Unit& u, int x, int* b, int* tile) {
+  if (*tile + 1 < u.end_tile) {
+    ++*tile;
+    return x + 1;
+  }
+  x += p.tiles - *tile;
+  ++*b;
+  *tile = 0;
+  return x;
+}
+
 // I: int where the host has bounded the call's cost below 2^31 (64-bit scans
 // and divisions cost a decoding call a microsecond), else long long.
 template <int SHIFT, bool COSTS, int THREADS, typename I>
@@ -167,13 +180,10 @@ __device__ __forceinline__ void paged_find_run_t(const PagedParams& p, const Seq
   if (x0 < x1) {
     u0 = paged_unit<SHIFT>(p, own, tile);
     mine = u0.n_blk * static_cast<I>(u0.n_blk ? block_cost<COSTS>(p, u0) : 0);
-    for (int x = x0 + 1; x < x1; ++x) {
-      if (++tile == p.tiles) {
-        tile = 0;
-        ++b;
-      }
+    for (int x = next_tile(p, u0, x0, &b, &tile); x < x1;) {
       const Unit u = paged_unit<SHIFT>(p, seq_lens(p, b), tile);
       if (u.n_blk) mine += u.n_blk * static_cast<I>(block_cost<COSTS>(p, u));
+      x = next_tile(p, u, x, &b, &tile);
     }
   }
   I incl = mine;
@@ -200,7 +210,7 @@ __device__ __forceinline__ void paged_find_run_t(const PagedParams& p, const Seq
     b = p.tiles == 1 ? x0 : x0 / p.tiles;
     tile = x0 - b * p.tiles;
     Unit u = u0;
-    for (int x = x0; x < x1; ++x) {
+    for (int x = x0; x < x1;) {
       if (x > x0) u = paged_unit<SHIFT>(p, seq_lens(p, b), tile);
       const int cost = u.n_blk ? block_cost<COSTS>(p, u) : 0;
       const I n = static_cast<I>(u.n_blk) * p.H_kv * cost;
@@ -221,10 +231,7 @@ __device__ __forceinline__ void paged_find_run_t(const PagedParams& p, const Seq
         break;
       }
       at += n;
-      if (++tile == p.tiles) {
-        tile = 0;
-        ++b;
-      }
+      x = next_tile(p, u, x, &b, &tile);
     }
   }
   if (threadIdx.x == 0) start->share = share;

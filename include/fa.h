@@ -434,7 +434,12 @@ fa_status fa_paged_append(const void* q, int64_t q_stride, void* q_out, int64_t 
  *   A row that sees no key gets O = 0, L = -inf.
  *   H is a positive multiple of H_kv, at most 128 query heads to a K/V head.
  *   max_seqlen_q, max_seqlen_k : host bounds on the new tokens and on kv_lens
- *   (at most 2^29).
+ *   (at most 2^29).  They may be loose: `total` and the block table's row bound
+ *   the lengths too.  Too large for the library (FA_ERR_UNSUPPORTED) is a call
+ *   whose sequences, each as long as these bounds allow, have more than 2^30
+ *   tiles of query rows or 2^37 blocks of keys over all tiles and heads; batch *
+ *   min(max_seqlen_q, total) <= 2^30 and that times H_kv * (min(max_seqlen_k,
+ *   the row's keys) / 64 + 2) <= 2^37 is always supported.
  *   workspace   : fa_fwd_paged_workspace_size() bytes, 256-byte aligned, for the
  *   partials of sequences that several CTAs share; its contents on entry do not
  *   matter, and calls that may overlap on the GPU need one each.
@@ -450,7 +455,8 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
                        int64_t H_kv, int64_t D, int causal, int64_t window_left, int64_t window_right, float scale,
                        fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of fa_fwd_paged (0 for an empty or unsupported call). */
+/* Workspace bytes of fa_fwd_paged (0 for an empty call or one that no `total`
+ * makes supported); never less for larger max_seqlen_q or max_seqlen_k. */
 size_t fa_fwd_paged_workspace_size(int64_t batch, int64_t max_seqlen_q, int64_t max_seqlen_k, int64_t H,
                                    int64_t H_kv, int64_t D);
 

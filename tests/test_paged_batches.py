@@ -285,3 +285,45 @@ def test_append_reports_every_bad_sequence_under_a_loose_bound(fa, bound):  # no
         kcg, vcg = on_gpu(kc, vc)
         fa.paged_append(k.cuda(), v.cuda(), kcg, vcg, ints(table), ints([50] * 61), ints(bad), 30 if bad[1] == 40 else bound)
         assert fa.STATUS[fa.fa_check_device_errors(None)] == "FA_ERR_INVALID_ARG"
+
+
+# ------------------------------------------------- loose bounds on lengths
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_lens", [[1] * 64, [3, 0, 1] * 30, [1] * 700, [150] + [1] * 63, [1] * 40 + [90, 33] + [2] * 9])
+@pytest.mark.parametrize("max_q,max_k", [(1 << 29, 131072), (1 << 29, 1 << 29), (4000, None)])
+def test_attention_under_loose_bounds(fa, D, q_lens, max_q, max_k):  # noqa: F811
+    """The largest bounds there are, at batches of many sequences."""
+    g = torch.Generator().manual_seed(75)
+    lens = [n + int(x) for n, x in zip(q_lens, torch.randint(1, 150, (len(q_lens),), generator=g))]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 1, D, 16, torch.bfloat16, 76)
+    q = rnd((cu[-1] + 1, 8, D), 77, torch.bfloat16)
+    o, lse = run(fa, q, kc, vc, table, lens, cu, max_q=max_q, max_k=max_k)
+    check(o, lse, q, kc, vc, table, lens, cu)
+
+
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("H,hk", [(1, 1), (8, 1), (128, 1)])
+def test_one_token_among_many_rows_without_sequence(fa, D, H, hk):  # noqa: F811
+    """A padded batch of one token: by its bounds a chunk, so the kernel for chunks takes it."""
+    kc, vc, table, cu = paged_setup([5000], [1], hk, D, 16, torch.bfloat16, 96)
+    q = rnd((2000, H, D), 97, torch.bfloat16)
+    o = torch.full((2000, H, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((H, 2000), 6.0, device="cuda")
+    run(fa, q, kc, vc, table, [5000], cu, max_q=2000, max_k=100000, out=o, lse=lse)
+    assert bool((o[1:] == 5).all()) and bool((lse[:, 1:] == 6).all())
+    check(o, lse, q, kc, vc, table, [5000], cu)
+
+
+def test_bad_lengths_behind_many_sequences_under_a_loose_bound(fa):  # noqa: F811
+    """Each sequence's lengths are looked at, also where most tiles of the bound do not exist."""
+    lens, q_lens = [30] * 900, [1] * 900
+    kc, vc, table, cu = paged_setup(lens, q_lens, 1, 64, 16, torch.float16, 98)
+    q = rnd((900, 8, 64), 99, torch.float16)
+    kcg, vcg = on_gpu(kc, vc)
+    for b in (0, 1, 450, 899):
+        now = list(lens)
+        now[b] = 1 << 20
+        o, lse = fa.forward_paged(q.cuda(), kcg, vcg, ints(table), ints(now), ints(cu), 1 << 20, 1 << 29)
+        assert fa.STATUS[fa.fa_check_device_errors(None)] == "FA_ERR_INVALID_ARG"
+        some = [i for i in range(max(0, b - 3), min(900, b + 4)) if i != b]
+        check(o[some], lse[:, some], q[some], kc, vc, table[some], [30] * len(some), list(range(len(some) + 1)))
