@@ -4,11 +4,13 @@ The shared object lands in ``exact_attention_18_gb300/_lib/libfa_gb300.so``
 (object files in ``_build/``); both are git-ignored.  Translation units are
 compiled in parallel with one ``-gencode`` target, then linked with nvcc.
 ``_lib/_fa_binding.so``, the tensor binding of the serving calls, is host C++
-against PyTorch's and Python's headers, linked to the library.
+against PyTorch's and Python's headers, linked to the library.  Where PyTorch is
+not installed the library alone is built: it needs nvcc and nothing else.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -25,6 +27,7 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfa_gb300.so")
 BINDING_SRC = os.path.join(CSRC, "fa_binding.cpp")
 BINDING_PATH = os.path.join(LIB_DIR, "_fa_binding.so")
+BINDING_FOR = os.path.join(BUILD_DIR, "fa_binding.for")  # what the binding was compiled against
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd4.cu", "fa_fwd4p.cu", "fa_bwd.cu", "fa_merge.cu", "fa_rope.cu",
            "fa_paged_d16.cu", "fa_paged_d32.cu", "fa_paged_d64.cu", "fa_paged_d128.cu",
@@ -63,9 +66,31 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _compile_binding(verbose: bool) -> str:
-    """The tensor binding's object file.  Finds PyTorch's headers without importing it."""
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+def _torch_dir() -> str | None:
+    """Where PyTorch is installed, found without importing it; None where it is not."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _binding_target(torch_dir: str) -> str:
+    """The PyTorch and Python that a binding is compiled against."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "unknown"
+    return f"torch {version} in {torch_dir}, {sys.implementation.cache_tag} {sysconfig.get_paths()['include']}\n"
+
+
+def _read(path: str) -> str | None:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def _compile_binding(torch_dir: str, verbose: bool) -> str:
+    """The tensor binding's object file."""
     cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     obj = os.path.join(BUILD_DIR, "fa_binding.o")
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-I" + INCLUDE,
@@ -80,8 +105,8 @@ def _compile_binding(verbose: bool) -> str:
     return obj
 
 
-def _link_binding(obj: str, verbose: bool) -> None:
-    torch_lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+def _link_binding(obj: str, torch_dir: str, verbose: bool) -> None:
+    torch_lib = os.path.join(torch_dir, "lib")
     tmp = BINDING_PATH + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-shared", obj, "-o", tmp, "-L" + LIB_DIR, "-lfa_gb300",
            "-Wl,-rpath,$ORIGIN", "-L" + torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
@@ -91,22 +116,28 @@ def _link_binding(obj: str, verbose: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link of the tensor binding failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_FOR, "w") as f:
+        f.write(_binding_target(torch_dir))
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Build (if stale) the library and its tensor binding; returns the library's path."""
+    """Build (if stale) the library, and where PyTorch is installed its tensor binding; returns the library's path."""
+    torch_dir = _torch_dir()
     lib_stale = force or _stale(LIB_PATH, _deps())
-    binding_stale = force or _stale(BINDING_PATH, [BINDING_SRC, os.path.join(INCLUDE, "fa.h")])
+    binding_stale = torch_dir is not None and (
+        force or _stale(BINDING_PATH, [BINDING_SRC, os.path.join(INCLUDE, "fa.h")])
+        or _read(BINDING_FOR) != _binding_target(torch_dir))
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding, verbose) if binding_stale else None
-        objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES)) if lib_stale else None
-        binding_obj = binding.result() if binding else None
-    if lib_stale:
-        _link_library(objs, verbose)
-    if binding_stale:
-        _link_binding(binding_obj, verbose)
+        binding = ex.submit(_compile_binding, torch_dir, verbose) if binding_stale else None
+        if lib_stale:
+            _link_library(list(ex.map(lambda s: _compile(s, verbose), SOURCES)), verbose)
+        # (the library is there by now, whatever becomes of the binding)
+        if binding:
+            _link_binding(binding.result(), torch_dir, verbose)
+    if torch_dir is None and verbose:
+        print("PyTorch is not installed: the library is built without its tensor binding", flush=True)
     return LIB_PATH
 
 
