@@ -577,6 +577,7 @@ struct PagedPart {
 };
 struct PagedPlan {
   PagedPart few, tile;
+  size_t go_at;  // calls of both kernels: byte offset of their word (PagedParams::go)
   size_t bytes;
 };
 
@@ -631,7 +632,16 @@ bool paged_plan(int64_t batch, int64_t max_q, int64_t max_k, int64_t H, int64_t 
              fa::kMaxBlockCost))
       return false;
   }
+  plan->go_at = plan->bytes;
+  if (plan->few.used && plan->tile.used) plan->bytes += 256;
   return true;
+}
+
+// A number that no other launch of the process has, and that other contents of a
+// workspace hardly are (an odd multiple, modulo 2^64, of a count).
+unsigned long long launch_ticket() {
+  static std::atomic<unsigned long long> count{0};
+  return (count.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9E3779B97F4A7C15ull;
 }
 
 // Tensor map of a packed [T, H, D] Q, box {row chunk, G heads, tok_tile tokens}.
@@ -1073,6 +1083,10 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
   mp.G = p.G;
   mp.H = p.H;
   mp.total = p.total;
+  if (plan.few.used && plan.tile.used) {
+    p.go = mp.go = reinterpret_cast<unsigned long long*>(ws + plan.go_at);
+    p.ticket = launch_ticket();
+  }
   int sets = 0, grid = 0;
   auto run = [&](const PagedPart& part, bool tile) -> fa_status {
     p.tok_tile = part.tok_tile;

@@ -20,7 +20,10 @@ constexpr int kMaxPagedLen = 1 << 29;
 // of its first access to the caller's memory, so it also never completes
 // before them.  What the caller's earlier kernels may have written is read with
 // plain loads, never through the read-only path (__ldg): that path may serve a
-// line that was cached before the wait.
+// line that was cached before the wait.  One grid may do without its wait at the
+// front: the few-row kernel behind the tile kernel, where it has acquired that
+// kernel's word that the grids before the call are done (say_go); it waits at
+// its end, so that it does not complete before that kernel.
 template <typename... Params, typename... Args>
 inline cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                                     const Args&... args) {
@@ -94,7 +97,9 @@ struct PagedParams {
   int small;             // the cost of all blocks of the call is below 2^31 / 304
   int sub_tok;           // tile kernel: tokens of one of a unit's tiles
   unsigned costs;        // tile kernel: byte i is the cost of a block of a unit that fills i + 1 tiles
-  int after_tile;        // few-row kernel: launched behind the tile kernel of the same call, whose CTAs fill the SMs
+  int after_tile;        // few-row kernel: launched behind the tile kernel of the same call
+  unsigned long long* go;    // calls of both kernels: the tile kernel writes `ticket` here when the grids before the
+  unsigned long long ticket; // call have completed; the join clears it.  A number of the launch's own.
   float scale_log2;
   int part_rows;         // rows of a partial's slot
   float* o_part;         // [2 grid][part_rows x D] fp32, laid out as in PagedParts
@@ -119,6 +124,7 @@ struct PagedMergeParams {
   void* o;
   float* lse;
   int G, H, total;
+  unsigned long long* go;  // cleared (nullptr: none)
 };
 
 // Query rows (new tokens x G) of a sequence up to which the few-row kernel takes

@@ -171,18 +171,22 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
   int* s_off = reinterpret_cast<int*>(s_red + 4 * N);     // [N] output row of row n after its unit's first
   short* s_tok = reinterpret_cast<short*>(s_off + N);     // [N] token of row n
 
-  // Behind the tile kernel of the same call: where no sequence is short enough
-  // for this kernel, it leaves before any set-up.  (Its CTAs start as that
-  // kernel's end, so there is no time to fill with set-up before the wait.)
+  // Behind the tile kernel of the same call this grid's CTAs start as that
+  // kernel's end, and work beside the last of them once they have its word that
+  // the grids before the call are done (the two share no output).  Waiting for
+  // the tile kernel itself would cost a chunk of 512 tokens beside 63 single ones
+  // 133 us for 122 at D = 128, 102 for 92 at D = 64.  Where no sequence is short
+  // enough for this kernel, it leaves before any set-up.
+  if (p.after_tile && !__syncthreads_or(threadIdx.x == 0 && heard_go(p))) griddep_wait();
   SeqLens own{0, 0, 0};
   const bool all_known = p.after_tile && p.batch <= L::kThreads;  // a thread each
   if (all_known) {
-    griddep_wait();
     if (static_cast<int>(threadIdx.x) < p.batch) own = seq_lens(p, threadIdx.x);
     const int n = own.e - own.a;
     if (!__syncthreads_or(n > 0 && n <= p.tok_hi)) {
       if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
       griddep_launch_dependents();
+      griddep_wait();
       return;
     }
   }
@@ -210,8 +214,8 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  // Up to here nothing of the caller's was touched (or this grid has waited already).
-  griddep_wait();
+  // (Behind other kernels nothing of the caller's was touched up to here.)
+  if (!p.after_tile) griddep_wait();
   griddep_launch_dependents();
   if (!all_known) {
     int per;
@@ -238,6 +242,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     // The whole warp runs this; lane i copies page box i of each tile.  With one
     // warp for both, its 450-750 cycles per tile bounded the kernel at D <= 64.
     const int kv = warp - kProducer;  // 0: K, 1: V
+    if (p.after_tile) fence_proxy_async_global();
     const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;
     const int frag = min(kPBlk, 1 << p.page_shift);
     const int n_frag = kPBlk / frag;
@@ -602,6 +607,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
+  if (p.after_tile) griddep_wait();
 }
 
 namespace {

@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_paged_merge_kernel(const Pag
   griddep_wait();
   griddep_launch_dependents();
   const int first = blockIdx.x;
+  if (p.go && threadIdx.x == 0 && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) *p.go = 0;
   // (an index into the parameters would put a copy of them on the stack)
   const bool z = blockIdx.z != 0;
   const PagedParts q{z ? p.parts[1].o_part : p.parts[0].o_part, z ? p.parts[1].lse_part : p.parts[0].lse_part,

@@ -203,7 +203,10 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   }
   // Up to here nothing of the caller's was touched.
   griddep_wait();
-  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    if (p.go && blockIdx.x == 0) say_go(p);
+    griddep_launch_dependents();
+  }
   SeqLens own{0, 0, 0};
   {
     int per;

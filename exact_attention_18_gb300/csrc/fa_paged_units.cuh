@@ -244,6 +244,22 @@ __device__ __forceinline__ void paged_find_run(const PagedParams& p, const SeqLe
   else paged_find_run_t<SHIFT, COSTS, THREADS, long long>(p, own, s_warp, start);
 }
 
+// The tile kernel's word to the few-row kernel behind it in the same call: the
+// grids before the call have completed and their writes are visible.  A grid's
+// own griddep_wait would say so too, but only when the tile kernel has ended;
+// the release, in a thread that has waited itself, and the acquire hand the
+// order on to a grid that runs beside it.
+__device__ __forceinline__ void say_go(const PagedParams& p) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.go), "l"(p.ticket) : "memory");
+}
+__device__ __forceinline__ bool heard_go(const PagedParams& p) {
+  unsigned long long x;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(p.go) : "memory");
+  return x == p.ticket;
+}
+// Orders what this thread has seen before its later bulk copies from global memory.
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
                                             int w) {
   asm volatile(

@@ -327,3 +327,37 @@ def test_bad_lengths_behind_many_sequences_under_a_loose_bound(fa):  # noqa: F81
         assert fa.STATUS[fa.fa_check_device_errors(None)] == "FA_ERR_INVALID_ARG"
         some = [i for i in range(max(0, b - 3), min(900, b + 4)) if i != b]
         check(o[some], lse[:, some], q[some], kc, vc, table[some], [30] * len(some), list(range(len(some) + 1)))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_mixed_call_in_a_workspace_of_anything(fa, D):  # noqa: F811
+    """Both kernels of a mixed call share a workspace: whatever it holds on entry, and used again and again, by calls
+    of one kernel in between, the result is the same; after a call whose waits run out, too."""
+    lens, q_lens = [600, 900, 50, 300], [200, 1, 4, 1]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, D, 32, torch.bfloat16, 63)
+    q = rnd((cu[-1], 8, D), 64, torch.bfloat16)
+    kcg, vcg = on_gpu(kc, vc)
+    args = (kcg, vcg, ints(table), ints(lens))
+    need = fa.fa_fwd_paged_workspace_size(4, 200, 900, 8, 2, D)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    o, lse = fa.forward_paged(q.cuda(), *args, ints(cu), 200, 900, workspace=ws)
+    check(o, lse, q, kc, vc, table, lens, cu)
+    one, single = q[:4].cuda(), ints([0, 1, 2, 3, 4])
+    for fill in (0, 255, 127, 1, None, "single", "late", None):
+        if isinstance(fill, int):
+            ws.fill_(fill)
+        elif fill == "single":
+            fa.forward_paged(one, *args, single, 1, 900, workspace=ws)
+        elif fill == "late":
+            fa.fa_set_wait_limit_ns(1)
+            try:
+                fa.forward_paged(q.cuda(), *args, ints(cu), 200, 900, workspace=ws)
+                torch.cuda.synchronize()
+            finally:
+                fa.fa_set_wait_limit_ns(0)
+            assert fa.STATUS[fa.fa_check_device_errors(None)] == "FA_ERR_TIMEOUT"
+        o2, l2 = fa.forward_paged(q.cuda(), *args, ints(cu), 200, 900, workspace=ws)
+        assert fa.fa_check_device_errors(None) == 0
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+    with pytest.raises(fa.FAError):
+        fa.forward_paged(q.cuda(), *args, ints(cu), 200, 900, workspace=ws[:-256])
