@@ -906,7 +906,7 @@ fa_status fa_rope_inv_freq(int64_t rot_dim, double base, fa_rope_scaling scaling
     hi = std::fmin(std::ceil(pair_of(slow_turns)), rot - 1.0);
     // The ramp's end (before pair 0) or its start (past the last) may lie beyond
     // every pair: all are then slow, or all fast.
-    if (hi < 0) lo = hi - 1.0;
+    if (pair_of(slow_turns) < 0) lo = hi - 1.0;
     else if (lo >= hi) hi = lo + 0.001;
   }
   for (int64_t i = 0; i < rot_dim / 2; ++i) {

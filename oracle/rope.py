@@ -28,7 +28,7 @@ def inv_freq(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len=0.0
     # index at which a pair makes `turns` turns in original_len positions
     at = lambda turns: rot_dim * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
     lo, hi = max(math.floor(at(fast_turns)), 0), min(math.ceil(at(slow_turns)), rot_dim - 1)
-    if hi < 0:      # every pair turns less than slow_turns times
+    if at(slow_turns) < 0:  # every pair turns less than slow_turns times
         lo = hi - 1
     elif lo >= hi:  # a ramp of no width, or one past the last pair
         hi = lo + 0.001
