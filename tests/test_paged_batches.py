@@ -361,3 +361,65 @@ def test_mixed_call_in_a_workspace_of_anything(fa, D):  # noqa: F811
         assert torch.equal(o, o2) and torch.equal(lse, l2)
     with pytest.raises(fa.FAError):
         fa.forward_paged(q.cuda(), *args, ints(cu), 200, 900, workspace=ws[:-256])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_mixed_calls_on_two_streams_and_in_graphs(fa, D):  # noqa: F811
+    """Mixed calls unsynchronised on two streams, each with its stream's scratch, beside two replayed graphs of the
+    same calls, each with its own."""
+    lens, q_lens = [2500, 900, 50, 300, 77], [200, 1, 4, 1, 1]
+    kc, vc, table, cu = paged_setup(lens, q_lens, 2, D, 32, torch.bfloat16, 65)
+    kcg, vcg = on_gpu(kc, vc)
+    args = (kcg, vcg, ints(table), ints(lens), ints(cu), 200, 2500)
+    qs = [rnd((cu[-1], 8, D), 66 + i, torch.bfloat16) for i in range(2)]
+    qg = [x.cuda() for x in qs]
+    want = [fa.forward_paged(x, *args) for x in qg]
+    check(*want[0], qs[0], kc, vc, table, lens, cu)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, [fa.forward_paged(qg[i], *args) for _ in range(3)]))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for i in range(2):
+            got.append((i, fa.forward_paged(qg[i], *args, stream=streams[i])))
+            with torch.cuda.stream(streams[1 - i]):
+                graphs[i][0].replay()
+    torch.cuda.synchronize()
+    assert fa.fa_check_device_errors(None) == 0
+    for i, (o, lse) in got + [(i, r) for i in range(2) for r in graphs[i][1]]:
+        assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+@pytest.mark.parametrize("order", ["rows", "heads"])
+@pytest.mark.parametrize("q_len", [1, 100])
+@pytest.mark.parametrize("D", [16, 64, 128])
+def test_padded_strides(fa, order, q_len, D):  # noqa: F811
+    """Strides that are multiples of 8 elements and of nothing else, append and attention."""
+    hk, page, lens, q_lens = 3, 16, [200, 130], [q_len, 1]
+    kc, vc, table, cu = paged_setup(lens, q_lens, hk, D, page, torch.float16, 68)
+    n = kc.shape[0]
+    if order == "rows":    # [pages, rows, heads, D] with room behind heads, rows and pages
+        head, row = D + 8, hk * (D + 8) + 16
+        strides = (page * row + 24, row, head, 1)
+    else:                  # [pages, heads, rows, D]
+        row, head = D + 8, page * (D + 8) + 40
+        strides = (hk * head + 8, row, head, 1)
+    caches = [torch.full((n * strides[0],), float("nan"), dtype=torch.float16, device="cuda") for _ in range(2)]
+    kcg, vcg = (c.as_strided(kc.shape, strides) for c in caches)
+    kcg.copy_(kc)
+    vcg.copy_(vc)
+    k, v, q = rnd((cu[-1], hk, D), 69, torch.float16), rnd((cu[-1], hk, D), 70, torch.float16), \
+        rnd((cu[-1], 2 * hk, D), 71, torch.float16)
+    args = (kcg, vcg, ints(table), ints(lens), ints(cu), q_len)
+    fa.paged_append(k.cuda(), v.cuda(), *args)
+    kn, vn = paged.append(kc, k, table, lens, cu), paged.append(vc, v, table, lens, cu)
+    assert torch.equal(kcg.cpu(), kn) and torch.equal(vcg.cpu(), vn)
+    for c, x in zip(caches, (kn, vn)):  # the room between is as it was
+        assert int(c.isnan().sum()) == c.numel() - x.numel()
+    o, lse = fa.forward_paged(q.cuda(), *args, 200)
+    assert fa.fa_check_device_errors(None) == 0
+    check(o, lse, q, kn, vn, table, lens, cu)
