@@ -129,10 +129,12 @@ struct PagedMergeParams {
 
 // Query rows (new tokens x G) of a sequence up to which the few-row kernel takes
 // it, and rows of a unit it is instantiated for: the smallest that holds `rows`.
-// Both kernels measured (us, few-row / tile; 16 sequences of 8192 keys, G = 8):
-// 40 rows D = 64 36.4 / 46.6, D = 128 46.4 / 67.1; 64 rows 34.6 / 46.4 and 48.0 /
-// 68.3; with an instantiation for 128 rows, 80 rows 58.7 / 47.3 and 86.5 / 70.7;
-// 128 rows 56.7 / 48.8 and 68.5 / 73.4; 160 rows 92.2 / 57.9 and 111 / 78.0.
+// Both kernels measured (us, few-row / tile; 16 sequences of 8192 keys, 4 K/V
+// heads, G = 8, pages of 16), D = 16, 32, 64, 128: 40 rows 36.2 / 39.2, 35.0 /
+// 42.8, 36.5 / 51.8, 53.8 / 71.2; 64 rows 36.6 / 39.6, 35.5 / 42.3, 37.4 / 51.5,
+// 55.5 / 71.9.  With an instantiation for 128 rows that was tried, D = 64 and 128:
+// 80 rows 58.7 / 47.3, 86.5 / 70.7; 128 rows 56.7 / 48.8, 68.5 / 73.4; 160 rows
+// 92.2 / 57.9, 111 / 78.0.
 constexpr int kFewRows = 64;
 inline int paged_rows(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
 constexpr int kPagedSms = 152;

@@ -63,8 +63,7 @@ struct PagedLayout {
   using GP = TileGeom<N, kPBlk>;   // P^T tile: 128 keys x N rows
   // Softmax warpgroups, each over kCols rows.  More of them hide more of each
   // other's latency: 16 sequences of 8192 keys at D = 64, N = 64 with 32 / 16
-  // rows a thread 38.7 / 36.4 us; drafted tokens in a window, N = 64, kernel
-  // alone, with 64 / 32 29 / 16 us.
+  // rows a thread 38.7 / 36.4 us.
   static constexpr int kCols = 16;
   static constexpr int kWgs = N / kCols;
   static constexpr int kThreads = 128 * kWgs + 96;  // and the producers of K and V, the MMA issuer
@@ -512,8 +511,10 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
             tmem_st_wait();
           }
         }
-        // P~ = 2^(c s - m), 16-bit, into the key's row of the P^T tile; the
-        // running sums take the unrounded values.
+        // P~ = 2^(c s - m) into the key's row of the P^T tile, rounded to 16 bits
+        // (the product takes V as it lies in the cache, so both operands have its
+        // type; a weight is off by 2^-8 of itself at most in bf16, 2^-11 in fp16);
+        // the running sums take the unrounded values.
         uint8_t* prow = p_tile + (i & 1) * GP::kTileBytes;
 #pragma unroll
         for (int k = 0; k < NC; k += 8) {

@@ -447,8 +447,11 @@ fa_status fa_paged_append(const void* q, int64_t q_stride, void* q_out, int64_t 
  * NaN included.  A NaN in a query, or in a key that it sees, makes that row's
  * O and L NaN.  A NaN or infinity in V at a key some row sees reaches that
  * row, and may reach other rows of the call that share the K/V head.
- * The result depends on the lengths but not on timing: repeated calls give the
- * same bits.
+ * Rounding: as in the other forward calls, the probabilities (relative to the
+ * row's running maximum) are rounded to the inputs' type for the product with V,
+ * and O once at the end; products, sums, maxima and partials are fp32.
+ * The result depends on the lengths and bounds, not on timing: repeated calls
+ * give the same bits.
  */
 fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache* cache, const int32_t* cu_seqlens,
                        int64_t batch, int64_t max_seqlen_q, int64_t max_seqlen_k, int64_t total, int64_t H,
