@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
   RunStart* s_start = reinterpret_cast<RunStart*>(tmem_slot + 2);
   float* s_m = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bar_full) + L::kNumBars * 8 + 8 + sizeof(RunStart));
   s_m = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(s_m) + 15) & ~static_cast<uintptr_t>(15));
-  float* s_negm = s_m + N;          // [N] -(maximum), 0 while no key was seen; -inf: not a row of the unit
+  float* s_negm = s_m + N;          // [N] -(maximum), 0 while no key was seen
   float* s_alpha = s_negm + N;      // [N] factor of the last change of maximum; at a segment's end 1 / l
   float* s_red = s_alpha + N;       // [N][4] per-warp partial of each row
   int* s_off = reinterpret_cast<int*>(s_red + 4 * N);     // [N] output row of row n after its unit's first
@@ -408,7 +408,10 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
       const int full_hi = min(u.kv_len, u.pos0 + 1 + p.win_right);
 #pragma unroll
       for (int k = 0; k < NC; ++k) l[k] = 0.f;
-      if (wt < NC) m_s[wt] = -INFINITY;
+      // Rows past the unit's hold other tokens' queries, or what shared memory held.
+      // +inf for their maximum never moves, and its negative puts their scores
+      // below every bound: they have no say in which blocks take the block maximum.
+      if (wt < NC) m_s[wt] = g * NC + wt < n_rows ? -INFINITY : INFINITY;
       // The first block, a cut block, the one after it, and any block as long as
       // a row has seen no score above -inf take the block maximum.
       bool exact_max = true;
@@ -470,16 +473,12 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
             const float mo = m_s[wt];
             const float mn = (mb > mo + kPagedTau || mo == -INFINITY) ? mb : mo;
             float a = 1.f;
-            // Rows past the unit's hold other tokens' queries, or what shared memory
-            // held: they keep no maximum, and -inf for its negative puts their
-            // scores below every bound, so that they never send a block here.
-            const bool is_row = g * NC + wt < n_rows;
-            if (mn != mo && is_row) {
+            if (mn != mo) {
               a = ex2(mo - mn);
               moved = true;
             }
-            m_s[wt] = is_row ? mn : 0.f;
-            negm_s[wt] = !is_row ? -INFINITY : (mn == -INFINITY ? 0.f : -mn);
+            m_s[wt] = mn;
+            negm_s[wt] = mn == -INFINITY ? 0.f : -mn;
             alpha_s[wt] = a;
           }
           moved = !named_sync_and(bar_id, 128, !moved);
