@@ -22,7 +22,9 @@
 // block is 64 KB, 2800 cycles of an SM's share of the memory's rate; decoding 32
 // sequences of up to 8192 keys keeps the tensor pipe active 4.5 % of the time
 // and takes 58 - 59 us with the join, 83 - 85 % of the copy rate (4 contexts of up
-// to 131072 keys: 150 - 157 us, 96 - 100 %).  So the kernel is organised around keeping copies in flight: one or two persistent CTAs per
+// to 131072 keys: 150 - 157 us, 96 - 100 %).  32 sequences of up to 8192 keys in
+// pages of 16 take 34 us at D = 64 (floor 25) and 24 at D = 16 (6): there a
+// block's chain shows.  So the kernel is organised around keeping copies in flight: one or two persistent CTAs per
 // SM, their shared memory given to a ring of K and V tiles, and work dealt in
 // 128-key blocks: the blocks of all units, in order, are cut into equal runs,
 // one per CTA, whatever the sequences' lengths (each CTA finds its run from
@@ -173,8 +175,8 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
   // Behind the tile kernel of the same call this grid's CTAs start as that
   // kernel's end, and work beside the last of them once they have its word that
   // the grids before the call are done (the two share no output).  Waiting for
-  // the tile kernel itself would cost a chunk of 512 tokens beside 63 single ones
-  // 133 us for 122 at D = 128, 102 for 92 at D = 64.  Where no sequence is short
+  // the tile kernel itself, a chunk of 512 tokens beside 63 single ones takes 135
+  // us for 125 at D = 128, 103 for 94 at D = 64.  Where no sequence is short
   // enough for this kernel, it leaves before any set-up.
   if (p.after_tile && !__syncthreads_or(threadIdx.x == 0 && heard_go(p))) griddep_wait();
   SeqLens own{0, 0, 0};

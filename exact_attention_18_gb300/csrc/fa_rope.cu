@@ -44,7 +44,8 @@ constexpr int kRopeIdle = 8 * kPagedSms;  // append: CTAs without tokens in a la
 enum RopeForm {
   kInterleaved,   // pairs (2i, 2i+1): any r, a vector holds whole pairs
   kHalf,          // pairs (i, r + i), r a multiple of 8: vectors at 8j and r + 8j
-  kHalfAny,       // any other r: partners come through shared memory
+  kHalfAny,       // any other r: partners come through shared memory, one element at a time (8192 tokens of 36
+                  // heads of 128: r = 64 23.7 us, r = 50 78; that form is instructions, not memory)
 };
 
 enum RopeMode {
