@@ -140,9 +140,11 @@ inline int paged_rows(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 
 constexpr int kPagedSms = 152;
 // Costs of the tile kernel's blocks by the row tiles of their unit.  256 units of
 // 8192 keys, 1 .. 4 tiles: D = 64 125, 171, 283, 301 us, D = 32 112, 149, 243, 275,
-// D = 16 106, 141, 225, 260; D = 128, 1 and 2 tiles: 203, 248.  A little is added
-// for short units' joins (ragged chunks of 16 heads, D = 64, with 3, 5, 7, 8 / 4, 5,
-// 8, 8: 87.3 / 85.7 us, chunks up to 1000 tokens 103.7 / 101.5).
+// D = 16 106, 141, 225, 260; D = 128, 1 and 2 tiles: 203, 248.  One table for
+// D <= 64, a little above the first for short units' joins.  With 3, 5, 7, 8 / 3,
+// 4, 7, 8 / 4, 5, 7, 8 / 4, 5, 8, 8 (D = 64): ragged chunks of 16 heads 86.7 / 84.7 /
+// 84.4 / 85.0 us, 16 chunks of up to 1000 tokens 114 / 132 / 117 / 119, prompts of
+// 40 and 20 tokens 36.4 / 31.7 / 32.1 / 32.1.
 constexpr int kMaxBlockCost = 8;
 constexpr unsigned paged_costs(int D) { return D == 128 ? 0x0807u : 0x08080504u; }
 // CTAs per SM of the few-row kernel.
