@@ -659,7 +659,7 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seq
 
     Query i of a sequence's n new tokens stands at key kv_lens - n + i.
     ``max_seqlen_q`` and ``max_seqlen_k`` are host bounds on the new tokens and
-    on ``kv_lens``; a violation, or a bad page, is found on the device and
+    on ``kv_lens`` and may be loose; a violation, or a bad page, is found on the device and
     reported by ``fa_check_device_errors``.  Without ``workspace`` the call uses
     scratch kept for its stream (its own while a graph is captured).
     """

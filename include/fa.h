@@ -413,8 +413,9 @@ typedef struct {
  *   positions   : DEVICE int32 [T], or NULL: a token's position is its key index;
  *   steps       : DEVICE uint64 [rot_dim / 2]; rot_dim = 0 (steps not used)
  *                 appends K as it is and copies Q;
- *   max_seqlen  : host bound on the new tokens of a sequence.
- * Two new tokens must not share a slot.  Other slots and rows of tokens that no
+ *   max_seqlen  : host bound on the new tokens of a sequence; may be loose.
+ * Two new tokens must not share a slot.  Where offsets decrease, other sequences
+ * of the call may be left alone beside the one that is reported.  Other slots and rows of tokens that no
  * sequence covers are left as they were.
  */
 fa_status fa_paged_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
