@@ -64,6 +64,11 @@ class PagedCache(ctypes.Structure):
                 ("head_stride", ctypes.c_int64)]
 
 
+class Scores(ctypes.Structure):
+    """``fa_scores`` of fa.h: tanh cap (0: none), device pointers of slopes and prefix lengths (None: none)."""
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
+
+
 _lib = None
 _binding = None
 
@@ -112,6 +117,14 @@ def _load():
     lib.fa_bwd_window_marked.restype = i32
     lib.fa_bwd_window_marked.argtypes = [vp] * 9 + [i64] * 5 + [i32, i64, i64, f32, i32, vp, sz, vp,
                                                                 ctypes.POINTER(vp)]
+    lib.fa_fwd_scores.restype = i32
+    lib.fa_fwd_scores.argtypes = [vp] * 5 + [i64] * 5 + [i32, i64, i64, vp, f32, i32, vp]
+    lib.fa_bwd_scores.restype = i32
+    lib.fa_bwd_scores.argtypes = [vp] * 9 + [i64] * 5 + [i32, i64, i64, vp, f32, i32, vp, sz, vp]
+    lib.fa_fwd_scores_varlen.restype = i32
+    lib.fa_fwd_scores_varlen.argtypes = [vp] * 6 + [i64] * 6 + [i32, i64, i64, vp, f32, i32, vp]
+    lib.fa_bwd_scores_varlen.restype = i32
+    lib.fa_bwd_scores_varlen.argtypes = [vp] * 10 + [i64] * 6 + [i32, i64, i64, vp, f32, i32, vp, sz, vp]
     lib.fa_fwd_splitkv.restype = i32
     lib.fa_fwd_splitkv.argtypes = [vp] * 5 + [i64] * 5 + [i32, i64, f32, i32, vp, sz, vp]
     lib.fa_fwd_splitkv_workspace_size.restype = sz
@@ -262,6 +275,33 @@ def fa_bwd_varlen_marked(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, batch, m
                                         stream, arr)
 
 
+def fa_fwd_scores(q, k, v, o, lse, B, H, H_kv, S, D, causal, window_left, window_right, scores, scale, dtype,
+                  stream) -> int:
+    """``scores``: a Scores structure passed by reference, or None."""
+    return _load().fa_fwd_scores(q, k, v, o, lse, B, H, H_kv, S, D, int(causal), int(window_left), int(window_right),
+                                 scores, float(scale), int(dtype), stream)
+
+
+def fa_bwd_scores(q, k, v, o, dout, lse, dq, dk, dv, B, H, H_kv, S, D, causal, window_left, window_right, scores, scale,
+                  dtype, workspace, workspace_bytes, stream) -> int:
+    return _load().fa_bwd_scores(q, k, v, o, dout, lse, dq, dk, dv, B, H, H_kv, S, D, int(causal), int(window_left),
+                                 int(window_right), scores, float(scale), int(dtype), workspace, workspace_bytes,
+                                 stream)
+
+
+def fa_fwd_scores_varlen(q, k, v, o, lse, cu_seqlens, batch, max_seqlen, total, H, H_kv, D, causal, window_left,
+                         window_right, scores, scale, dtype, stream) -> int:
+    return _load().fa_fwd_scores_varlen(q, k, v, o, lse, cu_seqlens, batch, max_seqlen, total, H, H_kv, D, int(causal),
+                                        int(window_left), int(window_right), scores, float(scale), int(dtype), stream)
+
+
+def fa_bwd_scores_varlen(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, batch, max_seqlen, total, H, H_kv, D, causal,
+                         window_left, window_right, scores, scale, dtype, workspace, workspace_bytes, stream) -> int:
+    return _load().fa_bwd_scores_varlen(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, batch, max_seqlen, total, H,
+                                        H_kv, D, int(causal), int(window_left), int(window_right), scores,
+                                        float(scale), int(dtype), workspace, workspace_bytes, stream)
+
+
 def fa_bwd_noalloc(q, k, v, o, dout, lse, dq, dk, dv, B, H, S, D, causal, scale, dtype, stream) -> int:
     """fa_bwd for callers that cannot allocate: its scratch is a fixed array inside the library."""
     return _load().fa_bwd_noalloc(q, k, v, o, dout, lse, dq, dk, dv, B, H, S, D, int(causal), float(scale),
@@ -381,14 +421,42 @@ def _kv_heads(q, k, v):
     return hk
 
 
+def _scores(q, heads, batch, softcap, slopes, prefix, others):
+    """The Scores of a call, or None where nothing modifies them; checks their tensors and the call's."""
+    import torch
+    if softcap is None and slopes is None and prefix is None:
+        return None
+    for t, n, dt, name in ((slopes, heads, torch.float32, "slopes"), (prefix, batch, torch.int32, "prefix")):
+        if t is not None and (t.dtype != dt or t.shape != (n,) or not t.is_contiguous() or not t.is_cuda):
+            raise ValueError(f"{name} must be a contiguous {dt} CUDA tensor of {n} entries")
+    if softcap is not None and not softcap > 0:
+        raise ValueError("softcap must be positive (None: no cap)")
+    if q.get_device() != torch.cuda.current_device() or any(
+            t is not None and t.get_device() != q.get_device() for t in (slopes, prefix, *others)):
+        raise ValueError("all tensors must be on the current CUDA device")
+    return Scores(0.0 if softcap is None else softcap, None if slopes is None else slopes.data_ptr(),
+                  None if prefix is None else prefix.data_ptr())
+
+
+def _like(t, shape, dtype, name):
+    """An output or statistic given by the caller: contiguous, of this shape and dtype."""
+    if t is not None and (t.dtype != dtype or t.numel() != math.prod(shape) or not t.is_contiguous() or not t.is_cuda):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)}")
+
+
 def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None, lse=None, stream=None,
-            window=None):
+            window=None, softcap: float | None = None, slopes=None, prefix=None):
     """O and fp32 natural-log LSE of exact attention; tensors [B, H, S, D] (or [B, S, D]).
 
     K and V may have H_kv heads with H a multiple of H_kv (grouped-query
     attention; query head h reads K/V head h // (H // H_kv)).  ``window =
     (left, right)`` restricts query i to keys i - left .. i + right (negative =
     unlimited).
+
+    Modified scores (``fa_fwd_scores``): ``softcap`` caps them, cap * tanh(score
+    / cap); fp32 ``slopes`` [H] subtract slopes[h] * |i - j|; int32 ``prefix``
+    [B] makes keys j < prefix[b] visible to every row (as far as the window's
+    left side allows).  ``backward`` takes the same.
     """
     import torch
     squeeze = q.dim() == 3
@@ -397,9 +465,18 @@ def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None,
     hk = _kv_heads(q, k, v)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
+    scores = _scores(q, H, B, softcap, slopes, prefix, (k, v, out, lse))
+    if scores is not None:
+        _like(out, q.shape, q.dtype, "out")
+        _like(lse, (B, H, S), torch.float32, "lse")
     o = torch.empty_like(q) if out is None else out.view(q.shape)
     l = torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse is None else lse.view(B, H, S)
-    if window is not None:
+    if scores is not None:
+        left, right = (-1, -1) if window is None else window
+        _check(fa_fwd_scores(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(), B, H, hk, S, D,
+                             causal, left, right, ctypes.byref(scores), scale, _dtype_code(q), _stream_ptr(stream)),
+               "fa_fwd_scores")
+    elif window is not None:
         _check(fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(), B, H, hk, S, D,
                              causal, window[0], window[1], scale, _dtype_code(q), _stream_ptr(stream)),
                "fa_fwd_window")
@@ -415,11 +492,12 @@ def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None,
 
 
 def backward(q, k, v, o, do, lse, causal: bool = False, scale: float | None = None, dq=None, dk=None, dv=None,
-             workspace=None, stream=None, window=None):
+             workspace=None, stream=None, window=None, softcap: float | None = None, slopes=None, prefix=None):
     """dQ, dK, dV of exact attention from the forward's O and LSE (recompute backward).
 
     With K, V of H_kv < H heads, dK and dV have H_kv heads and sum over each
-    K/V head's group of query heads.
+    K/V head's group of query heads.  ``softcap``, ``slopes`` and ``prefix`` as
+    the forward had them; slopes are constants and get no gradient.
     """
     import torch
     squeeze = q.dim() == 3
@@ -430,6 +508,11 @@ def backward(q, k, v, o, do, lse, causal: bool = False, scale: float | None = No
         raise ValueError("o and do must have q's shape")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
+    scores = _scores(q, H, B, softcap, slopes, prefix, (k, v, o, do, lse, dq, dk, dv, workspace))
+    if scores is not None:
+        for t, like, name in ((o, q, "o"), (do, q, "do"), (dq, q, "dq"), (dk, k, "dk"), (dv, k, "dv")):
+            _like(t, like.shape, q.dtype, name)
+        _like(lse, (B, H, S), torch.float32, "lse")
     lse = lse.reshape(B, H, S)
     dq = torch.empty_like(q) if dq is None else dq.view(q.shape)
     dk = torch.empty_like(k) if dk is None else dk.view(k.shape)
@@ -440,7 +523,11 @@ def backward(q, k, v, o, do, lse, causal: bool = False, scale: float | None = No
     args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr())
     ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_ptr(stream))
-    if window is not None:
+    if scores is not None:
+        left, right = (-1, -1) if window is None else window
+        _check(fa_bwd_scores(*args, B, H, hk, S, D, causal, left, right, ctypes.byref(scores), scale, _dtype_code(q),
+                             *ws), "fa_bwd_scores")
+    elif window is not None:
         _check(fa_bwd_window(*args, B, H, hk, S, D, causal, window[0], window[1], scale, _dtype_code(q), *ws),
                "fa_bwd_window")
     elif hk == H:
@@ -469,12 +556,14 @@ def _cu(cu_seqlens, T):
 
 
 def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, scale: float | None = None,
-                   out=None, lse=None, stream=None):
+                   out=None, lse=None, stream=None, window=None, softcap: float | None = None, slopes=None,
+                   prefix=None):
     """O [T, H, D] and L [H, T] of a packed batch (samples cu_seqlens[b] .. cu_seqlens[b+1]-1).
 
     ``max_seqlen`` must bound every sample length (a host integer, so no device
     read is needed); a violation is detected on the device and reported by
-    ``fa_check_device_errors``.
+    ``fa_check_device_errors``.  ``window``, ``softcap``, ``slopes`` [H] and
+    ``prefix`` [batch] as in ``forward``, within each sample.
     """
     import torch
     q = _packed(q, "q")
@@ -487,8 +576,19 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, s
     batch = _cu(cu_seqlens, T)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
+    scores = _scores(q, H, batch, softcap, slopes, prefix, (k, v, out, lse, cu_seqlens))
+    if scores is not None or window is not None:
+        _like(out, q.shape, q.dtype, "out")
+        _like(lse, (H, T), torch.float32, "lse")
     o = torch.empty_like(q) if out is None else out
     l = torch.empty((H, T), dtype=torch.float32, device=q.device) if lse is None else lse
+    if scores is not None or window is not None:
+        left, right = (-1, -1) if window is None else window
+        _check(fa_fwd_scores_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(),
+                                    cu_seqlens.data_ptr(), batch, int(max_seqlen), T, H, hk, D, causal, left, right,
+                                    None if scores is None else ctypes.byref(scores), scale, _dtype_code(q),
+                                    _stream_ptr(stream)), "fa_fwd_scores_varlen")
+        return o, l
     _check(fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(), cu_seqlens.data_ptr(),
                          batch, int(max_seqlen), T, H, hk, D, causal, scale, _dtype_code(q), _stream_ptr(stream)),
            "fa_fwd_varlen")
@@ -496,8 +596,12 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, s
 
 
 def backward_varlen(q, k, v, o, do, lse, cu_seqlens, max_seqlen: int, causal: bool = False,
-                    scale: float | None = None, workspace=None, stream=None):
-    """dQ [T, H, D], dK, dV [T, H_kv, D] of a packed batch from the forward's O and L."""
+                    scale: float | None = None, workspace=None, stream=None, window=None,
+                    softcap: float | None = None, slopes=None, prefix=None):
+    """dQ [T, H, D], dK, dV [T, H_kv, D] of a packed batch from the forward's O and L.
+
+    ``window``, ``softcap``, ``slopes`` and ``prefix`` as the forward had them.
+    """
     import torch
     q, o, do = _packed(q, "q"), _packed(o, "o"), _packed(do, "do")
     T, H, D = q.shape
@@ -508,10 +612,24 @@ def backward_varlen(q, k, v, o, do, lse, cu_seqlens, max_seqlen: int, causal: bo
     batch = _cu(cu_seqlens, T)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
+    scores = _scores(q, H, batch, softcap, slopes, prefix, (k, v, o, do, lse, cu_seqlens, workspace))
+    if scores is not None or window is not None:
+        for t, like, name in ((o, q, "o"), (do, q, "do"), (k, k, "k"), (v, k, "v")):
+            _like(t, like.shape, q.dtype, name)
+        _like(lse, (H, T), torch.float32, "lse")
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
     need = fa_bwd_varlen_workspace_size(batch, int(max_seqlen), T, H, hk, D)
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    if scores is not None or window is not None:
+        left, right = (-1, -1) if window is None else window
+        _check(fa_bwd_scores_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                    cu_seqlens.data_ptr(), batch, int(max_seqlen), T, H, hk, D, causal, left, right,
+                                    None if scores is None else ctypes.byref(scores), scale, _dtype_code(q),
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    _stream_ptr(stream)), "fa_bwd_scores_varlen")
+        return dq, dk, dv
     _check(fa_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
                          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_seqlens.data_ptr(), batch, int(max_seqlen),
                          T, H, hk, D, causal, scale, _dtype_code(q), workspace.data_ptr(),

@@ -232,6 +232,32 @@ fa_status encode_input(CUtensorMap* map, const void* base, bool bf16, const Shap
   return FA_OK;
 }
 
+// Modified scores of a call; *on: they need their own kernels.  (A packed call that
+// may have them takes those whatever they are: they clear what lies behind a sample.)
+fa_status check_scores(const fa_scores* in, float scale, bool prefix_ok, bool packed, bool* on,
+                       fa::ScoreParams* out) {
+  *on = false;
+  *out = fa::ScoreParams{};
+  if (!in) return FA_OK;
+  if (!std::isfinite(in->softcap) || in->softcap < 0)
+    return fail(FA_ERR_INVALID_ARG, "softcap must be finite and not negative (0: none)");
+  if (in->prefix && !prefix_ok) return fail(FA_ERR_UNSUPPORTED, "a prefix is for whole sequences, not for a cache");
+  if ((reinterpret_cast<uintptr_t>(in->slopes) & 3u) != 0) return fail(FA_ERR_ALIGNMENT, "slopes is not 4-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(in->prefix) & 3u) != 0) return fail(FA_ERR_ALIGNMENT, "prefix is not 4-byte aligned");
+  if (in->softcap > 0) {
+    out->cap = in->softcap * kLog2e;
+    out->in = scale / in->softcap;
+    out->in2 = 2.f * kLog2e * out->in;
+    // (beyond these the cap's own arithmetic leaves the range of fp32)
+    if (in->softcap < 1e-10f || in->softcap > 1e10f || !std::isfinite(out->in2))
+      return fail(FA_ERR_UNSUPPORTED, "softcap must be between 1e-10 and 1e10, and scale / softcap finite");
+  }
+  out->slopes = in->slopes;
+  out->prefix = in->prefix;
+  *on = packed || in->softcap > 0 || in->slopes || in->prefix;
+  return FA_OK;
+}
+
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Split-KV: keys per shard (a multiple of 128) and shard count for a request of n splits.
@@ -251,10 +277,13 @@ size_t splitkv_bytes(const Shape& sh, int shards) {
 // into shards whose fp32 partials go to `workspace`, then merged by L.
 fa_status fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, const Shape& sh, int causal,
                    float scale, fa_dtype dtype, void* stream, int64_t split = 0, void* workspace = nullptr,
-                   size_t workspace_bytes = 0) {
+                   size_t workspace_bytes = 0, const fa_scores* scores = nullptr) {
   g_detail[0] = 0;
   fa_status st = check_shape(sh, scale, dtype);
   if (st != FA_OK) return st;
+  bool scored = false;
+  fa::WithScores<fa::FwdParams> p;
+  if ((st = check_scores(scores, scale, true, sh.packed(), &scored, &p.sc))) return st;
   if (sh.empty()) return FA_OK;  // empty: nothing is read or written, pointers may be NULL
   if ((st = check_ptr(q, "q")) || (st = check_ptr(k, "k")) || (st = check_ptr(v, "v")) ||
       (st = check_ptr(o, "o")) || (st = check_ptr(lse, "lse")))
@@ -278,7 +307,6 @@ fa_status fwd_impl(const void* q, const void* k, const void* v, void* o, float* 
   if ((st = encode_input(&tq, q, bf16, sh, sh.H, "q")) || (st = encode_input(&tk, k, bf16, sh, sh.H_kv, "k", 64)) ||
       (st = encode_input(&tv, v, bf16, sh, sh.H_kv, "v", 64)))
     return st;
-  fa::FwdParams p;
   p.o = o;
   p.lse = lse;
   p.S = static_cast<int>(sh.S);
@@ -300,6 +328,10 @@ fa_status fwd_impl(const void* q, const void* k, const void* v, void* o, float* 
   if (!p.err) return fail(FA_ERR_CUDA, "cannot resolve the device error word on the current device");
   p.wait_ns = fa::wait_limit_ns();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (scored)
+    return from_cuda(fa::launch_fwd_scored(static_cast<int>(sh.D), bf16, tq, tk, tv, p,
+                                           static_cast<int>(sh.B * sh.H), s),
+                     "forward launch");
   if ((st = from_cuda(fa::launch_fwd(static_cast<int>(sh.D), bf16, split > 0 || sh.general(causal != 0), tq, tk, tv,
                                      p, static_cast<int>(sh.B * sh.H), s),
                       "forward launch")))
@@ -326,10 +358,14 @@ size_t bwd_workspace_layout(const Shape& sh, int* splits, size_t* delta_bytes) {
 
 fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
                    void* dq, void* dk, void* dv, const Shape& sh, int causal, float scale, fa_dtype dtype,
-                   void* workspace, size_t workspace_bytes, void* stream, void* const* marks) {
+                   void* workspace, size_t workspace_bytes, void* stream, void* const* marks,
+                   const fa_scores* scores = nullptr) {
   g_detail[0] = 0;
   fa_status st = check_shape(sh, scale, dtype);
   if (st != FA_OK) return st;
+  bool scored = false;
+  fa::WithScores<fa::BwdParams> p;
+  if ((st = check_scores(scores, scale, true, sh.packed(), &scored, &p.sc))) return st;
   if (sh.empty()) return FA_OK;  // empty: nothing is read or written, pointers may be NULL
   if ((st = check_ptr(q, "q")) || (st = check_ptr(k, "k")) || (st = check_ptr(v, "v")) ||
       (st = check_ptr(o, "o")) || (st = check_ptr(dout, "dout")) || (st = check_ptr(lse, "lse")) ||
@@ -355,7 +391,6 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, c
       (st = encode_input(&maps.v64, v, bf16, sh, sh.H_kv, "v", 64)) ||
       (st = encode_input(&maps.do64, dout, bf16, sh, sh.H, "dout", 64)))
     return st;
-  fa::BwdParams p;
   p.o = o;
   p.dout = dout;
   p.lse = lse;
@@ -387,27 +422,29 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, c
     if (!marks || !marks[i]) return FA_OK;
     return from_cuda(cudaEventRecord(static_cast<cudaEvent_t>(marks[i]), s), "event record");
   };
-  const bool general = sh.general(causal != 0);
+  const bool general = scored || sh.general(causal != 0);
+  auto pass = [&](bool kv_outer, bool dependent) {
+    if (scored) return fa::launch_bwd_scored(Di, bf16, kv_outer, maps, p, s);
+    return kv_outer ? fa::launch_bwd_dkdv(Di, bf16, general, maps, p, s, dependent)
+                    : fa::launch_bwd_dq(Di, bf16, general, maps, p, s, dependent);
+  };
   const bool fused_delta = fa::bwd_dq_computes_delta(Di, general);
   // Delta then dK/dV then dQ; or, when the dQ kernel computes Delta, dQ then dK/dV.
   if ((st = mark(0))) return st;
   if (fused_delta) {
-    if ((st = from_cuda(fa::launch_bwd_dq(Di, bf16, general, maps, p, s, false), "backward dQ launch"))) return st;
+    if ((st = from_cuda(pass(false, false), "backward dQ launch"))) return st;
   } else if ((st = from_cuda(fa::launch_bwd_preprocess(Di, bf16, p, q_rows, s), "backward preprocess launch"))) {
     return st;
   }
   if ((st = mark(1))) return st;
   // The second and third kernels are programmatic dependent launches: their
   // first CTAs start as the previous kernel's last ones finish.
-  if ((st = from_cuda(fa::launch_bwd_dkdv(Di, bf16, general, maps, p, s, true), "backward dK/dV launch")))
-    return st;
+  if ((st = from_cuda(pass(true, true), "backward dK/dV launch"))) return st;
   if (splits > 1 &&
       (st = from_cuda(fa::launch_bwd_dkv_reduce(Di, bf16, p, kv_rows, s), "backward dK/dV reduce launch")))
     return st;
   if ((st = mark(2))) return st;
-  if (!fused_delta &&
-      (st = from_cuda(fa::launch_bwd_dq(Di, bf16, general, maps, p, s, true), "backward dQ launch")))
-    return st;
+  if (!fused_delta && (st = from_cuda(pass(false, true), "backward dQ launch"))) return st;
   return mark(3);
 }
 
@@ -854,6 +891,45 @@ fa_status fa_bwd_varlen(const void* q, const void* k, const void* v, const void*
                         float scale, fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
   return fa_bwd_varlen_marked(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, batch, max_seqlen, total, H, H_kv, D,
                               causal, scale, dtype, workspace, workspace_bytes, stream, nullptr);
+}
+
+fa_status fa_fwd_scores(const void* q, const void* k, const void* v, void* o, float* lse, int64_t B, int64_t H,
+                        int64_t H_kv, int64_t S, int64_t D, int causal, int64_t window_left, int64_t window_right,
+                        const fa_scores* scores, float scale, fa_dtype dtype, void* stream) {
+  return fwd_impl(q, k, v, o, lse, windowed(B, H, H_kv, S, D, window_left, window_right), causal, scale, dtype, stream,
+                  0, nullptr, 0, scores);
+}
+
+fa_status fa_bwd_scores(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                        const float* lse, void* dq, void* dk, void* dv, int64_t B, int64_t H, int64_t H_kv, int64_t S,
+                        int64_t D, int causal, int64_t window_left, int64_t window_right, const fa_scores* scores,
+                        float scale, fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  return bwd_impl(q, k, v, o, dout, lse, dq, dk, dv, windowed(B, H, H_kv, S, D, window_left, window_right), causal,
+                  scale, dtype, workspace, workspace_bytes, stream, nullptr, scores);
+}
+
+fa_status fa_fwd_scores_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
+                               const int32_t* cu_seqlens, int64_t batch, int64_t max_seqlen, int64_t total, int64_t H,
+                               int64_t H_kv, int64_t D, int causal, int64_t window_left, int64_t window_right,
+                               const fa_scores* scores, float scale, fa_dtype dtype, void* stream) {
+  Shape sh = packed(cu_seqlens, batch, max_seqlen, total, H, H_kv, D);
+  sh.win_left = window_left;
+  sh.win_right = window_right;
+  const fa_scores plain = {};
+  return fwd_impl(q, k, v, o, lse, sh, causal, scale, dtype, stream, 0, nullptr, 0, scores ? scores : &plain);
+}
+
+fa_status fa_bwd_scores_varlen(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                               const float* lse, void* dq, void* dk, void* dv, const int32_t* cu_seqlens,
+                               int64_t batch, int64_t max_seqlen, int64_t total, int64_t H, int64_t H_kv, int64_t D,
+                               int causal, int64_t window_left, int64_t window_right, const fa_scores* scores,
+                               float scale, fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  Shape sh = packed(cu_seqlens, batch, max_seqlen, total, H, H_kv, D);
+  sh.win_left = window_left;
+  sh.win_right = window_right;
+  const fa_scores plain = {};
+  return bwd_impl(q, k, v, o, dout, lse, dq, dk, dv, sh, causal, scale, dtype, workspace, workspace_bytes, stream,
+                  nullptr, scores ? scores : &plain);
 }
 
 fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, const void* dout,

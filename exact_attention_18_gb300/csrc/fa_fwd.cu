@@ -39,6 +39,7 @@
 // Causal: tile t of query rows visits key blocks up to its diagonal block
 // ("T5 讲解" §⑤); masking is element-wise only on the diagonal block and on a
 // ragged last key block ("fa-triton" §Causal Mask 的处理：off-band 与 on-band).
+#include "fa_scores.cuh"
 #include "fa_softmax.cuh"
 
 namespace fa {
@@ -117,11 +118,13 @@ __device__ __forceinline__ float exp_block(const uint32_t* sr, float2 c2, float 
 
 // tm_q: 128-row boxes (a CTA's own query tiles); tm_k, tm_v: 64-row boxes
 // (each K/V block arrives as two half-block copies).  GENERAL: packed
-// batches and windows, as in the four-tile kernel.
-template <int D, bool BF16, bool GENERAL>
+// batches and windows, as in the four-tile kernel; SCORED: modified scores and a
+// prefix, likewise.
+template <int D, bool BF16, bool GENERAL, bool SCORED>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
+                  const __grid_constant__ CUtensorMap tm_v, const ScoredParams<FwdParams, SCORED> p) {
+  static_assert(GENERAL || !SCORED, "modified scores take the general instantiation");
   using L = FwdLayout<D>;
   using elem_t = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
 
@@ -142,6 +145,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   uint64_t* bar_turn = bar_drain + 2;            // [2][4] tile t's warps q may start their exponentials
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
+  // SCORED: a V block whose rows past a packed sample's end are still to be cleared has landed
+  uint64_t* bar_vtmp = reinterpret_cast<uint64_t*>(smem + L::kOffMisc + 8);
 
   const int warp = warp_index();
   const int lane = threadIdx.x & 31;
@@ -170,6 +175,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (row0 >= S) return;  // packed batch: this CTA lies past its sample
   }
   const int n_kv = (S + kBlockN - 1) / kBlockN;
+  int pfx = 0;  // keys before it are visible to every row
+  if constexpr (SCORED) pfx = prefix_len(p.sc, bh / p.heads, S);
   // Window (general instantiation): key j is visible to query i iff i - wl <= j <= i + wr.
   const int wl = GENERAL ? p.win_left : 0;
   const int wr = GENERAL ? p.win_right : 0;
@@ -188,7 +195,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     else return 0;
   };
   auto blocks_for = [&](int r) -> int {
-    if constexpr (GENERAL)
+    if constexpr (SCORED) return r >= S ? 0 : max(min(S - 1, r + kBlockM - 1 + wr), pfx - 1) / kBlockN + 1;
+    else if constexpr (GENERAL)
       return r >= S ? 0 : min((kv_hi + kBlockN - 1) / kBlockN, min(S - 1, r + kBlockM - 1 + wr) / kBlockN + 1);
     else return r >= S ? 0 : (p.causal ? min(n_kv, (r + kBlockM + kBlockN - 1) / kBlockN) : n_kv);
   };
@@ -201,6 +209,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int nb0 = end0 - beg0;
   const int nb1 = end1 - beg1;
   const int nbp = max(end0, end1);  // blocks the CTA loads
+  // As in the four-tile kernel: V rows past a packed sample's end are set to zero.
+  const bool clear_v = SCORED && packed && nbp > 0 && (kb_cta + nbp) * kBlockN > S;
   // TMA coordinates of `row` of `head` (x = column offset): (x, row, head) in
   // the {D, S, heads} maps, (x, head, tok0 + row) in the packed {D, heads, T} maps.
   auto tma_rows = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int x, int row, int head) {
@@ -230,6 +240,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     mbar_init(&bar_drain[0], 1);
     mbar_init(&bar_drain[1], 1);
     for (int i = 0; i < 8; ++i) mbar_init(&bar_turn[i], 1);
+    if constexpr (SCORED) mbar_init(bar_vtmp, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -279,13 +290,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const int sv = nv % L::kStagesV;
           const int uv = nv / L::kStagesV;
           if (uv > 0 && !mbar_wait(&bar_vempty[sv], (uv - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad)) break;
-          mbar_arrive_expect_tx(&bar_vfull[sv], L::kTileBytes);
+          uint64_t* vbar = SCORED && clear_v && nv == nbp - 1 ? bar_vtmp : &bar_vfull[sv];
+          mbar_arrive_expect_tx(vbar, L::kTileBytes);
 #pragma unroll
           for (int ch = 0; ch < L::kChunks; ++ch)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               tma_rows(smem + L::kOffV + sv * L::kTileBytes + ch * L::kChunkBytes + h * kHalfBytes, &tm_v,
-                       &bar_vfull[sv], ch * (L::kRowBytes / 2), (kb_cta + nv) * kBlockN + h * (kBlockN / 2), kvh);
+                       vbar, ch * (L::kRowBytes / 2), (kb_cta + nv) * kBlockN + h * (kBlockN / 2), kvh);
         }
         // Teardown: every copy this thread started must land before the CTA
         // exits (older copies of a ring were consumed before their stage was
@@ -293,6 +305,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         drain_wait(bar_q, 0, p.err);
         for (int x = (nk > L::kStagesK ? nk - L::kStagesK : 0); x < nk; ++x)
           drain_wait(&bar_kfull[x % L::kStagesK], (x / L::kStagesK) & 1, p.err);
+        if (SCORED && clear_v && nv == nbp) drain_wait(bar_vtmp, 0, p.err);
         for (int x = (nv > L::kStagesV ? nv - L::kStagesV : 0); x < nv; ++x)
           drain_wait(&bar_vfull[x % L::kStagesV], (x / L::kStagesV) & 1, p.err);
       }
@@ -373,6 +386,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       // Teardown: wait for every MMA this warp issued.
       mma_commit_warp(&bar_drain[t]);
       drain_wait(&bar_drain[t], 0, p.err);
+    } else if (SCORED && clear_v) {
+      // ------------------------------------------------------------ the last V block's cleared rows
+      const int st = (nbp - 1) % L::kStagesV;
+      if (warp_wait(bar_vtmp, 0, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad)) {
+        clear_rows<typename L::G>(smem + L::kOffV + st * L::kTileBytes, kBlockN, S - (kb_cta + nbp - 1) * kBlockN);
+        if (lane == 0) mbar_arrive(&bar_vfull[st]);
+      }
     }
   } else {
     regs_increase<kRegsHigh>();
@@ -389,11 +409,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t t_s = tmem + lane_base + L::kColS + 128u * t;
     const uint32_t t_p = tmem + lane_base + L::kColP + L::kStrideP * t;
     const uint32_t t_o = tmem + lane_base + L::kColO + D * t;
-    const float sl2 = p.scale_log2;
+    const float sl2 = SCORED ? 1.f : p.scale_log2;  // (modified scores are scaled)
     const float2 c2 = make_float2(sl2, sl2);
-    const bool neg_scale = sl2 < 0.f;
+    const bool neg_scale = !SCORED && sl2 < 0.f;
+    float slope = 0.f;
+    if constexpr (SCORED) {
+      if (p.sc.slopes != nullptr) slope = __ldg(p.sc.slopes + bh % p.heads) * 1.4426950408889634f;
+    }
     // Last (and, general instantiation, first) visible key of this row.
-    const int last = GENERAL ? min(S - 1, row_g + wr) : (p.causal ? min(S - 1, row_g) : S - 1);
+    const int last = SCORED    ? max(min(S - 1, row_g + wr), pfx - 1)
+                     : GENERAL ? min(S - 1, row_g + wr)
+                               : (p.causal ? min(S - 1, row_g) : S - 1);
     const int first_key = row_g - wl;
     float m = -INFINITY;  // running (possibly stale) maximum, base-2 scaled
     float l = 0.f;
@@ -412,9 +438,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const int lo = first_key - kv0;  // and (general instantiation) c >= lo
       // Masked blocks: the diagonal block under the causal mask (an edge of
       // the window band), and a ragged last key block.
-      const bool masked = GENERAL ? (kv0 + kBlockN > S) || (kv0 + kBlockN - 1 > tile_row0 + wr) ||
+      const bool masked = GENERAL ? (kv0 + kBlockN > S) || (kv0 + kBlockN - 1 > (SCORED ? max(tile_row0 + wr, pfx - 1) : tile_row0 + wr)) ||
                                         (kv0 < tile_row0 + kBlockM - 1 - wl)
                                   : (kv0 + kBlockN > S) || (p.causal && kv0 + kBlockN - 1 > tile_row0);
+      if constexpr (SCORED) {
+        // (causal: what lies behind the row is hidden, whatever its bias)
+        const ScoreSide side = kv0 + kBlockN - 1 <= tile_row0 || (p.causal && pfx == 0) ? kSideLeft
+                               : kv0 >= tile_row0 + kBlockM - 1                         ? kSideRight
+                                                                                        : kSideBoth;
+        score_row<kBlockN>(sr, p.sc, p.scale_log2, slope, kv0 - row_g, side);
+      }
       if (j == 0) m = block_max_scaled<kBlockN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
       // The two tiles' warps of one sub-partition take turns at the
       // exponentials, so one's loads, stores and waits overlap the other's.
@@ -530,11 +563,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 }
 
 namespace {
-template <int D, bool BF16, bool GENERAL>
-cudaError_t launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams& p,
-                         int BH, cudaStream_t stream) {
+template <int D, bool BF16, bool GENERAL, bool SCORED = false>
+cudaError_t launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                         const ScoredParams<FwdParams, SCORED>& p, int BH, cudaStream_t stream) {
   using L = FwdLayout<D>;
-  auto kern = fa_fwd_kernel<D, BF16, GENERAL>;
+  auto kern = fa_fwd_kernel<D, BF16, GENERAL, SCORED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
   if (e != cudaSuccess) return e;
   // The register split above assumes the launch gives exactly kLaunchRegs per
@@ -570,6 +603,13 @@ cudaError_t launch_fwd(int D, bool bf16, bool general, const CUtensorMap& tq, co
       return cudaErrorInvalidValue;
   }
 #undef FA_FWD_CASE
+}
+
+cudaError_t launch_fwd_scored(int D, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const WithScores<FwdParams>& p, int BH, cudaStream_t stream) {
+  if (D != 128) return launch_fwd4_scored(D, bf16, tq, tk, tv, p, BH, stream);
+  return bf16 ? launch_fwd_t<128, true, true, true>(tq, tk, tv, p, BH, stream)
+              : launch_fwd_t<128, false, true, true>(tq, tk, tv, p, BH, stream);
 }
 
 }  // namespace fa

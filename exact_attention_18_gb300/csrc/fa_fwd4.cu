@@ -48,6 +48,7 @@
 // blocks crossing either edge of the band are masked element-wise on both
 // sides.  GENERAL = false is the fixed-length full/causal kernel, kept free of
 // that bookkeeping.
+#include "fa_scores.cuh"
 #include "fa_softmax.cuh"
 
 namespace fa {
@@ -109,10 +110,12 @@ struct F4Layout {
 }  // namespace
 
 // tm_q: 128-row boxes (the CTA's query tiles); tm_k, tm_v: 64-row boxes.
-template <int D, bool BF16, bool GENERAL>
+// SCORED: modified scores and a prefix (the general instantiation's rows and blocks).
+template <int D, bool BF16, bool GENERAL, bool SCORED>
 __global__ void __launch_bounds__(kF4Threads, 1)
     fa_fwd4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
+                   const __grid_constant__ CUtensorMap tm_v, const ScoredParams<FwdParams, SCORED> p) {
+  static_assert(GENERAL || !SCORED, "modified scores take the general instantiation");
   using L = F4Layout<D, GENERAL>;
   using GQ = typename L::GQ;
   using GK = typename L::GK;
@@ -132,6 +135,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   uint64_t* bar_drain = bar_ofinal + kF4Tiles;    // one per MMA warp
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
+  // SCORED: a V block whose rows past a packed sample's end are still to be cleared has landed
+  uint64_t* bar_vtmp = reinterpret_cast<uint64_t*>(smem + L::kOffMisc + 8);
 
   const int warp = warp_index();
   const int lane = threadIdx.x & 31;
@@ -158,6 +163,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     if (row0 >= S) return;  // packed batch: this CTA lies past its sample
   }
   const int n_kv = (S + kBN - 1) / kBN;
+  int pfx = 0;  // keys before it are visible to every row
+  if constexpr (SCORED) pfx = prefix_len(p.sc, bh / p.heads, S);
   // Window (general instantiation): key j is visible to query i iff i - wl <= j <= i + wr.
   const int wl = GENERAL ? p.win_left : 0;
   const int wr = GENERAL ? p.win_right : 0;
@@ -177,13 +184,18 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     else return 0;
   };
   auto blocks_for = [&](int r) -> int {
-    if constexpr (GENERAL) return r >= S ? 0 : min((kv_hi + kBN - 1) / kBN, min(S - 1, r + kBlockM - 1 + wr) / kBN + 1);
+    if constexpr (SCORED) return r >= S ? 0 : max(min(S - 1, r + kBlockM - 1 + wr), pfx - 1) / kBN + 1;
+    else if constexpr (GENERAL)
+      return r >= S ? 0 : min((kv_hi + kBN - 1) / kBN, min(S - 1, r + kBlockM - 1 + wr) / kBN + 1);
     else return r >= S ? 0 : (p.causal ? min(n_kv, (r + kBlockM + kBN - 1) / kBN) : n_kv);
   };
   const int kb_cta = first_blk(row0);  // the CTA loads key blocks kb_cta, kb_cta + 1, ...
   int nbp = 0;                         // blocks the CTA loads
 #pragma unroll
   for (int t = 0; t < kF4Tiles; ++t) nbp = max(nbp, blocks_for(row0 + t * kBlockM) - kb_cta);
+  // Rows of the last V block past a packed sample's end belong to the next sample
+  // or to none, and may hold NaN: they are set to zero (0 * NaN is not 0).
+  const bool clear_v = SCORED && packed && nbp > 0 && (kb_cta + nbp) * kBN > S;
   // TMA coordinates of `row` of `head`: (row, head) in the {D, S, heads}
   // maps, (head, tok0 + row) in the packed {D, heads, T} maps.
   auto tma_rows = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int row, int head) {
@@ -206,6 +218,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       mbar_init(&bar_ofinal[t], 1);
     }
     for (int w = 0; w < kF4MmaWarps; ++w) mbar_init(&bar_drain[w], 1);
+    if constexpr (SCORED) mbar_init(bar_vtmp, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -240,14 +253,16 @@ __global__ void __launch_bounds__(kF4Threads, 1)
           if (use > 0 && !mbar_wait(&bar_empty[st], (use - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad)) break;
           mbar_arrive_expect_tx(&bar_kfull[st], GK::kTileBytes);
           tma_rows(smem + L::kOffK + st * GK::kTileBytes, &tm_k, &bar_kfull[st], (kb_cta + it) * kBN, kvh);
-          mbar_arrive_expect_tx(&bar_vfull[st], GK::kTileBytes);
-          tma_rows(smem + L::kOffV + st * GK::kTileBytes, &tm_v, &bar_vfull[st], (kb_cta + it) * kBN, kvh);
+          uint64_t* vbar = SCORED && clear_v && it == nbp - 1 ? bar_vtmp : &bar_vfull[st];
+          mbar_arrive_expect_tx(vbar, GK::kTileBytes);
+          tma_rows(smem + L::kOffV + st * GK::kTileBytes, &tm_v, vbar, (kb_cta + it) * kBN, kvh);
         }
         // Teardown: every copy this thread started must land before the CTA exits.
         drain_wait(bar_q, 0, p.err);
         for (int x = (it > L::kStages ? it - L::kStages : 0); x < it; ++x) {
           const int st = x % L::kStages;
           drain_wait(&bar_kfull[st], (x / L::kStages) & 1, p.err);
+          if (SCORED && clear_v && x == nbp - 1) drain_wait(bar_vtmp, 0, p.err);
           drain_wait(&bar_vfull[st], (x / L::kStages) & 1, p.err);
         }
       }
@@ -416,6 +431,13 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       // Teardown: wait for every MMA this warp issued.
       mma_commit_warp(&bar_drain[w]);
       drain_wait(&bar_drain[w], 0, p.err);
+    } else if (SCORED && clear_v) {
+      // ------------------------------------------------------------ the last V block's cleared rows
+      const int st = (nbp - 1) % L::kStages;
+      if (warp_wait(bar_vtmp, 0, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad)) {
+        clear_rows<GK>(smem + L::kOffV + st * GK::kTileBytes, kBN, S - (kb_cta + nbp - 1) * kBN);
+        if (lane == 0) mbar_arrive(&bar_vfull[st]);
+      }
     }
   } else {
     regs_increase<kF4RegsHigh>();
@@ -430,11 +452,17 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t t_s = tmem + lane_base + 128u * t;  // S_t, and P_t over it
     const uint32_t t_o = t_s + L::kColO;
-    const float sl2 = p.scale_log2;
+    const float sl2 = SCORED ? 1.f : p.scale_log2;  // (modified scores are scaled)
     const float2 c2 = make_float2(sl2, sl2);
-    const bool neg_scale = sl2 < 0.f;
+    const bool neg_scale = !SCORED && sl2 < 0.f;
+    float slope = 0.f;
+    if constexpr (SCORED) {
+      if (p.sc.slopes != nullptr) slope = __ldg(p.sc.slopes + bh % p.heads) * 1.4426950408889634f;
+    }
     // Last (and, general instantiation, first) visible key of this row.
-    const int last = GENERAL ? min(S - 1, row_g + wr) : (p.causal ? min(S - 1, row_g) : S - 1);
+    const int last = SCORED    ? max(min(S - 1, row_g + wr), pfx - 1)
+                     : GENERAL ? min(S - 1, row_g + wr)
+                               : (p.causal ? min(S - 1, row_g) : S - 1);
     const int first_key = row_g - wl;
     float m = -INFINITY;  // running (possibly stale) maximum, base-2 scaled
     float l = 0.f;
@@ -453,8 +481,16 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       // Masked blocks: those crossing the diagonal under the causal mask (an
       // edge of the window band), and a ragged last key block.
       const bool masked =
-          GENERAL ? (kv0 + kBN > S) || (kv0 + kBN - 1 > tile_row0 + wr) || (kv0 < tile_row0 + kBlockM - 1 - wl)
+          GENERAL ? (kv0 + kBN > S) || (kv0 + kBN - 1 > (SCORED ? max(tile_row0 + wr, pfx - 1) : tile_row0 + wr)) ||
+                        (kv0 < tile_row0 + kBlockM - 1 - wl)
                   : (kv0 + kBN > S) || (p.causal && kv0 + kBN - 1 > tile_row0);
+      if constexpr (SCORED) {
+        // (causal: what lies behind the row is hidden, whatever its bias)
+        const ScoreSide side = kv0 + kBN - 1 <= tile_row0 || (p.causal && pfx == 0) ? kSideLeft
+                               : kv0 >= tile_row0 + kBlockM - 1                     ? kSideRight
+                                                                                    : kSideBoth;
+        score_row<kBN>(sr, p.sc, p.scale_log2, slope, kv0 - row_g, side);
+      }
       if (j == 0) m = block_max_scaled<kBN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
       float alpha = 1.f;
       bool upd = false;
@@ -577,11 +613,11 @@ __global__ void __launch_bounds__(kF4Threads, 1)
 }
 
 namespace {
-template <int D, bool BF16, bool GENERAL>
-cudaError_t launch_fwd4_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams& p,
-                          int BH, cudaStream_t stream) {
+template <int D, bool BF16, bool GENERAL, bool SCORED = false>
+cudaError_t launch_fwd4_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          const ScoredParams<FwdParams, SCORED>& p, int BH, cudaStream_t stream) {
   using L = F4Layout<D, GENERAL>;
-  auto kern = fa_fwd4_kernel<D, BF16, GENERAL>;
+  auto kern = fa_fwd4_kernel<D, BF16, GENERAL, SCORED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
   if (e != cudaSuccess) return e;
   // The register split assumes the launch gives exactly kF4LaunchRegs per
@@ -613,6 +649,22 @@ cudaError_t launch_fwd4(int D, bool bf16, bool general, const CUtensorMap& tq, c
                   : launch_fwd4_t<DD, false, true>(tq, tk, tv, p, BH, stream);                 \
     return bf16 ? launch_fwd4_t<DD, true, false>(tq, tk, tv, p, BH, stream)                    \
                 : launch_fwd4_t<DD, false, false>(tq, tk, tv, p, BH, stream);
+  switch (D) {
+    FA_FWD4_CASE(16)
+    FA_FWD4_CASE(32)
+    FA_FWD4_CASE(64)
+    default:
+      return cudaErrorInvalidValue;
+  }
+#undef FA_FWD4_CASE
+}
+
+cudaError_t launch_fwd4_scored(int D, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const WithScores<FwdParams>& p, int BH, cudaStream_t stream) {
+#define FA_FWD4_CASE(DD)                                                       \
+  case DD:                                                                     \
+    return bf16 ? launch_fwd4_t<DD, true, true, true>(tq, tk, tv, p, BH, stream) \
+                : launch_fwd4_t<DD, false, true, true>(tq, tk, tv, p, BH, stream);
   switch (D) {
     FA_FWD4_CASE(16)
     FA_FWD4_CASE(32)

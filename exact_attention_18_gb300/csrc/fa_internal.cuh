@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace fa {
 
 constexpr int kBlockM = 128;  // query rows per tile (= TMEM lanes)
@@ -65,6 +67,22 @@ struct BwdParams {
   unsigned long long wait_ns;  // limit of each pipeline wait (fa_set_wait_limit_ns)
 };
 
+// Modified scores (fa_scores.cuh has the mathematics).
+struct ScoreParams {
+  float cap;            // cap * log2 e; 0: no cap
+  float in;             // scale / cap: v = in * x
+  float in2;            // 2 log2 e scale / cap: e^(2v) = 2^(in2 x)
+  const float* slopes;  // [H] in device memory, natural units; nullptr: no bias
+  const int* prefix;    // [B] in device memory: keys before prefix[b] are visible to all rows; nullptr: none
+};
+// A kernel's parameters with (SCORED) or without those of the scores.
+template <typename P>
+struct WithScores : P {
+  ScoreParams sc;
+};
+template <typename P, bool SCORED>
+using ScoredParams = typename std::conditional<SCORED, WithScores<P>, P>::type;
+
 // Tensor maps of the backward's four inputs, each viewed as 3-D {D, S, heads}
 // (B*H heads for Q and dO, B*H_kv for K and V):
 // 128-row boxes for a CTA's resident tiles, 64-row boxes for streamed blocks.
@@ -89,6 +107,12 @@ cudaError_t launch_fwd4p(int D, bool bf16, const CUtensorMap& tq, const CUtensor
 cudaError_t launch_fwd(int D, bool bf16, bool general, const CUtensorMap& tq, const CUtensorMap& tk,
                        const CUtensorMap& tv, const FwdParams& p, int BH, cudaStream_t stream);
 
+// The same with modified scores (general instantiations).
+cudaError_t launch_fwd4_scored(int D, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const WithScores<FwdParams>& p, int BH, cudaStream_t stream);
+cudaError_t launch_fwd_scored(int D, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const WithScores<FwdParams>& p, int BH, cudaStream_t stream);
+
 // rows: query rows (B*H*S, or T*H packed).
 // Split-KV merge: O = sum_s exp(L_s - L) O_s, L = ln sum_s exp(L_s), per row.
 cudaError_t launch_merge_lse(int D, bool bf16, const float* o_part, const float* lse_part, int shards, int64_t rows,
@@ -105,6 +129,10 @@ cudaError_t launch_bwd_dkdv(int D, bool bf16, bool general, const BwdMaps& maps,
                             cudaStream_t stream, bool dependent);
 cudaError_t launch_bwd_dq(int D, bool bf16, bool general, const BwdMaps& maps, const BwdParams& p,
                           cudaStream_t stream, bool dependent);
+// The dK/dV (kv_outer) or dQ pass with modified scores, always as a programmatic
+// dependent of the kernel before it.
+cudaError_t launch_bwd_scored(int D, bool bf16, bool kv_outer, const BwdMaps& maps, const WithScores<BwdParams>& p,
+                              cudaStream_t stream);
 // True when launch_bwd_dq's kernel computes Delta itself and writes it to p.delta
 // (the persistent dQ kernel): the backward then skips the Delta kernel and runs
 // the dQ pass before the dK/dV pass, which reads that Delta.

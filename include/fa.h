@@ -286,6 +286,62 @@ fa_status fa_bwd_varlen_marked(const void* q, const void* k, const void* v, cons
                                int causal, float scale, fa_dtype dtype, void* workspace, size_t workspace_bytes,
                                void* stream, void* const* marks);
 
+/* ------------------------------------------------------------------------
+ * Modified scores.  The score of query i and key j,
+ *
+ *     s_ij = cap * tanh(scale * q_i . k_j / cap) - slopes[h] * |i - j|
+ *
+ * stands in the place of scale * q_i . k_j; either part may be absent.  i and j
+ * are positions within the sequence (sample).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  float softcap;         /* cap > 0, from 1e-10 to 1e10; 0: scores are not capped */
+  const float* slopes;   /* DEVICE fp32 [H], one finite slope per query head, any sign; NULL: no bias */
+  const int32_t* prefix; /* DEVICE int32 [B] (packed: [batch]), or NULL: keys j < prefix[b] are visible to
+                            every query of the sequence, as far as the window's left side allows */
+} fa_scores;
+
+/*
+ * fa_fwd_window with modified scores: key j is visible to query i iff
+ * i - window_left <= j and (j <= i + window_right or j < prefix[b]), a negative
+ * side being unlimited and `causal` making the right side 0.  Prefix lengths may
+ * lie outside [0, S]: they count as the nearer end.  scores == NULL, or all of
+ * its parts absent, runs fa_fwd_window.  The window's sides and `causal` hide keys
+ * whatever the scores there are.  tanh is evaluated in fp32: a score is off by
+ * about 2^-20 of itself where |scale q.k| <= cap, by 2^-21 of cap beyond.
+ * Slopes must be finite and slopes[h] * S far below fp32's largest number.
+ */
+fa_status fa_fwd_scores(const void* q, const void* k, const void* v, void* o, float* lse, int64_t B, int64_t H,
+                        int64_t H_kv, int64_t S, int64_t D, int causal, int64_t window_left, int64_t window_right,
+                        const fa_scores* scores, float scale, fa_dtype dtype, void* stream);
+
+/*
+ * Its gradient: dq, dk, dv as fa_bwd_gqa, through the cap's derivative
+ * 1 - tanh^2(scale q.k / cap).  Slopes and prefix lengths are constants of the
+ * call and get no gradient.  Workspace: fa_bwd_gqa_workspace_size() bytes.
+ */
+fa_status fa_bwd_scores(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                        const float* lse, void* dq, void* dk, void* dv, int64_t B, int64_t H, int64_t H_kv, int64_t S,
+                        int64_t D, int causal, int64_t window_left, int64_t window_right, const fa_scores* scores,
+                        float scale, fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Both for packed batches (fa_fwd_varlen's layout and checks), with a window
+ * inside each sample: documents of a training batch, each its own sequence, with
+ * a prefix length each.  What tokens behind the last sample hold, NaN included,
+ * has no say.  Workspace of the backward: fa_bwd_varlen_workspace_size() bytes.
+ */
+fa_status fa_fwd_scores_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
+                               const int32_t* cu_seqlens, int64_t batch, int64_t max_seqlen, int64_t total, int64_t H,
+                               int64_t H_kv, int64_t D, int causal, int64_t window_left, int64_t window_right,
+                               const fa_scores* scores, float scale, fa_dtype dtype, void* stream);
+
+fa_status fa_bwd_scores_varlen(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                               const float* lse, void* dq, void* dk, void* dv, const int32_t* cu_seqlens,
+                               int64_t batch, int64_t max_seqlen, int64_t total, int64_t H, int64_t H_kv, int64_t D,
+                               int causal, int64_t window_left, int64_t window_right, const fa_scores* scores,
+                               float scale, fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * fa_bwd without a workspace argument, for callers that cannot allocate
  * device memory when they run the backward pass (for example code inside a
