@@ -11,7 +11,8 @@ The raw entry points keep the C names and signatures (pointers as ints):
 ``fa_fwd_window``, ``fa_bwd_window``, ``fa_bwd_window_marked``, ``fa_fwd_splitkv``,
 ``fa_fwd_splitkv_workspace_size``, ``fa_splitkv_num_splits``, ``fa_merge_lse``,
 ``fa_fwd_varlen``, ``fa_bwd_varlen``, ``fa_bwd_varlen_marked``,
-``fa_bwd_varlen_workspace_size``, ``fa_status_string``, ``fa_last_error_detail``,
+``fa_bwd_varlen_workspace_size``, ``fa_fwd_scores``, ``fa_bwd_scores``,
+``fa_fwd_scores_varlen``, ``fa_bwd_scores_varlen``, ``fa_status_string``, ``fa_last_error_detail``,
 ``fa_check_device_errors``, ``fa_set_wait_limit_ns``.  ``forward`` and ``backward`` wrap them for
 contiguous [B, H, S, D] CUDA tensors; K and V (and dK, dV) may have fewer heads
 H_kv dividing H (grouped-query and multi-query attention), in which case they
@@ -147,6 +148,10 @@ def _load():
     lib.fa_paged_append.argtypes = [vp, i64] * 4 + [vp] * 4 + [i64] * 7 + [i32, f32, i32, vp]
     lib.fa_fwd_paged.restype = i32
     lib.fa_fwd_paged.argtypes = [vp] * 5 + [i64] * 7 + [i32, i64, i64, f32, i32, vp, sz, vp]
+    lib.fa_fwd_paged_scores.restype = i32
+    lib.fa_fwd_paged_scores.argtypes = [vp] * 5 + [i64] * 7 + [i32, i64, i64, vp, f32, i32, vp, sz, vp]
+    lib.fa_fwd_paged_tree.restype = i32
+    lib.fa_fwd_paged_tree.argtypes = [vp] * 7 + [i64] * 10 + [vp, f32, i32, vp, sz, vp]
     lib.fa_fwd_paged_workspace_size.restype = sz
     lib.fa_fwd_paged_workspace_size.argtypes = [i64] * 6
     lib.fa_status_string.restype = ctypes.c_char_p
@@ -353,6 +358,22 @@ def fa_fwd_paged(q, o, lse, cache, cu_seqlens, batch, max_seqlen_q, max_seqlen_k
     return _load().fa_fwd_paged(q, o, lse, cache, cu_seqlens, batch, max_seqlen_q, max_seqlen_k, total, H, H_kv, D,
                                 int(causal), int(window_left), int(window_right), float(scale), int(dtype), workspace,
                                 workspace_bytes, stream)
+
+
+def fa_fwd_paged_scores(q, o, lse, cache, cu_seqlens, batch, max_seqlen_q, max_seqlen_k, total, H, H_kv, D, causal,
+                        window_left, window_right, scores, scale, dtype, workspace, workspace_bytes, stream) -> int:
+    """``cache``: a PagedCache, ``scores``: a Scores, passed by reference."""
+    return _load().fa_fwd_paged_scores(q, o, lse, cache, cu_seqlens, batch, max_seqlen_q, max_seqlen_k, total, H, H_kv,
+                                       D, int(causal), int(window_left), int(window_right), scores, float(scale),
+                                       int(dtype), workspace, workspace_bytes, stream)
+
+
+def fa_fwd_paged_tree(q, o, lse, cache, cu_seqlens, positions, tree, tree_stride, tree_words, batch, max_seqlen_q,
+                      max_seqlen_k, total, H, H_kv, D, window_left, scores, scale, dtype, workspace, workspace_bytes,
+                      stream) -> int:
+    return _load().fa_fwd_paged_tree(q, o, lse, cache, cu_seqlens, positions, tree, tree_stride, tree_words, batch,
+                                     max_seqlen_q, max_seqlen_k, total, H, H_kv, D, int(window_left), scores,
+                                     float(scale), int(dtype), workspace, workspace_bytes, stream)
 
 
 def fa_fwd_paged_workspace_size(batch, max_seqlen_q, max_seqlen_k, H, H_kv, D) -> int:
@@ -772,7 +793,7 @@ def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_s
 
 def forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q: int, max_seqlen_k: int,
                   causal: bool = True, window=None, scale: float | None = None, out=None, lse=None, workspace=None,
-                  stream=None):
+                  stream=None, softcap: float | None = None, slopes=None, tree=None, positions=None):
     """O [T, H, D] and L [H, T] of new tokens q [T, H, D] over a paged cache (arguments as ``paged_append``).
 
     Query i of a sequence's n new tokens stands at key kv_lens - n + i.
@@ -780,13 +801,21 @@ def forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seq
     on ``kv_lens`` and may be loose; a violation, or a bad page, is found on the device and
     reported by ``fa_check_device_errors``.  Without ``workspace`` the call uses
     scratch kept for its stream (its own while a graph is captured).
+
+    ``softcap`` and ``slopes`` [H] modify the scores as in ``forward``.  Drafted
+    tokens that form a tree: int32 ``tree`` [T, words], whose row of new token i
+    has bit j % 32 of word j // 32 set where it sees new token j of its sequence,
+    and int32 ``positions`` [T], where each stands (the first new key plus its
+    depth).  They see all keys before the new ones, from the window's left side on.
     """
     if stream is not None:
         import torch
         with torch.cuda.stream(stream):
             return forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q, max_seqlen_k,
-                                 causal, window, scale, out, lse, workspace)
+                                 causal, window, scale, out, lse, workspace, None, softcap, slopes, tree,
+                                 positions)
     left, right = (-1, -1) if window is None else window
     return _result((_binding or _load_binding()).forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens,
                                                                max_seqlen_q, max_seqlen_k, causal, left, right, scale,
-                                                               out, lse, workspace), "fa_fwd_paged")
+                                                               out, lse, workspace, softcap, slopes, tree,
+                                                               positions), "fa_fwd_paged")

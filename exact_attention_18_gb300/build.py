@@ -31,6 +31,7 @@ BINDING_FOR = os.path.join(BUILD_DIR, "fa_binding.for")  # what the binding was 
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd4.cu", "fa_fwd4p.cu", "fa_bwd.cu", "fa_bwd_scores.cu", "fa_merge.cu", "fa_rope.cu",
            "fa_paged_d16.cu", "fa_paged_d32.cu", "fa_paged_d64.cu", "fa_paged_d128.cu",
+           "fa_paged_scores_d16.cu", "fa_paged_scores_d32.cu", "fa_paged_scores_d64.cu", "fa_paged_scores_d128.cu",
            "fa_paged_merge.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE,

@@ -730,6 +730,152 @@ fa_status encode_paged_kv(CUtensorMap* map, const void* base, bool bf16, const f
   return FA_OK;
 }
 
+// The drafted trees of a call.
+struct Tree {
+  const int32_t* positions;
+  const uint32_t* rows;
+  int64_t stride, words;
+};
+
+fa_status paged_fwd_impl(const void* q, void* o, float* lse, const fa_paged_cache* cache, const int32_t* cu_seqlens,
+                         int64_t batch, int64_t max_seqlen_q, int64_t max_seqlen_k, int64_t total, int64_t H,
+                         int64_t H_kv, int64_t D, int causal, int64_t window_left, int64_t window_right, float scale,
+                         fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream,
+                         const fa_scores* scores, const Tree* tree) {
+  g_detail[0] = 0;
+  fa_status st;
+  if ((st = check_dtype_d(D, dtype)) || (st = check_tokens(total, H, H_kv)) || (st = check_heads(H, H_kv))) return st;
+  if (!std::isfinite(scale)) return fail(FA_ERR_INVALID_ARG, "scale must be finite");
+  fa::PagedScoredParams p = {};
+  bool scored = false;
+  if ((st = check_scores(scores, scale, false, false, &scored, &p.sc))) return st;
+  scored = scored || tree;
+  if (batch < 0 || max_seqlen_q < 0 || max_seqlen_k < 0)
+    return fail(FA_ERR_INVALID_ARG, "negative size: batch=%lld max_seqlen_q=%lld max_seqlen_k=%lld", (long long)batch,
+                (long long)max_seqlen_q, (long long)max_seqlen_k);
+  if (batch == 0 || max_seqlen_q == 0 || total == 0 || H == 0) return FA_OK;
+  if (max_seqlen_q > fa::kMaxPagedLen || max_seqlen_k > fa::kMaxPagedLen)
+    return fail(FA_ERR_UNSUPPORTED, "max_seqlen_q and max_seqlen_k must be at most 2^29");
+  if (H / H_kv > 128) return fail(FA_ERR_UNSUPPORTED, "more than 128 query heads to a K/V head");
+  if ((st = check_ptr(q, "q")) || (st = check_ptr(o, "o")) || (st = check_ptr(lse, "lse")) ||
+      (st = check_cache(cache, H_kv, D)) || (st = check_ints(cu_seqlens, "cu_seqlens", 4)))
+    return st;
+  if (tree) {
+    if ((st = check_ints(tree->positions, "positions", 4)) || (st = check_ints(tree->rows, "tree", 4))) return st;
+    const int64_t most = max_seqlen_q < total ? max_seqlen_q : total;
+    if (tree->words < (most + 31) / 32 || tree->stride < tree->words)
+      return fail(FA_ERR_INVALID_ARG, "tree rows of %lld words, %lld apart, for up to %lld new tokens",
+                  (long long)tree->words, (long long)tree->stride, (long long)most);
+    if (tree->stride >= (int64_t(1) << 31)) return fail(FA_ERR_UNSUPPORTED, "tree_stride must be below 2^31");
+    p.tree = tree->rows;
+    p.positions = tree->positions;
+    p.tree_stride = tree->stride;
+    p.tree_words = static_cast<int>(tree->words);
+  }
+  // No sequence has more new tokens than there are, or more keys than its row of
+  // the table holds, however loose the bounds.
+  const int64_t most_q = max_seqlen_q < total ? max_seqlen_q : total;
+  const int64_t most_k = max_seqlen_k < table_keys(cache) ? max_seqlen_k : table_keys(cache);
+  PagedPlan plan;
+  if (!paged_plan(batch, most_q, most_k, H, H_kv, D, true, &plan))
+    return fail(FA_ERR_UNSUPPORTED, "batch and lengths too large");
+  const int shift = log2_of(cache->page_size);
+  if (!workspace) return fail(FA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", plan.bytes);
+  if (workspace_bytes < plan.bytes)
+    return fail(FA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, plan.bytes);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(FA_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
+  const bool bf16 = dtype == FA_BF16;
+  const int64_t G = H / H_kv;
+  p.o = o;
+  p.lse = lse;
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = cache->kv_lens;
+  p.block_table = cache->block_table;
+  p.table_stride = cache->table_stride;
+  p.batch = static_cast<int>(batch);
+  p.H = static_cast<int>(H);
+  p.H_kv = static_cast<int>(H_kv);
+  p.G = static_cast<int>(G);
+  p.total = static_cast<int>(total);
+  p.max_q = static_cast<int>(max_seqlen_q);
+  p.max_k = static_cast<int>(most_k);
+  p.win_left = window_left < 0 || window_left >= max_seqlen_k ? fa::kNoWindow : static_cast<int>(window_left);
+  p.win_right =
+      causal ? 0 : (window_right < 0 || window_right >= max_seqlen_k + max_seqlen_q ? fa::kNoWindow : static_cast<int>(window_right));
+  p.page_shift = shift;
+  p.num_pages = static_cast<int>(cache->num_pages);
+  p.scale_log2 = scale * kLog2e;
+  p.err = fa::device_error_word();
+  if (!p.err) return fail(FA_ERR_CUDA, "cannot resolve the device error word on the current device");
+  p.wait_ns = fa::wait_limit_ns();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  fa::PagedMergeParams mp = {};
+  mp.o = o;
+  mp.lse = lse;
+  mp.G = p.G;
+  mp.H = p.H;
+  mp.total = p.total;
+  if (plan.few.used && plan.tile.used) {
+    p.go = mp.go = reinterpret_cast<unsigned long long*>(ws + plan.go_at);
+    p.ticket = launch_ticket();
+  }
+  int sets = 0, grid = 0;
+  auto run = [&](const PagedPart& part, bool tile) -> fa_status {
+    p.tok_tile = part.tok_tile;
+    p.tiles = part.tiles;
+    p.tok_lo = part.tok_lo;
+    p.tok_hi = part.tok_hi;
+    p.small = part.small;
+    p.sub_tok = static_cast<int>(128 / G);
+    p.costs = fa::paged_costs(static_cast<int>(D));
+    p.part_rows = part.part_rows;
+    p.after_tile = !tile && plan.tile.used;
+    p.o_part = reinterpret_cast<float*>(ws + part.o_at);
+    p.lse_part = reinterpret_cast<float*>(ws + part.lse_at);
+    p.desc = reinterpret_cast<int4*>(ws + part.desc_at);
+    mp.parts[sets++] = fa::PagedParts{p.o_part, p.lse_part, p.desc, part.part_rows, part.grid, tile ? 1 : 0};
+    if (part.grid > grid) grid = part.grid;
+    const int Di = static_cast<int>(D);
+    const int64_t block = tile ? fa::paged_tile_block(Di) : 128;
+    CUtensorMap tq, tk, tv;
+    fa_status r;
+    if ((r = encode_paged_q(&tq, q, bf16, total, H, D, G, tile ? static_cast<int>(128 / G) : part.tok_tile)) ||
+        (r = encode_paged_kv(&tk, cache->k, bf16, cache, H_kv, D, block, "cache.k")) ||
+        (r = encode_paged_kv(&tv, cache->v, bf16, cache, H_kv, D, block, "cache.v")))
+      return r;
+    cudaError_t e = cudaErrorInvalidValue;
+    if (scored) {
+      switch (D) {
+        case 16: e = fa::launch_paged_scored_d16(part.N, tile, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 32: e = fa::launch_paged_scored_d32(part.N, tile, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 64: e = fa::launch_paged_scored_d64(part.N, tile, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 128: e = fa::launch_paged_scored_d128(part.N, tile, bf16, tq, tk, tv, p, part.grid, s); break;
+      }
+    } else if (tile) {
+      switch (D) {
+        case 16: e = fa::launch_paged_tile_d16(bf16, tq, tk, tv, p, part.grid, s); break;
+        case 32: e = fa::launch_paged_tile_d32(bf16, tq, tk, tv, p, part.grid, s); break;
+        case 64: e = fa::launch_paged_tile_d64(bf16, tq, tk, tv, p, part.grid, s); break;
+        case 128: e = fa::launch_paged_tile_d128(bf16, tq, tk, tv, p, part.grid, s); break;
+      }
+    } else {
+      switch (D) {
+        case 16: e = fa::launch_paged_d16(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 32: e = fa::launch_paged_d32(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 64: e = fa::launch_paged_d64(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
+        case 128: e = fa::launch_paged_d128(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
+      }
+    }
+    return from_cuda(e, "paged attention launch");
+  };
+  // The long sequences first: the few-row kernel's CTAs start as theirs end.
+  if (plan.tile.used && (st = run(plan.tile, true))) return st;
+  if (plan.few.used && (st = run(plan.few, false))) return st;
+  return from_cuda(fa::launch_paged_merge(static_cast<int>(D), bf16, mp, grid, sets, s), "paged merge launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -1099,116 +1245,28 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
                        int64_t batch, int64_t max_seqlen_q, int64_t max_seqlen_k, int64_t total, int64_t H,
                        int64_t H_kv, int64_t D, int causal, int64_t window_left, int64_t window_right, float scale,
                        fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
-  g_detail[0] = 0;
-  fa_status st;
-  if ((st = check_dtype_d(D, dtype)) || (st = check_tokens(total, H, H_kv)) || (st = check_heads(H, H_kv))) return st;
-  if (!std::isfinite(scale)) return fail(FA_ERR_INVALID_ARG, "scale must be finite");
-  if (batch < 0 || max_seqlen_q < 0 || max_seqlen_k < 0)
-    return fail(FA_ERR_INVALID_ARG, "negative size: batch=%lld max_seqlen_q=%lld max_seqlen_k=%lld", (long long)batch,
-                (long long)max_seqlen_q, (long long)max_seqlen_k);
-  if (batch == 0 || max_seqlen_q == 0 || total == 0 || H == 0) return FA_OK;
-  if (max_seqlen_q > fa::kMaxPagedLen || max_seqlen_k > fa::kMaxPagedLen)
-    return fail(FA_ERR_UNSUPPORTED, "max_seqlen_q and max_seqlen_k must be at most 2^29");
-  if (H / H_kv > 128) return fail(FA_ERR_UNSUPPORTED, "more than 128 query heads to a K/V head");
-  if ((st = check_ptr(q, "q")) || (st = check_ptr(o, "o")) || (st = check_ptr(lse, "lse")) ||
-      (st = check_cache(cache, H_kv, D)) || (st = check_ints(cu_seqlens, "cu_seqlens", 4)))
-    return st;
-  // No sequence has more new tokens than there are, or more keys than its row of
-  // the table holds, however loose the bounds.
-  const int64_t most_q = max_seqlen_q < total ? max_seqlen_q : total;
-  const int64_t most_k = max_seqlen_k < table_keys(cache) ? max_seqlen_k : table_keys(cache);
-  PagedPlan plan;
-  if (!paged_plan(batch, most_q, most_k, H, H_kv, D, true, &plan))
-    return fail(FA_ERR_UNSUPPORTED, "batch and lengths too large");
-  const int shift = log2_of(cache->page_size);
-  if (!workspace) return fail(FA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", plan.bytes);
-  if (workspace_bytes < plan.bytes)
-    return fail(FA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, plan.bytes);
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-    return fail(FA_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
-  const bool bf16 = dtype == FA_BF16;
-  const int64_t G = H / H_kv;
-  fa::PagedParams p = {};
-  p.o = o;
-  p.lse = lse;
-  p.cu_seqlens = cu_seqlens;
-  p.kv_lens = cache->kv_lens;
-  p.block_table = cache->block_table;
-  p.table_stride = cache->table_stride;
-  p.batch = static_cast<int>(batch);
-  p.H = static_cast<int>(H);
-  p.H_kv = static_cast<int>(H_kv);
-  p.G = static_cast<int>(G);
-  p.total = static_cast<int>(total);
-  p.max_q = static_cast<int>(max_seqlen_q);
-  p.max_k = static_cast<int>(most_k);
-  p.win_left = window_left < 0 || window_left >= max_seqlen_k ? fa::kNoWindow : static_cast<int>(window_left);
-  p.win_right =
-      causal ? 0 : (window_right < 0 || window_right >= max_seqlen_k + max_seqlen_q ? fa::kNoWindow : static_cast<int>(window_right));
-  p.page_shift = shift;
-  p.num_pages = static_cast<int>(cache->num_pages);
-  p.scale_log2 = scale * kLog2e;
-  p.err = fa::device_error_word();
-  if (!p.err) return fail(FA_ERR_CUDA, "cannot resolve the device error word on the current device");
-  p.wait_ns = fa::wait_limit_ns();
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  char* ws = static_cast<char*>(workspace);
-  fa::PagedMergeParams mp = {};
-  mp.o = o;
-  mp.lse = lse;
-  mp.G = p.G;
-  mp.H = p.H;
-  mp.total = p.total;
-  if (plan.few.used && plan.tile.used) {
-    p.go = mp.go = reinterpret_cast<unsigned long long*>(ws + plan.go_at);
-    p.ticket = launch_ticket();
-  }
-  int sets = 0, grid = 0;
-  auto run = [&](const PagedPart& part, bool tile) -> fa_status {
-    p.tok_tile = part.tok_tile;
-    p.tiles = part.tiles;
-    p.tok_lo = part.tok_lo;
-    p.tok_hi = part.tok_hi;
-    p.small = part.small;
-    p.sub_tok = static_cast<int>(128 / G);
-    p.costs = fa::paged_costs(static_cast<int>(D));
-    p.part_rows = part.part_rows;
-    p.after_tile = !tile && plan.tile.used;
-    p.o_part = reinterpret_cast<float*>(ws + part.o_at);
-    p.lse_part = reinterpret_cast<float*>(ws + part.lse_at);
-    p.desc = reinterpret_cast<int4*>(ws + part.desc_at);
-    mp.parts[sets++] = fa::PagedParts{p.o_part, p.lse_part, p.desc, part.part_rows, part.grid, tile ? 1 : 0};
-    if (part.grid > grid) grid = part.grid;
-    const int Di = static_cast<int>(D);
-    const int64_t block = tile ? fa::paged_tile_block(Di) : 128;
-    CUtensorMap tq, tk, tv;
-    fa_status r;
-    if ((r = encode_paged_q(&tq, q, bf16, total, H, D, G, tile ? static_cast<int>(128 / G) : part.tok_tile)) ||
-        (r = encode_paged_kv(&tk, cache->k, bf16, cache, H_kv, D, block, "cache.k")) ||
-        (r = encode_paged_kv(&tv, cache->v, bf16, cache, H_kv, D, block, "cache.v")))
-      return r;
-    cudaError_t e = cudaErrorInvalidValue;
-    if (tile) {
-      switch (D) {
-        case 16: e = fa::launch_paged_tile_d16(bf16, tq, tk, tv, p, part.grid, s); break;
-        case 32: e = fa::launch_paged_tile_d32(bf16, tq, tk, tv, p, part.grid, s); break;
-        case 64: e = fa::launch_paged_tile_d64(bf16, tq, tk, tv, p, part.grid, s); break;
-        case 128: e = fa::launch_paged_tile_d128(bf16, tq, tk, tv, p, part.grid, s); break;
-      }
-    } else {
-      switch (D) {
-        case 16: e = fa::launch_paged_d16(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
-        case 32: e = fa::launch_paged_d32(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
-        case 64: e = fa::launch_paged_d64(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
-        case 128: e = fa::launch_paged_d128(part.N, bf16, tq, tk, tv, p, part.grid, s); break;
-      }
-    }
-    return from_cuda(e, "paged attention launch");
-  };
-  // The long sequences first: the few-row kernel's CTAs start as theirs end.
-  if (plan.tile.used && (st = run(plan.tile, true))) return st;
-  if (plan.few.used && (st = run(plan.few, false))) return st;
-  return from_cuda(fa::launch_paged_merge(static_cast<int>(D), bf16, mp, grid, sets, s), "paged merge launch");
+  return paged_fwd_impl(q, o, lse, cache, cu_seqlens, batch, max_seqlen_q, max_seqlen_k, total, H, H_kv, D, causal,
+                        window_left, window_right, scale, dtype, workspace, workspace_bytes, stream, nullptr, nullptr);
+}
+
+fa_status fa_fwd_paged_scores(const void* q, void* o, float* lse, const fa_paged_cache* cache,
+                              const int32_t* cu_seqlens, int64_t batch, int64_t max_seqlen_q, int64_t max_seqlen_k,
+                              int64_t total, int64_t H, int64_t H_kv, int64_t D, int causal, int64_t window_left,
+                              int64_t window_right, const fa_scores* scores, float scale, fa_dtype dtype,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_fwd_impl(q, o, lse, cache, cu_seqlens, batch, max_seqlen_q, max_seqlen_k, total, H, H_kv, D, causal,
+                        window_left, window_right, scale, dtype, workspace, workspace_bytes, stream, scores, nullptr);
+}
+
+fa_status fa_fwd_paged_tree(const void* q, void* o, float* lse, const fa_paged_cache* cache,
+                            const int32_t* cu_seqlens, const int32_t* positions, const uint32_t* tree,
+                            int64_t tree_stride, int64_t tree_words, int64_t batch, int64_t max_seqlen_q,
+                            int64_t max_seqlen_k, int64_t total, int64_t H, int64_t H_kv, int64_t D,
+                            int64_t window_left, const fa_scores* scores, float scale, fa_dtype dtype,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  const Tree t{positions, tree, tree_stride, tree_words};
+  return paged_fwd_impl(q, o, lse, cache, cu_seqlens, batch, max_seqlen_q, max_seqlen_k, total, H, H_kv, D, 0,
+                        window_left, -1, scale, dtype, workspace, workspace_bytes, stream, scores, &t);
 }
 
 const char* fa_status_string(fa_status status) {

@@ -106,6 +106,12 @@ const void* ints(const Tensor& x, at::ScalarType type, int64_t n, const char* na
   return x.const_data_ptr();
 }
 
+const void* floats(const Tensor& x, int64_t n, const char* name) {
+  if (x.scalar_type() != at::kFloat || x.dim() != 1 || x.size(0) != n || !x.is_contiguous())
+    throw BadValue(std::string(name) + " must be a contiguous 1-D float32 tensor of " + std::to_string(n) + " entries");
+  return x.const_data_ptr();
+}
+
 int64_t offsets(const Tensor& cu) {
   require(cu.scalar_type() == at::kInt && cu.dim() == 1 && cu.size(0) >= 1 && cu.is_contiguous(),
           "cu_seqlens must be a contiguous 1-D int32 tensor [batch + 1]");
@@ -293,17 +299,18 @@ PyObject* paged_append(PyObject*, PyObject* const* argv, Py_ssize_t n) {
 }
 
 // forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q, max_seqlen_k, causal, left,
-//               right, scale, out, lse, workspace)
+//               right, scale, out, lse, workspace, softcap, slopes, tree, positions)
 PyObject* forward_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    require(n == 15, "forward_paged: fifteen arguments");
+    require(n == 19, "forward_paged: nineteen arguments");
     const Args a{argv, n};
     const Tensor &q = a.tensor(0, "q"), &kc = a.tensor(1, "k_cache"), &vc = a.tensor(2, "v_cache"),
                  &table = a.tensor(3, "block_table"), &lens = a.tensor(4, "kv_lens"), &cu = a.tensor(5, "cu_seqlens");
-    const Tensor *o = a.maybe(12, "out"), *l = a.maybe(13, "lse"), *ws = a.maybe(14, "workspace");
+    const Tensor *o = a.maybe(12, "out"), *l = a.maybe(13, "lse"), *ws = a.maybe(14, "workspace"),
+                 *slopes = a.maybe(16, "slopes"), *tree = a.maybe(17, "tree"), *pos = a.maybe(18, "positions");
     const OneDevice dev(q);
     for (const Tensor* x : {&kc, &vc, &table, &lens, &cu}) dev.also(*x);
-    for (const Tensor* x : {o, l, ws}) dev.also(x);
+    for (const Tensor* x : {o, l, ws, slopes, tree, pos}) dev.also(x);
     require(q.dim() == 3 && q.is_contiguous(), "q must be a contiguous tensor [T, H, D]");
     require(kc.dim() == 4, "k_cache must be [pages, page_size, H_kv, D]");
     const int64_t T = q.size(0), H = q.size(1), D = q.size(2), hk = kc.size(2);
@@ -319,6 +326,25 @@ PyObject* forward_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     require(!ws || ws->is_contiguous(), "workspace must be contiguous");
     const int64_t max_q = a.integer(6), max_k = a.integer(7), left = a.integer(9), right = a.integer(10);
     const bool causal = a.flag(8);
+    fa_scores scores = {};
+    if (argv[15] != Py_None) {
+      scores.softcap = static_cast<float>(a.real(15));
+      require(scores.softcap > 0, "softcap must be positive (None: no cap)");
+    }
+    if (slopes) scores.slopes = static_cast<const float*>(floats(*slopes, H, "slopes"));
+    const bool modified = scores.softcap > 0 || slopes;
+    require(!tree == !pos, "tree and positions belong together");
+    int64_t words = 0, row_stride = 0;
+    if (tree) {
+      require(causal, "a tree's rows say what its tokens see: causal stays true");
+      require(right <= 0, "a tree has the window's left side alone");
+      require(tree->scalar_type() == at::kInt && tree->dim() == 2 && tree->size(0) == T &&
+                  (tree->stride(1) == 1 || tree->size(1) <= 1) && (T <= 1 || tree->stride(0) >= tree->size(1)),
+              "tree must be an int32 tensor [T, words] with dense rows");
+      words = tree->size(1);
+      row_stride = T > 1 ? tree->stride(0) : words;
+      ints(*pos, at::kInt, T, "positions");
+    }
     const float scale = argv[11] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)))
                                             : static_cast<float>(a.real(11));
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream().stream();
@@ -327,14 +353,25 @@ PyObject* forward_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     const Tensor out = o ? *o : empty(q.sizes(), type, q), lse = l ? *l : empty({H, T}, at::kFloat, q);
     const void *q_at = q.const_data_ptr(), *cu_at = cu.const_data_ptr();
     void *o_at = out.mutable_data_ptr(), *l_at = lse.mutable_data_ptr(), *work_at = work.mutable_data_ptr();
+    const void *tree_at = tree ? tree->const_data_ptr() : nullptr, *pos_at = tree ? pos->const_data_ptr() : nullptr;
     const size_t work_bytes = work.nbytes();
     fa_status st;
     {
       const Unlocked unlocked;
       std::unique_lock<std::mutex> turn(scratch_order(), std::defer_lock);  // (ends before the interpreter's is taken)
       if (!ws) turn.lock();
-      st = fa_fwd_paged(q_at, o_at, static_cast<float*>(l_at), &cache, static_cast<const int32_t*>(cu_at), batch, max_q,
-                        max_k, T, H, hk, D, causal, left, right, scale, code, work_at, work_bytes, stream);
+      const auto* offs = static_cast<const int32_t*>(cu_at);
+      float* l_out = static_cast<float*>(l_at);
+      if (tree)
+        st = fa_fwd_paged_tree(q_at, o_at, l_out, &cache, offs, static_cast<const int32_t*>(pos_at),
+                               static_cast<const uint32_t*>(tree_at), row_stride, words, batch, max_q, max_k, T, H, hk,
+                               D, left, &scores, scale, code, work_at, work_bytes, stream);
+      else if (modified)
+        st = fa_fwd_paged_scores(q_at, o_at, l_out, &cache, offs, batch, max_q, max_k, T, H, hk, D, causal, left, right,
+                                 &scores, scale, code, work_at, work_bytes, stream);
+      else
+        st = fa_fwd_paged(q_at, o_at, l_out, &cache, offs, batch, max_q, max_k, T, H, hk, D, causal, left, right, scale,
+                          code, work_at, work_bytes, stream);
     }
     return st == FA_OK ? pair(out, lse) : PyLong_FromLong(st);
   });

@@ -446,7 +446,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const ScoreSide side = kv0 + kBlockN - 1 <= tile_row0 || (p.causal && pfx == 0) ? kSideLeft
                                : kv0 >= tile_row0 + kBlockM - 1                         ? kSideRight
                                                                                         : kSideBoth;
-        score_row<kBlockN>(sr, p.sc, p.scale_log2, slope, kv0 - row_g, side);
+        cap_row<kBlockN>(sr, p.sc, p.scale_log2);
+        if (p.sc.slopes != nullptr) bias_row<kBlockN>(sr, slope, kv0 - row_g, side);
       }
       if (j == 0) m = block_max_scaled<kBlockN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
       // The two tiles' warps of one sub-partition take turns at the

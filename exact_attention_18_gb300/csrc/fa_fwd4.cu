@@ -489,7 +489,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         const ScoreSide side = kv0 + kBN - 1 <= tile_row0 || (p.causal && pfx == 0) ? kSideLeft
                                : kv0 >= tile_row0 + kBlockM - 1                     ? kSideRight
                                                                                     : kSideBoth;
-        score_row<kBN>(sr, p.sc, p.scale_log2, slope, kv0 - row_g, side);
+        cap_row<kBN>(sr, p.sc, p.scale_log2);
+        if (p.sc.slopes != nullptr) bias_row<kBN>(sr, slope, kv0 - row_g, side);
       }
       if (j == 0) m = block_max_scaled<kBN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
       float alpha = 1.f;

@@ -80,6 +80,7 @@ cudaError_t launch_rope(RopeParams p, bool bf16, bool append, int batch, cudaStr
 // tokens, K/V head): its rows are tok_tile tokens x G query heads, its work the
 // blocks of keys its rows can see.
 struct PagedParams {
+  static constexpr bool kScored = false;
   void* o;               // [T, H, D]
   float* lse;            // [H, T] natural log
   const int* cu_seqlens;
@@ -108,6 +109,20 @@ struct PagedParams {
                          // {first token, tokens (0 = none), K/V head, last CTA}
   int* err;
   unsigned long long wait_ns;
+};
+
+// The same with modified scores and, where `tree` is set, drafted trees: new token i
+// of a sequence stands at positions[i], held to the sequence's new key positions
+// [first, kv_len), first = kv_len - n.  It sees the keys before `first` from its
+// position minus win_left on, and new token j where bit j % 32 of word j / 32 of its
+// row is set; win_right does not count (it is kNoWindow).
+struct PagedScoredParams : PagedParams {
+  static constexpr bool kScored = true;
+  ScoreParams sc;
+  const unsigned* tree;  // [T] rows of tree_words words, tree_stride apart; nullptr: no trees
+  const int* positions;  // [T]; with trees only
+  int64_t tree_stride;
+  int tree_words;
 };
 
 // One main kernel's partials; parts[z] is joined by grid slice z.
@@ -161,6 +176,15 @@ cudaError_t launch_paged_tile_d64(bool bf16, const CUtensorMap& tq, const CUtens
                                   const PagedParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_paged_tile_d128(bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                   const PagedParams& p, int grid, cudaStream_t stream);
+// Either kernel with modified scores: the tile kernel, or the few-row one for N rows.
+cudaError_t launch_paged_scored_d16(int N, bool tile, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, const PagedScoredParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_paged_scored_d32(int N, bool tile, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, const PagedScoredParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_paged_scored_d64(int N, bool tile, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, const PagedScoredParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_paged_scored_d128(int N, bool tile, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, const PagedScoredParams& p, int grid, cudaStream_t stream);
 // `sets` of parts.
 cudaError_t launch_paged_merge(int D, bool bf16, const PagedMergeParams& p, int grid, int sets, cudaStream_t stream);
 cudaError_t launch_paged_d16(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -6,13 +6,13 @@ namespace fa {
 
 cudaError_t launch_paged_d64(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const PagedParams& p, int grid, cudaStream_t stream) {
-  return launch_paged_n<64>(N, bf16, tq, tk, tv, p, grid, stream);
+  return launch_paged_n<64, PagedParams>(N, bf16, tq, tk, tv, p, grid, stream);
 }
 
 cudaError_t launch_paged_tile_d64(bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                   const PagedParams& p, int grid, cudaStream_t stream) {
-  return bf16 ? launch_paged_tile_t<64, true>(tq, tk, tv, p, grid, stream)
-              : launch_paged_tile_t<64, false>(tq, tk, tv, p, grid, stream);
+  return bf16 ? launch_paged_tile_t<64, true, PagedParams>(tq, tk, tv, p, grid, stream)
+              : launch_paged_tile_t<64, false, PagedParams>(tq, tk, tv, p, grid, stream);
 }
 
 }  // namespace fa

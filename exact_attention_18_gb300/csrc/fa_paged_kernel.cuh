@@ -47,6 +47,7 @@
 #pragma once
 
 #include "fa_paged_units.cuh"
+#include "fa_scores.cuh"
 #include "fa_softmax.cuh"
 
 namespace fa {
@@ -89,7 +90,7 @@ struct PagedLayout {
   static constexpr int kOffSmall = kOffQ + 2 * kQBytes;
   // full[U], empty[U], qfull[2], qempty[2], sfull[2], pfull[2], pv[2], vtmp, drain
   static constexpr int kNumBars = 2 * kUnits + 10 + 2;
-  static_assert(kNumBars * 8 + 24 + sizeof(RunStart) + 8 * N * 4 + 2 * N <= kSmallBytes, "small arrays");
+  static_assert(kNumBars * 8 + 24 + sizeof(RunStart) + 10 * N * 4 + 2 * N <= kSmallBytes, "small arrays");
   // The request is padded so that no more CTAs than meant share an SM, nor one
   // of these with a kernel that takes the whole tensor memory (those ask for
   // 116 KB at least).
@@ -136,10 +137,12 @@ __device__ __forceinline__ uint32_t swizzled(int k, int c) {
 
 // tm_q: {D, H, T} map, box {row chunk, G, tok_tile}; tm_k, tm_v: {D, H_kv,
 // page_size, pages} maps, box {row chunk, 1, min(page_size, 128), 1}.
-template <int D, int N, bool BF16>
+// Params: PagedParams, or PagedScoredParams for modified scores and drafted trees.
+template <int D, int N, bool BF16, typename Params>
 __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>::kCtas)
     fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                    const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
+                    const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  constexpr bool kScored = Params::kScored;
   using L = PagedLayout<D, N>;
   using GK = typename L::GK;
   using GQ = typename L::GQ;
@@ -171,6 +174,8 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
   float* s_red = s_alpha + N;       // [N][4] per-warp partial of each row
   int* s_off = reinterpret_cast<int*>(s_red + 4 * N);     // [N] output row of row n after its unit's first
   short* s_tok = reinterpret_cast<short*>(s_off + N);     // [N] token of row n
+  int* s_pos = reinterpret_cast<int*>(s_tok + N);         // scored: [N] position of row n
+  float* s_slope = reinterpret_cast<float*>(s_pos + N);   // scored: [N] its head's slope, base 2
 
   // Behind the tile kernel of the same call this grid's CTAs start as that
   // kernel's end, and work beside the last of them once they have its word that
@@ -392,7 +397,9 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     float* red_s = s_red + g * NC * 4;
     const short* tok_s = s_tok + g * NC;
     const int* off_s = s_off + g * NC;
-    const float c = p.scale_log2;
+    const int* pos_s = s_pos + g * NC;
+    const float* slope_s = s_slope + g * NC;
+    const float c = kScored ? 1.f : p.scale_log2;  // (modified scores are scaled)
     const float2 c2 = make_float2(c, c);
     // This warpgroup's columns of the P^T tile.
     uint8_t* p_tile = smem + L::kOffP;
@@ -407,7 +414,22 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
       const int blk_first = u.lo / kPBlk + w.blk;
       // Blocks every row sees whole: keys in [full_lo, full_hi).
       const int full_lo = max(0, u.pos0 + u.n_tok - 1 - p.win_left);
-      const int full_hi = min(u.kv_len, u.pos0 + 1 + p.win_right);
+      int full_hi = min(u.kv_len, u.pos0 + 1 + p.win_right);
+      // Scored: the sequence's first new token, its key, and whether it is a tree's.
+      // (A sequence of this kernel has one tile: first == u.pos0.)
+      bool tree = false;
+      if constexpr (kScored) {
+        tree = p.tree != nullptr;
+        if (tree) full_hi = min(full_hi, u.pos0);
+        if (wt < NC) {
+          const int row = g * NC + wt;
+          int pos = u.pos0 + tok_s[wt];
+          if (tree && row < n_rows) pos = min(u.kv_len - 1, max(u.pos0, p.positions[u.tok0 + tok_s[wt]]));
+          s_pos[row] = pos;
+          s_slope[row] = p.sc.slopes != nullptr ? p.sc.slopes[w.kvh * p.G + row % p.G] * 1.4426950408889634f : 0.f;
+        }
+        named_sync(bar_id, 128);
+      }
 #pragma unroll
       for (int k = 0; k < NC; ++k) l[k] = 0.f;
       // Rows past the unit's hold other tokens' queries, or what shared memory held.
@@ -433,7 +455,32 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
           tmem_ld16(t_s + (i & 1) * N, sr);
         }
         float2 cc = c2;
-        if (cut && ok) {
+        if constexpr (kScored) {
+          if (ok) {
+            cap_row<NC>(sr, p.sc, p.scale_log2);
+            const bool drafted = tree && key >= u.pos0 && key < u.kv_len;
+            if (p.sc.slopes != nullptr) {
+              const int kp = drafted ? min(u.kv_len - 1, max(u.pos0, p.positions[u.tok0 + key - u.pos0])) : key;
+#pragma unroll
+              for (int k = 0; k < NC; ++k)
+                sr[k] = __float_as_uint(
+                    fmaf(-slope_s[k], fabsf(static_cast<float>(kp - pos_s[k])), __uint_as_float(sr[k])));
+            }
+            if (cut) {
+              const int j = key - u.pos0;  // new token of the key
+#pragma unroll
+              for (int k = 0; k < NC; ++k) {
+                const int pos = pos_s[k];
+                bool hidden = key >= u.kv_len || key < pos - p.win_left;
+                if (!tree) hidden = hidden || key > pos + p.win_right;
+                else if (drafted)
+                  hidden = g * NC + k >= n_rows ||
+                           !(p.tree[(u.tok0 + tok_s[k]) * p.tree_stride + (j >> 5)] >> (j & 31) & 1u);
+                if (hidden) sr[k] = __float_as_uint(-INFINITY);
+              }
+            }
+          }
+        } else if (cut && ok) {
           // The scaled scores in place of the scores (cc = 1 from here on),
           // -inf where the row does not see the key.
           cc = make_float2(1.f, 1.f);
@@ -614,26 +661,26 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
 
 namespace {
 
-template <int D, int N, bool BF16>
-cudaError_t launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+template <int D, int N, bool BF16, typename Params>
+cudaError_t launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Params& p,
                            int grid, cudaStream_t stream) {
   using L = PagedLayout<D, N>;
-  auto kern = fa_paged_kernel<D, N, BF16>;
+  auto kern = fa_paged_kernel<D, N, BF16, Params>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(grid), L::kThreads, L::kSmemBytes, stream, tq, tk, tv, p);
 }
 
-template <int D>
+template <int D, typename Params>
 cudaError_t launch_paged_n(int N, bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                           const PagedParams& p, int grid, cudaStream_t s) {
+                           const Params& p, int grid, cudaStream_t s) {
   switch (N) {
-    case 16: return bf16 ? launch_paged_t<D, 16, true>(tq, tk, tv, p, grid, s)
-                         : launch_paged_t<D, 16, false>(tq, tk, tv, p, grid, s);
-    case 32: return bf16 ? launch_paged_t<D, 32, true>(tq, tk, tv, p, grid, s)
-                         : launch_paged_t<D, 32, false>(tq, tk, tv, p, grid, s);
-    case 64: return bf16 ? launch_paged_t<D, 64, true>(tq, tk, tv, p, grid, s)
-                         : launch_paged_t<D, 64, false>(tq, tk, tv, p, grid, s);
+    case 16: return bf16 ? launch_paged_t<D, 16, true, Params>(tq, tk, tv, p, grid, s)
+                         : launch_paged_t<D, 16, false, Params>(tq, tk, tv, p, grid, s);
+    case 32: return bf16 ? launch_paged_t<D, 32, true, Params>(tq, tk, tv, p, grid, s)
+                         : launch_paged_t<D, 32, false, Params>(tq, tk, tv, p, grid, s);
+    case 64: return bf16 ? launch_paged_t<D, 64, true, Params>(tq, tk, tv, p, grid, s)
+                         : launch_paged_t<D, 64, false, Params>(tq, tk, tv, p, grid, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -27,6 +27,7 @@
 #pragma once
 
 #include "fa_paged_units.cuh"
+#include "fa_scores.cuh"
 #include "fa_softmax.cuh"
 
 namespace fa {
@@ -94,8 +95,8 @@ struct TileSpan {
   int beg, end;    // its blocks: beg, beg + turns, .. end - 1
 };
 
-template <int SHIFT, int TILES>
-__device__ __forceinline__ TileSpan tile_span(const PagedParams& p, const SegWalk<SHIFT, true>& w, int t, int tile_tok,
+template <int SHIFT, int TILES, typename P>
+__device__ __forceinline__ TileSpan tile_span(const P& p, const SegWalk<SHIFT, true>& w, int t, int tile_tok,
                                               int n) {
   TileSpan s;
   s.tiles = (w.u.n_tok + tile_tok - 1) / tile_tok;
@@ -107,7 +108,11 @@ __device__ __forceinline__ TileSpan tile_span(const PagedParams& p, const SegWal
   s.pos0 = w.u.pos0 + s.ta;
   s.beg = s.end = 0;
   if (s.turn >= s.turns) return s;
-  const int lo = max(0, s.pos0 - p.win_left), hi = min(w.u.kv_len, s.pos0 + s.n_tok + p.win_right);
+  int lo = max(0, s.pos0 - p.win_left);
+  const int hi = min(w.u.kv_len, s.pos0 + s.n_tok + p.win_right);
+  if constexpr (P::kScored) {
+    if (p.tree != nullptr) lo = w.u.lo;  // (any of the unit's rows may stand at the first new key)
+  }
   if (hi <= lo) return s;
   const int base = (w.u.lo >> SHIFT) + w.blk;  // the segment's first block
   const int beg = min(n, max(0, (lo >> SHIFT) - base));
@@ -118,14 +123,31 @@ __device__ __forceinline__ TileSpan tile_span(const PagedParams& p, const SegWal
   return s;
 }
 
+// Columns of a tree that a row sees among 32 keys: the first is new token b0 (below
+// 0: a key before them, and seen from column `from` on), `rest` keys are left.
+__device__ __forceinline__ unsigned tree_word(const unsigned* row, int words, int b0, int rest, int from) {
+  unsigned x = ~0u;
+  if (b0 > -32) {
+    const int i = b0 >> 5;  // -1 .. : the word that holds b0
+    const unsigned a = i < 0 ? ~0u : (row != nullptr && i < words ? row[i] : 0u);
+    const unsigned b = row != nullptr && i + 1 < words ? row[i + 1] : 0u;
+    x = __funnelshift_r(a, b, b0 & 31);
+  }
+  if (rest < 32) x &= rest <= 0 ? 0u : (1u << rest) - 1u;
+  if (from > 0) x &= from >= 32 ? 0u : ~0u << from;
+  return x;
+}
+
 }  // namespace
 
 // tm_q: {D, H, T} map, box {row chunk, G, tile tokens}; tm_k, tm_v: {D, H_kv,
 // page_size, pages} maps, box {row chunk, 1, min(page_size, block), 1}.
-template <int D, bool BF16>
+// Params: PagedParams, or PagedScoredParams for modified scores and drafted trees.
+template <int D, bool BF16, typename Params>
 __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     fa_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
+                         const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  constexpr bool kScored = Params::kScored;
   using L = PagedTileLayout<D>;
   using GQ = typename L::GQ;
   using GK = typename L::GK;
@@ -399,21 +421,22 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     const int rt = r / p.G, rh = r - rt * p.G;  // its token within the tile, head within the group
     const uint32_t t_s = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + t * L::kTileCols;
     const uint32_t t_o = t_s + L::kColO;
-    const float sl2 = p.scale_log2;
+    const float sl2 = kScored ? 1.f : p.scale_log2;  // (modified scores are scaled)
     // Blocks that a mask cuts.  D <= 64: the scores a row does not see become
     // -inf (+inf under a negative scale) in place, and one copy of the code
     // serves all blocks; a copy of its own for the few cut ones cost up to 5000
     // cycles of instruction fetch per unit (ragged chunks 129 -> 121 us).  At
     // D = 128 the selects between load and maximum cost more than that (chunks
     // of 2048: 668 us with a copy of its own, 723 in place).
-    constexpr bool kMaskInPlace = D <= 64;
+    // Modified scores are formed in place anyhow.
+    constexpr bool kMaskInPlace = D <= 64 || kScored;
     constexpr bool kShare = T == 4;  // tiles may share a unit's row tile
     // In place, a scale of 0 is applied ahead of the mask (0 times a hidden key's
     // infinity would not be -inf); a NaN stays one.
-    const bool zero_scale = kMaskInPlace && sl2 == 0.f;
+    const bool zero_scale = !kScored && kMaskInPlace && sl2 == 0.f;
     const float ce = zero_scale ? 1.f : sl2;
     const float2 c2 = make_float2(ce, ce);
-    const bool neg_scale = sl2 < 0.f;
+    const bool neg_scale = !kScored && sl2 < 0.f;
     const uint32_t hidden = __float_as_uint(neg_scale ? INFINITY : -INFINITY);
     int cnt = 0, fin = 0;  // blocks of this tile so far; segments in which it had blocks
     bool alive = true;
@@ -424,11 +447,33 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       // Relative to the segment's first key: this row's visible keys [lo0, lim0],
       // and the blocks [j_lo, j_hi) that every row of the tile sees whole.
       const int key_base = ((w.u.lo >> L::kShift) + w.blk) * BN;
-      const int pos = sp.pos0 + rt;
+      int pos = sp.pos0 + rt;
+      // Scored: the sequence's first new token and its key (trees), the row's words.
+      bool tree = false;
+      int first = 0, tok_first = 0;
+      const unsigned* row_bits = nullptr;
+      float slope = 0.f;
+      if constexpr (kScored) {
+        tree = p.tree != nullptr;
+        first = w.u.pos0 - w.tile * p.tok_tile;
+        tok_first = w.u.tok0 - w.tile * p.tok_tile;
+        if (p.sc.slopes != nullptr) slope = p.sc.slopes[w.kvh * p.G + rh] * 1.4426950408889634f;
+        if (tree && row_ok) {
+          pos = min(w.u.kv_len - 1, max(first, p.positions[w.u.tok0 + sp.ta + rt]));
+          row_bits = p.tree + (w.u.tok0 + sp.ta + rt) * p.tree_stride;
+        }
+      }
       const int lim0 = min(w.u.kv_len - 1, pos + p.win_right) - key_base, lo0 = pos - p.win_left - key_base;
-      const int j_lo = (sp.pos0 + sp.n_tok - 1 - p.win_left - key_base + BN - 1) >> L::kShift;
-      const int j_hi = (min(w.u.kv_len, sp.pos0 + 1 + p.win_right) - key_base) >> L::kShift;
+      int j_lo = (sp.pos0 + sp.n_tok - 1 - p.win_left - key_base + BN - 1) >> L::kShift;
+      int j_hi = (min(w.u.kv_len, sp.pos0 + 1 + p.win_right) - key_base) >> L::kShift;
+      if constexpr (kScored) {
+        if (tree) {
+          j_lo = (w.u.kv_len - 1 - p.win_left - key_base + BN - 1) >> L::kShift;
+          j_hi = (first - key_base) >> L::kShift;
+        }
+      }
       const int beg = sp.beg, end = sp.end, step = kShare ? sp.turns : 1;
+      const int kv_len = w.u.kv_len, tile_pos0 = sp.pos0, tile_rows = sp.n_tok;  // (scored)
       if (lane == 0) s_walk[warp].w = w;
       __syncwarp();
       // (the span is worked out again after the blocks: its other members would
@@ -445,7 +490,39 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         else tmem_ld64(t_s, sr);
         const int lim = lim0 - j * BN, lo = lo0 - j * BN;  // columns lo <= c <= lim are visible to this row
         const bool cut = j < j_lo || j >= j_hi;  // a mask cuts the block
-        if constexpr (kMaskInPlace) {
+        if constexpr (kScored) {
+          cap_row<BN>(sr, p.sc, p.scale_log2);
+          const int key0 = key_base + j * BN;
+          const bool drafted = tree && key0 + BN > first;  // the block holds new tokens of a tree
+          if (p.sc.slopes != nullptr) {
+            if (drafted) {
+#pragma unroll
+              for (int c = 0; c < BN; ++c) {
+                int kp = key0 + c;
+                if (kp >= first && kp < kv_len)
+                  kp = min(kv_len - 1, max(first, p.positions[tok_first + kp - first]));
+                sr[c] = __float_as_uint(fmaf(-slope, fabsf(static_cast<float>(kp - pos)), __uint_as_float(sr[c])));
+              }
+            } else {
+              const ScoreSide side = tree || p.win_right == 0 || key0 + BN - 1 <= tile_pos0 ? kSideLeft
+                                     : key0 >= tile_pos0 + tile_rows - 1                   ? kSideRight
+                                                                                           : kSideBoth;
+              bias_row<BN>(sr, slope, key0 - pos, side);
+            }
+          }
+          if (drafted) {
+#pragma unroll
+            for (int x = 0; x < BN / 32; ++x) {
+              const unsigned seen = tree_word(row_bits, p.tree_words, key0 + 32 * x - first,
+                                              kv_len - (key0 + 32 * x), min(pos - p.win_left, first) - (key0 + 32 * x));
+#pragma unroll
+              for (int c = 0; c < 32; ++c) sr[32 * x + c] = seen >> c & 1u ? sr[32 * x + c] : hidden;
+            }
+          } else if (cut) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c) sr[c] = c < lo || (!tree && c > lim) ? hidden : sr[c];
+          }
+        } else if constexpr (kMaskInPlace) {
           if (zero_scale) {
 #pragma unroll
             for (int c = 0; c < BN; ++c) sr[c] = __float_as_uint(0.f * __uint_as_float(sr[c]));
@@ -653,11 +730,11 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
 
 namespace {
 
-template <int D, bool BF16>
+template <int D, bool BF16, typename Params>
 cudaError_t launch_paged_tile_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                const PagedParams& p, int grid, cudaStream_t stream) {
+                                const Params& p, int grid, cudaStream_t stream) {
   using L = PagedTileLayout<D>;
-  auto kern = fa_paged_tile_kernel<D, BF16>;
+  auto kern = fa_paged_tile_kernel<D, BF16, Params>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
   if (e != cudaSuccess) return e;
   // The register split assumes the launch gives exactly kLaunchRegs per

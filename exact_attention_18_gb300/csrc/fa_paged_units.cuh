@@ -30,8 +30,8 @@ struct SeqLens {
 __device__ __forceinline__ SeqLens seq_lens(const PagedParams& p, int b) {
   return SeqLens{p.cu_seqlens[b], p.cu_seqlens[b + 1], p.kv_lens[b]};
 }
-template <int SHIFT>
-__device__ __forceinline__ Unit paged_unit(const PagedParams& p, const SeqLens& s, int tile) {
+template <int SHIFT, typename P>
+__device__ __forceinline__ Unit paged_unit(const P& p, const SeqLens& s, int tile) {
   Unit u;
   const int a = s.a, e = s.e, kv = s.kv;
   u.n_blk = 0;
@@ -55,6 +55,9 @@ __device__ __forceinline__ Unit paged_unit(const PagedParams& p, const SeqLens& 
   u.pos0 = kv - n + t0;
   u.kv_len = kv;
   u.lo = max(0, u.pos0 - p.win_left);
+  if constexpr (P::kScored) {
+    if (p.tree != nullptr) u.lo = max(0, kv - n - p.win_left);  // (a drafted token may stand at the first new key)
+  }
   u.hi = min(kv, u.pos0 + u.n_tok + p.win_right);
   if (u.hi <= u.lo) {
     u.lo = u.hi = 0;
@@ -98,7 +101,8 @@ struct SegWalk {
     if (left >= static_cast<long long>(rest) * cost) return rest;
     return (static_cast<int>(left) + cost - 1) / cost;
   }
-  __device__ __forceinline__ void start(const PagedParams& p, const RunStart& s) {
+  template <typename P>
+  __device__ __forceinline__ void start(const P& p, const RunStart& s) {
     b = s.b;
     tile = s.tile;
     kvh = s.kvh;
@@ -111,7 +115,8 @@ struct SegWalk {
     else cost = block_cost<COSTS>(p, u);
   }
   // Past the current segment of n blocks.
-  __device__ __forceinline__ void next(const PagedParams& p, int n) {
+  template <typename P>
+  __device__ __forceinline__ void next(const P& p, int n) {
     if constexpr (COSTS) left -= static_cast<long long>(n) * cost;
     else left -= n;
     blk = 0;
@@ -121,7 +126,8 @@ struct SegWalk {
     }
     if (++kvh == p.H_kv) next_unit(p);
   }
-  __device__ __forceinline__ void next_unit(const PagedParams& p) {
+  template <typename P>
+  __device__ __forceinline__ void next_unit(const P& p) {
     kvh = 0;
     do {
       if (++tile >= u.end_tile) {
@@ -168,8 +174,8 @@ __device__ __forceinline__ int next_tile(const PagedParams& p, const Unit& u, in
 
 // I: int where the host has bounded the call's cost below 2^31 (64-bit scans
 // and divisions cost a decoding call a microsecond), else long long.
-template <int SHIFT, bool COSTS, int THREADS, typename I>
-__device__ __forceinline__ void paged_find_run_t(const PagedParams& p, const SeqLens& own, I* s_warp, RunStart* start) {
+template <int SHIFT, bool COSTS, int THREADS, typename I, typename P>
+__device__ __forceinline__ void paged_find_run_t(const P& p, const SeqLens& own, I* s_warp, RunStart* start) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int per;
   const int x0 = paged_first_unit(p, THREADS, &per), x1 = min(p.batch * p.tiles, x0 + per);
@@ -237,8 +243,8 @@ __device__ __forceinline__ void paged_find_run_t(const PagedParams& p, const Seq
   if (threadIdx.x == 0) start->share = share;
 }
 
-template <int SHIFT, bool COSTS, int THREADS>
-__device__ __forceinline__ void paged_find_run(const PagedParams& p, const SeqLens& own, long long* s_warp,
+template <int SHIFT, bool COSTS, int THREADS, typename P>
+__device__ __forceinline__ void paged_find_run(const P& p, const SeqLens& own, long long* s_warp,
                                                RunStart* start) {
   if (p.small) paged_find_run_t<SHIFT, COSTS, THREADS, int>(p, own, reinterpret_cast<int*>(s_warp), start);
   else paged_find_run_t<SHIFT, COSTS, THREADS, long long>(p, own, s_warp, start);

@@ -83,12 +83,10 @@ __device__ __forceinline__ float2 tanh2(float2 x, const ScoreParams& sc, bool al
   return t;
 }
 
-// N products x of one row with the keys of columns 0 .. N - 1 become base-2 scores
-// in place.  scale_log2 counts without a cap.  slope: s_h (0: no bias); d0: first
-// column's key minus the row.  The whole warp calls it, with one `side`.
+// N products x of one row become capped, scaled base-2 scores in place (without a
+// cap: times scale_log2).  The whole warp calls it.
 template <int N>
-__device__ __forceinline__ void score_row(uint32_t* sr, const ScoreParams& sc, float scale_log2, float slope, int d0,
-                                          ScoreSide side) {
+__device__ __forceinline__ void cap_row(uint32_t* sr, const ScoreParams& sc, float scale_log2) {
   if (sc.cap != 0.f) {
     auto capped = [&](bool all_small) {
 #pragma unroll
@@ -105,7 +103,11 @@ __device__ __forceinline__ void score_row(uint32_t* sr, const ScoreParams& sc, f
 #pragma unroll
     for (int c = 0; c < N; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * scale_log2);
   }
-  if (sc.slopes == nullptr) return;
+}
+
+// Their bias: column c stands d0 + c behind the row.  slope: s_h.
+template <int N>
+__device__ __forceinline__ void bias_row(uint32_t* sr, float slope, int d0, ScoreSide side) {
   if (side == kSideBoth) {
 #pragma unroll
     for (int c = 0; c < N; ++c)

@@ -515,6 +515,43 @@ fa_status fa_fwd_paged(const void* q, void* o, float* lse, const fa_paged_cache*
                        int64_t H_kv, int64_t D, int causal, int64_t window_left, int64_t window_right, float scale,
                        fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * fa_fwd_paged with modified scores (positions are the key positions); their
+ * prefix must be NULL (a prefix's own chunk sees all of it with causal = 0).
+ */
+fa_status fa_fwd_paged_scores(const void* q, void* o, float* lse, const fa_paged_cache* cache,
+                              const int32_t* cu_seqlens, int64_t batch, int64_t max_seqlen_q, int64_t max_seqlen_k,
+                              int64_t total, int64_t H, int64_t H_kv, int64_t D, int causal, int64_t window_left,
+                              int64_t window_right, const fa_scores* scores, float scale, fa_dtype dtype,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of drafted tokens that form a tree (several continuations of a
+ * sequence, to be verified at once) over the cache.  The n new tokens of sequence
+ * b, already in the cache, are keys f .. kv_lens[b] - 1, f = kv_lens[b] - n, in any
+ * order that the caller's tree has.  New token i sees the keys j < f with
+ * positions[i] - window_left <= j (negative: all), and of the new tokens those
+ * whose bit is set in its row: new token j is bit j % 32 of word j / 32.  (Itself
+ * and its ancestors, as a rule; no bit is implied.)  A row that sees no key gets
+ * O = 0, L = -inf.
+ *   positions   : DEVICE int32 [T], where each new token stands in its sequence
+ *                 (f plus its depth, as a rule): the window's and the bias's i,
+ *                 and the bias's j of a new token as a key.  Held to
+ *                 [f, kv_lens[b] - 1].
+ *   tree        : DEVICE uint32, the rows of the T new tokens, tree_stride words
+ *                 apart; tree_words (at most tree_stride) words of a row are
+ *                 used, 32 * tree_words >= min(max_seqlen_q, total).  Bits past a
+ *                 sequence's new tokens are not used.
+ *   scores      : as in fa_fwd_paged_scores, or NULL.
+ * Everything else, the workspace too, is fa_fwd_paged's.
+ */
+fa_status fa_fwd_paged_tree(const void* q, void* o, float* lse, const fa_paged_cache* cache,
+                            const int32_t* cu_seqlens, const int32_t* positions, const uint32_t* tree,
+                            int64_t tree_stride, int64_t tree_words, int64_t batch, int64_t max_seqlen_q,
+                            int64_t max_seqlen_k, int64_t total, int64_t H, int64_t H_kv, int64_t D,
+                            int64_t window_left, const fa_scores* scores, float scale, fa_dtype dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
 /* Workspace bytes of fa_fwd_paged (0 for an empty call or one that no `total`
  * makes supported); never less for larger max_seqlen_q or max_seqlen_k. */
 size_t fa_fwd_paged_workspace_size(int64_t batch, int64_t max_seqlen_q, int64_t max_seqlen_k, int64_t H,

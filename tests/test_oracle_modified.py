@@ -144,6 +144,33 @@ def test_workspace_and_pointers(lib):
     assert fwd(s, H=4, hk=3) == 1
 
 
+def cache_of(page_size=16):
+    return fa.PagedCache(P, P, P, P, 4, 4, 64, page_size, page_size * 128, 128, 64)
+
+
+def paged_call(scores=None, tree=True, positions=P, rows=P, stride=2, words=2, max_q=40, total=80, D=64, ws=None):
+    c, s = cache_of(), None if scores is None else ctypes.byref(scores)
+    if tree:
+        return fa.fa_fwd_paged_tree(P, P, P, ctypes.byref(c), P, positions, rows, stride, words, 2, max_q, 64, total, 4,
+                                    2, D, -1, s, 0.125, fa.FA_BF16, ws, 0, None)
+    return fa.fa_fwd_paged_scores(P, P, P, ctypes.byref(c), P, 2, max_q, 64, total, 4, 2, D, True, -1, -1, s, 0.125,
+                                  fa.FA_BF16, ws, 0, None)
+
+
+def test_paged_refusals(lib):
+    """Bad trees and scores are refused before the workspace is looked at (4: it is missing)."""
+    assert paged_call() == 4 and paged_call(fa.Scores(3.0, P, None), tree=False) == 4
+    assert paged_call(words=1) == 1 and paged_call(stride=1) == 1 and paged_call(words=0, stride=0) == 1
+    assert paged_call(words=1, max_q=32) == 4 and paged_call(words=1, max_q=400, total=30) == 4
+    assert paged_call(positions=None) == 1 and paged_call(rows=None) == 1
+    assert paged_call(positions=P + 2) == 3 and paged_call(rows=P + 1) == 3
+    assert paged_call(stride=1 << 31) == 2 and paged_call(D=96) == 2
+    for tree in (True, False):
+        assert paged_call(fa.Scores(0.0, None, P), tree=tree) == 2
+        assert paged_call(fa.Scores(-3.0, None, None), tree=tree) == 1
+        assert paged_call(fa.Scores(0.0, P + 1, None), tree=tree) == 3
+
+
 def test_empty_calls(lib):
     s = fa.Scores(5.0, P, P)
     assert fwd(s, S=0) == 0 and fwd(s, B=0) == 0
