@@ -22,10 +22,14 @@ the same for packed batches: [T, H, D] tensors and int32 ``cu_seqlens``.
 
 Around attention: ``rope`` and ``rope_backward`` rotate packed Q and K by their
 positions (``rope_inv_freq`` and ``rope_steps`` make the frequency table),
-``paged_append`` puts new tokens into a paged key/value cache and
-``forward_paged`` attends to it (raw: ``fa_rope``, ``fa_rope_bwd``,
-``fa_rope_inv_freq``, ``fa_rope_steps``, ``fa_paged_append``, ``fa_fwd_paged``,
-``fa_fwd_paged_workspace_size``, with a ``PagedCache`` structure).
+``paged_append`` puts new tokens into a paged key/value cache,
+``forward_paged`` attends to it and ``paged_keep`` keeps the accepted tokens of a
+drafted tree (raw: ``fa_rope``, ``fa_rope_bwd``, ``fa_rope_inv_freq``,
+``fa_rope_steps``, ``fa_paged_append``, ``fa_fwd_paged``, ``fa_fwd_paged_scores``,
+``fa_fwd_paged_tree``, ``fa_paged_keep``, ``fa_fwd_paged_workspace_size``, with a
+``PagedCache`` structure).  Scores may be capped and biased (``softcap``,
+``slopes``) and sequences have a prefix (``prefix``): a ``Scores`` structure in
+the raw calls.
 
 The first call loads the compiled library and raises if it has not been built
 (``python -m exact_attention_18_gb300.build``); there is no fallback
@@ -152,6 +156,8 @@ def _load():
     lib.fa_fwd_paged_scores.argtypes = [vp] * 5 + [i64] * 7 + [i32, i64, i64, vp, f32, i32, vp, sz, vp]
     lib.fa_fwd_paged_tree.restype = i32
     lib.fa_fwd_paged_tree.argtypes = [vp] * 7 + [i64] * 10 + [vp, f32, i32, vp, sz, vp]
+    lib.fa_paged_keep.restype = i32
+    lib.fa_paged_keep.argtypes = [vp] * 3 + [i64, i64, vp] + [i64] * 4 + [i32, vp]
     lib.fa_fwd_paged_workspace_size.restype = sz
     lib.fa_fwd_paged_workspace_size.argtypes = [i64] * 6
     lib.fa_status_string.restype = ctypes.c_char_p
@@ -374,6 +380,12 @@ def fa_fwd_paged_tree(q, o, lse, cache, cu_seqlens, positions, tree, tree_stride
     return _load().fa_fwd_paged_tree(q, o, lse, cache, cu_seqlens, positions, tree, tree_stride, tree_words, batch,
                                      max_seqlen_q, max_seqlen_k, total, H, H_kv, D, int(window_left), scores,
                                      float(scale), int(dtype), workspace, workspace_bytes, stream)
+
+
+def fa_paged_keep(cache, cu_seqlens, path, path_stride, path_cols, path_lens, batch, max_seqlen, H_kv, D, dtype,
+                  stream) -> int:
+    return _load().fa_paged_keep(cache, cu_seqlens, path, path_stride, path_cols, path_lens, batch, max_seqlen, H_kv, D,
+                                 int(dtype), stream)
 
 
 def fa_fwd_paged_workspace_size(batch, max_seqlen_q, max_seqlen_k, H, H_kv, D) -> int:
@@ -789,6 +801,22 @@ def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_s
     return _result((_binding or _load_binding()).paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens,
                                                               max_seqlen, q, positions, steps, interleaved, magnitude,
                                                               q_out), "fa_paged_append")
+
+
+def paged_keep(k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen: int, path, path_lens, stream=None):
+    """Move the accepted tokens of each sequence's drafted tree to the slots behind its context.
+
+    Cache, ``kv_lens`` and ``cu_seqlens`` as the tree was attended to with.  Row
+    b of int32 ``path`` [batch, tokens] lists the ``path_lens[b]`` accepted new
+    tokens in increasing order; new token path[b, i] becomes key kv_lens[b] - n + i.
+    The caller then shortens ``kv_lens`` to kv_lens - n + path_lens.
+    """
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            return paged_keep(k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen, path, path_lens)
+    _result((_binding or _load_binding()).paged_keep(k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen,
+                                                     path, path_lens), "fa_paged_keep")
 
 
 def forward_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen_q: int, max_seqlen_k: int,

@@ -29,7 +29,7 @@ BINDING_SRC = os.path.join(CSRC, "fa_binding.cpp")
 BINDING_PATH = os.path.join(LIB_DIR, "_fa_binding.so")
 BINDING_FOR = os.path.join(BUILD_DIR, "fa_binding.for")  # what the binding was compiled against
 
-SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd4.cu", "fa_fwd4p.cu", "fa_bwd.cu", "fa_bwd_scores.cu", "fa_merge.cu", "fa_rope.cu",
+SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd4.cu", "fa_fwd4p.cu", "fa_bwd.cu", "fa_bwd_scores.cu", "fa_merge.cu", "fa_rope.cu", "fa_keep.cu",
            "fa_paged_d16.cu", "fa_paged_d32.cu", "fa_paged_d64.cu", "fa_paged_d128.cu",
            "fa_paged_scores_d16.cu", "fa_paged_scores_d32.cu", "fa_paged_scores_d64.cu", "fa_paged_scores_d128.cu",
            "fa_paged_merge.cu"]

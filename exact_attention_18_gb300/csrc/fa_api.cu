@@ -1269,6 +1269,51 @@ fa_status fa_fwd_paged_tree(const void* q, void* o, float* lse, const fa_paged_c
                         window_left, -1, scale, dtype, workspace, workspace_bytes, stream, scores, &t);
 }
 
+fa_status fa_paged_keep(const fa_paged_cache* cache, const int32_t* cu_seqlens, const int32_t* path,
+                        int64_t path_stride, int64_t path_cols, const int32_t* path_lens, int64_t batch,
+                        int64_t max_seqlen, int64_t H_kv, int64_t D, fa_dtype dtype, void* stream) {
+  g_detail[0] = 0;
+  fa_status st;
+  if ((st = check_dtype_d(D, dtype)) || (st = check_tokens(0, 0, H_kv))) return st;
+  if (batch < 0 || max_seqlen < 0 || path_cols < 0)
+    return fail(FA_ERR_INVALID_ARG, "negative size: batch=%lld max_seqlen=%lld path_cols=%lld", (long long)batch,
+                (long long)max_seqlen, (long long)path_cols);
+  if (batch >= (int64_t(1) << 31) || max_seqlen >= (int64_t(1) << 31) || path_cols >= (int64_t(1) << 31) ||
+      path_stride >= (int64_t(1) << 40))
+    return fail(FA_ERR_UNSUPPORTED, "batch, max_seqlen and path_cols must be below 2^31, path_stride below 2^40");
+  if (path_stride < path_cols)
+    return fail(FA_ERR_INVALID_ARG, "path rows of %lld entries, %lld apart", (long long)path_cols, (long long)path_stride);
+  if (batch == 0 || max_seqlen == 0 || path_cols == 0 || H_kv == 0) return FA_OK;
+  if ((st = check_cache(cache, H_kv, D)) || (st = check_ints(cu_seqlens, "cu_seqlens", 4)) ||
+      (st = check_ints(path, "path", 4)) || (st = check_ints(path_lens, "path_lens", 4)))
+    return st;
+  if ((2 * (D / 8) * H_kv + 127) / 128 > ((int64_t(1) << 31) - 1) / batch)
+    return fail(FA_ERR_UNSUPPORTED, "batch times H_kv * D too large");
+  fa::KeepParams p = {};
+  p.k = cache->k;
+  p.v = cache->v;
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = cache->kv_lens;
+  p.block_table = cache->block_table;
+  p.path = path;
+  p.path_lens = path_lens;
+  p.table_stride = cache->table_stride;
+  p.path_stride = path_stride;
+  p.page_stride = cache->page_stride;
+  p.row_stride = cache->row_stride;
+  p.head_stride = cache->head_stride;
+  p.path_cols = static_cast<int>(path_cols);
+  p.page_shift = log2_of(cache->page_size);
+  p.num_pages = static_cast<int>(cache->num_pages);
+  p.H_kv = static_cast<int>(H_kv);
+  p.D = static_cast<int>(D);
+  p.max_len = static_cast<int>(max_seqlen);
+  p.max_kv = static_cast<int>(table_keys(cache));
+  p.err = fa::device_error_word();
+  if (!p.err) return fail(FA_ERR_CUDA, "cannot resolve the device error word on the current device");
+  return from_cuda(fa::launch_keep(p, static_cast<int>(batch), static_cast<cudaStream_t>(stream)), "keep launch");
+}
+
 const char* fa_status_string(fa_status status) {
   switch (status) {
     case FA_OK: return "FA_OK";
@@ -1305,6 +1350,8 @@ fa_status fa_check_device_errors(void* stream) {
       return fail(FA_ERR_INVALID_ARG, "a paged cache length contradicts the call (checked on the device)");
     if (code == fa::kErrBadPage)
       return fail(FA_ERR_INVALID_ARG, "a block table entry in use is not a page (checked on the device)");
+    if (code == fa::kErrBadPath)
+      return fail(FA_ERR_INVALID_ARG, "a kept path contradicts the call (checked on the device)");
     return fail(FA_ERR_TIMEOUT, "device pipeline wait timed out (code %d)", code);
   }
   return FA_OK;

@@ -377,11 +377,45 @@ PyObject* forward_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   });
 }
 
+// paged_keep(k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen, path, path_lens)
+PyObject* paged_keep(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    require(n == 8, "paged_keep: eight arguments");
+    const Args a{argv, n};
+    const Tensor &kc = a.tensor(0, "k_cache"), &vc = a.tensor(1, "v_cache"), &table = a.tensor(2, "block_table"),
+                 &lens = a.tensor(3, "kv_lens"), &cu = a.tensor(4, "cu_seqlens"), &path = a.tensor(6, "path"),
+                 &path_lens = a.tensor(7, "path_lens");
+    const OneDevice dev(kc);
+    for (const Tensor* x : {&vc, &table, &lens, &cu, &path, &path_lens}) dev.also(*x);
+    require(kc.dim() == 4, "k_cache must be [pages, page_size, H_kv, D]");
+    const int64_t hk = kc.size(2), D = kc.size(3), batch = offsets(cu);
+    const fa_dtype code = dtype_code(kc);
+    const fa_paged_cache cache = paged_cache(kc, vc, table, lens, batch, hk, D, kc.scalar_type());
+    require(path.scalar_type() == at::kInt && path.dim() == 2 && path.size(0) == batch &&
+                (path.stride(1) == 1 || path.size(1) <= 1) && (batch <= 1 || path.stride(0) >= path.size(1)),
+            "path must be an int32 tensor [batch, tokens] with dense rows");
+    const int64_t cols = path.size(1), stride = batch > 1 ? path.stride(0) : cols;
+    const void *path_at = path.const_data_ptr(), *cu_at = cu.const_data_ptr(),
+               *lens_at = ints(path_lens, at::kInt, batch, "path_lens");
+    const int64_t max_len = a.integer(5);
+    void* stream = c10::cuda::getCurrentCUDAStream().stream();
+    fa_status st;
+    {
+      const Unlocked unlocked;
+      st = fa_paged_keep(&cache, static_cast<const int32_t*>(cu_at), static_cast<const int32_t*>(path_at), stride, cols,
+                         static_cast<const int32_t*>(lens_at), batch, max_len, hk, D, code, stream);
+    }
+    if (st != FA_OK) return PyLong_FromLong(st);
+    Py_RETURN_NONE;
+  });
+}
+
 PyMethodDef methods[] = {
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope)), METH_FASTCALL, nullptr},
     {"paged_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_append)), METH_FASTCALL, nullptr},
     {"forward_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(forward_paged)), METH_FASTCALL,
      nullptr},
+    {"paged_keep", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_keep)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fa_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -9,6 +9,7 @@ namespace fa {
 // Codes of these kernels for the device error word, after DeviceErrorCode's.
 constexpr int kErrBadCache = 6;  // a length below the new tokens', or past what the call allows
 constexpr int kErrBadPage = 7;   // a block table entry in use is not a page
+constexpr int kErrBadPath = 8;   // a kept path is longer than its row or the new tokens, or does not increase within them
 
 // Longest cache length (and largest window side): positions and their sums
 // with a window side stay inside 32 bits.
@@ -75,6 +76,27 @@ struct RopeParams {
 };
 
 cudaError_t launch_rope(RopeParams p, bool bf16, bool append, int batch, cudaStream_t stream);
+
+// The move of accepted paths (fa_keep.cu).
+struct KeepParams {
+  void* k;
+  void* v;
+  const int* cu_seqlens;
+  const int* kv_lens;
+  const int* block_table;
+  const int* path;       // [batch] rows of path_cols entries, path_stride apart
+  const int* path_lens;  // [batch]
+  int64_t table_stride, path_stride;
+  int64_t page_stride, row_stride, head_stride;
+  int path_cols;
+  int page_shift, num_pages;
+  int H_kv, D;
+  int max_len;           // largest number of new tokens of a sequence
+  int max_kv;            // largest cache length the block table can hold
+  int* err;
+};
+
+cudaError_t launch_keep(const KeepParams& p, int batch, cudaStream_t stream);
 
 // Attention over the cache.  A "unit" is one (sequence, tile of tok_tile
 // tokens, K/V head): its rows are tok_tile tokens x G query heads, its work the

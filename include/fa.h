@@ -552,6 +552,27 @@ fa_status fa_fwd_paged_tree(const void* q, void* o, float* lse, const fa_paged_c
                             int64_t window_left, const fa_scores* scores, float scale, fa_dtype dtype,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Keeps the accepted path of each sequence's drafted tree: of the n new tokens at
+ * keys f .. kv_lens[b] - 1, f = kv_lens[b] - n, token path[b][i] (K and V rows of
+ * all heads) moves to key f + i, i < path_lens[b].  The caller then shortens
+ * kv_lens[b] to f + path_lens[b].  kv_lens and cu_seqlens are those that the trees
+ * were attended to with.
+ *   path       : DEVICE int32, rows of path_cols entries, path_stride apart; the
+ *                first path_lens[b] of a row are used, increase strictly and lie
+ *                in [0, n) (a parent precedes its children).
+ *   path_lens  : DEVICE int32 [batch], 0 .. min(n, path_cols).
+ *   max_seqlen : host bound on the new tokens of a sequence; may be loose.
+ * A path that is longer, or does not increase within [0, n), leaves its sequence
+ * alone, and so do lengths that contradict the call; a row of an entry that is no
+ * page is read as zeros and never written; each makes fa_check_device_errors()
+ * return FA_ERR_INVALID_ARG.  Slots from f + path_lens[b] on, and other sequences',
+ * are left as they were.  Sequences must not share the pages of their new keys.
+ */
+fa_status fa_paged_keep(const fa_paged_cache* cache, const int32_t* cu_seqlens, const int32_t* path,
+                        int64_t path_stride, int64_t path_cols, const int32_t* path_lens, int64_t batch,
+                        int64_t max_seqlen, int64_t H_kv, int64_t D, fa_dtype dtype, void* stream);
+
 /* Workspace bytes of fa_fwd_paged (0 for an empty call or one that no `total`
  * makes supported); never less for larger max_seqlen_q or max_seqlen_k. */
 size_t fa_fwd_paged_workspace_size(int64_t batch, int64_t max_seqlen_q, int64_t max_seqlen_k, int64_t H,

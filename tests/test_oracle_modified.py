@@ -171,6 +171,21 @@ def test_paged_refusals(lib):
         assert paged_call(fa.Scores(0.0, P + 1, None), tree=tree) == 3
 
 
+def keep_call(cache=None, path=P, lens=P, stride=4, cols=4, batch=2, max_q=8, hk=2, D=64, dtype=None, cu=P):
+    c = cache_of() if cache is None else cache
+    return fa.fa_paged_keep(ctypes.byref(c), cu, path, stride, cols, lens, batch, max_q, hk, D,
+                            fa.FA_BF16 if dtype is None else dtype, None)
+
+
+def test_keep_refusals(lib):
+    assert keep_call(path=None) == 1 and keep_call(lens=None) == 1 and keep_call(cu=None) == 1
+    assert keep_call(path=P + 1) == 3 and keep_call(lens=P + 2) == 3
+    assert keep_call(stride=3) == 1 and keep_call(cols=-1) == 1 and keep_call(batch=-1) == 1 and keep_call(max_q=-1) == 1
+    assert keep_call(cache_of(page_size=24)) == 2 and keep_call(D=40) == 2 and keep_call(dtype=7) == 1
+    assert keep_call(batch=1 << 31) == 2 and keep_call(cols=1 << 31, stride=1 << 31) == 2 and keep_call(hk=1 << 20) == 2
+    assert keep_call(batch=0) == 0 and keep_call(cols=0, path=None) == 0 and keep_call(max_q=0) == 0 and keep_call(hk=0) == 0
+
+
 def test_empty_calls(lib):
     s = fa.Scores(5.0, P, P)
     assert fwd(s, S=0) == 0 and fwd(s, B=0) == 0
