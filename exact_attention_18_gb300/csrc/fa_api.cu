@@ -232,6 +232,31 @@ fa_status encode_input(CUtensorMap* map, const void* base, bool bf16, const Shap
   return FA_OK;
 }
 
+// The constants of a cap.  tanh(v) / v on |v| <= 1 is a polynomial in v^2 (minimax,
+// by Remez exchange; relative error 6e-7); with v = scale x / cap it becomes
+// cap log2 e tanh(v) = x * sum_k poly[k] x^(2k).  Coefficients that leave fp32's
+// normal range bound the |x| it is used for: below it to where the terms left out
+// are under 2^-22 of the value, above it to 0.
+void tanh_poly(float scale, float cap, fa::ScoreParams* p) {
+  constexpr double kC[fa::kTanhTerms] = {0.999999404, -0.333290428, 0.132814333, -0.0516056754, 0.0167431142,
+                                         -0.00306706037};
+  const double in = static_cast<double>(scale) / cap, c = static_cast<double>(cap) * 1.4426950408889634074;
+  p->cap = static_cast<float>(c);
+  p->in2 = static_cast<float>(2 * 1.4426950408889634074 * in);
+  double vmax = 1.0, f = c * in;
+  for (int k = 0; k < fa::kTanhTerms; ++k, f *= in * in) {
+    p->poly[k] = static_cast<float>(kC[k] * f);
+    const double size = std::fabs(kC[k] * f);
+    if (size > 1e37) vmax = 0;
+    if (k > 0 && size < 1e-37) {
+      p->poly[k] = 0.f;
+      vmax = std::fmin(vmax, std::pow(2.4e-7 / (2 * std::fabs(kC[k])), 1.0 / (2 * k)));
+    }
+  }
+  const double small = in == 0 ? 1e18 : std::fmin(vmax / std::fabs(in), 1e18);
+  p->small = static_cast<float>(small);
+}
+
 // Modified scores of a call; *on: they need their own kernels.  (A packed call that
 // may have them takes those whatever they are: they clear what lies behind a sample.)
 fa_status check_scores(const fa_scores* in, float scale, bool prefix_ok, bool packed, bool* on,
@@ -245,12 +270,10 @@ fa_status check_scores(const fa_scores* in, float scale, bool prefix_ok, bool pa
   if ((reinterpret_cast<uintptr_t>(in->slopes) & 3u) != 0) return fail(FA_ERR_ALIGNMENT, "slopes is not 4-byte aligned");
   if ((reinterpret_cast<uintptr_t>(in->prefix) & 3u) != 0) return fail(FA_ERR_ALIGNMENT, "prefix is not 4-byte aligned");
   if (in->softcap > 0) {
-    out->cap = in->softcap * kLog2e;
-    out->in = scale / in->softcap;
-    out->in2 = 2.f * kLog2e * out->in;
     // (beyond these the cap's own arithmetic leaves the range of fp32)
-    if (in->softcap < 1e-10f || in->softcap > 1e10f || !std::isfinite(out->in2))
+    if (in->softcap < 1e-10f || in->softcap > 1e10f || !std::isfinite(scale / in->softcap * 3.f))
       return fail(FA_ERR_UNSUPPORTED, "softcap must be between 1e-10 and 1e10, and scale / softcap finite");
+    tanh_poly(scale, in->softcap, out);
   }
   out->slopes = in->slopes;
   out->prefix = in->prefix;

@@ -82,26 +82,33 @@ __device__ __forceinline__ uint32_t packed_col(int kk) { return kk < 2 ? kk * 8 
 struct ScoreGrad {
   ScoreParams sc;
   float slope;     // s_h
+  float curve;     // -1 / c^2: the derivative of y = c tanh is 1 + curve y^2
   int d0;          // distance key - query of this thread's first row and column
-  ScoreSide side;  // of the block
+  int side;        // of the block: -1 all keys at or before their queries, 1 behind them, 0 both
   template <int N>
   __device__ __forceinline__ bool all_small(const uint32_t* xs) const {
-    return sc.cap == 0.f || !__any_sync(0xffffffffu, abs_max<N>(xs) * fabsf(sc.in) > kTanhMax);
+    return sc.cap == 0.f || !__any_sync(0xffffffffu, !(abs_max<N>(xs) <= sc.small));
   }
   // Base-2 scores of two products x plus `add`, and (under a cap) their derivative
   // by scale x.  d: key - query of the first; step: of the second minus that.
   __device__ __forceinline__ float2 score(float2 x, float2 c2, float2 add, int d, int step, bool small,
                                           float2* ds_dx) const {
     if (sc.slopes != nullptr) {
-      const float s = side == kSideRight ? -slope : slope;
+      const float s = side > 0 ? -slope : slope;
       float2 f = make_float2(static_cast<float>(d), static_cast<float>(d + step));
-      if (side == kSideBoth) f = make_float2(-fabsf(f.x), -fabsf(f.y));
+      if (side == 0) f = make_float2(-fabsf(f.x), -fabsf(f.y));
       add = __ffma2_rn(make_float2(s, s), f, add);
     }
     if (sc.cap == 0.f) return __ffma2_rn(x, c2, add);
-    const float2 t = tanh2(x, sc, small);
-    *ds_dx = __ffma2_rn(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f));
-    return __ffma2_rn(t, make_float2(sc.cap, sc.cap), add);
+    float2 y = __fmul2_rn(x, tanh_small(x, sc));
+    if (!small) {
+      const float2 u = __ffma2_rn(tanh_rest(x, sc.in2), make_float2(-2.f * sc.cap, -2.f * sc.cap),
+                                  make_float2(sc.cap, sc.cap));
+      y.x = fabsf(x.x) <= sc.small ? y.x : u.x;
+      y.y = fabsf(x.y) <= sc.small ? y.y : u.y;
+    }
+    *ds_dx = __ffma2_rn(__fmul2_rn(y, make_float2(curve, curve)), y, make_float2(1.f, 1.f));
+    return __fadd2_rn(y, add);
   }
 };
 
@@ -606,6 +613,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if constexpr (SCORED) {
       sg.sc = p.sc;
       sg.slope = 0.f;
+      sg.curve = -1.f / (p.sc.cap * p.sc.cap);  // (unused without a cap)
     }
     bool alive = true;
     int ph = pz0;  // SCORED, dK/dV pass: partner head of the block
@@ -656,7 +664,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           // (causal without a prefix: a key behind its query is hidden, whatever its bias)
           const int key0 = KV_OUTER ? own0 : partner0, key1 = key0 + (KV_OUTER ? 127 : kPN - 1);
           const int row0 = KV_OUTER ? partner0 : own0, row1 = row0 + (KV_OUTER ? kPN - 1 : 127);
-          sg.side = key1 <= row0 || (p.causal && pfx == 0) ? kSideLeft : key0 >= row1 ? kSideRight : kSideBoth;
+          sg.side = key1 <= row0 || (p.causal && pfx == 0) ? -1 : key0 >= row1 ? 1 : 0;
           if constexpr (KV_OUTER) {
             const int lim0 = own0 + q4 * 32 - partner0 - col0;
             const bool edge = (partner0 < own0 + 127 - wr && pfx < own0 + 128) || partner0 + kPN - 1 > own0 + wl;

@@ -58,6 +58,7 @@ static_assert(2 * 128 * kRegsHigh + 128 * kRegsLow <= kFwdThreads * kLaunchRegs,
 // A block's P~ = exp2(c s - m) is accepted with a stale maximum m while the
 // block's sum stays <= 2^8 (so every P~ <= 2^8, far inside the 16-bit range).
 constexpr float kSumLimit = 256.0f;
+constexpr float kTau = 8.0f;  // SCORED: log2 of the largest P~ kept with a stale maximum
 // The two tiles' softmax warps of one SM sub-partition alternate at the
 // exponentials of each key block.
 constexpr bool kTurns = true;
@@ -441,15 +442,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const bool masked = GENERAL ? (kv0 + kBlockN > S) || (kv0 + kBlockN - 1 > (SCORED ? max(tile_row0 + wr, pfx - 1) : tile_row0 + wr)) ||
                                         (kv0 < tile_row0 + kBlockM - 1 - wl)
                                   : (kv0 + kBlockN > S) || (p.causal && kv0 + kBlockN - 1 > tile_row0);
+      float fixed = 0.f;  // SCORED: what the row's scores in this block have in common
       if constexpr (SCORED) {
-        // (causal: what lies behind the row is hidden, whatever its bias)
-        const ScoreSide side = kv0 + kBlockN - 1 <= tile_row0 || (p.causal && pfx == 0) ? kSideLeft
-                               : kv0 >= tile_row0 + kBlockM - 1                         ? kSideRight
-                                                                                        : kSideBoth;
-        cap_row<kBlockN>(sr, p.sc, p.scale_log2);
-        if (p.sc.slopes != nullptr) bias_row<kBlockN>(sr, slope, kv0 - row_g, side);
+        const RowBias bias = row_bias(slope, kv0 - row_g, kv0 + kBlockN - 1 <= tile_row0 || (p.causal && pfx == 0),
+                                      kv0 >= tile_row0 + kBlockM - 1);
+        fixed = bias.fixed;
+        block_scores<kBlockN>(sr, t_s, p.sc, make_float2(p.scale_log2, p.scale_log2), bias, masked,
+                              PlainCols{masked ? lo : 0, masked ? lim : kBlockN});
       }
-      if (j == 0) m = block_max_scaled<kBlockN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
+      if (!SCORED && j == 0) m = block_max_scaled<kBlockN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
       // The two tiles' warps of one sub-partition take turns at the
       // exponentials, so one's loads, stores and waits overlap the other's.
       if (kTurns && (t == 0 ? j >= 1 && j - 1 < nb_other : j < nb_other) &&
@@ -460,22 +461,43 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       uint32_t pk[kBlockN / 2];
       float alpha = 1.f;
       bool upd = false;
-      float blk = exp_block<BF16, GENERAL>(sr, c2, m, masked, lo, lim, pk);
-      // Every P~ <= 2^8 holds if the block's sum does.  Otherwise (or on NaN)
-      // this block's maximum is too far above the stale m: move m to it,
-      // rescale, and redo the block ("T5 讲解" §④ online update).  A window can
-      // hide every key of a row's first blocks: the first block that shows the
-      // row a key then sets m.
-      bool need = !(blk <= kSumLimit);
-      if constexpr (GENERAL) need = need || (m == -INFINITY && max(lo, 0) <= min(lim, kBlockN - 1));
-      if (__any_sync(0xffffffffu, need)) {
-        const float m_blk = block_max_scaled<kBlockN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
-        if (need && m_blk > m) {
+      float blk;
+      if constexpr (SCORED) {
+        // The block's maximum ahead of its exponentials, as in the four-tile kernel.
+        const float m_blk = block_max_scaled<kBlockN>(sr, false, 0, kBlockN, 1.f, false) + fixed;
+        if (m_blk > m + kTau || (m == -INFINITY && m_blk > m)) {
           alpha = ex2(m - m_blk);
           m = m_blk;
           upd = true;
         }
-        if (__any_sync(0xffffffffu, upd)) blk = exp_block<BF16, GENERAL>(sr, c2, m, masked, lo, lim, pk);
+        const float nb = fixed - (m == -INFINITY ? 0.f : m);
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // (P~ goes straight over S in TMEM: its scores are in registers)
+#pragma unroll
+        for (int k0 = 0; k0 < kBlockN; k0 += 16) {
+          exp16<BF16, false>(sr, k0, c2, make_float2(nb, nb), 0, kBlockN, acc, pk + k0 / 2);
+          tmem_st8(t_p + k0 / 2, pk + k0 / 2);
+        }
+        const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+        blk = a.x + a.y;
+      } else {
+        blk = exp_block<BF16, GENERAL>(sr, c2, m, masked, lo, lim, pk);
+        // Every P~ <= 2^8 holds if the block's sum does.  Otherwise (or on NaN)
+        // this block's maximum is too far above the stale m: move m to it,
+        // rescale, and redo the block ("T5 讲解" §④ online update).  A window can
+        // hide every key of a row's first blocks: the first block that shows the
+        // row a key then sets m.
+        bool need = !(blk <= kSumLimit);
+        if constexpr (GENERAL) need = need || (m == -INFINITY && max(lo, 0) <= min(lim, kBlockN - 1));
+        if (__any_sync(0xffffffffu, need)) {
+          const float m_blk = block_max_scaled<kBlockN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
+          if (need && m_blk > m) {
+            alpha = ex2(m - m_blk);
+            m = m_blk;
+            upd = true;
+          }
+          if (__any_sync(0xffffffffu, upd)) blk = exp_block<BF16, GENERAL>(sr, c2, m, masked, lo, lim, pk);
+        }
       }
       if (kTurns && (t == 0 ? j < nb_other : j + 1 < nb_other)) {
         __syncwarp();
@@ -490,7 +512,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         break;
       }
       tc_fence_after();
-      if (__any_sync(0xffffffffu, upd)) {
+      if (__any_sync(0xffffffffu, upd) && (!SCORED || j > 0)) {
         // O holds the blocks before j relative to the old m: rescale this warp's rows.
 #pragma unroll
         for (int c = 0; c < D; c += 16) {
@@ -506,8 +528,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           tmem_st16(t_o + c, o16);
         }
       }
-      tmem_st32(t_p, pk);
-      tmem_st32(t_p + 32, pk + 32);
+      if constexpr (!SCORED) {
+        tmem_st32(t_p, pk);
+        tmem_st32(t_p + 32, pk + 32);
+      }
       tmem_st_wait();
       warp_arrive(&bar_pfull[t]);
     }

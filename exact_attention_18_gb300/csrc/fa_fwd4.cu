@@ -77,6 +77,7 @@ constexpr uint32_t kF4RegsHigh = kF4Threads == 640 ? 104 : 96;
 constexpr uint32_t kF4RegsLow = kF4Threads == 640 ? 64 : 48;
 static_assert(512 * kF4RegsHigh + (kF4Threads - 512) * kF4RegsLow <= kF4Threads * kF4LaunchRegs, "register split");
 constexpr float kF4SumLimit = 256.0f;
+constexpr float kF4Tau = 8.0f;  // SCORED: log2 of the largest P~ kept with a stale maximum
 // Measured causal fp16 D = 64 forwards (us), persistent two-pipeline kernel / this one:
 // S 1024 (B8 H16) 35.5 / 37.5, S 2048 (B4 H16) 46.3 / 50.9, S 4096 (B4 H16) 128.7 / 133.8,
 // S 8192 (B2 H16) 232.0 / 226.5, S 16384 (B1 H16) 437 / 422.6.
@@ -484,25 +485,26 @@ __global__ void __launch_bounds__(kF4Threads, 1)
           GENERAL ? (kv0 + kBN > S) || (kv0 + kBN - 1 > (SCORED ? max(tile_row0 + wr, pfx - 1) : tile_row0 + wr)) ||
                         (kv0 < tile_row0 + kBlockM - 1 - wl)
                   : (kv0 + kBN > S) || (p.causal && kv0 + kBN - 1 > tile_row0);
+      float fixed = 0.f;  // SCORED: what the row's scores in this block have in common
       if constexpr (SCORED) {
-        // (causal: what lies behind the row is hidden, whatever its bias)
-        const ScoreSide side = kv0 + kBN - 1 <= tile_row0 || (p.causal && pfx == 0) ? kSideLeft
-                               : kv0 >= tile_row0 + kBlockM - 1                     ? kSideRight
-                                                                                    : kSideBoth;
-        cap_row<kBN>(sr, p.sc, p.scale_log2);
-        if (p.sc.slopes != nullptr) bias_row<kBN>(sr, slope, kv0 - row_g, side);
+        const RowBias bias = row_bias(slope, kv0 - row_g, kv0 + kBN - 1 <= tile_row0 || (p.causal && pfx == 0),
+                                      kv0 >= tile_row0 + kBlockM - 1);
+        fixed = bias.fixed;
+        block_scores<kBN>(sr, t_s, p.sc, make_float2(p.scale_log2, p.scale_log2), bias, masked,
+                          PlainCols{masked ? lo : 0, masked ? lim : kBN});
       }
-      if (j == 0) m = block_max_scaled<kBN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
+      if (!SCORED && j == 0) m = block_max_scaled<kBN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
       float alpha = 1.f;
       bool upd = false;
       float blk;
       // P~ of the block, written 16 keys at a time over the S columns just read.
       auto exps = [&]() {
         const float m_use = (m == -INFINITY) ? 0.f : m;  // rows with no visible key so far
-        const float2 negm = make_float2(-m_use, -m_use);
+        const float nb = SCORED ? fixed - m_use : -m_use;
+        const float2 negm = make_float2(nb, nb);
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                          make_float2(0.f, 0.f)};
-        if (masked) {
+        if (!SCORED && masked) {
 #pragma unroll
           for (int k0 = 0; k0 < kBN; k0 += 16) {
             uint32_t pk[8];
@@ -520,41 +522,60 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
         return a.x + a.y;
       };
-      blk = exps();
-      // Every P~ <= 2^8 holds if the block's sum does.  Otherwise (or on NaN)
-      // the stale m is too far below this block's maximum: move m, rescale,
-      // and redo the block.
-      bool need = !(blk <= kF4SumLimit);
-      if constexpr (GENERAL) {
-        // A window can hide every key of a row's first blocks: m is still
-        // -inf there, and the first block that shows the row a key sets it.
-        need = need || (m == -INFINITY && max(lo, 0) <= min(lim, kBN - 1));
-      }
-      if (__any_sync(0xffffffffu, need)) {
-        const float m_blk = block_max_scaled<kBN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
-        if (need && m_blk > m) {
+      bool rescale;
+      if constexpr (SCORED) {
+        // The block's maximum ahead of its exponentials: m moves where it is exceeded by
+        // more than 2^8.  (Scores that were formed in place have their -inf, and a bias
+        // moves the maximum so often that a second try would be the rule.)
+        const float m_blk = block_max_scaled<kBN>(sr, false, 0, kBN, 1.f, false) + fixed;
+        if (m_blk > m + kF4Tau || (m == -INFINITY && m_blk > m)) {
           alpha = ex2(m - m_blk);
           m = m_blk;
           upd = true;
         }
-        if (__any_sync(0xffffffffu, upd)) {
-          tmem_st_wait();  // the first pass's stores land before they are overwritten
-          blk = exps();
-          // O_t holds the blocks before j relative to the old m (P_t(j-1) V(j-1)
-          // is complete: S_t(j) was committed after it).
-#pragma unroll
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o16[16];
-            tmem_ld16(t_o + c, o16);
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float2 v = __fmul2_rn(make_float2(__uint_as_float(o16[i]), __uint_as_float(o16[i + 1])),
-                                          make_float2(alpha, alpha));
-              o16[i] = __float_as_uint(v.x);
-              o16[i + 1] = __float_as_uint(v.y);
-            }
-            tmem_st16(t_o + c, o16);
+        rescale = __any_sync(0xffffffffu, upd) && j > 0;
+        blk = exps();
+      } else {
+        rescale = false;
+        blk = exps();
+        // Every P~ <= 2^8 holds if the block's sum does.  Otherwise (or on NaN)
+        // the stale m is too far below this block's maximum: move m, rescale,
+        // and redo the block.
+        bool need = !(blk <= kF4SumLimit);
+        if constexpr (GENERAL) {
+          // A window can hide every key of a row's first blocks: m is still
+          // -inf there, and the first block that shows the row a key sets it.
+          need = need || (m == -INFINITY && max(lo, 0) <= min(lim, kBN - 1));
+        }
+        if (__any_sync(0xffffffffu, need)) {
+          const float m_blk = block_max_scaled<kBN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
+          if (need && m_blk > m) {
+            alpha = ex2(m - m_blk);
+            m = m_blk;
+            upd = true;
           }
+          if (__any_sync(0xffffffffu, upd)) {
+            tmem_st_wait();  // the first pass's stores land before they are overwritten
+            blk = exps();
+            rescale = true;
+          }
+        }
+      }
+      if (rescale) {
+        // O_t holds the blocks before j relative to the old m (P_t(j-1) V(j-1)
+        // is complete: S_t(j) was committed after it).
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o16[16];
+          tmem_ld16(t_o + c, o16);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float2 v = __fmul2_rn(make_float2(__uint_as_float(o16[i]), __uint_as_float(o16[i + 1])),
+                                        make_float2(alpha, alpha));
+            o16[i] = __float_as_uint(v.x);
+            o16[i + 1] = __float_as_uint(v.y);
+          }
+          tmem_st16(t_o + c, o16);
         }
       }
       l = l * alpha + blk;

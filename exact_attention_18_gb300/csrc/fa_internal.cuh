@@ -68,10 +68,12 @@ struct BwdParams {
 };
 
 // Modified scores (fa_scores.cuh has the mathematics).
+constexpr int kTanhTerms = 6;
 struct ScoreParams {
   float cap;            // cap * log2 e; 0: no cap
-  float in;             // scale / cap: v = in * x
-  float in2;            // 2 log2 e scale / cap: e^(2v) = 2^(in2 x)
+  float in2;            // 2 log2 e scale / cap: e^(2v) = 2^(in2 x), v = scale x / cap
+  float small;          // |x| up to which the polynomial gives cap tanh(v)
+  float poly[kTanhTerms];  // its coefficients, of x^(2k + 1)
   const float* slopes;  // [H] in device memory, natural units; nullptr: no bias
   const int* prefix;    // [B] in device memory: keys before prefix[b] are visible to all rows; nullptr: none
 };

@@ -123,20 +123,25 @@ __device__ __forceinline__ TileSpan tile_span(const P& p, const SegWalk<SHIFT, t
   return s;
 }
 
-// Columns of a tree that a row sees among 32 keys: the first is new token b0 (below
-// 0: a key before them, and seen from column `from` on), `rest` keys are left.
-__device__ __forceinline__ unsigned tree_word(const unsigned* row, int words, int b0, int rest, int from) {
-  unsigned x = ~0u;
-  if (b0 > -32) {
-    const int i = b0 >> 5;  // -1 .. : the word that holds b0
-    const unsigned a = i < 0 ? ~0u : (row != nullptr && i < words ? row[i] : 0u);
-    const unsigned b = row != nullptr && i + 1 < words ? row[i + 1] : 0u;
-    x = __funnelshift_r(a, b, b0 & 31);
+// The columns of a block that holds new tokens of a tree: a row sees those whose bit
+// is set, and a drafted key stands at its position.
+template <int N>
+struct TreeCols {
+  int key0, first, kv_len;  // first key of the block, first new key, keys
+  const int* positions;     // of the sequence's new tokens
+  const unsigned* row;      // the row's bits (nullptr: none)
+  int from;                 // first column that the window leaves
+  static constexpr bool kOff = true;
+  __device__ __forceinline__ bool seen(int c) const {
+    const int j = key0 + c - first;  // new token
+    if (j < 0) return c >= from;
+    return row != nullptr && key0 + c < kv_len && (row[j >> 5] >> (j & 31) & 1u) != 0;
   }
-  if (rest < 32) x &= rest <= 0 ? 0u : (1u << rest) - 1u;
-  if (from > 0) x &= from >= 32 ? 0u : ~0u << from;
-  return x;
-}
+  __device__ __forceinline__ int off(int c) const {
+    if (key0 + c < first || key0 + c >= kv_len) return c;
+    return min(kv_len - 1, max(first, positions[key0 + c - first])) - key0;
+  }
+};
 
 }  // namespace
 
@@ -159,6 +164,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
   constexpr int kMma0 = L::kSoftWarps, kProducer = L::kSoftWarps + 2, kProducerV = L::kSoftWarps + 3;
   constexpr int kMmaWarps = L::kMmaWarps, kTilesPerMma = T / kMmaWarps;
   constexpr float kSumLimit = 256.0f;  // largest block sum of P~ kept with a stale maximum
+  constexpr float kTau = 8.0f;         // scored: log2 of the largest P~ kept with one
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -428,8 +434,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     // cycles of instruction fetch per unit (ragged chunks 129 -> 121 us).  At
     // D = 128 the selects between load and maximum cost more than that (chunks
     // of 2048: 668 us with a copy of its own, 723 in place).
-    // Modified scores are formed in place anyhow.
-    constexpr bool kMaskInPlace = D <= 64 || kScored;
+    constexpr bool kMaskInPlace = D <= 64;
     constexpr bool kShare = T == 4;  // tiles may share a unit's row tile
     // In place, a scale of 0 is applied ahead of the mask (0 times a hidden key's
     // infinity would not be -inf); a NaN stays one.
@@ -490,37 +495,24 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         else tmem_ld64(t_s, sr);
         const int lim = lim0 - j * BN, lo = lo0 - j * BN;  // columns lo <= c <= lim are visible to this row
         const bool cut = j < j_lo || j >= j_hi;  // a mask cuts the block
+        float fixed = 0.f;  // scored: what the row's scores in this block have in common
         if constexpr (kScored) {
-          cap_row<BN>(sr, p.sc, p.scale_log2);
           const int key0 = key_base + j * BN;
-          const bool drafted = tree && key0 + BN > first;  // the block holds new tokens of a tree
-          if (p.sc.slopes != nullptr) {
-            if (drafted) {
-#pragma unroll
-              for (int c = 0; c < BN; ++c) {
-                int kp = key0 + c;
-                if (kp >= first && kp < kv_len)
-                  kp = min(kv_len - 1, max(first, p.positions[tok_first + kp - first]));
-                sr[c] = __float_as_uint(fmaf(-slope, fabsf(static_cast<float>(kp - pos)), __uint_as_float(sr[c])));
-              }
-            } else {
-              const ScoreSide side = tree || p.win_right == 0 || key0 + BN - 1 <= tile_pos0 ? kSideLeft
-                                     : key0 >= tile_pos0 + tile_rows - 1                   ? kSideRight
-                                                                                           : kSideBoth;
-              bias_row<BN>(sr, slope, key0 - pos, side);
-            }
-          }
-          if (drafted) {
-#pragma unroll
-            for (int x = 0; x < BN / 32; ++x) {
-              const unsigned seen = tree_word(row_bits, p.tree_words, key0 + 32 * x - first,
-                                              kv_len - (key0 + 32 * x), min(pos - p.win_left, first) - (key0 + 32 * x));
-#pragma unroll
-              for (int c = 0; c < 32; ++c) sr[32 * x + c] = seen >> c & 1u ? sr[32 * x + c] : hidden;
-            }
-          } else if (cut) {
-#pragma unroll
-            for (int c = 0; c < BN; ++c) sr[c] = c < lo || (!tree && c > lim) ? hidden : sr[c];
+          const RowBias bias = row_bias(slope, key0 - pos, tree || p.win_right == 0 || key0 + BN - 1 <= tile_pos0,
+                                        key0 >= tile_pos0 + tile_rows - 1);
+          fixed = bias.fixed;
+          const float2 cs = make_float2(p.scale_log2, p.scale_log2);
+          if (tree && key0 + BN > first) {  // new tokens of a tree
+            TreeCols<BN> cols;
+            cols.key0 = key0;
+            cols.first = first;
+            cols.kv_len = kv_len;
+            cols.positions = p.positions + tok_first;
+            cols.row = row_bits;
+            cols.from = min(pos - p.win_left, first) - key0;
+            block_scores<BN>(sr, t_s, p.sc, cs, bias, true, cols);
+          } else {
+            block_scores<BN>(sr, t_s, p.sc, cs, bias, cut, PlainCols{cut ? lo : 0, cut ? lim : BN});
           }
         } else if constexpr (kMaskInPlace) {
           if (zero_scale) {
@@ -532,15 +524,17 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
             for (int c = 0; c < BN; ++c) sr[c] = c < lo || c > lim ? hidden : sr[c];
           }
         }
-        const bool masked = !kMaskInPlace && cut;
+        const bool masked = !kScored && !kMaskInPlace && cut;
         auto block_max = [&]() {
+          if constexpr (kScored) return block_max_scaled<BN>(sr, false, 0, BN, 1.f, false) + fixed;
           return block_max_scaled<BN, !kMaskInPlace>(sr, masked, lo, kMaskInPlace ? BN : lim, ce, neg_scale);
         };
-        if (j == beg) m = block_max();
+        if (!kScored && j == beg) m = block_max();
         float alpha = 1.f;
         auto exps = [&]() {
           const float m_use = m == -INFINITY ? 0.f : m;  // rows with no visible key so far
-          const float2 negm = make_float2(-m_use, -m_use);
+          const float nb = kScored ? fixed - m_use : -m_use;
+          const float2 negm = make_float2(nb, nb);
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                            make_float2(0.f, 0.f)};
           if (masked) {
@@ -561,36 +555,51 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
           return a.x + a.y;
         };
-        float blk = exps();
-        // A block whose sum breaks the bound (or a row's first visible key)
-        // moves the maximum, rescales O and is done again.  Lanes past the
-        // tile's rows hold anything and never ask for it.
-        const bool need = row_ok && (!(blk <= kSumLimit) || m == -INFINITY);
-        if (__any_sync(0xffffffffu, need)) {
+        float blk;
+        bool rescale = false;
+        if constexpr (kScored) {
+          // The block's maximum ahead of its exponentials, as in the forward kernels.
           const float m_blk = block_max();
-          const bool upd = need && m_blk > m;
+          const bool upd = row_ok && (m_blk > m + kTau || (m == -INFINITY && m_blk > m));
           if (upd) {
             alpha = ex2(m - m_blk);
             m = m_blk;
           }
-          if (__any_sync(0xffffffffu, upd)) {
-            tmem_st_wait();  // the first pass's stores land before they are overwritten
-            blk = exps();
-            if (j > beg) {
-#pragma unroll
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o16[16];
-                tmem_ld16(t_o + c, o16);
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                  const float2 v = __fmul2_rn(make_float2(__uint_as_float(o16[i]), __uint_as_float(o16[i + 1])),
-                                              make_float2(alpha, alpha));
-                  o16[i] = __float_as_uint(v.x);
-                  o16[i + 1] = __float_as_uint(v.y);
-                }
-                tmem_st16(t_o + c, o16);
-              }
+          rescale = __any_sync(0xffffffffu, upd) && j > beg;
+          blk = exps();
+        } else {
+          blk = exps();
+          // A block whose sum breaks the bound (or a row's first visible key)
+          // moves the maximum, rescales O and is done again.  Lanes past the
+          // tile's rows hold anything and never ask for it.
+          const bool need = row_ok && (!(blk <= kSumLimit) || m == -INFINITY);
+          if (__any_sync(0xffffffffu, need)) {
+            const float m_blk = block_max();
+            const bool upd = need && m_blk > m;
+            if (upd) {
+              alpha = ex2(m - m_blk);
+              m = m_blk;
             }
+            if (__any_sync(0xffffffffu, upd)) {
+              tmem_st_wait();  // the first pass's stores land before they are overwritten
+              blk = exps();
+              rescale = j > beg;
+            }
+          }
+        }
+        if (rescale) {
+#pragma unroll
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o16[16];
+            tmem_ld16(t_o + c, o16);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float2 v = __fmul2_rn(make_float2(__uint_as_float(o16[i]), __uint_as_float(o16[i + 1])),
+                                          make_float2(alpha, alpha));
+              o16[i] = __float_as_uint(v.x);
+              o16[i + 1] = __float_as_uint(v.y);
+            }
+            tmem_st16(t_o + c, o16);
           }
         }
         l = l * alpha + blk;

@@ -20,18 +20,16 @@
 
 namespace fa {
 
-// The minimax polynomial of degree 5 in w = v^2 for tanh(v) / v on |v| <= 1 (by
-// Remez exchange; relative error 6e-7, 7e-7 with the roundings below).
-constexpr float kTanhMax = 1.0f;
-__device__ __forceinline__ float2 tanh_small(float2 v) {
-  const float2 w = __fmul2_rn(v, v);
-  float2 t = make_float2(-0.00306706037f, -0.00306706037f);
-  t = __ffma2_rn(t, w, make_float2(0.0167431142f, 0.0167431142f));
-  t = __ffma2_rn(t, w, make_float2(-0.0516056754f, -0.0516056754f));
-  t = __ffma2_rn(t, w, make_float2(0.132814333f, 0.132814333f));
-  t = __ffma2_rn(t, w, make_float2(-0.333290428f, -0.333290428f));
-  t = __ffma2_rn(t, w, make_float2(0.999999404f, 0.999999404f));
-  return __fmul2_rn(t, v);
+// cap tanh(scale x / cap) of small x: x times a polynomial in x^2, the minimax
+// approximation of tanh(v) / v on |v| <= 1 (degree 5 in v^2, by Remez exchange:
+// relative error 6e-7, 7e-7 with fp32's roundings) with scale and cap folded into
+// the coefficients on the host (tanh_poly in fa_api.cu).
+__device__ __forceinline__ float2 tanh_small(float2 x, const ScoreParams& sc) {
+  const float2 w = __fmul2_rn(x, x);
+  float2 t = make_float2(sc.poly[kTanhTerms - 1], sc.poly[kTanhTerms - 1]);
+#pragma unroll
+  for (int k = kTanhTerms - 2; k >= 0; --k) t = __ffma2_rn(t, w, make_float2(sc.poly[k], sc.poly[k]));
+  return t;  // the factor of x
 }
 
 __device__ __forceinline__ float rcp(float x) {
@@ -40,91 +38,144 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// tanh(v) = 1 - 2 / (1 + e^(2v)) of two values x with v = in x.  A reciprocal each: one
-// of the product of both denominators would let a hidden neighbour's NaN through.
-__device__ __forceinline__ float2 tanh_exact(float2 x, float in2) {
+// r = 1 / (1 + e^(2v)): tanh(v) = 1 - 2 r.  A reciprocal each: one of the product of
+// both denominators would let a hidden neighbour's NaN through.
+__device__ __forceinline__ float2 tanh_rest(float2 x, float in2) {
   const float2 z = __fmul2_rn(x, make_float2(in2, in2));
   const float2 a = __fadd2_rn(make_float2(ptx::ex2(z.x), ptx::ex2(z.y)), make_float2(1.f, 1.f));
-  return __ffma2_rn(make_float2(rcp(a.x), rcp(a.y)), make_float2(-2.f, -2.f), make_float2(1.f, 1.f));
+  return make_float2(rcp(a.x), rcp(a.y));
 }
 
-// Largest |x| of N scores (N a multiple of 2); NaN does not count.
+// Largest |x| of N scores (N a multiple of 8); NaN does not count.
 template <int N>
 __device__ __forceinline__ float abs_max(const uint32_t* sr) {
-  constexpr int kChains = N >= 64 ? 4 : (N >= 16 ? 2 : 1);
+  constexpr int kChains = N >= 64 ? 4 : 2;
   float m[kChains];
 #pragma unroll
   for (int k = 0; k < kChains; ++k) {
     const uint32_t* v = sr + k * (N / kChains);
-    m[k] = fabsf(__uint_as_float(v[0]));
+    m[k] = 0.f;
 #pragma unroll
-    for (int c = 1; c < N / kChains; ++c) m[k] = fmaxf(m[k], fabsf(__uint_as_float(v[c])));
+    for (int c = 0; c < N / kChains; c += 2)
+      asm("max.abs.f32 %0, %1, %2, %3;"
+          : "=f"(m[k])
+          : "f"(m[k]), "f"(__uint_as_float(v[c])), "f"(__uint_as_float(v[c + 1])));
   }
 #pragma unroll
   for (int k = 1; k < kChains; ++k) m[0] = fmaxf(m[0], m[k]);
   return m[0];
 }
 
-// Where a row's keys lie, for the bias: all of the block at or before the row
-// (and in causal calls wherever it counts), all behind it, or on both sides.
-enum ScoreSide { kSideLeft = 0, kSideRight = 1, kSideBoth = 2 };
-
-// tanh of two scores x (v = in x) by the rule of both forms: a score alone decides
-// which one gives it, so that nothing else in the warp's registers has a say in its
-// bits.  `all_small` (of the warp): no score needs the exact form.
-__device__ __forceinline__ float2 tanh2(float2 x, const ScoreParams& sc, bool all_small) {
-  const float2 v = __fmul2_rn(x, make_float2(sc.in, sc.in));
-  float2 t = tanh_small(v);
-  if (!all_small) {
-    const float2 u = tanh_exact(x, sc.in2);
-    t.x = fabsf(v.x) <= kTanhMax ? t.x : u.x;
-    t.y = fabsf(v.y) <= kTanhMax ? t.y : u.y;
+// Scores of two products x plus b (bias, minus the maximum or L).  kCapAny looks at
+// each score; kCapSmall is for warps whose scores are all small: the same bits.
+enum CapForm { kNoCap = 0, kCapSmall = 1, kCapAny = 2 };
+template <CapForm F>
+__device__ __forceinline__ float2 score2(float2 x, float2 b, const ScoreParams& sc, float2 c2) {
+  if constexpr (F == kNoCap) return __ffma2_rn(x, c2, b);
+  float2 y = __ffma2_rn(x, tanh_small(x, sc), b);
+  if constexpr (F == kCapAny) {
+    const float2 u = __ffma2_rn(tanh_rest(x, sc.in2), make_float2(-2.f * sc.cap, -2.f * sc.cap),
+                                __fadd2_rn(b, make_float2(sc.cap, sc.cap)));
+    y.x = fabsf(x.x) <= sc.small ? y.x : u.x;
+    y.y = fabsf(x.y) <= sc.small ? y.y : u.y;
   }
-  return t;
+  return y;
 }
 
-// N products x of one row become capped, scaled base-2 scores in place (without a
-// cap: times scale_log2).  The whole warp calls it.
+// A row against the keys of a block, column c at distance d0 + c (key - row).  Its
+// bias is s c + s d0 with s = s_h for keys at or before the row, -s_h for those
+// behind: in a block on one side of all of its tile's rows, s d0 is a constant of
+// the row (`fixed`), which joins minus the maximum.  (Causal calls: what lies behind
+// the row is hidden, and a block counts as one at or before it.)
+struct RowBias {
+  float slope;  // s_h (0: no bias)
+  float s;      // of a one-sided block; 0 in one on both sides
+  float fixed;  // s d0
+  int d0;
+  bool both;
+};
+__device__ __forceinline__ RowBias row_bias(float slope, int d0, bool left, bool right) {
+  const float s = left ? slope : (right ? -slope : 0.f);
+  return RowBias{slope, s, s * static_cast<float>(d0), d0, !left && !right};
+}
+
+// The columns lo .. lim of a block, each key where its index says.
+struct PlainCols {
+  int lo, lim;
+  __device__ __forceinline__ bool seen(int c) const { return c >= lo && c <= lim; }
+  __device__ __forceinline__ int off(int c) const { return c; }
+  static constexpr bool kOff = false;
+};
+
+// The scores of a block, less the row's constant, in two forms that agree to the bit
+// where both apply.  In registers, for warps whose block is one-sided, uncut and
+// (under a cap) all small:
 template <int N>
-__device__ __forceinline__ void cap_row(uint32_t* sr, const ScoreParams& sc, float scale_log2) {
-  if (sc.cap != 0.f) {
-    auto capped = [&](bool all_small) {
+__device__ __forceinline__ void scores_fast(uint32_t* sr, const ScoreParams& sc, float2 c2, float s) {
+  auto each = [&](auto form) {
 #pragma unroll
-      for (int c = 0; c < N; c += 2) {
-        const float2 t = tanh2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc, all_small);
-        const float2 y = __fmul2_rn(t, make_float2(sc.cap, sc.cap));
-        sr[c] = __float_as_uint(y.x);
-        sr[c + 1] = __float_as_uint(y.y);
+    for (int c = 0; c < N; c += 2) {
+      const float2 y = form(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
+                            __fmul2_rn(make_float2(s, s), make_float2(static_cast<float>(c), static_cast<float>(c + 1))));
+      sr[c] = __float_as_uint(y.x);
+      sr[c + 1] = __float_as_uint(y.y);
+    }
+  };
+  if (sc.cap == 0.f)
+    each([&](float2 x, float2 b) { return score2<kNoCap>(x, b, sc, c2); });
+  else if (sc.slopes != nullptr)
+    each([&](float2 x, float2 b) { return score2<kCapSmall>(x, b, sc, c2); });
+  else
+    each([&](float2 x, float2) { return __fmul2_rn(x, tanh_small(x, sc)); });
+}
+// And for any block, -inf where the row does not see the key: from TMEM (column t_s
+// on) and back to it, 16 columns at a time in a rolled loop.  Blocks that need it are
+// few, and their code must be short: unrolled over a block's columns, beside the fast
+// form, it made the warps wait for instructions most of the time (causal B2 H16/4
+// S4096 D128, capped: 1410 us).
+template <int N, typename Cols>
+__device__ __forceinline__ void scores_slow(uint32_t t_s, const ScoreParams& sc, float2 c2, const RowBias& r,
+                                            const Cols& cols) {
+#pragma unroll 1
+  for (int k0 = 0; k0 < N; k0 += 16) {
+    uint32_t x16[16];
+    ptx::tmem_ld16(t_s + k0, x16);
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+      float2 b = make_float2(0.f, 0.f);
+      if (sc.slopes != nullptr) {
+        const int e0 = cols.off(k0 + c), e1 = cols.off(k0 + c + 1);
+        b = __fmul2_rn(make_float2(r.s, r.s), make_float2(static_cast<float>(e0), static_cast<float>(e1)));
+        if (r.both)
+          b = make_float2(-r.slope * fabsf(static_cast<float>(r.d0 + e0)),
+                          -r.slope * fabsf(static_cast<float>(r.d0 + e1)));
+        if (Cols::kOff && r.d0 + e0 > 0) b.x = fmaf(-r.slope, static_cast<float>(e0), -2.f * r.fixed);
+        if (Cols::kOff && r.d0 + e1 > 0) b.y = fmaf(-r.slope, static_cast<float>(e1), -2.f * r.fixed);
       }
-    };
-    if (__any_sync(0xffffffffu, abs_max<N>(sr) * fabsf(sc.in) > kTanhMax)) capped(false);
-    else capped(true);
-  } else {
-#pragma unroll
-    for (int c = 0; c < N; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * scale_log2);
+      const float2 x = make_float2(__uint_as_float(x16[c]), __uint_as_float(x16[c + 1]));
+      const float2 y = sc.cap != 0.f ? score2<kCapAny>(x, b, sc, c2) : score2<kNoCap>(x, b, sc, c2);
+      x16[c] = cols.seen(k0 + c) ? __float_as_uint(y.x) : __float_as_uint(-INFINITY);
+      x16[c + 1] = cols.seen(k0 + c + 1) ? __float_as_uint(y.y) : __float_as_uint(-INFINITY);
+    }
+    ptx::tmem_st16(t_s + k0, x16);
   }
+  ptx::tmem_st_wait();
 }
 
-// Their bias: column c stands d0 + c behind the row.  slope: s_h.
-template <int N>
-__device__ __forceinline__ void bias_row(uint32_t* sr, float slope, int d0, ScoreSide side) {
-  if (side == kSideBoth) {
-#pragma unroll
-    for (int c = 0; c < N; ++c)
-      sr[c] = __float_as_uint(fmaf(-slope, fabsf(static_cast<float>(d0 + c)), __uint_as_float(sr[c])));
-    return;
-  }
-  // -s |d| with d = d0 + c of one sign.  The distance d0 + c is formed first (exact
-  // below 2^24), so each score's bias is rounded once.
-  const float s = side == kSideLeft ? slope : -slope;
-  const float f0 = static_cast<float>(d0);
-  const float2 s2 = make_float2(s, s);
-#pragma unroll
-  for (int c = 0; c < N; c += 2) {
-    const float2 d = make_float2(f0 + static_cast<float>(c), f0 + static_cast<float>(c + 1));
-    const float2 y = __ffma2_rn(s2, d, make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])));
-    sr[c] = __float_as_uint(y.x);
-    sr[c + 1] = __float_as_uint(y.y);
+// A block's scores in place of the products that sr holds, loaded from column t_s on.
+// `cut`: some of them are not seen.
+template <int N, typename Cols>
+__device__ __forceinline__ void block_scores(uint32_t* sr, uint32_t t_s, const ScoreParams& sc, float2 c2,
+                                             const RowBias& r, bool cut, const Cols& cols) {
+  static_assert(N == 64 || N == 128, "block width");
+  const bool slow = cut || (sc.slopes != nullptr && r.both) ||
+                    (sc.cap != 0.f && __any_sync(0xffffffffu, !(abs_max<N>(sr) <= sc.small)));
+  if (slow) {
+    scores_slow<N>(t_s, sc, c2, r, cols);
+    if constexpr (N == 128) ptx::tmem_ld128(t_s, sr);
+    else ptx::tmem_ld64(t_s, sr);
+  } else {
+    scores_fast<N>(sr, sc, c2, r.s);
   }
 }
 
