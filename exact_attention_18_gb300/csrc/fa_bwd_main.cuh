@@ -77,41 +77,6 @@ struct BwdLayout {
 __device__ __forceinline__ uint32_t packed_col(int kk) { return kk < 2 ? kk * 8 : 32 + (kk - 2) * 8; }
 
 
-// Modified scores in the backward: what a thread needs to form them from the
-// products again, and the cap's derivative.
-struct ScoreGrad {
-  ScoreParams sc;
-  float slope;     // s_h
-  float curve;     // -1 / c^2: the derivative of y = c tanh is 1 + curve y^2
-  int d0;          // distance key - query of this thread's first row and column
-  int side;        // of the block: -1 all keys at or before their queries, 1 behind them, 0 both
-  template <int N>
-  __device__ __forceinline__ bool all_small(const uint32_t* xs) const {
-    return sc.cap == 0.f || !__any_sync(0xffffffffu, !(abs_max<N>(xs) <= sc.small));
-  }
-  // Base-2 scores of two products x plus `add`, and (under a cap) their derivative
-  // by scale x.  d: key - query of the first; step: of the second minus that.
-  __device__ __forceinline__ float2 score(float2 x, float2 c2, float2 add, int d, int step, bool small,
-                                          float2* ds_dx) const {
-    if (sc.slopes != nullptr) {
-      const float s = side > 0 ? -slope : slope;
-      float2 f = make_float2(static_cast<float>(d), static_cast<float>(d + step));
-      if (side == 0) f = make_float2(-fabsf(f.x), -fabsf(f.y));
-      add = __ffma2_rn(make_float2(s, s), f, add);
-    }
-    if (sc.cap == 0.f) return __ffma2_rn(x, c2, add);
-    float2 y = __fmul2_rn(x, tanh_small(x, sc));
-    if (!small) {
-      const float2 u = __ffma2_rn(tanh_rest(x, sc.in2), make_float2(-2.f * sc.cap, -2.f * sc.cap),
-                                  make_float2(sc.cap, sc.cap));
-      y.x = fabsf(x.x) <= sc.small ? y.x : u.x;
-      y.y = fabsf(x.y) <= sc.small ? y.y : u.y;
-    }
-    *ds_dx = __ffma2_rn(__fmul2_rn(y, make_float2(curve, curve)), y, make_float2(1.f, 1.f));
-    return __fadd2_rn(y, add);
-  }
-};
-
 // One warp's 32 partner columns of a block: from the scores X and the
 // gradient products Y (fp32, TMEM) form P = exp2(c X - L log2 e) and
 // dS = P o (Y - Delta) and write them back as 16-bit pairs over the columns
@@ -119,21 +84,16 @@ struct ScoreGrad {
 // column is a partner query whose L and Delta come from lv, dv; in the dQ
 // pass they are the thread's own row's.  With DIAG the causal mask zeroes
 // partner column c where c < lim (dK/dV pass) or c > lim (dQ pass); with WIN
-// (a window band, dQ pass) also where c < lo.  SCORED (dQ pass): the scores are
-// sg's, and dS gets the cap's derivative.
-template <bool BF16, bool KV_OUTER, bool DIAG, bool WIN = false, bool SCORED = false>
+// (a window band, dQ pass) also where c < lo.
+template <bool BF16, bool KV_OUTER, bool DIAG, bool WIN = false>
 __device__ __forceinline__ void grad_block(uint32_t tX, uint32_t tY, const float* lv, const float* dv, float2 c2,
-                                           float my_l2, float my_delta, int lim, int lo = 0,
-                                           const ScoreGrad& sg = ScoreGrad()) {
-  static_assert(!(SCORED && KV_OUTER), "the dK/dV pass has grad_block_kv");
+                                           float my_l2, float my_delta, int lim, int lo = 0) {
   constexpr float kLog2e = 1.4426950408889634f;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t xs[16], ys[16];
     tmem_ld16x2(tX + 16 * h, xs, tY + 16 * h, ys);
     uint32_t pk[8], dk[8];
-    bool small = true;
-    if constexpr (SCORED) small = sg.all_small<16>(xs);
 #pragma unroll
     for (int c = 0; c < 16; c += 2) {
       const int cc = 16 * h + c;
@@ -145,10 +105,7 @@ __device__ __forceinline__ void grad_block(uint32_t tX, uint32_t tY, const float
         nl2 = make_float2(-my_l2, -my_l2);
         dl = make_float2(my_delta, my_delta);
       }
-      const float2 x = make_float2(__uint_as_float(xs[c]), __uint_as_float(xs[c + 1]));
-      float2 y, ds_dx;
-      if constexpr (SCORED) y = sg.score(x, c2, nl2, sg.d0 + cc, 1, small, &ds_dx);
-      else y = __ffma2_rn(x, c2, nl2);
+      const float2 y = __ffma2_rn(make_float2(__uint_as_float(xs[c]), __uint_as_float(xs[c + 1])), c2, nl2);
       float2 pr = make_float2(ex2(y.x), ex2(y.y));
       if constexpr (DIAG) {
         if ((KV_OUTER ? cc < lim : cc > lim) || (WIN && cc < lo)) pr.x = 0.f;
@@ -156,10 +113,7 @@ __device__ __forceinline__ void grad_block(uint32_t tX, uint32_t tY, const float
       }
       const float2 gr = __fadd2_rn(make_float2(__uint_as_float(ys[c]), __uint_as_float(ys[c + 1])),
                                    make_float2(-dl.x, -dl.y));
-      float2 ds = __fmul2_rn(pr, gr);
-      if constexpr (SCORED) {
-        if (sg.sc.cap != 0.f) ds = __fmul2_rn(ds, ds_dx);
-      }
+      const float2 ds = __fmul2_rn(pr, gr);
       pk[c / 2] = pack2<BF16>(pr.x, pr.y);
       dk[c / 2] = pack2<BF16>(ds.x, ds.y);
     }
@@ -181,12 +135,10 @@ __device__ __forceinline__ void grad_block(uint32_t tX, uint32_t tY, const float
 // (8i + 2(t%4)) / 2 = 4i + t%4, the layout the accumulation MMAs read.
 // lim0: key index of the warp's first row minus its first partner column.
 // With WIN (a window band) the mask keeps, for key row j, the partner
-// queries j - wr .. j + wl: columns lim - wr .. lim + wl.  SCORED as above; its
-// prefix lets all queries see the keys with lim < pfx (pfx relative as lim is).
-template <bool BF16, bool DIAG, bool WIN = false, bool SCORED = false>
+// queries j - wr .. j + wl: columns lim - wr .. lim + wl.
+template <bool BF16, bool DIAG, bool WIN = false>
 __device__ __forceinline__ void grad_block_kv(uint32_t tX, uint32_t tY, const float* lv, const float* dv, float2 c2,
-                                              int lim0, int wr = 0, int wl = 0, int pfx = 0,
-                                              const ScoreGrad& sg = ScoreGrad()) {
+                                              int lim0, int wr = 0, int wl = 0) {
   constexpr float kLog2e = 1.4426950408889634f;
   const int lane = threadIdx.x & 31;
   const int u = lane & 3;   // column pair within each group of 8
@@ -207,43 +159,228 @@ __device__ __forceinline__ void grad_block_kv(uint32_t tX, uint32_t tY, const fl
     tmem_ld16x256b_x4(tY + lane_off, ys);
     tmem_ld_wait();
     uint32_t pk[8], dk[8];
-    bool small = true;
-    if constexpr (SCORED) small = sg.all_small<16>(xs);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int e = 4 * i + 2 * k;
-        const float2 x = make_float2(__uint_as_float(xs[e]), __uint_as_float(xs[e + 1]));
-        float2 y, ds_dx;
-        if constexpr (SCORED)
-          y = sg.score(x, c2, nl2[i], sg.d0 + 16 * half + r + 8 * k - (8 * i + 2 * u), -1, small, &ds_dx);
-        else
-          y = __ffma2_rn(x, c2, nl2[i]);
+        const float2 y = __ffma2_rn(make_float2(__uint_as_float(xs[e]), __uint_as_float(xs[e + 1])), c2, nl2[i]);
         float2 pr = make_float2(ex2(y.x), ex2(y.y));
         if constexpr (DIAG) {
           const int lim = lim0 + 16 * half + r + 8 * k;  // zero partner columns c < lim (query before key)
           const int cc = 8 * i + 2 * u;
           if constexpr (WIN) {
-            const int from = SCORED && lim < pfx ? -kNoWindow : lim - wr;
-            if (cc < from || cc > lim + wl) pr.x = 0.f;
-            if (cc + 1 < from || cc + 1 > lim + wl) pr.y = 0.f;
+            if (cc < lim - wr || cc > lim + wl) pr.x = 0.f;
+            if (cc + 1 < lim - wr || cc + 1 > lim + wl) pr.y = 0.f;
           } else {
             if (cc < lim) pr.x = 0.f;
             if (cc + 1 < lim) pr.y = 0.f;
           }
         }
         const float2 gr = __fadd2_rn(make_float2(__uint_as_float(ys[e]), __uint_as_float(ys[e + 1])), dl[i]);
-        float2 ds = __fmul2_rn(pr, gr);
-        if constexpr (SCORED) {
-          if (sg.sc.cap != 0.f) ds = __fmul2_rn(ds, ds_dx);
-        }
+        const float2 ds = __fmul2_rn(pr, gr);
         pk[2 * i + k] = pack2<BF16>(pr.x, pr.y);
         dk[2 * i + k] = pack2<BF16>(ds.x, ds.y);
       }
     }
     tmem_st16x128b_x4(tX + lane_off, pk);
     tmem_st16x128b_x4(tY + lane_off, dk);
+  }
+}
+
+// Modified scores.  Of two products x: y = their base-2 scores plus `add` (minus L
+// log2 e and the bias), and under a cap f = 1 - tanh^2, from the cap's own value
+// c tanh: f = 1 - (c tanh)^2 / c^2.
+template <CapForm F>
+__device__ __forceinline__ float2 grad_score(float2 x, float2 add, const ScoreParams& sc, float2 c2, float curve,
+                                             float2* f) {
+  if constexpr (F == kNoCap) return __ffma2_rn(x, c2, add);
+  float2 y = __fmul2_rn(x, tanh_small(x, sc));
+  if constexpr (F == kCapAny) {
+    const float2 u =
+        __ffma2_rn(tanh_rest(x, sc.in2), make_float2(-2.f * sc.cap, -2.f * sc.cap), make_float2(sc.cap, sc.cap));
+    y.x = fabsf(x.x) <= sc.small ? y.x : u.x;
+    y.y = fabsf(x.y) <= sc.small ? y.y : u.y;
+  }
+  *f = __ffma2_rn(__fmul2_rn(y, make_float2(curve, curve)), y, make_float2(1.f, 1.f));
+  return __fadd2_rn(y, add);
+}
+template <int N>
+__device__ __forceinline__ bool all_small(const uint32_t* xs, const ScoreParams& sc) {
+  return __all_sync(0xffffffffu, abs_max<N>(xs) <= sc.small);
+}
+
+// What a thread of either pass knows of a block beside the products.
+struct ScoreBlock {
+  float slope;   // s_h
+  float curve;   // -1 / c^2
+  int side;      // keys at or before their queries (-1), behind them (1), on both sides (0)
+  int d0;        // distance key - query at the thread's first row and column
+  bool edge;     // a mask cuts the block: the limits count
+  int lo, hi;    // dQ pass: visible columns; dK/dV pass: see below
+  int wl, pfx;   // dK/dV pass
+};
+
+// grad_block (dQ pass) with modified scores.  FAST: blocks that no mask cuts, on one
+// side of their queries, all of whose scores are small; the rest in a rolled loop
+// with the same arithmetic (their code is to be short, as in the forward).
+template <bool BF16, bool FAST, CapForm F, bool BIAS>
+__device__ __forceinline__ void grad_half_scored(uint32_t tX, uint32_t tY, int h, const ScoreParams& sc, float2 c2,
+                                                 float my_l2, float my_delta, const ScoreBlock& sb) {
+  uint32_t xs[16], ys[16];
+  tmem_ld16x2(tX + 16 * h, xs, tY + 16 * h, ys);
+  uint32_t dk[8];
+  // Column cc's bias is s cc + s d0; the latter joins -L.
+  const float s = sb.side > 0 ? -sb.slope : sb.slope;
+  const float nb = BIAS ? fmaf(s, static_cast<float>(sb.d0 + 16 * h), -my_l2) : -my_l2;
+#pragma unroll
+  for (int c = 0; c < 16; c += 2) {
+    float2 add = make_float2(nb, nb);
+    if constexpr (BIAS)
+      add = __ffma2_rn(make_float2(s, s), make_float2(static_cast<float>(c), static_cast<float>(c + 1)), add);
+    const int cc = 16 * h + c;
+    if (BIAS && !FAST && sb.side == 0)
+      add = make_float2(fmaf(-sb.slope, fabsf(static_cast<float>(sb.d0 + cc)), -my_l2),
+                        fmaf(-sb.slope, fabsf(static_cast<float>(sb.d0 + cc + 1)), -my_l2));
+    const float2 x = make_float2(__uint_as_float(xs[c]), __uint_as_float(xs[c + 1]));
+    float2 f;
+    const float2 y = grad_score<F>(x, add, sc, c2, sb.curve, &f);
+    float2 pr = make_float2(ex2(y.x), ex2(y.y));
+    if (!FAST && sb.edge) {
+      if (cc < sb.lo || cc > sb.hi) pr.x = 0.f;
+      if (cc + 1 < sb.lo || cc + 1 > sb.hi) pr.y = 0.f;
+    }
+    const float2 gr = __fadd2_rn(make_float2(__uint_as_float(ys[c]), __uint_as_float(ys[c + 1])),
+                                 make_float2(-my_delta, -my_delta));
+    float2 ds = __fmul2_rn(pr, gr);
+    if constexpr (F != kNoCap) ds = __fmul2_rn(ds, f);
+    dk[c / 2] = pack2<BF16>(ds.x, ds.y);
+  }
+  tmem_st8(tY + 8 * h, dk);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void grad_block_scored(uint32_t tX, uint32_t tY, const ScoreParams& sc, float2 c2,
+                                                  float my_l2, float my_delta, const ScoreBlock& sb) {
+  const bool capped = sc.cap != 0.f, biased = sc.slopes != nullptr;
+  bool fast = !sb.edge && (sb.side != 0 || !biased);
+  if (fast && capped) {
+    uint32_t xs[32];
+    tmem_ld32(tX, xs);
+    fast = all_small<32>(xs, sc);
+  }
+  auto both = [&](auto half) {
+    half(0);
+    half(1);
+  };
+  if (!fast) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      if (capped) grad_half_scored<BF16, false, kCapAny, true>(tX, tY, h, sc, c2, my_l2, my_delta, sb);
+      else grad_half_scored<BF16, false, kNoCap, true>(tX, tY, h, sc, c2, my_l2, my_delta, sb);
+    }
+  } else if (!capped) {
+    both([&](int h) { grad_half_scored<BF16, true, kNoCap, true>(tX, tY, h, sc, c2, my_l2, my_delta, sb); });
+  } else if (biased) {
+    both([&](int h) { grad_half_scored<BF16, true, kCapSmall, true>(tX, tY, h, sc, c2, my_l2, my_delta, sb); });
+  } else {
+    both([&](int h) { grad_half_scored<BF16, true, kCapSmall, false>(tX, tY, h, sc, c2, my_l2, my_delta, sb); });
+  }
+}
+
+// grad_block_kv with modified scores, in the same two forms.  A key row at distance
+// d0 + its row sees (from its own mask) the partner queries hi + row .. lo + row of
+// columns, all up to the latter where its key lies before the prefix (pfx).
+template <bool BF16, bool FAST, CapForm F, bool BIAS>
+__device__ __forceinline__ void grad_half_kv_scored(uint32_t tX, uint32_t tY, int half, const float2* nl2,
+                                                    const float2* dl, const ScoreParams& sc, float2 c2,
+                                                    const ScoreBlock& sb) {
+  const int lane = threadIdx.x & 31;
+  const int u = lane & 3, r = lane >> 2;
+  const uint32_t lane_off = static_cast<uint32_t>(16 * half) << 16;
+  uint32_t xs[16], ys[16];
+  tmem_ld16x256b_x4(tX + lane_off, xs);
+  tmem_ld16x256b_x4(tY + lane_off, ys);
+  tmem_ld_wait();
+  uint32_t pk[8], dk[8];
+  const float s = sb.side > 0 ? -sb.slope : sb.slope;
+  // s (row - first column of the thread), of its two rows of this half
+  float row[2] = {0.f, 0.f};
+  if constexpr (BIAS) {
+    row[0] = s * static_cast<float>(sb.d0 + 16 * half + r - 2 * u);
+    row[1] = s * static_cast<float>(sb.d0 + 16 * half + r + 8 - 2 * u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 nb = nl2[i];
+    if constexpr (BIAS)
+      nb = __ffma2_rn(make_float2(s, s), make_float2(-8.f * static_cast<float>(i), -8.f * static_cast<float>(i) - 1.f), nb);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int e = 4 * i + 2 * k;
+      const int line = 16 * half + r + 8 * k, cc = 8 * i + 2 * u;
+      float2 add = nb;
+      if constexpr (BIAS) add = __fadd2_rn(nb, make_float2(row[k], row[k]));
+      if (BIAS && !FAST && sb.side == 0)
+        add = make_float2(fmaf(-sb.slope, fabsf(static_cast<float>(sb.d0 + line - cc)), nl2[i].x),
+                          fmaf(-sb.slope, fabsf(static_cast<float>(sb.d0 + line - cc - 1)), nl2[i].y));
+      const float2 x = make_float2(__uint_as_float(xs[e]), __uint_as_float(xs[e + 1]));
+      float2 f;
+      const float2 y = grad_score<F>(x, add, sc, c2, sb.curve, &f);
+      float2 pr = make_float2(ex2(y.x), ex2(y.y));
+      if (!FAST && sb.edge) {
+        const int lim = sb.d0 + line;
+        const int from = lim < sb.pfx ? -kNoWindow : lim - sb.hi;
+        if (cc < from || cc > lim + sb.wl) pr.x = 0.f;
+        if (cc + 1 < from || cc + 1 > lim + sb.wl) pr.y = 0.f;
+      }
+      const float2 gr = __fadd2_rn(make_float2(__uint_as_float(ys[e]), __uint_as_float(ys[e + 1])), dl[i]);
+      float2 ds = __fmul2_rn(pr, gr);
+      if constexpr (F != kNoCap) ds = __fmul2_rn(ds, f);
+      pk[2 * i + k] = pack2<BF16>(pr.x, pr.y);
+      dk[2 * i + k] = pack2<BF16>(ds.x, ds.y);
+    }
+  }
+  tmem_st16x128b_x4(tX + lane_off, pk);
+  tmem_st16x128b_x4(tY + lane_off, dk);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void grad_block_kv_scored(uint32_t tX, uint32_t tY, const float* lv, const float* dv,
+                                                     const ScoreParams& sc, float2 c2, const ScoreBlock& sb) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const int u = threadIdx.x & 3;
+  float2 nl2[4], dl[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 l2 = *reinterpret_cast<const float2*>(lv + 8 * i + 2 * u);
+    nl2[i] = __fmul2_rn(l2, make_float2(-kLog2e, -kLog2e));
+    const float2 d2 = *reinterpret_cast<const float2*>(dv + 8 * i + 2 * u);
+    dl[i] = make_float2(-d2.x, -d2.y);
+  }
+  const bool capped = sc.cap != 0.f, biased = sc.slopes != nullptr;
+  bool fast = !sb.edge && (sb.side != 0 || !biased);
+  if (fast && capped) {
+    uint32_t xs[32];
+    tmem_ld32(tX, xs);
+    fast = all_small<32>(xs, sc);
+  }
+  auto both = [&](auto half) {
+    half(0);
+    half(1);
+  };
+  if (!fast) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      if (capped) grad_half_kv_scored<BF16, false, kCapAny, true>(tX, tY, h, nl2, dl, sc, c2, sb);
+      else grad_half_kv_scored<BF16, false, kNoCap, true>(tX, tY, h, nl2, dl, sc, c2, sb);
+    }
+  } else if (!capped) {
+    both([&](int h) { grad_half_kv_scored<BF16, true, kNoCap, true>(tX, tY, h, nl2, dl, sc, c2, sb); });
+  } else if (biased) {
+    both([&](int h) { grad_half_kv_scored<BF16, true, kCapSmall, true>(tX, tY, h, nl2, dl, sc, c2, sb); });
+  } else {
+    both([&](int h) { grad_half_kv_scored<BF16, true, kCapSmall, false>(tX, tY, h, nl2, dl, sc, c2, sb); });
   }
 }
 
@@ -609,11 +746,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       my_l2 = p.lse[li] * kLog2e;
       my_delta = p.delta[li];
     }
-    ScoreGrad sg;
+    ScoreBlock sb;
     if constexpr (SCORED) {
-      sg.sc = p.sc;
-      sg.slope = 0.f;
-      sg.curve = -1.f / (p.sc.cap * p.sc.cap);  // (unused without a cap)
+      sb.slope = 0.f;
+      sb.curve = -1.f / (p.sc.cap * p.sc.cap);  // (unused without a cap)
     }
     bool alive = true;
     int ph = pz0;  // SCORED, dK/dV pass: partner head of the block
@@ -629,7 +765,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int partner0 = (first + (KV_OUTER ? pi : i)) * kPN;
       if constexpr (SCORED) {
         if (p.sc.slopes != nullptr)
-          sg.slope = __ldg(p.sc.slopes + (KV_OUTER ? ph : bh) % p.heads) * kLog2e;
+          sb.slope = __ldg(p.sc.slopes + (KV_OUTER ? ph : bh) % p.heads) * kLog2e;
       }
       if constexpr (KV_OUTER) {
         pi += kBwdGroups;
@@ -664,25 +800,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           // (causal without a prefix: a key behind its query is hidden, whatever its bias)
           const int key0 = KV_OUTER ? own0 : partner0, key1 = key0 + (KV_OUTER ? 127 : kPN - 1);
           const int row0 = KV_OUTER ? partner0 : own0, row1 = row0 + (KV_OUTER ? kPN - 1 : 127);
-          sg.side = key1 <= row0 || (p.causal && pfx == 0) ? -1 : key0 >= row1 ? 1 : 0;
+          sb.side = key1 <= row0 || (p.causal && pfx == 0) ? -1 : key0 >= row1 ? 1 : 0;
           if constexpr (KV_OUTER) {
-            const int lim0 = own0 + q4 * 32 - partner0 - col0;
-            const bool edge = (partner0 < own0 + 127 - wr && pfx < own0 + 128) || partner0 + kPN - 1 > own0 + wl;
-            sg.d0 = lim0;
-            if (edge)
-              grad_block_kv<BF16, true, true, true>(tX, tY, lv, dv, c2, lim0, wr, wl, pfx - partner0 - col0, sg);
-            else
-              grad_block_kv<BF16, false, false, true>(tX, tY, lv, dv, c2, lim0, 0, 0, 0, sg);
+            sb.edge = (partner0 < own0 + 127 - wr && pfx < own0 + 128) || partner0 + kPN - 1 > own0 + wl;
+            sb.d0 = own0 + q4 * 32 - partner0 - col0;
+            sb.hi = wr;
+            sb.wl = wl;
+            sb.pfx = pfx - partner0 - col0;
+            grad_block_kv_scored<BF16>(tX, tY, lv, dv, p.sc, c2, sb);
           } else {
-            const bool edge = partner0 + kPN - 1 > max(own0 + wr, pfx - 1) || partner0 < own0 + 127 - wl ||
-                              (packed && partner0 + kPN > S);
-            const int hi = max(min(S - 1, my + wr), pfx - 1) - partner0 - col0;
-            const int lo = my - wl - partner0 - col0;
-            sg.d0 = partner0 + col0 - my;
-            if (edge)
-              grad_block<BF16, false, true, true, true>(tX, tY, lv, dv, c2, my_l2, my_delta, hi, lo, sg);
-            else
-              grad_block<BF16, false, false, false, true>(tX, tY, lv, dv, c2, my_l2, my_delta, hi, 0, sg);
+            sb.edge = partner0 + kPN - 1 > max(own0 + wr, pfx - 1) || partner0 < own0 + 127 - wl ||
+                      (packed && partner0 + kPN > S);
+            sb.hi = max(min(S - 1, my + wr), pfx - 1) - partner0 - col0;
+            sb.lo = my - wl - partner0 - col0;
+            sb.d0 = partner0 + col0 - my;
+            grad_block_scored<BF16>(tX, tY, p.sc, c2, my_l2, my_delta, sb);
           }
         } else if constexpr (KV_OUTER) {
           const bool edge = partner0 < own0 + 127 - wr || partner0 + kPN - 1 > own0 + wl;

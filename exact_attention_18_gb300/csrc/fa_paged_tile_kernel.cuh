@@ -124,18 +124,24 @@ __device__ __forceinline__ TileSpan tile_span(const P& p, const SegWalk<SHIFT, t
 }
 
 // The columns of a block that holds new tokens of a tree: a row sees those whose bit
-// is set, and a drafted key stands at its position.
-template <int N>
+// is set, and of the keys before them those from column `from` on; a drafted key
+// stands at its position.
 struct TreeCols {
   int key0, first, kv_len;  // first key of the block, first new key, keys
   const int* positions;     // of the sequence's new tokens
   const unsigned* row;      // the row's bits (nullptr: none)
-  int from;                 // first column that the window leaves
+  int words, from;
   static constexpr bool kOff = true;
-  __device__ __forceinline__ bool seen(int c) const {
-    const int j = key0 + c - first;  // new token
-    if (j < 0) return c >= from;
-    return row != nullptr && key0 + c < kv_len && (row[j >> 5] >> (j & 31) & 1u) != 0;
+  __device__ __forceinline__ unsigned word(int c0) const {
+    const int j0 = key0 + c0 - first;  // new token of the first of the 32 columns; below 0: a key before them
+    unsigned x = ~0u;
+    if (j0 > -32) {
+      const int i = j0 >> 5;  // -1 .. : the word that holds it
+      const unsigned a = i < 0 ? ~0u : (row != nullptr && i < words ? row[i] : 0u);
+      const unsigned b = row != nullptr && i + 1 < words ? row[i + 1] : 0u;
+      x = __funnelshift_r(a, b, j0 & 31);
+    }
+    return x & bit_range(min(from, first - key0) - c0, kv_len - key0 - c0);
   }
   __device__ __forceinline__ int off(int c) const {
     if (key0 + c < first || key0 + c >= kv_len) return c;
@@ -503,13 +509,14 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           fixed = bias.fixed;
           const float2 cs = make_float2(p.scale_log2, p.scale_log2);
           if (tree && key0 + BN > first) {  // new tokens of a tree
-            TreeCols<BN> cols;
+            TreeCols cols;
             cols.key0 = key0;
             cols.first = first;
             cols.kv_len = kv_len;
             cols.positions = p.positions + tok_first;
             cols.row = row_bits;
-            cols.from = min(pos - p.win_left, first) - key0;
+            cols.words = p.tree_words;
+            cols.from = pos - p.win_left - key0;
             block_scores<BN>(sr, t_s, p.sc, cs, bias, true, cols);
           } else {
             block_scores<BN>(sr, t_s, p.sc, cs, bias, cut, PlainCols{cut ? lo : 0, cut ? lim : BN});

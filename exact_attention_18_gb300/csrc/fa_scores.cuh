@@ -99,17 +99,25 @@ __device__ __forceinline__ RowBias row_bias(float slope, int d0, bool left, bool
   return RowBias{slope, s, s * static_cast<float>(d0), d0, !left && !right};
 }
 
-// The columns lo .. lim of a block, each key where its index says.
+// Columns [lo, hi) of 32 as bits.
+__device__ __forceinline__ unsigned bit_range(int lo, int hi) {
+  const unsigned from = lo <= 0 ? ~0u : (lo >= 32 ? 0u : ~0u << lo);
+  const unsigned to = hi >= 32 ? ~0u : (hi <= 0 ? 0u : ~(~0u << hi));
+  return from & to;
+}
+
+// Which columns of a block a row sees: lo .. lim.  off: where column c's key stands,
+// less the block's first key.
 struct PlainCols {
   int lo, lim;
-  __device__ __forceinline__ bool seen(int c) const { return c >= lo && c <= lim; }
-  __device__ __forceinline__ int off(int c) const { return c; }
   static constexpr bool kOff = false;
+  __device__ __forceinline__ unsigned word(int c0) const { return bit_range(lo - c0, lim + 1 - c0); }
+  __device__ __forceinline__ int off(int c) const { return c; }
 };
 
 // The scores of a block, less the row's constant, in two forms that agree to the bit
-// where both apply.  In registers, for warps whose block is one-sided, uncut and
-// (under a cap) all small:
+// where both apply.  In registers, for warps whose block is one-sided and (under a
+// cap) all small:
 template <int N>
 __device__ __forceinline__ void scores_fast(uint32_t* sr, const ScoreParams& sc, float2 c2, float s) {
   auto each = [&](auto form) {
@@ -121,18 +129,19 @@ __device__ __forceinline__ void scores_fast(uint32_t* sr, const ScoreParams& sc,
       sr[c + 1] = __float_as_uint(y.y);
     }
   };
-  if (sc.cap == 0.f)
-    each([&](float2 x, float2 b) { return score2<kNoCap>(x, b, sc, c2); });
-  else if (sc.slopes != nullptr)
+  if (sc.cap == 0.f) {
+    if (sc.slopes != nullptr) each([&](float2 x, float2 b) { return score2<kNoCap>(x, b, sc, c2); });
+    else each([&](float2 x, float2) { return __fmul2_rn(x, c2); });
+  } else if (sc.slopes != nullptr) {
     each([&](float2 x, float2 b) { return score2<kCapSmall>(x, b, sc, c2); });
-  else
+  } else {
     each([&](float2 x, float2) { return __fmul2_rn(x, tanh_small(x, sc)); });
+  }
 }
-// And for any block, -inf where the row does not see the key: from TMEM (column t_s
-// on) and back to it, 16 columns at a time in a rolled loop.  Blocks that need it are
-// few, and their code must be short: unrolled over a block's columns, beside the fast
-// form, it made the warps wait for instructions most of the time (causal B2 H16/4
-// S4096 D128, capped: 1410 us).
+// And for any block: from TMEM (column t_s on) and back to it, 16 columns at a time in
+// a rolled loop.  Blocks that need it are few, and their code must be short: unrolled
+// over a block's columns, beside the fast form, it made the warps wait for
+// instructions most of the time (causal B2 H16/4 S4096 D128, capped: 1410 us).
 template <int N, typename Cols>
 __device__ __forceinline__ void scores_slow(uint32_t t_s, const ScoreParams& sc, float2 c2, const RowBias& r,
                                             const Cols& cols) {
@@ -154,21 +163,21 @@ __device__ __forceinline__ void scores_slow(uint32_t t_s, const ScoreParams& sc,
       }
       const float2 x = make_float2(__uint_as_float(x16[c]), __uint_as_float(x16[c + 1]));
       const float2 y = sc.cap != 0.f ? score2<kCapAny>(x, b, sc, c2) : score2<kNoCap>(x, b, sc, c2);
-      x16[c] = cols.seen(k0 + c) ? __float_as_uint(y.x) : __float_as_uint(-INFINITY);
-      x16[c + 1] = cols.seen(k0 + c + 1) ? __float_as_uint(y.y) : __float_as_uint(-INFINITY);
+      x16[c] = __float_as_uint(y.x);
+      x16[c + 1] = __float_as_uint(y.y);
     }
     ptx::tmem_st16(t_s + k0, x16);
   }
   ptx::tmem_st_wait();
 }
 
-// A block's scores in place of the products that sr holds, loaded from column t_s on.
-// `cut`: some of them are not seen.
+// A block's scores in place of the products that sr holds, loaded from column t_s on;
+// -inf where `cut` and the row does not see the key.
 template <int N, typename Cols>
 __device__ __forceinline__ void block_scores(uint32_t* sr, uint32_t t_s, const ScoreParams& sc, float2 c2,
                                              const RowBias& r, bool cut, const Cols& cols) {
   static_assert(N == 64 || N == 128, "block width");
-  const bool slow = cut || (sc.slopes != nullptr && r.both) ||
+  const bool slow = (sc.slopes != nullptr && (r.both || Cols::kOff)) ||
                     (sc.cap != 0.f && __any_sync(0xffffffffu, !(abs_max<N>(sr) <= sc.small)));
   if (slow) {
     scores_slow<N>(t_s, sc, c2, r, cols);
@@ -176,6 +185,15 @@ __device__ __forceinline__ void block_scores(uint32_t* sr, uint32_t t_s, const S
     else ptx::tmem_ld64(t_s, sr);
   } else {
     scores_fast<N>(sr, sc, c2, r.s);
+  }
+  if (cut) {
+#pragma unroll
+    for (int c0 = 0; c0 < N; c0 += 32) {
+      const unsigned seen = cols.word(c0);
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        sr[c0 + c] = seen >> c & 1u ? sr[c0 + c] : __float_as_uint(-INFINITY);
+    }
   }
 }
 
