@@ -240,10 +240,10 @@ fa_status encode_input(CUtensorMap* map, const void* base, bool bf16, const Shap
 void tanh_poly(float scale, float cap, fa::ScoreParams* p) {
   constexpr double kC[fa::kTanhTerms] = {0.999999404, -0.333290428, 0.132814333, -0.0516056754, 0.0167431142,
                                          -0.00306706037};
-  const double in = static_cast<double>(scale) / cap, c = static_cast<double>(cap) * 1.4426950408889634074;
-  p->cap = static_cast<float>(c);
+  const double in = static_cast<double>(scale) / cap, top = static_cast<double>(cap) * 1.4426950408889634074;
+  p->cap = static_cast<float>(top);
   p->in2 = static_cast<float>(2 * 1.4426950408889634074 * in);
-  double vmax = 1.0, f = c * in;
+  double vmax = 1.0, f = top * in;
   for (int k = 0; k < fa::kTanhTerms; ++k, f *= in * in) {
     p->poly[k] = static_cast<float>(kC[k] * f);
     const double size = std::fabs(kC[k] * f);

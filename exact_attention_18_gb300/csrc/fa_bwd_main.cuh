@@ -195,13 +195,7 @@ template <CapForm F>
 __device__ __forceinline__ float2 grad_score(float2 x, float2 add, const ScoreParams& sc, float2 c2, float curve,
                                              float2* f) {
   if constexpr (F == kNoCap) return __ffma2_rn(x, c2, add);
-  float2 y = __fmul2_rn(x, tanh_small(x, sc));
-  if constexpr (F == kCapAny) {
-    const float2 u =
-        __ffma2_rn(tanh_rest(x, sc.in2), make_float2(-2.f * sc.cap, -2.f * sc.cap), make_float2(sc.cap, sc.cap));
-    y.x = fabsf(x.x) <= sc.small ? y.x : u.x;
-    y.y = fabsf(x.y) <= sc.small ? y.y : u.y;
-  }
+  const float2 y = score2<F>(x, sc, c2);
   *f = __ffma2_rn(__fmul2_rn(y, make_float2(curve, curve)), y, make_float2(1.f, 1.f));
   return __fadd2_rn(y, add);
 }
@@ -236,8 +230,7 @@ __device__ __forceinline__ void grad_half_scored(uint32_t tX, uint32_t tY, int h
 #pragma unroll
   for (int c = 0; c < 16; c += 2) {
     float2 add = make_float2(nb, nb);
-    if constexpr (BIAS)
-      add = __ffma2_rn(make_float2(s, s), make_float2(static_cast<float>(c), static_cast<float>(c + 1)), add);
+    if constexpr (BIAS) add = make_float2(fmaf(s, static_cast<float>(c), nb), fmaf(s, static_cast<float>(c + 1), nb));
     const int cc = 16 * h + c;
     if (BIAS && !FAST && sb.side == 0)
       add = make_float2(fmaf(-sb.slope, fabsf(static_cast<float>(sb.d0 + cc)), -my_l2),
@@ -313,8 +306,7 @@ __device__ __forceinline__ void grad_half_kv_scored(uint32_t tX, uint32_t tY, in
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float2 nb = nl2[i];
-    if constexpr (BIAS)
-      nb = __ffma2_rn(make_float2(s, s), make_float2(-8.f * static_cast<float>(i), -8.f * static_cast<float>(i) - 1.f), nb);
+    if constexpr (BIAS) nb = make_float2(fmaf(s, -8.f * static_cast<float>(i), nb.x), fmaf(s, -8.f * static_cast<float>(i) - 1.f, nb.y));
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int e = 4 * i + 2 * k;

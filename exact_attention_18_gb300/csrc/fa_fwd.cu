@@ -202,16 +202,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     else return r >= S ? 0 : (p.causal ? min(n_kv, (r + kBlockM + kBlockN - 1) / kBlockN) : n_kv);
   };
   const int kb_cta = first_blk(row0);  // the CTA loads key blocks kb_cta, kb_cta + 1, ...
-  // Tile t uses loaded blocks beg_t .. end_t - 1.
-  const int lo0 = first_blk(row0) - kb_cta, hi0 = blocks_for(row0) - kb_cta;
-  const int lo1 = first_blk(row0 + kBlockM) - kb_cta, hi1 = blocks_for(row0 + kBlockM) - kb_cta;
-  const int beg0 = hi0 > lo0 ? lo0 : 0, end0 = hi0 > lo0 ? hi0 : 0;
-  const int beg1 = hi1 > lo1 ? lo1 : 0, end1 = hi1 > lo1 ? hi1 : 0;
+  // Tile t uses loaded blocks beg_t .. end_t - 1 (SCORED: of the order `ord`).
+  const int hi0 = blocks_for(row0), hi1 = blocks_for(row0 + kBlockM);
+  BlockOrder ord{kb_cta, kb_cta};
+  if constexpr (SCORED)
+    ord = block_order(p.sc, kb_cta, max(hi0, hi1), wl == kNoWindow, (min(S, row0 + 2 * kBlockM) - 1) / kBlockN + 1);
+  auto block_at = [&](int x) -> int {
+    if constexpr (SCORED) return ord.at(x);
+    else return kb_cta + x;
+  };
+  auto span = [&](int lo, int hi, int* beg, int* end) {
+    *beg = 0;
+    *end = 0;
+    if (hi <= lo) return;
+    if constexpr (SCORED) {
+      ord.span(lo, hi, beg, end);
+    } else {
+      *beg = lo - kb_cta;
+      *end = hi - kb_cta;
+    }
+  };
+  int beg0, end0, beg1, end1;
+  span(first_blk(row0), hi0, &beg0, &end0);
+  span(first_blk(row0 + kBlockM), hi1, &beg1, &end1);
   const int nb0 = end0 - beg0;
   const int nb1 = end1 - beg1;
   const int nbp = max(end0, end1);  // blocks the CTA loads
   // As in the four-tile kernel: V rows past a packed sample's end are set to zero.
-  const bool clear_v = SCORED && packed && nbp > 0 && (kb_cta + nbp) * kBlockN > S;
+  const int x_clear = SCORED && packed && nbp > 0 && (kb_cta + nbp) * kBlockN > S ? ord.index(kb_cta + nbp - 1) : -1;
   // TMA coordinates of `row` of `head` (x = column offset): (x, row, head) in
   // the {D, S, heads} maps, (x, head, tok0 + row) in the packed {D, heads, T} maps.
   auto tma_rows = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int x, int row, int head) {
@@ -286,19 +304,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               tma_rows(smem + L::kOffK + sk * L::kTileBytes + ch * L::kChunkBytes + h * kHalfBytes, &tm_k,
-                       &bar_kfull[sk], ch * (L::kRowBytes / 2), (kb_cta + nk) * kBlockN + h * (kBlockN / 2), kvh);
+                       &bar_kfull[sk], ch * (L::kRowBytes / 2), block_at(nk) * kBlockN + h * (kBlockN / 2), kvh);
           ++nk;
           const int sv = nv % L::kStagesV;
           const int uv = nv / L::kStagesV;
           if (uv > 0 && !mbar_wait(&bar_vempty[sv], (uv - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad)) break;
-          uint64_t* vbar = SCORED && clear_v && nv == nbp - 1 ? bar_vtmp : &bar_vfull[sv];
+          uint64_t* vbar = SCORED && nv == x_clear ? bar_vtmp : &bar_vfull[sv];
           mbar_arrive_expect_tx(vbar, L::kTileBytes);
 #pragma unroll
           for (int ch = 0; ch < L::kChunks; ++ch)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               tma_rows(smem + L::kOffV + sv * L::kTileBytes + ch * L::kChunkBytes + h * kHalfBytes, &tm_v,
-                       vbar, ch * (L::kRowBytes / 2), (kb_cta + nv) * kBlockN + h * (kBlockN / 2), kvh);
+                       vbar, ch * (L::kRowBytes / 2), block_at(nv) * kBlockN + h * (kBlockN / 2), kvh);
         }
         // Teardown: every copy this thread started must land before the CTA
         // exits (older copies of a ring were consumed before their stage was
@@ -306,7 +324,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         drain_wait(bar_q, 0, p.err);
         for (int x = (nk > L::kStagesK ? nk - L::kStagesK : 0); x < nk; ++x)
           drain_wait(&bar_kfull[x % L::kStagesK], (x / L::kStagesK) & 1, p.err);
-        if (SCORED && clear_v && nv == nbp) drain_wait(bar_vtmp, 0, p.err);
+        if (SCORED && x_clear >= 0 && x_clear < nv) drain_wait(bar_vtmp, 0, p.err);
         for (int x = (nv > L::kStagesV ? nv - L::kStagesV : 0); x < nv; ++x)
           drain_wait(&bar_vfull[x % L::kStagesV], (x / L::kStagesV) & 1, p.err);
       }
@@ -387,9 +405,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       // Teardown: wait for every MMA this warp issued.
       mma_commit_warp(&bar_drain[t]);
       drain_wait(&bar_drain[t], 0, p.err);
-    } else if (SCORED && clear_v) {
+    } else if (SCORED && x_clear >= 0) {
       // ------------------------------------------------------------ the last V block's cleared rows
-      const int st = (nbp - 1) % L::kStagesV;
+      const int st = x_clear % L::kStagesV;
       if (warp_wait(bar_vtmp, 0, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad)) {
         clear_rows<typename L::G>(smem + L::kOffV + st * L::kTileBytes, kBlockN, S - (kb_cta + nbp - 1) * kBlockN);
         if (lane == 0) mbar_arrive(&bar_vfull[st]);
@@ -405,7 +423,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int row_g = tile_row0 + r;
     const int nb = t == 0 ? nb0 : nb1;
     const int nb_other = t == 0 ? nb1 : nb0;
-    const int kb0 = kb_cta + (t == 0 ? beg0 : beg1);  // the tile's first key block
+    const int x0 = t == 0 ? beg0 : beg1;  // the tile's first loaded block
     const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t t_s = tmem + lane_base + L::kColS + 128u * t;
     const uint32_t t_p = tmem + lane_base + L::kColP + L::kStrideP * t;
@@ -434,7 +452,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       tc_fence_after();
       tmem_ld128(t_s, sr);
       if (L::kSepP) warp_arrive(&bar_sfree[t]);  // S_t(j) is in registers: the MMA may overwrite it
-      const int kv0 = (kb0 + j) * kBlockN;
+      const int kv0 = block_at(x0 + j) * kBlockN;
       const int lim = last - kv0;      // columns c <= lim are visible to this row
       const int lo = first_key - kv0;  // and (general instantiation) c >= lo
       // Masked blocks: the diagonal block under the causal mask (an edge of

@@ -194,9 +194,30 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   int nbp = 0;                         // blocks the CTA loads
 #pragma unroll
   for (int t = 0; t < kF4Tiles; ++t) nbp = max(nbp, blocks_for(row0 + t * kBlockM) - kb_cta);
+  // (SCORED: in the order that `ord` gives; the x-th block loaded is block_at(x))
+  BlockOrder ord{kb_cta, kb_cta};
+  if constexpr (SCORED)
+    ord = block_order(p.sc, kb_cta, kb_cta + nbp, wl == kNoWindow, (min(S, row0 + kF4RowsPerCta) - 1) / kBN + 1);
+  auto block_at = [&](int x) -> int {
+    if constexpr (SCORED) return ord.at(x);
+    else return kb_cta + x;
+  };
+  // Loaded blocks [*beg, *end) of the tile that starts at row r.
+  auto span = [&](int r, int* beg, int* end) {
+    const int lo = first_blk(r), hi = blocks_for(r);
+    *beg = 0;
+    *end = 0;
+    if (hi <= lo) return;
+    if constexpr (SCORED) {
+      ord.span(lo, hi, beg, end);
+    } else {
+      *beg = lo - kb_cta;
+      *end = hi - kb_cta;
+    }
+  };
   // Rows of the last V block past a packed sample's end belong to the next sample
   // or to none, and may hold NaN: they are set to zero (0 * NaN is not 0).
-  const bool clear_v = SCORED && packed && nbp > 0 && (kb_cta + nbp) * kBN > S;
+  const int x_clear = SCORED && packed && nbp > 0 && (kb_cta + nbp) * kBN > S ? ord.index(kb_cta + nbp - 1) : -1;
   // TMA coordinates of `row` of `head`: (row, head) in the {D, S, heads}
   // maps, (head, tok0 + row) in the packed {D, heads, T} maps.
   auto tma_rows = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int row, int head) {
@@ -253,17 +274,17 @@ __global__ void __launch_bounds__(kF4Threads, 1)
           const int use = it / L::kStages;
           if (use > 0 && !mbar_wait(&bar_empty[st], (use - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad)) break;
           mbar_arrive_expect_tx(&bar_kfull[st], GK::kTileBytes);
-          tma_rows(smem + L::kOffK + st * GK::kTileBytes, &tm_k, &bar_kfull[st], (kb_cta + it) * kBN, kvh);
-          uint64_t* vbar = SCORED && clear_v && it == nbp - 1 ? bar_vtmp : &bar_vfull[st];
+          tma_rows(smem + L::kOffK + st * GK::kTileBytes, &tm_k, &bar_kfull[st], block_at(it) * kBN, kvh);
+          uint64_t* vbar = SCORED && it == x_clear ? bar_vtmp : &bar_vfull[st];
           mbar_arrive_expect_tx(vbar, GK::kTileBytes);
-          tma_rows(smem + L::kOffV + st * GK::kTileBytes, &tm_v, vbar, (kb_cta + it) * kBN, kvh);
+          tma_rows(smem + L::kOffV + st * GK::kTileBytes, &tm_v, vbar, block_at(it) * kBN, kvh);
         }
         // Teardown: every copy this thread started must land before the CTA exits.
         drain_wait(bar_q, 0, p.err);
+        if (SCORED && x_clear >= 0 && x_clear < it) drain_wait(bar_vtmp, 0, p.err);
         for (int x = (it > L::kStages ? it - L::kStages : 0); x < it; ++x) {
           const int st = x % L::kStages;
           drain_wait(&bar_kfull[st], (x / L::kStages) & 1, p.err);
-          if (SCORED && clear_v && x == nbp - 1) drain_wait(bar_vtmp, 0, p.err);
           drain_wait(&bar_vfull[st], (x / L::kStages) & 1, p.err);
         }
       }
@@ -279,9 +300,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
 #pragma unroll
       for (int h = 0; h < kF4TilesPerMma; ++h) {
         const int r = row0 + (w * kF4TilesPerMma + h) * kBlockM;
-        const int lo = first_blk(r) - kb_cta, hi = blocks_for(r) - kb_cta;
-        beg[h] = hi > lo ? lo : 0;
-        nbt[h] = hi > lo ? hi : 0;
+        span(r, &beg[h], &nbt[h]);
         nbw = max(nbw, nbt[h]);
       }
       constexpr uint32_t idesc_qk = make_idesc_f16(BF16, 128, kBN, false, false);
@@ -432,9 +451,9 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       // Teardown: wait for every MMA this warp issued.
       mma_commit_warp(&bar_drain[w]);
       drain_wait(&bar_drain[w], 0, p.err);
-    } else if (SCORED && clear_v) {
+    } else if (SCORED && x_clear >= 0) {
       // ------------------------------------------------------------ the last V block's cleared rows
-      const int st = (nbp - 1) % L::kStages;
+      const int st = x_clear % L::kStages;
       if (warp_wait(bar_vtmp, 0, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad)) {
         clear_rows<GK>(smem + L::kOffV + st * GK::kTileBytes, kBN, S - (kb_cta + nbp - 1) * kBN);
         if (lane == 0) mbar_arrive(&bar_vfull[st]);
@@ -448,8 +467,9 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     const int r = q4 * 32 + lane;
     const int tile_row0 = row0 + t * kBlockM;
     const int row_g = tile_row0 + r;
-    const int kb0 = first_blk(tile_row0);  // the tile's first key block
-    const int nb = max(0, blocks_for(tile_row0) - kb0);
+    int x0, x1;  // the tile's loaded blocks
+    span(tile_row0, &x0, &x1);
+    const int nb = x1 - x0;
     const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t t_s = tmem + lane_base + 128u * t;  // S_t, and P_t over it
     const uint32_t t_o = t_s + L::kColO;
@@ -476,7 +496,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       tc_fence_after();
       uint32_t sr[kBN];
       tmem_ld64(t_s, sr);
-      const int kv0 = (kb0 + j) * kBN;
+      const int kv0 = block_at(x0 + j) * kBN;
       const int lim = last - kv0;      // columns c <= lim are visible to this row
       const int lo = first_key - kv0;  // and (general instantiation) c >= lo
       // Masked blocks: those crossing the diagonal under the causal mask (an

@@ -458,14 +458,14 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
         if constexpr (kScored) {
           if (ok) {
             // In place: the scores, scaled; the cap by its polynomial or exactly, each by itself.
-            const float2 cs = make_float2(p.scale_log2, p.scale_log2), none = make_float2(0.f, 0.f);
+            const float2 cs = make_float2(p.scale_log2, p.scale_log2);
             const bool all_small = __all_sync(0xffffffffu, abs_max<NC>(sr) <= p.sc.small);
 #pragma unroll
             for (int k = 0; k < NC; k += 2) {
               const float2 x = make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
-              const float2 y = p.sc.cap == 0.f ? score2<kNoCap>(x, none, p.sc, cs)
-                               : all_small     ? score2<kCapSmall>(x, none, p.sc, cs)
-                                               : score2<kCapAny>(x, none, p.sc, cs);
+              const float2 y = p.sc.cap == 0.f ? score2<kNoCap>(x, p.sc, cs)
+                               : all_small     ? score2<kCapSmall>(x, p.sc, cs)
+                                               : score2<kCapAny>(x, p.sc, cs);
               sr[k] = __float_as_uint(y.x);
               sr[k + 1] = __float_as_uint(y.y);
             }

@@ -66,16 +66,16 @@ __device__ __forceinline__ float abs_max(const uint32_t* sr) {
   return m[0];
 }
 
-// Scores of two products x plus b (bias, minus the maximum or L).  kCapAny looks at
-// each score; kCapSmall is for warps whose scores are all small: the same bits.
+// Base-2 scores of two products x, less any bias.  kCapAny looks at each score;
+// kCapSmall is for warps whose scores are all small: the same bits.
 enum CapForm { kNoCap = 0, kCapSmall = 1, kCapAny = 2 };
 template <CapForm F>
-__device__ __forceinline__ float2 score2(float2 x, float2 b, const ScoreParams& sc, float2 c2) {
-  if constexpr (F == kNoCap) return __ffma2_rn(x, c2, b);
-  float2 y = __ffma2_rn(x, tanh_small(x, sc), b);
+__device__ __forceinline__ float2 score2(float2 x, const ScoreParams& sc, float2 c2) {
+  if constexpr (F == kNoCap) return __fmul2_rn(x, c2);
+  float2 y = __fmul2_rn(x, tanh_small(x, sc));
   if constexpr (F == kCapAny) {
-    const float2 u = __ffma2_rn(tanh_rest(x, sc.in2), make_float2(-2.f * sc.cap, -2.f * sc.cap),
-                                __fadd2_rn(b, make_float2(sc.cap, sc.cap)));
+    const float2 u =
+        __ffma2_rn(tanh_rest(x, sc.in2), make_float2(-2.f * sc.cap, -2.f * sc.cap), make_float2(sc.cap, sc.cap));
     y.x = fabsf(x.x) <= sc.small ? y.x : u.x;
     y.y = fabsf(x.y) <= sc.small ? y.y : u.y;
   }
@@ -120,22 +120,25 @@ struct PlainCols {
 // cap) all small:
 template <int N>
 __device__ __forceinline__ void scores_fast(uint32_t* sr, const ScoreParams& sc, float2 c2, float s) {
-  auto each = [&](auto form) {
+  // (The bias of a column takes its number as an immediate: one scalar FMA.  Packed, the
+  // pair of numbers is two moves on top.)
+  auto each = [&](auto form, bool biased) {
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
-      const float2 y = form(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
-                            __fmul2_rn(make_float2(s, s), make_float2(static_cast<float>(c), static_cast<float>(c + 1))));
+      float2 y = form(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])));
+      if (biased) y = make_float2(fmaf(s, static_cast<float>(c), y.x), fmaf(s, static_cast<float>(c + 1), y.y));
       sr[c] = __float_as_uint(y.x);
       sr[c + 1] = __float_as_uint(y.y);
     }
   };
-  if (sc.cap == 0.f) {
-    if (sc.slopes != nullptr) each([&](float2 x, float2 b) { return score2<kNoCap>(x, b, sc, c2); });
-    else each([&](float2 x, float2) { return __fmul2_rn(x, c2); });
-  } else if (sc.slopes != nullptr) {
-    each([&](float2 x, float2 b) { return score2<kCapSmall>(x, b, sc, c2); });
+  auto plain = [&](float2 x) { return score2<kNoCap>(x, sc, c2); };
+  auto capped = [&](float2 x) { return score2<kCapSmall>(x, sc, c2); };
+  if (sc.slopes == nullptr) {
+    if (sc.cap == 0.f) each(plain, false);
+    else each(capped, false);
   } else {
-    each([&](float2 x, float2) { return __fmul2_rn(x, tanh_small(x, sc)); });
+    if (sc.cap == 0.f) each(plain, true);
+    else each(capped, true);
   }
 }
 // And for any block: from TMEM (column t_s on) and back to it, 16 columns at a time in
@@ -151,18 +154,16 @@ __device__ __forceinline__ void scores_slow(uint32_t t_s, const ScoreParams& sc,
     ptx::tmem_ld16(t_s + k0, x16);
 #pragma unroll
     for (int c = 0; c < 16; c += 2) {
-      float2 b = make_float2(0.f, 0.f);
-      if (sc.slopes != nullptr) {
-        const int e0 = cols.off(k0 + c), e1 = cols.off(k0 + c + 1);
-        b = __fmul2_rn(make_float2(r.s, r.s), make_float2(static_cast<float>(e0), static_cast<float>(e1)));
-        if (r.both)
-          b = make_float2(-r.slope * fabsf(static_cast<float>(r.d0 + e0)),
-                          -r.slope * fabsf(static_cast<float>(r.d0 + e1)));
-        if (Cols::kOff && r.d0 + e0 > 0) b.x = fmaf(-r.slope, static_cast<float>(e0), -2.f * r.fixed);
-        if (Cols::kOff && r.d0 + e1 > 0) b.y = fmaf(-r.slope, static_cast<float>(e1), -2.f * r.fixed);
-      }
       const float2 x = make_float2(__uint_as_float(x16[c]), __uint_as_float(x16[c + 1]));
-      const float2 y = sc.cap != 0.f ? score2<kCapAny>(x, b, sc, c2) : score2<kNoCap>(x, b, sc, c2);
+      float2 y = sc.cap != 0.f ? score2<kCapAny>(x, sc, c2) : score2<kNoCap>(x, sc, c2);
+      if (sc.slopes != nullptr) {
+        auto biased = [&](float v, int e) {
+          if (r.both) return fmaf(-r.slope, fabsf(static_cast<float>(r.d0 + e)), v);
+          if (Cols::kOff && r.d0 + e > 0) return fmaf(-r.slope, static_cast<float>(e), v) - 2.f * r.fixed;
+          return fmaf(r.s, static_cast<float>(e), v);
+        };
+        y = make_float2(biased(y.x, cols.off(k0 + c)), biased(y.y, cols.off(k0 + c + 1)));
+      }
       x16[c] = __float_as_uint(y.x);
       x16[c + 1] = __float_as_uint(y.y);
     }
@@ -195,6 +196,34 @@ __device__ __forceinline__ void block_scores(uint32_t* sr, uint32_t t_s, const S
         sr[c0 + c] = seen >> c & 1u ? sr[c0 + c] : __float_as_uint(-INFINITY);
     }
   }
+}
+
+// The order in which a forward CTA takes its key blocks [lo, ..).  A bias makes the
+// keys next to a row its largest scores: from there outwards the running maximum
+// hardly moves, while towards them it moves, and O is rescaled, at every block (causal
+// B4 H16 S4096 D64: 219 us upwards).  So with a bias the blocks up to `split` come
+// first, downwards, then those behind, upwards; else all upwards (split = lo).
+struct BlockOrder {
+  int lo, split;
+  __device__ __forceinline__ int at(int x) const { return x < split - lo ? split - 1 - x : lo + x; }
+  __device__ __forceinline__ int index(int blk) const { return blk < split ? split - 1 - blk : blk - lo; }
+  // The blocks [a, b) are the loaded ones [*beg, *end): those of a tile lie together
+  // because either b <= split, or split = lo, or a = lo.
+  __device__ __forceinline__ void span(int a, int b, int* beg, int* end) const {
+    if (b <= split) {
+      *beg = split - b;
+      *end = split - a;
+    } else {
+      *beg = split > lo ? 0 : a - lo;
+      *end = b - lo;
+    }
+  }
+};
+// Of blocks [lo, hi); `diag`: the block after that of the CTA's last row; `open`: the
+// window has no left side, so every tile starts at lo.
+__device__ __forceinline__ BlockOrder block_order(const ScoreParams& sc, int lo, int hi, bool open, int diag) {
+  if (sc.slopes == nullptr) return BlockOrder{lo, lo};
+  return BlockOrder{lo, open ? max(lo, min(hi, diag)) : hi};
 }
 
 // Visible keys of a sample's rows under a prefix: its clamped length (0: none).
