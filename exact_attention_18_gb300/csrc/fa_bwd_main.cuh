@@ -215,15 +215,13 @@ struct ScoreBlock {
   int wl, pfx;   // dK/dV pass
 };
 
-// grad_block (dQ pass) with modified scores.  FAST: blocks that no mask cuts, on one
-// side of their queries, all of whose scores are small; the rest in a rolled loop
-// with the same arithmetic (their code is to be short, as in the forward).
+// grad_block (dQ pass) with modified scores: 16 columns whose products xs, ys are in
+// registers.  FAST: blocks that no mask cuts, on one side of their queries, whose
+// scores are all small (F = kCapSmall); the others have the same arithmetic.
 template <bool BF16, bool FAST, CapForm F, bool BIAS>
-__device__ __forceinline__ void grad_half_scored(uint32_t tX, uint32_t tY, int h, const ScoreParams& sc, float2 c2,
-                                                 float my_l2, float my_delta, const ScoreBlock& sb) {
-  uint32_t xs[16], ys[16];
-  tmem_ld16x2(tX + 16 * h, xs, tY + 16 * h, ys);
-  uint32_t dk[8];
+__device__ __forceinline__ void grad16_scored(const uint32_t* xs, const uint32_t* ys, uint32_t* dk, int h,
+                                              const ScoreParams& sc, float2 c2, float my_l2, float my_delta,
+                                              const ScoreBlock& sb) {
   // Column cc's bias is s cc + s d0; the latter joins -L.
   const float s = sb.side > 0 ? -sb.slope : sb.slope;
   const float nb = BIAS ? fmaf(s, static_cast<float>(sb.d0 + 16 * h), -my_l2) : -my_l2;
@@ -249,7 +247,6 @@ __device__ __forceinline__ void grad_half_scored(uint32_t tX, uint32_t tY, int h
     if constexpr (F != kNoCap) ds = __fmul2_rn(ds, f);
     dk[c / 2] = pack2<BF16>(ds.x, ds.y);
   }
-  tmem_st8(tY + 8 * h, dk);
 }
 
 template <bool BF16>
@@ -258,26 +255,39 @@ __device__ __forceinline__ void grad_block_scored(uint32_t tX, uint32_t tY, cons
   const bool capped = sc.cap != 0.f, biased = sc.slopes != nullptr;
   bool fast = !sb.edge && (sb.side != 0 || !biased);
   if (fast && capped) {
+    // (a load of X of its own: decided half by half, beside the other form's code, the
+    // capped passes took 3 to 7 % longer)
     uint32_t xs[32];
     tmem_ld32(tX, xs);
     fast = all_small<32>(xs, sc);
   }
-  auto both = [&](auto half) {
-    half(0);
-    half(1);
+  auto half = [&](int h, auto form) {
+    uint32_t xs[16], ys[16], dk[8];
+    tmem_ld16x2(tX + 16 * h, xs, tY + 16 * h, ys);
+    form(xs, ys, dk, h);
+    tmem_st8(tY + 8 * h, dk);
+  };
+  auto any = [&](const uint32_t* xs, const uint32_t* ys, uint32_t* dk, int h) {
+    if (capped) grad16_scored<BF16, false, kCapAny, true>(xs, ys, dk, h, sc, c2, my_l2, my_delta, sb);
+    else grad16_scored<BF16, false, kNoCap, true>(xs, ys, dk, h, sc, c2, my_l2, my_delta, sb);
   };
   if (!fast) {
+    // (a rolled loop: the rare form's code is to be short, as in the forward)
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      if (capped) grad_half_scored<BF16, false, kCapAny, true>(tX, tY, h, sc, c2, my_l2, my_delta, sb);
-      else grad_half_scored<BF16, false, kNoCap, true>(tX, tY, h, sc, c2, my_l2, my_delta, sb);
-    }
+    for (int h = 0; h < 2; ++h) half(h, any);
   } else if (!capped) {
-    both([&](int h) { grad_half_scored<BF16, true, kNoCap, true>(tX, tY, h, sc, c2, my_l2, my_delta, sb); });
-  } else if (biased) {
-    both([&](int h) { grad_half_scored<BF16, true, kCapSmall, true>(tX, tY, h, sc, c2, my_l2, my_delta, sb); });
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      half(h, [&](const uint32_t* xs, const uint32_t* ys, uint32_t* dk, int hh) {
+        grad16_scored<BF16, true, kNoCap, true>(xs, ys, dk, hh, sc, c2, my_l2, my_delta, sb);
+      });
   } else {
-    both([&](int h) { grad_half_scored<BF16, true, kCapSmall, false>(tX, tY, h, sc, c2, my_l2, my_delta, sb); });
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      half(h, [&](const uint32_t* xs, const uint32_t* ys, uint32_t* dk, int hh) {
+        if (biased) grad16_scored<BF16, true, kCapSmall, true>(xs, ys, dk, hh, sc, c2, my_l2, my_delta, sb);
+        else grad16_scored<BF16, true, kCapSmall, false>(xs, ys, dk, hh, sc, c2, my_l2, my_delta, sb);
+      });
   }
 }
 
@@ -285,17 +295,11 @@ __device__ __forceinline__ void grad_block_scored(uint32_t tX, uint32_t tY, cons
 // d0 + its row sees (from its own mask) the partner queries hi + row .. lo + row of
 // columns, all up to the latter where its key lies before the prefix (pfx).
 template <bool BF16, bool FAST, CapForm F, bool BIAS>
-__device__ __forceinline__ void grad_half_kv_scored(uint32_t tX, uint32_t tY, int half, const float2* nl2,
-                                                    const float2* dl, const ScoreParams& sc, float2 c2,
-                                                    const ScoreBlock& sb) {
+__device__ __forceinline__ void grad16_kv_scored(const uint32_t* xs, const uint32_t* ys, uint32_t* pk, uint32_t* dk,
+                                                 int half, const float2* nl2, const float2* dl, const ScoreParams& sc,
+                                                 float2 c2, const ScoreBlock& sb) {
   const int lane = threadIdx.x & 31;
   const int u = lane & 3, r = lane >> 2;
-  const uint32_t lane_off = static_cast<uint32_t>(16 * half) << 16;
-  uint32_t xs[16], ys[16];
-  tmem_ld16x256b_x4(tX + lane_off, xs);
-  tmem_ld16x256b_x4(tY + lane_off, ys);
-  tmem_ld_wait();
-  uint32_t pk[8], dk[8];
   const float s = sb.side > 0 ? -sb.slope : sb.slope;
   // s (row - first column of the thread), of its two rows of this half
   float row[2] = {0.f, 0.f};
@@ -306,7 +310,8 @@ __device__ __forceinline__ void grad_half_kv_scored(uint32_t tX, uint32_t tY, in
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float2 nb = nl2[i];
-    if constexpr (BIAS) nb = make_float2(fmaf(s, -8.f * static_cast<float>(i), nb.x), fmaf(s, -8.f * static_cast<float>(i) - 1.f, nb.y));
+    if constexpr (BIAS)
+      nb = make_float2(fmaf(s, -8.f * static_cast<float>(i), nb.x), fmaf(s, -8.f * static_cast<float>(i) - 1.f, nb.y));
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int e = 4 * i + 2 * k;
@@ -333,8 +338,6 @@ __device__ __forceinline__ void grad_half_kv_scored(uint32_t tX, uint32_t tY, in
       dk[2 * i + k] = pack2<BF16>(ds.x, ds.y);
     }
   }
-  tmem_st16x128b_x4(tX + lane_off, pk);
-  tmem_st16x128b_x4(tY + lane_off, dk);
 }
 
 template <bool BF16>
@@ -357,22 +360,36 @@ __device__ __forceinline__ void grad_block_kv_scored(uint32_t tX, uint32_t tY, c
     tmem_ld32(tX, xs);
     fast = all_small<32>(xs, sc);
   }
-  auto both = [&](auto half) {
-    half(0);
-    half(1);
+  auto half = [&](int h, auto form) {
+    const uint32_t lane_off = static_cast<uint32_t>(16 * h) << 16;
+    uint32_t xs[16], ys[16], pk[8], dk[8];
+    tmem_ld16x256b_x4(tX + lane_off, xs);
+    tmem_ld16x256b_x4(tY + lane_off, ys);
+    tmem_ld_wait();
+    form(xs, ys, pk, dk, h);
+    tmem_st16x128b_x4(tX + lane_off, pk);
+    tmem_st16x128b_x4(tY + lane_off, dk);
+  };
+  auto any = [&](const uint32_t* xs, const uint32_t* ys, uint32_t* pk, uint32_t* dk, int h) {
+    if (capped) grad16_kv_scored<BF16, false, kCapAny, true>(xs, ys, pk, dk, h, nl2, dl, sc, c2, sb);
+    else grad16_kv_scored<BF16, false, kNoCap, true>(xs, ys, pk, dk, h, nl2, dl, sc, c2, sb);
   };
   if (!fast) {
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      if (capped) grad_half_kv_scored<BF16, false, kCapAny, true>(tX, tY, h, nl2, dl, sc, c2, sb);
-      else grad_half_kv_scored<BF16, false, kNoCap, true>(tX, tY, h, nl2, dl, sc, c2, sb);
-    }
+    for (int h = 0; h < 2; ++h) half(h, any);
   } else if (!capped) {
-    both([&](int h) { grad_half_kv_scored<BF16, true, kNoCap, true>(tX, tY, h, nl2, dl, sc, c2, sb); });
-  } else if (biased) {
-    both([&](int h) { grad_half_kv_scored<BF16, true, kCapSmall, true>(tX, tY, h, nl2, dl, sc, c2, sb); });
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      half(h, [&](const uint32_t* xs, const uint32_t* ys, uint32_t* pk, uint32_t* dk, int hh) {
+        grad16_kv_scored<BF16, true, kNoCap, true>(xs, ys, pk, dk, hh, nl2, dl, sc, c2, sb);
+      });
   } else {
-    both([&](int h) { grad_half_kv_scored<BF16, true, kCapSmall, false>(tX, tY, h, nl2, dl, sc, c2, sb); });
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      half(h, [&](const uint32_t* xs, const uint32_t* ys, uint32_t* pk, uint32_t* dk, int hh) {
+        if (biased) grad16_kv_scored<BF16, true, kCapSmall, true>(xs, ys, pk, dk, hh, nl2, dl, sc, c2, sb);
+        else grad16_kv_scored<BF16, true, kCapSmall, false>(xs, ys, pk, dk, hh, nl2, dl, sc, c2, sb);
+      });
   }
 }
 

@@ -90,7 +90,7 @@ struct PagedLayout {
   static constexpr int kOffSmall = kOffQ + 2 * kQBytes;
   // full[U], empty[U], qfull[2], qempty[2], sfull[2], pfull[2], pv[2], vtmp, drain
   static constexpr int kNumBars = 2 * kUnits + 10 + 2;
-  static_assert(kNumBars * 8 + 24 + sizeof(RunStart) + 10 * N * 4 + 2 * N <= kSmallBytes, "small arrays");
+  static_assert(kNumBars * 8 + 24 + sizeof(RunStart) + 11 * N * 4 + 2 * N + 16 <= kSmallBytes, "small arrays");
   // The request is padded so that no more CTAs than meant share an SM, nor one
   // of these with a kernel that takes the whole tensor memory (those ask for
   // 116 KB at least).
@@ -174,8 +174,11 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
   float* s_red = s_alpha + N;       // [N][4] per-warp partial of each row
   int* s_off = reinterpret_cast<int*>(s_red + 4 * N);     // [N] output row of row n after its unit's first
   short* s_tok = reinterpret_cast<short*>(s_off + N);     // [N] token of row n
-  int* s_pos = reinterpret_cast<int*>(s_tok + N);         // scored: [N] position of row n
-  float* s_slope = reinterpret_cast<float*>(s_pos + N);   // scored: [N] its head's slope, base 2
+  // Scored: position of row n, the same less the unit's first as a float, and its
+  // head's slope in base 2, [N] each (16-byte aligned).
+  int* s_pos = reinterpret_cast<int*>((reinterpret_cast<uintptr_t>(s_tok + N) + 15) & ~static_cast<uintptr_t>(15));
+  float* s_fpos = reinterpret_cast<float*>(s_pos + N);
+  float* s_slope = s_fpos + N;
 
   // Behind the tile kernel of the same call this grid's CTAs start as that
   // kernel's end, and work beside the last of them once they have its word that
@@ -265,7 +268,9 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
       return p.num_pages;
     };
     for (int n; ok && (n = w.seg_len()) > 0; w.next(p, n), ++seg) {
-      int page = box_page(w.blk);
+      // Block of the unit that the segment's j-th is.
+      auto blk_at = [&](int j) { return w.blk + (downwards(p) ? n - 1 - j : j); };
+      int page = box_page(blk_at(0));
       if (kv == 0) {
         const int qb = seg & 1, qu = seg >> 1;
         if (qu > 0) ok = warp_wait(&bar_qempty[qb], (qu - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
@@ -280,8 +285,8 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
         __syncwarp();
       }
       for (int j = 0; ok && j < n; ++j) {
-        const int page_next = j + 1 < n ? box_page(w.blk + j + 1) : 0;
-        const int key0 = (w.u.lo / kPBlk + w.blk + j) * kPBlk;
+        const int page_next = j + 1 < n ? box_page(blk_at(j + 1)) : 0;
+        const int key0 = (w.u.lo / kPBlk + blk_at(j)) * kPBlk;
         const int row = (key0 + lane * frag) & ((1 << p.page_shift) - 1);
         const bool cut = key0 < w.u.lo || key0 + kPBlk > w.u.hi;
         const int st = c % U, use = c / U;
@@ -398,6 +403,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     const short* tok_s = s_tok + g * NC;
     const int* off_s = s_off + g * NC;
     const int* pos_s = s_pos + g * NC;
+    const float* fpos_s = s_fpos + g * NC;
     const float* slope_s = s_slope + g * NC;
     const float c = kScored ? 1.f : p.scale_log2;  // (modified scores are scaled)
     const float2 c2 = make_float2(c, c);
@@ -426,6 +432,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
           int pos = u.pos0 + tok_s[wt];
           if (tree && row < n_rows) pos = min(u.kv_len - 1, max(u.pos0, p.positions[u.tok0 + tok_s[wt]]));
           s_pos[row] = pos;
+          s_fpos[row] = static_cast<float>(pos - u.pos0);
           s_slope[row] = p.sc.slopes != nullptr ? p.sc.slopes[w.kvh * p.G + row % p.G] * 1.4426950408889634f : 0.f;
         }
         named_sync(bar_id, 128);
@@ -440,14 +447,34 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
       // a row has seen no score above -inf take the block maximum.
       bool exact_max = true;
       for (int jb = 0; jb < n; ++jb, ++i) {
+        // Scored, new tokens of a tree: the key's position and who sees it (bit k: row k
+        // of the warpgroup), loaded while the block's products are made.
+        const int key0 = (blk_first + (downwards(p) ? n - 1 - jb : jb)) * kPBlk;
+        const int my_key = key0 + key_lane;
+        int my_pos = my_key;
+        unsigned seen = 0;
+        bool drafted = false;
+        if constexpr (kScored) {
+          if (tree && key0 + kPBlk > u.pos0) {
+            drafted = my_key >= u.pos0 && my_key < u.kv_len;
+            if (drafted) {
+              const int j = my_key - u.pos0;  // the new token
+              if (p.sc.slopes != nullptr)
+                my_pos = min(u.kv_len - 1, max(u.pos0, p.positions[u.tok0 + j]));
+              const unsigned* bits = p.tree + u.tok0 * p.tree_stride + (j >> 5);
+#pragma unroll
+              for (int k = 0; k < NC; ++k)
+                if (g * NC + k < n_rows) seen |= (bits[tok_s[k] * p.tree_stride] >> (j & 31) & 1u) << k;
+            }
+          }
+        }
         bool ok = warp_wait(&bar_sfull[i & 1], (i >> 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
         // O(i-2) is done (S(i) was issued after it).  Waiting for it keeps this
         // warp one phase behind each of the two barriers, so that a wait for
         // O(i-1) below cannot take the phase before it for it.
         if (ok && i >= 2)
           ok = warp_wait(&bar_pv[i & 1], ((i >> 1) - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
-        const int key0 = (blk_first + jb) * kPBlk;
-        const int key = key0 + key_lane;
+        const int key = my_key;
         const bool cut = key0 < full_lo || key0 + kPBlk > full_hi;
         uint32_t sr[NC];
         if (ok) {
@@ -459,7 +486,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
           if (ok) {
             // In place: the scores, scaled; the cap by its polynomial or exactly, each by itself.
             const float2 cs = make_float2(p.scale_log2, p.scale_log2);
-            const bool all_small = __all_sync(0xffffffffu, abs_max<NC>(sr) <= p.sc.small);
+            const bool all_small = p.sc.cap == 0.f || __all_sync(0xffffffffu, abs_max<NC>(sr) <= p.sc.small);
 #pragma unroll
             for (int k = 0; k < NC; k += 2) {
               const float2 x = make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
@@ -469,24 +496,25 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
               sr[k] = __float_as_uint(y.x);
               sr[k + 1] = __float_as_uint(y.y);
             }
-            const bool drafted = tree && key >= u.pos0 && key < u.kv_len;
             if (p.sc.slopes != nullptr) {
-              const int kp = drafted ? min(u.kv_len - 1, max(u.pos0, p.positions[u.tok0 + key - u.pos0])) : key;
+              const float fkey = static_cast<float>(my_pos - u.pos0);
 #pragma unroll
-              for (int k = 0; k < NC; ++k)
-                sr[k] = __float_as_uint(
-                    fmaf(-slope_s[k], fabsf(static_cast<float>(kp - pos_s[k])), __uint_as_float(sr[k])));
+              for (int k = 0; k < NC; k += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(fpos_s + k);
+                const float4 s = *reinterpret_cast<const float4*>(slope_s + k);
+                sr[k] = __float_as_uint(fmaf(-s.x, fabsf(fkey - f.x), __uint_as_float(sr[k])));
+                sr[k + 1] = __float_as_uint(fmaf(-s.y, fabsf(fkey - f.y), __uint_as_float(sr[k + 1])));
+                sr[k + 2] = __float_as_uint(fmaf(-s.z, fabsf(fkey - f.z), __uint_as_float(sr[k + 2])));
+                sr[k + 3] = __float_as_uint(fmaf(-s.w, fabsf(fkey - f.w), __uint_as_float(sr[k + 3])));
+              }
             }
             if (cut) {
-              const int j = key - u.pos0;  // new token of the key
 #pragma unroll
               for (int k = 0; k < NC; ++k) {
                 const int pos = pos_s[k];
                 bool hidden = key >= u.kv_len || key < pos - p.win_left;
                 if (!tree) hidden = hidden || key > pos + p.win_right;
-                else if (drafted)
-                  hidden = g * NC + k >= n_rows ||
-                           !(p.tree[(u.tok0 + tok_s[k]) * p.tree_stride + (j >> 5)] >> (j & 31) & 1u);
+                else if (drafted) hidden = !(seen >> k & 1u);
                 if (hidden) sr[k] = __float_as_uint(-INFINITY);
               }
             }

@@ -92,7 +92,7 @@ struct TileSpan {
   int row_tile, turn;  // this tile's; turn >= turns: it is idle
   int ta, n_tok;   // first token within the unit, tokens
   int pos0;        // cache position of its first token
-  int beg, end;    // its blocks: beg, beg + turns, .. end - 1
+  int beg, end;    // its blocks, in the order they are taken: beg, beg + turns, .. end - 1
 };
 
 template <int SHIFT, int TILES, typename P>
@@ -115,8 +115,13 @@ __device__ __forceinline__ TileSpan tile_span(const P& p, const SegWalk<SHIFT, t
   }
   if (hi <= lo) return s;
   const int base = (w.u.lo >> SHIFT) + w.blk;  // the segment's first block
-  const int beg = min(n, max(0, (lo >> SHIFT) - base));
-  const int end = min(n, max(0, ((hi + (1 << SHIFT) - 1) >> SHIFT) - base));
+  int beg = min(n, max(0, (lo >> SHIFT) - base));
+  int end = min(n, max(0, ((hi + (1 << SHIFT) - 1) >> SHIFT) - base));
+  if (downwards(p)) {
+    const int b = beg;
+    beg = n - end;
+    end = n - b;
+  }
   s.beg = beg + ((s.turn - beg) & (s.turns - 1));
   s.end = end - ((end - 1 - s.turn) & (s.turns - 1));
   if (s.end <= s.beg) s.beg = s.end = 0;
@@ -284,7 +289,9 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         return p.num_pages;
       };
       for (int n; ok && (n = w.seg_len()) > 0; w.next(p, n), ++seg) {
-        int page = box_page(w.blk);
+        // Block of the unit that the segment's j-th is.
+        auto blk_at = [&](int j) { return w.blk + (downwards(p) ? n - 1 - j : j); };
+        int page = box_page(blk_at(0));
         if (kv == 0) {
           const int qb = seg % L::kQBufs, qu = seg / L::kQBufs;
           if (qu > 0) ok = warp_wait(&bar_qempty[qb], (qu - 1) & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutLoad);
@@ -301,8 +308,8 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           __syncwarp();
         }
         for (int j = 0; ok && j < n; ++j) {
-          const int page_next = j + 1 < n ? box_page(w.blk + j + 1) : 0;
-          const int key0 = ((w.u.lo >> L::kShift) + w.blk + j) * BN;
+          const int page_next = j + 1 < n ? box_page(blk_at(j + 1)) : 0;
+          const int key0 = ((w.u.lo >> L::kShift) + blk_at(j)) * BN;
           const int row = (key0 + lane * frag) & ((1 << p.page_shift) - 1);
           const bool clear = kv == 1 && (key0 < w.u.lo || key0 + BN > w.u.hi);
           if (pass > 0) {
@@ -499,11 +506,12 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         uint32_t sr[BN];
         if constexpr (BN == 128) tmem_ld128(t_s, sr);
         else tmem_ld64(t_s, sr);
-        const int lim = lim0 - j * BN, lo = lo0 - j * BN;  // columns lo <= c <= lim are visible to this row
-        const bool cut = j < j_lo || j >= j_hi;  // a mask cuts the block
+        const int jb = downwards(p) ? n - 1 - j : j;  // block of the segment
+        const int lim = lim0 - jb * BN, lo = lo0 - jb * BN;  // columns lo <= c <= lim are visible to this row
+        const bool cut = jb < j_lo || jb >= j_hi;  // a mask cuts the block
         float fixed = 0.f;  // scored: what the row's scores in this block have in common
         if constexpr (kScored) {
-          const int key0 = key_base + j * BN;
+          const int key0 = key_base + jb * BN;
           const RowBias bias = row_bias(slope, key0 - pos, tree || p.win_right == 0 || key0 + BN - 1 <= tile_pos0,
                                         key0 >= tile_pos0 + tile_rows - 1);
           fixed = bias.fixed;

@@ -85,6 +85,15 @@ struct RunStart {
   Unit u;
 };
 
+// A segment's blocks run from the last to the first under a bias: it makes the keys
+// next to a row its largest scores, and upwards every block would move the maximum
+// and rescale O (32 sequences of 5000 keys, D = 128: 68 us upwards).
+template <typename P>
+__device__ __forceinline__ bool downwards(const P& p) {
+  if constexpr (P::kScored) return p.sc.slopes != nullptr;
+  else return false;
+}
+
 // Walks the segments (runs of blocks of one unit) of a CTA's run of blocks.
 template <int SHIFT, bool COSTS>
 struct SegWalk {
