@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the attention computation runs in
 the library's CUDA kernels.  PyTorch supplies device memory and streams.  The
 wrappers of the rotary and cache calls, made once per layer and token when
-decoding, marshal in a compiled module (``csrc/fa_binding.cpp``).
+decoding, and of the calls with modified scores marshal in a compiled module
+(``csrc/fa_binding.cpp``).
 
 The raw entry points keep the C names and signatures (pointers as ints):
 ``fa_fwd``, ``fa_fwd_gqa``, ``fa_bwd``, ``fa_bwd_marked``, ``fa_bwd_gqa``,
@@ -454,27 +455,30 @@ def _kv_heads(q, k, v):
     return hk
 
 
-def _scores(q, heads, batch, softcap, slopes, prefix, others):
-    """The Scores of a call, or None where nothing modifies them; checks their tensors and the call's."""
-    import torch
-    if softcap is None and slopes is None and prefix is None:
-        return None
-    for t, n, dt, name in ((slopes, heads, torch.float32, "slopes"), (prefix, batch, torch.int32, "prefix")):
-        if t is not None and (t.dtype != dt or t.shape != (n,) or not t.is_contiguous() or not t.is_cuda):
-            raise ValueError(f"{name} must be a contiguous {dt} CUDA tensor of {n} entries")
-    if softcap is not None and not softcap > 0:
-        raise ValueError("softcap must be positive (None: no cap)")
-    if q.get_device() != torch.cuda.current_device() or any(
-            t is not None and t.get_device() != q.get_device() for t in (slopes, prefix, *others)):
-        raise ValueError("all tensors must be on the current CUDA device")
-    return Scores(0.0 if softcap is None else softcap, None if slopes is None else slopes.data_ptr(),
-                  None if prefix is None else prefix.data_ptr())
+def _attend(q, k, v, cu_seqlens, max_seqlen, causal, window, softcap, slopes, prefix, scale, out, lse, stream):
+    """The compiled form of a forward with modified scores (checks, outputs and marshalling)."""
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            return _attend(q, k, v, cu_seqlens, max_seqlen, causal, window, softcap, slopes, prefix, scale, out, lse, None)
+    left, right = (-1, -1) if window is None else window
+    return _result((_binding or _load_binding()).attend(q, k, v, cu_seqlens, max_seqlen, causal, left, right, softcap,
+                                                        slopes, prefix, scale, out, lse),
+                   "fa_fwd_scores" if cu_seqlens is None else "fa_fwd_scores_varlen")
 
 
-def _like(t, shape, dtype, name):
-    """An output or statistic given by the caller: contiguous, of this shape and dtype."""
-    if t is not None and (t.dtype != dtype or t.numel() != math.prod(shape) or not t.is_contiguous() or not t.is_cuda):
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)}")
+def _attend_backward(q, k, v, o, do, lse, cu_seqlens, max_seqlen, causal, window, softcap, slopes, prefix, scale, dq, dk,
+                     dv, workspace, stream):
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            return _attend_backward(q, k, v, o, do, lse, cu_seqlens, max_seqlen, causal, window, softcap, slopes, prefix,
+                                    scale, dq, dk, dv, workspace, None)
+    left, right = (-1, -1) if window is None else window
+    return _result((_binding or _load_binding()).attend_backward(q, k, v, o, do, lse, cu_seqlens, max_seqlen, causal, left,
+                                                                 right, softcap, slopes, prefix, scale, dq, dk, dv,
+                                                                 workspace),
+                   "fa_bwd_scores" if cu_seqlens is None else "fa_bwd_scores_varlen")
 
 
 def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None, lse=None, stream=None,
@@ -491,6 +495,8 @@ def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None,
     [B] makes keys j < prefix[b] visible to every row (as far as the window's
     left side allows).  ``backward`` takes the same.
     """
+    if softcap is not None or slopes is not None or prefix is not None:
+        return _attend(q, k, v, None, 0, causal, window, softcap, slopes, prefix, scale, out, lse, stream)
     import torch
     squeeze = q.dim() == 3
     q, k, v = _bhsd(q, "q"), _bhsd(k, "k"), _bhsd(v, "v")
@@ -498,18 +504,9 @@ def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None,
     hk = _kv_heads(q, k, v)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    scores = _scores(q, H, B, softcap, slopes, prefix, (k, v, out, lse))
-    if scores is not None:
-        _like(out, q.shape, q.dtype, "out")
-        _like(lse, (B, H, S), torch.float32, "lse")
     o = torch.empty_like(q) if out is None else out.view(q.shape)
     l = torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse is None else lse.view(B, H, S)
-    if scores is not None:
-        left, right = (-1, -1) if window is None else window
-        _check(fa_fwd_scores(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(), B, H, hk, S, D,
-                             causal, left, right, ctypes.byref(scores), scale, _dtype_code(q), _stream_ptr(stream)),
-               "fa_fwd_scores")
-    elif window is not None:
+    if window is not None:
         _check(fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(), B, H, hk, S, D,
                              causal, window[0], window[1], scale, _dtype_code(q), _stream_ptr(stream)),
                "fa_fwd_window")
@@ -532,6 +529,9 @@ def backward(q, k, v, o, do, lse, causal: bool = False, scale: float | None = No
     K/V head's group of query heads.  ``softcap``, ``slopes`` and ``prefix`` as
     the forward had them; slopes are constants and get no gradient.
     """
+    if softcap is not None or slopes is not None or prefix is not None:
+        return _attend_backward(q, k, v, o, do, lse, None, 0, causal, window, softcap, slopes, prefix, scale, dq, dk, dv,
+                                workspace, stream)
     import torch
     squeeze = q.dim() == 3
     q, k, v, o, do = (_bhsd(x, n) for x, n in ((q, "q"), (k, "k"), (v, "v"), (o, "o"), (do, "do")))
@@ -541,11 +541,6 @@ def backward(q, k, v, o, do, lse, causal: bool = False, scale: float | None = No
         raise ValueError("o and do must have q's shape")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    scores = _scores(q, H, B, softcap, slopes, prefix, (k, v, o, do, lse, dq, dk, dv, workspace))
-    if scores is not None:
-        for t, like, name in ((o, q, "o"), (do, q, "do"), (dq, q, "dq"), (dk, k, "dk"), (dv, k, "dv")):
-            _like(t, like.shape, q.dtype, name)
-        _like(lse, (B, H, S), torch.float32, "lse")
     lse = lse.reshape(B, H, S)
     dq = torch.empty_like(q) if dq is None else dq.view(q.shape)
     dk = torch.empty_like(k) if dk is None else dk.view(k.shape)
@@ -556,11 +551,7 @@ def backward(q, k, v, o, do, lse, causal: bool = False, scale: float | None = No
     args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr())
     ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_ptr(stream))
-    if scores is not None:
-        left, right = (-1, -1) if window is None else window
-        _check(fa_bwd_scores(*args, B, H, hk, S, D, causal, left, right, ctypes.byref(scores), scale, _dtype_code(q),
-                             *ws), "fa_bwd_scores")
-    elif window is not None:
+    if window is not None:
         _check(fa_bwd_window(*args, B, H, hk, S, D, causal, window[0], window[1], scale, _dtype_code(q), *ws),
                "fa_bwd_window")
     elif hk == H:
@@ -598,6 +589,8 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, s
     ``fa_check_device_errors``.  ``window``, ``softcap``, ``slopes`` [H] and
     ``prefix`` [batch] as in ``forward``, within each sample.
     """
+    if window is not None or softcap is not None or slopes is not None or prefix is not None:
+        return _attend(q, k, v, cu_seqlens, max_seqlen, causal, window, softcap, slopes, prefix, scale, out, lse, stream)
     import torch
     q = _packed(q, "q")
     T, H, D = q.shape
@@ -609,19 +602,8 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, s
     batch = _cu(cu_seqlens, T)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    scores = _scores(q, H, batch, softcap, slopes, prefix, (k, v, out, lse, cu_seqlens))
-    if scores is not None or window is not None:
-        _like(out, q.shape, q.dtype, "out")
-        _like(lse, (H, T), torch.float32, "lse")
     o = torch.empty_like(q) if out is None else out
     l = torch.empty((H, T), dtype=torch.float32, device=q.device) if lse is None else lse
-    if scores is not None or window is not None:
-        left, right = (-1, -1) if window is None else window
-        _check(fa_fwd_scores_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(),
-                                    cu_seqlens.data_ptr(), batch, int(max_seqlen), T, H, hk, D, causal, left, right,
-                                    None if scores is None else ctypes.byref(scores), scale, _dtype_code(q),
-                                    _stream_ptr(stream)), "fa_fwd_scores_varlen")
-        return o, l
     _check(fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(), cu_seqlens.data_ptr(),
                          batch, int(max_seqlen), T, H, hk, D, causal, scale, _dtype_code(q), _stream_ptr(stream)),
            "fa_fwd_varlen")
@@ -635,6 +617,9 @@ def backward_varlen(q, k, v, o, do, lse, cu_seqlens, max_seqlen: int, causal: bo
 
     ``window``, ``softcap``, ``slopes`` and ``prefix`` as the forward had them.
     """
+    if window is not None or softcap is not None or slopes is not None or prefix is not None:
+        return _attend_backward(q, k, v, o, do, lse, cu_seqlens, max_seqlen, causal, window, softcap, slopes, prefix,
+                                scale, None, None, None, workspace, stream)
     import torch
     q, o, do = _packed(q, "q"), _packed(o, "o"), _packed(do, "do")
     T, H, D = q.shape
@@ -645,24 +630,10 @@ def backward_varlen(q, k, v, o, do, lse, cu_seqlens, max_seqlen: int, causal: bo
     batch = _cu(cu_seqlens, T)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    scores = _scores(q, H, batch, softcap, slopes, prefix, (k, v, o, do, lse, cu_seqlens, workspace))
-    if scores is not None or window is not None:
-        for t, like, name in ((o, q, "o"), (do, q, "do"), (k, k, "k"), (v, k, "v")):
-            _like(t, like.shape, q.dtype, name)
-        _like(lse, (H, T), torch.float32, "lse")
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
     need = fa_bwd_varlen_workspace_size(batch, int(max_seqlen), T, H, hk, D)
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    if scores is not None or window is not None:
-        left, right = (-1, -1) if window is None else window
-        _check(fa_bwd_scores_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
-                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                    cu_seqlens.data_ptr(), batch, int(max_seqlen), T, H, hk, D, causal, left, right,
-                                    None if scores is None else ctypes.byref(scores), scale, _dtype_code(q),
-                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                    _stream_ptr(stream)), "fa_bwd_scores_varlen")
-        return dq, dk, dv
     _check(fa_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
                          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_seqlens.data_ptr(), batch, int(max_seqlen),
                          T, H, hk, D, causal, scale, _dtype_code(q), workspace.data_ptr(),

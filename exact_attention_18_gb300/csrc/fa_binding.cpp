@@ -1,6 +1,7 @@
-// Native marshalling of the cache operators' tensor wrappers.
+// Native marshalling of the tensor wrappers of the cache operators and of attention
+// with modified scores.
 //
-// A decoding step makes these calls once per layer on a few rows, where the
+// A decoding step makes the former calls once per layer on a few rows, where the
 // kernels take 3 to 10 us; checking tensors and building arguments in Python
 // took 20 to 30.  Here the same checks read the tensors directly, outputs come
 // from the framework's allocator, and the library is called through its C ABI
@@ -26,6 +27,7 @@
 #include <stdexcept>
 #include <string>
 #include <utility>
+#include <vector>
 
 #include "../../include/fa.h"
 
@@ -377,6 +379,154 @@ PyObject* forward_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   });
 }
 
+// Whole sequences with modified scores: [B, heads, S, D] (or [B, S, D], one head), or
+// packed [T, heads, D] with offsets.
+struct Whole {
+  bool packed, squeezed;
+  int64_t B, H, hk, S, D, T;  // packed: B sequences of up to S of the T tokens
+  at::ScalarType type;
+  fa_dtype code;
+  const int32_t* cu = nullptr;
+  std::vector<int64_t> q_shape, kv_shape, lse_shape;
+  Whole(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor* offs, int64_t max_seqlen, const OneDevice& dev)
+      : packed(offs != nullptr), type(q.scalar_type()), code(dtype_code(q)) {
+    squeezed = !packed && q.dim() == 3;
+    const int64_t dims = packed || squeezed ? 3 : 4;
+    require(q.dim() == dims && k.dim() == dims,
+            packed ? "q and k must be [T, heads, D]" : "q and k must be [B, heads, S, D] (or both [B, S, D])");
+    if (packed) {
+      T = q.size(0), H = q.size(1), D = q.size(2), hk = k.size(1);
+      B = offsets(*offs);
+      S = max_seqlen;
+      dev.also(*offs);
+      cu = static_cast<const int32_t*>(offs->const_data_ptr());
+      q_shape = {T, H, D}, kv_shape = {T, hk, D}, lse_shape = {H, T};
+    } else if (squeezed) {
+      B = q.size(0), S = q.size(1), D = q.size(2), H = hk = 1, T = 0;
+      q_shape = kv_shape = {B, S, D}, lse_shape = {B, S};
+    } else {
+      B = q.size(0), H = q.size(1), S = q.size(2), D = q.size(3), hk = k.size(1), T = 0;
+      q_shape = {B, H, S, D}, kv_shape = {B, hk, S, D}, lse_shape = {B, H, S};
+    }
+    require((hk >= 1 && H % hk == 0) || (H == 0 && hk == 0), "q's heads must be a multiple of k's and v's");
+    like(q, q_shape, type, "q", dev);
+    like(k, kv_shape, type, "k", dev);
+    like(v, kv_shape, type, "v", dev);
+  }
+  static void like(const Tensor& x, at::IntArrayRef shape, at::ScalarType t, const char* name, const OneDevice& dev) {
+    dev.also(x);
+    if (x.sizes() != shape || x.scalar_type() != t || !x.is_contiguous())
+      throw BadValue(std::string(name) + " must be a contiguous tensor of the call's shape and dtype");
+  }
+  static Tensor given(const Tensor* x, at::IntArrayRef shape, at::ScalarType t, const char* name, const Tensor& q,
+                      const OneDevice& dev) {
+    if (!x) return empty(shape, t, q);
+    like(*x, shape, t, name, dev);
+    return *x;
+  }
+  fa_scores scores(const Args& a, int at, const OneDevice& dev) const {  // softcap, slopes, prefix
+    fa_scores s = {};
+    if (a.v[at] != Py_None) {
+      s.softcap = static_cast<float>(a.real(at));
+      require(s.softcap > 0, "softcap must be positive (None: no cap)");
+    }
+    const Tensor *slopes = a.maybe(at + 1, "slopes"), *prefix = a.maybe(at + 2, "prefix");
+    dev.also(slopes);
+    dev.also(prefix);
+    if (slopes) s.slopes = static_cast<const float*>(floats(*slopes, H, "slopes"));
+    if (prefix) s.prefix = static_cast<const int32_t*>(ints(*prefix, at::kInt, B, "prefix"));
+    return s;
+  }
+  float scale(const Args& a, int at) const {
+    return a.v[at] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)))
+                              : static_cast<float>(a.real(at));
+  }
+};
+
+// attend(q, k, v, cu_seqlens, max_seqlen, causal, left, right, softcap, slopes, prefix, scale, out, lse)
+PyObject* attend(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    require(n == 14, "attend: fourteen arguments");
+    const Args a{argv, n};
+    const Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k"), &v = a.tensor(2, "v");
+    const OneDevice dev(q);
+    const Tensor* cu = a.maybe(3, "cu_seqlens");
+    const Whole w(q, k, v, cu, cu ? a.integer(4) : 0, dev);
+    const bool causal = a.flag(5);
+    const int64_t left = a.integer(6), right = a.integer(7);
+    const fa_scores scores = w.scores(a, 8, dev);
+    const float scale = w.scale(a, 11);
+    const Tensor out = Whole::given(a.maybe(12, "out"), w.q_shape, w.type, "out", q, dev);
+    const Tensor lse = Whole::given(a.maybe(13, "lse"), w.lse_shape, at::kFloat, "lse", q, dev);
+    void* stream = c10::cuda::getCurrentCUDAStream().stream();
+    const void *q_at = q.const_data_ptr(), *k_at = k.const_data_ptr(), *v_at = v.const_data_ptr();
+    void* o_at = out.mutable_data_ptr();
+    float* l_at = static_cast<float*>(lse.mutable_data_ptr());
+    fa_status st;
+    {
+      const Unlocked unlocked;
+      st = w.packed ? fa_fwd_scores_varlen(q_at, k_at, v_at, o_at, l_at, w.cu, w.B, w.S, w.T, w.H, w.hk, w.D, causal,
+                                           left, right, &scores, scale, w.code, stream)
+                    : fa_fwd_scores(q_at, k_at, v_at, o_at, l_at, w.B, w.H, w.hk, w.S, w.D, causal, left, right,
+                                    &scores, scale, w.code, stream);
+    }
+    return st == FA_OK ? pair(out, lse) : PyLong_FromLong(st);
+  });
+}
+
+// attend_backward(q, k, v, o, do, lse, cu_seqlens, max_seqlen, causal, left, right, softcap, slopes, prefix, scale,
+//                 dq, dk, dv, workspace)
+PyObject* attend_backward(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    require(n == 19, "attend_backward: nineteen arguments");
+    const Args a{argv, n};
+    const Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k"), &v = a.tensor(2, "v"), &o = a.tensor(3, "o"),
+                 &dout = a.tensor(4, "do"), &lse = a.tensor(5, "lse");
+    const OneDevice dev(q);
+    const Tensor* cu = a.maybe(6, "cu_seqlens");
+    const Whole w(q, k, v, cu, cu ? a.integer(7) : 0, dev);
+    Whole::like(o, w.q_shape, w.type, "o", dev);
+    Whole::like(dout, w.q_shape, w.type, "do", dev);
+    Whole::like(lse, w.lse_shape, at::kFloat, "lse", dev);
+    const bool causal = a.flag(8);
+    const int64_t left = a.integer(9), right = a.integer(10);
+    const fa_scores scores = w.scores(a, 11, dev);
+    const float scale = w.scale(a, 14);
+    const Tensor dq = Whole::given(a.maybe(15, "dq"), w.q_shape, w.type, "dq", q, dev);
+    const Tensor dk = Whole::given(a.maybe(16, "dk"), w.kv_shape, w.type, "dk", q, dev);
+    const Tensor dv = Whole::given(a.maybe(17, "dv"), w.kv_shape, w.type, "dv", q, dev);
+    const Tensor* ws = a.maybe(18, "workspace");
+    dev.also(ws);
+    require(!ws || ws->is_contiguous(), "workspace must be contiguous");
+    const size_t need = w.packed ? fa_bwd_varlen_workspace_size(w.B, w.S, w.T, w.H, w.hk, w.D)
+                                 : fa_bwd_gqa_workspace_size(w.B, w.H, w.hk, w.S, w.D);
+    const Tensor work = ws ? *ws : empty({std::max<int64_t>(static_cast<int64_t>(need), 256)}, at::kByte, q);
+    void* stream = c10::cuda::getCurrentCUDAStream().stream();
+    const void *q_at = q.const_data_ptr(), *k_at = k.const_data_ptr(), *v_at = v.const_data_ptr(),
+               *o_at = o.const_data_ptr(), *do_at = dout.const_data_ptr();
+    const float* l_at = static_cast<const float*>(lse.const_data_ptr());
+    void *dq_at = dq.mutable_data_ptr(), *dk_at = dk.mutable_data_ptr(), *dv_at = dv.mutable_data_ptr(),
+         *work_at = work.mutable_data_ptr();
+    const size_t work_bytes = work.nbytes();
+    fa_status st;
+    {
+      const Unlocked unlocked;
+      st = w.packed ? fa_bwd_scores_varlen(q_at, k_at, v_at, o_at, do_at, l_at, dq_at, dk_at, dv_at, w.cu, w.B, w.S,
+                                           w.T, w.H, w.hk, w.D, causal, left, right, &scores, scale, w.code, work_at,
+                                           work_bytes, stream)
+                    : fa_bwd_scores(q_at, k_at, v_at, o_at, do_at, l_at, dq_at, dk_at, dv_at, w.B, w.H, w.hk, w.S, w.D,
+                                    causal, left, right, &scores, scale, w.code, work_at, work_bytes, stream);
+    }
+    if (st != FA_OK) return PyLong_FromLong(st);
+    PyObject *x = THPVariable_Wrap(dq), *y = x ? THPVariable_Wrap(dk) : nullptr, *z = y ? THPVariable_Wrap(dv) : nullptr;
+    PyObject* t = z ? PyTuple_Pack(3, x, y, z) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    Py_XDECREF(z);
+    return t;
+  });
+}
+
 // paged_keep(k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_seqlen, path, path_lens)
 PyObject* paged_keep(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -414,6 +564,9 @@ PyMethodDef methods[] = {
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope)), METH_FASTCALL, nullptr},
     {"paged_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_append)), METH_FASTCALL, nullptr},
     {"forward_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(forward_paged)), METH_FASTCALL,
+     nullptr},
+    {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attend)), METH_FASTCALL, nullptr},
+    {"attend_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attend_backward)), METH_FASTCALL,
      nullptr},
     {"paged_keep", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_keep)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -274,3 +274,23 @@ def test_tensors_are_checked(fa):
             fa.forward(q, k, v, **kw)
     with pytest.raises(fa.FAError):
         fa.forward(q, k, v, softcap=math.inf)
+
+
+def test_three_dimensions_and_given_outputs(fa):
+    """[B, S, D] tensors are one head; outputs given by the caller are filled."""
+    q, k, v, do = (rnd((2, 1, 70, 64), i, torch.float16).cuda() for i in range(4))
+    kw = dict(causal=True, softcap=5.0, slopes=torch.tensor([0.25], device="cuda"))
+    o, lse = fa.forward(q, k, v, **kw)
+    grads = fa.backward(q, k, v, o, do, lse, **kw)
+    out, l3 = torch.empty_like(q[:, 0]), torch.empty(2, 70, device="cuda")
+    o3, lse3 = fa.forward(*(x[:, 0].contiguous() for x in (q, k, v)), out=out, lse=l3, **kw)
+    assert o3.data_ptr() == out.data_ptr() and torch.equal(o3, o[:, 0]) and torch.equal(lse3, lse[:, 0])
+    given = [torch.empty_like(out) for _ in range(3)]
+    g3 = fa.backward(*(x[:, 0].contiguous() for x in (q, k, v)), o3, do[:, 0].contiguous(), lse3, dq=given[0],
+                     dk=given[1], dv=given[2], workspace=torch.empty(1 << 16, dtype=torch.uint8, device="cuda"), **kw)
+    for a, b, g in zip(g3, grads, given):
+        assert a.data_ptr() == g.data_ptr() and torch.equal(a, b[:, 0])
+    with pytest.raises(fa.FAError):
+        fa.backward(q, k, v, o, do, lse, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"), **kw)
+    with pytest.raises(ValueError):
+        fa.backward(q, k, v, o, do.half().expand(2, 1, 70, 64)[:, :, ::2], lse, **kw)
