@@ -47,14 +47,20 @@ using namespace ptx;
 
 namespace {
 
-constexpr int kFwdThreads = 384;
+// Warps: the softmax warps, then the producer, two MMA issuers and one more.
 // Register split (per thread): the launch gives every thread kLaunchRegs; the
-// producer/MMA warpgroup drops to kRegsLow and both softmax warpgroups rise
-// to kRegsHigh; the shares may not exceed the launch total 384 * kLaunchRegs.
-constexpr int kLaunchRegs = 168;
-constexpr uint32_t kRegsHigh = 224;
-constexpr uint32_t kRegsLow = 56;
-static_assert(2 * 128 * kRegsHigh + 128 * kRegsLow <= kFwdThreads * kLaunchRegs, "register split");
+// last four warps drop to kRegsLow and the softmax warps rise to kRegsHigh; the
+// shares may not exceed the launch total.
+template <bool SCORED>
+struct FwdRoles {
+  static constexpr int kSoft = SCORED ? 16 : 8;
+  static constexpr int kProducer = kSoft, kMma0 = kSoft + 1;
+  static constexpr int kThreads = 32 * kSoft + 128;
+  static constexpr int kLaunchRegs = SCORED ? 96 : 168;
+  static constexpr uint32_t kRegsHigh = SCORED ? 104 : 224;
+  static constexpr uint32_t kRegsLow = SCORED ? 64 : 56;
+  static_assert(32 * kSoft * kRegsHigh + 128 * kRegsLow <= kThreads * kLaunchRegs, "register split");
+};
 // A block's P~ = exp2(c s - m) is accepted with a stale maximum m while the
 // block's sum stays <= 2^8 (so every P~ <= 2^8, far inside the 16-bit range).
 constexpr float kSumLimit = 256.0f;
@@ -122,11 +128,12 @@ __device__ __forceinline__ float exp_block(const uint32_t* sr, float2 c2, float 
 // batches and windows, as in the four-tile kernel; SCORED: modified scores and a
 // prefix, likewise.
 template <int D, bool BF16, bool GENERAL, bool SCORED>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(FwdRoles<SCORED>::kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const ScoredParams<FwdParams, SCORED> p) {
   static_assert(GENERAL || !SCORED, "modified scores take the general instantiation");
   using L = FwdLayout<D>;
+  using R = FwdRoles<SCORED>;
   using elem_t = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
 
   extern __shared__ uint8_t smem_raw[];
@@ -203,28 +210,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   };
   const int kb_cta = first_blk(row0);  // the CTA loads key blocks kb_cta, kb_cta + 1, ...
   // Tile t uses loaded blocks beg_t .. end_t - 1 (SCORED: of the order `ord`).
-  const int hi0 = blocks_for(row0), hi1 = blocks_for(row0 + kBlockM);
+  const int lo0 = first_blk(row0) - kb_cta, hi0 = blocks_for(row0) - kb_cta;
+  const int lo1 = first_blk(row0 + kBlockM) - kb_cta, hi1 = blocks_for(row0 + kBlockM) - kb_cta;
+  int beg0 = hi0 > lo0 ? lo0 : 0, end0 = hi0 > lo0 ? hi0 : 0;
+  int beg1 = hi1 > lo1 ? lo1 : 0, end1 = hi1 > lo1 ? hi1 : 0;
   BlockOrder ord{kb_cta, kb_cta};
-  if constexpr (SCORED)
-    ord = block_order(p.sc, kb_cta, max(hi0, hi1), wl == kNoWindow, (min(S, row0 + 2 * kBlockM) - 1) / kBlockN + 1);
+  if constexpr (SCORED) {
+    ord = block_order(true, kb_cta, kb_cta + max(end0, end1), wl == kNoWindow,
+                      (min(S, row0 + 2 * kBlockM) - 1) / kBlockN + 1);
+    ord.span(kb_cta + lo0, kb_cta + hi0, &beg0, &end0);
+    if (row0 + kBlockM < S) ord.span(kb_cta + lo1, kb_cta + hi1, &beg1, &end1);
+  }
   auto block_at = [&](int x) -> int {
     if constexpr (SCORED) return ord.at(x);
     else return kb_cta + x;
   };
-  auto span = [&](int lo, int hi, int* beg, int* end) {
-    *beg = 0;
-    *end = 0;
-    if (hi <= lo) return;
-    if constexpr (SCORED) {
-      ord.span(lo, hi, beg, end);
-    } else {
-      *beg = lo - kb_cta;
-      *end = hi - kb_cta;
-    }
-  };
-  int beg0, end0, beg1, end1;
-  span(first_blk(row0), hi0, &beg0, &end0);
-  span(first_blk(row0 + kBlockM), hi1, &beg1, &end1);
   const int nb0 = end0 - beg0;
   const int nb1 = end1 - beg1;
   const int nbp = max(end0, end1);  // blocks the CTA loads
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bar_sfull[t], 1);
-      mbar_init(&bar_sfree[t], 4);  // one arrival per softmax warp
-      mbar_init(&bar_pfull[t], 4);
+      mbar_init(&bar_sfree[t], 4);  // one arrival per softmax warp (separate-P layout)
+      mbar_init(&bar_pfull[t], R::kSoft / 2);  // one arrival per softmax warp of the tile
       mbar_init(&bar_pvdone[t], 1);
       mbar_init(&bar_ofinal[t], 1);
     }
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == R::kMma0) {
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
@@ -275,9 +275,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const uint32_t sK = smem_u32(smem + L::kOffK);
   const uint32_t sV = smem_u32(smem + L::kOffV);
 
-  if (warp >= 8) {
-    regs_decrease<kRegsLow>();
-    if (warp == 8) {
+  if (warp >= R::kSoft) {
+    regs_decrease<R::kRegsLow>();
+    if (warp == R::kProducer) {
       // ------------------------------------------------------------ producer
       if (lane == 0) {
         prefetch_tmap(&tm_q);
@@ -328,13 +328,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int x = (nv > L::kStagesV ? nv - L::kStagesV : 0); x < nv; ++x)
           drain_wait(&bar_vfull[x % L::kStagesV], (x / L::kStagesV) & 1, p.err);
       }
-    } else if (warp == 9 || warp == 10) {
+    } else if (warp == R::kMma0 || warp == R::kMma0 + 1) {
       // ------------------------------------------------------------ MMA issuers
-      // Warp 9 issues tile 0's MMAs, warp 10 tile 1's, so one warp's commits
+      // The first issues tile 0's MMAs, the second tile 1's, so one warp's commits
       // and barrier waits overlap the other's MMAs.  Each warp runs its code
       // converged and one elected lane issues each MMA; descriptors are built
       // once per stage and advanced by compile-time offsets.
-      const int t = warp - 9;
+      const int t = warp - R::kMma0;
       const int beg = t == 0 ? beg0 : beg1;  // this tile's loaded blocks beg .. nbt - 1
       const int nbt = t == 0 ? end0 : end1;
       constexpr uint32_t idesc_qk = make_idesc_f16(BF16, 128, kBlockN, false, false);
@@ -413,8 +413,132 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (lane == 0) mbar_arrive(&bar_vfull[st]);
       }
     }
+  } else if constexpr (SCORED) {
+    regs_increase<R::kRegsHigh>();
+    // ------------------------------------------------------------ softmax warps, modified scores
+    // Two threads a row, 64 keys of a block each: forming the scores lengthens the
+    // block's chain, and sixteen warps hide more of each other's latency than eight
+    // (causal B1 H32/4 S4096, a thread a row / two: capped 180 / 176 us, with a bias
+    // as well 184 / 169).  The two share the row's maximum: each puts its half's into a column of S it has loaded, and the pair
+    // of warps meets at a barrier of its own.
+    const int t = warp >> 3;           // tile
+    const int hf = (warp >> 2) & 1;    // half of the block's keys, and of O's columns
+    const int q4 = warp & 3;           // lane quarter
+    const int r = q4 * 32 + lane;      // row within the tile == TMEM lane
+    const int pair = 1 + t * 4 + q4;   // barrier of the two warps
+    constexpr int kHalf = kBlockN / 2;
+    const int tile_row0 = row0 + t * kBlockM;
+    const int row_g = tile_row0 + r;
+    const int nb = t == 0 ? nb0 : nb1;
+    const int x0 = t == 0 ? beg0 : beg1;  // the tile's first loaded block
+    const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + L::kColS + 128u * t;
+    const uint32_t t_mine = t_s + hf * kHalf;
+    const uint32_t t_p = t_s + hf * (kHalf / 2);
+    const uint32_t t_o = tmem + lane_base + L::kColO + D * t + hf * (D / 2);
+    const float2 c2 = make_float2(p.scale_log2, p.scale_log2), one = make_float2(1.f, 1.f);
+    const float slope =
+        p.sc.slopes != nullptr ? __ldg(p.sc.slopes + bh % p.heads) * 1.4426950408889634f : 0.f;
+    const int last = max(min(S - 1, row_g + wr), pfx - 1);  // last and first visible key of this row
+    const int first_key = row_g - wl;
+    float m = -INFINITY;  // running (possibly stale) maximum, base-2 scaled
+    float l = 0.f;        // this thread's share of the running sum
+    bool alive = true;
+    for (int j = 0; j < nb; ++j) {
+      bool ok = warp_wait(&bar_sfull[t], j & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
+      const int kv0 = block_at(x0 + j) * kBlockN + hf * kHalf;  // this half's first key
+      const int blk0 = kv0 - hf * kHalf;
+      const bool masked = blk0 + kBlockN > S || blk0 + kBlockN - 1 > max(tile_row0 + wr, pfx - 1) ||
+                          blk0 < tile_row0 + kBlockM - 1 - wl;
+      uint32_t sr[kHalf];
+      float fixed = 0.f, m_half = -INFINITY;
+      if (ok) {
+        tc_fence_after();
+        tmem_ld64(t_mine, sr);
+        const RowBias bias = row_bias(slope, kv0 - row_g, blk0 + kBlockN - 1 <= tile_row0 || (p.causal && pfx == 0),
+                                      blk0 >= tile_row0 + kBlockM - 1);
+        fixed = bias.fixed;
+        block_scores<kHalf>(sr, t_mine, p.sc, c2, bias, masked,
+                            PlainCols{masked ? first_key - kv0 : 0, masked ? last - kv0 : kHalf});
+        // The block's maximum ahead of its exponentials, as in the four-tile kernel.
+        m_half = block_max_scaled<kHalf>(sr, false, 0, kHalf, 1.f, false) + fixed;
+        // Column 63 (first half) or 64: read by the other half before P~ covers it.
+        tmem_st1(t_s + kHalf - 1 + hf, __float_as_uint(m_half));
+        tmem_st_wait();
+        tc_fence_before();
+      }
+      // (a warp whose wait ran out meets the other one all the same, and both leave)
+      if (!named_sync_and(pair, 64, ok)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      const float m_blk = fmaxf(m_half, __uint_as_float(tmem_ld1(t_s + kHalf - hf)));
+      float alpha = 1.f;
+      bool upd = false;
+      if (m_blk > m + kTau || (m == -INFINITY && m_blk > m)) {
+        alpha = ex2(m - m_blk);
+        m = m_blk;
+        upd = true;
+      }
+      const float base = fixed - (m == -INFINITY ? 0.f : m);
+      float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int k0 = 0; k0 < kHalf; k0 += 16) {
+        uint32_t pk[8];
+        exp16<BF16, false>(sr, k0, one, make_float2(base, base), 0, kHalf, acc, pk);
+        tmem_st8(t_p + k0 / 2, pk);
+      }
+      const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+      l = l * alpha + (a.x + a.y);
+      if (__any_sync(0xffffffffu, upd) && j > 0) {
+        // O holds the blocks before j relative to the old m: rescale this warp's share.
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 16) {
+          uint32_t o16[16];
+          tmem_ld16(t_o + c, o16);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float2 v = __fmul2_rn(make_float2(__uint_as_float(o16[i]), __uint_as_float(o16[i + 1])),
+                                        make_float2(alpha, alpha));
+            o16[i] = __float_as_uint(v.x);
+            o16[i + 1] = __float_as_uint(v.y);
+          }
+          tmem_st16(t_o + c, o16);
+        }
+      }
+      tmem_st_wait();
+      warp_arrive(&bar_pfull[t]);
+    }
+    // ------------------------------------------------------------ epilogue
+    if (alive && nb > 0) {
+      // The row's sum, through columns of S that neither P~ nor a score product uses now.
+      tmem_st1(t_s + kHalf + hf, __float_as_uint(l));
+      tmem_st_wait();
+      tc_fence_before();
+      named_sync(pair, 64);
+      tc_fence_after();
+      l += __uint_as_float(tmem_ld1(t_s + kHalf + 1 - hf));
+      if (warp_wait(&bar_ofinal[t], 0, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax)) {
+        tc_fence_after();
+        const float inv_l = 1.f / l;
+        const bool row_ok = row_g < S;
+        const int rr = row_ok ? row_g : 0;
+        const size_t o_row = packed ? static_cast<size_t>(tok0 + rr) * p.heads + q_head
+                                    : static_cast<size_t>(bh) * S + rr;
+        const size_t l_idx = packed ? static_cast<size_t>(q_head) * p.total + tok0 + rr : o_row;
+        elem_t* orow = reinterpret_cast<elem_t*>(p.o) + o_row * D + hf * (D / 2);
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 16) {
+          uint32_t o16[16];
+          tmem_ld16(t_o + c, o16);
+          if (row_ok) store_row16<BF16>(orow + c, o16, inv_l);
+        }
+        if (row_ok && hf == 0) p.lse[l_idx] = (m + log2f(l)) * 0.69314718055994530942f;
+      }
+    }
   } else {
-    regs_increase<kRegsHigh>();
+    regs_increase<R::kRegsHigh>();
     // ------------------------------------------------------------ softmax warpgroups
     const int t = warp >> 2;            // tile
     const int q4 = warp & 3;            // lane quarter (and SM sub-partition) of this warp
@@ -423,22 +547,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int row_g = tile_row0 + r;
     const int nb = t == 0 ? nb0 : nb1;
     const int nb_other = t == 0 ? nb1 : nb0;
-    const int x0 = t == 0 ? beg0 : beg1;  // the tile's first loaded block
+    const int kb0 = kb_cta + (t == 0 ? beg0 : beg1);  // the tile's first key block
     const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t t_s = tmem + lane_base + L::kColS + 128u * t;
     const uint32_t t_p = tmem + lane_base + L::kColP + L::kStrideP * t;
     const uint32_t t_o = tmem + lane_base + L::kColO + D * t;
-    const float sl2 = SCORED ? 1.f : p.scale_log2;  // (modified scores are scaled)
+    const float sl2 = p.scale_log2;
     const float2 c2 = make_float2(sl2, sl2);
-    const bool neg_scale = !SCORED && sl2 < 0.f;
-    float slope = 0.f;
-    if constexpr (SCORED) {
-      if (p.sc.slopes != nullptr) slope = __ldg(p.sc.slopes + bh % p.heads) * 1.4426950408889634f;
-    }
+    const bool neg_scale = sl2 < 0.f;
     // Last (and, general instantiation, first) visible key of this row.
-    const int last = SCORED    ? max(min(S - 1, row_g + wr), pfx - 1)
-                     : GENERAL ? min(S - 1, row_g + wr)
-                               : (p.causal ? min(S - 1, row_g) : S - 1);
+    const int last = GENERAL ? min(S - 1, row_g + wr) : (p.causal ? min(S - 1, row_g) : S - 1);
     const int first_key = row_g - wl;
     float m = -INFINITY;  // running (possibly stale) maximum, base-2 scaled
     float l = 0.f;
@@ -452,23 +570,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       tc_fence_after();
       tmem_ld128(t_s, sr);
       if (L::kSepP) warp_arrive(&bar_sfree[t]);  // S_t(j) is in registers: the MMA may overwrite it
-      const int kv0 = block_at(x0 + j) * kBlockN;
+      const int kv0 = (kb0 + j) * kBlockN;
       const int lim = last - kv0;      // columns c <= lim are visible to this row
       const int lo = first_key - kv0;  // and (general instantiation) c >= lo
       // Masked blocks: the diagonal block under the causal mask (an edge of
       // the window band), and a ragged last key block.
-      const bool masked = GENERAL ? (kv0 + kBlockN > S) || (kv0 + kBlockN - 1 > (SCORED ? max(tile_row0 + wr, pfx - 1) : tile_row0 + wr)) ||
+      const bool masked = GENERAL ? (kv0 + kBlockN > S) || (kv0 + kBlockN - 1 > tile_row0 + wr) ||
                                         (kv0 < tile_row0 + kBlockM - 1 - wl)
                                   : (kv0 + kBlockN > S) || (p.causal && kv0 + kBlockN - 1 > tile_row0);
-      float fixed = 0.f;  // SCORED: what the row's scores in this block have in common
-      if constexpr (SCORED) {
-        const RowBias bias = row_bias(slope, kv0 - row_g, kv0 + kBlockN - 1 <= tile_row0 || (p.causal && pfx == 0),
-                                      kv0 >= tile_row0 + kBlockM - 1);
-        fixed = bias.fixed;
-        block_scores<kBlockN>(sr, t_s, p.sc, make_float2(p.scale_log2, p.scale_log2), bias, masked,
-                              PlainCols{masked ? lo : 0, masked ? lim : kBlockN});
-      }
-      if (!SCORED && j == 0) m = block_max_scaled<kBlockN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
+      if (j == 0) m = block_max_scaled<kBlockN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
       // The two tiles' warps of one sub-partition take turns at the
       // exponentials, so one's loads, stores and waits overlap the other's.
       if (kTurns && (t == 0 ? j >= 1 && j - 1 < nb_other : j < nb_other) &&
@@ -479,43 +589,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       uint32_t pk[kBlockN / 2];
       float alpha = 1.f;
       bool upd = false;
-      float blk;
-      if constexpr (SCORED) {
-        // The block's maximum ahead of its exponentials, as in the four-tile kernel.
-        const float m_blk = block_max_scaled<kBlockN>(sr, false, 0, kBlockN, 1.f, false) + fixed;
-        if (m_blk > m + kTau || (m == -INFINITY && m_blk > m)) {
+      float blk = exp_block<BF16, GENERAL>(sr, c2, m, masked, lo, lim, pk);
+      // Every P~ <= 2^8 holds if the block's sum does.  Otherwise (or on NaN)
+      // this block's maximum is too far above the stale m: move m to it,
+      // rescale, and redo the block ("T5 讲解" §④ online update).  A window can
+      // hide every key of a row's first blocks: the first block that shows the
+      // row a key then sets m.
+      bool need = !(blk <= kSumLimit);
+      if constexpr (GENERAL) need = need || (m == -INFINITY && max(lo, 0) <= min(lim, kBlockN - 1));
+      if (__any_sync(0xffffffffu, need)) {
+        const float m_blk = block_max_scaled<kBlockN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
+        if (need && m_blk > m) {
           alpha = ex2(m - m_blk);
           m = m_blk;
           upd = true;
         }
-        const float nb = fixed - (m == -INFINITY ? 0.f : m);
-        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // (P~ goes straight over S in TMEM: its scores are in registers)
-#pragma unroll
-        for (int k0 = 0; k0 < kBlockN; k0 += 16) {
-          exp16<BF16, false>(sr, k0, c2, make_float2(nb, nb), 0, kBlockN, acc, pk + k0 / 2);
-          tmem_st8(t_p + k0 / 2, pk + k0 / 2);
-        }
-        const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-        blk = a.x + a.y;
-      } else {
-        blk = exp_block<BF16, GENERAL>(sr, c2, m, masked, lo, lim, pk);
-        // Every P~ <= 2^8 holds if the block's sum does.  Otherwise (or on NaN)
-        // this block's maximum is too far above the stale m: move m to it,
-        // rescale, and redo the block ("T5 讲解" §④ online update).  A window can
-        // hide every key of a row's first blocks: the first block that shows the
-        // row a key then sets m.
-        bool need = !(blk <= kSumLimit);
-        if constexpr (GENERAL) need = need || (m == -INFINITY && max(lo, 0) <= min(lim, kBlockN - 1));
-        if (__any_sync(0xffffffffu, need)) {
-          const float m_blk = block_max_scaled<kBlockN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
-          if (need && m_blk > m) {
-            alpha = ex2(m - m_blk);
-            m = m_blk;
-            upd = true;
-          }
-          if (__any_sync(0xffffffffu, upd)) blk = exp_block<BF16, GENERAL>(sr, c2, m, masked, lo, lim, pk);
-        }
+        if (__any_sync(0xffffffffu, upd)) blk = exp_block<BF16, GENERAL>(sr, c2, m, masked, lo, lim, pk);
       }
       if (kTurns && (t == 0 ? j < nb_other : j + 1 < nb_other)) {
         __syncwarp();
@@ -530,7 +619,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         break;
       }
       tc_fence_after();
-      if (__any_sync(0xffffffffu, upd) && (!SCORED || j > 0)) {
+      if (__any_sync(0xffffffffu, upd)) {
         // O holds the blocks before j relative to the old m: rescale this warp's rows.
 #pragma unroll
         for (int c = 0; c < D; c += 16) {
@@ -546,10 +635,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           tmem_st16(t_o + c, o16);
         }
       }
-      if constexpr (!SCORED) {
-        tmem_st32(t_p, pk);
-        tmem_st32(t_p + 32, pk + 32);
-      }
+      tmem_st32(t_p, pk);
+      tmem_st32(t_p + 32, pk + 32);
       tmem_st_wait();
       warp_arrive(&bar_pfull[t]);
     }
@@ -599,7 +686,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == R::kMma0) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
@@ -618,11 +705,11 @@ cudaError_t launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   cudaFuncAttributes attr;
   e = cudaFuncGetAttributes(&attr, kern);
   if (e != cudaSuccess) return e;
-  if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  if (attr.numRegs != FwdRoles<SCORED>::kLaunchRegs) return cudaErrorInvalidConfiguration;
   // Split-KV: one grid slice per key shard.
   const int shards = (GENERAL && p.kv_chunk > 0) ? (p.S + p.kv_chunk - 1) / p.kv_chunk : 1;
   dim3 grid(BH, p.n_m_tiles, shards);
-  kern<<<grid, kFwdThreads, L::kSmemBytes, stream>>>(tq, tk, tv, p);
+  kern<<<grid, FwdRoles<SCORED>::kThreads, L::kSmemBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }
 }  // namespace

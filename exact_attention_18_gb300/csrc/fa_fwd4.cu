@@ -197,22 +197,20 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   // (SCORED: in the order that `ord` gives; the x-th block loaded is block_at(x))
   BlockOrder ord{kb_cta, kb_cta};
   if constexpr (SCORED)
-    ord = block_order(p.sc, kb_cta, kb_cta + nbp, wl == kNoWindow, (min(S, row0 + kF4RowsPerCta) - 1) / kBN + 1);
+    ord = block_order(p.sc.slopes != nullptr, kb_cta, kb_cta + nbp, wl == kNoWindow, (min(S, row0 + kF4RowsPerCta) - 1) / kBN + 1);
   auto block_at = [&](int x) -> int {
     if constexpr (SCORED) return ord.at(x);
     else return kb_cta + x;
   };
   // Loaded blocks [*beg, *end) of the tile that starts at row r.
   auto span = [&](int r, int* beg, int* end) {
-    const int lo = first_blk(r), hi = blocks_for(r);
-    *beg = 0;
-    *end = 0;
-    if (hi <= lo) return;
     if constexpr (SCORED) {
-      ord.span(lo, hi, beg, end);
+      *beg = *end = 0;
+      if (r < S) ord.span(first_blk(r), blocks_for(r), beg, end);
     } else {
-      *beg = lo - kb_cta;
-      *end = hi - kb_cta;
+      const int lo = first_blk(r) - kb_cta, hi = blocks_for(r) - kb_cta;
+      *beg = hi > lo ? lo : 0;
+      *end = hi > lo ? hi : 0;
     }
   };
   // Rows of the last V block past a packed sample's end belong to the next sample
@@ -459,9 +457,9 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         if (lane == 0) mbar_arrive(&bar_vfull[st]);
       }
     }
-  } else {
+  } else if constexpr (SCORED) {
     regs_increase<kF4RegsHigh>();
-    // ------------------------------------------------------------ softmax warps
+    // ------------------------------------------------------------ softmax warps, modified scores
     const int t = warp >> 2;  // tile
     const int q4 = warp & 3;  // lane quarter
     const int r = q4 * 32 + lane;
@@ -473,17 +471,10 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t t_s = tmem + lane_base + 128u * t;  // S_t, and P_t over it
     const uint32_t t_o = t_s + L::kColO;
-    const float sl2 = SCORED ? 1.f : p.scale_log2;  // (modified scores are scaled)
-    const float2 c2 = make_float2(sl2, sl2);
-    const bool neg_scale = !SCORED && sl2 < 0.f;
-    float slope = 0.f;
-    if constexpr (SCORED) {
-      if (p.sc.slopes != nullptr) slope = __ldg(p.sc.slopes + bh % p.heads) * 1.4426950408889634f;
-    }
-    // Last (and, general instantiation, first) visible key of this row.
-    const int last = SCORED    ? max(min(S - 1, row_g + wr), pfx - 1)
-                     : GENERAL ? min(S - 1, row_g + wr)
-                               : (p.causal ? min(S - 1, row_g) : S - 1);
+    const float2 c2 = make_float2(p.scale_log2, p.scale_log2), one = make_float2(1.f, 1.f);
+    const float slope =
+        p.sc.slopes != nullptr ? __ldg(p.sc.slopes + bh % p.heads) * 1.4426950408889634f : 0.f;
+    const int last = max(min(S - 1, row_g + wr), pfx - 1);  // last and first visible key of this row
     const int first_key = row_g - wl;
     float m = -INFINITY;  // running (possibly stale) maximum, base-2 scaled
     float l = 0.f;
@@ -497,34 +488,123 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       uint32_t sr[kBN];
       tmem_ld64(t_s, sr);
       const int kv0 = block_at(x0 + j) * kBN;
+      // Blocks that cross an edge of the rows' bands, and a ragged last key block.
+      const bool masked = kv0 + kBN > S || kv0 + kBN - 1 > max(tile_row0 + wr, pfx - 1) ||
+                          kv0 < tile_row0 + kBlockM - 1 - wl;
+      const RowBias bias = row_bias(slope, kv0 - row_g, kv0 + kBN - 1 <= tile_row0 || (p.causal && pfx == 0),
+                                    kv0 >= tile_row0 + kBlockM - 1);
+      block_scores<kBN>(sr, t_s, p.sc, c2, bias, masked,
+                        PlainCols{masked ? first_key - kv0 : 0, masked ? last - kv0 : kBN});
+      // The block's maximum ahead of its exponentials: m moves where it is exceeded by
+      // more than 2^8.  The plain scores' way (exponentials first, and again where
+      // their sum tells) has two copies of them, which with the scores' own code is
+      // more than the instruction caches like: causal B1 H32/4 S4096 D128, capped 225
+      // us for 180; chunks of 64 tokens over 5000 keys with a bias 130 for 108.
+      const float m_blk = block_max_scaled<kBN>(sr, false, 0, kBN, 1.f, false) + bias.fixed;
+      float alpha = 1.f;
+      bool upd = false;
+      if (m_blk > m + kF4Tau || (m == -INFINITY && m_blk > m)) {
+        alpha = ex2(m - m_blk);
+        m = m_blk;
+        upd = true;
+      }
+      const float base = bias.fixed - (m == -INFINITY ? 0.f : m);  // (rows with no visible key so far)
+      float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int k0 = 0; k0 < kBN; k0 += 16) {
+        uint32_t pk[8];
+        exp16<BF16, false>(sr, k0, one, make_float2(base, base), 0, kBN, acc, pk);
+        tmem_st8(t_s + k0 / 2, pk);
+      }
+      const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+      l = l * alpha + (a.x + a.y);
+      if (__any_sync(0xffffffffu, upd) && j > 0) {
+        // O_t holds the blocks before j relative to the old m (P_t(j-1) V(j-1)
+        // is complete: S_t(j) was committed after it).
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o16[16];
+          tmem_ld16(t_o + c, o16);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float2 v = __fmul2_rn(make_float2(__uint_as_float(o16[i]), __uint_as_float(o16[i + 1])),
+                                        make_float2(alpha, alpha));
+            o16[i] = __float_as_uint(v.x);
+            o16[i + 1] = __float_as_uint(v.y);
+          }
+          tmem_st16(t_o + c, o16);
+        }
+      }
+      tmem_st_wait();
+      warp_arrive(&bar_pfull[t]);
+    }
+    // ------------------------------------------------------------ epilogue
+    if (alive && nb > 0 && warp_wait(&bar_ofinal[t], 0, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax)) {
+      tc_fence_after();
+      const float inv_l = 1.f / l;
+      const bool row_ok = row_g < S;
+      const int rr = row_ok ? row_g : 0;
+      const size_t o_row =
+          packed ? static_cast<size_t>(tok0 + rr) * p.heads + q_head : static_cast<size_t>(bh) * S + rr;
+      const size_t l_idx = packed ? static_cast<size_t>(q_head) * p.total + tok0 + rr : o_row;
+      elem_t* orow = reinterpret_cast<elem_t*>(p.o) + o_row * D;
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        uint32_t o16[16];
+        tmem_ld16(t_o + c, o16);
+        if (row_ok) store_row16<BF16>(orow + c, o16, inv_l);
+      }
+      if (row_ok) p.lse[l_idx] = (m + log2f(l)) * 0.69314718055994530942f;
+    }
+  } else {
+    regs_increase<kF4RegsHigh>();
+    // ------------------------------------------------------------ softmax warps
+    const int t = warp >> 2;  // tile
+    const int q4 = warp & 3;  // lane quarter
+    const int r = q4 * 32 + lane;
+    const int tile_row0 = row0 + t * kBlockM;
+    const int row_g = tile_row0 + r;
+    const int kb0 = first_blk(tile_row0);  // the tile's first key block
+    const int nb = max(0, blocks_for(tile_row0) - kb0);
+    const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + 128u * t;  // S_t, and P_t over it
+    const uint32_t t_o = t_s + L::kColO;
+    const float sl2 = p.scale_log2;
+    const float2 c2 = make_float2(sl2, sl2);
+    const bool neg_scale = sl2 < 0.f;
+    // Last (and, general instantiation, first) visible key of this row.
+    const int last = GENERAL ? min(S - 1, row_g + wr) : (p.causal ? min(S - 1, row_g) : S - 1);
+    const int first_key = row_g - wl;
+    float m = -INFINITY;  // running (possibly stale) maximum, base-2 scaled
+    float l = 0.f;
+    bool alive = true;
+    for (int j = 0; j < nb; ++j) {
+      if (!warp_wait(&bar_sfull[t], j & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t sr[kBN];
+      tmem_ld64(t_s, sr);
+      const int kv0 = (kb0 + j) * kBN;
       const int lim = last - kv0;      // columns c <= lim are visible to this row
       const int lo = first_key - kv0;  // and (general instantiation) c >= lo
       // Masked blocks: those crossing the diagonal under the causal mask (an
       // edge of the window band), and a ragged last key block.
       const bool masked =
-          GENERAL ? (kv0 + kBN > S) || (kv0 + kBN - 1 > (SCORED ? max(tile_row0 + wr, pfx - 1) : tile_row0 + wr)) ||
-                        (kv0 < tile_row0 + kBlockM - 1 - wl)
+          GENERAL ? (kv0 + kBN > S) || (kv0 + kBN - 1 > tile_row0 + wr) || (kv0 < tile_row0 + kBlockM - 1 - wl)
                   : (kv0 + kBN > S) || (p.causal && kv0 + kBN - 1 > tile_row0);
-      float fixed = 0.f;  // SCORED: what the row's scores in this block have in common
-      if constexpr (SCORED) {
-        const RowBias bias = row_bias(slope, kv0 - row_g, kv0 + kBN - 1 <= tile_row0 || (p.causal && pfx == 0),
-                                      kv0 >= tile_row0 + kBlockM - 1);
-        fixed = bias.fixed;
-        block_scores<kBN>(sr, t_s, p.sc, make_float2(p.scale_log2, p.scale_log2), bias, masked,
-                          PlainCols{masked ? lo : 0, masked ? lim : kBN});
-      }
-      if (!SCORED && j == 0) m = block_max_scaled<kBN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
+      if (j == 0) m = block_max_scaled<kBN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
       float alpha = 1.f;
       bool upd = false;
       float blk;
       // P~ of the block, written 16 keys at a time over the S columns just read.
       auto exps = [&]() {
         const float m_use = (m == -INFINITY) ? 0.f : m;  // rows with no visible key so far
-        const float nb = SCORED ? fixed - m_use : -m_use;
-        const float2 negm = make_float2(nb, nb);
+        const float2 negm = make_float2(-m_use, -m_use);
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                          make_float2(0.f, 0.f)};
-        if (!SCORED && masked) {
+        if (masked) {
 #pragma unroll
           for (int k0 = 0; k0 < kBN; k0 += 16) {
             uint32_t pk[8];
@@ -542,60 +622,41 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
         return a.x + a.y;
       };
-      bool rescale;
-      if constexpr (SCORED) {
-        // The block's maximum ahead of its exponentials: m moves where it is exceeded by
-        // more than 2^8.  (Scores that were formed in place have their -inf, and a bias
-        // moves the maximum so often that a second try would be the rule.)
-        const float m_blk = block_max_scaled<kBN>(sr, false, 0, kBN, 1.f, false) + fixed;
-        if (m_blk > m + kF4Tau || (m == -INFINITY && m_blk > m)) {
+      blk = exps();
+      // Every P~ <= 2^8 holds if the block's sum does.  Otherwise (or on NaN)
+      // the stale m is too far below this block's maximum: move m, rescale,
+      // and redo the block.
+      bool need = !(blk <= kF4SumLimit);
+      if constexpr (GENERAL) {
+        // A window can hide every key of a row's first blocks: m is still
+        // -inf there, and the first block that shows the row a key sets it.
+        need = need || (m == -INFINITY && max(lo, 0) <= min(lim, kBN - 1));
+      }
+      if (__any_sync(0xffffffffu, need)) {
+        const float m_blk = block_max_scaled<kBN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
+        if (need && m_blk > m) {
           alpha = ex2(m - m_blk);
           m = m_blk;
           upd = true;
         }
-        rescale = __any_sync(0xffffffffu, upd) && j > 0;
-        blk = exps();
-      } else {
-        rescale = false;
-        blk = exps();
-        // Every P~ <= 2^8 holds if the block's sum does.  Otherwise (or on NaN)
-        // the stale m is too far below this block's maximum: move m, rescale,
-        // and redo the block.
-        bool need = !(blk <= kF4SumLimit);
-        if constexpr (GENERAL) {
-          // A window can hide every key of a row's first blocks: m is still
-          // -inf there, and the first block that shows the row a key sets it.
-          need = need || (m == -INFINITY && max(lo, 0) <= min(lim, kBN - 1));
-        }
-        if (__any_sync(0xffffffffu, need)) {
-          const float m_blk = block_max_scaled<kBN, GENERAL>(sr, masked, lo, lim, sl2, neg_scale);
-          if (need && m_blk > m) {
-            alpha = ex2(m - m_blk);
-            m = m_blk;
-            upd = true;
-          }
-          if (__any_sync(0xffffffffu, upd)) {
-            tmem_st_wait();  // the first pass's stores land before they are overwritten
-            blk = exps();
-            rescale = true;
-          }
-        }
-      }
-      if (rescale) {
-        // O_t holds the blocks before j relative to the old m (P_t(j-1) V(j-1)
-        // is complete: S_t(j) was committed after it).
+        if (__any_sync(0xffffffffu, upd)) {
+          tmem_st_wait();  // the first pass's stores land before they are overwritten
+          blk = exps();
+          // O_t holds the blocks before j relative to the old m (P_t(j-1) V(j-1)
+          // is complete: S_t(j) was committed after it).
 #pragma unroll
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o16[16];
-          tmem_ld16(t_o + c, o16);
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o16[16];
+            tmem_ld16(t_o + c, o16);
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float2 v = __fmul2_rn(make_float2(__uint_as_float(o16[i]), __uint_as_float(o16[i + 1])),
-                                        make_float2(alpha, alpha));
-            o16[i] = __float_as_uint(v.x);
-            o16[i + 1] = __float_as_uint(v.y);
+            for (int i = 0; i < 16; i += 2) {
+              const float2 v = __fmul2_rn(make_float2(__uint_as_float(o16[i]), __uint_as_float(o16[i + 1])),
+                                          make_float2(alpha, alpha));
+              o16[i] = __float_as_uint(v.x);
+              o16[i + 1] = __float_as_uint(v.y);
+            }
+            tmem_st16(t_o + c, o16);
           }
-          tmem_st16(t_o + c, o16);
         }
       }
       l = l * alpha + blk;

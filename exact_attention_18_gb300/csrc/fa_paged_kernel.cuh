@@ -269,7 +269,10 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     };
     for (int n; ok && (n = w.seg_len()) > 0; w.next(p, n), ++seg) {
       // Block of the unit that the segment's j-th is.
-      auto blk_at = [&](int j) { return w.blk + (downwards(p) ? n - 1 - j : j); };
+      auto blk_at = [&](int j) {
+        if constexpr (kScored) return w.blk + (downwards(p) ? n - 1 - j : j);
+        else return w.blk + j;
+      };
       int page = box_page(blk_at(0));
       if (kv == 0) {
         const int qb = seg & 1, qu = seg >> 1;

@@ -108,20 +108,13 @@ __device__ __forceinline__ TileSpan tile_span(const P& p, const SegWalk<SHIFT, t
   s.pos0 = w.u.pos0 + s.ta;
   s.beg = s.end = 0;
   if (s.turn >= s.turns) return s;
-  int lo = max(0, s.pos0 - p.win_left);
-  const int hi = min(w.u.kv_len, s.pos0 + s.n_tok + p.win_right);
-  if constexpr (P::kScored) {
-    if (p.tree != nullptr) lo = w.u.lo;  // (any of the unit's rows may stand at the first new key)
-  }
+  // (a tree: any of the unit's rows may stand at the first new key)
+  const int lo = has_tree(p) ? w.u.lo : max(0, s.pos0 - p.win_left), hi = min(w.u.kv_len, s.pos0 + s.n_tok + p.win_right);
   if (hi <= lo) return s;
   const int base = (w.u.lo >> SHIFT) + w.blk;  // the segment's first block
-  int beg = min(n, max(0, (lo >> SHIFT) - base));
-  int end = min(n, max(0, ((hi + (1 << SHIFT) - 1) >> SHIFT) - base));
-  if (downwards(p)) {
-    const int b = beg;
-    beg = n - end;
-    end = n - b;
-  }
+  const int first = min(n, max(0, (lo >> SHIFT) - base));
+  const int last = min(n, max(0, ((hi + (1 << SHIFT) - 1) >> SHIFT) - base));
+  const int beg = downwards(p) ? n - last : first, end = downwards(p) ? n - first : last;
   s.beg = beg + ((s.turn - beg) & (s.turns - 1));
   s.end = end - ((end - 1 - s.turn) & (s.turns - 1));
   if (s.end <= s.beg) s.beg = s.end = 0;
@@ -290,7 +283,10 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       };
       for (int n; ok && (n = w.seg_len()) > 0; w.next(p, n), ++seg) {
         // Block of the unit that the segment's j-th is.
-        auto blk_at = [&](int j) { return w.blk + (downwards(p) ? n - 1 - j : j); };
+        auto blk_at = [&](int j) {
+          if constexpr (kScored) return w.blk + (downwards(p) ? n - 1 - j : j);
+          else return w.blk + j;
+        };
         int page = box_page(blk_at(0));
         if (kv == 0) {
           const int qb = seg % L::kQBufs, qu = seg / L::kQBufs;
@@ -440,7 +436,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     const int rt = r / p.G, rh = r - rt * p.G;  // its token within the tile, head within the group
     const uint32_t t_s = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + t * L::kTileCols;
     const uint32_t t_o = t_s + L::kColO;
-    const float sl2 = kScored ? 1.f : p.scale_log2;  // (modified scores are scaled)
+    const float sl2 = p.scale_log2;
     // Blocks that a mask cuts.  D <= 64: the scores a row does not see become
     // -inf (+inf under a negative scale) in place, and one copy of the code
     // serves all blocks; a copy of its own for the few cut ones cost up to 5000
@@ -451,10 +447,10 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
     constexpr bool kShare = T == 4;  // tiles may share a unit's row tile
     // In place, a scale of 0 is applied ahead of the mask (0 times a hidden key's
     // infinity would not be -inf); a NaN stays one.
-    const bool zero_scale = !kScored && kMaskInPlace && sl2 == 0.f;
+    const bool zero_scale = kMaskInPlace && sl2 == 0.f;
     const float ce = zero_scale ? 1.f : sl2;
     const float2 c2 = make_float2(ce, ce);
-    const bool neg_scale = !kScored && sl2 < 0.f;
+    const bool neg_scale = sl2 < 0.f;
     const uint32_t hidden = __float_as_uint(neg_scale ? INFINITY : -INFINITY);
     int cnt = 0, fin = 0;  // blocks of this tile so far; segments in which it had blocks
     bool alive = true;
@@ -465,38 +461,120 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       // Relative to the segment's first key: this row's visible keys [lo0, lim0],
       // and the blocks [j_lo, j_hi) that every row of the tile sees whole.
       const int key_base = ((w.u.lo >> L::kShift) + w.blk) * BN;
-      int pos = sp.pos0 + rt;
-      // Scored: the sequence's first new token and its key (trees), the row's words.
-      bool tree = false;
-      int first = 0, tok_first = 0;
-      const unsigned* row_bits = nullptr;
-      float slope = 0.f;
-      if constexpr (kScored) {
-        tree = p.tree != nullptr;
-        first = w.u.pos0 - w.tile * p.tok_tile;
-        tok_first = w.u.tok0 - w.tile * p.tok_tile;
-        if (p.sc.slopes != nullptr) slope = p.sc.slopes[w.kvh * p.G + rh] * 1.4426950408889634f;
-        if (tree && row_ok) {
-          pos = min(w.u.kv_len - 1, max(first, p.positions[w.u.tok0 + sp.ta + rt]));
-          row_bits = p.tree + (w.u.tok0 + sp.ta + rt) * p.tree_stride;
-        }
-      }
+      const int pos = sp.pos0 + rt;
       const int lim0 = min(w.u.kv_len - 1, pos + p.win_right) - key_base, lo0 = pos - p.win_left - key_base;
-      int j_lo = (sp.pos0 + sp.n_tok - 1 - p.win_left - key_base + BN - 1) >> L::kShift;
-      int j_hi = (min(w.u.kv_len, sp.pos0 + 1 + p.win_right) - key_base) >> L::kShift;
+      const int j_lo = (sp.pos0 + sp.n_tok - 1 - p.win_left - key_base + BN - 1) >> L::kShift;
+      const int j_hi = (min(w.u.kv_len, sp.pos0 + 1 + p.win_right) - key_base) >> L::kShift;
+      // Scored: what the row and its sequence are for the scores, and the same limits.
+      struct {
+        bool tree;
+        int pos, first, tok_first, kv_len, tile_pos0, tile_rows;  // first new key, its token
+        const unsigned* bits;  // a tree row's (nullptr: none)
+        float slope;
+        int lim0, lo0, j_lo, j_hi;
+      } sc;
       if constexpr (kScored) {
-        if (tree) {
-          j_lo = (w.u.kv_len - 1 - p.win_left - key_base + BN - 1) >> L::kShift;
-          j_hi = (first - key_base) >> L::kShift;
+        sc.tree = p.tree != nullptr;
+        sc.pos = pos;
+        sc.first = w.u.pos0 - w.tile * p.tok_tile;
+        sc.tok_first = w.u.tok0 - w.tile * p.tok_tile;
+        sc.kv_len = w.u.kv_len;
+        sc.tile_pos0 = sp.pos0;
+        sc.tile_rows = sp.n_tok;
+        sc.bits = nullptr;
+        sc.slope = p.sc.slopes != nullptr ? p.sc.slopes[w.kvh * p.G + rh] * 1.4426950408889634f : 0.f;
+        sc.lim0 = lim0;
+        sc.lo0 = lo0;
+        sc.j_lo = j_lo;
+        sc.j_hi = j_hi;
+        if (sc.tree) {
+          if (row_ok) {
+            sc.pos = min(sc.kv_len - 1, max(sc.first, p.positions[w.u.tok0 + sp.ta + rt]));
+            sc.bits = p.tree + (w.u.tok0 + sp.ta + rt) * p.tree_stride;
+          }
+          sc.lim0 = min(sc.kv_len - 1, sc.pos + p.win_right) - key_base;
+          sc.lo0 = sc.pos - p.win_left - key_base;
+          sc.j_lo = (sc.kv_len - 1 - p.win_left - key_base + BN - 1) >> L::kShift;
+          sc.j_hi = (sc.first - key_base) >> L::kShift;
         }
       }
       const int beg = sp.beg, end = sp.end, step = kShare ? sp.turns : 1;
-      const int kv_len = w.u.kv_len, tile_pos0 = sp.pos0, tile_rows = sp.n_tok;  // (scored)
       if (lane == 0) s_walk[warp].w = w;
       __syncwarp();
       // (the span is worked out again after the blocks: its other members would
       // take registers from the block loop)
       float m = -INFINITY, l = 0.f;
+      if constexpr (kScored) {
+        const int n_seg = n;
+        for (int j = beg; j < end; j += step, ++cnt) {
+          if (!warp_wait(&bar_sfull[t], cnt & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax)) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          uint32_t sr[BN];
+          if constexpr (BN == 128) tmem_ld128(t_s, sr);
+          else tmem_ld64(t_s, sr);
+          const int jb = downwards(p) ? n_seg - 1 - j : j;  // block of the segment
+          const int lim = sc.lim0 - jb * BN, lo = sc.lo0 - jb * BN;  // columns lo <= c <= lim are visible to this row
+          const bool cut = jb < sc.j_lo || jb >= sc.j_hi;  // a mask cuts the block
+          const int key0 = key_base + jb * BN;
+          const RowBias bias =
+              row_bias(sc.slope, key0 - sc.pos, sc.tree || p.win_right == 0 || key0 + BN - 1 <= sc.tile_pos0,
+                       key0 >= sc.tile_pos0 + sc.tile_rows - 1);
+          const float2 cs = make_float2(p.scale_log2, p.scale_log2), one = make_float2(1.f, 1.f);
+          if (sc.tree && key0 + BN > sc.first) {  // new tokens of a tree
+            TreeCols cols;
+            cols.key0 = key0;
+            cols.first = sc.first;
+            cols.kv_len = sc.kv_len;
+            cols.positions = p.positions + sc.tok_first;
+            cols.row = sc.bits;
+            cols.words = p.tree_words;
+            cols.from = sc.pos - p.win_left - key0;
+            block_scores<BN>(sr, t_s, p.sc, cs, bias, true, cols);
+          } else {
+            block_scores<BN>(sr, t_s, p.sc, cs, bias, cut, PlainCols{cut ? lo : 0, cut ? lim : BN});
+          }
+          // The block's maximum ahead of its exponentials, as in the forward kernels.
+          // Lanes past the tile's rows hold anything and never move theirs.
+          const float m_blk = block_max_scaled<BN>(sr, false, 0, BN, 1.f, false) + bias.fixed;
+          float alpha = 1.f;
+          const bool upd = row_ok && (m_blk > m + kTau || (m == -INFINITY && m_blk > m));
+          if (upd) {
+            alpha = ex2(m - m_blk);
+            m = m_blk;
+          }
+          const float base = bias.fixed - (m == -INFINITY ? 0.f : m);  // (rows with no visible key so far)
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                           make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int k0 = 0; k0 < BN; k0 += 16) {
+            uint32_t pk[8];
+            exp16<BF16, false>(sr, k0, one, make_float2(base, base), 0, BN, acc, pk);
+            tmem_st8(t_s + k0 / 2, pk);
+          }
+          const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+          l = l * alpha + (a.x + a.y);
+          if (__any_sync(0xffffffffu, upd) && j > beg) {
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o16[16];
+              tmem_ld16(t_o + c, o16);
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const float2 v = __fmul2_rn(make_float2(__uint_as_float(o16[i]), __uint_as_float(o16[i + 1])),
+                                            make_float2(alpha, alpha));
+                o16[i] = __float_as_uint(v.x);
+                o16[i + 1] = __float_as_uint(v.y);
+              }
+              tmem_st16(t_o + c, o16);
+            }
+          }
+          tmem_st_wait();
+          warp_arrive(&bar_pfull[t]);
+        }
+      } else
       for (int j = beg; j < end; j += step, ++cnt) {
         if (!warp_wait(&bar_sfull[t], cnt & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax)) {
           alive = false;
@@ -506,30 +584,9 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         uint32_t sr[BN];
         if constexpr (BN == 128) tmem_ld128(t_s, sr);
         else tmem_ld64(t_s, sr);
-        const int jb = downwards(p) ? n - 1 - j : j;  // block of the segment
-        const int lim = lim0 - jb * BN, lo = lo0 - jb * BN;  // columns lo <= c <= lim are visible to this row
-        const bool cut = jb < j_lo || jb >= j_hi;  // a mask cuts the block
-        float fixed = 0.f;  // scored: what the row's scores in this block have in common
-        if constexpr (kScored) {
-          const int key0 = key_base + jb * BN;
-          const RowBias bias = row_bias(slope, key0 - pos, tree || p.win_right == 0 || key0 + BN - 1 <= tile_pos0,
-                                        key0 >= tile_pos0 + tile_rows - 1);
-          fixed = bias.fixed;
-          const float2 cs = make_float2(p.scale_log2, p.scale_log2);
-          if (tree && key0 + BN > first) {  // new tokens of a tree
-            TreeCols cols;
-            cols.key0 = key0;
-            cols.first = first;
-            cols.kv_len = kv_len;
-            cols.positions = p.positions + tok_first;
-            cols.row = row_bits;
-            cols.words = p.tree_words;
-            cols.from = pos - p.win_left - key0;
-            block_scores<BN>(sr, t_s, p.sc, cs, bias, true, cols);
-          } else {
-            block_scores<BN>(sr, t_s, p.sc, cs, bias, cut, PlainCols{cut ? lo : 0, cut ? lim : BN});
-          }
-        } else if constexpr (kMaskInPlace) {
+        const int lim = lim0 - j * BN, lo = lo0 - j * BN;  // columns lo <= c <= lim are visible to this row
+        const bool cut = j < j_lo || j >= j_hi;  // a mask cuts the block
+        if constexpr (kMaskInPlace) {
           if (zero_scale) {
 #pragma unroll
             for (int c = 0; c < BN; ++c) sr[c] = __float_as_uint(0.f * __uint_as_float(sr[c]));
@@ -539,17 +596,15 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
             for (int c = 0; c < BN; ++c) sr[c] = c < lo || c > lim ? hidden : sr[c];
           }
         }
-        const bool masked = !kScored && !kMaskInPlace && cut;
+        const bool masked = !kMaskInPlace && cut;
         auto block_max = [&]() {
-          if constexpr (kScored) return block_max_scaled<BN>(sr, false, 0, BN, 1.f, false) + fixed;
           return block_max_scaled<BN, !kMaskInPlace>(sr, masked, lo, kMaskInPlace ? BN : lim, ce, neg_scale);
         };
-        if (!kScored && j == beg) m = block_max();
+        if (j == beg) m = block_max();
         float alpha = 1.f;
         auto exps = [&]() {
           const float m_use = m == -INFINITY ? 0.f : m;  // rows with no visible key so far
-          const float nb = kScored ? fixed - m_use : -m_use;
-          const float2 negm = make_float2(nb, nb);
+          const float2 negm = make_float2(-m_use, -m_use);
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                            make_float2(0.f, 0.f)};
           if (masked) {
@@ -570,51 +625,36 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
           return a.x + a.y;
         };
-        float blk;
-        bool rescale = false;
-        if constexpr (kScored) {
-          // The block's maximum ahead of its exponentials, as in the forward kernels.
+        float blk = exps();
+        // A block whose sum breaks the bound (or a row's first visible key)
+        // moves the maximum, rescales O and is done again.  Lanes past the
+        // tile's rows hold anything and never ask for it.
+        const bool need = row_ok && (!(blk <= kSumLimit) || m == -INFINITY);
+        if (__any_sync(0xffffffffu, need)) {
           const float m_blk = block_max();
-          const bool upd = row_ok && (m_blk > m + kTau || (m == -INFINITY && m_blk > m));
+          const bool upd = need && m_blk > m;
           if (upd) {
             alpha = ex2(m - m_blk);
             m = m_blk;
           }
-          rescale = __any_sync(0xffffffffu, upd) && j > beg;
-          blk = exps();
-        } else {
-          blk = exps();
-          // A block whose sum breaks the bound (or a row's first visible key)
-          // moves the maximum, rescales O and is done again.  Lanes past the
-          // tile's rows hold anything and never ask for it.
-          const bool need = row_ok && (!(blk <= kSumLimit) || m == -INFINITY);
-          if (__any_sync(0xffffffffu, need)) {
-            const float m_blk = block_max();
-            const bool upd = need && m_blk > m;
-            if (upd) {
-              alpha = ex2(m - m_blk);
-              m = m_blk;
-            }
-            if (__any_sync(0xffffffffu, upd)) {
-              tmem_st_wait();  // the first pass's stores land before they are overwritten
-              blk = exps();
-              rescale = j > beg;
-            }
-          }
-        }
-        if (rescale) {
+          if (__any_sync(0xffffffffu, upd)) {
+            tmem_st_wait();  // the first pass's stores land before they are overwritten
+            blk = exps();
+            if (j > beg) {
 #pragma unroll
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o16[16];
-            tmem_ld16(t_o + c, o16);
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o16[16];
+                tmem_ld16(t_o + c, o16);
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float2 v = __fmul2_rn(make_float2(__uint_as_float(o16[i]), __uint_as_float(o16[i + 1])),
-                                          make_float2(alpha, alpha));
-              o16[i] = __float_as_uint(v.x);
-              o16[i + 1] = __float_as_uint(v.y);
+                for (int i = 0; i < 16; i += 2) {
+                  const float2 v = __fmul2_rn(make_float2(__uint_as_float(o16[i]), __uint_as_float(o16[i + 1])),
+                                              make_float2(alpha, alpha));
+                  o16[i] = __float_as_uint(v.x);
+                  o16[i + 1] = __float_as_uint(v.y);
+                }
+                tmem_st16(t_o + c, o16);
+              }
             }
-            tmem_st16(t_o + c, o16);
           }
         }
         l = l * alpha + blk;

@@ -85,6 +85,12 @@ struct RunStart {
   Unit u;
 };
 
+template <typename P>
+__device__ __forceinline__ bool has_tree(const P& p) {
+  if constexpr (P::kScored) return p.tree != nullptr;
+  else return false;
+}
+
 // A segment's blocks run from the last to the first under a bias: it makes the keys
 // next to a row its largest scores, and upwards every block would move the maximum
 // and rescale O (32 sequences of 5000 keys, D = 128: 68 us upwards).
