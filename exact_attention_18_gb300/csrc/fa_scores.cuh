@@ -11,9 +11,9 @@
 // tanh.approx (whose 2^-11 would show in the weights: 0.02 of a score at a cap of
 // 50).  tanh(v) = 1 - 2 / (1 + e^(2v)) takes an exp2 and a reciprocal.  The FMA
 // units, which the softmax leaves idle, do better on a polynomial as long as
-// |v| <= 1, the common case: a cap is set well above most scores.  A score with
-// |v| <= 1 gets the polynomial's value, another the exact form's, and a warp whose
-// scores of a block are all small skips the latter.
+// |v| <= 1.1, the common case: a cap is set well above most scores.  Such a score gets
+// the polynomial's value, another the exact form's, and a warp whose scores of a block
+// are all small skips the latter.
 #pragma once
 
 #include "fa_kernel_common.cuh"
@@ -21,9 +21,9 @@
 namespace fa {
 
 // cap tanh(scale x / cap) of small x: x times a polynomial in x^2, the minimax
-// approximation of tanh(v) / v on |v| <= 1 (degree 5 in v^2, by Remez exchange:
-// relative error 6e-7, 7e-7 with fp32's roundings) with scale and cap folded into
-// the coefficients on the host (tanh_poly in fa_api.cu).
+// approximation of tanh(v) / v on |v| <= 1.1 (degree 5 in v^2: relative error 1.6e-6
+// with fp32's roundings) with scale and cap folded into the coefficients on the host
+// (tanh_poly in fa_api.cu).
 __device__ __forceinline__ float2 tanh_small(float2 x, const ScoreParams& sc) {
   const float2 w = __fmul2_rn(x, x);
   float2 t = make_float2(sc.poly[kTanhTerms - 1], sc.poly[kTanhTerms - 1]);

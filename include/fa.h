@@ -307,8 +307,8 @@ typedef struct {
  * side being unlimited and `causal` making the right side 0.  Prefix lengths may
  * lie outside [0, S]: they count as the nearer end.  scores == NULL, or all of
  * its parts absent, runs fa_fwd_window.  The window's sides and `causal` hide keys
- * whatever the scores there are.  tanh is evaluated in fp32: a score is off by
- * about 2^-20 of itself where |scale q.k| <= cap, by 2^-21 of cap beyond.
+ * whatever the scores there are.  tanh is evaluated in fp32: beside the product's
+ * own error a score is off by at most 2^-19 of itself, or by 2^-21 of cap.
  * Slopes must be finite and slopes[h] * S far below fp32's largest number.
  */
 fa_status fa_fwd_scores(const void* q, const void* k, const void* v, void* o, float* lse, int64_t B, int64_t H,

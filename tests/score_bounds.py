@@ -3,8 +3,9 @@
 u is half a step of the 16-bit type.  First order in each error, the product of two covered by a factor 1.1.
 
 A score's error e_ij: products of D terms summed in fp32, truncated at worst, scale sum_d |q_d k_d| (D + 4) 2^-23;
-under a cap, its arithmetic: 2^-20 of the score where |x| <= cap, 2^-20 of the cap beyond (the derivative of tanh is
-at most 1, so the product's error does not grow); the bias and the sums with the row's maximum or L: 2^-22 (|s| +
+under a cap, its arithmetic: 2^-19 of the score where |x| <= 1.1 cap (a minimax polynomial with a relative error of
+1.5e-6 = 2^-19.3, and fp32's roundings), 2^-20 of the cap beyond (the derivative of tanh is at most 1, so the
+product's error does not grow); the bias and the sums with the row's maximum or L: 2^-22 (|s| +
 |bias| + |L|); its exponential, 2^-21.
 
 A weight p_ij is off by e_ij p_ij, and by the row's sum: c_i p_ij with c_i = sum_j p_ij e_ij + n 2^-24 (fp32 sums of n
@@ -15,7 +16,7 @@ and O is rounded once (u |O|, fp16's subnormals 2^-25).  L: c_i + 2^-22 |L| + 2^
 Backward: P = exp(s - L) is off by (e_ij + errL_i) p_ij and rounded (u p_ij; fp16 2^-25).  Delta_i from the stored O:
 sum_d |dO_d| (errO_d + D 2^-24 |O_d|); dP: D 2^-23 sum_d |dO_d v_d|; g = dP - Delta, so dS = p g f is off by
   (e_ij + errL_i + u) |dS_ij| + p_ij f_ij (err dP + err Delta) + p_ij |g_ij| errf_ij + 2^-25 (fp16),
-errf = 2 |t| err t + 2^-22 with err t = (error of the product) / cap + 2^-21.  The products over n rows or keys sum in
+errf = 2 |t| err t + 2^-22 with err t = (error of the product) / cap + 2^-19 |t|.  The products over n rows or keys sum in
 fp32: n 2^-23 of their absolute terms.
 """
 import math
@@ -32,7 +33,7 @@ def score_error(r, q, k, scale, softcap):
     ex = abs(scale) * (D + 4) * 2.0 ** -23 * (as_f64(q).abs() @ as_f64(k).abs().T)
     e = ex + 2.0 ** -21
     if softcap is not None:
-        e = e + 2.0 ** -20 * torch.minimum(r["x"].abs(), torch.full_like(ex, softcap))
+        e = e + 2.0 ** -19 * torch.minimum(r["x"].abs(), torch.full_like(ex, softcap))
     s = torch.where(torch.isfinite(r["s"]), r["s"], torch.zeros_like(r["s"]))
     l = torch.where(torch.isfinite(r["lse"]), r["lse"], torch.zeros_like(r["lse"]))
     return ex, e + 2.0 ** -22 * (s.abs() + r["bias"].abs() + l.abs()[:, None])
@@ -69,7 +70,7 @@ def backward_bounds(r, q, k, v, do, scale, softcap, dtype):
     ds = (ep + u) * r["ds"].abs() + p * f * (dp + delta[:, None]) + sub * seen
     if softcap is not None:
         t = torch.sqrt((1 - f).clamp(min=0))
-        ds = ds + p * g * (2 * t * (ex / softcap + 2.0 ** -21) + 2.0 ** -22)
+        ds = ds + p * g * (2 * t * (ex / softcap + 2.0 ** -19 * t + 2.0 ** -21) + 2.0 ** -22)
     acc = n * 2.0 ** -23
     dsa = r["ds"].abs()
     dq = abs(scale) * ((ds + acc * dsa) @ ka)
