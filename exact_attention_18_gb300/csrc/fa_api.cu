@@ -234,7 +234,7 @@ fa_status encode_input(CUtensorMap* map, const void* base, bool bf16, const Shap
 
 // The constants of a cap.  tanh(v) / v on |v| <= 1.1 is a polynomial in v^2 (minimax
 // of degree 5, by Remez exchange; relative error 1.5e-6, 1.6e-6 with fp32's roundings);
-// with v = scale x / cap it becomes cap log2 e tanh(v) = x * sum_k poly[k] x^(2k).
+// with v = scale x / cap it becomes tanh(v) = x * sum_k poly[k] x^(2k).
 // Coefficients that leave fp32's normal range bound the |x| it is used for: below it
 // to where the terms left out are under 2^-22 of the value, above it to 0.
 // Range and degree were measured (us; scores of deviation 4 under 50 B2 H32/4 S4096
@@ -243,10 +243,10 @@ fa_status encode_input(CUtensorMap* map, const void* base, bool bf16, const Shap
 void tanh_poly(float scale, float cap, fa::ScoreParams* p) {
   constexpr double kC[fa::kTanhTerms] = {0.99999849, -0.33324176, 0.13241123, -0.050452815, 0.015411088, -0.0025325383};
   constexpr double kMax = 1.1;
-  const double in = static_cast<double>(scale) / cap, top = static_cast<double>(cap) * 1.4426950408889634074;
-  p->cap = static_cast<float>(top);
+  const double in = static_cast<double>(scale) / cap;
+  p->cap = static_cast<float>(cap * 1.4426950408889634074);
   p->in2 = static_cast<float>(2 * 1.4426950408889634074 * in);
-  double vmax = kMax, f = top * in;
+  double vmax = kMax, f = in;
   for (int k = 0; k < fa::kTanhTerms; ++k, f *= in * in) {
     p->poly[k] = static_cast<float>(kC[k] * f);
     const double size = std::fabs(kC[k] * f);
@@ -266,6 +266,11 @@ fa_status check_scores(const fa_scores* in, float scale, bool prefix_ok, bool pa
                        fa::ScoreParams* out) {
   *on = false;
   *out = fa::ScoreParams{};
+  const float scale_log2 = scale * kLog2e;
+  const bool by_scale = scale_log2 >= 1e-4f;
+  out->unit = by_scale ? scale_log2 : 1.f;
+  out->pre = by_scale ? 0.f : scale_log2;
+  out->per_unit = 1.f / out->unit;
   if (!in) return FA_OK;
   if (!std::isfinite(in->softcap) || in->softcap < 0)
     return fail(FA_ERR_INVALID_ARG, "softcap must be finite and not negative (0: none)");
@@ -277,6 +282,9 @@ fa_status check_scores(const fa_scores* in, float scale, bool prefix_ok, bool pa
     if (in->softcap < 1e-10f || in->softcap > 1e10f || !std::isfinite(scale / in->softcap * 3.f))
       return fail(FA_ERR_UNSUPPORTED, "softcap must be between 1e-10 and 1e10, and scale / softcap finite");
     tanh_poly(scale, in->softcap, out);
+    out->unit = out->cap;
+    out->pre = 0.f;
+    out->per_unit = 1.f / out->unit;
   }
   out->slopes = in->slopes;
   out->prefix = in->prefix;

@@ -189,15 +189,13 @@ __device__ __forceinline__ void grad_block_kv(uint32_t tX, uint32_t tY, const fl
 }
 
 // Modified scores.  Of two products x: y = their base-2 scores plus `add` (minus L
-// log2 e and the bias), and under a cap f = 1 - tanh^2, from the cap's own value
-// c tanh: f = 1 - (c tanh)^2 / c^2.
+// log2 e and the bias), and under a cap f = 1 - tanh^2.
 template <CapForm F>
-__device__ __forceinline__ float2 grad_score(float2 x, float2 add, const ScoreParams& sc, float2 c2, float curve,
-                                             float2* f) {
+__device__ __forceinline__ float2 grad_score(float2 x, float2 add, const ScoreParams& sc, float2 c2, float2* f) {
   if constexpr (F == kNoCap) return __ffma2_rn(x, c2, add);
-  const float2 y = score2<F>(x, sc, c2);
-  *f = __ffma2_rn(__fmul2_rn(y, make_float2(curve, curve)), y, make_float2(1.f, 1.f));
-  return __fadd2_rn(y, add);
+  const float2 t = tanh2<F>(x, sc);
+  *f = __ffma2_rn(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f));
+  return __ffma2_rn(t, make_float2(sc.cap, sc.cap), add);
 }
 template <int N>
 __device__ __forceinline__ bool all_small(const uint32_t* xs, const ScoreParams& sc) {
@@ -207,7 +205,6 @@ __device__ __forceinline__ bool all_small(const uint32_t* xs, const ScoreParams&
 // What a thread of either pass knows of a block beside the products.
 struct ScoreBlock {
   float slope;   // s_h
-  float curve;   // -1 / c^2
   int side;      // keys at or before their queries (-1), behind them (1), on both sides (0)
   int d0;        // distance key - query at the thread's first row and column
   bool edge;     // a mask cuts the block: the limits count
@@ -235,7 +232,7 @@ __device__ __forceinline__ void grad16_scored(const uint32_t* xs, const uint32_t
                         fmaf(-sb.slope, fabsf(static_cast<float>(sb.d0 + cc + 1)), -my_l2));
     const float2 x = make_float2(__uint_as_float(xs[c]), __uint_as_float(xs[c + 1]));
     float2 f;
-    const float2 y = grad_score<F>(x, add, sc, c2, sb.curve, &f);
+    const float2 y = grad_score<F>(x, add, sc, c2, &f);
     float2 pr = make_float2(ex2(y.x), ex2(y.y));
     if (!FAST && sb.edge) {
       if (cc < sb.lo || cc > sb.hi) pr.x = 0.f;
@@ -253,41 +250,28 @@ template <bool BF16>
 __device__ __forceinline__ void grad_block_scored(uint32_t tX, uint32_t tY, const ScoreParams& sc, float2 c2,
                                                   float my_l2, float my_delta, const ScoreBlock& sb) {
   const bool capped = sc.cap != 0.f, biased = sc.slopes != nullptr;
-  bool fast = !sb.edge && (sb.side != 0 || !biased);
-  if (fast && capped) {
-    // (a load of X of its own: decided half by half, beside the other form's code, the
-    // capped passes took 3 to 7 % longer)
-    uint32_t xs[32];
-    tmem_ld32(tX, xs);
-    fast = all_small<32>(xs, sc);
+  // The whole of X first: which form the block takes, and the products of both halves.
+  uint32_t xs[32], ys[16], dk[8];
+  const bool fast = !sb.edge && (sb.side != 0 || !biased);
+  tmem_ld32(tX, xs);
+  if (fast && (!capped || all_small<32>(xs, sc))) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      tmem_ld16(tY + 16 * h, ys);
+      if (!capped) grad16_scored<BF16, true, kNoCap, true>(xs + 16 * h, ys, dk, h, sc, c2, my_l2, my_delta, sb);
+      else if (biased) grad16_scored<BF16, true, kCapSmall, true>(xs + 16 * h, ys, dk, h, sc, c2, my_l2, my_delta, sb);
+      else grad16_scored<BF16, true, kCapSmall, false>(xs + 16 * h, ys, dk, h, sc, c2, my_l2, my_delta, sb);
+      tmem_st8(tY + 8 * h, dk);
+    }
+    return;
   }
-  auto half = [&](int h, auto form) {
-    uint32_t xs[16], ys[16], dk[8];
+  // (a rolled loop: the rare form's code is to be short, as in the forward)
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
     tmem_ld16x2(tX + 16 * h, xs, tY + 16 * h, ys);
-    form(xs, ys, dk, h);
-    tmem_st8(tY + 8 * h, dk);
-  };
-  auto any = [&](const uint32_t* xs, const uint32_t* ys, uint32_t* dk, int h) {
     if (capped) grad16_scored<BF16, false, kCapAny, true>(xs, ys, dk, h, sc, c2, my_l2, my_delta, sb);
     else grad16_scored<BF16, false, kNoCap, true>(xs, ys, dk, h, sc, c2, my_l2, my_delta, sb);
-  };
-  if (!fast) {
-    // (a rolled loop: the rare form's code is to be short, as in the forward)
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) half(h, any);
-  } else if (!capped) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      half(h, [&](const uint32_t* xs, const uint32_t* ys, uint32_t* dk, int hh) {
-        grad16_scored<BF16, true, kNoCap, true>(xs, ys, dk, hh, sc, c2, my_l2, my_delta, sb);
-      });
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      half(h, [&](const uint32_t* xs, const uint32_t* ys, uint32_t* dk, int hh) {
-        if (biased) grad16_scored<BF16, true, kCapSmall, true>(xs, ys, dk, hh, sc, c2, my_l2, my_delta, sb);
-        else grad16_scored<BF16, true, kCapSmall, false>(xs, ys, dk, hh, sc, c2, my_l2, my_delta, sb);
-      });
+    tmem_st8(tY + 8 * h, dk);
   }
 }
 
@@ -323,7 +307,7 @@ __device__ __forceinline__ void grad16_kv_scored(const uint32_t* xs, const uint3
                           fmaf(-sb.slope, fabsf(static_cast<float>(sb.d0 + line - cc - 1)), nl2[i].y));
       const float2 x = make_float2(__uint_as_float(xs[e]), __uint_as_float(xs[e + 1]));
       float2 f;
-      const float2 y = grad_score<F>(x, add, sc, c2, sb.curve, &f);
+      const float2 y = grad_score<F>(x, add, sc, c2, &f);
       float2 pr = make_float2(ex2(y.x), ex2(y.y));
       if (!FAST && sb.edge) {
         const int lim = sb.d0 + line;
@@ -354,42 +338,36 @@ __device__ __forceinline__ void grad_block_kv_scored(uint32_t tX, uint32_t tY, c
     dl[i] = make_float2(-d2.x, -d2.y);
   }
   const bool capped = sc.cap != 0.f, biased = sc.slopes != nullptr;
-  bool fast = !sb.edge && (sb.side != 0 || !biased);
-  if (fast && capped) {
-    uint32_t xs[32];
-    tmem_ld32(tX, xs);
-    fast = all_small<32>(xs, sc);
-  }
-  auto half = [&](int h, auto form) {
-    const uint32_t lane_off = static_cast<uint32_t>(16 * h) << 16;
-    uint32_t xs[16], ys[16], pk[8], dk[8];
-    tmem_ld16x256b_x4(tX + lane_off, xs);
-    tmem_ld16x256b_x4(tY + lane_off, ys);
-    tmem_ld_wait();
-    form(xs, ys, pk, dk, h);
-    tmem_st16x128b_x4(tX + lane_off, pk);
-    tmem_st16x128b_x4(tY + lane_off, dk);
+  constexpr uint32_t kHalfLanes = 16u << 16;
+  uint32_t xs[32], ys[16], pk[8], dk[8];
+  auto store = [&](uint32_t off) {
+    tmem_st16x128b_x4(tX + off, pk);
+    tmem_st16x128b_x4(tY + off, dk);
   };
-  auto any = [&](const uint32_t* xs, const uint32_t* ys, uint32_t* pk, uint32_t* dk, int h) {
+  const bool fast = !sb.edge && (sb.side != 0 || !biased);
+  tmem_ld16x256b_x4(tX, xs);
+  tmem_ld16x256b_x4(tX + kHalfLanes, xs + 16);
+  tmem_ld_wait();
+  if (fast && (!capped || all_small<32>(xs, sc))) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      tmem_ld16x256b_x4(tY + h * kHalfLanes, ys);
+      tmem_ld_wait();
+      if (!capped) grad16_kv_scored<BF16, true, kNoCap, true>(xs + 16 * h, ys, pk, dk, h, nl2, dl, sc, c2, sb);
+      else if (biased) grad16_kv_scored<BF16, true, kCapSmall, true>(xs + 16 * h, ys, pk, dk, h, nl2, dl, sc, c2, sb);
+      else grad16_kv_scored<BF16, true, kCapSmall, false>(xs + 16 * h, ys, pk, dk, h, nl2, dl, sc, c2, sb);
+      store(h * kHalfLanes);
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    tmem_ld16x256b_x4(tX + h * kHalfLanes, xs);
+    tmem_ld16x256b_x4(tY + h * kHalfLanes, ys);
+    tmem_ld_wait();
     if (capped) grad16_kv_scored<BF16, false, kCapAny, true>(xs, ys, pk, dk, h, nl2, dl, sc, c2, sb);
     else grad16_kv_scored<BF16, false, kNoCap, true>(xs, ys, pk, dk, h, nl2, dl, sc, c2, sb);
-  };
-  if (!fast) {
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) half(h, any);
-  } else if (!capped) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      half(h, [&](const uint32_t* xs, const uint32_t* ys, uint32_t* pk, uint32_t* dk, int hh) {
-        grad16_kv_scored<BF16, true, kNoCap, true>(xs, ys, pk, dk, hh, nl2, dl, sc, c2, sb);
-      });
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      half(h, [&](const uint32_t* xs, const uint32_t* ys, uint32_t* pk, uint32_t* dk, int hh) {
-        if (biased) grad16_kv_scored<BF16, true, kCapSmall, true>(xs, ys, pk, dk, hh, nl2, dl, sc, c2, sb);
-        else grad16_kv_scored<BF16, true, kCapSmall, false>(xs, ys, pk, dk, hh, nl2, dl, sc, c2, sb);
-      });
+    store(h * kHalfLanes);
   }
 }
 
@@ -756,10 +734,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       my_delta = p.delta[li];
     }
     ScoreBlock sb;
-    if constexpr (SCORED) {
-      sb.slope = 0.f;
-      sb.curve = -1.f / (p.sc.cap * p.sc.cap);  // (unused without a cap)
-    }
+    sb.slope = 0.f;
     bool alive = true;
     int ph = pz0;  // SCORED, dK/dV pass: partner head of the block
     int pi = g;  // i modulo nper: the partner block within its head (dK/dV pass)

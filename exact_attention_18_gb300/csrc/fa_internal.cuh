@@ -71,8 +71,14 @@ struct BwdParams {
 constexpr int kTanhTerms = 6;
 struct ScoreParams {
   float cap;            // cap * log2 e; 0: no cap
+  // What the scores are in units of between the products and the exponentials, whose
+  // multiply-add puts it in: the cap, so that they are tanh, or the scale, so that they
+  // are the products as they come.  A scale that is no sensible unit (negative, 0,
+  // tiny) is multiplied in beforehand instead.
+  float unit, per_unit;  // base 2; its reciprocal
+  float pre;             // factor of the products beforehand; 0: none
   float in2;            // 2 log2 e scale / cap: e^(2v) = 2^(in2 x), v = scale x / cap
-  float small;          // |x| up to which the polynomial gives cap tanh(v)
+  float small;          // |x| up to which the polynomial gives tanh(v)
   float poly[kTanhTerms];  // its coefficients, of x^(2k + 1)
   const float* slopes;  // [H] in device memory, natural units; nullptr: no bias
   const int* prefix;    // [B] in device memory: keys before prefix[b] are visible to all rows; nullptr: none

@@ -488,14 +488,15 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
         if constexpr (kScored) {
           if (ok) {
             // In place: the scores, scaled; the cap by its polynomial or exactly, each by itself.
-            const float2 cs = make_float2(p.scale_log2, p.scale_log2);
+            const float factor = p.sc.cap != 0.f ? p.sc.unit : p.scale_log2;
+            const float2 cs = make_float2(factor, factor);
             const bool all_small = p.sc.cap == 0.f || __all_sync(0xffffffffu, abs_max<NC>(sr) <= p.sc.small);
 #pragma unroll
             for (int k = 0; k < NC; k += 2) {
               const float2 x = make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
-              const float2 y = p.sc.cap == 0.f ? score2<kNoCap>(x, p.sc, cs)
-                               : all_small     ? score2<kCapSmall>(x, p.sc, cs)
-                                               : score2<kCapAny>(x, p.sc, cs);
+              float2 y = x;
+              if (p.sc.cap != 0.f) y = all_small ? tanh2<kCapSmall>(x, p.sc) : tanh2<kCapAny>(x, p.sc);
+              y = __fmul2_rn(y, cs);
               sr[k] = __float_as_uint(y.x);
               sr[k + 1] = __float_as_uint(y.y);
             }

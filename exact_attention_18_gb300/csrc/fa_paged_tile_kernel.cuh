@@ -122,28 +122,41 @@ __device__ __forceinline__ TileSpan tile_span(const P& p, const SegWalk<SHIFT, t
 }
 
 // The columns of a block that holds new tokens of a tree: a row sees those whose bit
-// is set, and of the keys before them those from column `from` on; a drafted key
-// stands at its position.
+// is set, and of the keys before them those that its window leaves; a drafted key
+// stands at its position.  Loaded while the block's products are made, the positions
+// a lane each.
+template <int N>
 struct TreeCols {
-  int key0, first, kv_len;  // first key of the block, first new key, keys
-  const int* positions;     // of the sequence's new tokens
-  const unsigned* row;      // the row's bits (nullptr: none)
-  int words, from;
+  unsigned seen[N / 32];
+  int at[N / 32];  // of lane l: where key 32 x + l of the block stands, less its first key
   static constexpr bool kOff = true;
-  __device__ __forceinline__ unsigned word(int c0) const {
-    const int j0 = key0 + c0 - first;  // new token of the first of the 32 columns; below 0: a key before them
-    unsigned x = ~0u;
-    if (j0 > -32) {
-      const int i = j0 >> 5;  // -1 .. : the word that holds it
-      const unsigned a = i < 0 ? ~0u : (row != nullptr && i < words ? row[i] : 0u);
-      const unsigned b = row != nullptr && i + 1 < words ? row[i + 1] : 0u;
-      x = __funnelshift_r(a, b, j0 & 31);
+  // key0: the block's first key; first: the sequence's first new key; row: the bits of
+  // this lane's row (nullptr: none); from: first column that the window leaves.
+  __device__ __forceinline__ void load(int key0, int first, int kv_len, const int* positions, const unsigned* row,
+                                       int words, int from) {
+#pragma unroll
+    for (int x = 0; x < N / 32; ++x) {
+      const int j0 = key0 + 32 * x - first;  // new token of the first of the 32 columns; below 0: a key before them
+      unsigned w = ~0u;
+      if (j0 > -32) {
+        const int i = j0 >> 5;  // -1 .. : the word that holds it
+        const unsigned lo = i < 0 ? ~0u : (row != nullptr && i < words ? row[i] : 0u);
+        const unsigned hi = row != nullptr && i + 1 < words ? row[i + 1] : 0u;
+        w = __funnelshift_r(lo, hi, j0 & 31);
+      }
+      seen[x] = w & bit_range(min(from, first - key0) - 32 * x, kv_len - key0 - 32 * x);
+      const int c = 32 * x + static_cast<int>(threadIdx.x & 31), j = key0 + c - first;
+      at[x] = j < 0 || key0 + c >= kv_len || positions == nullptr ? c
+                                                                  : min(kv_len - 1, max(first, positions[j])) - key0;
     }
-    return x & bit_range(min(from, first - key0) - c0, kv_len - key0 - c0);
   }
+  __device__ __forceinline__ unsigned word(int c0) const { return seen[c0 / 32]; }
+  // (all lanes ask for the same column)
   __device__ __forceinline__ int off(int c) const {
-    if (key0 + c < first || key0 + c >= kv_len) return c;
-    return min(kv_len - 1, max(first, positions[key0 + c - first])) - key0;
+    int v = at[0];
+#pragma unroll
+    for (int x = 1; x < N / 32; ++x) v = c / 32 == x ? at[x] : v;
+    return __shfl_sync(0xffffffffu, v, c & 31);
   }
 };
 
@@ -482,7 +495,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         sc.tile_pos0 = sp.pos0;
         sc.tile_rows = sp.n_tok;
         sc.bits = nullptr;
-        sc.slope = p.sc.slopes != nullptr ? p.sc.slopes[w.kvh * p.G + rh] * 1.4426950408889634f : 0.f;
+        sc.slope = p.sc.slopes != nullptr ? p.sc.slopes[w.kvh * p.G + rh] * 1.4426950408889634f * p.sc.per_unit : 0.f;
         sc.lim0 = lim0;
         sc.lo0 = lo0;
         sc.j_lo = j_lo;
@@ -507,6 +520,15 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       if constexpr (kScored) {
         const int n_seg = n;
         for (int j = beg; j < end; j += step, ++cnt) {
+          const int jb = downwards(p) ? n_seg - 1 - j : j;  // block of the segment
+          const int lim = sc.lim0 - jb * BN, lo = sc.lo0 - jb * BN;  // columns lo <= c <= lim are visible to this row
+          const bool cut = jb < sc.j_lo || jb >= sc.j_hi;  // a mask cuts the block
+          const int key0 = key_base + jb * BN;
+          TreeCols<BN> cols;
+          const bool drafted = sc.tree && key0 + BN > sc.first;  // the block holds new tokens of a tree
+          if (drafted)
+            cols.load(key0, sc.first, sc.kv_len, p.sc.slopes != nullptr ? p.positions + sc.tok_first : nullptr, sc.bits,
+                      p.tree_words, lo);
           if (!warp_wait(&bar_sfull[t], cnt & 1, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax)) {
             alive = false;
             break;
@@ -515,30 +537,14 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           uint32_t sr[BN];
           if constexpr (BN == 128) tmem_ld128(t_s, sr);
           else tmem_ld64(t_s, sr);
-          const int jb = downwards(p) ? n_seg - 1 - j : j;  // block of the segment
-          const int lim = sc.lim0 - jb * BN, lo = sc.lo0 - jb * BN;  // columns lo <= c <= lim are visible to this row
-          const bool cut = jb < sc.j_lo || jb >= sc.j_hi;  // a mask cuts the block
-          const int key0 = key_base + jb * BN;
           const RowBias bias =
-              row_bias(sc.slope, key0 - sc.pos, sc.tree || p.win_right == 0 || key0 + BN - 1 <= sc.tile_pos0,
+              row_bias(p.sc, sc.slope, key0 - sc.pos, sc.tree || p.win_right == 0 || key0 + BN - 1 <= sc.tile_pos0,
                        key0 >= sc.tile_pos0 + sc.tile_rows - 1);
-          const float2 cs = make_float2(p.scale_log2, p.scale_log2), one = make_float2(1.f, 1.f);
-          if (sc.tree && key0 + BN > sc.first) {  // new tokens of a tree
-            TreeCols cols;
-            cols.key0 = key0;
-            cols.first = sc.first;
-            cols.kv_len = sc.kv_len;
-            cols.positions = p.positions + sc.tok_first;
-            cols.row = sc.bits;
-            cols.words = p.tree_words;
-            cols.from = sc.pos - p.win_left - key0;
-            block_scores<BN>(sr, t_s, p.sc, cs, bias, true, cols);
-          } else {
-            block_scores<BN>(sr, t_s, p.sc, cs, bias, cut, PlainCols{cut ? lo : 0, cut ? lim : BN});
-          }
+          if (drafted) block_scores<BN>(sr, t_s, p.sc, bias, true, cols);
+          else block_scores<BN>(sr, t_s, p.sc, bias, cut, PlainCols{cut ? lo : 0, cut ? lim : BN});
           // The block's maximum ahead of its exponentials, as in the forward kernels.
           // Lanes past the tile's rows hold anything and never move theirs.
-          const float m_blk = block_max_scaled<BN>(sr, false, 0, BN, 1.f, false) + bias.fixed;
+          const float m_blk = block_top<BN>(sr, p.sc) + bias.fixed;
           float alpha = 1.f;
           const bool upd = row_ok && (m_blk > m + kTau || (m == -INFINITY && m_blk > m));
           if (upd) {
@@ -551,7 +557,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
 #pragma unroll
           for (int k0 = 0; k0 < BN; k0 += 16) {
             uint32_t pk[8];
-            exp16<BF16, false>(sr, k0, one, make_float2(base, base), 0, BN, acc, pk);
+            exp16<BF16, false>(sr, k0, make_float2(p.sc.unit, p.sc.unit), make_float2(base, base), 0, BN, acc, pk);
             tmem_st8(t_s + k0 / 2, pk);
           }
           const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));

@@ -17,19 +17,20 @@
 #pragma once
 
 #include "fa_kernel_common.cuh"
+#include "fa_softmax.cuh"
 
 namespace fa {
 
-// cap tanh(scale x / cap) of small x: x times a polynomial in x^2, the minimax
+// tanh(scale x / cap) of small x: x times a polynomial in x^2, the minimax
 // approximation of tanh(v) / v on |v| <= 1.1 (degree 5 in v^2: relative error 1.6e-6
-// with fp32's roundings) with scale and cap folded into the coefficients on the host
+// with fp32's roundings) with scale / cap folded into the coefficients on the host
 // (tanh_poly in fa_api.cu).
 __device__ __forceinline__ float2 tanh_small(float2 x, const ScoreParams& sc) {
   const float2 w = __fmul2_rn(x, x);
   float2 t = make_float2(sc.poly[kTanhTerms - 1], sc.poly[kTanhTerms - 1]);
 #pragma unroll
   for (int k = kTanhTerms - 2; k >= 0; --k) t = __ffma2_rn(t, w, make_float2(sc.poly[k], sc.poly[k]));
-  return t;  // the factor of x
+  return __fmul2_rn(t, x);
 }
 
 __device__ __forceinline__ float rcp(float x) {
@@ -38,12 +39,12 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// r = 1 / (1 + e^(2v)): tanh(v) = 1 - 2 r.  A reciprocal each: one of the product of
-// both denominators would let a hidden neighbour's NaN through.
-__device__ __forceinline__ float2 tanh_rest(float2 x, float in2) {
-  const float2 z = __fmul2_rn(x, make_float2(in2, in2));
+// tanh(v) = 1 - 2 / (1 + e^(2v)), v = scale x / cap.  A reciprocal each: one of the
+// product of both denominators would let a hidden neighbour's NaN through.
+__device__ __forceinline__ float2 tanh_exact(float2 x, const ScoreParams& sc) {
+  const float2 z = __fmul2_rn(x, make_float2(sc.in2, sc.in2));
   const float2 a = __fadd2_rn(make_float2(ptx::ex2(z.x), ptx::ex2(z.y)), make_float2(1.f, 1.f));
-  return make_float2(rcp(a.x), rcp(a.y));
+  return __ffma2_rn(make_float2(rcp(a.x), rcp(a.y)), make_float2(-2.f, -2.f), make_float2(1.f, 1.f));
 }
 
 // Largest |x| of N scores (N a multiple of 8); NaN does not count.
@@ -66,20 +67,18 @@ __device__ __forceinline__ float abs_max(const uint32_t* sr) {
   return m[0];
 }
 
-// Base-2 scores of two products x, less any bias.  kCapAny looks at each score;
-// kCapSmall is for warps whose scores are all small: the same bits.
+// tanh of two products by the rule of both forms.  kCapAny looks at each; kCapSmall
+// is for warps whose products are all small: the same bits.
 enum CapForm { kNoCap = 0, kCapSmall = 1, kCapAny = 2 };
 template <CapForm F>
-__device__ __forceinline__ float2 score2(float2 x, const ScoreParams& sc, float2 c2) {
-  if constexpr (F == kNoCap) return __fmul2_rn(x, c2);
-  float2 y = __fmul2_rn(x, tanh_small(x, sc));
+__device__ __forceinline__ float2 tanh2(float2 x, const ScoreParams& sc) {
+  float2 t = tanh_small(x, sc);
   if constexpr (F == kCapAny) {
-    const float2 u =
-        __ffma2_rn(tanh_rest(x, sc.in2), make_float2(-2.f * sc.cap, -2.f * sc.cap), make_float2(sc.cap, sc.cap));
-    y.x = fabsf(x.x) <= sc.small ? y.x : u.x;
-    y.y = fabsf(x.y) <= sc.small ? y.y : u.y;
+    const float2 u = tanh_exact(x, sc);
+    t.x = fabsf(x.x) <= sc.small ? t.x : u.x;
+    t.y = fabsf(x.y) <= sc.small ? t.y : u.y;
   }
-  return y;
+  return t;
 }
 
 // A row against the keys of a block, column c at distance d0 + c (key - row).  Its
@@ -88,15 +87,16 @@ __device__ __forceinline__ float2 score2(float2 x, const ScoreParams& sc, float2
 // the row (`fixed`), which joins minus the maximum.  (Causal calls: what lies behind
 // the row is hidden, and a block counts as one at or before it.)
 struct RowBias {
-  float slope;  // s_h (0: no bias)
-  float s;      // of a one-sided block; 0 in one on both sides
-  float fixed;  // s d0
+  float slope;  // s_h (0: no bias), in the call's unit
+  float s;      // the same with its sign, of a one-sided block; 0 in one on both sides
+  float fixed;  // s d0, base 2
   int d0;
   bool both;
 };
-__device__ __forceinline__ RowBias row_bias(float slope, int d0, bool left, bool right) {
+// slope: s_h in the call's unit.
+__device__ __forceinline__ RowBias row_bias(const ScoreParams& sc, float slope, int d0, bool left, bool right) {
   const float s = left ? slope : (right ? -slope : 0.f);
-  return RowBias{slope, s, s * static_cast<float>(d0), d0, !left && !right};
+  return RowBias{slope, s, s * static_cast<float>(d0) * sc.unit, d0, !left && !right};
 }
 
 // Columns [lo, hi) of 32 as bits.
@@ -115,11 +115,11 @@ struct PlainCols {
   __device__ __forceinline__ int off(int c) const { return c; }
 };
 
-// The scores of a block, less the row's constant, in two forms that agree to the bit
-// where both apply.  In registers, for warps whose block is one-sided and (under a
-// cap) all small:
+// The scores of a block in the call's unit, less the row's constant, in two forms that
+// agree to the bit where both apply.  In registers, for warps whose block is one-sided
+// and (under a cap) all small, and a sensible scale:
 template <int N>
-__device__ __forceinline__ void scores_fast(uint32_t* sr, const ScoreParams& sc, float2 c2, float s) {
+__device__ __forceinline__ void scores_fast(uint32_t* sr, const ScoreParams& sc, float s) {
   // (The bias of a column takes its number as an immediate: one scalar FMA.  Packed, the
   // pair of numbers is two moves on top.)
   auto each = [&](auto form, bool biased) {
@@ -131,14 +131,14 @@ __device__ __forceinline__ void scores_fast(uint32_t* sr, const ScoreParams& sc,
       sr[c + 1] = __float_as_uint(y.y);
     }
   };
-  auto plain = [&](float2 x) { return score2<kNoCap>(x, sc, c2); };
-  auto capped = [&](float2 x) { return score2<kCapSmall>(x, sc, c2); };
+  auto capped = [&](float2 x) { return tanh2<kCapSmall>(x, sc); };
+  // (Which form stands first is felt: a capped block without a bias is 2 % faster here
+  // than behind the others, a biased one without a cap 1 to 4 % slower.)
   if (sc.slopes == nullptr) {
-    if (sc.cap == 0.f) each(plain, false);
-    else each(capped, false);
+    if (sc.cap != 0.f) each(capped, false);
   } else {
-    if (sc.cap == 0.f) each(plain, true);
-    else each(capped, true);
+    if (sc.cap != 0.f) each(capped, true);
+    else each([](float2 x) { return x; }, true);
   }
 }
 // And for any block: from TMEM (column t_s on) and back to it, 16 columns at a time in
@@ -146,20 +146,21 @@ __device__ __forceinline__ void scores_fast(uint32_t* sr, const ScoreParams& sc,
 // over a block's columns, beside the fast form, it made the warps wait for
 // instructions most of the time (causal B2 H16/4 S4096 D128, capped: 1410 us).
 template <int N, typename Cols>
-__device__ __forceinline__ void scores_slow(uint32_t t_s, const ScoreParams& sc, float2 c2, const RowBias& r,
-                                            const Cols& cols) {
+__device__ __forceinline__ void scores_slow(uint32_t t_s, const ScoreParams& sc, const RowBias& r,
+                                            const Cols& cols, float back) {
 #pragma unroll 1
   for (int k0 = 0; k0 < N; k0 += 16) {
     uint32_t x16[16];
     ptx::tmem_ld16(t_s + k0, x16);
 #pragma unroll
     for (int c = 0; c < 16; c += 2) {
-      const float2 x = make_float2(__uint_as_float(x16[c]), __uint_as_float(x16[c + 1]));
-      float2 y = sc.cap != 0.f ? score2<kCapAny>(x, sc, c2) : score2<kNoCap>(x, sc, c2);
+      float2 y = make_float2(__uint_as_float(x16[c]), __uint_as_float(x16[c + 1]));
+      if (sc.cap != 0.f) y = tanh2<kCapAny>(y, sc);
+      else if (sc.pre != 0.f) y = __fmul2_rn(y, make_float2(sc.pre, sc.pre));
       if (sc.slopes != nullptr) {
         auto biased = [&](float v, int e) {
           if (r.both) return fmaf(-r.slope, fabsf(static_cast<float>(r.d0 + e)), v);
-          if (Cols::kOff && r.d0 + e > 0) return fmaf(-r.slope, static_cast<float>(e), v) - 2.f * r.fixed;
+          if (Cols::kOff && r.d0 + e > 0) return fmaf(-r.slope, static_cast<float>(e), v) - back;
           return fmaf(r.s, static_cast<float>(e), v);
         };
         y = make_float2(biased(y.x, cols.off(k0 + c)), biased(y.y, cols.off(k0 + c + 1)));
@@ -175,17 +176,18 @@ __device__ __forceinline__ void scores_slow(uint32_t t_s, const ScoreParams& sc,
 // A block's scores in place of the products that sr holds, loaded from column t_s on;
 // -inf where `cut` and the row does not see the key.
 template <int N, typename Cols>
-__device__ __forceinline__ void block_scores(uint32_t* sr, uint32_t t_s, const ScoreParams& sc, float2 c2,
+__device__ __forceinline__ void block_scores(uint32_t* sr, uint32_t t_s, const ScoreParams& sc,
                                              const RowBias& r, bool cut, const Cols& cols) {
   static_assert(N == 64 || N == 128, "block width");
-  const bool slow = (sc.slopes != nullptr && (r.both || Cols::kOff)) ||
+  const bool slow = sc.pre != 0.f || (sc.slopes != nullptr && (r.both || Cols::kOff)) ||
                     (sc.cap != 0.f && __any_sync(0xffffffffu, !(abs_max<N>(sr) <= sc.small)));
   if (slow) {
-    scores_slow<N>(t_s, sc, c2, r, cols);
+    // (a drafted key behind its row: -s d, less the constant s d0 that is added later)
+    scores_slow<N>(t_s, sc, r, cols, 2.f * r.fixed * sc.per_unit);
     if constexpr (N == 128) ptx::tmem_ld128(t_s, sr);
     else ptx::tmem_ld64(t_s, sr);
   } else {
-    scores_fast<N>(sr, sc, c2, r.s);
+    scores_fast<N>(sr, sc, r.s);
   }
   if (cut) {
 #pragma unroll
@@ -196,6 +198,12 @@ __device__ __forceinline__ void block_scores(uint32_t* sr, uint32_t t_s, const S
         sr[c0 + c] = seen >> c & 1u ? sr[c0 + c] : __float_as_uint(-INFINITY);
     }
   }
+}
+
+// Maximum of a block's scores, base 2.
+template <int N>
+__device__ __forceinline__ float block_top(const uint32_t* sr, const ScoreParams& sc) {
+  return block_max_scaled<N>(sr, false, 0, N, sc.unit, false);
 }
 
 // The order in which a forward CTA takes its key blocks [lo, ..).  A bias makes the
