@@ -205,7 +205,7 @@ __device__ __forceinline__ bool all_small(const uint32_t* xs, const ScoreParams&
 // What a thread of either pass knows of a block beside the products.
 struct ScoreBlock {
   float slope;   // s_h
-  int side;      // keys at or before their queries (-1), behind them (1), on both sides (0)
+  int side;      // keys at or before their queries (-1), behind them (1), on both sides or steep (0)
   int d0;        // distance key - query at the thread's first row and column
   bool edge;     // a mask cuts the block: the limits count
   int lo, hi;    // dQ pass: visible columns; dK/dV pass: see below
@@ -785,6 +785,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           const int key0 = KV_OUTER ? own0 : partner0, key1 = key0 + (KV_OUTER ? 127 : kPN - 1);
           const int row0 = KV_OUTER ? partner0 : own0, row1 = row0 + (KV_OUTER ? kPN - 1 : 127);
           sb.side = key1 <= row0 || (p.causal && pfx == 0) ? -1 : key0 >= row1 ? 1 : 0;
+          if (fabsf(sb.slope) > kSteep) sb.side = 0;  // each distance by itself, as in the forward
           if constexpr (KV_OUTER) {
             sb.edge = (partner0 < own0 + 127 - wr && pfx < own0 + 128) || partner0 + kPN - 1 > own0 + wl;
             sb.d0 = own0 + q4 * 32 - partner0 - col0;
@@ -793,8 +794,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             sb.pfx = pfx - partner0 - col0;
             grad_block_kv_scored<BF16>(tX, tY, lv, dv, p.sc, c2, sb);
           } else {
-            sb.edge = partner0 + kPN - 1 > max(own0 + wr, pfx - 1) || partner0 < own0 + 127 - wl ||
-                      (packed && partner0 + kPN > S);
+            // (A key past S is a row of zeros, but a bias that favours distance would give it
+            // an infinite P.)
+            sb.edge = partner0 + kPN - 1 > max(own0 + wr, pfx - 1) || partner0 < own0 + 127 - wl || partner0 + kPN > S;
             sb.hi = max(min(S - 1, my + wr), pfx - 1) - partner0 - col0;
             sb.lo = my - wl - partner0 - col0;
             sb.d0 = partner0 + col0 - my;

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(FwdRoles<SCORED>::kThreads, 1)
           drain_wait(&bar_kfull[x % L::kStagesK], (x / L::kStagesK) & 1, p.err);
         if (SCORED && x_clear >= 0 && x_clear < nv) drain_wait(bar_vtmp, 0, p.err);
         for (int x = (nv > L::kStagesV ? nv - L::kStagesV : 0); x < nv; ++x)
-          drain_wait(&bar_vfull[x % L::kStagesV], (x / L::kStagesV) & 1, p.err);
+          if (!SCORED || x != x_clear) drain_wait(&bar_vfull[x % L::kStagesV], (x / L::kStagesV) & 1, p.err);
       }
     } else if (warp == R::kMma0 || warp == R::kMma0 + 1) {
       // ------------------------------------------------------------ MMA issuers

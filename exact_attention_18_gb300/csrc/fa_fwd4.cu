@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         for (int x = (it > L::kStages ? it - L::kStages : 0); x < it; ++x) {
           const int st = x % L::kStages;
           drain_wait(&bar_kfull[st], (x / L::kStages) & 1, p.err);
-          drain_wait(&bar_vfull[st], (x / L::kStages) & 1, p.err);
+          if (!SCORED || x != x_clear) drain_wait(&bar_vfull[st], (x / L::kStages) & 1, p.err);
         }
       }
     } else if (warp >= kF4MmaWarp0 && warp < kF4MmaWarp0 + kF4MmaWarps) {

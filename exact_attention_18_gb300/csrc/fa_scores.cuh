@@ -86,17 +86,23 @@ __device__ __forceinline__ float2 tanh2(float2 x, const ScoreParams& sc) {
 // behind: in a block on one side of all of its tile's rows, s d0 is a constant of
 // the row (`fixed`), which joins minus the maximum.  (Causal calls: what lies behind
 // the row is hidden, and a block counts as one at or before it.)
+// The two parts are larger than their sum by up to a block's width of slopes, and so is
+// their rounding: under 2^-15 in all for slopes up to 1, about the product's own.
+// Steeper rows take each key's distance by itself, as blocks on both sides do: exact
+// for the keys next to the row, which are all that such a row weighs.
+constexpr float kSteep = 1.5f;  // base 2: a slope of 1.04
 struct RowBias {
   float slope;  // s_h (0: no bias), in the call's unit
-  float s;      // the same with its sign, of a one-sided block; 0 in one on both sides
+  float s;      // the same with its sign, of a one-sided block; 0 where `both`
   float fixed;  // s d0, base 2
   int d0;
-  bool both;
+  bool both;    // (of a warp's rows, some may be steep)
 };
 // slope: s_h in the call's unit.
 __device__ __forceinline__ RowBias row_bias(const ScoreParams& sc, float slope, int d0, bool left, bool right) {
-  const float s = left ? slope : (right ? -slope : 0.f);
-  return RowBias{slope, s, s * static_cast<float>(d0) * sc.unit, d0, !left && !right};
+  const bool both = (!left && !right) || fabsf(slope) * sc.unit > kSteep;
+  const float s = both ? 0.f : (left ? slope : -slope);
+  return RowBias{slope, s, s * static_cast<float>(d0) * sc.unit, d0, both};
 }
 
 // Columns [lo, hi) of 32 as bits.
@@ -179,7 +185,7 @@ template <int N, typename Cols>
 __device__ __forceinline__ void block_scores(uint32_t* sr, uint32_t t_s, const ScoreParams& sc,
                                              const RowBias& r, bool cut, const Cols& cols) {
   static_assert(N == 64 || N == 128, "block width");
-  const bool slow = sc.pre != 0.f || (sc.slopes != nullptr && (r.both || Cols::kOff)) ||
+  const bool slow = sc.pre != 0.f || (sc.slopes != nullptr && (Cols::kOff || __any_sync(0xffffffffu, r.both))) ||
                     (sc.cap != 0.f && __any_sync(0xffffffffu, !(abs_max<N>(sr) <= sc.small)));
   if (slow) {
     // (a drafted key behind its row: -s d, less the constant s d0 that is added later)
@@ -200,10 +206,11 @@ __device__ __forceinline__ void block_scores(uint32_t* sr, uint32_t t_s, const S
   }
 }
 
-// Maximum of a block's scores, base 2.
+// Maximum of a block's scores, base 2, rounded upwards: the exponentials' multiply-add
+// then gives no score above 0, however large a far key's bias and so their rounding.
 template <int N>
 __device__ __forceinline__ float block_top(const uint32_t* sr, const ScoreParams& sc) {
-  return block_max_scaled<N>(sr, false, 0, N, sc.unit, false);
+  return __fmul_ru(block_max_scaled<N>(sr, false, 0, N, 1.f, false), sc.unit);
 }
 
 // The order in which a forward CTA takes its key blocks [lo, ..).  A bias makes the

@@ -309,7 +309,8 @@ typedef struct {
  * its parts absent, runs fa_fwd_window.  The window's sides and `causal` hide keys
  * whatever the scores there are.  tanh is evaluated in fp32: beside the product's
  * own error a score is off by at most 2^-19 of itself, or by 2^-21 of cap.
- * Slopes must be finite and slopes[h] * S far below fp32's largest number.
+ * Slopes must be finite and slopes[h] * S far below fp32's largest number.  The
+ * bias is off by at most 2^-22 of itself, and by up to 2^-15 for slopes up to 1.
  */
 fa_status fa_fwd_scores(const void* q, const void* k, const void* v, void* o, float* lse, int64_t B, int64_t H,
                         int64_t H_kv, int64_t S, int64_t D, int causal, int64_t window_left, int64_t window_right,
@@ -537,7 +538,8 @@ fa_status fa_fwd_paged_scores(const void* q, void* o, float* lse, const fa_paged
  *   positions   : DEVICE int32 [T], where each new token stands in its sequence
  *                 (f plus its depth, as a rule): the window's and the bias's i,
  *                 and the bias's j of a new token as a key.  Held to
- *                 [f, kv_lens[b] - 1].
+ *                 [f, kv_lens[b] - 1].  (With kv_lens[b] < n the first new
+ *                 tokens, which would stand before key 0, are no keys.)
  *   tree        : DEVICE uint32, the rows of the T new tokens, tree_stride words
  *                 apart; tree_words (at most tree_stride) words of a row are
  *                 used, 32 * tree_words >= min(max_seqlen_q, total).  Bits past a
