@@ -3,6 +3,16 @@
 //   P = exp(S' - L),  dS' = P o (dP - Delta),  dS = dS' o (1 - t^2),
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
 // The bias is a constant of the call: it enters P alone.
+//
+// Roundings to 16 bits, as in the plain backward: P and dS as operands (half a step of
+// each), the stored O that Delta is taken from, the results.  With scores far apart P
+// is near 1 and dP - Delta a difference of like numbers, so the error of O in Delta is
+// the largest part of dQ's and dK's.
+//
+// What bounds it (causal B1 H16/4 S4096 D128 bf16, capped): 159 us for the dK/dV pass
+// and 120 for the dQ pass, tensor pipes 39 % active, instructions issued 44 %: the
+// products of a block wait for its scores' arithmetic and the other way round, two
+// groups of eight warps apart.  D = 64 with a bias (H16 fp16): 86 and 66 us, issue 63 %.
 #include "fa_bwd_main.cuh"
 
 namespace fa {

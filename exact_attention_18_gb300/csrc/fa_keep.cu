@@ -12,7 +12,8 @@
 // What bounds it: latency.  A few rows a sequence are 0.1 to 3 MB in all; the chain
 // offsets -> path -> block table -> row -> store and the launch are the time.  The
 // loads of a batch are independent, and the grid starts as a programmatic dependent
-// of the kernel before it.
+// of the kernel before it.  48 sequences that keep up to 9 of 64 tokens, 8 heads of 128:
+// 3.8 us in a stream of calls (1.2 MB: 0.4 us at the copy rate); one sequence 2.8.
 #include "fa_kernel_common.cuh"
 #include "fa_paged.cuh"
 

@@ -44,6 +44,11 @@
 // window) may hold anything: their scores are never used, and their V rows
 // are set to zero in shared memory, since 0 * NaN in the second product would
 // not be 0.
+//
+// P = PagedScoredParams: modified scores (fa_scores.cuh) and trees of drafted tokens.
+// A thread's key has one position and one bit a row, so both are a few instructions a
+// score; decoding 32 sequences of 5000 keys, 32 heads on 4 of 128: 59 us plain, 63
+// capped, 60 with a bias, 62 as trees with both.
 #pragma once
 
 #include "fa_paged_units.cuh"
