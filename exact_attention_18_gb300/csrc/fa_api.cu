@@ -236,7 +236,7 @@ fa_status encode_input(CUtensorMap* map, const void* base, bool bf16, const Shap
 // of degree 5, by Remez exchange; relative error 1.5e-6, 1.6e-6 with fp32's roundings);
 // with v = scale x / cap it becomes tanh(v) = x * sum_k poly[k] x^(2k).
 // Coefficients that leave fp32's normal range bound the |x| it is used for: below it
-// to where the terms left out are under 2^-22 of the value, above it to 0.
+// to where the terms left out are under 2^-22 of the value, above it to none.
 // Range and degree were measured (us; scores of deviation 4 under 50 B2 H32/4 S4096
 // D128, of 8 under 30 B7 H16/2 up to 2500 D64): degree 5 to 1.0 334, 172; degree 6 to
 // 1.25 353, 129; a block that holds a score beyond takes the longer way.
@@ -250,14 +250,14 @@ void tanh_poly(float scale, float cap, fa::ScoreParams* p) {
   for (int k = 0; k < fa::kTanhTerms; ++k, f *= in * in) {
     p->poly[k] = static_cast<float>(kC[k] * f);
     const double size = std::fabs(kC[k] * f);
-    if (size > 1e37) vmax = 0;
+    if (size > 1e37) vmax = -1;  // no score is small, 0 neither: 0 * inf
     if (k > 0 && size < 1e-37) {
       p->poly[k] = 0.f;
       vmax = std::fmin(vmax, std::pow(2.4e-7 / (2 * std::fabs(kC[k])), 1.0 / (2 * k)));
     }
   }
   const double small = in == 0 ? 1e18 : std::fmin(vmax / std::fabs(in), 1e18);
-  p->small = static_cast<float>(small);
+  p->small = vmax < 0 ? -1.f : static_cast<float>(small);
 }
 
 // Modified scores of a call; *on: they need their own kernels.  (A packed call that

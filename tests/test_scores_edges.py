@@ -360,6 +360,55 @@ def test_steep_slopes_in_a_cache(fa, D):
             inside(lb[h], r["lse"], tol_l, f"L b={b} h={h}")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [1e-10, 1e-4, 1e10])
+def test_ends_of_the_cap(fa, D, cap):
+    """The smallest and largest caps, products of 0 among them: scores of +-cap and 0, or as without one."""
+    q, k, v, do = (rnd((1, 2, 170, D), i, torch.float16) for i in range(4))
+    q[:, :, ::7] = 0
+    kw = dict(causal=True, softcap=cap)
+    g = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.forward(*g[:3], **kw)
+    grads = fa.backward(*g[:3], o, g[3], lse, **kw)
+    tr = lambda x: x[0].cpu().transpose(0, 1)  # noqa: E731
+    check_sequence(tr(q), tr(k), tr(v), tr(do), tr(o), lse[0].cpu(), [tr(x) for x in grads], True, None, 0, cap, None,
+                   D ** -0.5)
+    kc, vc, table, cu = paged_setup([170], [40], 2, D, 16, torch.float16, 5)
+    kg, vg = on_gpu(kc, vc)
+    qp = tr(q)[-40:].contiguous()
+    at = paged.slots(table[0], torch.arange(170), 16)
+    kk, vv = kc.reshape(-1, 2, D)[at], vc.reshape(-1, 2, D)[at]
+    for n in (40, 2):
+        o, lse = fa.forward_paged(qp[-n:].cuda(), kg, vg, ints(table), ints([170]), ints([0, n]), n, 170, softcap=cap)
+        i, j = torch.arange(170 - n, 170), torch.arange(170)
+        rs = modified.sequence(qp[-n:], kk, vv, j[None, :] <= i[:, None], i, j, D ** -0.5, cap, None)
+        for h, r in enumerate(rs):
+            tol_o, tol_l, _ = forward_bounds(r, qp[-n:, h], kk[:, h], vv[:, h], D ** -0.5, cap, torch.float16)
+            inside(o[:, h], r["o"], tol_o, f"O h={h}")
+            inside(lse[h], r["lse"], tol_l, f"L h={h}")
+    assert fa.fa_check_device_errors(None) == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cu", [[0, 100, 400], [0, 300, 200, 400], [0, 100, 900], [-4, 100, 200]])
+def test_offsets_that_contradict_the_call(fa, D, cu):
+    """A sample longer than the bound, decreasing offsets, offsets out of the batch: reported, nothing read or
+    written out of range, and the next call is right."""
+    q, k, v, do = (rnd((400, 2, D), i, torch.float16).cuda() for i in range(4))
+    kw = dict(causal=True, softcap=9.0, slopes=alibi(2).cuda())
+    good = ints([0, 150, 400])
+    o, lse = fa.forward_varlen(q, k, v, good, 250, **kw)
+    grads = fa.backward_varlen(q, k, v, o, do, lse, good, 250, **kw)
+    fa.forward_varlen(q, k, v, ints(cu), 250, **kw)
+    assert fa.STATUS[fa.fa_check_device_errors(None)] == "FA_ERR_INVALID_ARG"
+    fa.backward_varlen(q, k, v, o, do, lse, ints(cu), 250, **kw)
+    assert fa.STATUS[fa.fa_check_device_errors(None)] == "FA_ERR_INVALID_ARG"
+    o2, lse2 = fa.forward_varlen(q, k, v, good, 250, **kw)
+    grads2 = fa.backward_varlen(q, k, v, o, do, lse, good, 250, **kw)
+    assert fa.fa_check_device_errors(None) == 0
+    assert all(torch.equal(a, b) for a, b in zip((o, lse, *grads), (o2, lse2, *grads2)))
+
+
 def test_empty_calls(fa):
     e = lambda *s: torch.empty(*s, dtype=torch.float16, device="cuda")  # noqa: E731
     for shape in ((0, 2, 10, 64), (1, 2, 0, 64)):
