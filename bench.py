@@ -50,15 +50,16 @@ WORKLOADS = ("c2", "c4", "c5", "leaderboard", "gqa", "mqa", "varlen", "window", 
 FLUSH_BYTES = 256 << 20  # > 129 MB L2
 _CSRC = "exact_attention_18_gb300/csrc/"
 _COMMON = [_CSRC + f for f in ("fa_kernel_common.cuh", "sm103_ptx.cuh", "fa_internal.cuh")]
+_BWD = [_CSRC + f for f in ("fa_bwd.cu", "fa_bwd_main.cuh", "fa_scores.cuh", "fa_softmax.cuh")] + _COMMON
 # The sources each kernel is compiled from: a committed ncu traffic figure is used only while
 # these are unchanged since its capture.
 KERNEL_SOURCES = {
-    "fa_fwd4_kernel": [_CSRC + "fa_fwd4.cu", _CSRC + "fa_softmax.cuh"] + _COMMON,
+    "fa_fwd4_kernel": [_CSRC + f for f in ("fa_fwd4.cu", "fa_scores.cuh", "fa_softmax.cuh")] + _COMMON,
     "fa_fwd4p_kernel": [_CSRC + "fa_fwd4p.cu", _CSRC + "fa_softmax.cuh"] + _COMMON,
-    "fa_fwd_kernel": [_CSRC + "fa_fwd.cu", _CSRC + "fa_softmax.cuh"] + _COMMON,
-    "fa_bwd_preprocess_kernel": [_CSRC + "fa_bwd.cu"] + _COMMON,
-    "fa_bwd_dkdv_kernel": [_CSRC + "fa_bwd.cu"] + _COMMON,
-    "fa_bwd_dq_kernel": [_CSRC + "fa_bwd.cu"] + _COMMON,
+    "fa_fwd_kernel": [_CSRC + f for f in ("fa_fwd.cu", "fa_scores.cuh", "fa_softmax.cuh")] + _COMMON,
+    "fa_bwd_preprocess_kernel": _BWD,
+    "fa_bwd_dkdv_kernel": _BWD,
+    "fa_bwd_dq_kernel": _BWD,
 }
 
 
