@@ -44,8 +44,8 @@
 // batches with either.  Sixteen softmax warps, two threads a row, and each block's
 // maximum ahead of its exponentials.  What bounds it is the softmax warps' work: a
 // capped block takes 12 warp instructions for 32 scores, issued 51 % of the time, the
-// tensor pipes 35 % active (causal B2 H16/4 S4096 bf16, 176 us: 0.78 PFLOP/s; with a
-// bias 144, windowed without either 171).
+// tensor pipes 35 % active (causal B2 H32/4 S4096 bf16, 339 us: 0.81 PFLOP/s; B1 167, with a
+// bias 141, windowed without either 171).
 #include "fa_scores.cuh"
 #include "fa_softmax.cuh"
 
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(FwdRoles<SCORED>::kThreads, 1)
   int beg1 = hi1 > lo1 ? lo1 : 0, end1 = hi1 > lo1 ? hi1 : 0;
   BlockOrder ord{kb_cta, kb_cta};
   if constexpr (SCORED) {
-    ord = block_order(true, kb_cta, kb_cta + max(end0, end1), wl == kNoWindow,
+    ord = block_order(kb_cta, kb_cta + max(end0, end1), wl == kNoWindow,
                       (min(S, row0 + 2 * kBlockM) - 1) / kBlockN + 1);
     ord.span(kb_cta + lo0, kb_cta + hi0, &beg0, &end0);
     if (row0 + kBlockM < S) ord.span(kb_cta + lo1, kb_cta + hi1, &beg1, &end1);

@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   // (SCORED: in the order that `ord` gives; the x-th block loaded is block_at(x))
   BlockOrder ord{kb_cta, kb_cta};
   if constexpr (SCORED)
-    ord = block_order(p.sc.slopes != nullptr, kb_cta, kb_cta + nbp, wl == kNoWindow, (min(S, row0 + kF4RowsPerCta) - 1) / kBN + 1);
+    ord = block_order(kb_cta, kb_cta + nbp, wl == kNoWindow,
+                      (min(S, row0 + kF4RowsPerCta) - 1) / kBN + 1);
   auto block_at = [&](int x) -> int {
     if constexpr (SCORED) return ord.at(x);
     else return kb_cta + x;

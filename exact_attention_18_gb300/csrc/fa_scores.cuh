@@ -216,10 +216,10 @@ __device__ __forceinline__ float block_top(const uint32_t* sr, const ScoreParams
 // The order in which a forward CTA takes its key blocks [lo, ..).  A bias makes the
 // keys next to a row its largest scores: from there outwards the running maximum
 // hardly moves, while towards them it moves, and O is rescaled, at every block.  So
-// with a bias the blocks up to `split` come first, downwards, then those behind,
-// upwards; else all upwards (split = lo).  Upwards / downwards (us, causal): biased
-// D = 128 (B1 H32/4 S4096) 147 / 140, D = 64 (B2 H16 S4096) 109 / 107; capped D = 128
-// 176 / 166, so there always downwards, D = 64 140 / 140, two K/V heads 108 / 111.
+// the blocks up to `split` come first, downwards, then those behind, upwards.  All
+// upwards / so (us, causal S4096): biased D = 128 (B1 H32/4) 158 / 141, D = 64 (B2 H16)
+// 106 / 93; capped, where the blocks that a mask cuts then come while others still
+// load, 178 / 167 and 136 / 134.
 struct BlockOrder {
   int lo, split;
   __device__ __forceinline__ int at(int x) const { return x < split - lo ? split - 1 - x : lo + x; }
@@ -238,8 +238,7 @@ struct BlockOrder {
 };
 // Of blocks [lo, hi); `diag`: the block after that of the CTA's last row; `open`: the
 // window has no left side, so every tile starts at lo.
-__device__ __forceinline__ BlockOrder block_order(bool downwards, int lo, int hi, bool open, int diag) {
-  if (!downwards) return BlockOrder{lo, lo};
+__device__ __forceinline__ BlockOrder block_order(int lo, int hi, bool open, int diag) {
   return BlockOrder{lo, open ? max(lo, min(hi, diag)) : hi};
 }
 
