@@ -157,13 +157,14 @@ struct TreeCols {
     }
   }
   __device__ __forceinline__ unsigned word(int c0) const { return seen[c0 / 32]; }
-  // (all lanes ask for the same column)
-  __device__ __forceinline__ int off(int c) const {
+  __device__ __forceinline__ int group(int k0) const {
     int v = at[0];
 #pragma unroll
-    for (int x = 1; x < N / 32; ++x) v = c / 32 == x ? at[x] : v;
-    return __shfl_sync(0xffffffffu, v, c & 31);
+    for (int x = 1; x < N / 32; ++x) v = k0 / 32 == x ? at[x] : v;
+    return v;
   }
+  // (all lanes ask for the same column)
+  __device__ __forceinline__ int off(int grp, int c) const { return __shfl_sync(0xffffffffu, grp, c & 31); }
 };
 
 }  // namespace

@@ -113,12 +113,13 @@ __device__ __forceinline__ unsigned bit_range(int lo, int hi) {
 }
 
 // Which columns of a block a row sees: lo .. lim.  off: where column c's key stands,
-// less the block's first key.
+// less the block's first key (group: what it needs to know of 16 columns).
 struct PlainCols {
   int lo, lim;
   static constexpr bool kOff = false;
   __device__ __forceinline__ unsigned word(int c0) const { return bit_range(lo - c0, lim + 1 - c0); }
-  __device__ __forceinline__ int off(int c) const { return c; }
+  __device__ __forceinline__ int group(int) const { return 0; }
+  __device__ __forceinline__ int off(int, int c) const { return c; }
 };
 
 // The scores of a block in the call's unit, less the row's constant, in two forms that
@@ -153,15 +154,16 @@ __device__ __forceinline__ void scores_fast(uint32_t* sr, const ScoreParams& sc,
 // instructions most of the time (causal B2 H16/4 S4096 D128, capped: 1410 us).
 template <int N, typename Cols>
 __device__ __forceinline__ void scores_slow(uint32_t t_s, const ScoreParams& sc, const RowBias& r,
-                                            const Cols& cols, float back) {
+                                            const Cols& cols, float back, bool large) {
 #pragma unroll 1
   for (int k0 = 0; k0 < N; k0 += 16) {
     uint32_t x16[16];
     ptx::tmem_ld16(t_s + k0, x16);
+    const int grp = cols.group(k0);
 #pragma unroll
     for (int c = 0; c < 16; c += 2) {
       float2 y = make_float2(__uint_as_float(x16[c]), __uint_as_float(x16[c + 1]));
-      if (sc.cap != 0.f) y = tanh2<kCapAny>(y, sc);
+      if (sc.cap != 0.f) y = Cols::kOff && !large ? tanh2<kCapSmall>(y, sc) : tanh2<kCapAny>(y, sc);
       else if (sc.pre != 0.f) y = __fmul2_rn(y, make_float2(sc.pre, sc.pre));
       if (sc.slopes != nullptr) {
         auto biased = [&](float v, int e) {
@@ -169,7 +171,7 @@ __device__ __forceinline__ void scores_slow(uint32_t t_s, const ScoreParams& sc,
           if (Cols::kOff && r.d0 + e > 0) return fmaf(-r.slope, static_cast<float>(e), v) - back;
           return fmaf(r.s, static_cast<float>(e), v);
         };
-        y = make_float2(biased(y.x, cols.off(k0 + c)), biased(y.y, cols.off(k0 + c + 1)));
+        y = make_float2(biased(y.x, cols.off(grp, k0 + c)), biased(y.y, cols.off(grp, k0 + c + 1)));
       }
       x16[c] = __float_as_uint(y.x);
       x16[c + 1] = __float_as_uint(y.y);
@@ -185,11 +187,12 @@ template <int N, typename Cols>
 __device__ __forceinline__ void block_scores(uint32_t* sr, uint32_t t_s, const ScoreParams& sc,
                                              const RowBias& r, bool cut, const Cols& cols) {
   static_assert(N == 64 || N == 128, "block width");
-  const bool slow = sc.pre != 0.f || (sc.slopes != nullptr && (Cols::kOff || __any_sync(0xffffffffu, r.both))) ||
-                    (sc.cap != 0.f && __any_sync(0xffffffffu, !(abs_max<N>(sr) <= sc.small)));
+  const bool large = sc.cap != 0.f && __any_sync(0xffffffffu, !(abs_max<N>(sr) <= sc.small));
+  const bool slow =
+      large || sc.pre != 0.f || (sc.slopes != nullptr && (Cols::kOff || __any_sync(0xffffffffu, r.both)));
   if (slow) {
     // (a drafted key behind its row: -s d, less the constant s d0 that is added later)
-    scores_slow<N>(t_s, sc, r, cols, 2.f * r.fixed * sc.per_unit);
+    scores_slow<N>(t_s, sc, r, cols, 2.f * r.fixed * sc.per_unit, large);
     if constexpr (N == 128) ptx::tmem_ld128(t_s, sr);
     else ptx::tmem_ld64(t_s, sr);
   } else {
