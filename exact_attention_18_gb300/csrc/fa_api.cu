@@ -238,8 +238,9 @@ fa_status encode_input(CUtensorMap* map, const void* base, bool bf16, const Shap
 // Coefficients that leave fp32's normal range bound the |x| it is used for: below it
 // to where the terms left out are under 2^-22 of the value, above it to none.
 // Range and degree were measured (us; scores of deviation 4 under 50 B2 H32/4 S4096
-// D128, of 8 under 30 B7 H16/2 up to 2500 D64): degree 5 to 1.0 334, 172; degree 6 to
-// 1.25 353, 129; a block that holds a score beyond takes the longer way.
+// D128, of 8 under 30 B7 H16/2 up to 2500 D64): degree 5 to 1.05 (9.5e-7) 335, 157, to
+// 1.1 340, 143; degree 6 to 1.25 5 % more, 10 % less.  A block that holds a score beyond
+// takes the longer way.
 void tanh_poly(float scale, float cap, fa::ScoreParams* p) {
   constexpr double kC[fa::kTanhTerms] = {0.99999849, -0.33324176, 0.13241123, -0.050452815, 0.015411088, -0.0025325383};
   constexpr double kMax = 1.1;
@@ -269,7 +270,8 @@ fa_status check_scores(const fa_scores* in, float scale, bool prefix_ok, bool pa
   const float scale_log2 = scale * kLog2e;
   const bool by_scale = scale_log2 >= 1e-4f;
   out->unit = by_scale ? scale_log2 : 1.f;
-  out->pre = by_scale ? 0.f : scale_log2;
+  out->pre = scale_log2;
+  out->premul = by_scale ? 0 : 1;
   out->per_unit = 1.f / out->unit;
   if (!in) return FA_OK;
   if (!std::isfinite(in->softcap) || in->softcap < 0)
@@ -283,7 +285,7 @@ fa_status check_scores(const fa_scores* in, float scale, bool prefix_ok, bool pa
       return fail(FA_ERR_UNSUPPORTED, "softcap must be between 1e-10 and 1e10, and scale / softcap finite");
     tanh_poly(scale, in->softcap, out);
     out->unit = out->cap;
-    out->pre = 0.f;
+    out->premul = 0;
     out->per_unit = 1.f / out->unit;
   }
   out->slopes = in->slopes;

@@ -76,7 +76,8 @@ struct ScoreParams {
   // are the products as they come.  A scale that is no sensible unit (negative, 0,
   // tiny) is multiplied in beforehand instead.
   float unit, per_unit;  // base 2; its reciprocal
-  float pre;             // factor of the products beforehand; 0: none
+  float pre;             // factor of the products beforehand,
+  int premul;            // if there is one
   float in2;            // 2 log2 e scale / cap: e^(2v) = 2^(in2 x), v = scale x / cap
   float small;          // |x| up to which the polynomial gives tanh(v)
   float poly[kTanhTerms];  // its coefficients, of x^(2k + 1)

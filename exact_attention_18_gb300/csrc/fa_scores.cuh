@@ -164,7 +164,7 @@ __device__ __forceinline__ void scores_slow(uint32_t t_s, const ScoreParams& sc,
     for (int c = 0; c < 16; c += 2) {
       float2 y = make_float2(__uint_as_float(x16[c]), __uint_as_float(x16[c + 1]));
       if (sc.cap != 0.f) y = Cols::kOff && !large ? tanh2<kCapSmall>(y, sc) : tanh2<kCapAny>(y, sc);
-      else if (sc.pre != 0.f) y = __fmul2_rn(y, make_float2(sc.pre, sc.pre));
+      else if (sc.premul) y = __fmul2_rn(y, make_float2(sc.pre, sc.pre));
       if (sc.slopes != nullptr) {
         auto biased = [&](float v, int e) {
           if (r.both) return fmaf(-r.slope, fabsf(static_cast<float>(r.d0 + e)), v);
@@ -189,7 +189,7 @@ __device__ __forceinline__ void block_scores(uint32_t* sr, uint32_t t_s, const S
   static_assert(N == 64 || N == 128, "block width");
   const bool large = sc.cap != 0.f && __any_sync(0xffffffffu, !(abs_max<N>(sr) <= sc.small));
   const bool slow =
-      large || sc.pre != 0.f || (sc.slopes != nullptr && (Cols::kOff || __any_sync(0xffffffffu, r.both)));
+      large || sc.premul || (sc.slopes != nullptr && (Cols::kOff || __any_sync(0xffffffffu, r.both)));
   if (slow) {
     // (a drafted key behind its row: -s d, less the constant s d0 that is added later)
     scores_slow<N>(t_s, sc, r, cols, 2.f * r.fixed * sc.per_unit, large);

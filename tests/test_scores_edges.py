@@ -232,6 +232,14 @@ def test_ends_of_ranges(fa, D):
     fixed_case(fa, 1, 2, 1, 150, D, "bf16", scale=-1e-3, bias=True, causal=False)
 
 
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("scale", [None, 0.0, -0.2])
+def test_prefix_alone(fa, D, scale):
+    """Plain scores under a prefix, forward and backward; scales that no unit can be made of."""
+    fixed_case(fa, 2, 4, 2, 300, D, "fp16", prefix=170, scale=scale)
+    fixed_case(fa, 1, 2, 1, 200, D, "bf16", prefix=65, window=(50, 0), scale=scale)
+
+
 def test_long_rows(fa):
     """More keys than a tile's CTA holds at once, and distances past 2^13."""
     fixed_case(fa, 1, 2, 1, 8300, 64, "fp16", bias=True, softcap=30.0, window=(8200, 0), backward=False)
