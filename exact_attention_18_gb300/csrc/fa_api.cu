@@ -466,6 +466,7 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, c
   };
   const bool fused_delta = fa::bwd_dq_computes_delta(Di, general);
   // Delta then dK/dV then dQ; or, when the dQ kernel computes Delta, dQ then dK/dV.
+  // With modified scores Delta, dQ (which makes it exact), dK/dV.
   if ((st = mark(0))) return st;
   if (fused_delta) {
     if ((st = from_cuda(pass(false, false), "backward dQ launch"))) return st;
@@ -473,6 +474,7 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, c
     return st;
   }
   if ((st = mark(1))) return st;
+  if (scored && (st = from_cuda(pass(false, true), "backward dQ launch"))) return st;
   // The second and third kernels are programmatic dependent launches: their
   // first CTAs start as the previous kernel's last ones finish.
   if ((st = from_cuda(pass(true, true), "backward dK/dV launch"))) return st;
@@ -480,7 +482,7 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, c
       (st = from_cuda(fa::launch_bwd_dkv_reduce(Di, bf16, p, kv_rows, s), "backward dK/dV reduce launch")))
     return st;
   if ((st = mark(2))) return st;
-  if (!fused_delta && (st = from_cuda(pass(false, true), "backward dQ launch"))) return st;
+  if (!fused_delta && !scored && (st = from_cuda(pass(false, true), "backward dQ launch"))) return st;
   return mark(3);
 }
 

@@ -215,10 +215,11 @@ struct ScoreBlock {
 // grad_block (dQ pass) with modified scores: 16 columns whose products xs, ys are in
 // registers.  FAST: blocks that no mask cuts, on one side of their queries, whose
 // scores are all small (F = kCapSmall); the others have the same arithmetic.
+// Beside dS it gives P o f, and adds P o dP to `sum` (see the kernel).
 template <bool BF16, bool FAST, CapForm F, bool BIAS>
-__device__ __forceinline__ void grad16_scored(const uint32_t* xs, const uint32_t* ys, uint32_t* dk, int h,
-                                              const ScoreParams& sc, float2 c2, float my_l2, float my_delta,
-                                              const ScoreBlock& sb) {
+__device__ __forceinline__ void grad16_scored(const uint32_t* xs, const uint32_t* ys, uint32_t* pk, uint32_t* dk,
+                                              int h, const ScoreParams& sc, float2 c2, float my_l2, float my_delta,
+                                              const ScoreBlock& sb, float2& sum) {
   // Column cc's bias is s cc + s d0; the latter joins -L.
   const float s = sb.side > 0 ? -sb.slope : sb.slope;
   const float nb = BIAS ? fmaf(s, static_cast<float>(sb.d0 + 16 * h), -my_l2) : -my_l2;
@@ -238,29 +239,33 @@ __device__ __forceinline__ void grad16_scored(const uint32_t* xs, const uint32_t
       if (cc < sb.lo || cc > sb.hi) pr.x = 0.f;
       if (cc + 1 < sb.lo || cc + 1 > sb.hi) pr.y = 0.f;
     }
-    const float2 gr = __fadd2_rn(make_float2(__uint_as_float(ys[c]), __uint_as_float(ys[c + 1])),
-                                 make_float2(-my_delta, -my_delta));
-    float2 ds = __fmul2_rn(pr, gr);
-    if constexpr (F != kNoCap) ds = __fmul2_rn(ds, f);
+    const float2 dp = make_float2(__uint_as_float(ys[c]), __uint_as_float(ys[c + 1]));
+    const float2 gr = __fadd2_rn(dp, make_float2(-my_delta, -my_delta));
+    sum = __ffma2_rn(pr, dp, sum);
+    if constexpr (F != kNoCap) pr = __fmul2_rn(pr, f);
+    const float2 ds = __fmul2_rn(pr, gr);
+    pk[c / 2] = pack2<BF16>(pr.x, pr.y);
     dk[c / 2] = pack2<BF16>(ds.x, ds.y);
   }
 }
 
 template <bool BF16>
 __device__ __forceinline__ void grad_block_scored(uint32_t tX, uint32_t tY, const ScoreParams& sc, float2 c2,
-                                                  float my_l2, float my_delta, const ScoreBlock& sb) {
+                                                  float my_l2, float my_delta, const ScoreBlock& sb, float2& sum) {
   const bool capped = sc.cap != 0.f, biased = sc.slopes != nullptr;
   // The whole of X first: which form the block takes, and the products of both halves.
-  uint32_t xs[32], ys[16], dk[8];
+  uint32_t xs[32], ys[16], pk[8], dk[8];
   const bool fast = !sb.edge && (sb.side != 0 || !biased);
   tmem_ld32(tX, xs);
   if (fast && (!capped || all_small<32>(xs, sc))) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       tmem_ld16(tY + 16 * h, ys);
-      if (!capped) grad16_scored<BF16, true, kNoCap, true>(xs + 16 * h, ys, dk, h, sc, c2, my_l2, my_delta, sb);
-      else if (biased) grad16_scored<BF16, true, kCapSmall, true>(xs + 16 * h, ys, dk, h, sc, c2, my_l2, my_delta, sb);
-      else grad16_scored<BF16, true, kCapSmall, false>(xs + 16 * h, ys, dk, h, sc, c2, my_l2, my_delta, sb);
+      const uint32_t* x = xs + 16 * h;
+      if (!capped) grad16_scored<BF16, true, kNoCap, true>(x, ys, pk, dk, h, sc, c2, my_l2, my_delta, sb, sum);
+      else if (biased) grad16_scored<BF16, true, kCapSmall, true>(x, ys, pk, dk, h, sc, c2, my_l2, my_delta, sb, sum);
+      else grad16_scored<BF16, true, kCapSmall, false>(x, ys, pk, dk, h, sc, c2, my_l2, my_delta, sb, sum);
+      tmem_st8(tX + 8 * h, pk);
       tmem_st8(tY + 8 * h, dk);
     }
     return;
@@ -269,8 +274,9 @@ __device__ __forceinline__ void grad_block_scored(uint32_t tX, uint32_t tY, cons
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     tmem_ld16x2(tX + 16 * h, xs, tY + 16 * h, ys);
-    if (capped) grad16_scored<BF16, false, kCapAny, true>(xs, ys, dk, h, sc, c2, my_l2, my_delta, sb);
-    else grad16_scored<BF16, false, kNoCap, true>(xs, ys, dk, h, sc, c2, my_l2, my_delta, sb);
+    if (capped) grad16_scored<BF16, false, kCapAny, true>(xs, ys, pk, dk, h, sc, c2, my_l2, my_delta, sb, sum);
+    else grad16_scored<BF16, false, kNoCap, true>(xs, ys, pk, dk, h, sc, c2, my_l2, my_delta, sb, sum);
+    tmem_st8(tX + 8 * h, pk);
     tmem_st8(tY + 8 * h, dk);
   }
 }
@@ -520,7 +526,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t sB2 = smem_u32(smem + L::kOffB2);
   // The dQ pass after the dK/dV pass may start its CTAs as this grid's last
   // ones run; it reads nothing this pass writes before its griddep_wait.
-  if constexpr (KV_OUTER) griddep_launch_dependents();
+  // (SCORED: the other way round; the dK/dV pass reads the dQ pass's Delta.)
+  if constexpr (KV_OUTER || SCORED) griddep_launch_dependents();
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
@@ -628,7 +635,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const uint64_t a1_desc = make_sdesc(sA1, 16, 8 * GA::kRowBytes, GA::kSwz);
       const uint64_t a2_desc = make_sdesc(sA2, 16, 8 * GA::kRowBytes, GA::kSwz);
       ok = warp_wait(bar_afull, 0, abort_flag, p.err, p.wait_ns, kErrTimeoutMma);
-      constexpr bool kAFromTmem = !KV_OUTER && L::kTmemA;
+      constexpr bool kAFromTmem = !KV_OUTER && !SCORED && L::kTmemA;  // (SCORED: those columns are M's)
       if (kAFromTmem && ok) {
         tc_fence_after();
 #pragma unroll
@@ -696,6 +703,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int kk = 0; kk < kPN / 16; ++kk)  // dQ += dS K_j
             mma_ts_warp(tmem + L::kColAcc1, tb + 64 + packed_col(kk), desc_plus(b1, mnmajor_step_bytes<D>(kk)),
                         idesc_acc, (x > 0 || kk > 0) ? accf.on : accf.off);
+          if constexpr (SCORED) {
+#pragma unroll
+            for (int kk = 0; kk < kPN / 16; ++kk)  // M += (P o f) K_j
+              mma_ts_warp(tmem + L::kColAcc2, tb + packed_col(kk), desc_plus(b1, mnmajor_step_bytes<D>(kk)),
+                          idesc_acc, (x > 0 || kk > 0) ? accf.on : accf.off);
+          }
         }
         // The stage's tiles are free once this completes: X, Y(x) finished
         // before the group could form P and dS.
@@ -731,10 +744,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (!KV_OUTER && my < S) {
       const int64_t li = GENERAL ? static_cast<int64_t>(own_h) * lstride + loff + my : rowbase + my;
       my_l2 = p.lse[li] * kLog2e;
-      my_delta = p.delta[li];
+      // (SCORED: from L2, since another CTA may write its rows of the same line)
+      my_delta = SCORED ? __ldcg(p.delta + li) : p.delta[li];
     }
     ScoreBlock sb;
     sb.slope = 0.f;
+    float2 p_dp = make_float2(0.f, 0.f);  // SCORED, dQ pass: the thread's share of its row's P . dP
     bool alive = true;
     int ph = pz0;  // SCORED, dK/dV pass: partner head of the block
     int pi = g;  // i modulo nper: the partner block within its head (dK/dV pass)
@@ -800,7 +815,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             sb.hi = max(min(S - 1, my + wr), pfx - 1) - partner0 - col0;
             sb.lo = my - wl - partner0 - col0;
             sb.d0 = partner0 + col0 - my;
-            grad_block_scored<BF16>(tX, tY, p.sc, c2, my_l2, my_delta, sb);
+            grad_block_scored<BF16>(tX, tY, p.sc, c2, my_l2, my_delta, sb, p_dp);
           }
         } else if constexpr (KV_OUTER) {
           const bool edge = partner0 < own0 + 127 - wr || partner0 + kPN - 1 > own0 + wl;
@@ -841,6 +856,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (lane == 0) mbar_arrive(&bar_pfull[i % kPFullBars]);
     }
     // ------------------------------------------------------------ epilogue
+    // SCORED, dQ pass.  Delta of the stored O is off by half a 16-bit step of O, which
+    // for rows whose weight lies on few keys is more than what is left of dP - Delta
+    // there.  The row's P . dP, summed here in fp32, is the exact one: dQ formed with
+    // the other is off by their difference times M = (P o f) K, and the dK/dV pass
+    // after this one reads it in the other's place.
+    float off_delta = 0.f;
+    if constexpr (SCORED && !KV_OUTER) {
+      float* part = vecs;  // [4][128]: group and column half, row
+      part[(2 * g + hf) * 128 + q4 * 32 + lane] = p_dp.x + p_dp.y;
+      named_sync(1, 32 * kProducerWarp);  // (the warps whose wait ran out come here too)
+      const float* mine = part + q4 * 32 + lane;
+      const float exact = (mine[0] + mine[128]) + (mine[256] + mine[384]);
+      off_delta = exact - my_delta;
+      if (warp < 4 && my < S) p.delta[static_cast<int64_t>(own_h) * lstride + loff + my] = exact;
+    }
     const bool done = alive && mbar_wait<kSpinOther, kUnrollOther>(bar_accfinal, 0, abort_flag, p.err, p.wait_ns, kErrTimeoutSoftmax);
     // The 16 warps split the accumulator columns of their 32 rows into up to
     // four parts of at least 16 columns.
@@ -889,6 +919,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int c = c_begin; c < c_begin + kEpiCols; c += 16) {
           uint32_t v16[16];
           tmem_ld16(t_acc + L::kColAcc1 + c, v16);
+          if constexpr (SCORED) {
+            uint32_t m16[16];
+            tmem_ld16(t_acc + L::kColAcc2 + c, m16);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              v16[e] = __float_as_uint(fmaf(-off_delta, __uint_as_float(m16[e]), __uint_as_float(v16[e])));
+          }
           if (row_ok) store_row16<BF16>(dq_row + c, v16, p.scale);
         }
       }

@@ -4,15 +4,22 @@
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
 // The bias is a constant of the call: it enters P alone.
 //
-// Roundings to 16 bits, as in the plain backward: P and dS as operands (half a step of
-// each), the stored O that Delta is taken from, the results.  With scores far apart P
-// is near 1 and dP - Delta a difference of like numbers, so the error of O in Delta is
-// the largest part of dQ's and dK's.
+// Delta.  rowsum(dO o O) of the stored O is off by half a 16-bit step of O, and where a
+// row's weight lies on few keys dP - Delta is small against that: dQ and dK were off by
+// 3.4e-3 of their size at scores of deviation 4 (bf16; 5.7e-3 at 8), where 16-bit
+// operands and results alone make 2.4e-3.  So the dQ pass, which goes first, sums the
+// row's P . dP in fp32 on its way and corrects what it has formed with the other:
+//   Delta' = sum_j P_j dP_j,  dQ = scale (dS K - (Delta' - Delta) M),  M = (P o f) K,
+// one product more, and the dK/dV pass reads Delta'.  Without / with it (us): causal
+// B1 H32/4 S4096 D128 capped 512 / 511, with a bias 382 / 421; B2 H16 S4096 D64 386 /
+// 396, 286 / 303.
 //
-// What bounds it (causal B1 H16/4 S4096 D128 bf16, capped): 159 us for the dK/dV pass
-// and 120 for the dQ pass, tensor pipes 39 % active, instructions issued 44 %: the
+// Roundings to 16 bits: P, P o f and dS as operands (half a step of each), the results.
+//
+// What bounds it (causal B1 H16/4 S4096 D128 bf16, capped): 159 us for the dK/dV pass,
+// tensor pipes 39 % active, instructions issued 44 %, and about 120 for the dQ pass: the
 // products of a block wait for its scores' arithmetic and the other way round, two
-// groups of eight warps apart.  D = 64 with a bias (H16 fp16): 86 and 66 us, issue 63 %.
+// groups of eight warps apart.
 #include "fa_bwd_main.cuh"
 
 namespace fa {

@@ -435,6 +435,56 @@ def test_empty_calls(fa):
     assert fa.fa_check_device_errors(None) == 0
 
 
+def exact_delta_bounds(r, q, k, v, do, scale, softcap, dtype):
+    """backward_bounds' dQ and dK with the row's Delta summed in fp32 from P and dP instead of taken from the stored O.
+
+    Delta' = sum_j P dP is off by sum_j p (e + errL)|dP| + p err dP + n 2^-24 p |dP|.  dS is formed with the stored O's
+    Delta, off by d16, and corrected by the difference times (P o f) K: both operands' roundings then act on terms up to
+    p f d16 larger, u each."""
+    u, n, D = torch.finfo(dtype).eps / 2, r["p"].shape[1], q.shape[-1]
+    sub = 2.0 ** -25 if dtype == torch.float16 else 0.0
+    tol_o, tol_l, (ex, e) = forward_bounds(r, q, k, v, scale, softcap, dtype)
+    qa, ka, va, da = (x.double().abs() for x in (q, k, v, do))
+    p, g, f, dpa = r["p"], r["g"].abs(), r["f"], r["dp"].abs()
+    ep = e + tol_l[:, None]
+    dp = D * 2.0 ** -23 * (da @ va.T)
+    d16 = (da * (tol_o + D * 2.0 ** -24 * r["o"].abs())).sum(1)[:, None]
+    d32 = (p * ((ep + n * 2.0 ** -24) * dpa + dp)).sum(1)[:, None]
+    ds = (ep + u) * r["ds"].abs() + p * f * (dp + d32 + 2 * u * d16) + 2 * sub * (r["s"] > -float("inf")).double() * (1 + d16)
+    if softcap is not None:
+        t = torch.sqrt((1 - f).clamp(min=0))
+        ds = ds + p * (g + d16) * (2 * t * (ex / softcap + 2.0 ** -19 * t + 2.0 ** -21) + 2.0 ** -22)
+    acc = n * 2.0 ** -23
+    dsa = r["ds"].abs() + p * f * d16
+    return 1.1 * abs(scale) * ((ds + acc * dsa) @ ka) + 1e-12, 1.1 * abs(scale) * ((ds + acc * dsa).T @ qa) + 1e-12
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("mods", [dict(softcap=30.0), dict(bias=True), dict(softcap=50.0, bias=True)],
+                         ids=["cap", "bias", "both"])
+@pytest.mark.parametrize("S", [4, 300])
+def test_gradients_of_peaked_rows(fa, S, mods, dtype, D):
+    """Rows whose weight lies on few keys: what dP - Delta leaves there is small against dP, and the rounding of the
+    stored O has no part in dQ and dK.  The mean square error stays near the roundings of operands and results."""
+    H, gain = 2, 10.0
+    q, k, v, do = (rnd((1, H, S, D), 90 + i, torch.float32).mul(gain ** 0.5 if i < 2 else 1).to(dtype) for i in range(4))
+    cap, slopes = mods.get("softcap"), alibi(H) if "bias" in mods else None
+    kw = dict(causal=True, softcap=cap, slopes=None if slopes is None else slopes.cuda())
+    gpu = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.forward(*gpu[:3], **kw)
+    dq, dk, _ = fa.backward(*gpu[:3], o, gpu[3], lse, **kw)
+    assert fa.fa_check_device_errors(None) == 0
+    at, u = torch.arange(S), torch.finfo(dtype).eps / 2
+    tr = lambda x: x[0].transpose(0, 1)  # noqa: E731
+    rs = modified.sequence(tr(q), tr(k), tr(v), modified.visible(S, True), at, at, D ** -0.5, cap, slopes, tr(do))
+    sub = 2.0 ** -25 if dtype == torch.float16 else 0.0
+    for h, r in enumerate(rs):
+        bq, bk = exact_delta_bounds(r, q[0, h], k[0, h], v[0, h], do[0, h], D ** -0.5, cap, dtype)
+        inside(dq[0, h], r["dq"], bq + u * r["dq"].abs() + sub, f"dQ h={h}")
+        inside(dk[0, h], r["dk"], bk + u * r["dk"].abs() + sub, f"dK h={h}")
+
+
 def test_backward_of_few_rows_and_many_heads(fa):
     """One token, one head a group; the workspace's split partials hold each head's share."""
     fixed_case(fa, 2, 16, 1, 1, 64, "fp16", softcap=5.0, bias=True)
