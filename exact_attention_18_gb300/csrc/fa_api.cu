@@ -232,18 +232,19 @@ fa_status encode_input(CUtensorMap* map, const void* base, bool bf16, const Shap
   return FA_OK;
 }
 
-// The constants of a cap.  tanh(v) / v on |v| <= 1.1 is a polynomial in v^2 (minimax
-// of degree 5, by Remez exchange; relative error 1.5e-6, 1.6e-6 with fp32's roundings);
+// The constants of a cap.  tanh(v) / v on |v| <= 1.25 is a polynomial in v^2 (minimax
+// of degree 6, by Remez exchange; relative error 6.2e-7, 7.4e-7 with fp32's roundings);
 // with v = scale x / cap it becomes tanh(v) = x * sum_k poly[k] x^(2k).
 // Coefficients that leave fp32's normal range bound the |x| it is used for: below it
 // to where the terms left out are under 2^-22 of the value, above it to none.
 // Range and degree were measured (us; scores of deviation 4 under 50 B2 H32/4 S4096
-// D128, of 8 under 30 B7 H16/2 up to 2500 D64): degree 5 to 1.05 (9.5e-7) 335, 157, to
-// 1.1 340, 143; degree 6 to 1.25 5 % more, 10 % less.  A block that holds a score beyond
-// takes the longer way.
+// D128, of 8 under 30 B7 H16/2 up to 2500 D64): degree 5 to 1.05 (error 9.5e-7) 335,
+// 157, to 1.1 (1.5e-6) 336, 143; degree 6 to 1.25 349, 124.  A block that holds a score
+// beyond takes the longer way.
 void tanh_poly(float scale, float cap, fa::ScoreParams* p) {
-  constexpr double kC[fa::kTanhTerms] = {0.99999849, -0.33324176, 0.13241123, -0.050452815, 0.015411088, -0.0025325383};
-  constexpr double kMax = 1.1;
+  constexpr double kC[fa::kTanhTerms] = {0.999999376, -0.333293396, 0.132906482, -0.0522054417,
+                                          0.0182291227, -0.00462690537, 0.00058449404};
+  constexpr double kMax = 1.25;
   const double in = static_cast<double>(scale) / cap;
   p->cap = static_cast<float>(cap * 1.4426950408889634074);
   p->in2 = static_cast<float>(2 * 1.4426950408889634074 * in);

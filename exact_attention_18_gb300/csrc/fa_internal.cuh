@@ -68,7 +68,7 @@ struct BwdParams {
 };
 
 // Modified scores (fa_scores.cuh has the mathematics).
-constexpr int kTanhTerms = 6;
+constexpr int kTanhTerms = 7;
 struct ScoreParams {
   float cap;            // cap * log2 e; 0: no cap
   // What the scores are in units of between the products and the exponentials, whose

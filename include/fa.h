@@ -308,7 +308,7 @@ typedef struct {
  * lie outside [0, S]: they count as the nearer end.  scores == NULL, or all of
  * its parts absent, runs fa_fwd_window.  The window's sides and `causal` hide keys
  * whatever the scores there are.  tanh is evaluated in fp32: beside the product's
- * own error a score is off by at most 2^-19 of itself, or by 2^-21 of cap.
+ * own error a score is off by at most 2^-20 of itself, or by 2^-21 of cap.
  * Slopes must be finite and slopes[h] * S far below fp32's largest number.  The
  * bias is off by at most 2^-22 of itself, and by up to 2^-15 for slopes up to 1.
  */
