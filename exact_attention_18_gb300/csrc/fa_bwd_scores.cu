@@ -11,15 +11,16 @@
 // row's P . dP in fp32 on its way and corrects what it has formed with the other:
 //   Delta' = sum_j P_j dP_j,  dQ = scale (dS K - (Delta' - Delta) M),  M = (P o f) K,
 // one product more, and the dK/dV pass reads Delta'.  Without / with it (us): causal
-// B1 H32/4 S4096 D128 capped 512 / 511, with a bias 382 / 421; B2 H16 S4096 D64 386 /
-// 396, 286 / 303.
+// B1 H32/4 S4096 D128 with a bias 382 / 421, capped (a degree less than now) 512 / 511;
+// B2 H16 S4096 D64 286 / 303, 386 / 396.
 //
 // Roundings to 16 bits: P, P o f and dS as operands (half a step of each), the results.
 //
-// What bounds it (causal B1 H16/4 S4096 D128 bf16, capped): 159 us for the dK/dV pass,
-// tensor pipes 39 % active, instructions issued 44 %, and about 120 for the dQ pass: the
+// What bounds it (causal B1 H16/4 S4096 D128 bf16, capped): 137 us for the dQ pass and
+// 157 for the dK/dV pass, tensor pipes 45 and 40 % active, instructions issued 45 %: the
 // products of a block wait for its scores' arithmetic and the other way round, two
-// groups of eight warps apart.
+// groups of eight warps apart.  D = 64 with a bias (H16 fp16): 75 and 86 us, issue 61 and
+// 63 %.
 #include "fa_bwd_main.cuh"
 
 namespace fa {

@@ -43,9 +43,9 @@
 // SCORED = true (D = 128): modified scores (fa_scores.cuh), prefixes, and packed
 // batches with either.  Sixteen softmax warps, two threads a row, and each block's
 // maximum ahead of its exponentials.  What bounds it is the softmax warps' work: a
-// capped block takes 12 warp instructions for 32 scores, issued 51 % of the time, the
-// tensor pipes 35 % active (causal B2 H32/4 S4096 bf16, 339 us: 0.81 PFLOP/s; B1 167, with a
-// bias 141, windowed without either 171).
+// capped block takes 13 warp instructions for 32 scores, issued half of the time, the
+// tensor pipes 35 % active (causal B2 H32/4 S4096 bf16, 349 us: 0.79 PFLOP/s; B1 172, with a
+// bias 147, windowed without either 171).
 #include "fa_scores.cuh"
 #include "fa_softmax.cuh"
 
@@ -58,8 +58,8 @@ namespace {
 // Register split (per thread): the launch gives every thread kLaunchRegs; the
 // last four warps drop to kRegsLow and the softmax warps rise to kRegsHigh; the
 // shares may not exceed the launch total.  (SCORED: 112 and 32 leave the softmax warps
-// without spills.  104 and 64 / 112 and 32, us: causal B2 H32/4 S4096 capped 344 / 339, B1
-// with a bias 141 / 141, both 170 / 172.)
+// without spills.  104 and 64 / 112 and 32, us, with a polynomial of one degree less:
+// causal B2 H32/4 S4096 capped 344 / 339, B1 with a bias 141 / 141, both 170 / 172.)
 template <bool SCORED>
 struct FwdRoles {
   static constexpr int kSoft = SCORED ? 16 : 8;
