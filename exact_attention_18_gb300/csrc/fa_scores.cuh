@@ -5,7 +5,8 @@
 //   y = c tanh(scale x / cap) - s_h |i - j|,   c = cap log2 e, s_h = slopes[h] log2 e,
 //
 // or scale log2 e x in the first term's place without a cap.  Only the scores'
-// registers change: what follows sees them as scores of scale 1.
+// registers change: what follows sees scores of another scale, the call's unit
+// (ScoreParams in fa_internal.cuh).
 //
 // tanh.  The unit that has exp2 gives 32 of them a clock and SM, but 16 of
 // tanh.approx (whose 2^-11 would show in the weights: 0.02 of a score at a cap of
