@@ -246,6 +246,61 @@ def test_long_rows(fa):
     fixed_case(fa, 1, 1, 1, 4200, 128, "bf16", bias=True, causal=False, gain=2.0)
 
 
+@pytest.mark.parametrize("D,H", [(128, 64), (64, 128)])
+def test_offsets_past_2_31_elements(fa, D, H):
+    """A packed batch of more than 2^31 elements a tensor: its last document, forward and backward, has the bits that
+    it has alone, and so has a head of a document before it."""
+    n, last, lens = 1500, 700, [280000 - 2200, 1500, 700]
+    T = sum(lens)
+    assert T * H * D > 2 ** 31
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GiB of free device memory")
+    g = torch.Generator("cuda").manual_seed(3)
+    q, k, v, do = (torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    for x in (q, k, v, do):
+        x[-(n + last):].normal_(generator=g)
+    kw = dict(causal=True, window=(500, 0), softcap=20.0, slopes=alibi(H).cuda())
+
+    def run(t, lengths):
+        cu = ints([sum(lengths[:i]) for i in range(len(lengths) + 1)])
+        o, lse = fa.forward_varlen(*t[:3], cu, max(lengths), **kw)
+        return (o, lse, *fa.backward_varlen(*t[:3], o, t[3], lse, cu, max(lengths), **kw))
+
+    big = run((q, k, v, do), lens)
+    tail = n + last
+    small = run([x[-tail:].contiguous() for x in (q, k, v, do)], [n, last])
+    assert fa.fa_check_device_errors(None) == 0, fa.fa_last_error_detail()
+    for name, a, b in zip(("O", "L", "dQ", "dK", "dV"), big, small):
+        a = a[:, -tail:] if name == "L" else a[-tail:]
+        assert torch.equal(a, b), name
+        assert not bool(b.isnan().any()) and bool(b.any())
+    assert not bool(big[0][:-tail].any()) and not bool(big[2][:-tail].any()) and not bool(big[4][:-tail].any())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_pages_past_2_32_bytes(fa, D):
+    """Pages more than 2^32 bytes apart: the bits of the same pages side by side, few rows, chunks and trees."""
+    page, hk, H, gap = 128, 1, 4, (1 << 31) + 128
+    near = torch.randn(2, 3, page, hk, D, generator=torch.Generator().manual_seed(8)).half().cuda()
+    pools = [torch.empty(2 * gap + page * hk * D, dtype=torch.float16, device="cuda") for _ in range(2)]
+    far = [x.as_strided((3, page, hk, D), (gap, hk * D, D, 1)) for x in pools]
+    for x, y in zip(far, near):
+        x.copy_(y)
+    table, kw = ints([[2, 0, 1]]), dict(softcap=9.0, slopes=alibi(H).cuda())
+    for n, tree in ((1, False), (6, True), (150, False), (150, True)):
+        q = rnd((n, H, D), n, torch.float16).cuda()
+        if tree:
+            bits, depth = make_tree(n, "tree", 0)
+            kw.update(tree=words_of(bits, 5).cuda(), positions=(340 - n + depth).to(torch.int32).cuda())
+        else:
+            kw.pop("tree", None), kw.pop("positions", None)
+        args = (table, ints([340]), ints([0, n]), n, 340)
+        a, b = fa.forward_paged(q, *far, *args, **kw), fa.forward_paged(q, *near, *args, **kw)
+        assert fa.fa_check_device_errors(None) == 0, fa.fa_last_error_detail()
+        assert all(torch.equal(x, y) for x, y in zip(a, b)) and not bool(a[0].isnan().any())
+
+
 @pytest.mark.parametrize("G", [64, 128])
 @pytest.mark.parametrize("D", [64, 128])
 def test_wide_groups(fa, D, G):
