@@ -3,8 +3,8 @@
 u is half a step of the 16-bit type.  First order in each error, the product of two covered by a factor 1.1.
 
 A score's error e_ij: products of D terms summed in fp32, truncated at worst, scale sum_d |q_d k_d| (D + 4) 2^-23;
-under a cap, its arithmetic: 2^-19 of the score where |x| <= 1.1 cap (a minimax polynomial with a relative error of
-1.5e-6 = 2^-19.3, and fp32's roundings), 2^-20 of the cap beyond (the derivative of tanh is at most 1, so the
+under a cap, its arithmetic: 2^-19 of the score where |x| <= 1.25 cap (a minimax polynomial with a relative error
+under 2^-20, and fp32's roundings), 2^-20 of the cap beyond (the derivative of tanh is at most 1, so the
 product's error does not grow); the bias and the sums with the row's maximum or L: 2^-22 (|s| +
 |bias| + |L|); its exponential, 2^-21.
 
@@ -13,7 +13,7 @@ terms).  O: P is rounded to 16 bits (u p_ij; in fp16 also half a subnormal step,
 row's maximum, where their sum is 1 at least: 2^-25 sum_j |v_j| e^(max s - L)), V's product sums in fp32 (n 2^-24),
 and O is rounded once (u |O|, fp16's subnormals 2^-25).  L: c_i + 2^-22 |L| + 2^-21.
 
-Backward: P = exp(s - L) is off by (e_ij + errL_i) p_ij and rounded (u p_ij; fp16 2^-25).  Delta_i from the stored O:
+Backward: P = exp(s - L) is off by (e_ij + errL_i) p_ij and rounded (u p_ij; fp16 2^-25).  Delta_i as from the stored O (the kernels do better: test_scores_edges.py has that bound):
 sum_d |dO_d| (errO_d + D 2^-24 |O_d|); dP: D 2^-23 sum_d |dO_d v_d|; g = dP - Delta, so dS = p g f is off by
   (e_ij + errL_i + u) |dS_ij| + p_ij f_ij (err dP + err Delta) + p_ij |g_ij| errf_ij + 2^-25 (fp16),
 errf = 2 |t| err t + 2^-22 with err t = (error of the product) / cap + 2^-19 |t|.  The products over n rows or keys sum in
