@@ -445,8 +445,8 @@ __global__ void __launch_bounds__(FwdRoles<SCORED>::kThreads, 1)
     const uint32_t t_mine = t_s + hf * kHalf;
     const uint32_t t_p = t_s + hf * (kHalf / 2);
     const uint32_t t_o = tmem + lane_base + L::kColO + D * t + hf * (D / 2);
-    const float slope =
-        p.sc.slopes != nullptr ? __ldg(p.sc.slopes + bh % p.heads) * 1.4426950408889634f * p.sc.per_unit : 0.f;
+    const float slope2 = p.sc.slopes != nullptr ? __ldg(p.sc.slopes + bh % p.heads) * 1.4426950408889634f : 0.f;
+    const RowSlope slope = row_slope(p.sc, slope2, is_steep(slope2));
     const int last = max(min(S - 1, row_g + wr), pfx - 1);  // last and first visible key of this row
     const int first_key = row_g - wl;
     float m = -INFINITY;  // running (possibly stale) maximum, base-2 scaled
@@ -459,17 +459,18 @@ __global__ void __launch_bounds__(FwdRoles<SCORED>::kThreads, 1)
       const bool masked = blk0 + kBlockN > S || blk0 + kBlockN - 1 > max(tile_row0 + wr, pfx - 1) ||
                           blk0 < tile_row0 + kBlockM - 1 - wl;
       uint32_t sr[kHalf];
-      float fixed = 0.f, m_half = -INFINITY;
+      float fixed = 0.f, unit = 1.f, m_half = -INFINITY;
       if (ok) {
         tc_fence_after();
         tmem_ld64(t_mine, sr);
-        const RowBias bias = row_bias(p.sc, slope, kv0 - row_g, blk0 + kBlockN - 1 <= tile_row0 || (p.causal && pfx == 0),
+        const RowBias bias = row_bias(slope, kv0 - row_g, blk0 + kBlockN - 1 <= tile_row0 || (p.causal && pfx == 0),
                                       blk0 >= tile_row0 + kBlockM - 1);
         fixed = bias.fixed;
+        unit = bias.unit;
         block_scores<kHalf>(sr, t_mine, p.sc, bias, masked,
                             PlainCols{masked ? first_key - kv0 : 0, masked ? last - kv0 : kHalf});
         // The block's maximum ahead of its exponentials, as in the four-tile kernel.
-        m_half = block_top<kHalf>(sr, p.sc) + fixed;
+        m_half = block_top<kHalf>(sr, bias.unit) + fixed;
         // Column 63 (first half) or 64: read by the other half before P~ covers it.
         tmem_st1(t_s + kHalf - 1 + hf, __float_as_uint(m_half));
         tmem_st_wait();
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(FwdRoles<SCORED>::kThreads, 1)
 #pragma unroll
       for (int k0 = 0; k0 < kHalf; k0 += 16) {
         uint32_t pk[8];
-        exp16<BF16, false>(sr, k0, make_float2(p.sc.unit, p.sc.unit), make_float2(base, base), 0, kHalf, acc, pk);
+        exp16<BF16, false>(sr, k0, make_float2(unit, unit), make_float2(base, base), 0, kHalf, acc, pk);
         tmem_st8(t_p + k0 / 2, pk);
       }
       const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));

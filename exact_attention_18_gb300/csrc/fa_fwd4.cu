@@ -478,8 +478,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t t_s = tmem + lane_base + 128u * t;  // S_t, and P_t over it
     const uint32_t t_o = t_s + L::kColO;
-    const float slope =
-        p.sc.slopes != nullptr ? __ldg(p.sc.slopes + bh % p.heads) * 1.4426950408889634f * p.sc.per_unit : 0.f;
+    const float slope2 = p.sc.slopes != nullptr ? __ldg(p.sc.slopes + bh % p.heads) * 1.4426950408889634f : 0.f;
+    const RowSlope slope = row_slope(p.sc, slope2, __any_sync(0xffffffffu, is_steep(slope2)));
     const int last = max(min(S - 1, row_g + wr), pfx - 1);  // last and first visible key of this row
     const int first_key = row_g - wl;
     float m = -INFINITY;  // running (possibly stale) maximum, base-2 scaled
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       const bool masked = kv0 + kBN > S || kv0 + kBN - 1 > max(tile_row0 + wr, pfx - 1) ||
                           kv0 < tile_row0 + kBlockM - 1 - wl;
       const RowBias bias =
-          row_bias(p.sc, slope, kv0 - row_g, kv0 + kBN - 1 <= tile_row0 || (p.causal && pfx == 0),
+          row_bias(slope, kv0 - row_g, kv0 + kBN - 1 <= tile_row0 || (p.causal && pfx == 0),
                    kv0 >= tile_row0 + kBlockM - 1);
       block_scores<kBN>(sr, t_s, p.sc, bias, masked,
                         PlainCols{masked ? first_key - kv0 : 0, masked ? last - kv0 : kBN});
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       // their sum tells) has two copies of them, which with the scores' own code is
       // more than the instruction caches like: causal B1 H32/4 S4096 D128, capped 225
       // us for 180; chunks of 64 tokens over 5000 keys with a bias 130 for 108.
-      const float m_blk = block_top<kBN>(sr, p.sc) + bias.fixed;
+      const float m_blk = block_top<kBN>(sr, bias.unit) + bias.fixed;
       float alpha = 1.f;
       bool upd = false;
       if (m_blk > m + kF4Tau || (m == -INFINITY && m_blk > m)) {
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
 #pragma unroll
       for (int k0 = 0; k0 < kBN; k0 += 16) {
         uint32_t pk[8];
-        exp16<BF16, false>(sr, k0, make_float2(p.sc.unit, p.sc.unit), make_float2(base, base), 0, kBN, acc, pk);
+        exp16<BF16, false>(sr, k0, make_float2(bias.unit, bias.unit), make_float2(base, base), 0, kBN, acc, pk);
         tmem_st8(t_s + k0 / 2, pk);
       }
       const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));

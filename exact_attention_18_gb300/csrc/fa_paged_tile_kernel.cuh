@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         bool tree;
         int pos, first, tok_first, kv_len, tile_pos0, tile_rows;  // first new key, its token
         const unsigned* bits;  // a tree row's (nullptr: none)
-        float slope;
+        RowSlope slope;
         int lim0, lo0, j_lo, j_hi;
       } sc;
       if constexpr (kScored) {
@@ -502,7 +502,8 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
         sc.tile_pos0 = sp.pos0;
         sc.tile_rows = sp.n_tok;
         sc.bits = nullptr;
-        sc.slope = p.sc.slopes != nullptr ? p.sc.slopes[w.kvh * p.G + rh] * 1.4426950408889634f * p.sc.per_unit : 0.f;
+        const float slope2 = p.sc.slopes != nullptr ? p.sc.slopes[w.kvh * p.G + rh] * 1.4426950408889634f : 0.f;
+        sc.slope = row_slope(p.sc, slope2, __any_sync(0xffffffffu, is_steep(slope2)));
         sc.lim0 = lim0;
         sc.lo0 = lo0;
         sc.j_lo = j_lo;
@@ -545,13 +546,13 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           if constexpr (BN == 128) tmem_ld128(t_s, sr);
           else tmem_ld64(t_s, sr);
           const RowBias bias =
-              row_bias(p.sc, sc.slope, key0 - sc.pos, sc.tree || p.win_right == 0 || key0 + BN - 1 <= sc.tile_pos0,
+              row_bias(sc.slope, key0 - sc.pos, sc.tree || p.win_right == 0 || key0 + BN - 1 <= sc.tile_pos0,
                        key0 >= sc.tile_pos0 + sc.tile_rows - 1);
           if (drafted) block_scores<BN>(sr, t_s, p.sc, bias, true, cols);
           else block_scores<BN>(sr, t_s, p.sc, bias, cut, PlainCols{cut ? lo : 0, cut ? lim : BN});
           // The block's maximum ahead of its exponentials, as in the forward kernels.
           // Lanes past the tile's rows hold anything and never move theirs.
-          const float m_blk = block_top<BN>(sr, p.sc) + bias.fixed;
+          const float m_blk = block_top<BN>(sr, bias.unit) + bias.fixed;
           float alpha = 1.f;
           const bool upd = row_ok && (m_blk > m + kTau || (m == -INFINITY && m_blk > m));
           if (upd) {
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
 #pragma unroll
           for (int k0 = 0; k0 < BN; k0 += 16) {
             uint32_t pk[8];
-            exp16<BF16, false>(sr, k0, make_float2(p.sc.unit, p.sc.unit), make_float2(base, base), 0, BN, acc, pk);
+            exp16<BF16, false>(sr, k0, make_float2(bias.unit, bias.unit), make_float2(base, base), 0, BN, acc, pk);
             tmem_st8(t_s + k0 / 2, pk);
           }
           const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));

@@ -90,20 +90,36 @@ __device__ __forceinline__ float2 tanh2(float2 x, const ScoreParams& sc) {
 // The two parts are larger than their sum by up to a block's width of slopes, and so is
 // their rounding: under 2^-15 in all for slopes up to 1, about the product's own.
 // Steeper rows take each key's distance by itself, as blocks on both sides do: exact
-// for the keys next to the row, which are all that such a row weighs.
+// for the keys next to the row, which are all that such a row weighs.  Their scores are
+// in base 2: a steep slope over a small unit leaves fp32's range, and a maximum as large
+// as their biases (a row that sees far keys alone, a negative slope) is off by its
+// product with the unit's rounding, which the exponentials would take for a score.
 constexpr float kSteep = 1.5f;  // base 2: a slope of 1.04
 struct RowBias {
-  float slope;  // s_h (0: no bias), in the call's unit
+  float slope;  // s_h (0: no bias), in the row's unit
   float s;      // the same with its sign, of a one-sided block; 0 where `both`
   float fixed;  // s d0, base 2
+  float unit;   // of the row's scores, base 2: the call's, or 1 of a steep row
   int d0;
-  bool both;    // (of a warp's rows, some may be steep)
+  bool both, steep;
 };
-// slope: s_h in the call's unit.
-__device__ __forceinline__ RowBias row_bias(const ScoreParams& sc, float slope, int d0, bool left, bool right) {
-  const bool both = (!left && !right) || fabsf(slope) * sc.unit > kSteep;
-  const float s = both ? 0.f : (left ? slope : -slope);
-  return RowBias{slope, s, s * static_cast<float>(d0) * sc.unit, d0, both};
+// What a row keeps of its slope: the slope in the row's unit, and that unit.  slope2: s_h,
+// base 2; steep: is_steep of it, or of any row of the warp.  A vote leaves unit and flag
+// in uniform registers (causal B4 H16 S4096 D64 with a bias, a thread's own / the vote's:
+// 189 / 183 us; 16 trees of 64 tokens 88.5 / 87.8); at D = 128 it spills (capped B2 H32/4
+// S4096: 350 / 375).
+struct RowSlope {
+  float slope, unit;
+  bool steep;
+};
+__device__ __forceinline__ bool is_steep(float slope2) { return fabsf(slope2) > kSteep; }
+__device__ __forceinline__ RowSlope row_slope(const ScoreParams& sc, float slope2, bool steep) {
+  return RowSlope{steep ? slope2 : slope2 * sc.per_unit, steep ? 1.f : sc.unit, steep};
+}
+__device__ __forceinline__ RowBias row_bias(const RowSlope& row, int d0, bool left, bool right) {
+  const bool both = (!left && !right) || row.steep;
+  const float s = both ? 0.f : (left ? row.slope : -row.slope);
+  return RowBias{row.slope, s, s * static_cast<float>(d0) * row.unit, row.unit, d0, both, row.steep};
 }
 
 // Columns [lo, hi) of 32 as bits.
@@ -123,7 +139,7 @@ struct PlainCols {
   __device__ __forceinline__ int off(int, int c) const { return c; }
 };
 
-// The scores of a block in the call's unit, less the row's constant, in two forms that
+// The scores of a block in the row's unit, less the row's constant, in two forms that
 // agree to the bit where both apply.  In registers, for warps whose block is one-sided
 // and (under a cap) all small, and a sensible scale:
 template <int N>
@@ -167,6 +183,7 @@ __device__ __forceinline__ void scores_slow(uint32_t t_s, const ScoreParams& sc,
       if (sc.cap != 0.f) y = Cols::kOff && !large ? tanh2<kCapSmall>(y, sc) : tanh2<kCapAny>(y, sc);
       else if (sc.premul) y = __fmul2_rn(y, make_float2(sc.pre, sc.pre));
       if (sc.slopes != nullptr) {
+        if (r.steep) y = __fmul2_rn(y, make_float2(sc.unit, sc.unit));
         auto biased = [&](float v, int e) {
           if (r.both) return fmaf(-r.slope, fabsf(static_cast<float>(r.d0 + e)), v);
           if (Cols::kOff && r.d0 + e > 0) return fmaf(-r.slope, static_cast<float>(e), v) - back;
@@ -213,8 +230,8 @@ __device__ __forceinline__ void block_scores(uint32_t* sr, uint32_t t_s, const S
 // Maximum of a block's scores, base 2, rounded upwards: the exponentials' multiply-add
 // then gives no score above 0, however large a far key's bias and so their rounding.
 template <int N>
-__device__ __forceinline__ float block_top(const uint32_t* sr, const ScoreParams& sc) {
-  return __fmul_ru(block_max_scaled<N>(sr, false, 0, N, 1.f, false), sc.unit);
+__device__ __forceinline__ float block_top(const uint32_t* sr, float unit) {
+  return __fmul_ru(block_max_scaled<N>(sr, false, 0, N, 1.f, false), unit);
 }
 
 // The order in which a forward CTA takes its key blocks [lo, ..).  A bias makes the
