@@ -446,7 +446,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     packed = p.cu_seqlens != nullptr;
     if (packed) {
       const int b = bh / heads_own;
-      if (!packed_sample(p.cu_seqlens, b, p.S, p.total, p.err, &tok0, &S_)) return;
+      // (A CTA that leaves here or below still waits for the kernel before it: were all of
+      // a grid's CTAs to leave at once, what follows on the stream could start beside it.)
+      if (!packed_sample(p.cu_seqlens, b, p.S, p.total, p.err, &tok0, &S_)) {
+        griddep_wait();
+        return;
+      }
       own_h = bh - b * heads_own;
       pz0 = KV_OUTER ? own_h * p.group + kv_part * hpc : own_h / p.group;
     }
@@ -463,7 +468,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int own = KV_OUTER ? cy : (p.causal ? nt - 1 - cy : cy);
   const int own0 = own * 128;
   if constexpr (GENERAL) {
-    if (own0 >= S) return;  // packed batch: this CTA lies past its sample
+    if (own0 >= S) {  // packed batch: this CTA lies past its sample
+      griddep_wait();
+      return;
+    }
   }
   // Window (general instantiation): key j is visible to query i iff i - wl <= j <= i + wr.
   const int wl = GENERAL ? p.win_left : 0;
