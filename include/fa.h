@@ -310,7 +310,7 @@ typedef struct {
  * whatever the scores there are.  tanh is evaluated in fp32: beside the product's
  * own error a score is off by at most 2^-20 of itself, or by 2^-21 of cap.
  * Slopes must be finite and slopes[h] * S far below fp32's largest number.  The
- * bias is off by at most 2^-22 of itself, and by up to 2^-15 for slopes up to 1.
+ * bias is off by at most 2^-21 of itself, and by up to 2^-15 for slopes up to 1.
  */
 fa_status fa_fwd_scores(const void* q, const void* k, const void* v, void* o, float* lse, int64_t B, int64_t H,
                         int64_t H_kv, int64_t S, int64_t D, int causal, int64_t window_left, int64_t window_right,
@@ -319,7 +319,9 @@ fa_status fa_fwd_scores(const void* q, const void* k, const void* v, void* o, fl
 /*
  * Its gradient: dq, dk, dv as fa_bwd_gqa, through the cap's derivative
  * 1 - tanh^2(scale q.k / cap).  Slopes and prefix lengths are constants of the
- * call and get no gradient.  Workspace: fa_bwd_gqa_workspace_size() bytes.
+ * call and get no gradient.  The weights are exp(s - L) of the stored fp32 L: off
+ * by up to 2^-20 |L| of themselves, which a negative slope can make much (|L| is
+ * about |slopes[h]| * S there; keep it below some thousands).  Workspace: fa_bwd_gqa_workspace_size() bytes.
  */
 fa_status fa_bwd_scores(const void* q, const void* k, const void* v, const void* o, const void* dout,
                         const float* lse, void* dq, void* dk, void* dv, int64_t B, int64_t H, int64_t H_kv, int64_t S,
