@@ -12,8 +12,8 @@
 // tanh.approx (whose 2^-11 would show in the weights: 0.02 of a score at a cap of
 // 50).  tanh(v) = 1 - 2 / (1 + e^(2v)) takes an exp2 and a reciprocal.  The FMA
 // units, which the softmax leaves idle, do better on a polynomial as long as
-// |v| <= 1.25, the common case: a cap is set well above most scores.  Such a score gets
-// the polynomial's value, another the exact form's, and a warp whose scores of a block
+// |v| <= 1.25 (0.49 for caps of 400 scales or more), the common case: a cap is set well
+// above most scores.  Such a score gets the polynomial's value, another the exact form's, and a warp whose scores of a block
 // are all small skips the latter.
 #pragma once
 
@@ -23,7 +23,7 @@
 namespace fa {
 
 // tanh(scale x / cap) of small x: x times a polynomial in x^2, the minimax
-// approximation of tanh(v) / v on |v| <= 1.25 (degree 6 in v^2: relative error 7.4e-7
+// approximation of tanh(v) / v on |v| <= 1.25 (degree 6 in v^2: relative error 8.4e-7
 // with fp32's roundings) with scale / cap folded into the coefficients on the host
 // (tanh_poly in fa_api.cu).
 __device__ __forceinline__ float2 tanh_small(float2 x, const ScoreParams& sc) {
