@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
     for (int n; ok && (n = w.seg_len()) > 0; w.next(p, n), ++seg) {
       // Block of the unit that the segment's j-th is.
       auto blk_at = [&](int j) {
-        if constexpr (kScored) return w.blk + (downwards(p) ? n - 1 - j : j);
+        if constexpr (kScored) return w.blk + n - 1 - j;
         else return w.blk + j;
       };
       int page = box_page(blk_at(0));
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(PagedLayout<D, N>::kThreads, PagedLayout<D, N>
       for (int jb = 0; jb < n; ++jb, ++i) {
         // Scored, new tokens of a tree: the key's position and who sees it (bit k: row k
         // of the warpgroup), loaded while the block's products are made.
-        const int key0 = (blk_first + (downwards(p) ? n - 1 - jb : jb)) * kPBlk;
+        const int key0 = (blk_first + (kScored ? n - 1 - jb : jb)) * kPBlk;
         const int my_key = key0 + key_lane;
         int my_pos = my_key;
         unsigned seen = 0;

@@ -120,7 +120,7 @@ __device__ __forceinline__ TileSpan tile_span(const P& p, const SegWalk<SHIFT, t
   const int base = (w.u.lo >> SHIFT) + w.blk;  // the segment's first block
   const int first = min(n, max(0, (lo >> SHIFT) - base));
   const int last = min(n, max(0, ((hi + (1 << SHIFT) - 1) >> SHIFT) - base));
-  const int beg = downwards(p) ? n - last : first, end = downwards(p) ? n - first : last;
+  const int beg = P::kScored ? n - last : first, end = P::kScored ? n - first : last;
   s.beg = beg + ((s.turn - beg) & (s.turns - 1));
   s.end = end - ((end - 1 - s.turn) & (s.turns - 1));
   if (s.end <= s.beg) s.beg = s.end = 0;
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       for (int n; ok && (n = w.seg_len()) > 0; w.next(p, n), ++seg) {
         // Block of the unit that the segment's j-th is.
         auto blk_at = [&](int j) {
-          if constexpr (kScored) return w.blk + (downwards(p) ? n - 1 - j : j);
+          if constexpr (kScored) return w.blk + n - 1 - j;
           else return w.blk + j;
         };
         int page = box_page(blk_at(0));
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
       if constexpr (kScored) {
         const int n_seg = n;
         for (int j = beg; j < end; j += step, ++cnt) {
-          const int jb = downwards(p) ? n_seg - 1 - j : j;  // block of the segment
+          const int jb = n_seg - 1 - j;  // block of the segment
           const int lim = sc.lim0 - jb * BN, lo = sc.lo0 - jb * BN;  // columns lo <= c <= lim are visible to this row
           const bool cut = jb < sc.j_lo || jb >= sc.j_hi;  // a mask cuts the block
           const int key0 = key_base + jb * BN;

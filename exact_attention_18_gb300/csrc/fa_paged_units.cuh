@@ -91,18 +91,14 @@ __device__ __forceinline__ bool has_tree(const P& p) {
   else return false;
 }
 
-// With modified scores a segment's blocks run from the last to the first.  A bias makes
-// the keys next to a row its largest scores, and upwards every block would move the
-// maximum and rescale O (32 sequences of 5000 keys, D = 128: 68 us for 61).  Without one
-// it is the blocks that a mask or a tree cuts that then come while the next ones load
-// (16 x 64 tokens over 5000 keys, D = 128, upwards / downwards: capped 130 / 127 us,
-// trees 95 / 88; D = 64 the same either way).
-template <typename P>
-__device__ __forceinline__ constexpr bool downwards(const P&) {
-  return P::kScored;
-}
-
 // Walks the segments (runs of blocks of one unit) of a CTA's run of blocks.
+//
+// With modified scores the kernels take a segment's blocks from the last to the first.
+// A bias makes the keys next to a row its largest scores, and upwards every block would
+// move the maximum and rescale O (32 sequences of 5000 keys, D = 128: 68 us for 61).
+// Without one it is the blocks that a mask or a tree cuts that then come while the next
+// ones load (16 x 64 tokens over 5000 keys, D = 128, upwards / downwards: capped 130 /
+// 127 us, trees 95 / 88; D = 64 the same either way).
 template <int SHIFT, bool COSTS>
 struct SegWalk {
   int b, tile, kvh;
