@@ -44,8 +44,8 @@
 // batches with either.  Sixteen softmax warps, two threads a row, and each block's
 // maximum ahead of its exponentials.  What bounds it is the softmax warps' work: a
 // capped block takes 13 warp instructions for 32 scores, issued half of the time, the
-// tensor pipes 35 % active (causal B2 H32/4 S4096 bf16, 349 us: 0.79 PFLOP/s; B1 172, with a
-// bias 147, windowed without either 171).
+// tensor pipes 35 % active (causal B2 H32/4 S4096 bf16, 350 us: 0.79 PFLOP/s; B1 172, with a
+// bias 135, windowed without either 171).
 #include "fa_scores.cuh"
 #include "fa_softmax.cuh"
 

@@ -51,8 +51,8 @@
 //
 // SCORED = true: modified scores (fa_scores.cuh), prefixes, and packed batches with
 // either.  Each block's maximum comes ahead of its exponentials.  Causal B2 H16 S4096
-// fp16, D = 64: capped 142 us, with a bias 93 (0.74 PFLOP/s), windowed without either
-// 73.  Instruction issue bounds it: 7.5 warp instructions for 32 biased scores, issued
+// fp16, D = 64: capped 142 us, with a bias 92 (0.75 PFLOP/s), windowed without either
+// 72.  Instruction issue bounds it: 7.5 warp instructions for 32 biased scores, issued
 // 60 % of the time, tensor pipes 33 % active, the exponential unit 33 %.
 #include "fa_scores.cuh"
 #include "fa_softmax.cuh"

@@ -74,7 +74,7 @@ struct ScoreParams {
   // What the scores are in units of between the products and the exponentials, whose
   // multiply-add puts it in: the cap, so that they are tanh, or the scale, so that they
   // are the products as they come.  A scale that is no sensible unit (negative, 0,
-  // tiny) is multiplied in beforehand instead.
+  // tiny) is multiplied in beforehand instead.  (Rows of a steep slope: base 2.)
   float unit, per_unit;  // base 2; its reciprocal
   float pre;             // factor of the products beforehand,
   int premul;            // if there is one

@@ -47,8 +47,8 @@
 //
 // P = PagedScoredParams: modified scores (fa_scores.cuh) and trees of drafted tokens.
 // A thread's key has one position and one bit a row, so both are a few instructions a
-// score; decoding 32 sequences of 5000 keys, 32 heads on 4 of 128: 59 us plain, 63
-// capped, 60 with a bias, 62 as trees with both.
+// score; decoding 32 sequences of 5000 keys, 32 heads on 4 of 128: 59 us plain, 62
+// capped, 61 with a bias, 62 as trees with both.
 #pragma once
 
 #include "fa_paged_units.cuh"

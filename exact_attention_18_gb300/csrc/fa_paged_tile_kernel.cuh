@@ -27,9 +27,9 @@
 //
 // P = PagedScoredParams: modified scores (fa_scores.cuh) and trees of drafted tokens.
 // A unit's blocks then run downwards, and each block's maximum comes ahead of its
-// exponentials.  Sixteen trees of 64 tokens over 5000 keys, 32 heads on 4 of 128: 88 us
-// (plain chunks 93), capped chunks 127; four chunks of 700 tokens over 6000 keys, 16 heads
-// on 4 of 64: plain 84, with a bias 102, capped 142, both 153, trees with both 220.
+// exponentials.  Sixteen trees of 64 tokens over 5000 keys, 32 heads on 4 of 128: 89 us
+// (plain chunks 92), capped chunks 125; four chunks of 700 tokens over 6000 keys, 16 heads
+// on 4 of 64: plain 84, with a bias 104, capped 143, both 152, trees with both 214.
 #pragma once
 
 #include "fa_paged_units.cuh"
