@@ -157,6 +157,13 @@ struct TreeCols {
     }
   }
   __device__ __forceinline__ unsigned word(int c0) const { return seen[c0 / 32]; }
+  // All of the block's keys stand at their slots, as a chain's do.
+  __device__ __forceinline__ bool in_place() const {
+    bool own = true;
+#pragma unroll
+    for (int x = 0; x < N / 32; ++x) own = own && at[x] == 32 * x + static_cast<int>(threadIdx.x & 31);
+    return __all_sync(0xffffffffu, own);
+  }
   __device__ __forceinline__ int group(int k0) const {
     int v = at[0];
 #pragma unroll
@@ -545,9 +552,13 @@ __global__ void __launch_bounds__(PagedTileLayout<D>::kThreads, 1)
           uint32_t sr[BN];
           if constexpr (BN == 128) tmem_ld128(t_s, sr);
           else tmem_ld64(t_s, sr);
-          const RowBias bias =
+          RowBias bias =
               row_bias(sc.slope, key0 - sc.pos, sc.tree || p.win_right == 0 || key0 + BN - 1 <= sc.tile_pos0,
                        key0 >= sc.tile_pos0 + sc.tile_rows - 1);
+          if (drafted && !cols.in_place()) {  // keys that may stand far from their slots: no constant fits them
+            bias.both = true;
+            bias.fixed = 0.f;
+          }
           if (drafted) block_scores<BN>(sr, t_s, p.sc, bias, true, cols);
           else block_scores<BN>(sr, t_s, p.sc, bias, cut, PlainCols{cut ? lo : 0, cut ? lim : BN});
           // The block's maximum ahead of its exponentials, as in the forward kernels.

@@ -89,11 +89,12 @@ __device__ __forceinline__ float2 tanh2(float2 x, const ScoreParams& sc) {
 // the row is hidden, and a block counts as one at or before it.)
 // The two parts are larger than their sum by up to a block's width of slopes, and so is
 // their rounding: under 2^-15 in all for slopes up to 1, about the product's own.
-// Steeper rows take each key's distance by itself, as blocks on both sides do: exact
-// for the keys next to the row, which are all that such a row weighs.  Their scores are
-// in base 2: a steep slope over a small unit leaves fp32's range, and a maximum as large
-// as their biases (a row that sees far keys alone, a negative slope) is off by its
-// product with the unit's rounding, which the exponentials would take for a score.
+// Blocks on both sides take each key's distance by itself, and so do blocks of drafted
+// keys that do not stand at their slots, and steep rows: exact for the keys next to such a
+// row, which are all that it weighs.  A steep row's scores are in base 2: a steep slope
+// over a small unit leaves fp32's range, and a maximum as large as its biases (it sees far
+// keys alone, or the slope is negative) is off by its product with the unit's rounding,
+// which the exponentials would take for a score.
 constexpr float kSteep = 1.5f;  // base 2: a slope of 1.04
 struct RowBias {
   float slope;  // s_h (0: no bias), in the row's unit

@@ -310,7 +310,8 @@ typedef struct {
  * whatever the scores there are.  tanh is evaluated in fp32: beside the product's
  * own error a score is off by at most 2^-20 of itself, or by 2^-21 of cap.
  * Slopes must be finite and slopes[h] * S far below fp32's largest number.  The
- * bias is off by at most 2^-21 of itself, and by up to 2^-15 for slopes up to 1.
+ * bias is off by at most 2^-21 of itself, and by up to 2^-15 max(1, slope) for
+ * slopes up to 1.04.
  */
 fa_status fa_fwd_scores(const void* q, const void* k, const void* v, void* o, float* lse, int64_t B, int64_t H,
                         int64_t H_kv, int64_t S, int64_t D, int causal, int64_t window_left, int64_t window_right,

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+from tests.test_paged_scores import words_of
 from tests.test_rope import ints, on_gpu, paged_setup
 from tests.test_scores import rnd
 
@@ -114,3 +115,28 @@ def test_gradient_of_a_negative_slope(fa, D):
         tol += u * want.abs() + 2.0 ** -25
         assert bool(((dv[0, h].cpu().double() - want).abs() <= tol).all()), f"dV h={h}"
         assert not bool(dq.isnan().any()) and not bool(dk.isnan().any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("n", [12, 150, 1400])
+def test_tree_whose_slots_are_far_from_its_positions(fa, n, D):
+    """Drafted tokens in any order of the slots: a row's nearest keys lie hundreds of slots away, and their bias is off
+    by no more for it.  Scores of 0; each row sees all positions up to its own: L_i = ln sum_d e^(-s d)."""
+    f, H, dt = 300, 4, torch.float16
+    kv = f + n
+    slopes = torch.tensor([1.0, 0.73, 1.03, 0.31])
+    kc, vc, table, cu = paged_setup([kv], [n], 1, D, 16, dt, 5)
+    kg, vg = on_gpu(kc, vc)
+    depth = torch.randperm(n, generator=torch.Generator().manual_seed(7))
+    bits = depth[None, :] <= depth[:, None]
+    words = -(-n // 32)
+    o, lse = fa.forward_paged(torch.zeros(n, H, D, dtype=dt, device="cuda"), kg, vg, ints(table), ints([kv]), ints(cu), n,
+                              kv, slopes=slopes.cuda(), tree=words_of(bits, words).cuda(),
+                              positions=(f + depth).to(torch.int32).cuda())
+    assert fa.fa_check_device_errors(None) == 0
+    for h in range(H):
+        s = float(slopes[h])
+        ref = torch.log((1 - torch.exp(-s * (f + depth + 1).double())) / (1 - math.exp(-s)))
+        tol = 2.0 ** -15 * max(1.0, s) + 2.0 ** -20
+        assert bool(((lse[h].cpu().double() - ref).abs() <= tol).all()), f"L h={h}"
