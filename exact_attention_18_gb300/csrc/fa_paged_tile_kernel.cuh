@@ -28,8 +28,8 @@
 // P = PagedScoredParams: modified scores (fa_scores.cuh) and trees of drafted tokens.
 // A unit's blocks then run downwards, and each block's maximum comes ahead of its
 // exponentials.  Sixteen trees of 64 tokens over 5000 keys, 32 heads on 4 of 128: 89 us
-// (plain chunks 92), capped chunks 125; four chunks of 700 tokens over 6000 keys, 16 heads
-// on 4 of 64: plain 84, with a bias 104, capped 143, both 152, trees with both 214.
+// (plain chunks 92), capped chunks 127; four chunks of 700 tokens over 6000 keys, 16 heads
+// on 4 of 64: plain 84, with a bias 103, capped 143, both 153, trees with both 217.
 #pragma once
 
 #include "fa_paged_units.cuh"
